@@ -1,6 +1,6 @@
 """Build the CUDA library ``libbsgemv.so`` in-tree (sm_103a only).
 
-Every translation unit under ``csrc/`` is compiled by nvcc in parallel with
+Every translation unit under ``csrc/`` and ``csrc/decode/`` is compiled by nvcc in parallel with
 ``-gencode arch=compute_103a,code=sm_103a -O3 -lineinfo`` and linked into
 ``block_scaled_bit_gb300/lib/libbsgemv.so`` (CUDA runtime linked statically; the driver's
 ``cuTensorMapEncodeTiled`` is looked up at run time).  A stamp holding the hash of the sources
@@ -18,6 +18,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+CSRC_DIRS = [CSRC, os.path.join(CSRC, "decode")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "lib")
 OBJ_DIR = os.path.join(LIB_DIR, "_obj")
@@ -35,15 +36,17 @@ def nvcc() -> str:
     return cand
 
 
+def _files(endings) -> list:
+    return [os.path.join(d, f) for d in CSRC_DIRS for f in os.listdir(d) if f.endswith(endings)]
+
+
 def sources() -> list:
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cpp")))
+    return sorted(_files((".cu", ".cpp")))
 
 
 def _digest(extra=()) -> str:
     h = hashlib.sha1()
-    for path in sorted(sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
-                                    if f.endswith((".h", ".cuh"))]
-                       + [os.path.join(INCLUDE, "bsgemv.h")]):
+    for path in sorted(sources() + _files((".h", ".cuh")) + [os.path.join(INCLUDE, "bsgemv.h")]):
         with open(path, "rb") as f:
             h.update(os.path.basename(path).encode())
             h.update(f.read())

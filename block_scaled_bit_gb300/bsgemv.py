@@ -16,6 +16,7 @@ FORMATS = {"int4": 1, "int8": 2, "fp8": 3, "nvfp4": 4}
 ACT_BF16 = 0x100
 VARIANTS = {"auto": 0, "mma": 1, "cuda_core": 2}
 SPLITS = {"auto": 0, "stream_k": 1, "cluster": 2}
+MOE_RENORMALIZE, MOE_LOGITS_F32 = 1, 2
 
 OK = 0
 ERR_INVALID_ARG = -1
@@ -36,6 +37,13 @@ EXPORTS = ("bsgemv_plan", "bsgemv_run", "bsgemv_run_bias", "bsgemv_run_host",
            "bsgemv_plan_set_test_fault",
            "bsgemv_dense_plan", "bsgemv_dense_run", "bsgemv_dense_describe",
            "bsgemv_dense_geometry_for", "bsgemv_dense_device_status", "bsgemv_dense_destroy",
+           "bsgemv_moe_plan", "bsgemv_moe_run", "bsgemv_moe_run_routed",
+           "bsgemv_moe_device_status", "bsgemv_moe_destroy",
+           "bsgemv_attn_plan", "bsgemv_attn_run", "bsgemv_attn_device_status",
+           "bsgemv_attn_destroy",
+           "bsgemv_cache_plan", "bsgemv_cache_copy", "bsgemv_cache_fork", "bsgemv_cache_free",
+           "bsgemv_cache_extend", "bsgemv_cache_write", "bsgemv_cache_compact",
+           "bsgemv_cache_destroy",
            "bsgemv_version")
 
 
@@ -97,6 +105,25 @@ def lib() -> ctypes.CDLL:
         L.bsgemv_device_status.argtypes = [vp, vp]
         L.bsgemv_run_noalloc.argtypes = [ci, ci, ci, i64, i64, vp, vp, vp, vp, vp, ci, vp]
         L.bsgemv_plan_set_test_fault.argtypes = [vp, ci, i64]
+        f32 = ctypes.c_float
+        L.bsgemv_moe_plan.argtypes = [ctypes.POINTER(vp), ci, ci, ci, i64, i64, ci, ci, ci, ci]
+        L.bsgemv_moe_run.argtypes = [vp] * 10 + [ci, vp]
+        L.bsgemv_moe_run_routed.argtypes = [vp] * 11 + [ci, vp]
+        L.bsgemv_moe_device_status.argtypes = [vp, vp]
+        L.bsgemv_moe_destroy.argtypes = [vp]
+        L.bsgemv_attn_plan.argtypes = [ctypes.POINTER(vp)] + [ci] * 6
+        L.bsgemv_attn_run.argtypes = [vp, vp, i64, vp, vp, i64, i64, i64, ci, vp, ci, vp, i64, vp,
+                                      ci, f32, vp, vp, vp]
+        L.bsgemv_attn_device_status.argtypes = [vp, vp]
+        L.bsgemv_attn_destroy.argtypes = [vp]
+        L.bsgemv_cache_plan.argtypes = [ctypes.POINTER(vp), ci, ci, i64, ci, ci, ci]
+        L.bsgemv_cache_copy.argtypes = [vp, vp, vp, vp, ci, vp]
+        L.bsgemv_cache_fork.argtypes = [vp] * 8 + [ci, vp]
+        L.bsgemv_cache_free.argtypes = [vp] * 5 + [ci, vp]
+        L.bsgemv_cache_extend.argtypes = [vp] * 7 + [ci, vp]
+        L.bsgemv_cache_write.argtypes = [vp] * 7 + [i64, ci, ci, i64, i64, ci, ci, ci, vp]
+        L.bsgemv_cache_compact.argtypes = [vp] * 9
+        L.bsgemv_cache_destroy.argtypes = [vp]
         for name in EXPORTS:
             if name != "bsgemv_status_string":
                 getattr(L, name).restype = ci
@@ -306,6 +333,170 @@ class DensePlan:
 
     def device_status(self, stream=None) -> int:
         return lib().bsgemv_dense_device_status(self._h, _stream(stream))
+
+
+class _Handle:
+    """Owner of one library handle: closed by close(), the end of a with block or collection."""
+
+    _destroy = ""
+
+    def close(self) -> None:
+        if getattr(self, "_h", None) is not None and self._h.value:
+            getattr(lib(), self._destroy)(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+class MoePlan(_Handle):
+    """A mixture-of-experts layer for up to max_T <= 32 tokens: top-k routing, the chosen experts'
+    gate / up / down products in a block-scaled format, and the weighted sum (bsgemv_moe_plan).
+    logits: "act" (the activation dtype) or "f32"."""
+
+    _destroy = "bsgemv_moe_destroy"
+
+    def __init__(self, fmt: str, act: str, block_size: int, has_zp: bool, H: int, I: int, E: int,
+                 top_k: int, max_T: int = 32, renormalize: bool = True, logits: str = "act"):
+        self.fmt, self.act, self.block_size, self.has_zp = fmt, act, block_size, bool(has_zp)
+        self.H, self.I, self.E, self.top_k, self.max_T = H, I, E, top_k, max_T
+        flags = (MOE_RENORMALIZE if renormalize else 0) | \
+            {"act": 0, "f32": MOE_LOGITS_F32}[logits]
+        h = ctypes.c_void_p()
+        _check(lib().bsgemv_moe_plan(ctypes.byref(h), format_code(fmt, act), block_size,
+                                     int(has_zp), H, I, E, top_k, max_T, flags),
+               "bsgemv_moe_plan")
+        self._h = h
+
+    def run_status(self, x, logits, W13, scales13, zp13, W2, scales2, zp2, y,
+                   T: int | None = None, stream=None) -> int:
+        T = x.shape[0] if T is None else T
+        return lib().bsgemv_moe_run(self._h, _ptr(x), _ptr(logits), _ptr(W13), _ptr(scales13),
+                                    _ptr(zp13), _ptr(W2), _ptr(scales2), _ptr(zp2), _ptr(y),
+                                    int(T), _stream(stream))
+
+    def run(self, x, logits, W13, scales13, zp13, W2, scales2, zp2, y, T: int | None = None,
+            stream=None) -> None:
+        """Enqueue y = the layer of x [T, H] under router logits [T, E]."""
+        _check(self.run_status(x, logits, W13, scales13, zp13, W2, scales2, zp2, y, T, stream),
+               "bsgemv_moe_run")
+
+    def run_routed(self, x, ids, weights, W13, scales13, zp13, W2, scales2, zp2, y,
+                   T: int | None = None, stream=None) -> None:
+        """The layer with the caller's routing: ids [T, top_k] int32, weights [T, top_k] fp32."""
+        T = x.shape[0] if T is None else T
+        _check(lib().bsgemv_moe_run_routed(self._h, _ptr(x), _ptr(ids), _ptr(weights), _ptr(W13),
+                                           _ptr(scales13), _ptr(zp13), _ptr(W2), _ptr(scales2),
+                                           _ptr(zp2), _ptr(y), int(T), _stream(stream)),
+               "bsgemv_moe_run_routed")
+
+    def device_status(self, stream=None) -> int:
+        return lib().bsgemv_moe_device_status(self._h, _stream(stream))
+
+
+class AttnPlan(_Handle):
+    """Single-token attention of up to max_B sequences that share a prefix, over a paged cache
+    (bsgemv_attn_plan)."""
+
+    _destroy = "bsgemv_attn_destroy"
+
+    def __init__(self, act: str, Hq: int, Hkv: int, D: int, page_size: int, max_B: int):
+        self.act, self.Hq, self.Hkv, self.D = act, Hq, Hkv, D
+        self.page_size, self.max_B = page_size, max_B
+        h = ctypes.c_void_p()
+        _check(lib().bsgemv_attn_plan(ctypes.byref(h), int(act == "bf16"), Hq, Hkv, D, page_size,
+                                      max_B), "bsgemv_attn_plan")
+        self._h = h
+
+    def run_status(self, q, k, v, prefix_table, prefix_len: int, tables, lens, out, lse=None,
+                   scale: float | None = None, stream=None) -> int:
+        if k.stride() != v.stride() or k.shape != v.shape or k.stride(-1) != 1 or \
+                q.stride(-1) != 1 or q.stride(1) != self.D or not out.is_contiguous() or \
+                tables.stride(-1) != 1 or tuple(k.shape[1:]) != (self.Hkv, self.page_size, self.D):
+            return ERR_INVALID_ARG
+        scale = self.D ** -0.5 if scale is None else scale
+        return lib().bsgemv_attn_run(self._h, _ptr(q), q.stride(0), _ptr(k), _ptr(v), k.stride(0),
+                                     k.stride(1), k.stride(2), k.shape[0], _ptr(prefix_table),
+                                     int(prefix_len), _ptr(tables), tables.stride(0), _ptr(lens),
+                                     q.shape[0], scale, _ptr(out), _ptr(lse), _stream(stream))
+
+    def run(self, q, k, v, prefix_table, prefix_len: int, tables, lens, out, lse=None,
+            scale: float | None = None, stream=None) -> None:
+        """out [B, Hq, D] from q [B, Hq, D] (any stride between sequences); k and v are views
+        [pages, Hkv, page_size, D] of the cache in either layout (strides are passed on); scale
+        defaults to D ** -0.5."""
+        _check(self.run_status(q, k, v, prefix_table, prefix_len, tables, lens, out, lse, scale,
+                               stream), "bsgemv_attn_run")
+
+    def device_status(self, stream=None) -> int:
+        return lib().bsgemv_attn_device_status(self._h, _stream(stream))
+
+
+class PageCache(_Handle):
+    """The pages of a cache (bsgemv_cache_plan): pool [planes, num_pages, page_bytes], refs
+    [num_pages], tables [max_seqs, max_pages] and lens [max_seqs] (int32) are the caller's."""
+
+    _destroy = "bsgemv_cache_destroy"
+
+    def __init__(self, planes: int, num_pages: int, page_bytes: int, page_size: int,
+                 max_seqs: int, max_pages: int):
+        self.planes, self.num_pages, self.page_bytes = planes, num_pages, page_bytes
+        self.page_size, self.max_seqs, self.max_pages = page_size, max_seqs, max_pages
+        h = ctypes.c_void_p()
+        _check(lib().bsgemv_cache_plan(ctypes.byref(h), planes, num_pages, page_bytes, page_size,
+                                       max_seqs, max_pages), "bsgemv_cache_plan")
+        self._h = h
+
+    def copy(self, pool, src, dst, stream=None) -> None:
+        """Page src[i] to page dst[i] in every plane."""
+        _check(lib().bsgemv_cache_copy(self._h, _ptr(pool), _ptr(src), _ptr(dst), src.shape[0],
+                                       _stream(stream)), "bsgemv_cache_copy")
+
+    def fork(self, pool, refs, tables, lens, parents, children, new_pages=None,
+             stream=None) -> None:
+        """Slot children[i] becomes a copy of sequence parents[i]."""
+        _check(lib().bsgemv_cache_fork(self._h, _ptr(pool), _ptr(refs), _ptr(tables), _ptr(lens),
+                                       _ptr(parents), _ptr(children), _ptr(new_pages),
+                                       parents.shape[0], _stream(stream)), "bsgemv_cache_fork")
+
+    def free(self, refs, tables, lens, seqs, stream=None) -> None:
+        """Release the sequences."""
+        _check(lib().bsgemv_cache_free(self._h, _ptr(refs), _ptr(tables), _ptr(lens), _ptr(seqs),
+                                       seqs.shape[0], _stream(stream)), "bsgemv_cache_free")
+
+    def extend(self, pool, refs, tables, lens, seqs, grown=None, stream=None) -> None:
+        """Room for one more token in each of the sequences."""
+        _check(lib().bsgemv_cache_extend(self._h, _ptr(pool), _ptr(refs), _ptr(tables),
+                                         _ptr(lens), _ptr(seqs), _ptr(grown), seqs.shape[0],
+                                         _stream(stream)), "bsgemv_cache_extend")
+
+    def write(self, pool, tables, lens, seqs, k, v, head_stride: int, row_stride: int,
+              k_plane: int, v_plane: int, stream=None) -> None:
+        """k, v [n, heads, D] (any stride between sequences) to the sequences' last positions."""
+        if k.stride() != v.stride() or k.shape != v.shape or k.stride(-1) != 1 or \
+                k.stride(1) != k.shape[2]:
+            raise BsgemvError(ERR_INVALID_ARG, "bsgemv_cache_write")
+        _check(lib().bsgemv_cache_write(self._h, _ptr(pool), _ptr(tables), _ptr(lens), _ptr(seqs),
+                                        _ptr(k), _ptr(v), k.stride(0), k.shape[1], k.shape[2],
+                                        head_stride, row_stride, k_plane, v_plane, seqs.shape[0],
+                                        _stream(stream)), "bsgemv_cache_write")
+
+    def compact(self, pool, refs, tables, lens, refs_out, tables_out, live_out,
+                stream=None) -> None:
+        """Live pages to the front; the new state in refs_out, tables_out and live_out [1]."""
+        _check(lib().bsgemv_cache_compact(self._h, _ptr(pool), _ptr(refs), _ptr(tables),
+                                          _ptr(lens), _ptr(refs_out), _ptr(tables_out),
+                                          _ptr(live_out), _stream(stream)),
+               "bsgemv_cache_compact")
 
 
 def upload(case, device="cuda"):

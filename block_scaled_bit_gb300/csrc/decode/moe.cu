@@ -1,0 +1,158 @@
+// moe.cu -- the mixture-of-experts layer for a few tokens (host entry points and kernels).
+//
+//   route     one block: top-k of each token's logits, the experts that are wanted and their
+//             tokens (a 32-bit mask per expert: max_T <= 32)
+//   gate_up   h[row][i] = p * silu(g) * u for every (expert, token) pair, fp32
+//   down      y[t][n]   = sum over the token's experts, in expert order
+#include <math.h>
+
+#include <new>
+
+#include "decode_internal.h"
+#include "moe_kernel.cuh"
+
+struct bsgemv_moe_plan_s {
+  int device = -1, sms = 0;
+  int fmt = 0, bf16 = 0, block_size = 0, has_zp = 0;
+  int64_t H = 0, I = 0;
+  int E = 0, top_k = 0, max_T = 0, flags = 0;
+  void* ws = nullptr;
+};
+
+namespace bsg {
+namespace {
+
+// Workspace: [error word and counters 256 B][Routing][h].
+MoeParams params_of(const bsgemv_moe_plan_s* p, const void* x, const void* W13, const void* s13,
+                    const void* zp13, const void* W2, const void* s2, const void* zp2, void* y,
+                    int T) {
+  MoeParams q = {};
+  q.fmt = p->fmt;
+  q.bf16 = p->bf16;
+  q.bs = p->block_size;
+  q.has_zp = p->has_zp;
+  q.H = p->H;
+  q.I = p->I;
+  q.E = p->E;
+  q.top_k = p->top_k;
+  q.T = T;
+  q.flags = p->flags;
+  q.x = static_cast<const uint16_t*>(x);
+  q.up = weight_of(p->fmt, p->block_size, p->has_zp, 2 * p->I, p->H, W13, s13, zp13);
+  q.down = weight_of(p->fmt, p->block_size, p->has_zp, p->H, p->I, W2, s2, zp2);
+  q.y = static_cast<uint16_t*>(y);
+  char* w = static_cast<char*>(p->ws);
+  q.err = reinterpret_cast<unsigned*>(w);
+  q.route = reinterpret_cast<Routing*>(w + 256);
+  q.h = reinterpret_cast<float*>(w + 256 + routing_bytes());
+  return q;
+}
+
+int run(bsgemv_moe_plan_s* p, const void* x, const void* logits, const int32_t* ids,
+        const float* weights, const void* W13, const void* s13, const void* zp13, const void* W2,
+        const void* s2, const void* zp2, void* y, int T, void* stream) {
+  if (p == nullptr || T < 1) return BSGEMV_ERR_INVALID_ARG;
+  if (T > p->max_T) return BSGEMV_ERR_M_TOO_LARGE;
+  if (!x || !W13 || !s13 || !W2 || !s2 || !y || (!logits && (!ids || !weights)))
+    return BSGEMV_ERR_INVALID_ARG;
+  const bool third = p->has_zp || p->fmt == kNvfp4;
+  if (third != (zp13 != nullptr) || third != (zp2 != nullptr)) return BSGEMV_ERR_INVALID_ARG;
+  const uintptr_t es = p->fmt == kFp8 ? 4 : (p->fmt == kNvfp4 ? 4 : 2);
+  const uintptr_t zs = p->fmt == kNvfp4 ? 4 : 1;
+  if (!aligned_to(x, 16) || !aligned_to(W13, 16) || !aligned_to(W2, 16) || !aligned_to(y, 16) ||
+      !aligned_to(s13, es) || !aligned_to(s2, es) || !aligned_to(zp13, zs) ||
+      !aligned_to(zp2, zs) ||
+      !aligned_to(logits, (p->flags & BSGEMV_MOE_LOGITS_F32) ? 4 : 2) || !aligned_to(ids, 4) ||
+      !aligned_to(weights, 4))
+    return BSGEMV_ERR_MISALIGNED;
+  const int rc = decode_check_device(p->device);
+  if (rc != BSGEMV_OK) return rc;
+  MoeParams q = params_of(p, x, W13, s13, zp13, W2, s2, zp2, y, T);
+  q.logits = logits;
+  q.ids = ids;
+  q.weights = weights;
+  return launch_moe(q, p->sms, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+}  // namespace bsg
+
+using namespace bsg;
+
+extern "C" {
+
+int bsgemv_moe_plan(bsgemv_moe_plan_t* out, int format, int block_size, int has_zp, int64_t H,
+                    int64_t I, int E, int top_k, int max_T, int flags) {
+  if (out == nullptr) return BSGEMV_ERR_INVALID_ARG;
+  *out = nullptr;
+  const int fmt = format & 0xFF;
+  if ((format & ~(0xFF | BSGEMV_ACT_BF16)) != 0 || fmt < kInt4 || fmt > kNvfp4 ||
+      (has_zp != 0 && has_zp != 1) || H < 1 || I < 1 || E < 1 || top_k < 1 || top_k > E ||
+      max_T < 1 || max_T > kMoeMaxT ||
+      (flags & ~(BSGEMV_MOE_RENORMALIZE | BSGEMV_MOE_LOGITS_F32)) != 0)
+    return BSGEMV_ERR_INVALID_ARG;
+  const bool ints = fmt == kInt4 || fmt == kInt8;
+  const bool bs_ok = ints ? (block_size == 16 || block_size == 32 || block_size == 64 ||
+                             block_size == 128)
+                          : block_size == (fmt == kFp8 ? 128 : 16);
+  if (!bs_ok || (has_zp && !ints) || E > kMoeMaxE || top_k > kMoeMaxK || H % 64 || I % 64 ||
+      H % block_size || I % block_size || H >= (1 << 24) || I >= (1 << 24))
+    return BSGEMV_ERR_UNSUPPORTED;
+  int dev = -1, sms = 0;
+  int rc = decode_device(&dev, &sms);
+  if (rc != BSGEMV_OK) return rc;
+  bsgemv_moe_plan_s* p = new (std::nothrow) bsgemv_moe_plan_s();
+  if (!p) return BSGEMV_ERR_CUDA;
+  p->device = dev;
+  p->sms = sms;
+  p->fmt = fmt;
+  p->bf16 = (format & BSGEMV_ACT_BF16) != 0;
+  p->block_size = block_size;
+  p->has_zp = has_zp;
+  p->H = H;
+  p->I = I;
+  p->E = E;
+  p->top_k = top_k;
+  p->max_T = max_T;
+  p->flags = flags;
+  rc = decode_alloc(&p->ws, moe_workspace_bytes(H, I, top_k, max_T, sms));
+  if (rc != BSGEMV_OK) {
+    delete p;
+    return rc;
+  }
+  *out = p;
+  return BSGEMV_OK;
+}
+
+int bsgemv_moe_run(bsgemv_moe_plan_t plan, const void* x, const void* logits, const void* W13,
+                   const void* scales13, const void* zp13, const void* W2, const void* scales2,
+                   const void* zp2, void* y, int T, void* stream) {
+  if (logits == nullptr) return BSGEMV_ERR_INVALID_ARG;
+  return run(plan, x, logits, nullptr, nullptr, W13, scales13, zp13, W2, scales2, zp2, y, T,
+             stream);
+}
+
+int bsgemv_moe_run_routed(bsgemv_moe_plan_t plan, const void* x, const int32_t* ids,
+                          const float* weights, const void* W13, const void* scales13,
+                          const void* zp13, const void* W2, const void* scales2, const void* zp2,
+                          void* y, int T, void* stream) {
+  return run(plan, x, nullptr, ids, weights, W13, scales13, zp13, W2, scales2, zp2, y, T, stream);
+}
+
+int bsgemv_moe_device_status(bsgemv_moe_plan_t plan, void* stream) {
+  if (plan == nullptr) return BSGEMV_ERR_INVALID_ARG;
+  const int rc = decode_check_device(plan->device);
+  if (rc != BSGEMV_OK) return rc;
+  return decode_error_status(static_cast<unsigned*>(plan->ws), stream);
+}
+
+int bsgemv_moe_destroy(bsgemv_moe_plan_t plan) {
+  if (plan == nullptr) return BSGEMV_OK;
+  int rc = BSGEMV_OK;
+  if (cudaDeviceSynchronize() != cudaSuccess) rc = BSGEMV_ERR_CUDA;
+  cudaFree(plan->ws);
+  delete plan;
+  return rc;
+}
+
+}  // extern "C"

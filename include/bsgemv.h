@@ -329,6 +329,189 @@ int bsgemv_dense_device_status(bsgemv_dense_plan_t plan, void* stream);
 /* Free the plan (synchronises the device first).  NULL is a no-op. */
 int bsgemv_dense_destroy(bsgemv_dense_plan_t plan);
 
+/*
+ * ---------------------------------------------------------------------------------------------
+ * The rest of a decode step: the mixture-of-experts layer, attention over a paged cache and the
+ * pages of that cache.  Same conventions as above (streams, statuses, caller-owned tensors, one
+ * stream at a time per plan, enqueue only unless said otherwise).
+ *
+ * Mixture-of-experts layer for a few tokens.  For token t with router logits l[t, 0 .. E-1]:
+ *
+ *     e_1 .. e_k = the k largest logits (equal logits: the lowest expert first)
+ *     p_j        = exp(l[e_j]) / sum of exp(l) over the chosen experts
+ *                  (over all E without BSGEMV_MOE_RENORMALIZE)
+ *     g, u       = W13[e_j] . x[t]    rows 0 .. I-1 and I .. 2I-1 of the [2I, H] weight
+ *     y[t]       = sum over j of p_j * W2[e_j] . (g / (1 + exp(-g)) * u)       W2: [H, I]
+ *
+ * x, y and (unless BSGEMV_MOE_LOGITS_F32) the logits are in the activation dtype.  Sums, softmax
+ * and the intermediate are fp32 (the intermediate enters the second product as two bf16 parts
+ * that hold 16 of its bits); y is rounded once.  An expert's weights are read
+ * once for all tokens that chose it, and other experts' weights are not read.  A logit of -inf is
+ * never chosen; a row with nothing to choose gives y = 0.  A row that holds a NaN or +inf logit
+ * gives NaN, as the softmax has it.  What one token chose never reaches another token's row, NaN
+ * weights included.
+ *
+ * Weights of all experts are stacked: W13 [E][2I][row bytes of H], W2 [E][H][row bytes of I],
+ * scales and zero points likewise, each in the layout table's format.  zp13 / zp2: NULL without
+ * zero points and for FP8; for NVFP4 the device pointers of E fp32 global scales, one per expert.
+ */
+typedef struct bsgemv_moe_plan_s* bsgemv_moe_plan_t;
+
+enum bsgemv_moe_flags {
+  BSGEMV_MOE_RENORMALIZE = 1, /* weights of the chosen experts sum to one */
+  BSGEMV_MOE_LOGITS_F32 = 2   /* logits are fp32 whatever the activation dtype */
+};
+
+/*
+ * format, block_size, has_zp as bsgemv_plan, except that integer block sizes are 16, 32, 64 or
+ * 128.  H and I: multiples of 64 and of block_size, at least 64, below 2^24.
+ * 1 <= E <= 1024, 1 <= top_k <= min(E, 16), 1 <= max_T <= 32, flags of bsgemv_moe_flags.
+ */
+int bsgemv_moe_plan(bsgemv_moe_plan_t* out, int format, int block_size, int has_zp, int64_t H,
+                    int64_t I, int E, int top_k, int max_T, int flags);
+
+/* Enqueue the layer for T (1 .. max_T) tokens.  x, W13, W2 and y 16-byte aligned; scales aligned
+ * to their element (NVFP4: 4 bytes), logits to theirs.  Deterministic: repeated calls are
+ * bit-identical. */
+int bsgemv_moe_run(bsgemv_moe_plan_t plan, const void* x, const void* logits, const void* W13,
+                   const void* scales13, const void* zp13, const void* W2, const void* scales2,
+                   const void* zp2, void* y, int T, void* stream);
+
+/* The same layer for a router of the caller's own: ids [T][top_k] int32 and weights [T][top_k]
+ * fp32 (device) in place of the logits.  An id outside 0 .. E-1 is an unused place; an expert
+ * named twice by a token counts with the sum of its weights. */
+int bsgemv_moe_run_routed(bsgemv_moe_plan_t plan, const void* x, const int32_t* ids,
+                          const float* weights, const void* W13, const void* scales13,
+                          const void* zp13, const void* W2, const void* scales2, const void* zp2,
+                          void* y, int T, void* stream);
+
+/* Synchronise `stream`, then read and clear the plan's error word (as bsgemv_device_status). */
+int bsgemv_moe_device_status(bsgemv_moe_plan_t plan, void* stream);
+
+/* Free the plan (synchronises the device first).  NULL is a no-op. */
+int bsgemv_moe_destroy(bsgemv_moe_plan_t plan);
+
+/*
+ * Single-token attention of B sequences that share a prefix, over a paged cache: for sequence b
+ * and query head h (kv head h / (Hq / Hkv)),
+ *
+ *     out[b, h] = sum over j < lens[b] of softmax_j(scale * q[b, h] . k_j) v_j
+ *
+ * Positions 0 .. prefix_len-1 are every sequence's (their K and V are read once for all), the
+ * rest are a sequence's own.  Position j lies in row j % page_size of a page: of page
+ * prefix_table[j / page_size] for the prefix, of page tables[b * table_stride + j / page_size]
+ * for own positions (a page in which the prefix ends is read from prefix_table up to prefix_len
+ * and from the sequence's table after it).  What pages hold outside these positions does not
+ * matter, NaN included.  A slot with lens[b] < max(prefix_len, 1) holds no sequence: its
+ * out rows are 0 and its lse -inf, and its row of `tables` is not read.
+ *
+ * q [B][Hq][D] with q_stride elements between sequences, out [B][Hq][D] contiguous, fp16 or bf16
+ * like the cache.  k and v: element (page, head, row, d) of the cache at
+ * page * page_stride + head * head_stride + row * row_stride + d elements, num_pages pages;
+ * both layouts ([page][head][row][D] and [page][row][head][D]) are strides.  lse, if not NULL:
+ * [B][Hq] fp32, log of the softmax's denominator with the maximum put back.  Scores, softmax and
+ * sums are fp32; the softmax numerators are rounded to the cache's dtype for the second product
+ * and summed as rounded.
+ */
+typedef struct bsgemv_attn_plan_s* bsgemv_attn_plan_t;
+
+/* D one of 64, 128, 256; page_size a power of two from 8 to 1024; Hkv >= 1, Hq a multiple of Hkv
+ * with Hq / Hkv <= 64 and Hq <= 1024; 1 <= max_B <= 1024.  act_bf16: 0 = fp16, 1 = bf16. */
+int bsgemv_attn_plan(bsgemv_attn_plan_t* out, int act_bf16, int Hq, int Hkv, int D,
+                     int page_size, int max_B);
+
+/* Enqueue the attention of B (1 .. max_B) slots.  q, k, v, out 16-byte aligned, all strides
+ * multiples of 8 elements; prefix_table, tables, lens int32 device memory (prefix_table may be
+ * NULL when prefix_len == 0).  prefix_len is a host value: 0 <= prefix_len < 2^30.  Page ids
+ * outside 0 .. num_pages-1 are read as zeros.  Deterministic: repeated calls are bit-identical. */
+int bsgemv_attn_run(bsgemv_attn_plan_t plan, const void* q, int64_t q_stride, const void* k,
+                    const void* v, int64_t page_stride, int64_t head_stride, int64_t row_stride,
+                    int num_pages, const int32_t* prefix_table, int prefix_len,
+                    const int32_t* tables, int64_t table_stride, const int32_t* lens, int B,
+                    float scale, void* out, float* lse, void* stream);
+
+/* Synchronise `stream`, then read and clear the plan's error word (as bsgemv_device_status). */
+int bsgemv_attn_device_status(bsgemv_attn_plan_t plan, void* stream);
+
+/* Free the plan (synchronises the device first).  NULL is a no-op. */
+int bsgemv_attn_destroy(bsgemv_attn_plan_t plan);
+
+/*
+ * The pages of a cache.  The caller owns
+ *
+ *     pool    [planes][num_pages][page_bytes]   K and V of every layer, a plane each
+ *     refs    [num_pages] int32                 sequences that hold the page; 0 = free
+ *     tables  [max_seqs][max_pages] int32       pages of each sequence, -1 after the last
+ *     lens    [max_seqs] int32                  tokens of each sequence
+ *
+ * in device memory; position j of sequence s lies in page tables[s][j / page_size].  All free
+ * pages are alike: a page that is taken is always the free page with the lowest index, so the
+ * state alone decides the result.  Lists of sequences and pages are int32 device arrays; an
+ * entry outside its range is skipped.  No call synchronises.
+ */
+typedef struct bsgemv_cache_s* bsgemv_cache_t;
+
+/* planes >= 1, num_pages >= 1 (below 2^24), page_bytes a positive multiple of 16, page_size >= 1,
+ * 1 <= max_seqs <= 65536, max_pages >= 1 with max_seqs * max_pages below 2^31. */
+int bsgemv_cache_plan(bsgemv_cache_t* out, int planes, int num_pages, int64_t page_bytes,
+                      int page_size, int max_seqs, int max_pages);
+
+/* Copy page src[i] to page dst[i] in every plane, i < n.  The pages of dst are distinct and none
+ * is in src. */
+int bsgemv_cache_copy(bsgemv_cache_t cache, void* pool, const int32_t* src, const int32_t* dst,
+                      int n, void* stream);
+
+/*
+ * Slot children[i] becomes a copy of sequence parents[i], i < n <= max_seqs, all at once (a child
+ * may be the parent of another entry): whole pages are shared, and a page that is only partly
+ * filled is copied into a free page, so that both can grow.  What a child held before is released
+ * first; children are distinct.  parents[i] == children[i] leaves the slot alone.
+ * new_pages [n], if not NULL: the page taken for the copy, -1 where none was needed, -2 where the
+ * pool had none left: that child becomes empty (earlier entries are served first).
+ */
+int bsgemv_cache_fork(bsgemv_cache_t cache, void* pool, int32_t* refs, int32_t* tables,
+                      int32_t* lens, const int32_t* parents, const int32_t* children,
+                      int32_t* new_pages, int n, void* stream);
+
+/* Release sequences seqs[0 .. n-1] (distinct): their pages lose a reference, their rows become
+ * -1 and their lengths 0. */
+int bsgemv_cache_free(bsgemv_cache_t cache, int32_t* refs, int32_t* tables, int32_t* lens,
+                      const int32_t* seqs, int n, void* stream);
+
+/*
+ * One more token for each of the sequences seqs[0 .. n-1] (distinct): lens grows by one, with a
+ * page taken where the last one is full, and a copy of the last page where other sequences hold
+ * it too.  A sequence that finds no free page (earlier entries are served first) or no room in
+ * its row stays as it is; grown [n], if not NULL, is 1 or 0.
+ */
+int bsgemv_cache_extend(bsgemv_cache_t cache, void* pool, int32_t* refs, int32_t* tables,
+                        int32_t* lens, const int32_t* seqs, int32_t* grown, int n, void* stream);
+
+/*
+ * Put one token's K and V of one layer at the last position (lens - 1) of each of the sequences
+ * seqs[0 .. n-1]: for i < n, head h < heads and d: k[i * kv_stride + h * D + d] goes to element
+ * h * head_stride + row * row_stride + d of its page in plane k_plane, and v likewise in v_plane.
+ * 2-byte elements; D and the strides multiples of 8; k, v and pool 16-byte aligned.
+ */
+int bsgemv_cache_write(bsgemv_cache_t cache, void* pool, const int32_t* tables,
+                       const int32_t* lens, const int32_t* seqs, const void* k, const void* v,
+                       int64_t kv_stride, int heads, int D, int64_t head_stride,
+                       int64_t row_stride, int k_plane, int v_plane, int n, void* stream);
+
+/*
+ * Move the live pages to the front: with L live pages, the i-th live page at or after L (in index
+ * order) moves to the i-th free page before L, in every plane.  refs_out and tables_out (which
+ * may be refs and tables themselves) get the new state, live_out [1] L; the moved pages' old
+ * places keep their bytes, so tables that were read before stay readable until those pages are
+ * taken again.  Entries of rows after a sequence's last page become -1.
+ */
+int bsgemv_cache_compact(bsgemv_cache_t cache, void* pool, const int32_t* refs,
+                         const int32_t* tables, const int32_t* lens, int32_t* refs_out,
+                         int32_t* tables_out, int32_t* live_out, void* stream);
+
+/* Free the handle (synchronises the device first).  NULL is a no-op. */
+int bsgemv_cache_destroy(bsgemv_cache_t cache);
+
 /* Library version as MAJOR * 10000 + MINOR * 100 + PATCH. */
 int bsgemv_version(void);
 
