@@ -1,7 +1,38 @@
 // decode_host.cpp -- host helpers of the decode-step entry points.
 #include "decode_internal.h"
 
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
 namespace bsg {
+
+int decode_encode(CUtensorMap* tm, CUtensorMapDataType type, int rank, const void* base,
+                  const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                  CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess && q == cudaDriverEntryPointSuccess)
+      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  if (!encode) return BSGEMV_ERR_CUDA;
+  cuuint64_t d[5], st[4] = {};
+  cuuint32_t b[5], unit[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    unit[i] = 1;
+    if (i + 1 < rank) st[i] = strides[i];
+  }
+  const CUresult r = encode(tm, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st,
+                            b, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? BSGEMV_OK : BSGEMV_ERR_CUDA;
+}
 
 int decode_device(int* dev, int* sms) {
   int major = 0, minor = 0;

@@ -31,4 +31,52 @@ inline int decode_launched() {
   return cudaGetLastError() == cudaSuccess ? BSGEMV_OK : BSGEMV_ERR_CUDA;
 }
 
+// A tiled tensor map with zero fill (strides in bytes, from the second dimension on).
+int decode_encode(CUtensorMap* tm, CUtensorMapDataType type, int rank, const void* base,
+                  const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                  CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion);
+
+// Allow `kernel` `smem` bytes of dynamic shared memory on the current device (`rec`: what it was
+// allowed before), with the largest carveout, as for the GEMV's kernels.
+template <class Kernel>
+int decode_smem(Kernel kernel, AttrRecord& rec, int smem) {
+  int dev = -1;
+  uint64_t ctx = 0;
+  if (!current_device_context(&dev, &ctx)) return BSGEMV_ERR_CUDA;
+  const int d = rec.slot(dev, ctx);
+  if (smem > rec.smem[d].load()) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared) != cudaSuccess) {
+      cudaGetLastError();
+      return BSGEMV_ERR_CUDA;
+    }
+    rec.smem[d].store(smem);
+  }
+  return BSGEMV_OK;
+}
+
+// Launch with programmatic serialisation: the kernel may start while the one before it in the
+// stream drains, and waits for it (griddepcontrol.wait) before it touches what that one writes.
+template <class... Params, class... Args>
+int decode_launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                  const Args&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return BSGEMV_ERR_CUDA;
+  }
+  return BSGEMV_OK;
+}
+
 }  // namespace bsg

@@ -2,7 +2,7 @@
 //
 //   route     one block: top-k of each token's logits, the experts that are wanted and their
 //             tokens (a 32-bit mask per expert: max_T <= 32)
-//   gate_up   h[row][i] = p * silu(g) * u for every (expert, token) pair, fp32
+//   up        h[row][i] = p * silu(g) * u for every (expert, token) pair
 //   down      y[t][n]   = sum over the token's experts, in expert order
 #include <math.h>
 
@@ -17,35 +17,38 @@ struct bsgemv_moe_plan_s {
   int64_t H = 0, I = 0;
   int E = 0, top_k = 0, max_T = 0, flags = 0;
   void* ws = nullptr;
+  bsg::MoeLayout at = {};
+  // tensor maps of the last few (W13, W2) pairs (a layer each: a plan serves layers in turn)
+  struct MapEntry {
+    const void *W13 = nullptr, *W2 = nullptr;
+    CUtensorMap up, down;
+  };
+  static constexpr int kMaps = 64;
+  MapEntry maps[kMaps];
+  int next_map = 0;
 };
 
 namespace bsg {
 namespace {
 
-// Workspace: [error word and counters 256 B][Routing][h].
-MoeParams params_of(const bsgemv_moe_plan_s* p, const void* x, const void* W13, const void* s13,
-                    const void* zp13, const void* W2, const void* s2, const void* zp2, void* y,
-                    int T) {
-  MoeParams q = {};
-  q.fmt = p->fmt;
-  q.bf16 = p->bf16;
-  q.bs = p->block_size;
-  q.has_zp = p->has_zp;
-  q.H = p->H;
-  q.I = p->I;
-  q.E = p->E;
-  q.top_k = p->top_k;
-  q.T = T;
-  q.flags = p->flags;
-  q.x = static_cast<const uint16_t*>(x);
-  q.up = weight_of(p->fmt, p->block_size, p->has_zp, 2 * p->I, p->H, W13, s13, zp13);
-  q.down = weight_of(p->fmt, p->block_size, p->has_zp, p->H, p->I, W2, s2, zp2);
-  q.y = static_cast<uint16_t*>(y);
-  char* w = static_cast<char*>(p->ws);
-  q.err = reinterpret_cast<unsigned*>(w);
-  q.route = reinterpret_cast<Routing*>(w + 256);
-  q.h = reinterpret_cast<float*>(w + 256 + routing_bytes());
-  return q;
+int maps_of(bsgemv_moe_plan_s* p, const MoeWeight& up, const MoeWeight& down, MoeParams* q) {
+  for (auto& m : p->maps)
+    if (m.W13 == up.W && m.W2 == down.W) {
+      q->tm_up = m.up;
+      q->tm_down = m.down;
+      return BSGEMV_OK;
+    }
+  auto& m = p->maps[p->next_map];
+  m.W13 = nullptr;
+  int rc = moe_encode(&m.up, up, p->E);
+  if (rc == BSGEMV_OK) rc = moe_encode(&m.down, down, p->E);
+  if (rc != BSGEMV_OK) return rc;
+  p->next_map = (p->next_map + 1) % bsgemv_moe_plan_s::kMaps;
+  m.W13 = up.W;
+  m.W2 = down.W;
+  q->tm_up = m.up;
+  q->tm_down = m.down;
+  return BSGEMV_OK;
 }
 
 int run(bsgemv_moe_plan_s* p, const void* x, const void* logits, const int32_t* ids,
@@ -57,20 +60,42 @@ int run(bsgemv_moe_plan_s* p, const void* x, const void* logits, const int32_t* 
     return BSGEMV_ERR_INVALID_ARG;
   const bool third = p->has_zp || p->fmt == kNvfp4;
   if (third != (zp13 != nullptr) || third != (zp2 != nullptr)) return BSGEMV_ERR_INVALID_ARG;
-  const uintptr_t es = p->fmt == kFp8 ? 4 : (p->fmt == kNvfp4 ? 4 : 2);
-  const uintptr_t zs = p->fmt == kNvfp4 ? 4 : 1;
   if (!aligned_to(x, 16) || !aligned_to(W13, 16) || !aligned_to(W2, 16) || !aligned_to(y, 16) ||
-      !aligned_to(s13, es) || !aligned_to(s2, es) || !aligned_to(zp13, zs) ||
-      !aligned_to(zp2, zs) ||
+      !aligned_to(s13, 4) || !aligned_to(s2, 4) || !aligned_to(zp13, 4) || !aligned_to(zp2, 4) ||
       !aligned_to(logits, (p->flags & BSGEMV_MOE_LOGITS_F32) ? 4 : 2) || !aligned_to(ids, 4) ||
       !aligned_to(weights, 4))
     return BSGEMV_ERR_MISALIGNED;
-  const int rc = decode_check_device(p->device);
+  int rc = decode_check_device(p->device);
   if (rc != BSGEMV_OK) return rc;
-  MoeParams q = params_of(p, x, W13, s13, zp13, W2, s2, zp2, y, T);
+  MoeParams q = {};
+  q.fmt = p->fmt;
+  q.bf16 = p->bf16;
+  q.bs = p->block_size;
+  q.has_zp = p->has_zp;
+  q.H = p->H;
+  q.I = p->I;
+  q.E = p->E;
+  q.top_k = p->top_k;
+  q.T = T;
+  q.max_T = p->max_T;
+  q.flags = p->flags;
+  q.x = static_cast<const uint16_t*>(x);
   q.logits = logits;
   q.ids = ids;
   q.weights = weights;
+  q.up = weight_of(p->fmt, p->block_size, p->has_zp, 2 * p->I, p->H, W13, s13, zp13);
+  q.down = weight_of(p->fmt, p->block_size, p->has_zp, p->H, p->I, W2, s2, zp2);
+  rc = maps_of(p, q.up, q.down, &q);
+  if (rc != BSGEMV_OK) return rc;
+  q.y = static_cast<uint16_t*>(y);
+  char* w = static_cast<char*>(p->ws);
+  q.err = reinterpret_cast<unsigned*>(w);
+  q.route = reinterpret_cast<Routing*>(w + p->at.route);
+  q.counters_up = reinterpret_cast<unsigned*>(w + p->at.counters_up);
+  q.counters_down = reinterpret_cast<unsigned*>(w + p->at.counters_down);
+  q.partials = reinterpret_cast<float*>(w + p->at.partials);
+  q.h_hi = reinterpret_cast<uint16_t*>(w + p->at.h_hi);
+  q.h_lo = reinterpret_cast<uint16_t*>(w + p->at.h_lo);
   return launch_moe(q, p->sms, static_cast<cudaStream_t>(stream));
 }
 
@@ -96,7 +121,8 @@ int bsgemv_moe_plan(bsgemv_moe_plan_t* out, int format, int block_size, int has_
                              block_size == 128)
                           : block_size == (fmt == kFp8 ? 128 : 16);
   if (!bs_ok || (has_zp && !ints) || E > kMoeMaxE || top_k > kMoeMaxK || H % 64 || I % 64 ||
-      H % block_size || I % block_size || H >= (1 << 24) || I >= (1 << 24))
+      H % block_size || I % block_size || H >= (1 << 24) || I >= (1 << 24) ||
+      2 * I * E >= (int64_t{1} << 31) || H * E >= (int64_t{1} << 31))
     return BSGEMV_ERR_UNSUPPORTED;
   int dev = -1, sms = 0;
   int rc = decode_device(&dev, &sms);
@@ -115,7 +141,8 @@ int bsgemv_moe_plan(bsgemv_moe_plan_t* out, int format, int block_size, int has_
   p->top_k = top_k;
   p->max_T = max_T;
   p->flags = flags;
-  rc = decode_alloc(&p->ws, moe_workspace_bytes(H, I, top_k, max_T, sms));
+  p->at = moe_layout(H, I, E, top_k, max_T, sms);
+  rc = decode_alloc(&p->ws, p->at.total);
   if (rc != BSGEMV_OK) {
     delete p;
     return rc;

@@ -1,0 +1,11 @@
+// moe_int8.cu -- the expert layer's products on 8-bit integer weights.
+#include "moe_launch.cuh"
+
+namespace bsg {
+
+int launch_moe_int8(const MoeGemmParams& p, bool bf16, bool wide, bool down, int ctas, int smem,
+                    cudaStream_t s) {
+  return launch_moe_fmt<kInt8, false>(p, bf16, wide, down, ctas, smem, s);
+}
+
+}  // namespace bsg

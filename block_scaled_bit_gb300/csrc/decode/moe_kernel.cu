@@ -1,4 +1,5 @@
 // moe_kernel.cu -- the kernels of the mixture-of-experts layer and their launches.
+#include "moe_gemm.cuh"
 #include "moe_kernel.cuh"
 
 namespace bsg {
@@ -12,13 +13,15 @@ BSG_DEV float logit_at(const MoeParams& p, int t, int e) {
   return p.bf16 ? half_to_f32<true>(v, 0) : half_to_f32<false>(v, 0);
 }
 
-__global__ void __launch_bounds__(1024) moe_route(MoeParams p) {
+__global__ void __launch_bounds__(1024) moe_route(const __grid_constant__ MoeParams p) {
   __shared__ uint32_t mask[kMoeMaxE];
   __shared__ int ids[kMoeMaxT][kMoeMaxK];
   __shared__ float wts[kMoeMaxT][kMoeMaxK];
   __shared__ uint32_t nan_rows;
   __shared__ int warp_a[32], warp_r[32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  pdl_launch_dependents();
+  pdl_wait();
   for (int e = threadIdx.x; e < kMoeMaxE; e += blockDim.x) mask[e] = 0;
   if (threadIdx.x == 0) nan_rows = 0;
   __syncthreads();
@@ -125,94 +128,137 @@ __global__ void __launch_bounds__(1024) moe_route(MoeParams p) {
   }
 }
 
-// ------------------------------------------------------------------------------ products
-// Element k of a weight row as fp32 (exact but for the product with the scale).
-BSG_DEV float element(const MoeParams& p, const MoeWeight& w, int64_t row, int e, int64_t k) {
-  const uint8_t* src = w.W + row * w.row_bytes;
-  const int64_t b = k / p.bs;
-  const uint8_t* sp = w.scales + row * w.scale_pitch;
-  const bool four = p.fmt == kInt4 || p.fmt == kNvfp4;
-  const uint32_t code = four ? (src[k >> 1] >> (4 * (k & 1))) & 15u : src[k];
-  if (p.fmt == kNvfp4) {
-    uint32_t v[4];
-    e2m1x8_to_f16x2x4(code, v);
-    return half_to_f32<false>(v[0], 0) * half_to_f32<false>(e4m3x2_to_f16x2(sp[b]), 0) * w.gscale[e];
-  }
-  if (p.fmt == kFp8)
-    return half_to_f32<false>(e4m3x2_to_f16x2(code), 0) * reinterpret_cast<const float*>(sp)[b];
-  uint32_t z = p.fmt == kInt4 ? 8u : 128u;
+}  // namespace
+
+// ------------------------------------------------------------------------------ launches
+namespace {
+
+// Blocks per SM: one n8 tile of tokens or four (more accumulators, more activation rows).
+int blocks_per_sm(int max_T) { return max_T <= 8 ? 4 : 3; }
+
+constexpr int kSmemPerSm = 233472;  // 228 KB, of which each block takes 1 KB for itself
+
+int align_up(int v, int a) { return (v + a - 1) / a * a; }
+
+// The largest unit (16, 8 or 4 bytes) that every row's scales start on and are made of, or 0.
+int copy_unit(const void* base, int64_t pitch, int bytes) {
+  for (int u = 16; u >= 4; u /= 2)
+    if (aligned_to(base, u) && pitch % u == 0 && bytes % u == 0) return u;
+  return 0;
+}
+
+int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
+  const bool four = c.fmt == kInt4 || c.fmt == kNvfp4;
+  const bool wide = c.max_T > 8;
+  const MoeWeight& w = down ? c.down : c.up;
+  MoeGemmParams p = {};
+  p.tm = down ? c.tm_down : c.tm_up;
+  p.x0 = down ? c.h_hi : c.x;
+  p.x1 = down ? c.h_lo : nullptr;
+  p.route = c.route;
+  p.scales = w.scales;
+  p.zp = w.zp;
+  p.gscale = w.gscale;
+  p.partials = c.partials;
+  p.counters = down ? c.counters_down : c.counters_up;
+  p.err = c.err;
+  p.out0 = down ? c.y : c.h_hi;
+  p.out1 = down ? nullptr : c.h_lo;
+  p.wait_ns = kDefaultWaitNs;
+  p.K = w.k;
+  p.rows = static_cast<int>(w.rows);
+  p.s_end = w.scale_pitch * w.rows * c.E;
+  p.z_end = w.zp_pitch * w.rows * c.E;
+  p.s_pitch = w.scale_pitch;
+  p.z_pitch = w.zp_pitch;
+  p.out_pitch = down ? c.H : c.I;
+  p.second = down ? 32 : static_cast<int>(c.I);
+  p.step = down ? 64 : 32;
+  p.tiles = static_cast<int>(down ? c.H / 64 : c.I / 32);
+  const int kc = four ? 256 : 128;
+  p.spt = static_cast<int>((w.k + kc - 1) / kc);
+  p.T = c.T;
+  p.top_rows = c.max_T * c.top_k;
+  p.out_bf16 = c.bf16;
+  p.bs_log2 = __builtin_ctz(static_cast<unsigned>(c.bs));
+  const int blocks = kc / c.bs;
+  p.s_bytes = blocks * (c.fmt == kFp8 ? 4 : c.fmt == kNvfp4 ? 1 : 2);
+  p.s_unit = copy_unit(w.scales, w.scale_pitch, p.s_bytes);
+  p.s_stride = p.s_unit ? p.s_bytes : (p.s_bytes + 6) / 4 * 4;
   if (w.zp) {
-    const uint8_t* zr = w.zp + row * w.zp_pitch;
-    z = p.fmt == kInt4 ? (zr[b >> 1] >> (4 * (b & 1))) & 15u : zr[b];
+    p.z_bytes = c.fmt == kInt4 ? blocks / 2 : blocks;
+    p.z_unit = copy_unit(w.zp, w.zp_pitch, p.z_bytes);
+    p.z_stride = p.z_unit ? p.z_bytes : (p.z_bytes + 6) / 4 * 4;
   }
-  return static_cast<float>(static_cast<int>(code) - static_cast<int>(z)) *
-         __half2float(reinterpret_cast<const __half*>(sp)[b]);
-}
-
-BSG_DEV float warp_sum(float v) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
-  return v;
-}
-
-BSG_DEV float act_value(const MoeParams& p, const uint16_t* v) {
-  return p.bf16 ? half_to_f32<true>(*v, 0) : half_to_f32<false>(*v, 0);
-}
-
-// One warp per (intermediate column, active expert).
-__global__ void moe_gate_up(MoeParams p) {
-  const Routing* R = p.route;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31, a = blockIdx.y;
-  if (a >= R->active || i >= p.I) return;
-  const int e = R->expert[a];
-  const int64_t row = e * 2 * p.I + i;
-  for (int r = R->off[a]; r < R->off[a + 1]; ++r) {
-    const uint16_t* x = p.x + R->token[r] * p.H;
-    float g = 0.f, u = 0.f;
-    for (int64_t k = lane; k < p.H; k += 32) {
-      const float xv = act_value(p, x + k);
-      g += xv * element(p, p.up, row, e, k);
-      u += xv * element(p, p.up, row + p.I, e, k);
-    }
-    g = warp_sum(g);
-    u = warp_sum(u);
-    if (lane == 0) p.h[r * p.I + i] = R->weight[r] * (g / (1.f + expf(-g))) * u;
+  p.side_bytes = align_up(kMoeTileRows * (p.s_stride + p.z_stride), 16);
+  const int row_bytes = (2 * kc + (four ? 64 : 32)) * (down ? 2 : 1);
+  const int budget = kSmemPerSm / blocks_per_sm(c.max_T) - 1024;
+  const int route_bytes = align_up((4 * p.top_rows + 1) * 4, 16);
+  p.slot_floats = down ? c.max_T * 16 : (wide ? 4 : 1) * 128;
+  int smem = 0;
+  for (p.stages = 12; p.stages >= 2; --p.stages) {
+    const int typical = p.stages * (c.max_T < 3 ? c.max_T : 3);
+    p.row_cap = typical > c.max_T ? typical : c.max_T;
+    int at = p.stages * kMoeBoxB;
+    p.off_side = at;
+    at += p.stages * p.side_bytes;
+    p.off_rows = at;
+    at += p.row_cap * row_bytes;
+    p.off_route = at;
+    at += route_bytes;
+    p.off_bar = at;
+    at += align_up(16 * p.stages + 8, 16);
+    p.off_sum = at;
+    at += down ? 4 * c.T * 16 * 4 : 0;
+    smem = at + 1024;  // the ring starts on a 1024-byte boundary
+    if (smem <= budget || p.stages == 2) break;
   }
-}
-
-// One warp per output column.
-__global__ void moe_down(MoeParams p) {
-  const Routing* R = p.route;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31, t = blockIdx.y;
-  if (n >= p.H) return;
-  float y = 0.f;
-  for (int a = 0; a < R->active; ++a) {
-    if (!((R->mask[a] >> t) & 1u)) continue;
-    const int e = R->expert[a], r = R->off[a] + __popc(R->mask[a] & ((1u << t) - 1u));
-    float s = 0.f;
-    for (int64_t k = lane; k < p.I; k += 32)
-      s += p.h[r * p.I + k] * element(p, p.down, e * p.H + n, e, k);
-    y += warp_sum(s);
-  }
-  if ((R->nan_rows >> t) & 1u) y = __int_as_float(0x7FC00000);
-  if (lane == 0) {
-    uint16_t* out = p.y + t * p.H + n;
-    if (p.bf16) *reinterpret_cast<__nv_bfloat16*>(out) = __float2bfloat16_rn(y);
-    else *reinterpret_cast<__half*>(out) = __float2half_rn(y);
+  const int ctas = sms * blocks_per_sm(c.max_T);
+  switch (c.fmt) {
+    case kInt4: return launch_moe_int4(p, c.bf16, wide, down, ctas, smem, s);
+    case kInt8: return launch_moe_int8(p, c.bf16, wide, down, ctas, smem, s);
+    case kFp8: return launch_moe_fp8(p, c.bf16, wide, down, ctas, smem, s);
+    default: return launch_moe_nvfp4(p, c.bf16, wide, down, ctas, smem, s);
   }
 }
 
 }  // namespace
 
+MoeLayout moe_layout(int64_t H, int64_t I, int E, int top_k, int max_T, int sms) {
+  MoeLayout l = {};
+  size_t at = 256;
+  const auto take = [&at](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  const size_t rows = static_cast<size_t>(max_T) * top_k;
+  const size_t active = rows < static_cast<size_t>(E) ? rows : static_cast<size_t>(E);
+  const size_t ctas = static_cast<size_t>(sms) * blocks_per_sm(max_T);
+  const size_t slot = max_T <= 8 ? 128 : 512;  // floats: up 128 per n8 tile, down 16 max_T
+  l.route = take(sizeof(Routing));
+  l.counters_up = take(active * (I / 32) * 4 * sizeof(unsigned));
+  l.counters_down = take(static_cast<size_t>(H / 64) * 4 * sizeof(unsigned));
+  l.partials = take(ctas * 2 * 4 * slot * sizeof(float));
+  l.h_hi = take(rows * I * 2);
+  l.h_lo = take(rows * I * 2);
+  l.total = at;
+  return l;
+}
+
+int moe_encode(CUtensorMap* tm, const MoeWeight& w, int E) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(w.row_bytes), static_cast<uint64_t>(w.rows) * E};
+  const uint64_t strides[1] = {static_cast<uint64_t>(w.row_bytes)};
+  const uint32_t box[2] = {128, 32};
+  return decode_encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, w.W, dims, strides, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
 int launch_moe(const MoeParams& p, int sms, cudaStream_t s) {
-  (void)sms;
-  moe_route<<<1, 1024, 0, s>>>(p);
-  const int experts = p.E < p.T * p.top_k ? p.E : p.T * p.top_k;
-  moe_gate_up<<<dim3(unsigned((p.I + 3) / 4), experts), 128, 0, s>>>(p);
-  moe_down<<<dim3(unsigned((p.H + 3) / 4), p.T), 128, 0, s>>>(p);
-  return decode_launched();
+  int rc = decode_launch(moe_route, dim3(1), dim3(1024), 0, s, p);
+  if (rc == BSGEMV_OK) rc = launch_product(p, false, sms, s);
+  if (rc == BSGEMV_OK) rc = launch_product(p, true, sms, s);
+  return rc;
 }
 
 }  // namespace bsg

@@ -35,19 +35,23 @@ struct MoeWeight {
   int64_t rows, k;
 };
 
+// A call, as the host code hands it to the kernels.
 struct MoeParams {
   int fmt, bf16, bs, has_zp, flags;
   int64_t H, I;
-  int E, top_k, T;
+  int E, top_k, T, max_T;
   const uint16_t* x;
   const void* logits;
   const int32_t* ids;
   const float* weights;
   MoeWeight up, down;
+  CUtensorMap tm_up, tm_down;  // weight bytes, boxes of [32 rows][128 bytes], 128-byte swizzle
   uint16_t* y;
   unsigned* err;
+  unsigned *counters_up, *counters_down;  // arrivals per (tile, decode warp), left at zero
+  float* partials;
   Routing* route;
-  float* h;   // [rows][I]
+  uint16_t *h_hi, *h_lo;       // [rows][I] bf16
 };
 
 inline MoeWeight weight_of(int fmt, int bs, int has_zp, int64_t rows, int64_t k, const void* W,
@@ -66,12 +70,26 @@ inline MoeWeight weight_of(int fmt, int bs, int has_zp, int64_t rows, int64_t k,
   return w;
 }
 
-inline size_t moe_workspace_bytes(int64_t H, int64_t I, int top_k, int max_T, int sms) {
-  (void)H;
-  (void)sms;
-  return 256 + routing_bytes() + size_t(max_T) * top_k * I * sizeof(float);
-}
+// The workspace's parts, in bytes from its start (the error word is at 0).
+struct MoeLayout {
+  size_t route, counters_up, counters_down, partials, h_hi, h_lo, total;
+};
+MoeLayout moe_layout(int64_t H, int64_t I, int E, int top_k, int max_T, int sms);
+
+// Tensor map of one stacked weight (BSGEMV_ERR_CUDA if it cannot be encoded).
+int moe_encode(CUtensorMap* tm, const MoeWeight& w, int E);
 
 int launch_moe(const MoeParams& p, int sms, cudaStream_t s);
+
+// One product's launch per weight format (a translation unit each).
+struct MoeGemmParams;
+int launch_moe_int4(const MoeGemmParams& p, bool bf16, bool wide, bool down, int ctas, int smem,
+                    cudaStream_t s);
+int launch_moe_int8(const MoeGemmParams& p, bool bf16, bool wide, bool down, int ctas, int smem,
+                    cudaStream_t s);
+int launch_moe_fp8(const MoeGemmParams& p, bool bf16, bool wide, bool down, int ctas, int smem,
+                   cudaStream_t s);
+int launch_moe_nvfp4(const MoeGemmParams& p, bool bf16, bool wide, bool down, int ctas, int smem,
+                     cudaStream_t s);
 
 }  // namespace bsg

@@ -364,14 +364,14 @@ enum bsgemv_moe_flags {
 
 /*
  * format, block_size, has_zp as bsgemv_plan, except that integer block sizes are 16, 32, 64 or
- * 128.  H and I: multiples of 64 and of block_size, at least 64, below 2^24.
- * 1 <= E <= 1024, 1 <= top_k <= min(E, 16), 1 <= max_T <= 32, flags of bsgemv_moe_flags.
+ * 128.  H and I: multiples of 64 and of block_size, at least 64, below 2^24;
+ * 2 I E and H E below 2^31.  1 <= E <= 1024, 1 <= top_k <= min(E, 16), 1 <= max_T <= 32, flags of bsgemv_moe_flags.
  */
 int bsgemv_moe_plan(bsgemv_moe_plan_t* out, int format, int block_size, int has_zp, int64_t H,
                     int64_t I, int E, int top_k, int max_T, int flags);
 
-/* Enqueue the layer for T (1 .. max_T) tokens.  x, W13, W2 and y 16-byte aligned; scales aligned
- * to their element (NVFP4: 4 bytes), logits to theirs.  Deterministic: repeated calls are
+/* Enqueue the layer for T (1 .. max_T) tokens.  x, W13, W2 and y 16-byte aligned; scales and
+ * zero points 4-byte aligned, logits to their element.  Deterministic: repeated calls are
  * bit-identical. */
 int bsgemv_moe_run(bsgemv_moe_plan_t plan, const void* x, const void* logits, const void* W13,
                    const void* scales13, const void* zp13, const void* W2, const void* scales2,
