@@ -2,7 +2,9 @@
 //
 //   route     one block: top-k of each token's logits, the experts that are wanted and their
 //             tokens (a 32-bit mask per expert: max_T <= 32)
+//             ... and, in other blocks, x packed for the tensor cores
 //   up        h[row][i] = p * silu(g) * u for every (expert, token) pair
+//   pack      h packed likewise
 //   down      y[t][n]   = sum over the token's experts, in expert order
 #include <math.h>
 
@@ -94,8 +96,9 @@ int run(bsgemv_moe_plan_s* p, const void* x, const void* logits, const int32_t* 
   q.counters_up = reinterpret_cast<unsigned*>(w + p->at.counters_up);
   q.counters_down = reinterpret_cast<unsigned*>(w + p->at.counters_down);
   q.partials = reinterpret_cast<float*>(w + p->at.partials);
-  q.h_hi = reinterpret_cast<uint16_t*>(w + p->at.h_hi);
-  q.h_lo = reinterpret_cast<uint16_t*>(w + p->at.h_lo);
+  q.h = reinterpret_cast<float*>(w + p->at.h);
+  q.x_packed = reinterpret_cast<uint8_t*>(w + p->at.x_packed);
+  q.h_packed = reinterpret_cast<uint8_t*>(w + p->at.h_packed);
   return launch_moe(q, p->sms, static_cast<cudaStream_t>(stream));
 }
 
@@ -122,7 +125,8 @@ int bsgemv_moe_plan(bsgemv_moe_plan_t* out, int format, int block_size, int has_
                           : block_size == (fmt == kFp8 ? 128 : 16);
   if (!bs_ok || (has_zp && !ints) || E > kMoeMaxE || top_k > kMoeMaxK || H % 64 || I % 64 ||
       H % block_size || I % block_size || H >= (1 << 24) || I >= (1 << 24) ||
-      2 * I * E >= (int64_t{1} << 31) || H * E >= (int64_t{1} << 31))
+      2 * I * E >= (int64_t{1} << 31) || H * E >= (int64_t{1} << 31) ||
+      moe_stages(fmt, H, I, E, top_k, max_T) >= (int64_t{1} << 31))
     return BSGEMV_ERR_UNSUPPORTED;
   int dev = -1, sms = 0;
   int rc = decode_device(&dev, &sms);
@@ -141,7 +145,7 @@ int bsgemv_moe_plan(bsgemv_moe_plan_t* out, int format, int block_size, int has_
   p->top_k = top_k;
   p->max_T = max_T;
   p->flags = flags;
-  p->at = moe_layout(H, I, E, top_k, max_T, sms);
+  p->at = moe_layout(fmt, H, I, E, top_k, max_T, sms);
   rc = decode_alloc(&p->ws, p->at.total);
   if (rc != BSGEMV_OK) {
     delete p;

@@ -3,9 +3,9 @@
 
 namespace bsg {
 
-int launch_moe_fp8(const MoeGemmParams& p, bool bf16, bool wide, bool down, int ctas, int smem,
-                    cudaStream_t s) {
-  return launch_moe_fmt<kFp8, false>(p, bf16, wide, down, ctas, smem, s);
+int launch_moe_fp8(const MoeGemmParams& p, bool wide, bool down, int ctas, int smem,
+                   cudaStream_t s) {
+  return launch_moe_fmt<kFp8, 8>(p, wide, down, ctas, smem, s);
 }
 
 }  // namespace bsg

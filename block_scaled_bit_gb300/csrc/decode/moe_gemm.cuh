@@ -17,11 +17,17 @@
 // place.  All stages are cut into equal ranges, one per block; a tile cut by a range boundary is
 // finished by the last block to arrive, which adds the parts in block order (deterministic).
 //
-// The weights go through mma.sync m16n8k16 as the A operand and the tokens as B, eight per tile
-// and at most MT tiles; the decoders and the k permutation are the GEMV's.  x is exact in
-// its own type.  h is fp32; as a 16-bit operand it is two bf16 parts, h = hi + lo, each multiplied
-// (relative error 2^-16, and the range of fp32: an f16 h would overflow above 65504 and round at
-// 2^-11, as large as the output's own rounding).  bf16 holds every format's decoded weights.
+// The weights go through mma.sync m16n8k16 as the A operand, decoded to f16 (every format's codes
+// are exact in f16, and the decoders to bf16 take three conversions more per pair at a quarter
+// of the rate), and the tokens as B, eight per tile and at most MT tiles; the decoders and the k
+// permutation are the GEMV's.  The activations come packed for this by small kernels (moe_pack):
+// per row and stage the values in f16 with a power of two taken out, and that factor, which
+// multiplies the stage's fp32 sums: f16 x as it is; bf16 x scaled to just below the top of f16's
+// range, exact for every element within 2^29 of the largest of its 128 or 256, the others off by
+// 2^-40 of that; h (fp32) likewise in two f16 parts, h = hi + lo, each multiplied: 22 bits, where
+// one part would round at 2^-12, as much as an f16 output's own rounding.  A stage's row is
+// then one bulk copy.  (Converted inside the kernel by a warp of its own, the rows took that
+// warp 300 instructions a stage, and the kernel ran at a third of the copy bandwidth.)
 // Columns of a fragment past the expert's tokens repeat its first row and are dropped; what an
 // expert adds to a token is added to that token's sum only (a NaN weight stays with its tokens).
 #pragma once
@@ -31,19 +37,28 @@
 
 namespace bsg {
 
-constexpr int kMoeThreads = 160;  // copy warp + four decode warps
+// Untiled copy of `bytes` (a multiple of 16, both addresses too), counted on `bar`.
+BSG_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst), "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+constexpr int kMoeThreads = 160;  // copy warp, four decode warps
 constexpr int kMoeTileRows = 64;
 constexpr int kMoeBoxB = kMoeTileRows * 128;
 
 struct MoeGemmParams {
   CUtensorMap tm;             // weight bytes [E * rows][row bytes], box [32][128], 128B swizzle
-  const uint16_t *x0, *x1;    // activations: x (UP), or h's two parts (DOWN)
+  const uint8_t* x;           // packed activations [token (UP) or row (DOWN)][stage][row bytes]
   const Routing* route;
   const uint8_t *scales, *zp;
   const float* gscale;        // NVFP4: [E]
   float* partials;
   unsigned *counters, *err;
-  uint16_t *out0, *out1;      // UP: h's two parts [rows][I]; DOWN: y [T][H], null
+  float* h;                   // UP: [rows][I]
+  uint16_t* y;                // DOWN: [T][H]
   uint64_t wait_ns;
   int64_t K;                  // elements of an activation row
   int64_t s_end, z_end;       // bytes of scales and zero points
@@ -54,8 +69,7 @@ struct MoeGemmParams {
   int step;                   // row distance of two tiles
   int tiles, spt;             // tiles of an expert, stages of a tile's k
   int T, top_rows;            // tokens; routing rows a call can have
-  int out_bf16;
-  int bs_log2;
+  int bf16;                   // x and y are bf16, else f16
   int s_bytes, z_bytes;       // bytes of a row's scales / zero points per stage
   int s_unit, z_unit;         // copy unit in bytes (16, 8, 4), 0: windows of words and a shift
   int s_stride, z_stride;     // bytes of a row in the ring
@@ -64,29 +78,30 @@ struct MoeGemmParams {
   int slot_floats;            // floats of a partial sum (one warp's part of a tile)
 };
 
-template <int FMT, bool BF16, int MT, bool DOWN, bool SUB2>
+// CPB: 16-byte chunks of a row per scale block (the GEMV's block_mode): 0 = a chunk holds two
+// blocks, 8 = one block is the whole stage; NVFP4 folds its scales into the operand.
+template <int FMT, int MT, bool DOWN, int CPB>
 struct MoeGemm {
   static constexpr bool kFour = FMT == kInt4 || FMT == kNvfp4;
   static constexpr bool kFold = FMT == kNvfp4;
   static constexpr bool kInts = FMT == kInt4 || FMT == kInt8;
-  static constexpr bool kOpBf16 = DOWN || BF16;      // operand type of the mma
   static constexpr int kKpc = kFour ? 32 : 16;       // k per 16-byte chunk
   static constexpr int kSteps = kKpc / 16;
   static constexpr int kKc = 8 * kKpc;               // k per stage
   static constexpr int kChunkB = 2 * kKpc;           // activation bytes of a chunk
-  static constexpr int kPitch = 2 * kKc + kChunkB;   // a row in the ring: rows start 16 banks
-                                                     // (8-bit formats: 8) apart
+  static constexpr int kPitch = moe_pitch(kFour);
   static constexpr int kParts = DOWN ? 2 : 1;
   static constexpr int kRowB = kParts * kPitch;
-  static_assert(!SUB2 || FMT == kInt4, "two scale blocks per chunk: int4 with 16-element blocks");
+  static constexpr int kSub = CPB == 0 ? 2 : 1;      // scale blocks per chunk
+  static_assert(CPB != 0 || FMT == kInt4, "two scale blocks per chunk: int4, 16-element blocks");
 
   struct Ctx {
     const MoeGemmParams& p;
     uint8_t* base;
     uint32_t base_u;
     int active;
-    int64_t s0, s1, total;
-    int G;
+    int s0, s1, total;  // this block's stages, all stages (below 2^31: the plan's condition)
+    int G, base_len, extra;  // blocks with work; the first `extra` have one stage more
     BSG_DEV uint32_t full(int i) const { return base_u + p.off_bar + 8 * i; }
     BSG_DEV uint32_t empty(int i) const { return base_u + p.off_bar + 8 * (p.stages + i); }
     BSG_DEV volatile uint32_t* abort_word() const {
@@ -103,38 +118,85 @@ struct MoeGemm {
     }
   };
 
-  // Position of a stage: active expert a, tile, stage ks of the tile's k for that expert.
-  struct Walk {
-    int a, tile, ks;
-    BSG_DEV void next(const Ctx& c) {
-      if (++ks < c.p.spt) return;
-      ks = 0;
-      if constexpr (DOWN) {
-        if (++a == c.active) { a = 0; ++tile; }
-      } else {
-        if (++tile == c.p.tiles) { tile = 0; ++a; }
-      }
-    }
+  // A run: stages ks .. ks + n - 1 of one expert's part of a tile (n ends with that part or with
+  // the block's range).
+  struct Run {
+    int a, tile, ks, n, left;  // left: stages of the range after this run
   };
-  static BSG_DEV Walk walk_at(const Ctx& c, int64_t s) {
-    Walk w;
-    const int64_t run = s / c.p.spt;
-    w.ks = static_cast<int>(s - run * c.p.spt);
+  static BSG_DEV Run first_run(const Ctx& c) {
+    Run w;
+    const int run = c.s0 / c.p.spt;
+    w.ks = c.s0 - run * c.p.spt;
     if constexpr (DOWN) {
-      w.tile = static_cast<int>(run / c.active);
-      w.a = static_cast<int>(run - static_cast<int64_t>(w.tile) * c.active);
+      w.tile = run / c.active;
+      w.a = run - w.tile * c.active;
     } else {
-      w.a = static_cast<int>(run / c.p.tiles);
-      w.tile = static_cast<int>(run - static_cast<int64_t>(w.a) * c.p.tiles);
+      w.a = run / c.p.tiles;
+      w.tile = run - w.a * c.p.tiles;
     }
+    w.left = c.s1 - c.s0;
+    w.n = min(c.p.spt - w.ks, w.left);
+    w.left -= w.n;
     return w;
+  }
+  static BSG_DEV void next_run(const Ctx& c, Run& w) {
+    w.ks = 0;
+    if constexpr (DOWN) {
+      if (++w.a == c.active) { w.a = 0; ++w.tile; }
+    } else {
+      if (++w.tile == c.p.tiles) { w.tile = 0; ++w.a; }
+    }
+    w.n = min(c.p.spt, w.left);
+    w.left -= w.n;
   }
 
   // ---------------------------------------------------------------- copy warp
-  static BSG_DEV int64_t weight_row(const Ctx& c, const Walk& w) {
-    return static_cast<int64_t>(c.expert(w.a)) * c.p.rows + static_cast<int64_t>(w.tile) * c.p.step;
+  static BSG_DEV int weight_row(const Ctx& c, const Run& w) {
+    return c.expert(w.a) * c.p.rows + w.tile * c.p.step;
   }
+  static BSG_DEV int rows_of(const Ctx& c, int a) { return c.off(a + 1) - c.off(a); }
+  static BSG_DEV int wrap(const Ctx& c, int r) { return r >= c.p.row_cap ? r - c.p.row_cap : r; }
 
+  // Scales (or zero points) of this lane's two rows of a tile, lane and lane + 32: copied in
+  // units of `unit` bytes where every row's part starts on one, else as the whole words that
+  // hold it (the reader adds the start's low two bits).  Nothing at or past `end` is read.
+  struct Side {
+    const uint8_t* src;
+    int64_t off[2];  // of the row's first byte
+    int64_t end;
+    int unit, count, stride, bytes;
+  };
+  static BSG_DEV Side side_of(const uint8_t* src, int64_t pitch, int64_t end, int unit, int stride,
+                              int bytes, int row, int second, int lane) {
+    Side s;
+    s.src = src;
+    s.off[0] = (row + lane) * pitch;
+    s.off[1] = (row + lane + second) * pitch;
+    s.end = end;
+    s.unit = unit;
+    s.count = unit ? bytes / unit : stride / 4;
+    s.stride = stride;
+    s.bytes = bytes;
+    return s;
+  }
+  template <int UNIT>
+  static BSG_DEV void side_units(const Side& s, uint32_t dst, int at, int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t off = (s.off[h] + at) & ~static_cast<int64_t>(3);
+      const int64_t left = s.end - off;
+      const uint8_t* src = s.src + off;
+      uint32_t to = dst + (lane + 32 * h) * s.stride;
+      if (left >= s.count * UNIT) {
+        for (int i = 0; i < s.count; ++i, to += UNIT, src += UNIT) cp_unit<UNIT>(to, src, UNIT);
+      } else {  // the array's last rows
+        for (int i = 0; i < s.count; ++i, to += UNIT) {
+          const int have = static_cast<int>(max(static_cast<int64_t>(0), min(left - i * UNIT, static_cast<int64_t>(UNIT))));
+          cp_unit<UNIT>(to, have > 0 ? src + i * UNIT : s.src, have);
+        }
+      }
+    }
+  }
   template <int UNIT>
   static BSG_DEV void cp_unit(uint32_t dst, const uint8_t* src, int bytes) {
     if constexpr (UNIT == 16)
@@ -145,129 +207,113 @@ struct MoeGemm {
                    "r"(bytes)
                    : "memory");
   }
-
-  // `bytes` bytes of each of the tile's 64 rows at row offset `at`: in units of `unit` bytes
-  // where every row's start is a multiple of it, else the whole words that hold them (the reader
-  // adds the start's low two bits).  Nothing at or past `end` is read.
-  template <int UNIT>
-  static BSG_DEV void side_rows(uint32_t dst, const uint8_t* src, int64_t row, int second,
-                                int64_t pitch, int64_t at, int words, int stride, int64_t end,
-                                int lane) {
-    for (int u = lane; u < kMoeTileRows * words; u += 32) {
-      const int r = u / words, i = u - r * words;
-      const int64_t grow = row + (r < 32 ? r : second + r - 32);
-      const int64_t off = ((grow * pitch + at) & ~static_cast<int64_t>(3)) + i * UNIT;
-      const int64_t left = end - off;
-      cp_unit<UNIT>(dst + r * stride + i * UNIT, src + (left > 0 ? off : 0),
-                    left >= UNIT ? UNIT : (left > 0 ? static_cast<int>(left) : 0));
-    }
-  }
-  static BSG_DEV void side_copy(uint32_t dst, const uint8_t* src, int64_t row, int second,
-                                int64_t pitch, int64_t at, int bytes, int unit, int stride,
-                                int64_t end, int lane) {
-    if (unit == 16) side_rows<16>(dst, src, row, second, pitch, at, bytes / 16, stride, end, lane);
-    else if (unit == 8) side_rows<8>(dst, src, row, second, pitch, at, bytes / 8, stride, end, lane);
-    else side_rows<4>(dst, src, row, second, pitch, at, stride / 4, stride, end, lane);
+  static BSG_DEV void side_copy(const Side& s, uint32_t dst, int ks, int lane) {
+    if (s.unit == 16) side_units<16>(s, dst, ks * s.bytes, lane);
+    else if (s.unit == 8) side_units<8>(s, dst, ks * s.bytes, lane);
+    else side_units<4>(s, dst, ks * s.bytes, lane);
   }
 
-  static BSG_DEV void issue_weights(const Ctx& c, const Walk& w, int slot, uint64_t pol, int lane) {
-    const int64_t row = weight_row(c, w);
+  // The weight boxes, scales and zero points of stages of one run.
+  struct Weights {
+    int row;
+    Side s, z;
+  };
+  static BSG_DEV Weights weights_of(const Ctx& c, const Run& w, int lane) {
+    const MoeGemmParams& p = c.p;
+    Weights x;
+    x.row = weight_row(c, w);
+    x.s = side_of(p.scales, p.s_pitch, p.s_end, p.s_unit, p.s_stride, p.s_bytes, x.row, p.second, lane);
+    if (kInts && p.zp)
+      x.z = side_of(p.zp, p.z_pitch, p.z_end, p.z_unit, p.z_stride, p.z_bytes, x.row, p.second, lane);
+    return x;
+  }
+  static BSG_DEV void issue_weights(const Ctx& c, const Weights& x, int ks, int slot, uint64_t pol,
+                                    int lane) {
     if (lane == 0) {
       const uint32_t dst = c.base_u + slot * kMoeBoxB;
-      tma_load_2d_hint(dst, &c.p.tm, w.ks * 128, static_cast<int>(row), c.full(slot), pol);
-      tma_load_2d_hint(dst + kMoeBoxB / 2, &c.p.tm, w.ks * 128,
-                       static_cast<int>(row + c.p.second), c.full(slot), pol);
+      tma_load_2d_hint(dst, &c.p.tm, ks * 128, x.row, c.full(slot), pol);
+      tma_load_2d_hint(dst + kMoeBoxB / 2, &c.p.tm, ks * 128, x.row + c.p.second, c.full(slot), pol);
     }
     const uint32_t side = c.base_u + c.p.off_side + slot * c.p.side_bytes;
-    side_copy(side, c.p.scales, row, c.p.second, c.p.s_pitch,
-              static_cast<int64_t>(w.ks) * c.p.s_bytes, c.p.s_bytes, c.p.s_unit, c.p.s_stride,
-              c.p.s_end, lane);
-    if (kInts && c.p.zp)
-      side_copy(side + kMoeTileRows * c.p.s_stride, c.p.zp, row, c.p.second, c.p.z_pitch,
-                static_cast<int64_t>(w.ks) * c.p.z_bytes, c.p.z_bytes, c.p.z_unit, c.p.z_stride,
-                c.p.z_end, lane);
+    side_copy(x.s, side, ks, lane);
+    if (kInts && c.p.zp) side_copy(x.z, side + kMoeTileRows * c.p.s_stride, ks, lane);
   }
 
-  // The stage's activations of the expert's m rows into ring rows `at` .. (modulo row_cap).
-  static BSG_DEV void issue_rows(const Ctx& c, const Walk& w, int at, int lane) {
-    const int r0 = c.off(w.a), m = c.off(w.a + 1) - r0;
-    constexpr int kUnits = kKc / 8;
-    const int64_t k0 = static_cast<int64_t>(w.ks) * kKc;
-    for (int u = lane; u < m * kUnits; u += 32) {
-      const int j = u / kUnits, i = u - j * kUnits;
-      const int64_t k = k0 + i * 8;
-      const bool in = k < c.p.K;
-      const int64_t src = (DOWN ? r0 + j : c.token(r0 + j)) * c.p.K + (in ? k : 0);
-      int ring = at + j;
-      if (ring >= c.p.row_cap) ring -= c.p.row_cap;
-      const uint32_t dst = c.base_u + c.p.off_rows + ring * kRowB + i * 16;
-      cp_async16(dst, c.p.x0 + src, in ? 16u : 0u);
-      if constexpr (DOWN) cp_async16(dst + kPitch, c.p.x1 + src, in ? 16u : 0u);
-    }
-  }
-
-  // Issue every stage of the range in order, as far ahead as the rings allow.  The weights and
-  // scales of the first stages go out before the wait for the previous kernel where they do not
-  // depend on it (DOWN: the routing is older than the previous kernel).
-  static BSG_DEV void produce(const Ctx& c, int lane) {
+  // Weights, scales and activations of every stage in order, as far ahead as the rings allow.
+  // DOWN's first weights go out before the wait for the previous kernel (they do not depend on
+  // it, and the routing is older).  Everything that a run's stages share is worked out once per
+  // run: this warp's time per stage bounds the block's rate.  Returns the stages issued.
+  static BSG_DEV int produce(const Ctx& c, int lane) {
     const MoeGemmParams& p = c.p;
     const uint64_t pol = policy_evict_first();
-    const int64_t n = c.s1 - c.s0;
     if (lane == 0) prefetch_tmap(&p.tm);
-    Walk w = walk_at(c, c.s0), tail = w;
+    Run w = first_run(c), tail = w;
     int early = 0;
     if constexpr (DOWN) {
-      Walk e = w;
-      for (; early < p.stages && early < n; ++early) {
-        if (lane == 0) mbar_expect_tx(c.full(early), kMoeBoxB);
-        issue_weights(c, e, early, pol, lane);
-        e.next(c);
+      Run e = w;
+      while (early < p.stages) {
+        const Weights x = weights_of(c, e, lane);
+        const int most = min(e.n, p.stages - early);
+        for (int i = 0; i < most; ++i, ++early) {
+          if (lane == 0) mbar_expect_tx(c.full(early), kMoeBoxB);
+          issue_weights(c, x, e.ks + i, early, pol, lane);
+        }
+        if (e.left == 0) break;
+        next_run(c, e);
       }
       pdl_wait();
     }
-    int64_t released = 0;  // stages whose slots and rows are free again
-    int used = 0, head = 0;
-    int slot = 0, tslot = 0;
+    int used = 0, head = 0, slot = 0, i = 0, free_slots = p.stages;
+    int tslot = 0, tail_m = rows_of(c, tail.a);
     uint32_t tphase = 0;
-    bool ok = true;
-    int64_t i = 0;
-    for (; i < n && ok; ++i) {
-      const int m = c.off(w.a + 1) - c.off(w.a);
-      while (i - released >= p.stages || used + m > p.row_cap) {
-        ok = mbar_wait(c.empty(tslot), tphase, p.err, kErrTimeoutEmpty, p.wait_ns);
-        if (!ok) break;
-        used -= c.off(tail.a + 1) - c.off(tail.a);
-        tail.next(c);
-        ++released;
-        if (++tslot == p.stages) { tslot = 0; tphase ^= 1u; }
+    while (true) {
+      const Weights x = weights_of(c, w, lane);
+      const int r0 = c.off(w.a), m = c.off(w.a + 1) - r0;
+      const uint32_t tx = m * kRowB;
+      const int64_t row = DOWN ? r0 + lane : (lane < m ? c.token(r0 + lane) : 0);
+      const uint8_t* src = p.x + (row * p.spt + w.ks) * kRowB;  // this lane's row (lane < m)
+      for (int k = 0; k < w.n; ++k, ++i) {
+        while (free_slots == 0 || used + m > p.row_cap) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(c.empty(tslot), tphase, p.err, kErrTimeoutEmpty,
+                                                 p.wait_ns))) {
+            if (lane == 0) *c.abort_word() = 1u;
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            return i;
+          }
+          used -= tail_m;
+          ++free_slots;
+          if (--tail.n == 0 && tail.left > 0) {
+            next_run(c, tail);
+            tail_m = rows_of(c, tail.a);
+          }
+          if (++tslot == p.stages) { tslot = 0; tphase ^= 1u; }
+        }
+        const uint32_t full = c.full(slot);
+        if (lane == 0) mbar_expect_tx(full, i < early ? tx : tx + kMoeBoxB);
+        __syncwarp();  // the bytes are expected before any lane's copy can complete
+        if (i >= early) issue_weights(c, x, w.ks + k, slot, pol, lane);
+        if (lane < m)
+          bulk_load(c.base_u + p.off_rows + wrap(c, head + lane) * kRowB, src, kRowB, full);
+        src += kRowB;
+        cp_async_mbar_arrive(full);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+        used += m;
+        --free_slots;
+        head = wrap(c, head + m);
+        if (++slot == p.stages) slot = 0;
       }
-      if (!ok) break;
-      if (i >= early) {
-        if (lane == 0) mbar_expect_tx(c.full(slot), kMoeBoxB);
-        issue_weights(c, w, slot, pol, lane);
-      }
-      issue_rows(c, w, head, lane);
-      cp_async_mbar_arrive(c.full(slot));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(c.full(slot));
-      used += m;
-      head += m;
-      if (head >= p.row_cap) head -= p.row_cap;
-      w.next(c);
-      if (++slot == p.stages) slot = 0;
+      if (w.left == 0) break;
+      next_run(c, w);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (!ok && lane == 0) {
-      *c.abort_word() = 1u;
-      // copies in flight land before the block ends: the stages issued and not yet released
-      // (tslot's full barrier has completed or is completing the phase of its current use)
-      int sl = tslot;
-      uint32_t ph = tphase;
-      for (int64_t j = released; j < i; ++j) {
-        mbar_wait(c.full(sl), ph, p.err, kErrTimeoutFull, p.wait_ns);
-        if (++sl == p.stages) { sl = 0; ph ^= 1u; }
-      }
-    }
+    return i;
+  }
+
+  // After a wait that ran out: the copies in flight land before the block ends (bounded again).
+  static BSG_DEV void drain(const Ctx& c, int n) {
+    for (int i = n > c.p.stages ? n - c.p.stages : 0; i < n; ++i)
+      mbar_wait(c.full(i % c.p.stages), (i / c.p.stages) & 1, c.p.err, kErrTimeoutFull, c.p.wait_ns);
   }
 
   // ---------------------------------------------------------------- decode warps
@@ -277,8 +323,9 @@ struct MoeGemm {
   struct Lane {
     int cw, lane, g, t;
     uint32_t w[4];  // ldmatrix address of chunk pair j in a stage's weights
+    int s[2], z[2];  // rows g and g + 8 in a stage's scales and zero points
   };
-  static BSG_DEV Lane make_lane(int cw, int lane) {
+  static BSG_DEV Lane make_lane(const MoeGemmParams& p, int cw, int lane) {
     Lane L;
     L.cw = cw;
     L.lane = lane;
@@ -287,6 +334,11 @@ struct MoeGemm {
     const int i = lane >> 3, r = tile_row(cw, i & 1) + (lane & 7);
 #pragma unroll
     for (int j = 0; j < 4; ++j) L.w[j] = r * 128 + (((2 * j + (i >> 1)) ^ (r & 7)) << 4);
+#pragma unroll
+    for (int rr = 0; rr < 2; ++rr) {
+      L.s[rr] = (tile_row(cw, rr) + L.g) * p.s_stride;
+      L.z[rr] = kMoeTileRows * p.s_stride + (tile_row(cw, rr) + L.g) * p.z_stride;
+    }
     return L;
   }
 
@@ -322,109 +374,98 @@ struct MoeGemm {
     return lsh<uint8_t>(row + blk);
   }
 
-  // acc += the stage's products.  rows[mt]: the ring row of this lane's column in n8 tile mt.
-  static BSG_DEV void consume(const Ctx& c, const Lane& L, const Walk& w, int slot, int nt,
-                              const uint8_t* const (&rows)[MT], float (&acc)[MT][4]) {
+  // The stage's products with one n8 tile of tokens.  row: the ring row of this lane's B column.
+  // (An expert with more than eight tokens has its stage decoded once for each eight: the
+  // weights come from HBM once all the same, and all but the first eight are rare.)
+  // ss, zs: what the rows' windows of words add to their starts.
+  static BSG_DEV void consume(const Ctx& c, const Lane& L, int ks, int slot, const uint8_t* row,
+                              const int (&ss)[2], const int (&zs)[2], float (&st)[4]) {
     const MoeGemmParams& p = c.p;
     const uint32_t wa = c.base_u + slot * kMoeBoxB;
+    // chunk pair j, loaded one pair ahead: (chunk 2j: row g, g + 8), (chunk 2j + 1: row g, g + 8)
+    uint32_t v[2][4];
+    ldsm_x4_at<0>(wa + L.w[0], v[0][0], v[0][1], v[0][2], v[0][3]);
     const uint8_t* side = c.base + p.off_side + slot * p.side_bytes;
-    const int left = static_cast<int>(p.K - static_cast<int64_t>(w.ks) * kKc);
+    const int left = static_cast<int>(p.K) - ks * kKc;
     const int pairs = left >= kKc ? 4 : (left + 2 * kKpc - 1) / (2 * kKpc);
-    const uint8_t *sr[2], *zr[2];
-    {
-      const int64_t row = weight_row(c, w);
-#pragma unroll
-      for (int rr = 0; rr < 2; ++rr) {
-        const int r = tile_row(L.cw, rr) + L.g;
-        const int64_t grow = row + (r < 32 ? r : p.second + r - 32);
-        sr[rr] = side + r * p.s_stride;
-        zr[rr] = side + kMoeTileRows * p.s_stride + r * p.z_stride;
-        if (p.s_unit == 0)
-          sr[rr] += (grow * p.s_pitch + static_cast<int64_t>(w.ks) * p.s_bytes) & 3;
-        if (kInts && p.z_unit == 0)
-          zr[rr] += (grow * p.z_pitch + static_cast<int64_t>(w.ks) * p.z_bytes) & 3;
-      }
-    }
-    const int bmask = (1 << p.bs_log2) - 1;
-    float s[2] = {0.f, 0.f}, s2[2] = {0.f, 0.f};
+    const uint8_t* const sr[2] = {side + L.s[0] + ss[0], side + L.s[1] + ss[1]};
+    const uint8_t* const zr[2] = {side + L.z[0] + zs[0], side + L.z[1] + zs[1]};
     uint32_t zl[2] = {0u, 0u}, zh[2] = {0u, 0u};
-    float tmp[SUB2 ? 2 : 1][MT][4];
+    if constexpr (kInts)
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) zp_consts<FMT, false>(FMT == kInt4 ? 8u : 128u, zl[rr], zh[rr]);
+    float tmp[kSub][4];  // a scale block's sums
+#pragma unroll
+    for (int x = 0; x < 4; ++x) st[x] = 0.f;
+    float s[kSub][2];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (j >= pairs) break;
-      uint32_t v[4];
-      ldsm_x4_at<0>(wa + L.w[j], v[0], v[1], v[2], v[3]);
+      if (j < 3)
+        ldsm_x4_at<0>(wa + L.w[j + 1], v[(j + 1) & 1][0], v[(j + 1) & 1][1], v[(j + 1) & 1][2],
+                      v[(j + 1) & 1][3]);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const int chunk = 2 * j + q, k = chunk * kKpc;
-        const uint32_t lo = v[2 * q], hi = v[2 * q + 1];
+        const int chunk = 2 * j + q;
+        const uint32_t lo = v[j & 1][2 * q], hi = v[j & 1][2 * q + 1];
         uint32_t a[kSteps][4];
-        bool opens = true, closes = true;
+        constexpr int kRun = CPB == 0 ? 1 : CPB;
+        const bool opens = !kFold && chunk % kRun == 0, closes = !kFold && (chunk + 1) % kRun == 0;
         if constexpr (kFold) {
 #pragma unroll
           for (int rr = 0; rr < 2; ++rr)  // 16-element block 2 chunk + t / 2
             zl[rr] = e4m3x2_to_f16x2(0x0101u * lsh<uint8_t>(sr[rr] + 2 * chunk + (L.t >> 1)));
-          decode_nvfp4<kOpBf16>(lo, hi, zl[0], zl[1], a);
+          decode_nvfp4<false>(lo, hi, zl[0], zl[1], a);
         } else {
-          opens = SUB2 || (k & bmask) == 0;
-          closes = SUB2 || ((k + kKpc) & bmask) == 0;
           if (opens) {
-            const int blk = k >> p.bs_log2;
+            const int blk = CPB == 0 ? 2 * chunk : chunk / kRun;
 #pragma unroll
             for (int rr = 0; rr < 2; ++rr) {
-              s[rr] = scale_at(sr[rr], blk);
-              if constexpr (SUB2) s2[rr] = scale_at(sr[rr], blk + 1);
-              if constexpr (kInts) {
-                uint32_t z = FMT == kInt4 ? 8u : 128u;
-                if (p.zp) z = zp_at(zr[rr], SUB2 ? blk + (L.t >> 1) : blk);
-                zp_consts<FMT, kOpBf16>(z, zl[rr], zh[rr]);
-              }
+#pragma unroll
+              for (int u = 0; u < kSub; ++u) s[u][rr] = scale_at(sr[rr], blk + u);
+              if constexpr (kInts)
+                if (p.zp)
+                  zp_consts<FMT, false>(zp_at(zr[rr], CPB == 0 ? blk + (L.t >> 1) : blk), zl[rr], zh[rr]);
             }
           }
-          if constexpr (FMT == kInt4) decode_int4<kOpBf16>(lo, hi, zl[0], zh[0], zl[1], zh[1], a);
-          else if constexpr (FMT == kInt8) decode_int8<kOpBf16>(lo, hi, zl[0], zl[1], a);
-          else decode_fp8<kOpBf16>(lo, hi, a);
+          if constexpr (FMT == kInt4) decode_int4<false>(lo, hi, zl[0], zh[0], zl[1], zh[1], a);
+          else if constexpr (FMT == kInt8) decode_int8<false>(lo, hi, zl[0], zl[1], a);
+          else decode_fp8<false>(lo, hi, a);
         }
+        uint32_t b[kParts][kSteps][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          if (MT > 1 && mt >= nt) break;
-          if (!kFold && opens) {
+        for (int part = 0; part < kParts; ++part)
+          fragment(row + part * kPitch, L.t, chunk, b[part]);
 #pragma unroll
-            for (int u = 0; u < (SUB2 ? 2 : 1); ++u)
+        for (int part = 0; part < kParts; ++part)
 #pragma unroll
-              for (int x = 0; x < 4; ++x) tmp[u][mt][x] = 0.f;
-          }
+          for (int i = 0; i < kSteps; ++i) {
+            if constexpr (kFold) {
+              mma16816<false>(st, a[i], b[part][i][0], b[part][i][1]);
+            } else {
+              const bool first = opens && part == 0 && i == 0;
 #pragma unroll
-          for (int part = 0; part < kParts; ++part) {
-            uint32_t b[kSteps][2];
-            fragment(rows[mt] + part * kPitch, L.t, chunk, b);
-#pragma unroll
-            for (int st = 0; st < kSteps; ++st) {
-              if constexpr (kFold) {
-                mma16816<kOpBf16>(acc[mt], a[st], b[st][0], b[st][1]);
-              } else if constexpr (SUB2) {  // quad lanes t < 2 hold the chunk's first block
-                const bool first = L.t < 2;
-                mma16816<kOpBf16>(tmp[0][mt], a[st], first ? b[st][0] : 0u, first ? b[st][1] : 0u);
-                mma16816<kOpBf16>(tmp[SUB2][mt], a[st], first ? 0u : b[st][0], first ? 0u : b[st][1]);
-              } else {
-                mma16816<kOpBf16>(tmp[0][mt], a[st], b[st][0], b[st][1]);
+              for (int u = 0; u < kSub; ++u) {
+                // two blocks in a chunk: quad lanes t < 2 hold the first
+                const bool mine = kSub == 1 || (L.t >> 1) == u;
+                const uint32_t b0 = mine ? b[part][i][0] : 0u, b1 = mine ? b[part][i][1] : 0u;
+                if (first) mma16816_zc<false>(tmp[u], a[i], b0, b1);
+                else mma16816<false>(tmp[u], a[i], b0, b1);
               }
             }
           }
-          if (!kFold && closes) {
+        if (closes) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              acc[mt][x] = fmaf(tmp[0][mt][x], s[x >> 1], acc[mt][x]);
-              if constexpr (SUB2) acc[mt][x] = fmaf(tmp[SUB2][mt][x], s2[x >> 1], acc[mt][x]);
-            }
-          }
+          for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) st[x] = fmaf(tmp[u][x], s[u][x >> 1], st[x]);
         }
       }
     }
   }
 
-  // h = p silu(g) u of this lane's two columns per n8 tile, as two bf16 parts.
-  static BSG_DEV void store_h(const Ctx& c, const Lane& L, int a, int tile, int nt,
+  // h = p silu(g) u of this lane's two columns per n8 tile.
+  static BSG_DEV void store_h(const Ctx& c, const Lane& L, int a, int tile,
                               const float (&acc)[MT][4]) {
     const MoeGemmParams& p = c.p;
     const int r0 = c.off(a), m = c.off(a + 1) - r0;
@@ -437,15 +478,8 @@ struct MoeGemm {
         const int j = 8 * mt + 2 * L.t + x;
         if (j >= m) continue;
         const float g = acc[mt][x] * gs, u = acc[mt][2 + x] * gs;
-        const float h = c.weight(r0 + j) * (g / (1.f + expf(-g))) * u;
-        const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-        const float hf = __bfloat162float(hi);
-        const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(hf) ? h - hf : 0.f);
-        const int64_t at = (r0 + j) * p.out_pitch + col;
-        p.out0[at] = __bfloat16_as_ushort(hi);
-        p.out1[at] = __bfloat16_as_ushort(lo);
+        p.h[(r0 + j) * p.out_pitch + col] = c.weight(r0 + j) * (g / (1.f + expf(-g))) * u;
       }
-    (void)nt;
   }
 
   // DOWN: add an expert's products to the sums of its tokens (this warp's 16 rows).
@@ -470,29 +504,29 @@ struct MoeGemm {
     const int t = idx >> 4;
     if ((c.p.route->nan_rows >> t) & 1u) v = __int_as_float(0x7FC00000);
     const int64_t at = t * c.p.out_pitch + static_cast<int64_t>(tile) * 64 + 16 * cw + (idx & 15);
-    c.p.out0[at] = c.p.out_bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v))
-                                : __half_as_ushort(__float2half_rn(v));
+    c.p.y[at] = c.p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v))
+                         : __half_as_ushort(__float2half_rn(v));
   }
 
   // Block that holds stage s, and the first stage of block b's range.
-  static BSG_DEV int owner(const Ctx& c, int64_t s) {
-    return static_cast<int>(((s + 1) * c.G - 1) / c.total);
+  static BSG_DEV int owner(const Ctx& c, int s) {
+    const int cut = c.extra * (c.base_len + 1);
+    return s < cut ? s / (c.base_len + 1) : c.extra + (s - cut) / c.base_len;
   }
-  static BSG_DEV int64_t start(const Ctx& c, int b) { return c.total * b / c.G; }
+  static BSG_DEV int start(const Ctx& c, int b) { return b * c.base_len + min(b, c.extra); }
 
-  // Stages of a tile (the unit that is finished in one place) and the number of the tile.
-  static BSG_DEV int64_t tile_len(const Ctx& c) {
-    return DOWN ? static_cast<int64_t>(c.active) * c.p.spt : c.p.spt;
-  }
+  // Stages of a tile (the unit that is finished in one place).
+  static BSG_DEV int tile_len(const Ctx& c) { return DOWN ? c.active * c.p.spt : c.p.spt; }
 
   static BSG_DEV float* partial(const Ctx& c, int block, int which, int cw) {
     return c.p.partials + ((static_cast<int64_t>(block) * 2 + which) * 4 + cw) * c.p.slot_floats;
   }
 
   // A part of a tile is in the workspace: the last of its blocks to come adds the parts, in block
-  // order, and finishes the tile.
-  static BSG_DEV void arrive(const Ctx& c, const Lane& L, int64_t number) {
-    const int64_t len = tile_len(c), x0 = number * len;
+  // order, and finishes the tile.  (The parts' loads go out eight at a time; one after the other
+  // they took longer than the products of a small call.)
+  static BSG_DEV void arrive(const Ctx& c, const Lane& L, int number) {
+    const int len = tile_len(c), x0 = number * len;
     const int first = owner(c, x0), last = owner(c, x0 + len - 1);
     __syncwarp();
     unsigned old = 0;
@@ -501,39 +535,54 @@ struct MoeGemm {
     if (old != static_cast<unsigned>(last - first)) return;
     __syncwarp();
     if (L.lane == 0) c.p.counters[number * 4 + L.cw] = 0u;
+    // the first block's part opens the tile, the others' continue it
+    const int64_t stride = static_cast<int64_t>(c.p.slot_floats) * 8;  // of two blocks
+    const float* src0 = partial(c, first, 1, L.cw);
+    const float* src = partial(c, first, 0, L.cw);  // + (b - first) * stride
+    const int n = last - first + 1;
     if constexpr (DOWN) {
       for (int i = L.lane; i < c.p.T * 16; i += 32) {
         float v = 0.f;
-        for (int b = first; b <= last; ++b)
-          v += __ldcg(partial(c, b, start(c, b) <= x0 ? 1 : 0, L.cw) + i);
-        store_y(c, L.cw, static_cast<int>(number), i, v);
+        for (int b0 = 0; b0 < n; b0 += 8) {
+          float u[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            u[j] = b0 + j < n ? __ldcg((b0 + j ? src + (b0 + j) * stride : src0) + i) : 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v += u[j];
+        }
+        store_y(c, L.cw, number, i, v);
       }
     } else {
-      const int a = static_cast<int>(number / c.p.tiles);
       float acc[MT][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) acc[mt][x] = 0.f;
-      for (int b = first; b <= last; ++b) {
-        const float4* src = reinterpret_cast<const float4*>(
-            partial(c, b, start(c, b) <= x0 ? 1 : 0, L.cw)) + L.lane;
+        for (int b0 = 0; b0 < n; b0 += 4) {
+          float4 u[4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const float4 v = __ldcg(src + mt * 32);
-          acc[mt][0] += v.x;
-          acc[mt][1] += v.y;
-          acc[mt][2] += v.z;
-          acc[mt][3] += v.w;
+          for (int j = 0; j < 4; ++j)
+            u[j] = b0 + j < n ? __ldcg(reinterpret_cast<const float4*>(
+                                    b0 + j ? src + (b0 + j) * stride : src0) + L.lane + mt * 32)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[mt][0] += u[j].x;
+            acc[mt][1] += u[j].y;
+            acc[mt][2] += u[j].z;
+            acc[mt][3] += u[j].w;
+          }
         }
       }
-      store_h(c, L, a, static_cast<int>(number - static_cast<int64_t>(a) * c.p.tiles), MT, acc);
+      const int a = number / c.p.tiles;
+      store_h(c, L, a, number - a * c.p.tiles, acc);
     }
   }
 
   static BSG_DEV void work(const Ctx& c, int cw, int lane) {
     const MoeGemmParams& p = c.p;
-    const Lane L = make_lane(cw, lane);
+    const Lane L = make_lane(p, cw, lane);
     if constexpr (DOWN) {
       for (int i = lane; i < p.T * 16; i += 32) c.sums(cw)[i] = 0.f;
       __syncwarp();
@@ -541,30 +590,54 @@ struct MoeGemm {
     int slot = 0, head = 0;
     uint32_t phase = 0;
     bool ok = true;
-    Walk w = walk_at(c, c.s0);
-    int64_t s = c.s0;
-    int64_t seg = s;  // DOWN: first stage of the tile segment being summed
-    while (s < c.s1) {
-      const int n = static_cast<int>(min(static_cast<int64_t>(p.spt - w.ks), c.s1 - s));
+    Run w = first_run(c);
+    int s = c.s0;
+    int seg = s;  // DOWN: first stage of the tile segment being summed
+    while (true) {
+      const int n = w.n;
       const int r0 = c.off(w.a), m = c.off(w.a + 1) - r0, nt = (m + 7) / 8;
       float acc[MT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int x = 0; x < 4; ++x) acc[mt][x] = 0.f;
-      Walk v = w;
-      for (int i = 0; i < n; ++i, ++v.ks) {
-        ok = ok && mbar_wait(c.full(slot), phase, p.err, kErrTimeoutFull, p.wait_ns);
-        if (ok) {
-          const uint8_t* rows[MT];
+      uint32_t sw[2] = {0u, 0u}, zw[2] = {0u, 0u};  // starts of the rows' scales, low bits
+      if (p.s_unit == 0 || p.z_unit == 0) {
+        const uint32_t row = static_cast<uint32_t>(weight_row(c, w));
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const int j = 8 * mt + L.g;
-            int ring = head + (j < m ? j : 0);
-            if (ring >= p.row_cap) ring -= p.row_cap;
-            rows[mt] = c.base + p.off_rows + ring * kRowB;
+        for (int rr = 0; rr < 2; ++rr) {
+          const uint32_t r = tile_row(cw, rr) + L.g, at = row + (r < 32 ? r : p.second + r - 32);
+          sw[rr] = at * static_cast<uint32_t>(p.s_pitch);
+          zw[rr] = at * static_cast<uint32_t>(p.z_pitch);
+        }
+      }
+      for (int i = 0; i < n; ++i) {
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(c.full(slot), phase, p.err, kErrTimeoutFull,
+                                                     p.wait_ns));
+        if (ok) {
+          const uint32_t ks = w.ks + i;
+          int ss[2] = {0, 0}, zs[2] = {0, 0};
+#pragma unroll
+          for (int rr = 0; rr < 2; ++rr) {
+            if (p.s_unit == 0) ss[rr] = (sw[rr] + ks * p.s_bytes) & 3;
+            if (kInts && p.z_unit == 0) zs[rr] = (zw[rr] + ks * p.z_bytes) & 3;
           }
-          consume(c, L, v, slot, nt, rows, acc);
+          for (int grp = 0; grp < nt; ++grp) {
+            const auto row_of = [&](int col) {
+              return c.base + p.off_rows + wrap(c, head + (col < m ? col : 0)) * kRowB;
+            };
+            float st[4];
+            consume(c, L, ks, slot, row_of(8 * grp + L.g), ss, zs, st);
+            const int col = 8 * grp + 2 * L.t;  // this lane's two result columns
+            const float f0 = lsh<float>(row_of(col) + 2 * kKc);
+            const float f1 = lsh<float>(row_of(col + 1) + 2 * kKc);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              if (MT == 1 || mt == grp) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) acc[mt][x] = fmaf(st[x], x & 1 ? f1 : f0, acc[mt][x]);
+              }
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(c.empty(slot));
         }
@@ -578,7 +651,7 @@ struct MoeGemm {
         s += n;
         const bool tile_ends = ends && w.a + 1 == c.active;
         if (tile_ends || s == c.s1) {
-          const int64_t x0 = static_cast<int64_t>(w.tile) * tile_len(c);
+          const int x0 = w.tile * tile_len(c);
           float* sum = c.sums(cw);
           if (tile_ends && seg == x0) {
             for (int i = lane; i < p.T * 16; i += 32) store_y(c, cw, w.tile, i, sum[i]);
@@ -594,17 +667,17 @@ struct MoeGemm {
       } else {
         s += n;
         if (opens && ends) {
-          store_h(c, L, w.a, w.tile, nt, acc);
+          store_h(c, L, w.a, w.tile, acc);
         } else {
           float4* dst = reinterpret_cast<float4*>(partial(c, blockIdx.x, opens ? 1 : 0, cw)) + lane;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
             __stcg(dst + mt * 32, make_float4(acc[mt][0], acc[mt][1], acc[mt][2], acc[mt][3]));
-          arrive(c, L, static_cast<int64_t>(w.a) * p.tiles + w.tile);
+          arrive(c, L, w.a * p.tiles + w.tile);
         }
       }
-      w.ks += n - 1;
-      w.next(c);
+      if (w.left == 0) break;
+      next_run(c, w);
     }
     if (!ok && lane == 0) *c.abort_word() = 1u;
   }
@@ -612,7 +685,7 @@ struct MoeGemm {
   static BSG_DEV void block(const MoeGemmParams& p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    Ctx c{p, base, smem_u32(base), 0, 0, 0, 0, 0};
+    Ctx c{p, base, smem_u32(base), 0, 0, 0, 0, 0, 0, 0};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
       for (int i = 0; i < p.stages; ++i) {
@@ -627,44 +700,44 @@ struct MoeGemm {
     if constexpr (!DOWN) pdl_wait();
     pdl_launch_dependents();
     const Routing* R = p.route;
-    c.active = R->active;
     int* to = reinterpret_cast<int*>(base + p.off_route);
-    for (int i = threadIdx.x; i <= c.active; i += kMoeThreads) {
-      if (i < c.active) to[i] = R->expert[i];
+    for (int i = threadIdx.x; i < p.top_rows; i += kMoeThreads) {
+      to[i] = R->expert[i];
       to[p.top_rows + i] = R->off[i];
-    }
-    const int rows = R->off[c.active];
-    for (int i = threadIdx.x; i < rows; i += kMoeThreads) {
       to[2 * p.top_rows + 1 + i] = R->token[i];
       to[3 * p.top_rows + 1 + i] = __float_as_int(R->weight[i]);
     }
+    if (threadIdx.x == 0) to[2 * p.top_rows] = R->off[p.top_rows];
+    c.active = R->active;
     __syncthreads();
-    c.total = static_cast<int64_t>(c.active) * p.tiles * p.spt;
-    c.G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), c.total));
+    c.total = c.active * p.tiles * p.spt;
+    c.G = min(static_cast<int>(gridDim.x), c.total);
     if (static_cast<int>(blockIdx.x) < c.G) {
+      c.base_len = c.total / c.G;
+      c.extra = c.total - c.base_len * c.G;
       c.s0 = start(c, blockIdx.x);
       c.s1 = start(c, blockIdx.x + 1);
-      if (warp == 0) produce(c, lane);
+      int issued = 0;
+      if (warp == 0) issued = produce(c, lane);
       else work(c, warp - 1, lane);
-    } else {
-      if constexpr (DOWN) {
-        pdl_wait();
-        if (c.total == 0)  // no token chose anything: empty rows are 0, NaN rows NaN
-          for (int64_t i = static_cast<int64_t>(blockIdx.x) * kMoeThreads + threadIdx.x;
-               i < p.T * p.out_pitch; i += static_cast<int64_t>(gridDim.x) * kMoeThreads) {
-            const int t = static_cast<int>(i / p.out_pitch);
-            const bool nan = (R->nan_rows >> t) & 1u;
-            p.out0[i] = nan ? (p.out_bf16 ? 0x7FC0 : 0x7E00) : 0;
-          }
-      }
+      __syncthreads();
+      if (*c.abort_word() != 0u && threadIdx.x == 0) drain(c, issued);
+    } else if constexpr (DOWN) {
+      pdl_wait();
+      if (c.total == 0)  // no token chose anything: empty rows are 0, NaN rows NaN
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * kMoeThreads + threadIdx.x;
+             i < p.T * p.out_pitch; i += static_cast<int64_t>(gridDim.x) * kMoeThreads) {
+          const bool nan = (R->nan_rows >> (i / p.out_pitch)) & 1u;
+          p.y[i] = nan ? (p.bf16 ? 0x7FC0 : 0x7E00) : 0;
+        }
     }
   }
 };
 
-template <int FMT, bool BF16, int MT, bool DOWN, bool SUB2>
+template <int FMT, int MT, bool DOWN, int CPB>
 __global__ void __launch_bounds__(kMoeThreads, MT == 1 ? 4 : 3)
     moe_gemm_kernel(const __grid_constant__ MoeGemmParams p) {
-  MoeGemm<FMT, BF16, MT, DOWN, SUB2>::block(p);
+  MoeGemm<FMT, MT, DOWN, CPB>::block(p);
 }
 
 }  // namespace bsg

@@ -3,10 +3,14 @@
 
 namespace bsg {
 
-int launch_moe_int4(const MoeGemmParams& p, bool bf16, bool wide, bool down, int ctas, int smem,
+int launch_moe_int4(const MoeGemmParams& p, int cpb, bool wide, bool down, int ctas, int smem,
                     cudaStream_t s) {
-  if (p.bs_log2 == 4) return launch_moe_fmt<kInt4, true>(p, bf16, wide, down, ctas, smem, s);
-  return launch_moe_fmt<kInt4, false>(p, bf16, wide, down, ctas, smem, s);
+  switch (cpb) {
+    case 0: return launch_moe_fmt<kInt4, 0>(p, wide, down, ctas, smem, s);
+    case 1: return launch_moe_fmt<kInt4, 1>(p, wide, down, ctas, smem, s);
+    case 2: return launch_moe_fmt<kInt4, 2>(p, wide, down, ctas, smem, s);
+    default: return launch_moe_fmt<kInt4, 4>(p, wide, down, ctas, smem, s);
+  }
 }
 
 }  // namespace bsg

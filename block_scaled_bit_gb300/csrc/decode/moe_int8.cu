@@ -3,9 +3,14 @@
 
 namespace bsg {
 
-int launch_moe_int8(const MoeGemmParams& p, bool bf16, bool wide, bool down, int ctas, int smem,
+int launch_moe_int8(const MoeGemmParams& p, int cpb, bool wide, bool down, int ctas, int smem,
                     cudaStream_t s) {
-  return launch_moe_fmt<kInt8, false>(p, bf16, wide, down, ctas, smem, s);
+  switch (cpb) {
+    case 1: return launch_moe_fmt<kInt8, 1>(p, wide, down, ctas, smem, s);
+    case 2: return launch_moe_fmt<kInt8, 2>(p, wide, down, ctas, smem, s);
+    case 4: return launch_moe_fmt<kInt8, 4>(p, wide, down, ctas, smem, s);
+    default: return launch_moe_fmt<kInt8, 8>(p, wide, down, ctas, smem, s);
+  }
 }
 
 }  // namespace bsg

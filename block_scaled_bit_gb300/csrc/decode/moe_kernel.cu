@@ -13,7 +13,165 @@ BSG_DEV float logit_at(const MoeParams& p, int t, int e) {
   return p.bf16 ? half_to_f32<true>(v, 0) : half_to_f32<false>(v, 0);
 }
 
-__global__ void __launch_bounds__(1024) moe_route(const __grid_constant__ MoeParams p) {
+// Order of fp32 values as unsigned integers (-0 below +0 does not arise: +0 is added first).
+BSG_DEV uint32_t order_of(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+
+// One warp's token: the top_k of its logits, N per lane in registers.  Each pick takes the
+// largest value left, among equal ones the lowest index (two warp reductions).
+template <int N>
+BSG_DEV void choose(const MoeParams& p, int t, int lane, int* ids, float* wts, uint32_t* nan_rows) {
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = lane + 32 * i;
+    v[i] = e < p.E ? logit_at(p, t, e) + 0.f : -INFINITY;
+  }
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) bad |= isnan(v[i]) || v[i] == INFINITY;
+  bad = __any_sync(~0u, bad);
+  float top = -INFINITY, chosen = 0.f, total = 0.f, mine = 0.f;
+  int my_id = -1;
+  const uint32_t none = order_of(-INFINITY);
+  for (int j = 0; j < p.top_k; ++j) {
+    float best = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) best = fmaxf(best, v[i]);
+    const uint32_t key = __reduce_max_sync(~0u, order_of(best));
+    if (bad || key == none) break;
+    int at = kMoeMaxE;
+#pragma unroll
+    for (int i = N - 1; i >= 0; --i)
+      if (order_of(v[i]) == key) at = lane + 32 * i;
+    at = static_cast<int>(__reduce_min_sync(~0u, static_cast<unsigned>(at)));
+    const float value = __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+    if (j == 0) {
+      top = value;
+      if (!(p.flags & BSGEMV_MOE_RENORMALIZE)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) total += expf(v[i] - top);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(~0u, total, d);
+      }
+    }
+    const float q = expf(value - top);
+    chosen += q;
+    if (lane == j) {
+      my_id = at;
+      mine = q;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (lane + 32 * i == at) v[i] = -INFINITY;
+  }
+  if (p.flags & BSGEMV_MOE_RENORMALIZE) total = chosen;
+  if (lane < p.top_k) {
+    ids[lane] = my_id;
+    wts[lane] = mine / total;
+  }
+  if (bad && lane == 0) atomicOr(nan_rows, 1u << t);
+}
+
+// ------------------------------------------------------------------------------ packing
+BSG_DEV uint32_t pack_f16(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int N>
+BSG_DEV void put(uint8_t* dst, const uint32_t (&h)[N]) {
+  if constexpr (N == 4) *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+  else *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[1]);
+}
+
+// One warp packs one stage of a row, PER consecutive values a lane (see moe_gemm.cuh): the
+// largest finite magnitude scaled into [2^14, 2^15), f16 values (PARTS = 2: and their remainders),
+// the factor that undoes the scale.
+template <int PER, int PARTS>
+BSG_DEV void pack_stage(float (&v)[PER], uint8_t* dst, int lane) {
+  constexpr int kPitch = moe_pitch(PER == 8);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+    top = max(top, m < 0x7F800000u ? m : 0u);
+  }
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  const int e = min(max(static_cast<int>(top >> 23), 16), 240);  // scale and factor stay normal
+  const float scale = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - e) << 23);
+  if (lane == 0)
+    *reinterpret_cast<float*>(dst + 64 * PER) = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+  uint32_t hi[PER / 2];
+#pragma unroll
+  for (int i = 0; i < PER / 2; ++i) {
+    v[2 * i] *= scale;
+    v[2 * i + 1] *= scale;
+    hi[i] = pack_f16(v[2 * i], v[2 * i + 1]);
+  }
+  put(dst + lane * (2 * PER), hi);
+  if constexpr (PARTS == 2) {
+    uint32_t lo[PER / 2];
+#pragma unroll
+    for (int i = 0; i < PER / 2; ++i) {
+      const float a = half_to_f32<false>(hi[i], 0), b = half_to_f32<false>(hi[i], 1);
+      lo[i] = pack_f16(isfinite(a) ? v[2 * i] - a : 0.f, isfinite(b) ? v[2 * i + 1] - b : 0.f);
+    }
+    put(dst + kPitch + lane * (2 * PER), lo);
+  }
+}
+
+// Stage `ks` of token t's activations.  (k past the row packs zeros; K is a multiple of 64.)
+template <int PER>
+BSG_DEV void pack_x(const MoeParams& p, int t, int ks, int spt, int lane) {
+  uint8_t* dst = p.x_packed + (static_cast<int64_t>(t) * spt + ks) * moe_pitch(PER == 8);
+  const int64_t k = static_cast<int64_t>(ks) * (32 * PER) + lane * PER;
+  const uint2* src = reinterpret_cast<const uint2*>(p.x + t * p.H + (k < p.H ? k : 0));
+  uint32_t raw[PER / 2];
+#pragma unroll
+  for (int i = 0; i < PER / 4; ++i) {
+    const uint2 u = k < p.H ? __ldg(src + i) : make_uint2(0u, 0u);
+    raw[2 * i] = u.x;
+    raw[2 * i + 1] = u.y;
+  }
+  if (!p.bf16) {
+    put(dst + lane * (2 * PER), raw);
+    if (lane == 0) *reinterpret_cast<float*>(dst + 64 * PER) = 1.f;
+    return;
+  }
+  float v[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) v[i] = half_to_f32<true>(raw[i / 2], i & 1);
+  pack_stage<PER, 1>(v, dst, lane);
+}
+
+// h packed, one warp per row and stage.
+template <int PER>
+__global__ void __launch_bounds__(256) moe_pack(const __grid_constant__ MoeParams p, int spt) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int unit = blockIdx.x * 8 + (threadIdx.x >> 5), r = unit / spt, ks = unit - r * spt;
+  if (r >= p.route->off[p.route->active]) return;
+  const int64_t k = static_cast<int64_t>(ks) * (32 * PER) + lane * PER;
+  const float4* src = reinterpret_cast<const float4*>(p.h + r * p.I + (k < p.I ? k : 0));
+  float v[PER];
+#pragma unroll
+  for (int i = 0; i < PER / 4; ++i) {
+    const float4 f = k < p.I ? __ldcg(src + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    v[4 * i] = f.x;
+    v[4 * i + 1] = f.y;
+    v[4 * i + 2] = f.z;
+    v[4 * i + 3] = f.w;
+  }
+  pack_stage<PER, 2>(v, p.h_packed + static_cast<int64_t>(unit) * 2 * moe_pitch(PER == 8), lane);
+}
+
+// Block 0 routes: a warp per token, then a thread per expert.  The other blocks pack x, one warp
+// per token and stage.
+__global__ void __launch_bounds__(1024) moe_route(const __grid_constant__ MoeParams p, int spt) {
   __shared__ uint32_t mask[kMoeMaxE];
   __shared__ int ids[kMoeMaxT][kMoeMaxK];
   __shared__ float wts[kMoeMaxT][kMoeMaxK];
@@ -21,72 +179,36 @@ __global__ void __launch_bounds__(1024) moe_route(const __grid_constant__ MoePar
   __shared__ int warp_a[32], warp_r[32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   pdl_launch_dependents();
-  pdl_wait();
-  for (int e = threadIdx.x; e < kMoeMaxE; e += blockDim.x) mask[e] = 0;
+  if (blockIdx.x > 0) {
+    pdl_wait();
+    const int unit = (blockIdx.x - 1) * 32 + w, t = unit / spt;
+    if (t >= p.T) return;
+    const bool four = p.fmt == kInt4 || p.fmt == kNvfp4;
+    if (four) pack_x<8>(p, t, unit - t * spt, spt, lane);
+    else pack_x<4>(p, t, unit - t * spt, spt, lane);
+    return;
+  }
+  mask[threadIdx.x] = 0;
   if (threadIdx.x == 0) nan_rows = 0;
   __syncthreads();
+  pdl_wait();
   if (w < p.T) {
     const int t = w;
     if (p.ids) {
-      for (int j = lane; j < p.top_k; j += 32) {
-        const int e = p.ids[t * p.top_k + j];
-        ids[t][j] = e >= 0 && e < p.E ? e : -1;
-        wts[t][j] = p.weights[t * p.top_k + j];
+      if (lane < p.top_k) {
+        const int e = p.ids[t * p.top_k + lane];
+        ids[t][lane] = e >= 0 && e < p.E ? e : -1;
+        wts[t][lane] = p.weights[t * p.top_k + lane];
       }
+    } else if (p.E <= 128) {
+      choose<4>(p, t, lane, ids[t], wts[t], &nan_rows);
+    } else if (p.E <= 256) {
+      choose<8>(p, t, lane, ids[t], wts[t], &nan_rows);
     } else {
-      float top = -INFINITY;
-      bool bad = false;
-      for (int e = lane; e < p.E; e += 32) {
-        const float v = logit_at(p, t, e);
-        bad |= isnan(v) || v == INFINITY;
-        top = fmaxf(top, v);
-      }
-#pragma unroll
-      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-      bad = __any_sync(~0u, bad);
-      if (bad && lane == 0) atomicOr(&nan_rows, 1u << t);
-      float total = 0.f;
-      if (!(p.flags & BSGEMV_MOE_RENORMALIZE) && !bad && top > -INFINITY) {
-        for (int e = lane; e < p.E; e += 32) total += expf(logit_at(p, t, e) - top);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(~0u, total, d);
-      }
-      // picks in the order (value descending, index ascending): each is the best after the last
-      float last_v = INFINITY;
-      int last_e = -1;
-      float chosen = 0.f;
-      for (int j = 0; j < p.top_k; ++j) {
-        float bv = -INFINITY;
-        int be = kMoeMaxE;
-        if (!bad)
-          for (int e = lane; e < p.E; e += 32) {
-            const float v = logit_at(p, t, e);
-            const bool after = v < last_v || (v == last_v && e > last_e);
-            if (after && v > bv) { bv = v; be = e; }
-          }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) {
-          const float ov = __shfl_xor_sync(~0u, bv, d);
-          const int oe = __shfl_xor_sync(~0u, be, d);
-          if (ov > bv || (ov == bv && oe < be)) { bv = ov; be = oe; }
-        }
-        const bool some = bv > -INFINITY;
-        const float q = some ? expf(bv - top) : 0.f;
-        chosen += q;
-        if (lane == 0) {
-          ids[t][j] = some ? be : -1;
-          wts[t][j] = q;
-        }
-        last_v = bv;
-        last_e = be;
-      }
-      if (p.flags & BSGEMV_MOE_RENORMALIZE) total = chosen;
-      __syncwarp();
-      if (lane < p.top_k && ids[t][lane] >= 0) wts[t][lane] /= total;
+      choose<32>(p, t, lane, ids[t], wts[t], &nan_rows);
     }
     __syncwarp();
-    for (int j = lane; j < p.top_k; j += 32)
-      if (ids[t][j] >= 0) atomicOr(&mask[ids[t][j]], 1u << t);
+    if (lane < p.top_k && ids[t][lane] >= 0) atomicOr(&mask[ids[t][lane]], 1u << t);
   }
   __syncthreads();
   // active experts and their rows: exclusive sums over the experts in index order
@@ -153,8 +275,7 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
   const MoeWeight& w = down ? c.down : c.up;
   MoeGemmParams p = {};
   p.tm = down ? c.tm_down : c.tm_up;
-  p.x0 = down ? c.h_hi : c.x;
-  p.x1 = down ? c.h_lo : nullptr;
+  p.x = down ? c.h_packed : c.x_packed;
   p.route = c.route;
   p.scales = w.scales;
   p.zp = w.zp;
@@ -162,8 +283,8 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
   p.partials = c.partials;
   p.counters = down ? c.counters_down : c.counters_up;
   p.err = c.err;
-  p.out0 = down ? c.y : c.h_hi;
-  p.out1 = down ? nullptr : c.h_lo;
+  p.h = c.h;
+  p.y = c.y;
   p.wait_ns = kDefaultWaitNs;
   p.K = w.k;
   p.rows = static_cast<int>(w.rows);
@@ -175,23 +296,23 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
   p.second = down ? 32 : static_cast<int>(c.I);
   p.step = down ? 64 : 32;
   p.tiles = static_cast<int>(down ? c.H / 64 : c.I / 32);
-  const int kc = four ? 256 : 128;
+  const int kc = moe_stage_k(four);
   p.spt = static_cast<int>((w.k + kc - 1) / kc);
   p.T = c.T;
   p.top_rows = c.max_T * c.top_k;
-  p.out_bf16 = c.bf16;
-  p.bs_log2 = __builtin_ctz(static_cast<unsigned>(c.bs));
+  p.bf16 = c.bf16;
   const int blocks = kc / c.bs;
   p.s_bytes = blocks * (c.fmt == kFp8 ? 4 : c.fmt == kNvfp4 ? 1 : 2);
   p.s_unit = copy_unit(w.scales, w.scale_pitch, p.s_bytes);
   p.s_stride = p.s_unit ? p.s_bytes : (p.s_bytes + 6) / 4 * 4;
+  p.z_unit = 16;  // (no zero points: none to shift)
   if (w.zp) {
     p.z_bytes = c.fmt == kInt4 ? blocks / 2 : blocks;
     p.z_unit = copy_unit(w.zp, w.zp_pitch, p.z_bytes);
     p.z_stride = p.z_unit ? p.z_bytes : (p.z_bytes + 6) / 4 * 4;
   }
   p.side_bytes = align_up(kMoeTileRows * (p.s_stride + p.z_stride), 16);
-  const int row_bytes = (2 * kc + (four ? 64 : 32)) * (down ? 2 : 1);
+  const int row_bytes = moe_pitch(four) * (down ? 2 : 1);
   const int budget = kSmemPerSm / blocks_per_sm(c.max_T) - 1024;
   const int route_bytes = align_up((4 * p.top_rows + 1) * 4, 16);
   p.slot_floats = down ? c.max_T * 16 : (wide ? 4 : 1) * 128;
@@ -214,17 +335,18 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
     if (smem <= budget || p.stages == 2) break;
   }
   const int ctas = sms * blocks_per_sm(c.max_T);
+  const int cpb = block_mode(c.fmt, c.bs);
   switch (c.fmt) {
-    case kInt4: return launch_moe_int4(p, c.bf16, wide, down, ctas, smem, s);
-    case kInt8: return launch_moe_int8(p, c.bf16, wide, down, ctas, smem, s);
-    case kFp8: return launch_moe_fp8(p, c.bf16, wide, down, ctas, smem, s);
-    default: return launch_moe_nvfp4(p, c.bf16, wide, down, ctas, smem, s);
+    case kInt4: return launch_moe_int4(p, cpb, wide, down, ctas, smem, s);
+    case kInt8: return launch_moe_int8(p, cpb, wide, down, ctas, smem, s);
+    case kFp8: return launch_moe_fp8(p, wide, down, ctas, smem, s);
+    default: return launch_moe_nvfp4(p, wide, down, ctas, smem, s);
   }
 }
 
 }  // namespace
 
-MoeLayout moe_layout(int64_t H, int64_t I, int E, int top_k, int max_T, int sms) {
+MoeLayout moe_layout(int fmt, int64_t H, int64_t I, int E, int top_k, int max_T, int sms) {
   MoeLayout l = {};
   size_t at = 256;
   const auto take = [&at](size_t bytes) {
@@ -240,8 +362,11 @@ MoeLayout moe_layout(int64_t H, int64_t I, int E, int top_k, int max_T, int sms)
   l.counters_up = take(active * (I / 32) * 4 * sizeof(unsigned));
   l.counters_down = take(static_cast<size_t>(H / 64) * 4 * sizeof(unsigned));
   l.partials = take(ctas * 2 * 4 * slot * sizeof(float));
-  l.h_hi = take(rows * I * 2);
-  l.h_lo = take(rows * I * 2);
+  l.h = take(rows * I * sizeof(float));
+  const bool four = fmt == kInt4 || fmt == kNvfp4;
+  const size_t kc = moe_stage_k(four), pitch = moe_pitch(four);
+  l.x_packed = take(max_T * ((H + kc - 1) / kc) * pitch);
+  l.h_packed = take(rows * ((I + kc - 1) / kc) * 2 * pitch);
   l.total = at;
   return l;
 }
@@ -255,8 +380,14 @@ int moe_encode(CUtensorMap* tm, const MoeWeight& w, int E) {
 }
 
 int launch_moe(const MoeParams& p, int sms, cudaStream_t s) {
-  int rc = decode_launch(moe_route, dim3(1), dim3(1024), 0, s, p);
+  const bool four = p.fmt == kInt4 || p.fmt == kNvfp4;
+  const int kc = moe_stage_k(four);
+  const int up = static_cast<int>((p.H + kc - 1) / kc), down = static_cast<int>((p.I + kc - 1) / kc);
+  int rc = decode_launch(moe_route, dim3(1 + (p.T * up + 31) / 32), dim3(1024), 0, s, p, up);
   if (rc == BSGEMV_OK) rc = launch_product(p, false, sms, s);
+  if (rc == BSGEMV_OK)
+    rc = decode_launch(four ? moe_pack<8> : moe_pack<4>, dim3((p.T * p.top_k * down + 7) / 8),
+                       dim3(256), 0, s, p, down);
   if (rc == BSGEMV_OK) rc = launch_product(p, true, sms, s);
   return rc;
 }

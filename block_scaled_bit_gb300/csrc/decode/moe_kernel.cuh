@@ -11,6 +11,12 @@ constexpr int kMoeMaxE = 1024;
 constexpr int kMoeMaxK = 16;
 constexpr int kMoeMaxRows = kMoeMaxT * kMoeMaxK;  // (expert, token) pairs of a call
 
+// k of a stage, and the bytes of a packed row of activations of one stage: the values in f16, then
+// the fp32 factor that undoes their scale, padded so that the rows of the shared-memory ring
+// start 16 banks apart (8-bit formats: 8).
+__host__ __device__ constexpr int moe_stage_k(bool four) { return four ? 256 : 128; }
+__host__ __device__ constexpr int moe_pitch(bool four) { return 2 * moe_stage_k(four) + (four ? 64 : 32); }
+
 // What a call's tokens chose.  Active experts in index order; expert a's pairs are the rows
 // off[a] .. off[a + 1] - 1 in token order.
 struct Routing {
@@ -51,7 +57,8 @@ struct MoeParams {
   unsigned *counters_up, *counters_down;  // arrivals per (tile, decode warp), left at zero
   float* partials;
   Routing* route;
-  uint16_t *h_hi, *h_lo;       // [rows][I] bf16
+  float* h;                    // [rows][I]
+  uint8_t *x_packed, *h_packed;  // [T][stages of H][pitch], [rows][stages of I][2 pitches]
 };
 
 inline MoeWeight weight_of(int fmt, int bs, int has_zp, int64_t rows, int64_t k, const void* W,
@@ -72,9 +79,17 @@ inline MoeWeight weight_of(int fmt, int bs, int has_zp, int64_t rows, int64_t k,
 
 // The workspace's parts, in bytes from its start (the error word is at 0).
 struct MoeLayout {
-  size_t route, counters_up, counters_down, partials, h_hi, h_lo, total;
+  size_t route, counters_up, counters_down, partials, h, x_packed, h_packed, total;
 };
-MoeLayout moe_layout(int64_t H, int64_t I, int E, int top_k, int max_T, int sms);
+MoeLayout moe_layout(int fmt, int64_t H, int64_t I, int E, int top_k, int max_T, int sms);
+
+// The most stages of weights that a call can have in one of its products.
+inline int64_t moe_stages(int fmt, int64_t H, int64_t I, int E, int top_k, int max_T) {
+  const int64_t kc = moe_stage_k(fmt == kInt4 || fmt == kNvfp4);
+  const int64_t active = E < top_k * max_T ? E : top_k * max_T;
+  const int64_t up = (I / 32) * ((H + kc - 1) / kc), down = (H / 64) * ((I + kc - 1) / kc);
+  return active * (up > down ? up : down);
+}
 
 // Tensor map of one stacked weight (BSGEMV_ERR_CUDA if it cannot be encoded).
 int moe_encode(CUtensorMap* tm, const MoeWeight& w, int E);
@@ -83,13 +98,13 @@ int launch_moe(const MoeParams& p, int sms, cudaStream_t s);
 
 // One product's launch per weight format (a translation unit each).
 struct MoeGemmParams;
-int launch_moe_int4(const MoeGemmParams& p, bool bf16, bool wide, bool down, int ctas, int smem,
+int launch_moe_int4(const MoeGemmParams& p, int cpb, bool wide, bool down, int ctas, int smem,
                     cudaStream_t s);
-int launch_moe_int8(const MoeGemmParams& p, bool bf16, bool wide, bool down, int ctas, int smem,
+int launch_moe_int8(const MoeGemmParams& p, int cpb, bool wide, bool down, int ctas, int smem,
                     cudaStream_t s);
-int launch_moe_fp8(const MoeGemmParams& p, bool bf16, bool wide, bool down, int ctas, int smem,
+int launch_moe_fp8(const MoeGemmParams& p, bool wide, bool down, int ctas, int smem,
                    cudaStream_t s);
-int launch_moe_nvfp4(const MoeGemmParams& p, bool bf16, bool wide, bool down, int ctas, int smem,
+int launch_moe_nvfp4(const MoeGemmParams& p, bool wide, bool down, int ctas, int smem,
                      cudaStream_t s);
 
 }  // namespace bsg

@@ -344,8 +344,8 @@ int bsgemv_dense_destroy(bsgemv_dense_plan_t plan);
  *     y[t]       = sum over j of p_j * W2[e_j] . (g / (1 + exp(-g)) * u)       W2: [H, I]
  *
  * x, y and (unless BSGEMV_MOE_LOGITS_F32) the logits are in the activation dtype.  Sums, softmax
- * and the intermediate are fp32 (the intermediate enters the second product as two bf16 parts
- * that hold 16 of its bits); y is rounded once.  An expert's weights are read
+ * and the intermediate are fp32 (the intermediate enters the second product as two f16 parts with
+ * a power of two per row, at least 16 of its bits); y is rounded once.  An expert's weights are read
  * once for all tokens that chose it, and other experts' weights are not read.  A logit of -inf is
  * never chosen; a row with nothing to choose gives y = 0.  A row that holds a NaN or +inf logit
  * gives NaN, as the softmax has it.  What one token chose never reaches another token's row, NaN
