@@ -11,6 +11,7 @@ struct bsgemv_attn_plan_s {
   int device = -1, sms = 0;
   int bf16 = 0, Hq = 0, Hkv = 0, D = 0, page_size = 0, max_B = 0;
   void* ws = nullptr;
+  bsg::AttnLayout at = {};
 };
 
 using namespace bsg;
@@ -40,7 +41,8 @@ int bsgemv_attn_plan(bsgemv_attn_plan_t* out, int act_bf16, int Hq, int Hkv, int
   p->D = D;
   p->page_size = page_size;
   p->max_B = max_B;
-  rc = decode_alloc(&p->ws, 256);
+  p->at = attn_layout(Hq, Hkv, D, max_B, sms);
+  rc = decode_alloc(&p->ws, p->at.total);
   if (rc != BSGEMV_OK) {
     delete p;
     return rc;
@@ -65,6 +67,10 @@ int bsgemv_attn_run(bsgemv_attn_plan_t plan, const void* q, int64_t q_stride, co
       !aligned_to(prefix_table, 4) || !aligned_to(tables, 4) || !aligned_to(lens, 4) ||
       !aligned_to(lse, 4) || q_stride % 8 || page_stride % 8 || head_stride % 8 || row_stride % 8)
     return BSGEMV_ERR_MISALIGNED;
+  // the line of tiles (attn_stream.cuh) is counted in 32 bits
+  const int64_t row_tiles = (static_cast<int64_t>(B) * (plan->Hq / plan->Hkv) + 15) / 16;
+  if (row_tiles * plan->Hkv * (prefix_len / (4096 / plan->D) + 1) >= (int64_t{1} << 30))
+    return BSGEMV_ERR_UNSUPPORTED;
   const int rc = decode_check_device(plan->device);
   if (rc != BSGEMV_OK) return rc;
   AttnParams p = {};
@@ -85,11 +91,13 @@ int bsgemv_attn_run(bsgemv_attn_plan_t plan, const void* q, int64_t q_stride, co
   p.Hq = plan->Hq;
   p.Hkv = plan->Hkv;
   p.D = plan->D;
-  p.page_size = plan->page_size;
+  p.page_log2 = __builtin_ctz(static_cast<unsigned>(plan->page_size));
   p.bf16 = plan->bf16;
-  p.scale = scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
+  p.err = static_cast<unsigned*>(plan->ws);
+  p.parts = reinterpret_cast<float*>(static_cast<char*>(plan->ws) + plan->at.parts);
   return launch_attn(p, plan->sms, static_cast<cudaStream_t>(stream));
 }
 

@@ -1,92 +1,101 @@
-// attn_kernel.cu -- the paged shared-prefix attention.
-#include "attn_kernel.cuh"
-
-#include "../bsgemv_kernel.cuh"
-#include "decode_internal.h"
+// attn_kernel.cu -- launches of the paged shared-prefix attention, and the kernel that puts the
+// parts together.
+#include "attn_stream.cuh"
 
 namespace bsg {
 namespace {
 
-constexpr int kKeys = 128;
-
-BSG_DEV float value(const AttnParams& p, const uint16_t* v) {
-  return p.bf16 ? half_to_f32<true>(*v, 0) : half_to_f32<false>(*v, 0);
-}
-
-BSG_DEV void put(const AttnParams& p, uint16_t* out, float v) {
-  if (p.bf16) *reinterpret_cast<__nv_bfloat16*>(out) = __float2bfloat16_rn(v);
-  else *reinterpret_cast<__half*>(out) = __float2half_rn(v);
-}
-
-// Element offset of position j's row for kv head h, or -1 where its page id is out of range.
-BSG_DEV int64_t row_at(const AttnParams& p, int b, int h, int j) {
-  const int at = j / p.page_size;
-  const int page = j < p.prefix_len ? p.prefix_table[at] : p.tables[b * p.table_stride + at];
-  if (page < 0 || page >= p.num_pages) return -1;
-  return page * p.page_stride + h * p.head_stride + (j % p.page_size) * p.row_stride;
-}
-
-// One block of 128 threads per (sequence, query head): scores of 128 positions at a time, one
-// per thread, then each thread's output elements; running maximum and sum in fp32.
-__global__ void __launch_bounds__(kKeys) attn_simple(AttnParams p) {
-  __shared__ float qs[256], ps[kKeys], red[4];
-  __shared__ int64_t rows[kKeys];
-  const int b = blockIdx.y, hq = blockIdx.x, h = hq / (p.Hq / p.Hkv), tid = threadIdx.x;
-  const int len = p.lens[b];
-  uint16_t* out = p.out + (static_cast<int64_t>(b) * p.Hq + hq) * p.D;
-  if (len < max(p.prefix_len, 1)) {
-    for (int d = tid; d < p.D; d += kKeys) out[d] = 0;
-    if (tid == 0 && p.lse) p.lse[b * p.Hq + hq] = -INFINITY;
-    return;
-  }
-  for (int d = tid; d < p.D; d += kKeys) qs[d] = value(p, p.q + b * p.q_stride + hq * p.D + d);
-  float m = -INFINITY, l = 0.f, acc[2] = {0.f, 0.f};
-  for (int j0 = 0; j0 < len; j0 += kKeys) {
-    const int j = j0 + tid;
-    __syncthreads();
-    const int64_t at = j < len ? row_at(p, b, h, j) : -1;
-    rows[tid] = at;
-    float s = -INFINITY;
-    if (j < len) {
-      s = 0.f;
-      if (at >= 0)
-        for (int d = 0; d < p.D; ++d) s += qs[d] * value(p, p.k + at + d);
-      s *= p.scale;
-    }
-    float top = s;
+// One warp per (sequence, query head): its parts, in order, D / 32 elements a lane.
+template <bool BF16, int D>
+__global__ void __launch_bounds__(128)
+    attn_merge(const __grid_constant__ AttnParams p, bool with_prefix, int workers) {
+  extern __shared__ int cum[];
+  const int lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  attn_prefix_sums<D>(p, cum, cum + p.B + 1);
+  const AttnSplit s = attn_split<D>(p, cum, with_prefix, workers);
+  pdl_wait();
+  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row >= p.B * p.Hq) return;
+  const int b = row / p.Hq, hq = row - b * p.Hq, G = p.Hq / p.Hkv, h = hq / G, g = hq - h * G;
+  constexpr int kPer = D / 32;
+  float o[kPer], m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-    if ((tid & 31) == 0) red[tid >> 5] = top;
-    __syncthreads();
-    const float next = fmaxf(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), m);
-    const float base = next == -INFINITY ? 0.f : next;
-    ps[tid] = expf(s - base);
-    const float keep = expf(m - base);
-    m = next;
-    l *= keep;
-    acc[0] *= keep;
-    acc[1] *= keep;
-    __syncthreads();
-    const int n = min(kKeys, len - j0);
-    for (int i = 0; i < n; ++i) {
-      const float pv = ps[i];
-      l += pv;
-      if (rows[i] >= 0)
-        for (int x = 0; x < 2; ++x)
-          if (tid + x * kKeys < p.D) acc[x] += pv * value(p, p.v + rows[i] + tid + x * kKeys);
+  for (int i = 0; i < kPer; ++i) o[i] = 0.f;
+  const bool here = p.lens[b] >= max(p.prefix_len, 1);
+  const auto add = [&](const float* part, int r) {  // rows of D, then m, then l, of 16 rows
+    const float mi = __ldcg(part + kAttnRows * D + r), li = __ldcg(part + kAttnRows * (D + 1) + r);
+    float v[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) {
+      const float2 f = __ldcg(reinterpret_cast<const float2*>(part + r * D + lane * kPer) + i);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
     }
+    const float next = fmaxf(m, mi), base = next == -INFINITY ? 0.f : next;
+    const float keep = exp2f(m - base), take = exp2f(mi - base);
+    m = next;
+    l = l * keep + li * take;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) o[i] = o[i] * keep + v[i] * take;
+  };
+  const auto add_unit = [&](int unit, int first, int tiles, int r) {
+    const int w1 = attn_owner(s, first + tiles - 1);
+    for (int w = attn_owner(s, first); w <= w1; ++w)
+      add(p.parts + static_cast<int64_t>(w + unit) * attn_slot_floats(D), r);
+  };
+  if (here) {
+    const int tiles = cum[b + 1] - cum[b];
+    const int i = h * s.row_tiles + g / kAttnRows;
+    if (s.pre_tiles) {
+      const int r = b * G + g, u = h * (s.pre_units / p.Hkv) + r / kAttnRows;
+      add_unit(s.own_units + u, s.pre_start + u * s.pre_tiles, s.pre_tiles, r % kAttnRows);
+    }
+    if (tiles)
+      add_unit(b * p.Hkv * s.row_tiles + i, cum[b] * p.Hkv * s.row_tiles + i * tiles, tiles,
+               g % kAttnRows);
   }
-  for (int x = 0; x < 2; ++x)
-    if (tid + x * kKeys < p.D) put(p, out + tid + x * kKeys, acc[x] / l);
-  if (tid == 0 && p.lse) p.lse[b * p.Hq + hq] = m + logf(l);
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(row) * D + lane * kPer);
+#pragma unroll
+  for (int i = 0; i < kPer / 2; ++i)
+    out[i] = here ? AttnStream<BF16, D>::pack(o[2 * i] / l, o[2 * i + 1] / l) : 0u;
+  if (lane == 0 && p.lse) p.lse[row] = here ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <bool BF16, int D>
+int launch(const AttnParams& p, int sms, cudaStream_t s) {
+  static AttrRecord rec;
+  using T = AttnTile<D>;
+  const int sums = (p.B + 1 + 33) * 4;
+  const int smem = kAttnWarps * T::kWarpB + sums;
+  int rc = decode_smem(attn_stream_kernel<BF16, D>, rec, smem);
+  if (rc != BSGEMV_OK) return rc;
+  const bool with_prefix = p.prefix_len > 0;
+  rc = decode_launch(attn_stream_kernel<BF16, D>, dim3(sms), dim3(32 * kAttnWarps), smem, s, p,
+                     with_prefix);
+  if (rc != BSGEMV_OK) return rc;
+  return decode_launch(attn_merge<BF16, D>, dim3((p.B * p.Hq + 3) / 4), dim3(128), sums, s, p,
+                       with_prefix, sms * kAttnWarps);
 }
 
 }  // namespace
 
+AttnLayout attn_layout(int Hq, int Hkv, int D, int max_B, int sms) {
+  AttnLayout l = {};
+  const size_t G = Hq / Hkv;
+  const size_t units = static_cast<size_t>(max_B) * Hkv * ((G + kAttnRows - 1) / kAttnRows) +
+                       Hkv * ((max_B * G + kAttnRows - 1) / kAttnRows);
+  l.parts = 256;
+  l.total = l.parts + (units + static_cast<size_t>(sms) * kAttnWarps) * attn_slot_floats(D) * 4;
+  return l;
+}
+
 int launch_attn(const AttnParams& p, int sms, cudaStream_t s) {
-  (void)sms;
-  attn_simple<<<dim3(p.Hq, p.B), kKeys, 0, s>>>(p);
-  return decode_launched();
+  switch (p.D) {
+    case 64: return p.bf16 ? launch<true, 64>(p, sms, s) : launch<false, 64>(p, sms, s);
+    case 128: return p.bf16 ? launch<true, 128>(p, sms, s) : launch<false, 128>(p, sms, s);
+    default: return p.bf16 ? launch<true, 256>(p, sms, s) : launch<false, 256>(p, sms, s);
+  }
 }
 
 }  // namespace bsg

@@ -1,13 +1,22 @@
-// attn_kernel.cuh -- parameters and launch of the paged shared-prefix attention.
+// attn_kernel.cuh -- parameters, work split and launches of the paged shared-prefix attention.
+//
+// Every part of the work -- a tile of query rows of one kv head with a range of positions --
+// leaves its softmax unnormalised in the workspace: per row the running maximum m (of the scores in
+// base 2), the sum l of the rounded numerators and the fp32 row of their products with V.
+// attn_merge puts a row's parts together:  o = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 namespace bsg {
 
 constexpr int kAttnMaxB = 1024;
 constexpr int kAttnMaxGroup = 64;
+constexpr int kAttnRows = 16;      // query rows of a streaming part (an mma tile)
+constexpr int kAttnWarps = 4;      // warps of a streaming block, each a worker of its own
 
 struct AttnParams {
   const uint16_t *q, *k, *v;
@@ -18,11 +27,18 @@ struct AttnParams {
   const int32_t* tables;
   int64_t table_stride;
   const int32_t* lens;
-  int B, Hq, Hkv, D, page_size, bf16;
-  float scale;
+  int B, Hq, Hkv, D, page_log2, bf16;
+  float scale_log2;   // scale * log2(e)
   uint16_t* out;
   float* lse;
+  unsigned* err;
+  float* parts;       // streaming parts: slots of [16][D] sums, then [16] m, [16] l
 };
+
+struct AttnLayout {
+  size_t parts, total;
+};
+AttnLayout attn_layout(int Hq, int Hkv, int D, int max_B, int sms);
 
 int launch_attn(const AttnParams& p, int sms, cudaStream_t s);
 

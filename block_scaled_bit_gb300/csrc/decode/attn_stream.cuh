@@ -1,0 +1,429 @@
+// attn_stream.cuh -- attention of few query rows over many positions: the streaming kernel.
+//
+// Sixteen query rows of one kv head (the heads that share it, of one sequence) against the
+// sequence's own positions.  Bound: K and V are read once from HBM; 16 rows give 16 flops a byte,
+// far below the tensor cores' ridge.  So every warp is a worker with a stream of its own: tiles of
+// 16 KB (4096 / D positions of K and V) through a ring in shared memory by cp.async, two tiles in
+// flight, no synchronisation but the warp's own; scores and P V on mma.sync m16n8k16, softmax in
+// registers with the running maximum in base 2.
+//
+// All tiles of all (sequence, kv head, row tile) are laid in a line and cut into equal ranges, one
+// per warp, so that the lengths' spread does not matter; a range leaves one part per unit that it
+// touches.  Warp w's part of unit u lies in slot w + u (each next part moves on in w or in u).
+#pragma once
+
+#include "../bsgemv_kernel.cuh"
+#include "attn_kernel.cuh"
+#include "decode_internal.h"
+
+namespace bsg {
+
+// The line of tiles.  Units: (sequence b, kv head h, row tile r) in this order, then the prefix's
+// (h, row tile over all sequences' rows), where the streaming kernel does the prefix.
+struct AttnSplit {
+  int row_tiles;     // row tiles of a sequence's group
+  int own_units;     // B * Hkv * row_tiles
+  int pre_units;     // prefix units, 0 where another kernel does it
+  int pre_tiles;     // tiles of a prefix unit
+  int pre_start;     // first tile of the prefix units
+  int total;         // tiles in all (below 2^31)
+  int base, extra;   // tiles of a worker; the first `extra` have one more
+  int workers;       // workers with tiles
+};
+
+template <int D>
+struct AttnTile {
+  static constexpr int kKeys = 4096 / D;         // positions of a tile
+  static constexpr int kStages = D == 256 ? 2 : 3;
+  static constexpr int kHalf = kKeys * D * 2;    // bytes of K (or V) in a tile: 8 KB
+  static constexpr int kQ = D == 256 ? kAttnRows * D * 2 : 0;  // queries kept in shared memory
+  static constexpr int kWarpB = kStages * 2 * kHalf + kQ;
+};
+
+// Tiles of sequence b's own positions: [prefix_len, len) in tiles that start at a multiple of
+// kKeys.  A slot without a sequence has none.
+template <int D>
+BSG_DEV int own_tiles(const AttnParams& p, int b) {
+  const int len = p.lens[b];
+  if (len < max(p.prefix_len, 1) || len == p.prefix_len) return 0;
+  constexpr int K = AttnTile<D>::kKeys;
+  return (len + K - 1) / K - p.prefix_len / K;
+}
+
+// cum[b] = tiles of one (head, row tile) of the sequences before b, b <= B, by the whole block;
+// cum must hold B + 1 integers, tmp 33.
+template <int D>
+BSG_DEV void attn_prefix_sums(const AttnParams& p, int* cum, int* tmp) {
+  const int n = blockDim.x, per = (p.B + n - 1) / n, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int b0 = threadIdx.x * per;
+  int sum = 0;
+  for (int i = 0; i < per; ++i)
+    if (b0 + i < p.B) {
+      const int t = own_tiles<D>(p, b0 + i);
+      cum[b0 + i] = sum;
+      sum += t;
+    }
+  int inc = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) tmp[w] = inc;
+  __syncthreads();
+  int before = inc - sum;
+  for (int i = 0; i < w; ++i) before += tmp[i];
+  for (int i = 0; i < per; ++i)
+    if (b0 + i < p.B) cum[b0 + i] += before;
+  if (threadIdx.x == n - 1) cum[p.B] = before + sum;
+  __syncthreads();
+}
+
+template <int D>
+BSG_DEV AttnSplit attn_split(const AttnParams& p, const int* cum, bool with_prefix, int workers) {
+  AttnSplit s;
+  const int G = p.Hq / p.Hkv;
+  s.row_tiles = (G + kAttnRows - 1) / kAttnRows;
+  s.own_units = p.B * p.Hkv * s.row_tiles;
+  s.pre_start = cum[p.B] * p.Hkv * s.row_tiles;
+  s.pre_tiles = with_prefix ? (p.prefix_len + AttnTile<D>::kKeys - 1) / AttnTile<D>::kKeys : 0;
+  s.pre_units = s.pre_tiles ? p.Hkv * ((p.B * G + kAttnRows - 1) / kAttnRows) : 0;
+  s.total = s.pre_start + s.pre_units * s.pre_tiles;
+  s.workers = min(workers, s.total);
+  s.base = s.workers ? s.total / s.workers : 0;
+  s.extra = s.total - s.base * s.workers;
+  return s;
+}
+
+BSG_DEV int attn_start(const AttnSplit& s, int w) { return w * s.base + min(w, s.extra); }
+BSG_DEV int attn_owner(const AttnSplit& s, int tile) {
+  const int cut = s.extra * (s.base + 1);
+  return tile < cut ? tile / (s.base + 1) : s.extra + (tile - cut) / s.base;
+}
+
+__host__ __device__ constexpr int attn_slot_floats(int D) { return kAttnRows * (D + 2); }
+
+// One unit being worked on.
+struct AttnUnit {
+  int unit, b, h, r;        // b = -1: the prefix
+  int lo, hi;               // positions
+  int first;                // line position of its first tile
+  int tiles;
+};
+
+template <int D>
+BSG_DEV AttnUnit attn_unit_at(const AttnParams& p, const AttnSplit& s, const int* cum, int tile) {
+  AttnUnit u;
+  constexpr int K = AttnTile<D>::kKeys;
+  if (tile >= s.pre_start) {
+    const int i = (tile - s.pre_start) / s.pre_tiles, rows = s.pre_units / p.Hkv;
+    u.unit = s.own_units + i;
+    u.b = -1;
+    u.h = i / rows;
+    u.r = i - u.h * rows;
+    u.first = s.pre_start + i * s.pre_tiles;
+    u.tiles = s.pre_tiles;
+    u.lo = 0;
+    u.hi = p.prefix_len;
+    return u;
+  }
+  // the last b with cum[b] * units per sequence <= tile (empty sequences share their start)
+  const int per = p.Hkv * s.row_tiles;
+  int a = 0, z = p.B;
+  while (z - a > 1) {
+    const int mid = (a + z) >> 1;
+    if (cum[mid] * per <= tile) a = mid;
+    else z = mid;
+  }
+  u.b = a;
+  u.tiles = cum[a + 1] - cum[a];
+  const int i = (tile - cum[a] * per) / u.tiles;
+  u.h = i / s.row_tiles;
+  u.r = i - u.h * s.row_tiles;
+  u.unit = (a * p.Hkv + u.h) * s.row_tiles + u.r;
+  u.first = cum[a] * per + i * u.tiles;
+  u.lo = p.prefix_len;
+  u.hi = p.lens[a];
+  (void)K;
+  return u;
+}
+
+template <bool BF16, int D>
+struct AttnStream {
+  using T = AttnTile<D>;
+  static constexpr int K = T::kKeys;
+  static constexpr int kSteps = D / 16;   // mma k-steps of the scores
+  static constexpr int kCpr = D / 8;      // 16-byte chunks of a row
+
+  // Byte offset of chunk c of row r in a half tile: chunks swizzled by the row.
+  static BSG_DEV uint32_t at(int r, int c) { return r * (D * 2) + ((c ^ (r & 7)) << 4); }
+
+  // Element offset of a position's row in the cache, -1 outside the unit or the pages.
+  static BSG_DEV int64_t row_of(const AttnParams& p, const AttnUnit& u, int pos) {
+    if (pos < u.lo || pos >= u.hi) return -1;
+    const int i = pos >> p.page_log2;
+    const int page = u.b < 0 ? p.prefix_table[i] : p.tables[u.b * p.table_stride + i];
+    if (page < 0 || page >= p.num_pages) return -1;
+    return page * p.page_stride + u.h * p.head_stride +
+           (pos & ((1 << p.page_log2) - 1)) * p.row_stride;
+  }
+
+  // A tile's rows into a ring stage (rows outside the unit: zeros).  Lane j knows where rows j
+  // (and j + 32) are; each step moves 32 chunks.
+  static constexpr int kOff = K > 32 ? 2 : 1;
+  static BSG_DEV void offsets(const AttnParams& p, const AttnUnit& u, int tile, int lane,
+                              int64_t (&off)[kOff]) {
+    const int pos = (u.lo / K + tile) * K + lane;
+#pragma unroll
+    for (int i = 0; i < kOff; ++i) off[i] = (lane + 32 * i < K) ? row_of(p, u, pos + 32 * i) : -1;
+  }
+  static BSG_DEV void issue(const AttnParams& p, uint32_t stage, const int64_t (&off)[kOff],
+                            int lane) {
+    constexpr int kIter = K * kCpr / 32;
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const int x = i * 32 + lane, r = x / kCpr, c = x % kCpr;
+      int64_t o = __shfl_sync(0xFFFFFFFFu, off[0], r & 31);
+      if constexpr (kOff == 2) {
+        const int64_t o1 = __shfl_sync(0xFFFFFFFFu, off[1], r & 31);
+        if (r >= 32) o = o1;
+      }
+      const uint32_t n = o >= 0 ? 16u : 0u;
+      const int64_t e = (o >= 0 ? o : 0) + c * 8;
+      const uint32_t dst = stage + at(r, c);
+      cp_async16(dst, p.k + (o >= 0 ? e : 0), n);
+      cp_async16(dst + T::kHalf, p.v + (o >= 0 ? e : 0), n);
+    }
+  }
+
+  static BSG_DEV void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+  }
+  static BSG_DEV void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+  }
+  static BSG_DEV uint32_t pack(float a, float b) {
+    uint32_t d;
+    if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    return d;
+  }
+
+  // Query row i of a unit: its 16-bit elements, nullptr past the last.
+  static BSG_DEV const uint16_t* q_row(const AttnParams& p, const AttnUnit& u, int i) {
+    const int G = p.Hq / p.Hkv;
+    int b = u.b, g = u.r * kAttnRows + i;
+    if (b < 0) {
+      b = g / G;
+      g -= b * G;
+      if (b >= p.B) return nullptr;
+    } else if (g >= G) {
+      return nullptr;
+    }
+    return p.q + b * p.q_stride + static_cast<int64_t>(u.h * G + g) * D;
+  }
+
+  struct Acc {
+    float o[D / 8][4];   // rows g and g + 8: columns 8 n + 2 t, + 1
+    float m[2], l[2];
+  };
+
+  // Scores, softmax and P V of one tile.
+  static BSG_DEV void tile(const AttnParams& p, const AttnUnit& u, int pos0, uint32_t stage,
+                           const uint32_t (&q)[D == 256 ? 1 : kSteps][4], uint32_t qs, int lane,
+                           Acc& a) {
+    float s[K / 8][4];
+#pragma unroll
+    for (int n = 0; n < K / 8; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[n][x] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      uint32_t f[4];
+      if constexpr (D == 256) {
+        ldsm4(qs + at(lane & 15, 2 * k + (lane >> 4)), f);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) f[x] = q[k][x];
+      }
+#pragma unroll
+      for (int n = 0; n < K / 8; n += 2) {
+        // matrices: keys 8 n .. + 7 (k halves 0, 1), keys 8 n + 8 .. (halves 0, 1)
+        uint32_t kb[4];
+        ldsm4(stage + at(8 * n + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), kb);
+        mma16816<BF16>(s[n], f, kb[0], kb[1]);
+        mma16816<BF16>(s[n + 1], f, kb[2], kb[3]);
+      }
+    }
+    const int t = lane & 3;
+    const bool whole = pos0 >= u.lo && pos0 + K <= u.hi;
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int n = 0; n < K / 8; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        float v = s[n][x] * p.scale_log2;
+        if (!whole) {
+          const int pos = pos0 + 8 * n + 2 * t + (x & 1);
+          v = pos >= u.lo && pos < u.hi ? v : -INFINITY;
+        }
+        s[n][x] = v;
+        top[x >> 1] = fmaxf(top[x >> 1], v);
+      }
+    float base[2];
+    bool moved = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
+      top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
+      moved |= top[i] > a.m[i];
+    }
+    if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float next = fmaxf(a.m[i], top[i]);
+        const float keep = a.m[i] == -INFINITY ? 0.f : exp2f(a.m[i] - next);
+        a.m[i] = next;
+        a.l[i] *= keep;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          a.o[n][2 * i] *= keep;
+          a.o[n][2 * i + 1] *= keep;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) base[i] = a.m[i] == -INFINITY ? 0.f : a.m[i];
+#pragma unroll
+    for (int k = 0; k < K / 16; ++k) {
+      uint32_t f[4];  // P of keys 16 k .. + 15, rounded
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int n = 2 * k + (x >> 1), i = x & 1;
+        f[x] = pack(exp2f(s[n][2 * i] - base[i]), exp2f(s[n][2 * i + 1] - base[i]));
+        a.l[i] += half_to_f32<BF16>(f[x], 0) + half_to_f32<BF16>(f[x], 1);
+      }
+#pragma unroll
+      for (int n = 0; n < D / 8; n += 2) {
+        uint32_t vb[4];
+        ldsm4_t(stage + T::kHalf + at(16 * k + (lane & 15), n + (lane >> 4)), vb);
+        mma16816<BF16>(a.o[n], f, vb[0], vb[1]);
+        mma16816<BF16>(a.o[n + 1], f, vb[2], vb[3]);
+      }
+    }
+  }
+
+  static BSG_DEV void store_part(const AttnParams& p, int slot, int lane, Acc& a) {
+    float* part = p.parts + static_cast<int64_t>(slot) * attn_slot_floats(D);
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      a.l[i] += __shfl_xor_sync(0xFFFFFFFFu, a.l[i], 1);
+      a.l[i] += __shfl_xor_sync(0xFFFFFFFFu, a.l[i], 2);
+      float* row = part + (g + 8 * i) * D + 2 * t;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        __stcg(reinterpret_cast<float2*>(row + 8 * n), make_float2(a.o[n][2 * i], a.o[n][2 * i + 1]));
+      if (t == 0) {
+        __stcg(part + kAttnRows * D + g + 8 * i, a.m[i]);
+        __stcg(part + kAttnRows * (D + 1) + g + 8 * i, a.l[i]);
+      }
+    }
+  }
+
+  static BSG_DEV void worker(const AttnParams& p, const AttnSplit& s, const int* cum, uint32_t ring,
+                             uint8_t* ring_p, int w, int lane) {
+    if (w >= s.workers) return;
+    const int x0 = attn_start(s, w), x1 = attn_start(s, w + 1);
+    // the loads run ahead of the products, over units' ends: each has its own place in the line
+    AttnUnit in = attn_unit_at<D>(p, s, cum, x0), out = in;
+    int xi = x0;
+    int64_t off[kOff];
+    offsets(p, in, xi - in.first, lane, off);
+    const auto load = [&](int stage) {
+      if (xi < x1) {
+        issue(p, ring + stage * 2 * T::kHalf, off, lane);
+        if (++xi < x1) {
+          if (xi == in.first + in.tiles) in = attn_unit_at<D>(p, s, cum, xi);
+          offsets(p, in, xi - in.first, lane, off);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < T::kStages - 1; ++i) load(i);
+    uint32_t q[D == 256 ? 1 : kSteps][4];
+    const uint32_t qs = ring + T::kStages * 2 * T::kHalf;
+    Acc a;
+    int stage = 0;
+    bool fresh = true;
+    for (int x = x0; x < x1; ++x) {
+      if (x == out.first + out.tiles) out = attn_unit_at<D>(p, s, cum, x);
+      if (fresh) {
+        fresh = false;
+        if constexpr (D == 256) {
+          uint8_t* dst = ring_p + T::kStages * 2 * T::kHalf;
+          __syncwarp();
+          for (int i = lane; i < kAttnRows * kCpr; i += 32) {
+            const int r = i / kCpr, c = i % kCpr;
+            const uint16_t* src = q_row(p, out, r);
+            *reinterpret_cast<uint4*>(dst + at(r, c)) =
+                src ? *reinterpret_cast<const uint4*>(src + c * 8) : make_uint4(0, 0, 0, 0);
+          }
+          __syncwarp();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint16_t* src = q_row(p, out, (lane >> 2) + 8 * i);
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+              const uint32_t* e = reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * (lane & 3));
+              q[k][i] = src ? e[0] : 0u;
+              q[k][2 + i] = src ? e[4] : 0u;
+            }
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) a.o[n][y] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          a.m[i] = -INFINITY;
+          a.l[i] = 0.f;
+        }
+      }
+      asm volatile("cp.async.wait_group %0;" ::"n"(T::kStages - 2) : "memory");
+      __syncwarp();
+      tile(p, out, (out.lo / K + x - out.first) * K, ring + stage * 2 * T::kHalf, q, qs, lane, a);
+      __syncwarp();  // every lane is done with the stage that the next load fills
+      load(stage == 0 ? T::kStages - 1 : stage - 1);
+      if (++stage == T::kStages) stage = 0;
+      if (x + 1 == x1 || x + 1 == out.first + out.tiles) {
+        store_part(p, w + out.unit, lane, a);
+        fresh = true;
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+};
+
+template <bool BF16, int D>
+__global__ void __launch_bounds__(32 * kAttnWarps, 1)
+    attn_stream_kernel(const __grid_constant__ AttnParams p, bool with_prefix) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  using T = AttnTile<D>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* cum = reinterpret_cast<int*>(smem + kAttnWarps * T::kWarpB);
+  pdl_wait();
+  pdl_launch_dependents();  // (after the wait: the merge reads the lengths before its own)
+  attn_prefix_sums<D>(p, cum, cum + p.B + 1);
+  const AttnSplit s = attn_split<D>(p, cum, with_prefix, gridDim.x * kAttnWarps);
+  // neighbouring ranges on different SMs: warp-major over the blocks
+  AttnStream<BF16, D>::worker(p, s, cum, smem_u32(smem) + warp * T::kWarpB,
+                              smem + warp * T::kWarpB, warp * gridDim.x + blockIdx.x, lane);
+}
+
+}  // namespace bsg
