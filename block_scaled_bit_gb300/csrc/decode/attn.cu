@@ -12,7 +12,42 @@ struct bsgemv_attn_plan_s {
   int bf16 = 0, Hq = 0, Hkv = 0, D = 0, page_size = 0, max_B = 0;
   void* ws = nullptr;
   bsg::AttnLayout at = {};
+  // tensor maps of the last few caches seen (a layer each)
+  struct MapEntry {
+    bool valid = false, usable = false;
+    const void *k = nullptr, *v = nullptr;
+    int64_t page_stride = 0, head_stride = 0, row_stride = 0;
+    int num_pages = 0;
+    bsg::AttnMaps maps;
+  };
+  static constexpr int kMaps = 64;
+  MapEntry maps[kMaps];
+  int next_map = 0;
 };
+
+namespace {
+
+// The cache's tensor maps, nullptr where its strides cannot be described.
+const bsg::AttnMaps* maps_of(bsgemv_attn_plan_s* plan, const bsg::AttnParams& p) {
+  for (auto& m : plan->maps)
+    if (m.valid && m.k == p.k && m.v == p.v && m.page_stride == p.page_stride &&
+        m.head_stride == p.head_stride && m.row_stride == p.row_stride &&
+        m.num_pages == p.num_pages)
+      return m.usable ? &m.maps : nullptr;
+  auto& m = plan->maps[plan->next_map];
+  plan->next_map = (plan->next_map + 1) % bsgemv_attn_plan_s::kMaps;
+  m.valid = true;
+  m.usable = bsg::attn_encode(p, &m.maps);
+  m.k = p.k;
+  m.v = p.v;
+  m.page_stride = p.page_stride;
+  m.head_stride = p.head_stride;
+  m.row_stride = p.row_stride;
+  m.num_pages = p.num_pages;
+  return m.usable ? &m.maps : nullptr;
+}
+
+}  // namespace
 
 using namespace bsg;
 
@@ -98,7 +133,12 @@ int bsgemv_attn_run(bsgemv_attn_plan_t plan, const void* q, int64_t q_stride, co
   p.lse = lse;
   p.err = static_cast<unsigned*>(plan->ws);
   p.parts = reinterpret_cast<float*>(static_cast<char*>(plan->ws) + plan->at.parts);
-  return launch_attn(p, plan->sms, static_cast<cudaStream_t>(stream));
+  p.pre_parts = reinterpret_cast<float*>(static_cast<char*>(plan->ws) + plan->at.pre_parts);
+  int mode = prefix_len > 0 ? kAttnPrefixStream : kAttnNoPrefix;
+  const AttnMaps* maps = nullptr;
+  if (mode && B * (plan->Hq / plan->Hkv) >= kAttnTensorRows && (maps = maps_of(plan, p)) != nullptr)
+    mode = kAttnPrefixTensor;
+  return launch_attn(p, mode, maps, plan->sms, static_cast<cudaStream_t>(stream));
 }
 
 int bsgemv_attn_device_status(bsgemv_attn_plan_t plan, void* stream) {

@@ -33,13 +33,28 @@ struct AttnParams {
   float* lse;
   unsigned* err;
   float* parts;       // streaming parts: slots of [16][D] sums, then [16] m, [16] l
+  float* pre_parts;   // the prefix kernel's parts
 };
 
+// What a call does with the prefix.
+enum AttnPrefixMode { kAttnNoPrefix = 0, kAttnPrefixStream = 1, kAttnPrefixTensor = 2 };
+
 struct AttnLayout {
-  size_t parts, total;
+  size_t parts, pre_parts, total;
 };
 AttnLayout attn_layout(int Hq, int Hkv, int D, int max_B, int sms);
 
-int launch_attn(const AttnParams& p, int sms, cudaStream_t s);
+// Query rows of a kv head from which the prefix goes through the tensor-memory kernel: at 16 rows
+// the streaming kernel reads the prefix once as well, and starts faster.
+constexpr int kAttnTensorRows = 17;
+
+// Tensor maps of the cache for the prefix kernel (false: the strides cannot be described).
+struct AttnMaps {
+  CUtensorMap k, v;
+};
+bool attn_encode(const AttnParams& p, AttnMaps* m);
+
+// maps: for kAttnPrefixTensor, else unused.
+int launch_attn(const AttnParams& p, int mode, const AttnMaps* maps, int sms, cudaStream_t s);
 
 }  // namespace bsg

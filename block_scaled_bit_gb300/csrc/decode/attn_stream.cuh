@@ -412,18 +412,22 @@ struct AttnStream {
 
 template <bool BF16, int D>
 __global__ void __launch_bounds__(32 * kAttnWarps, 1)
-    attn_stream_kernel(const __grid_constant__ AttnParams p, bool with_prefix) {
+    attn_stream_kernel(const __grid_constant__ AttnParams p, int mode) {
   extern __shared__ __align__(128) uint8_t smem[];
   using T = AttnTile<D>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* cum = reinterpret_cast<int*>(smem + kAttnWarps * T::kWarpB);
-  pdl_wait();
+  // After the prefix kernel (which has waited for everything before it) nothing here depends on
+  // the kernel before; the wait at the end keeps the order for the merge.
+  if (mode != kAttnPrefixTensor) pdl_wait();
   pdl_launch_dependents();  // (after the wait: the merge reads the lengths before its own)
   attn_prefix_sums<D>(p, cum, cum + p.B + 1);
-  const AttnSplit s = attn_split<D>(p, cum, with_prefix, gridDim.x * kAttnWarps);
+  const AttnSplit s =
+      attn_split<D>(p, cum, mode == kAttnPrefixStream, gridDim.x * kAttnWarps);
   // neighbouring ranges on different SMs: warp-major over the blocks
   AttnStream<BF16, D>::worker(p, s, cum, smem_u32(smem) + warp * T::kWarpB,
                               smem + warp * T::kWarpB, warp * gridDim.x + blockIdx.x, lane);
+  if (mode == kAttnPrefixTensor) pdl_wait();
 }
 
 }  // namespace bsg
