@@ -104,7 +104,7 @@ int bsgemv_attn_run(bsgemv_attn_plan_t plan, const void* q, int64_t q_stride, co
     return BSGEMV_ERR_MISALIGNED;
   // the line of tiles (attn_stream.cuh) is counted in 32 bits
   const int64_t row_tiles = (static_cast<int64_t>(B) * (plan->Hq / plan->Hkv) + 15) / 16;
-  if (row_tiles * plan->Hkv * (prefix_len / (4096 / plan->D) + 1) >= (int64_t{1} << 30))
+  if (row_tiles * plan->Hkv * (prefix_len / (4096 / plan->D) + 8) >= (int64_t{1} << 30))
     return BSGEMV_ERR_UNSUPPORTED;
   const int rc = decode_check_device(plan->device);
   if (rc != BSGEMV_OK) return rc;

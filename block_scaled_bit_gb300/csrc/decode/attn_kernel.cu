@@ -5,7 +5,9 @@
 namespace bsg {
 namespace {
 
-// One warp per (sequence, query head): its parts, in order, D / 32 elements a lane.
+// One warp per (sequence, query head), D / 32 elements a lane.  A row has tens of parts, so nothing
+// is read one after the other: each lane fetches one part's m and l, the warp agrees on the
+// weights, then the rows are fetched four at a time.
 template <bool BF16, int D>
 __global__ void __launch_bounds__(128)
     attn_merge(const __grid_constant__ AttnParams p, int mode, int sms) {
@@ -19,59 +21,105 @@ __global__ void __launch_bounds__(128)
   if (row >= p.B * p.Hq) return;
   const int b = row / p.Hq, hq = row - b * p.Hq, G = p.Hq / p.Hkv, h = hq / G, g = hq - h * G;
   constexpr int kPer = D / 32;
-  float o[kPer], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) o[i] = 0.f;
   const bool here = p.lens[b] >= max(p.prefix_len, 1);
-  // row r of a part of `rows` rows: [rows][D], then m, then l
-  const auto add = [&](const float* part, int rows, int r) {
-    const float mi = __ldcg(part + rows * D + r), li = __ldcg(part + rows * (D + 1) + r);
-    if (mi == -INFINITY) return;  // nothing in it (and its sums may not be written)
-    float v[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer / 2; ++i) {
-      const float2 f = __ldcg(reinterpret_cast<const float2*>(part + r * D + lane * kPer) + i);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-    const float next = fmaxf(m, mi), base = next == -INFINITY ? 0.f : next;
-    const float keep = exp2f(m - base), take = exp2f(mi - base);
-    m = next;
-    l = l * keep + li * take;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = o[i] * keep + v[i] * take;
-  };
-  const auto add_unit = [&](int unit, int first, int tiles, int r) {
-    const int w1 = attn_owner(s, first + tiles - 1);
-    for (int w = attn_owner(s, first); w <= w1; ++w)
-      add(p.parts + static_cast<int64_t>(w + unit) * attn_slot_floats(D), kAttnRows, r);
-  };
+
+  // The row's parts: the prefix's, then its own; a part is [rows][D] sums, [rows] m, [rows] l.
+  struct List {
+    const float* first;     // part 0
+    int64_t next;           // floats to the following part
+    int count, rows, r;     // r: the row in a part
+    bool grouped;           // columns in groups of four (the prefix kernel), else whole rows
+  } pre = {nullptr, 0, 0, 1, 0, false}, own = pre;
+  int twice = 1;            // two streams' rows in each part of the prefix
   if (here) {
-    const int tiles = cum[b + 1] - cum[b];
-    const int i = h * s.row_tiles + g / kAttnRows;
+    // (x0, tiles: a unit's stretch of the line)
+    const auto stream_list = [&](int unit, int x0, int tiles, int r) {
+      const int w0 = attn_owner(s, x0 + kAttnCost), w1 = attn_owner(s, x0 + tiles - 1);
+      return List{p.parts + static_cast<int64_t>(w0 + unit) * attn_slot_floats(D),
+                  attn_slot_floats(D), w1 - w0 + 1, kAttnRows, r, false};
+    };
     if (mode == kAttnPrefixTensor) {
       const AttnPreSplit t = attn_pre_split<D>(p.B, p.Hq, p.Hkv, p.prefix_len, sms);
       constexpr int kRows = AttnPre<D>::kSlotRows;
       const int r = b * G + g, per = t.pair ? 128 : kRows;
-      const int unit = h * t.blocks + r / per, x0 = unit * t.tiles;
+      const int unit = h * t.blocks + r / per;
+      const int x0 = unit * (t.tiles + kAttnPreCost) + kAttnPreCost;  // of its first tile
       const auto owner = [&](int x) {
         const int cut = t.extra * (t.base + 1);
         return x < cut ? x / (t.base + 1) : t.extra + (x - cut) / t.base;
       };
-      const int w1 = owner(x0 + t.tiles - 1);
-      for (int w = owner(x0); w <= w1; ++w) {
-        const float* part =
-            p.pre_parts + (static_cast<int64_t>(w) + unit) * attn_pre_slot_floats(D);
-        add(part, kRows, r % per);
-        if (t.pair) add(part, kRows, 128 + r);
-      }
+      const int w0 = owner(x0), w1 = owner(x0 + t.tiles - 1);
+      twice = t.pair ? 2 : 1;
+      pre = List{p.pre_parts + static_cast<int64_t>(w0 + unit) * attn_pre_slot_floats(D),
+                 attn_pre_slot_floats(D), (w1 - w0 + 1) * twice, kRows, r % per, true};
     } else if (s.pre_tiles) {
       const int r = b * G + g, u = h * (s.pre_units / p.Hkv) + r / kAttnRows;
-      add_unit(s.own_units + u, s.pre_start + u * s.pre_tiles, s.pre_tiles, r % kAttnRows);
+      pre = stream_list(s.own_units + u, s.pre_start + u * s.pre_tiles, s.pre_tiles, r % kAttnRows);
     }
+    const int tiles = cum[b + 1] - cum[b], i = h * s.row_tiles + g / kAttnRows;
     if (tiles)
-      add_unit(b * p.Hkv * s.row_tiles + i, cum[b] * p.Hkv * s.row_tiles + i * tiles, tiles,
-               g % kAttnRows);
+      own = stream_list(b * p.Hkv * s.row_tiles + i, cum[b] * p.Hkv * s.row_tiles + i * tiles,
+                        tiles, g % kAttnRows);
+  }
+  const int n = pre.count + own.count;
+  float o[kPer], m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) o[i] = 0.f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + lane, many = min(32, n - i0);
+    const float* src = nullptr;
+    float mi = -INFINITY, li = 0.f;
+    if (i < n) {
+      const bool first = i < pre.count;
+      const List& x = first ? pre : own;
+      const int at = first ? i / twice : i - pre.count;
+      const int r = first && twice == 2 ? x.r + 128 * (i & 1) : x.r;
+      const float* part = x.first + at * x.next;
+      src = x.grouped ? part + r * 4 : part + r * D;
+      mi = __ldcg(part + x.rows * D + r);
+      li = __ldcg(part + x.rows * (D + 1) + r);
+    }
+    float top = mi;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    const float next = fmaxf(m, top), base = next == -INFINITY ? 0.f : next;
+    const float keep = ex2(m - base);
+    // a part without positions has m = -inf: its sums may not be written and are not read
+    const float take = mi == -INFINITY ? 0.f : ex2(mi - base);
+    float sum = mi == -INFINITY ? 0.f : li * take;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    m = next;
+    l = l * keep + sum;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) o[x] *= keep;
+    for (int j0 = 0; j0 < many; j0 += 4) {
+      float v[4][kPer], t[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int from = min(j0 + j, many - 1);
+        const float* row_j = reinterpret_cast<const float*>(
+            __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(src), from));
+        const float mj = __shfl_sync(0xFFFFFFFFu, mi, from);
+        t[j] = j0 + j < many ? __shfl_sync(0xFFFFFFFFu, take, from) : 0.f;
+        const int rows = i0 + from < pre.count && pre.grouped ? pre.rows : 0;
+#pragma unroll
+        for (int x = 0; x < kPer / 2; ++x) {
+          const float2 f = mj == -INFINITY || j0 + j >= many
+                               ? make_float2(0.f, 0.f)
+                               : __ldcg(reinterpret_cast<const float2*>(
+                                     row_j + (rows ? (lane * kPer + 2 * x) / 4 * (4 * rows) +
+                                                         (lane * kPer + 2 * x) % 4
+                                                   : lane * kPer + 2 * x)));
+          v[j][2 * x] = f.x;
+          v[j][2 * x + 1] = f.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) o[x] = fmaf(v[j][x], t[j], o[x]);
+    }
   }
   uint32_t* out = reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(row) * D + lane * kPer);
 #pragma unroll
@@ -127,7 +175,7 @@ AttnLayout attn_layout(int Hq, int Hkv, int D, int max_B, int sms) {
 }
 
 bool attn_encode(const AttnParams& p, AttnMaps* m) {
-  const int ps = 1 << p.page_log2, keys = p.D == 256 ? 64 : 128;
+  const int ps = 1 << p.page_log2, keys = 64;
   const uint64_t dims[4] = {static_cast<uint64_t>(p.D), static_cast<uint64_t>(ps),
                             static_cast<uint64_t>(p.Hkv), static_cast<uint64_t>(p.num_pages)};
   // (the stride of a dimension of one is of no account)

@@ -4,46 +4,52 @@
 // once for every 256 rows.  Bound: 128 rows give 128 flops a byte of K and V, 256 rows 256, so
 // up to there the kernel is a memory stream, beyond it the tensor cores' and the exponentials'.
 //
-// A block (one per SM) holds two streams of work, each a warpgroup with its own scores, running
-// maximum and sum, and output accumulator in tensor memory:
+// A block (one per SM) holds two streams of work, each a warpgroup with its own running maximum and
+// sum, and an output accumulator in tensor memory:
 //   more than 128 rows   stream s works on query rows 128 s .. 128 s + 127, both on every key tile
 //   up to 128 rows       both work on the same rows, stream s on the key tiles i with i % 2 == s
-//   D = 256              one stream (its accumulator takes 256 of the 512 columns), two score
-//                        buffers, so that the next scores are computed during a softmax
-// Warp 8 copies K and V tiles (TMA, one box per page or 128 positions, 128-byte swizzle), one
-// thread of warp 9 issues the MMAs:  S = Q K^T  (both from shared memory, M = 128),
-// O += P V  (P from tensor memory, where it takes the place of its scores; V's d is contiguous, an
-// MN-major operand).  A row of S lies in one lane, so softmax needs no exchange between threads.
-// O is scaled to a new maximum only when a row's has grown by more than 2^8 since O's (P stays
-// below 2^8, far from overflow), which is rare after the first tiles.
-// The line of (kv head, row block, key tile) is cut into equal ranges, one per block.
+//   D = 256              one stream (its accumulator takes 256 of the 512 columns)
+// A job is a key tile of 64 positions for one stream. Warp 8 copies K and V tiles (TMA, one box
+// per page or tile and 64 d, 128-byte swizzle), one lane of warp 9 issues the MMAs:
+// S = Q K^T (both from shared memory, M = 128) and O += P V (P from tensor memory, where it takes
+// the place of its scores; V's d is contiguous, an MN-major operand).  Scores are computed a
+// ring of four (D = 256: two) buffers ahead, so that a softmax never waits for its own products:
+// with one buffer of 128 positions per stream, S, softmax and P V ran one after the other and took
+// 5300 cycles a 128 positions where the copy takes 2800.  A row of S lies in one lane, so softmax
+// needs no exchange between threads.  O is scaled to a new maximum only when a row's has grown by
+// more than 2^8 since O's (P stays below 2^8, far from overflow), which is rare after the first
+// tiles.
+// The line of (kv head, row block, key tile) is cut into equal ranges, one per block; a unit counts
+// kAttnPreCost tiles more than it has, what it costs a block to begin and end one.
 #pragma once
 
 #include "attn_stream.cuh"
 
 namespace bsg {
 
+constexpr int kAttnPreCost = 4;
+
 template <int D>
 struct AttnPre {
-  static constexpr int kKeys = D == 256 ? 64 : 128;     // positions of a tile
+  static constexpr int kKeys = 64;                      // positions of a tile
   static constexpr int kStreams = D == 256 ? 1 : 2;
-  static constexpr int kBufs = 2;                       // score buffers in all
+  static constexpr int kBufs = 2 * kStreams;            // score buffers
   static constexpr int kTileB = kKeys * D * 2;          // bytes of a K (or V) tile
   static constexpr int kQB = 128 * D * 2;               // bytes of a query tile
-  static constexpr int kQTiles = kStreams;
-  static constexpr int kRing = (224 * 1024 - kQTiles * kQB) / kTileB;
-  static constexpr int kOffRing = kQTiles * kQB;
+  static constexpr int kRingMax = (224 * 1024 - kStreams * kQB) / kTileB;
+  static constexpr int kRing = kRingMax < 16 ? kRingMax : 16;
+  static constexpr int kOffRing = kStreams * kQB;
   static constexpr int kOffBar = kOffRing + kRing * kTileB;
-  static constexpr int kSmem = kOffBar + 320 + 1024;    // (the tiles start on 1024 bytes)
+  static constexpr int kBars = 2 * kRing + 3 * kBufs + 1;
+  static constexpr int kSmem = kOffBar + (kBars * 8 + 12 + 15) / 16 * 16 + 1024;  // (1024-byte tiles)
   static constexpr int kThreads = 32 * (4 * kStreams + 2);
   static constexpr int kSlotRows = 128 * kStreams;
-  static constexpr int kColS = 0;                       // tensor memory columns: scores
-  static constexpr int kColO = kBufs * kKeys;           // then the accumulators
+  static constexpr int kColO = kBufs * kKeys;           // tensor memory: scores, then O
   static_assert(kColO + kStreams * D <= 512, "tensor memory");
-  static_assert(kRing >= 4 && kSmem <= 232448, "shared memory");
+  static_assert(kRing >= 5 && kSmem <= 232448, "shared memory");
 };
 
-// Units of the prefix: (kv head, row block); tiles of a unit.
+// Units of the prefix: (kv head, row block).  A unit's stretch of the line is kAttnPreCost + tiles.
 struct AttnPreSplit {
   int blocks;    // row blocks of a kv head
   int tiles;     // key tiles of a unit
@@ -61,13 +67,15 @@ __host__ __device__ inline AttnPreSplit attn_pre_split(int B, int Hq, int Hkv, i
   const int block_rows = s.pair ? 128 : T::kSlotRows;
   s.blocks = (rows + block_rows - 1) / block_rows;
   s.tiles = (prefix_len + T::kKeys - 1) / T::kKeys;
-  s.total = Hkv * s.blocks * s.tiles;
+  s.total = Hkv * s.blocks * (s.tiles + kAttnPreCost);
   s.workers = workers < s.total ? workers : s.total;
   s.base = s.total / s.workers;
   s.extra = s.total - s.base * s.workers;
   return s;
 }
 
+// A part is [D / 4][rows] groups of four columns, then [rows] m, [rows] l: a row is a thread's, so
+// this is the order in which a warp's stores are whole lines.
 __host__ __device__ constexpr int attn_pre_slot_floats(int D) {
   return (D == 256 ? 128 : 256) * (D + 2);
 }
@@ -107,21 +115,30 @@ BSG_DEV void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    bar) : "memory");
 }
-// D (+)= A B: A and B from shared memory (descriptors).
-BSG_DEV void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// D (+)= A B: A and B from shared memory (descriptors as low word and the common high word).
+BSG_DEV void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b),
-      "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b),
+      "r"(hi), "r"(idesc), "r"(static_cast<uint32_t>(add))
       : "memory");
 }
 // A from tensor memory.
-BSG_DEV void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+BSG_DEV void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b),
-      "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b),
+      "r"(hi), "r"(idesc), "r"(static_cast<uint32_t>(add))
       : "memory");
+}
+// One lane of the warp (the same each time).
+BSG_DEV bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(is));
+  return is != 0;
 }
 // 32 columns of this warp's 32 lanes (a lane's row), and back.
 BSG_DEV void tc_ld32(uint32_t addr, uint32_t* r) {
@@ -156,11 +173,12 @@ BSG_DEV float ex2(float x) {
 }
 BSG_DEV void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Shared-memory matrix descriptor: start, leading and stride byte offsets, 128-byte swizzle.
-BSG_DEV uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
-         (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory matrix descriptor, 128-byte swizzle: low word from the start address and the
+// leading byte offset (a byte offset adds offset / 16 to it), high word from the stride byte offset.
+BSG_DEV uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+  return ((addr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
 }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8 rows of 128 bytes
 
 template <bool BF16, int D>
 struct AttnPrefix {
@@ -182,66 +200,84 @@ struct AttnPrefix {
     BSG_DEV uint32_t bar(int i) const { return base_u + T::kOffBar + 8 * i; }
     BSG_DEV uint32_t full(int i) const { return bar(i); }                   // ring tile landed
     BSG_DEV uint32_t empty(int i) const { return bar(T::kRing + i); }       // ring tile read
-    BSG_DEV uint32_t scores(int b) const { return bar(2 * T::kRing + b); }  // S written
-    BSG_DEV uint32_t probs(int b) const { return bar(2 * T::kRing + 2 + b); }  // P written
-    BSG_DEV uint32_t out(int b) const { return bar(2 * T::kRing + 4 + b); }    // P V done
-    BSG_DEV uint32_t query() const { return bar(2 * T::kRing + 6); }           // Q written
+    // of job j (numbered over the block's whole range): its buffer's barriers and their phase
+    static BSG_DEV int buf(int j) { return j % T::kBufs; }
+    static BSG_DEV uint32_t phase(int j) { return (j / T::kBufs) & 1; }
+    BSG_DEV uint32_t scores(int j) const { return bar(2 * T::kRing + buf(j)); }               // S written
+    BSG_DEV uint32_t probs(int j) const { return bar(2 * T::kRing + T::kBufs + buf(j)); }     // P written
+    BSG_DEV uint32_t out(int j) const { return bar(2 * T::kRing + 2 * T::kBufs + buf(j)); }   // P V done
+    BSG_DEV uint32_t query() const { return bar(2 * T::kRing + 3 * T::kBufs); }               // Q written
     BSG_DEV uint32_t tile(int i) const { return base_u + T::kOffRing + i * T::kTileB; }
     BSG_DEV volatile uint32_t* words() const {
-      return reinterpret_cast<volatile uint32_t*>(base + T::kOffBar + 8 * (2 * T::kRing + 7));
+      return reinterpret_cast<volatile uint32_t*>(base + T::kOffBar + 8 * T::kBars);
     }
     BSG_DEV bool wait(uint32_t b, uint32_t parity, unsigned code) const {
       return mbar_wait(b, parity, p.a.err, code, p.wait_ns);
     }
   };
 
-  // A part of a unit: key tiles t0 .. t0 + n - 1.
+  static BSG_DEV bool wait_warp(const Ctx& c, uint32_t bar, uint32_t phase) {
+    return __all_sync(0xFFFFFFFFu, c.wait(bar, phase, kErrTimeoutFull));
+  }
+
+  // A part of a unit: key tiles t0 .. t0 + n - 1; end: where its stretch ends in this range.
   struct Seg {
-    int unit, t0, n;
+    int unit, t0, n, end;
   };
   static BSG_DEV Seg seg_at(const Ctx& c, int x) {
     Seg g;
-    g.unit = x / c.s.tiles;
-    g.t0 = x - g.unit * c.s.tiles;
-    g.n = min(c.s.tiles - g.t0, c.x1 - x);
+    const int len = c.s.tiles + kAttnPreCost;
+    g.unit = x / len;
+    const int at = x - g.unit * len;
+    g.end = min((g.unit + 1) * len, c.x1);
+    g.t0 = max(at - kAttnPreCost, 0);
+    g.n = max(g.end - g.unit * len - kAttnPreCost - g.t0, 0);
     return g;
   }
 
-  // ---- copy warp: one thread; tiles K, V, K, V, ...
-  static BSG_DEV void copy(const Ctx& c) {
+  // ---- copy warp: tiles K, V, K, V, ...; a lane per box of a tile (at most 32: 16 pages of 8
+  // positions x 2 blocks of 64 d).  Page ids are fetched a tile ahead: fetched when needed, their
+  // latency, page after page, was most of the kernel's time.
+  static BSG_DEV int fetch_page(const Ctx& c, int tile, int r) {
+    const AttnParams& a = c.p.a;
+    const int pos = tile * K + r;
+    // past the prefix: a page past the cache, which reads as zeros
+    return pos < a.prefix_len ? __ldg(a.prefix_table + (pos >> a.page_log2)) : a.num_pages;
+  }
+  static BSG_DEV bool copy(const Ctx& c, int lane) {
     const AttnPreParams& p = c.p;
-    prefetch_tmap(&p.tm_k);
-    prefetch_tmap(&p.tm_v);
+    if (lane == 0) {
+      prefetch_tmap(&p.tm_k);
+      prefetch_tmap(&p.tm_v);
+    }
+    const int boxes = K / p.box_rows * kSub, r = lane / kSub * p.box_rows, d = lane % kSub;
     int slot = 0, i = 0;
     uint32_t phase = 1;
-    const int ps = 1 << p.a.page_log2;
     for (int x = c.x0; x < c.x1;) {
       const Seg g = seg_at(c, x);
       const int head = g.unit / c.s.blocks;
-      for (int t = 0; t < g.n; ++t)
+      int page = fetch_page(c, g.t0, r);
+      for (int t = g.t0; t < g.t0 + g.n; ++t) {
+        const int here = page, pos = t * K + r;
+        page = fetch_page(c, t + 1, r);
         for (int kv = 0; kv < 2; ++kv, ++i) {
-          if (i >= T::kRing && !c.wait(c.empty(slot), phase, kErrTimeoutEmpty)) {
-            c.words()[1] = 1u;
-            c.words()[2] = i;
-            return;
+          if (i >= T::kRing && !wait_warp(c, c.empty(slot), phase)) {
+            if (lane == 0) c.words()[2] = i;
+            return false;
           }
           const uint32_t bar = c.full(slot);
-          mbar_arrive_expect_tx(bar, T::kTileB);
-          for (int r = 0; r < K; r += p.box_rows) {
-            const int pos = (g.t0 + t) * K + r;
-            // past the prefix: a page past the cache, which reads as zeros
-            const int page = pos < p.a.prefix_len ? __ldg(p.a.prefix_table + (pos >> p.a.page_log2))
-                                                  : p.a.num_pages;
-#pragma unroll
-            for (int d = 0; d < kSub; ++d)
-              tma_load_4d(c.tile(slot) + d * (K * 128) + r * 128, kv ? &p.tm_v : &p.tm_k, d * 64,
-                          pos & (ps - 1), head, page, bar);
-          }
+          if (lane == 0) mbar_arrive_expect_tx(bar, T::kTileB);
+          __syncwarp();
+          if (lane < boxes)
+            tma_load_4d(c.tile(slot) + d * (K * 128) + r * 128, kv ? &p.tm_v : &p.tm_k, d * 64,
+                        pos & ((1 << p.a.page_log2) - 1), head, here, bar);
           if (++slot == T::kRing) { slot = 0; phase ^= 1u; }
         }
-      x += g.n;
+      }
+      x = g.end;
     }
-    c.words()[2] = i;
+    if (lane == 0) c.words()[2] = i;
+    return true;
   }
 
   // After a wait that ran out: the copies in flight land before the block ends (bounded).
@@ -251,26 +287,8 @@ struct AttnPrefix {
       c.wait(c.full(i % T::kRing), (i / T::kRing) & 1, kErrTimeoutFull);
   }
 
-  // ---- Jobs: (tile, stream) in order -- two a tile where the streams have rows of their own,
-  // else one.  With two streams a segment's job j is stream j % 2's and uses that buffer; with
-  // one, jobs alternate between the buffers across segments.  `Uses` numbers each buffer's
-  // jobs, which gives the phase of its barriers.
-  struct Uses {
-    int n0 = 0, n1 = 0;  // two streams: uses of each buffer so far; one stream: jobs so far, -
-    BSG_DEV int buf(int j) const { return T::kStreams == 2 ? j & 1 : (n0 + j) & 1; }
-    BSG_DEV uint32_t phase(int j) const {
-      return T::kStreams == 2 ? (((j & 1) ? n1 : n0) + (j >> 1)) & 1 : ((n0 + j) >> 1) & 1;
-    }
-    BSG_DEV void add(int jobs) {
-      if constexpr (T::kStreams == 2) {
-        n0 += (jobs + 1) >> 1;
-        n1 += jobs >> 1;
-      } else {
-        n0 += jobs;
-      }
-    }
-  };
-
+  // ---- MMA warp.  Jobs in order: (tile, stream) -- two a tile where the streams have rows of
+  // their own, else one, the streams in turn.
   struct Ring {
     int slot = 0;
     uint32_t phase = 0;
@@ -279,72 +297,81 @@ struct AttnPrefix {
     }
   };
 
-  static BSG_DEV void mma_scores(const Ctx& c, int buf, int q, int slot) {
-    const uint32_t qa = c.base_u + q * T::kQB, ka = c.tile(slot);
+  static BSG_DEV void mma_scores(uint32_t s, uint32_t q, uint32_t k_lo) {
 #pragma unroll
     for (int k = 0; k < D / 16; ++k)
-      tc_mma_ss(c.tmem + T::kColS + buf * K,
-                smem_desc(qa + (k / 4) * (128 * 128) + (k % 4) * 32, 16, 1024),
-                smem_desc(ka + (k / 4) * (K * 128) + (k % 4) * 32, 16, 1024), kIdescS, k > 0);
+      tc_mma_ss(s, q + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16,
+                k_lo + ((k / 4) * (K * 128) + (k % 4) * 32) / 16, kDescHi, kIdescS, k > 0);
   }
-  static BSG_DEV void mma_out(const Ctx& c, int buf, int stream, int slot, bool add) {
-    const uint32_t va = c.tile(slot);
+  static BSG_DEV void mma_out(uint32_t o, uint32_t pr, uint32_t v_lo, bool add) {
 #pragma unroll
     for (int k = 0; k < K / 16; ++k)
-      tc_mma_ts(c.tmem + T::kColO + stream * D, c.tmem + T::kColS + buf * K + k * 8,
-                smem_desc(va + k * 2048, K * 128, 1024), kIdescO, add || k > 0);
+      tc_mma_ts(o, pr + k * 8, v_lo + k * 2048 / 16, kDescHi, kIdescO, add || k > 0);
   }
 
+  // The whole warp runs this, so that addresses and descriptors stay in uniform registers; one
+  // elected lane issues.  (Run by one thread, with 64-bit descriptors worked out for every MMA, the
+  // issue took 1700 cycles a job where the tensor cores take 640.)
   static BSG_DEV bool issue(const Ctx& c) {
     const bool both = T::kStreams == 2 && !c.s.pair;  // two jobs a tile
     const int per = both ? 2 : 1;
-    Ring kr, vr;     // ring places of the next job's K, of the next P V job's V
+    const bool lead = elect_one();
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, c.tmem, 0);
+    const uint32_t q_lo = desc_lo(c.base_u, 16);
+    const uint32_t k_lo = desc_lo(c.base_u + T::kOffRing, 16);
+    const uint32_t v_lo = desc_lo(c.base_u + T::kOffRing, K * 128);
+    Ring kr, vr;     // ring places of the next scores' K, of the next P V's V
     vr.next();       // (V follows its K)
-    Uses uses;
+    int job = 0;     // the segment's first job
     uint32_t seg_phase = 0;
     for (int x = c.x0; x < c.x1;) {
       const Seg g = seg_at(c, x);
+      x = g.end;
+      if (g.n == 0) continue;
       const int jobs = g.n * per;
-      if (!c.wait(c.query(), seg_phase, kErrTimeoutFull)) return false;
+      if (!wait_warp(c, c.query(), seg_phase)) return false;
       seg_phase ^= 1u;
       tc_after();
-      // scores of the segment's job j (its buffer is free: the P V two jobs before is done)
+      // scores of the segment's job j, whose buffer is free
       const auto scores = [&](int j) -> bool {
-        const int buf = uses.buf(j);
-        if (j % per == 0 && !c.wait(c.full(kr.slot), kr.phase, kErrTimeoutFull)) return false;
-        mma_scores(c, buf, both ? j & 1 : 0, kr.slot);
-        tc_commit(c.scores(buf));
+        if (j % per == 0 && !wait_warp(c, c.full(kr.slot), kr.phase)) return false;
+        if (lead) {
+          mma_scores(tmem + Ctx::buf(job + j) * K, q_lo + (both ? j & 1 : 0) * (T::kQB / 16),
+                     k_lo + kr.slot * (T::kTileB / 16));
+          tc_commit(c.scores(job + j));
+          if (j % per == per - 1) tc_commit(c.empty(kr.slot));
+        }
         if (j % per == per - 1) {
-          tc_commit(c.empty(kr.slot));
           kr.next();
           kr.next();
         }
         return true;
       };
-      for (int j = 0; j < 2 && j < jobs; ++j)
+      for (int j = 0; j < T::kBufs && j < jobs; ++j)
         if (!scores(j)) return false;
       for (int j = 0; j < jobs; ++j) {
-        const int buf = uses.buf(j);
-        const uint32_t phase = uses.phase(j);
-        if (!c.wait(c.probs(buf), phase, kErrTimeoutFull)) return false;
+        const int J = job + j;
+        if (!wait_warp(c, c.probs(J), Ctx::phase(J))) return false;
         tc_after();
-        if (j % per == 0 && !c.wait(c.full(vr.slot), vr.phase, kErrTimeoutFull)) return false;
-        // the first job of each accumulator in the segment starts it
-        mma_out(c, buf, T::kStreams == 2 ? buf : 0, vr.slot, T::kStreams == 2 ? j >= 2 : j >= 1);
-        tc_commit(c.out(buf));
+        if (j % per == 0 && !wait_warp(c, c.full(vr.slot), vr.phase)) return false;
+        if (lead) {
+          // the first job of a stream in the segment starts its accumulator
+          mma_out(tmem + T::kColO + (T::kStreams == 2 ? j & 1 : 0) * D, tmem + Ctx::buf(J) * K,
+                  v_lo + vr.slot * (T::kTileB / 16), j >= T::kStreams);
+          tc_commit(c.out(J));
+          if (j % per == per - 1) tc_commit(c.empty(vr.slot));
+        }
         if (j % per == per - 1) {
-          tc_commit(c.empty(vr.slot));
           vr.next();
           vr.next();
         }
-        if (j + 2 < jobs) {
-          // P lies where the next scores of this buffer go
-          if (!c.wait(c.out(buf), phase, kErrTimeoutFull)) return false;
-          if (!scores(j + 2)) return false;
+        // the next scores for the buffer that the job before has used: its P is read
+        if (j >= 1 && j - 1 + T::kBufs < jobs) {
+          if (!wait_warp(c, c.out(J - 1), Ctx::phase(J - 1))) return false;
+          if (!scores(j - 1 + T::kBufs)) return false;
         }
       }
-      uses.add(jobs);
-      x += g.n;
+      job += jobs;
     }
     return true;
   }
@@ -358,41 +385,89 @@ struct AttnPrefix {
     const int G = a.Hq / a.Hkv, head = g.unit / c.s.blocks, block = g.unit - head * c.s.blocks;
     const int first = block * (c.s.pair ? 128 : T::kSlotRows) + q * 128;
     uint8_t* dst = c.base + q * T::kQB;
-    for (int i = tid; i < 128 * (D / 8); i += nthr) {
-      const int r = i / (D / 8), ch = i % (D / 8), row = first + r, b = row / G;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (b < a.B)
-        v = __ldg(reinterpret_cast<const uint4*>(
-            a.q + b * a.q_stride + static_cast<int64_t>(head * G + row - b * G) * D + ch * 8));
-      *reinterpret_cast<uint4*>(dst + (ch / 8) * (128 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+    // eight loads in flight a thread: one after the other they took longer than the products
+    for (int i0 = tid; i0 < 128 * (D / 8); i0 += 8 * nthr) {
+      uint4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * nthr, row = first + i / (D / 8), b = row / G;
+        v[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < 128 * (D / 8) && b < a.B)
+          v[u] = __ldg(reinterpret_cast<const uint4*>(
+              a.q + b * a.q_stride + static_cast<int64_t>(head * G + row - b * G) * D +
+              i % (D / 8) * 8));
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * nthr, r = i / (D / 8), ch = i % (D / 8);
+        if (i >= 128 * (D / 8)) break;
+        if (a.scale_log2 < 0.f) {
+          v[u].x ^= 0x80008000u;
+          v[u].y ^= 0x80008000u;
+          v[u].z ^= 0x80008000u;
+          v[u].w ^= 0x80008000u;
+        }
+        *reinterpret_cast<uint4*>(dst + (ch / 8) * (128 * 128) + r * 128 +
+                                  (((ch & 7) ^ (r & 7)) << 4)) = v[u];
+      }
     }
     fence_async_shared();
   }
 
-  static BSG_DEV bool wait_warp(const Ctx& c, uint32_t bar, uint32_t phase) {
-    return __all_sync(0xFFFFFFFFu, c.wait(bar, phase, kErrTimeoutFull));
-  }
-
   static BSG_DEV bool softmax(const Ctx& c, int stream, int tid) {
-    Uses uses;
+    int job = 0;         // the segment's first job
     uint32_t ring0 = 0;  // ring number of the segment's first K tile
     bool ok = true;
     const bool both = T::kStreams == 2 && !c.s.pair;
     for (int x = c.x0; x < c.x1;) {
       const Seg g = seg_at(c, x);
+      x = g.end;
+      if (g.n == 0) continue;
       // everyone is done with the queries of the segment before (a warp whose wait ran out still
       // comes here)
       asm volatile("bar.sync 1, %0;" ::"n"(128 * T::kStreams) : "memory");
-      if (ok) ok = segment(c, g, stream, tid, both, uses, ring0);
-      uses.add(g.n * (both ? 2 : 1));
+      if (ok) ok = segment(c, g, stream, tid, both, job, ring0);
+      job += g.n * (both ? 2 : 1);
       ring0 += 2 * g.n;
-      x += g.n;
     }
     return ok;
   }
 
+  // The largest of a row's scores (the first `valid` of them).
+  template <bool PART>
+  static BSG_DEV float row_max(const uint32_t (&raw)[K], int valid) {
+    float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      if (!PART || i < valid) t[i & 3] = fmaxf(t[i & 3], __uint_as_float(raw[i]));
+    return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+  }
+
+  // Scores to rounded numerators 2^(scale s - base), packed into the first half of raw; their sum.
+  template <bool PART>
+  static BSG_DEV float numerators(uint32_t (&raw)[K], float scale, float base, int valid) {
+    const uint64_t sc = f32x2(scale, scale), mb = f32x2(-base, -base);
+    uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+    for (int i = 0; i < K / 2; ++i) {
+      uint64_t e;
+      asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e)
+          : "l"(f32x2(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]))), "l"(sc), "l"(mb));
+      float a = ex2(f32x2_lo(e)), b = ex2(f32x2_hi(e));
+      if (PART) {
+        a = 2 * i < valid ? a : 0.f;
+        b = 2 * i + 1 < valid ? b : 0.f;
+      }
+      const uint32_t f = pack(a, b);
+      asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[i & 1])
+          : "l"(f32x2(half_to_f32<BF16>(f, 0), half_to_f32<BF16>(f, 1))));
+      raw[i] = f;
+    }
+    return (f32x2_lo(sum[0]) + f32x2_hi(sum[0])) + (f32x2_lo(sum[1]) + f32x2_hi(sum[1]));
+  }
+
   static BSG_DEV bool segment(const Ctx& c, const Seg& g, int stream, int tid, bool both,
-                              const Uses& uses, uint32_t ring0) {
+                              int job, uint32_t ring0) {
     const AttnPreParams& p = c.p;
     const uint32_t lanes = static_cast<uint32_t>((tid >> 5) * 32) << 16;
     const uint32_t to = c.tmem + T::kColO + stream * D + lanes;
@@ -400,30 +475,21 @@ struct AttnPrefix {
     else load_q(c, g, 0, stream * 128 + tid, 256);
     mbar_arrive(c.query());
     const int jobs = g.n * (both ? 2 : 1);
+    const float scale = fabsf(p.a.scale_log2);  // (a negative scale's sign went into Q)
     float m = -INFINITY, l = 0.f;  // m: the maximum that O and l are scaled to
     int last = -1;
     for (int j = stream; j < jobs; j += T::kStreams) {  // this stream's jobs
-      const int buf = uses.buf(j), tile = both ? j >> 1 : j;
-      if (!wait_warp(c, c.scores(buf), uses.phase(j))) return false;
+      const int J = job + j, tile = both ? j >> 1 : j;
+      if (!wait_warp(c, c.scores(J), Ctx::phase(J))) return false;
       tc_after();
-      const uint32_t ts = c.tmem + T::kColS + buf * K + lanes;
+      const uint32_t ts = c.tmem + Ctx::buf(J) * K + lanes;
       uint32_t raw[K];
 #pragma unroll
       for (int i = 0; i < K; i += 32) tc_ld32(ts + i, raw + i);
       tc_wait_ld();
-      const int valid = p.a.prefix_len - (g.t0 + tile) * K;  // positions of this tile, if below K
-#pragma unroll
-      for (int i = 0; i < K; ++i)
-        raw[i] = __float_as_uint(__uint_as_float(raw[i]) * p.a.scale_log2);
-      if (valid < K) {
-#pragma unroll
-        for (int i = 0; i < K; ++i)
-          if (i >= valid) raw[i] = 0xFF800000u;  // -inf
-      }
-      float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < K; ++i) top4[i & 3] = fmaxf(top4[i & 3], __uint_as_float(raw[i]));
-      const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+      // positions of this tile, if below K: the others' scores do not count
+      const int valid = p.a.prefix_len - (g.t0 + tile) * K;
+      const float top = valid < K ? row_max<true>(raw, valid) * scale : row_max<false>(raw, K) * scale;
       // O and l move to a new maximum when it is more than 8 above theirs (or the first)
       const bool grow = top > m + 8.f;
       if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -433,7 +499,7 @@ struct AttnPrefix {
         m = next;
         if (last >= 0) {
           // the accumulator's last product is done
-          if (!wait_warp(c, c.out(uses.buf(last)), uses.phase(last))) return false;
+          if (!wait_warp(c, c.out(last), Ctx::phase(last))) return false;
           tc_after();
 #pragma unroll 1
           for (int i = 0; i < D; i += 32) {
@@ -448,16 +514,8 @@ struct AttnPrefix {
         }
       }
       const float base = m == -INFINITY ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < K / 2; ++i) {
-        const uint32_t f = pack(ex2(__uint_as_float(raw[2 * i]) - base),
-                                ex2(__uint_as_float(raw[2 * i + 1]) - base));
-        sum[(2 * i) & 3] += half_to_f32<BF16>(f, 0);
-        sum[(2 * i + 1) & 3] += half_to_f32<BF16>(f, 1);
-        raw[i] = f;
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      l += valid < K ? numerators<true>(raw, scale, base, valid)
+                     : numerators<false>(raw, scale, base, K);
 #pragma unroll
       for (int i = 0; i < K / 2; i += 32) tc_st32(ts + i, raw + i);
       tc_wait_st();
@@ -474,8 +532,8 @@ struct AttnPrefix {
         fence_async_shared();
       }
       tc_before();
-      mbar_arrive(c.probs(buf));
-      last = j;
+      mbar_arrive(c.probs(J));
+      last = J;
     }
     // the part: O, m and l
     float* part = p.parts + (static_cast<int64_t>(blockIdx.x) + g.unit) * attn_pre_slot_floats(D);
@@ -483,7 +541,7 @@ struct AttnPrefix {
     __stcg(part + T::kSlotRows * D + row, m);
     __stcg(part + T::kSlotRows * (D + 1) + row, l);
     if (last < 0) return true;  // (m = -inf: the merge leaves this part out)
-    if (!wait_warp(c, c.out(uses.buf(last)), uses.phase(last))) return false;
+    if (!wait_warp(c, c.out(last), Ctx::phase(last))) return false;
     tc_after();
 #pragma unroll 1
     for (int i = 0; i < D; i += 32) {
@@ -492,7 +550,7 @@ struct AttnPrefix {
       tc_wait_ld();
 #pragma unroll
       for (int y = 0; y < 32; y += 4)
-        __stcg(reinterpret_cast<float4*>(part + static_cast<int64_t>(row) * D + i + y),
+        __stcg(reinterpret_cast<float4*>(part) + (i + y) / 4 * T::kSlotRows + row,
                make_float4(__uint_as_float(o[y]), __uint_as_float(o[y + 1]),
                            __uint_as_float(o[y + 2]), __uint_as_float(o[y + 3])));
     }
@@ -512,7 +570,7 @@ struct AttnPrefix {
         mbar_init(c.full(i), 1);
         mbar_init(c.empty(i), 1);
       }
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < T::kBufs; ++b) {
         mbar_init(c.scores(b), 1);
         mbar_init(c.probs(b), 128);
         mbar_init(c.out(b), 1);
@@ -533,9 +591,9 @@ struct AttnPrefix {
     pdl_launch_dependents();
     bool ok = true;
     if (warp == kCopyWarp) {
-      if ((threadIdx.x & 31) == 0) copy(c);
+      ok = copy(c, threadIdx.x & 31);
     } else if (warp == kMmaWarp) {
-      if ((threadIdx.x & 31) == 0) ok = issue(c);
+      ok = issue(c);
     } else {
       ok = softmax(c, warp / 4, threadIdx.x & 127);
     }

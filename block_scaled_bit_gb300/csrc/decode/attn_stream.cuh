@@ -8,7 +8,9 @@
 // registers with the running maximum in base 2.
 //
 // All tiles of all (sequence, kv head, row tile) are laid in a line and cut into equal ranges, one
-// per warp, so that the lengths' spread does not matter; a range leaves one part per unit that it
+// per warp, so that the lengths' spread does not matter; a unit counts kAttnCost tiles more than
+// it has, what it costs a warp to begin and end one (without them, a warp with a dozen short
+// sequences took twice as long as the others).  A range leaves one part per unit that it
 // touches.  Warp w's part of unit u lies in slot w + u (each next part moves on in w or in u).
 #pragma once
 
@@ -24,12 +26,14 @@ struct AttnSplit {
   int row_tiles;     // row tiles of a sequence's group
   int own_units;     // B * Hkv * row_tiles
   int pre_units;     // prefix units, 0 where another kernel does it
-  int pre_tiles;     // tiles of a prefix unit
-  int pre_start;     // first tile of the prefix units
-  int total;         // tiles in all (below 2^31)
-  int base, extra;   // tiles of a worker; the first `extra` have one more
-  int workers;       // workers with tiles
+  int pre_tiles;     // stretch of a prefix unit
+  int pre_start;     // where the prefix units start
+  int total;         // the line's length (below 2^31)
+  int base, extra;   // a worker's range; the first `extra` have one more
+  int workers;       // workers with a range
 };
+
+constexpr int kAttnCost = 2;
 
 template <int D>
 struct AttnTile {
@@ -50,7 +54,7 @@ BSG_DEV int own_tiles(const AttnParams& p, int b) {
   return (len + K - 1) / K - p.prefix_len / K;
 }
 
-// cum[b] = tiles of one (head, row tile) of the sequences before b, b <= B, by the whole block;
+// cum[b] = stretch (tiles and cost) of one (head, row tile) of the sequences before b, b <= B, by the whole block;
 // cum must hold B + 1 integers, tmp 33.
 template <int D>
 BSG_DEV void attn_prefix_sums(const AttnParams& p, int* cum, int* tmp) {
@@ -61,7 +65,7 @@ BSG_DEV void attn_prefix_sums(const AttnParams& p, int* cum, int* tmp) {
     if (b0 + i < p.B) {
       const int t = own_tiles<D>(p, b0 + i);
       cum[b0 + i] = sum;
-      sum += t;
+      sum += t ? t + kAttnCost : 0;
     }
   int inc = sum;
 #pragma unroll
@@ -86,7 +90,7 @@ BSG_DEV AttnSplit attn_split(const AttnParams& p, const int* cum, bool with_pref
   s.row_tiles = (G + kAttnRows - 1) / kAttnRows;
   s.own_units = p.B * p.Hkv * s.row_tiles;
   s.pre_start = cum[p.B] * p.Hkv * s.row_tiles;
-  s.pre_tiles = with_prefix ? (p.prefix_len + AttnTile<D>::kKeys - 1) / AttnTile<D>::kKeys : 0;
+  s.pre_tiles = with_prefix ? (p.prefix_len + AttnTile<D>::kKeys - 1) / AttnTile<D>::kKeys + kAttnCost : 0;
   s.pre_units = s.pre_tiles ? p.Hkv * ((p.B * G + kAttnRows - 1) / kAttnRows) : 0;
   s.total = s.pre_start + s.pre_units * s.pre_tiles;
   s.workers = min(workers, s.total);
@@ -107,7 +111,7 @@ __host__ __device__ constexpr int attn_slot_floats(int D) { return kAttnRows * (
 struct AttnUnit {
   int unit, b, h, r;        // b = -1: the prefix
   int lo, hi;               // positions
-  int first;                // line position of its first tile
+  int first;                // line position of its first tile, after the cost
   int tiles;
 };
 
@@ -121,8 +125,8 @@ BSG_DEV AttnUnit attn_unit_at(const AttnParams& p, const AttnSplit& s, const int
     u.b = -1;
     u.h = i / rows;
     u.r = i - u.h * rows;
-    u.first = s.pre_start + i * s.pre_tiles;
-    u.tiles = s.pre_tiles;
+    u.first = s.pre_start + i * s.pre_tiles + kAttnCost;
+    u.tiles = s.pre_tiles - kAttnCost;
     u.lo = 0;
     u.hi = p.prefix_len;
     return u;
@@ -136,12 +140,12 @@ BSG_DEV AttnUnit attn_unit_at(const AttnParams& p, const AttnSplit& s, const int
     else z = mid;
   }
   u.b = a;
-  u.tiles = cum[a + 1] - cum[a];
-  const int i = (tile - cum[a] * per) / u.tiles;
+  const int len = cum[a + 1] - cum[a], i = (tile - cum[a] * per) / len;
+  u.tiles = len - kAttnCost;
   u.h = i / s.row_tiles;
   u.r = i - u.h * s.row_tiles;
   u.unit = (a * p.Hkv + u.h) * s.row_tiles + u.r;
-  u.first = cum[a] * per + i * u.tiles;
+  u.first = cum[a] * per + i * len + kAttnCost;
   u.lo = p.prefix_len;
   u.hi = p.lens[a];
   (void)K;
@@ -158,24 +162,33 @@ struct AttnStream {
   // Byte offset of chunk c of row r in a half tile: chunks swizzled by the row.
   static BSG_DEV uint32_t at(int r, int c) { return r * (D * 2) + ((c ^ (r & 7)) << 4); }
 
-  // Element offset of a position's row in the cache, -1 outside the unit or the pages.
-  static BSG_DEV int64_t row_of(const AttnParams& p, const AttnUnit& u, int pos) {
-    if (pos < u.lo || pos >= u.hi) return -1;
-    const int i = pos >> p.page_log2;
-    const int page = u.b < 0 ? p.prefix_table[i] : p.tables[u.b * p.table_stride + i];
-    if (page < 0 || page >= p.num_pages) return -1;
-    return page * p.page_stride + u.h * p.head_stride +
-           (pos & ((1 << p.page_log2) - 1)) * p.row_stride;
-  }
-
   // A tile's rows into a ring stage (rows outside the unit: zeros).  Lane j knows where rows j
-  // (and j + 32) are; each step moves 32 chunks.
+  // (and j + 32) are; each step moves 32 chunks.  Page ids are fetched a tile ahead and used only
+  // when the tile is issued, so that their latency passes under the products.
   static constexpr int kOff = K > 32 ? 2 : 1;
-  static BSG_DEV void offsets(const AttnParams& p, const AttnUnit& u, int tile, int lane,
-                              int64_t (&off)[kOff]) {
-    const int pos = (u.lo / K + tile) * K + lane;
+  static BSG_DEV void fetch(const AttnParams& p, const AttnUnit& u, int tile, int lane,
+                            int (&page)[kOff]) {
 #pragma unroll
-    for (int i = 0; i < kOff; ++i) off[i] = (lane + 32 * i < K) ? row_of(p, u, pos + 32 * i) : -1;
+    for (int i = 0; i < kOff; ++i) {
+      const int pos = (u.lo / K + tile) * K + lane + 32 * i;
+      page[i] = -1;
+      if (lane + 32 * i < K && pos >= u.lo && pos < u.hi) {
+        const int at = pos >> p.page_log2;
+        page[i] = u.b < 0 ? __ldg(p.prefix_table + at) : __ldg(p.tables + u.b * p.table_stride + at);
+      }
+    }
+  }
+  // Element offsets of the rows in the cache, -1 outside the unit or the pages.
+  static BSG_DEV void offsets(const AttnParams& p, const AttnUnit& u, int tile, int lane,
+                              const int (&page)[kOff], int64_t (&off)[kOff]) {
+#pragma unroll
+    for (int i = 0; i < kOff; ++i) {
+      const int pos = (u.lo / K + tile) * K + lane + 32 * i;
+      off[i] = page[i] < 0 || page[i] >= p.num_pages
+                   ? -1
+                   : page[i] * p.page_stride + u.h * p.head_stride +
+                         (pos & ((1 << p.page_log2) - 1)) * p.row_stride;
+    }
   }
   static BSG_DEV void issue(const AttnParams& p, uint32_t stage, const int64_t (&off)[kOff],
                             int lane) {
@@ -338,17 +351,30 @@ struct AttnStream {
     if (w >= s.workers) return;
     const int x0 = attn_start(s, w), x1 = attn_start(s, w + 1);
     // the loads run ahead of the products, over units' ends: each has its own place in the line
-    AttnUnit in = attn_unit_at<D>(p, s, cum, x0), out = in;
-    int xi = x0;
-    int64_t off[kOff];
-    offsets(p, in, xi - in.first, lane, off);
+    struct Place {
+      AttnUnit u;
+      int x;
+    };
+    // the first tile at or after a place (x1: none left)
+    const auto settle = [&](Place& a) {
+      while (a.x < x1 && (a.x < a.u.first || a.x >= a.u.first + a.u.tiles)) {
+        if (a.x < a.u.first) a.x = min(a.u.first, x1);
+        else a.u = attn_unit_at<D>(p, s, cum, a.x);
+      }
+    };
+    Place in = {attn_unit_at<D>(p, s, cum, x0), x0};
+    settle(in);
+    Place out = in;
+    int page[kOff];
+    if (in.x < x1) fetch(p, in.u, in.x - in.u.first, lane, page);
     const auto load = [&](int stage) {
-      if (xi < x1) {
+      if (in.x < x1) {
+        int64_t off[kOff];
+        offsets(p, in.u, in.x - in.u.first, lane, page, off);
         issue(p, ring + stage * 2 * T::kHalf, off, lane);
-        if (++xi < x1) {
-          if (xi == in.first + in.tiles) in = attn_unit_at<D>(p, s, cum, xi);
-          offsets(p, in, xi - in.first, lane, off);
-        }
+        ++in.x;
+        settle(in);
+        if (in.x < x1) fetch(p, in.u, in.x - in.u.first, lane, page);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -359,8 +385,8 @@ struct AttnStream {
     Acc a;
     int stage = 0;
     bool fresh = true;
-    for (int x = x0; x < x1; ++x) {
-      if (x == out.first + out.tiles) out = attn_unit_at<D>(p, s, cum, x);
+    while (out.x < x1) {
+      const AttnUnit& u = out.u;
       if (fresh) {
         fresh = false;
         if constexpr (D == 256) {
@@ -368,7 +394,7 @@ struct AttnStream {
           __syncwarp();
           for (int i = lane; i < kAttnRows * kCpr; i += 32) {
             const int r = i / kCpr, c = i % kCpr;
-            const uint16_t* src = q_row(p, out, r);
+            const uint16_t* src = q_row(p, u, r);
             *reinterpret_cast<uint4*>(dst + at(r, c)) =
                 src ? *reinterpret_cast<const uint4*>(src + c * 8) : make_uint4(0, 0, 0, 0);
           }
@@ -376,7 +402,7 @@ struct AttnStream {
         } else {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint16_t* src = q_row(p, out, (lane >> 2) + 8 * i);
+            const uint16_t* src = q_row(p, u, (lane >> 2) + 8 * i);
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
               const uint32_t* e = reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * (lane & 3));
@@ -397,13 +423,15 @@ struct AttnStream {
       }
       asm volatile("cp.async.wait_group %0;" ::"n"(T::kStages - 2) : "memory");
       __syncwarp();
-      tile(p, out, (out.lo / K + x - out.first) * K, ring + stage * 2 * T::kHalf, q, qs, lane, a);
+      tile(p, u, (u.lo / K + out.x - u.first) * K, ring + stage * 2 * T::kHalf, q, qs, lane, a);
       __syncwarp();  // every lane is done with the stage that the next load fills
       load(stage == 0 ? T::kStages - 1 : stage - 1);
       if (++stage == T::kStages) stage = 0;
-      if (x + 1 == x1 || x + 1 == out.first + out.tiles) {
-        store_part(p, w + out.unit, lane, a);
+      ++out.x;
+      if (out.x == x1 || out.x == u.first + u.tiles) {
+        store_part(p, w + u.unit, lane, a);
         fresh = true;
+        settle(out);
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
