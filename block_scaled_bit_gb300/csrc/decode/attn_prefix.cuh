@@ -201,8 +201,8 @@ struct AttnPrefix {
     BSG_DEV uint32_t full(int i) const { return bar(i); }                   // ring tile landed
     BSG_DEV uint32_t empty(int i) const { return bar(T::kRing + i); }       // ring tile read
     // of job j (numbered over the block's whole range): its buffer's barriers and their phase
-    static BSG_DEV int buf(int j) { return j % T::kBufs; }
-    static BSG_DEV uint32_t phase(int j) { return (j / T::kBufs) & 1; }
+    static BSG_DEV uint32_t buf(uint32_t j) { return j % T::kBufs; }
+    static BSG_DEV uint32_t phase(uint32_t j) { return (j / T::kBufs) & 1; }
     BSG_DEV uint32_t scores(int j) const { return bar(2 * T::kRing + buf(j)); }               // S written
     BSG_DEV uint32_t probs(int j) const { return bar(2 * T::kRing + T::kBufs + buf(j)); }     // P written
     BSG_DEV uint32_t out(int j) const { return bar(2 * T::kRing + 2 * T::kBufs + buf(j)); }   // P V done
@@ -290,7 +290,7 @@ struct AttnPrefix {
   // ---- MMA warp.  Jobs in order: (tile, stream) -- two a tile where the streams have rows of
   // their own, else one, the streams in turn.
   struct Ring {
-    int slot = 0;
+    uint32_t slot = 0;
     uint32_t phase = 0;
     BSG_DEV void next() {
       if (++slot == T::kRing) { slot = 0; phase ^= 1u; }
@@ -310,68 +310,85 @@ struct AttnPrefix {
   }
 
   // The whole warp runs this, so that addresses and descriptors stay in uniform registers; one
-  // elected lane issues.  (Run by one thread, with 64-bit descriptors worked out for every MMA, the
-  // issue took 1700 cycles a job where the tensor cores take 640.)
+  // elected lane issues.  The warp's own instructions bound the rate of jobs (run by one thread,
+  // with descriptors and phases worked out for every MMA, a job took 1700 cycles, and the tensor
+  // cores need 640), so the state is kept in steps: buffer and phase of the next P V, of the next
+  // scores, and of the job whose buffer those take.
+  struct Turn {  // a buffer's number and its barriers' phase
+    uint32_t b = 0, phase = 0;
+    BSG_DEV void next() {
+      b = (b + 1) & (T::kBufs - 1);
+      phase ^= b == 0 ? 1u : 0u;
+    }
+  };
   static BSG_DEV bool issue(const Ctx& c) {
     const bool both = T::kStreams == 2 && !c.s.pair;  // two jobs a tile
-    const int per = both ? 2 : 1;
+    const uint32_t per = both ? 2 : 1;
     const bool lead = elect_one();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, c.tmem, 0);
     const uint32_t q_lo = desc_lo(c.base_u, 16);
     const uint32_t k_lo = desc_lo(c.base_u + T::kOffRing, 16);
     const uint32_t v_lo = desc_lo(c.base_u + T::kOffRing, K * 128);
-    Ring kr, vr;     // ring places of the next scores' K, of the next P V's V
-    vr.next();       // (V follows its K)
-    int job = 0;     // the segment's first job
+    const uint32_t full = c.full(0), empty = c.empty(0), scored = c.scores(0), probs = c.probs(0),
+                   outs = c.out(0);
+    Ring kr, vr;             // ring places of the next scores' K, of the next P V's V
+    vr.next();               // (V follows its K)
+    Turn sc, pv, old;        // next scores, next P V, the P V before
     uint32_t seg_phase = 0;
     for (int x = c.x0; x < c.x1;) {
       const Seg g = seg_at(c, x);
       x = g.end;
       if (g.n == 0) continue;
-      const int jobs = g.n * per;
-      if (!wait_warp(c, c.query(), seg_phase)) return false;
+      const uint32_t jobs = g.n * per;
+      if (!c.wait(c.query(), seg_phase, kErrTimeoutFull)) return false;
       seg_phase ^= 1u;
       tc_after();
-      // scores of the segment's job j, whose buffer is free
-      const auto scores = [&](int j) -> bool {
-        if (j % per == 0 && !wait_warp(c, c.full(kr.slot), kr.phase)) return false;
+      uint32_t sj = 0;  // the segment's next scores
+      const auto scores = [&]() -> bool {
+        const uint32_t odd = sj & 1u;
+        const bool first = !both || odd == 0, last = !both || odd == 1;
+        if (first && !c.wait(full + 8 * kr.slot, kr.phase, kErrTimeoutFull)) return false;
         if (lead) {
-          mma_scores(tmem + Ctx::buf(job + j) * K, q_lo + (both ? j & 1 : 0) * (T::kQB / 16),
+          mma_scores(tmem + sc.b * K, q_lo + (both ? odd : 0u) * (T::kQB / 16),
                      k_lo + kr.slot * (T::kTileB / 16));
-          tc_commit(c.scores(job + j));
-          if (j % per == per - 1) tc_commit(c.empty(kr.slot));
+          tc_commit(scored + 8 * sc.b);
+          if (last) tc_commit(empty + 8 * kr.slot);
         }
-        if (j % per == per - 1) {
+        if (last) {
           kr.next();
           kr.next();
         }
+        sc.next();
+        ++sj;
         return true;
       };
-      for (int j = 0; j < T::kBufs && j < jobs; ++j)
-        if (!scores(j)) return false;
-      for (int j = 0; j < jobs; ++j) {
-        const int J = job + j;
-        if (!wait_warp(c, c.probs(J), Ctx::phase(J))) return false;
+      while (sj < T::kBufs && sj < jobs)
+        if (!scores()) return false;
+      for (uint32_t j = 0; j < jobs; ++j) {
+        const uint32_t odd = j & 1u;
+        const bool first = !both || odd == 0, last = !both || odd == 1;
+        if (!c.wait(probs + 8 * pv.b, pv.phase, kErrTimeoutFull)) return false;
+        if (first && !c.wait(full + 8 * vr.slot, vr.phase, kErrTimeoutFull)) return false;
         tc_after();
-        if (j % per == 0 && !wait_warp(c, c.full(vr.slot), vr.phase)) return false;
         if (lead) {
           // the first job of a stream in the segment starts its accumulator
-          mma_out(tmem + T::kColO + (T::kStreams == 2 ? j & 1 : 0) * D, tmem + Ctx::buf(J) * K,
+          mma_out(tmem + T::kColO + (T::kStreams == 2 ? odd : 0u) * D, tmem + pv.b * K,
                   v_lo + vr.slot * (T::kTileB / 16), j >= T::kStreams);
-          tc_commit(c.out(J));
-          if (j % per == per - 1) tc_commit(c.empty(vr.slot));
+          tc_commit(outs + 8 * pv.b);
+          if (last) tc_commit(empty + 8 * vr.slot);
         }
-        if (j % per == per - 1) {
+        if (last) {
           vr.next();
           vr.next();
         }
-        // the next scores for the buffer that the job before has used: its P is read
-        if (j >= 1 && j - 1 + T::kBufs < jobs) {
-          if (!wait_warp(c, c.out(J - 1), Ctx::phase(J - 1))) return false;
-          if (!scores(j - 1 + T::kBufs)) return false;
+        // the next scores, for the buffer that the job before has used: its P is read
+        if (j >= 1 && sj < jobs) {
+          if (!c.wait(outs + 8 * old.b, old.phase, kErrTimeoutFull)) return false;
+          if (!scores()) return false;
         }
+        old = pv;
+        pv.next();
       }
-      job += jobs;
     }
     return true;
   }
