@@ -9,13 +9,13 @@
 //   more than 128 rows   stream s works on query rows 128 s .. 128 s + 127, both on every key tile
 //   up to 128 rows       both work on the same rows, stream s on the key tiles i with i % 2 == s
 //   D = 256              one stream (its accumulator takes 256 of the 512 columns)
-// A job is a key tile of 64 positions for one stream. Warp 8 copies K and V tiles (TMA, one box
-// per page or tile and 64 d, 128-byte swizzle), one lane of warp 9 issues the MMAs:
-// S = Q K^T (both from shared memory, M = 128) and O += P V (P from tensor memory, where it takes
-// the place of its scores; V's d is contiguous, an MN-major operand).  Scores are computed a
-// ring of four (D = 256: two) buffers ahead, so that a softmax never waits for its own products:
-// with one buffer of 128 positions per stream, S, softmax and P V ran one after the other and took
-// 5300 cycles a 128 positions where the copy takes 2800.  A row of S lies in one lane, so softmax
+// A job is a key tile of 64 positions for one stream.  One warp copies K and V tiles (TMA, one box
+// per page or tile and 64 d, 128-byte swizzle); a warp per stream issues its MMAs:  S = Q K^T (both from shared memory, M = 128) and O += P V (P from tensor memory, where it takes
+// the place of its scores; V's d is contiguous, an MN-major operand).  A stream has two score
+// buffers, so that a softmax never waits for its own products: with one buffer of 128 positions,
+// S, softmax and P V ran one after the other and took 5300 cycles a 128 positions where the copy
+// takes 2800.  And it has an MMA warp of its own: one warp for both waited in turn for either's
+// probabilities and buffers, 450 of the 1350 cycles of a job, while the tensor cores ran dry.  A row of S lies in one lane, so softmax
 // needs no exchange between threads.  O is scaled to a new maximum only when a row's has grown by
 // more than 2^8 since O's (P stays below 2^8, far from overflow), which is rare after the first
 // tiles.
@@ -42,7 +42,7 @@ struct AttnPre {
   static constexpr int kOffBar = kOffRing + kRing * kTileB;
   static constexpr int kBars = 2 * kRing + 3 * kBufs + 1;
   static constexpr int kSmem = kOffBar + (kBars * 8 + 12 + 15) / 16 * 16 + 1024;  // (1024-byte tiles)
-  static constexpr int kThreads = 32 * (4 * kStreams + 2);
+  static constexpr int kThreads = 32 * (5 * kStreams + 1);
   static constexpr int kSlotRows = 128 * kStreams;
   static constexpr int kColO = kBufs * kKeys;           // tensor memory: scores, then O
   static_assert(kColO + kStreams * D <= 512, "tensor memory");
@@ -200,12 +200,12 @@ struct AttnPrefix {
     BSG_DEV uint32_t bar(int i) const { return base_u + T::kOffBar + 8 * i; }
     BSG_DEV uint32_t full(int i) const { return bar(i); }                   // ring tile landed
     BSG_DEV uint32_t empty(int i) const { return bar(T::kRing + i); }       // ring tile read
-    // of job j (numbered over the block's whole range): its buffer's barriers and their phase
-    static BSG_DEV uint32_t buf(uint32_t j) { return j % T::kBufs; }
-    static BSG_DEV uint32_t phase(uint32_t j) { return (j / T::kBufs) & 1; }
-    BSG_DEV uint32_t scores(int j) const { return bar(2 * T::kRing + buf(j)); }               // S written
-    BSG_DEV uint32_t probs(int j) const { return bar(2 * T::kRing + T::kBufs + buf(j)); }     // P written
-    BSG_DEV uint32_t out(int j) const { return bar(2 * T::kRing + 2 * T::kBufs + buf(j)); }   // P V done
+    // of a stream's job j (numbered over the block's whole range): its buffer's barriers, their phase
+    static BSG_DEV uint32_t buf(uint32_t stream, uint32_t j) { return 2 * stream + (j & 1u); }
+    static BSG_DEV uint32_t phase(uint32_t j) { return (j >> 1) & 1u; }
+    BSG_DEV uint32_t scores(uint32_t b) const { return bar(2 * T::kRing + b); }               // S written
+    BSG_DEV uint32_t probs(uint32_t b) const { return bar(2 * T::kRing + T::kBufs + b); }     // P written
+    BSG_DEV uint32_t out(uint32_t b) const { return bar(2 * T::kRing + 2 * T::kBufs + b); }   // P V done
     BSG_DEV uint32_t query() const { return bar(2 * T::kRing + 3 * T::kBufs); }               // Q written
     BSG_DEV uint32_t tile(int i) const { return base_u + T::kOffRing + i * T::kTileB; }
     BSG_DEV volatile uint32_t* words() const {
@@ -224,6 +224,13 @@ struct AttnPrefix {
   struct Seg {
     int unit, t0, n, end;
   };
+  // A stream's jobs in a segment of n tiles, and the tile of its j-th.
+  static BSG_DEV uint32_t jobs_of(const Ctx& c, uint32_t stream, int n) {
+    return c.s.pair ? (n + 1 - stream) >> 1 : n;
+  }
+  static BSG_DEV uint32_t tile_of(const Ctx& c, uint32_t stream, uint32_t j) {
+    return c.s.pair ? 2 * j + stream : j;
+  }
   static BSG_DEV Seg seg_at(const Ctx& c, int x) {
     Seg g;
     const int len = c.s.tiles + kAttnPreCost;
@@ -287,13 +294,16 @@ struct AttnPrefix {
       c.wait(c.full(i % T::kRing), (i / T::kRing) & 1, kErrTimeoutFull);
   }
 
-  // ---- MMA warp.  Jobs in order: (tile, stream) -- two a tile where the streams have rows of
-  // their own, else one, the streams in turn.
+  // ---- MMA warp of a stream
+  // Place in the ring of tiles, moved on by any number.
   struct Ring {
-    uint32_t slot = 0;
-    uint32_t phase = 0;
-    BSG_DEV void next() {
-      if (++slot == T::kRing) { slot = 0; phase ^= 1u; }
+    uint32_t slot, phase;
+    BSG_DEV void move(uint32_t n) {
+      slot += n;
+      while (slot >= T::kRing) {
+        slot -= T::kRing;
+        phase ^= 1u;
+      }
     }
   };
 
@@ -309,86 +319,64 @@ struct AttnPrefix {
       tc_mma_ts(o, pr + k * 8, v_lo + k * 2048 / 16, kDescHi, kIdescO, add || k > 0);
   }
 
-  // The whole warp runs this, so that addresses and descriptors stay in uniform registers; one
-  // elected lane issues.  The warp's own instructions bound the rate of jobs (run by one thread,
-  // with descriptors and phases worked out for every MMA, a job took 1700 cycles, and the tensor
-  // cores need 640), so the state is kept in steps: buffer and phase of the next P V, of the next
-  // scores, and of the job whose buffer those take.
-  struct Turn {  // a buffer's number and its barriers' phase
-    uint32_t b = 0, phase = 0;
-    BSG_DEV void next() {
-      b = (b + 1) & (T::kBufs - 1);
-      phase ^= b == 0 ? 1u : 0u;
-    }
-  };
-  static BSG_DEV bool issue(const Ctx& c) {
-    const bool both = T::kStreams == 2 && !c.s.pair;  // two jobs a tile
-    const uint32_t per = both ? 2 : 1;
+  // The whole warp runs this; one elected lane issues.  (Run by one thread, with 64-bit descriptors
+  // and phases worked out for every MMA, a job took 1700 cycles; the tensor cores need 640.)
+  static BSG_DEV bool issue(const Ctx& c, uint32_t stream) {
     const bool lead = elect_one();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, c.tmem, 0);
-    const uint32_t q_lo = desc_lo(c.base_u, 16);
+    const uint32_t q_lo = desc_lo(c.base_u + (c.s.pair ? 0u : stream) * T::kQB, 16);
     const uint32_t k_lo = desc_lo(c.base_u + T::kOffRing, 16);
     const uint32_t v_lo = desc_lo(c.base_u + T::kOffRing, K * 128);
-    const uint32_t full = c.full(0), empty = c.empty(0), scored = c.scores(0), probs = c.probs(0),
-                   outs = c.out(0);
-    Ring kr, vr;             // ring places of the next scores' K, of the next P V's V
-    vr.next();               // (V follows its K)
-    Turn sc, pv, old;        // next scores, next P V, the P V before
-    uint32_t seg_phase = 0;
+    const uint32_t o = tmem + T::kColO + stream * D;
+    const uint32_t step = c.s.pair ? 4 : 2;  // ring tiles from a job's K (or V) to the next's
+    Ring base = {0, 0};                      // the segment's first K
+    uint32_t job = 0, seg_phase = 0;         // the segment's first job
     for (int x = c.x0; x < c.x1;) {
       const Seg g = seg_at(c, x);
       x = g.end;
       if (g.n == 0) continue;
-      const uint32_t jobs = g.n * per;
+      const uint32_t jobs = jobs_of(c, stream, g.n);
+      Ring kr = base, vr;
+      kr.move(2 * tile_of(c, stream, 0));
+      vr = kr;
+      vr.move(1);
+      base.move(2 * g.n);
       if (!c.wait(c.query(), seg_phase, kErrTimeoutFull)) return false;
       seg_phase ^= 1u;
       tc_after();
-      uint32_t sj = 0;  // the segment's next scores
+      uint32_t sj = 0;  // the segment's next scores; their buffer is free
       const auto scores = [&]() -> bool {
-        const uint32_t odd = sj & 1u;
-        const bool first = !both || odd == 0, last = !both || odd == 1;
-        if (first && !c.wait(full + 8 * kr.slot, kr.phase, kErrTimeoutFull)) return false;
+        const uint32_t b = Ctx::buf(stream, job + sj);
+        if (!c.wait(c.full(kr.slot), kr.phase, kErrTimeoutFull)) return false;
         if (lead) {
-          mma_scores(tmem + sc.b * K, q_lo + (both ? odd : 0u) * (T::kQB / 16),
-                     k_lo + kr.slot * (T::kTileB / 16));
-          tc_commit(scored + 8 * sc.b);
-          if (last) tc_commit(empty + 8 * kr.slot);
+          mma_scores(tmem + b * K, q_lo, k_lo + kr.slot * (T::kTileB / 16));
+          tc_commit(c.scores(b));
+          tc_commit(c.empty(kr.slot));
         }
-        if (last) {
-          kr.next();
-          kr.next();
-        }
-        sc.next();
+        kr.move(step);
         ++sj;
         return true;
       };
-      while (sj < T::kBufs && sj < jobs)
+      while (sj < 2 && sj < jobs)
         if (!scores()) return false;
       for (uint32_t j = 0; j < jobs; ++j) {
-        const uint32_t odd = j & 1u;
-        const bool first = !both || odd == 0, last = !both || odd == 1;
-        if (!c.wait(probs + 8 * pv.b, pv.phase, kErrTimeoutFull)) return false;
-        if (first && !c.wait(full + 8 * vr.slot, vr.phase, kErrTimeoutFull)) return false;
+        const uint32_t b = Ctx::buf(stream, job + j), phase = Ctx::phase(job + j);
+        if (!c.wait(c.probs(b), phase, kErrTimeoutFull)) return false;
+        if (!c.wait(c.full(vr.slot), vr.phase, kErrTimeoutFull)) return false;
         tc_after();
         if (lead) {
-          // the first job of a stream in the segment starts its accumulator
-          mma_out(tmem + T::kColO + (T::kStreams == 2 ? odd : 0u) * D, tmem + pv.b * K,
-                  v_lo + vr.slot * (T::kTileB / 16), j >= T::kStreams);
-          tc_commit(outs + 8 * pv.b);
-          if (last) tc_commit(empty + 8 * vr.slot);
+          mma_out(o, tmem + b * K, v_lo + vr.slot * (T::kTileB / 16), j > 0);
+          tc_commit(c.out(b));
+          tc_commit(c.empty(vr.slot));
         }
-        if (last) {
-          vr.next();
-          vr.next();
-        }
-        // the next scores, for the buffer that the job before has used: its P is read
-        if (j >= 1 && sj < jobs) {
-          if (!c.wait(outs + 8 * old.b, old.phase, kErrTimeoutFull)) return false;
+        vr.move(step);
+        if (sj < jobs) {
+          // the next scores go where this job's P is read
+          if (!c.wait(c.out(b), phase, kErrTimeoutFull)) return false;
           if (!scores()) return false;
         }
-        old = pv;
-        pv.next();
       }
+      job += jobs;
     }
     return true;
   }
@@ -432,10 +420,9 @@ struct AttnPrefix {
   }
 
   static BSG_DEV bool softmax(const Ctx& c, int stream, int tid) {
-    int job = 0;         // the segment's first job
+    uint32_t job = 0;    // the segment's first job
     uint32_t ring0 = 0;  // ring number of the segment's first K tile
     bool ok = true;
-    const bool both = T::kStreams == 2 && !c.s.pair;
     for (int x = c.x0; x < c.x1;) {
       const Seg g = seg_at(c, x);
       x = g.end;
@@ -443,8 +430,8 @@ struct AttnPrefix {
       // everyone is done with the queries of the segment before (a warp whose wait ran out still
       // comes here)
       asm volatile("bar.sync 1, %0;" ::"n"(128 * T::kStreams) : "memory");
-      if (ok) ok = segment(c, g, stream, tid, both, job, ring0);
-      job += g.n * (both ? 2 : 1);
+      if (ok) ok = segment(c, g, stream, tid, job, ring0);
+      job += jobs_of(c, stream, g.n);
       ring0 += 2 * g.n;
     }
     return ok;
@@ -483,29 +470,29 @@ struct AttnPrefix {
     return (f32x2_lo(sum[0]) + f32x2_hi(sum[0])) + (f32x2_lo(sum[1]) + f32x2_hi(sum[1]));
   }
 
-  static BSG_DEV bool segment(const Ctx& c, const Seg& g, int stream, int tid, bool both,
-                              int job, uint32_t ring0) {
+  static BSG_DEV bool segment(const Ctx& c, const Seg& g, int stream, int tid, uint32_t job,
+                              uint32_t ring0) {
     const AttnPreParams& p = c.p;
     const uint32_t lanes = static_cast<uint32_t>((tid >> 5) * 32) << 16;
     const uint32_t to = c.tmem + T::kColO + stream * D + lanes;
-    if (both || T::kStreams == 1) load_q(c, g, stream, tid, 128);
-    else load_q(c, g, 0, stream * 128 + tid, 256);
+    if (c.s.pair) load_q(c, g, 0, stream * 128 + tid, 256);
+    else load_q(c, g, stream, tid, 128);
     mbar_arrive(c.query());
-    const int jobs = g.n * (both ? 2 : 1);
+    const uint32_t jobs = jobs_of(c, stream, g.n);
     const float scale = fabsf(p.a.scale_log2);  // (a negative scale's sign went into Q)
     float m = -INFINITY, l = 0.f;  // m: the maximum that O and l are scaled to
-    int last = -1;
-    for (int j = stream; j < jobs; j += T::kStreams) {  // this stream's jobs
-      const int J = job + j, tile = both ? j >> 1 : j;
-      if (!wait_warp(c, c.scores(J), Ctx::phase(J))) return false;
+    for (uint32_t j = 0; j < jobs; ++j) {
+      const uint32_t b = Ctx::buf(stream, job + j), tile = tile_of(c, stream, j);
+      const uint32_t before = job + j - 1;  // the job before, where there is one in the segment
+      if (!wait_warp(c, c.scores(b), Ctx::phase(job + j))) return false;
       tc_after();
-      const uint32_t ts = c.tmem + Ctx::buf(J) * K + lanes;
+      const uint32_t ts = c.tmem + b * K + lanes;
       uint32_t raw[K];
 #pragma unroll
       for (int i = 0; i < K; i += 32) tc_ld32(ts + i, raw + i);
       tc_wait_ld();
       // positions of this tile, if below K: the others' scores do not count
-      const int valid = p.a.prefix_len - (g.t0 + tile) * K;
+      const int valid = p.a.prefix_len - (g.t0 + static_cast<int>(tile)) * K;
       const float top = valid < K ? row_max<true>(raw, valid) * scale : row_max<false>(raw, K) * scale;
       // O and l move to a new maximum when it is more than 8 above theirs (or the first)
       const bool grow = top > m + 8.f;
@@ -514,9 +501,9 @@ struct AttnPrefix {
         const float keep = grow ? ex2(m - next) : 1.f;
         l *= keep;
         m = next;
-        if (last >= 0) {
+        if (j > 0) {
           // the accumulator's last product is done
-          if (!wait_warp(c, c.out(last), Ctx::phase(last))) return false;
+          if (!wait_warp(c, c.out(Ctx::buf(stream, before)), Ctx::phase(before))) return false;
           tc_after();
 #pragma unroll 1
           for (int i = 0; i < D; i += 32) {
@@ -549,16 +536,16 @@ struct AttnPrefix {
         fence_async_shared();
       }
       tc_before();
-      mbar_arrive(c.probs(J));
-      last = J;
+      mbar_arrive(c.probs(b));
     }
     // the part: O, m and l
     float* part = p.parts + (static_cast<int64_t>(blockIdx.x) + g.unit) * attn_pre_slot_floats(D);
     const int row = stream * 128 + tid;
     __stcg(part + T::kSlotRows * D + row, m);
     __stcg(part + T::kSlotRows * (D + 1) + row, l);
-    if (last < 0) return true;  // (m = -inf: the merge leaves this part out)
-    if (!wait_warp(c, c.out(last), Ctx::phase(last))) return false;
+    if (jobs == 0) return true;  // (m = -inf: the merge leaves this part out)
+    const uint32_t last = job + jobs - 1;
+    if (!wait_warp(c, c.out(Ctx::buf(stream, last)), Ctx::phase(last))) return false;
     tc_after();
 #pragma unroll 1
     for (int i = 0; i < D; i += 32) {
@@ -585,7 +572,7 @@ struct AttnPrefix {
     if (threadIdx.x == 0) {
       for (int i = 0; i < T::kRing; ++i) {
         mbar_init(c.full(i), 1);
-        mbar_init(c.empty(i), 1);
+        mbar_init(c.empty(i), c.s.pair ? 1 : T::kStreams);  // streams that read a tile
       }
       for (int b = 0; b < T::kBufs; ++b) {
         mbar_init(c.scores(b), 1);
@@ -609,8 +596,8 @@ struct AttnPrefix {
     bool ok = true;
     if (warp == kCopyWarp) {
       ok = copy(c, threadIdx.x & 31);
-    } else if (warp == kMmaWarp) {
-      ok = issue(c);
+    } else if (warp >= kMmaWarp) {
+      ok = issue(c, warp - kMmaWarp);
     } else {
       ok = softmax(c, warp / 4, threadIdx.x & 127);
     }
