@@ -14,7 +14,7 @@ struct bsgemv_attn_plan_s {
   bsg::AttnLayout at = {};
   // tensor maps of the last few caches seen (a layer each)
   struct MapEntry {
-    bool valid = false, usable = false;
+    bool valid = false;
     const void *k = nullptr, *v = nullptr;
     int64_t page_stride = 0, head_stride = 0, row_stride = 0;
     int num_pages = 0;
@@ -33,18 +33,19 @@ const bsg::AttnMaps* maps_of(bsgemv_attn_plan_s* plan, const bsg::AttnParams& p)
     if (m.valid && m.k == p.k && m.v == p.v && m.page_stride == p.page_stride &&
         m.head_stride == p.head_stride && m.row_stride == p.row_stride &&
         m.num_pages == p.num_pages)
-      return m.usable ? &m.maps : nullptr;
+      return &m.maps;
   auto& m = plan->maps[plan->next_map];
+  m.valid = false;
+  if (!bsg::attn_encode(p, &m.maps)) return nullptr;
   plan->next_map = (plan->next_map + 1) % bsgemv_attn_plan_s::kMaps;
   m.valid = true;
-  m.usable = bsg::attn_encode(p, &m.maps);
   m.k = p.k;
   m.v = p.v;
   m.page_stride = p.page_stride;
   m.head_stride = p.head_stride;
   m.row_stride = p.row_stride;
   m.num_pages = p.num_pages;
-  return m.usable ? &m.maps : nullptr;
+  return &m.maps;
 }
 
 }  // namespace
@@ -134,11 +135,12 @@ int bsgemv_attn_run(bsgemv_attn_plan_t plan, const void* q, int64_t q_stride, co
   p.err = static_cast<unsigned*>(plan->ws);
   p.parts = reinterpret_cast<float*>(static_cast<char*>(plan->ws) + plan->at.parts);
   p.pre_parts = reinterpret_cast<float*>(static_cast<char*>(plan->ws) + plan->at.pre_parts);
+  p.cum = reinterpret_cast<int*>(static_cast<char*>(plan->ws) + plan->at.cum);
+  const AttnMaps* maps = maps_of(plan, p);
+  if (maps == nullptr) return BSGEMV_ERR_UNSUPPORTED;
   int mode = prefix_len > 0 ? kAttnPrefixStream : kAttnNoPrefix;
-  const AttnMaps* maps = nullptr;
-  if (mode && B * (plan->Hq / plan->Hkv) >= kAttnTensorRows && (maps = maps_of(plan, p)) != nullptr)
-    mode = kAttnPrefixTensor;
-  return launch_attn(p, mode, maps, plan->sms, static_cast<cudaStream_t>(stream));
+  if (mode && B * (plan->Hq / plan->Hkv) >= kAttnTensorRows) mode = kAttnPrefixTensor;
+  return launch_attn(p, mode, *maps, plan->sms, static_cast<cudaStream_t>(stream));
 }
 
 int bsgemv_attn_device_status(bsgemv_attn_plan_t plan, void* stream) {

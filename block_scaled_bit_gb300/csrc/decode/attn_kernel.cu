@@ -5,30 +5,31 @@
 namespace bsg {
 namespace {
 
-// One warp per (sequence, query head), D / 32 elements a lane.  A row has tens of parts, so nothing
-// is read one after the other: each lane fetches one part's m and l, the warp agrees on the
-// weights, then the rows are fetched four at a time.
+// One block per (sequence, query head), D / 32 elements a lane.  A row has tens of parts, so
+// nothing is read one after the other: every warp takes a quarter of the parts, each of its lanes
+// fetches one part's m and l, the warp agrees on the weights, then the rows are fetched eight at a
+// time; the warps' sums are put together in shared memory.
 template <bool BF16, int D>
 __global__ void __launch_bounds__(128)
     attn_merge(const __grid_constant__ AttnParams p, int mode, int sms) {
-  extern __shared__ int cum[];
-  const int lane = threadIdx.x & 31;
-  pdl_launch_dependents();
-  attn_prefix_sums<D>(p, cum, cum + p.B + 1);
-  const AttnSplit s = attn_split<D>(p, cum, mode == kAttnPrefixStream, sms * kAttnWarps);
-  pdl_wait();
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= p.B * p.Hq) return;
-  const int b = row / p.Hq, hq = row - b * p.Hq, G = p.Hq / p.Hkv, h = hq / G, g = hq - h * G;
   constexpr int kPer = D / 32;
-  const bool here = p.lens[b] >= max(p.prefix_len, 1);
+  __shared__ float sums[4][D], tops[4], totals[4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x, b = row / p.Hq, hq = row - b * p.Hq;
+  const int G = p.Hq / p.Hkv, h = hq / G, g = hq - h * G;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int len = p.lens[b], c0 = __ldcg(p.cum + b), c1 = __ldcg(p.cum + b + 1);
+  const AttnSplit s =
+      attn_split<D>(p, __ldcg(p.cum + p.B), mode == kAttnPrefixStream, sms * kAttnWarps);
+  const bool here = len >= max(p.prefix_len, 1);
 
-  // The row's parts: the prefix's, then its own; a part is [rows][D] sums, [rows] m, [rows] l.
+  // The row's parts: the prefix's, then its own; a part is sums, [rows] m, [rows] l.
   struct List {
     const float* first;     // part 0
     int64_t next;           // floats to the following part
     int count, rows, r;     // r: the row in a part
-    bool grouped;           // columns in groups of four (the prefix kernel), else whole rows
+    bool grouped;           // sums as [D / 4][rows][4] (the prefix kernel), else [rows][D]
   } pre = {nullptr, 0, 0, 1, 0, false}, own = pre;
   int twice = 1;            // two streams' rows in each part of the prefix
   if (here) {
@@ -56,16 +57,17 @@ __global__ void __launch_bounds__(128)
       const int r = b * G + g, u = h * (s.pre_units / p.Hkv) + r / kAttnRows;
       pre = stream_list(s.own_units + u, s.pre_start + u * s.pre_tiles, s.pre_tiles, r % kAttnRows);
     }
-    const int tiles = cum[b + 1] - cum[b], i = h * s.row_tiles + g / kAttnRows;
+    const int tiles = c1 - c0, i = h * s.row_tiles + g / kAttnRows;
     if (tiles)
-      own = stream_list(b * p.Hkv * s.row_tiles + i, cum[b] * p.Hkv * s.row_tiles + i * tiles,
-                        tiles, g % kAttnRows);
+      own = stream_list(b * p.Hkv * s.row_tiles + i, c0 * p.Hkv * s.row_tiles + i * tiles, tiles,
+                        g % kAttnRows);
   }
-  const int n = pre.count + own.count;
+  const int all = pre.count + own.count;
+  const int n0 = all * warp / 4, n = all * (warp + 1) / 4;  // this warp's
   float o[kPer], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) o[i] = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
+  for (int i0 = n0; i0 < n; i0 += 32) {
     const int i = i0 + lane, many = min(32, n - i0);
     const float* src = nullptr;
     float mi = -INFINITY, li = 0.f;
@@ -93,56 +95,76 @@ __global__ void __launch_bounds__(128)
     l = l * keep + sum;
 #pragma unroll
     for (int x = 0; x < kPer; ++x) o[x] *= keep;
-    for (int j0 = 0; j0 < many; j0 += 4) {
-      float v[4][kPer], t[4];
+    constexpr int kAhead = D == 256 ? 4 : 8;
+    for (int j0 = 0; j0 < many; j0 += kAhead) {
+      float v[kAhead][kPer], t[kAhead];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kAhead; ++j) {
         const int from = min(j0 + j, many - 1);
         const float* row_j = reinterpret_cast<const float*>(
             __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(src), from));
         const float mj = __shfl_sync(0xFFFFFFFFu, mi, from);
-        t[j] = j0 + j < many ? __shfl_sync(0xFFFFFFFFu, take, from) : 0.f;
+        t[j] = __shfl_sync(0xFFFFFFFFu, take, from);
+        const bool none = mj == -INFINITY || j0 + j >= many;
         const int rows = i0 + from < pre.count && pre.grouped ? pre.rows : 0;
 #pragma unroll
         for (int x = 0; x < kPer / 2; ++x) {
-          const float2 f = mj == -INFINITY || j0 + j >= many
-                               ? make_float2(0.f, 0.f)
-                               : __ldcg(reinterpret_cast<const float2*>(
-                                     row_j + (rows ? (lane * kPer + 2 * x) / 4 * (4 * rows) +
-                                                         (lane * kPer + 2 * x) % 4
-                                                   : lane * kPer + 2 * x)));
+          const int col = lane * kPer + 2 * x;
+          const float2 f = none ? make_float2(0.f, 0.f)
+                                : __ldcg(reinterpret_cast<const float2*>(
+                                      row_j + (rows ? col / 4 * (4 * rows) + col % 4 : col)));
           v[j][2 * x] = f.x;
           v[j][2 * x + 1] = f.y;
         }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < kAhead; ++j)
 #pragma unroll
         for (int x = 0; x < kPer; ++x) o[x] = fmaf(v[j][x], t[j], o[x]);
     }
   }
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(row) * D + lane * kPer);
 #pragma unroll
-  for (int i = 0; i < kPer / 2; ++i)
-    out[i] = here ? AttnStream<BF16, D>::pack(o[2 * i] / l, o[2 * i + 1] / l) : 0u;
-  if (lane == 0 && p.lse) p.lse[row] = here ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  for (int x = 0; x < kPer; ++x) sums[warp][lane * kPer + x] = o[x];
+  if (lane == 0) {
+    tops[warp] = m;
+    totals[warp] = l;
+  }
+  __syncthreads();
+  const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+  const float base = top == -INFINITY ? 0.f : top;
+  float total = 0.f, w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = ex2(tops[i] - base);
+    total += w[i] * totals[i];
+  }
+  for (int d = 2 * threadIdx.x; d < D; d += 256) {
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x += w[i] * sums[i][d];
+      y += w[i] * sums[i][d + 1];
+    }
+    *reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(row) * D + d) =
+        here ? AttnStream<BF16, D>::pack(x / total, y / total) : 0u;
+  }
+  if (threadIdx.x == 0 && p.lse)
+    p.lse[row] = here ? (top + log2f(total)) * 0.6931471805599453f : -INFINITY;
 }
 
 template <bool BF16, int D>
-int launch(const AttnParams& p, int mode, const AttnMaps* maps, int sms, cudaStream_t s) {
+int launch(const AttnParams& p, int mode, const AttnMaps& maps, int sms, cudaStream_t s) {
   static AttrRecord rec, pre_rec;
   using T = AttnTile<D>;
-  const int sums = (p.B + 1 + 33) * 4;
-  const int smem = kAttnWarps * T::kWarpB + sums;
-  int rc = decode_smem(attn_stream_kernel<BF16, D>, rec, smem);
-  if (rc != BSGEMV_OK) return rc;
+  const int ps = 1 << p.page_log2;
+  int rc;
   if (mode == kAttnPrefixTensor) {
     using P = AttnPre<D>;
     AttnPreParams q;
-    q.tm_k = maps->k;
-    q.tm_v = maps->v;
+    q.tm_k = maps.pre_k;
+    q.tm_v = maps.pre_v;
     q.a = p;
-    q.box_rows = (1 << p.page_log2) < P::kKeys ? 1 << p.page_log2 : P::kKeys;
+    q.box_rows = ps < P::kKeys ? ps : P::kKeys;
     q.parts = p.pre_parts;
     q.wait_ns = kDefaultWaitNs;
     rc = decode_smem(attn_prefix_kernel<BF16, D>, pre_rec, P::kSmem);
@@ -152,11 +174,18 @@ int launch(const AttnParams& p, int mode, const AttnMaps* maps, int sms, cudaStr
                        P::kSmem, s, q);
     if (rc != BSGEMV_OK) return rc;
   }
-  rc = decode_launch(attn_stream_kernel<BF16, D>, dim3(sms), dim3(32 * kAttnWarps), smem, s, p,
+  AttnStreamParams q;
+  q.tm_k = maps.k;
+  q.tm_v = maps.v;
+  q.a = p;
+  q.box_rows = ps < T::kKeys ? ps : T::kKeys;
+  const int smem = 1024 + kAttnWarps * (T::kWarpB + 32) + (p.B + 1 + 33) * 4;
+  rc = decode_smem(attn_stream_kernel<BF16, D>, rec, smem);
+  if (rc != BSGEMV_OK) return rc;
+  rc = decode_launch(attn_stream_kernel<BF16, D>, dim3(sms), dim3(32 * kAttnWarps), smem, s, q,
                      mode);
   if (rc != BSGEMV_OK) return rc;
-  return decode_launch(attn_merge<BF16, D>, dim3((p.B * p.Hq + 3) / 4), dim3(128), sums, s, p,
-                       mode, sms);
+  return decode_launch(attn_merge<BF16, D>, dim3(p.B * p.Hq), dim3(128), 0, s, p, mode, sms);
 }
 
 }  // namespace
@@ -168,31 +197,35 @@ AttnLayout attn_layout(int Hq, int Hkv, int D, int max_B, int sms) {
                        Hkv * ((max_B * G + kAttnRows - 1) / kAttnRows);
   const size_t slots = units + static_cast<size_t>(sms) * kAttnWarps;
   const size_t pre = Hkv * ((max_B * G + 127) / 128) + sms;
-  l.parts = 256;
+  l.cum = 256;
+  l.parts = l.cum + (static_cast<size_t>(max_B + 1) * 4 + 255) / 256 * 256;
   l.pre_parts = l.parts + (slots * attn_slot_floats(D) * 4 + 255) / 256 * 256;
   l.total = l.pre_parts + pre * attn_pre_slot_floats(D) * 4;
   return l;
 }
 
 bool attn_encode(const AttnParams& p, AttnMaps* m) {
-  const int ps = 1 << p.page_log2, keys = 64;
+  const int ps = 1 << p.page_log2;
   const uint64_t dims[4] = {static_cast<uint64_t>(p.D), static_cast<uint64_t>(ps),
                             static_cast<uint64_t>(p.Hkv), static_cast<uint64_t>(p.num_pages)};
   // (the stride of a dimension of one is of no account)
   const uint64_t row = p.row_stride * 2;
   const uint64_t strides[3] = {row, p.Hkv > 1 ? p.head_stride * 2 : row * ps,
                                p.num_pages > 1 ? p.page_stride * 2 : row * ps * p.Hkv};
-  const uint32_t box[4] = {64, static_cast<uint32_t>(ps < keys ? ps : keys), 1, 1};
   const CUtensorMapDataType type =
       p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  for (int i = 0; i < 2; ++i)
-    if (decode_encode(i ? &m->v : &m->k, type, 4, i ? p.v : p.k, dims, strides, box,
+  CUtensorMap* const maps[4] = {&m->k, &m->v, &m->pre_k, &m->pre_v};
+  for (int i = 0; i < 4; ++i) {
+    const int keys = i < 2 ? 4096 / p.D : 64;  // positions of a tile
+    const uint32_t box[4] = {64, static_cast<uint32_t>(ps < keys ? ps : keys), 1, 1};
+    if (decode_encode(maps[i], type, 4, i & 1 ? p.v : p.k, dims, strides, box,
                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) != BSGEMV_OK)
       return false;
+  }
   return true;
 }
 
-int launch_attn(const AttnParams& p, int mode, const AttnMaps* maps, int sms, cudaStream_t s) {
+int launch_attn(const AttnParams& p, int mode, const AttnMaps& maps, int sms, cudaStream_t s) {
   switch (p.D) {
     case 64:
       return p.bf16 ? launch<true, 64>(p, mode, maps, sms, s) : launch<false, 64>(p, mode, maps, sms, s);

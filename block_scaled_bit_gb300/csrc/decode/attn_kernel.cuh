@@ -34,13 +34,14 @@ struct AttnParams {
   unsigned* err;
   float* parts;       // streaming parts: slots of [16][D] sums, then [16] m, [16] l
   float* pre_parts;   // the prefix kernel's parts
+  int* cum;           // [B + 1] the sequences' stretches of the line, from the streaming kernel
 };
 
 // What a call does with the prefix.
 enum AttnPrefixMode { kAttnNoPrefix = 0, kAttnPrefixStream = 1, kAttnPrefixTensor = 2 };
 
 struct AttnLayout {
-  size_t parts, pre_parts, total;
+  size_t cum, parts, pre_parts, total;
 };
 AttnLayout attn_layout(int Hq, int Hkv, int D, int max_B, int sms);
 
@@ -48,13 +49,14 @@ AttnLayout attn_layout(int Hq, int Hkv, int D, int max_B, int sms);
 // the streaming kernel reads the prefix once as well, and starts faster.
 constexpr int kAttnTensorRows = 17;
 
-// Tensor maps of the cache for the prefix kernel (false: the strides cannot be described).
+// Tensor maps of the cache: [page][head][row][D], boxes of 64 d and as many rows as a page and a
+// tile of the kernel have (false: the strides cannot be described).
 struct AttnMaps {
-  CUtensorMap k, v;
+  CUtensorMap k, v;          // the streaming kernel's
+  CUtensorMap pre_k, pre_v;  // the prefix kernel's
 };
 bool attn_encode(const AttnParams& p, AttnMaps* m);
 
-// maps: for kAttnPrefixTensor, else unused.
-int launch_attn(const AttnParams& p, int mode, const AttnMaps* maps, int sms, cudaStream_t s);
+int launch_attn(const AttnParams& p, int mode, const AttnMaps& maps, int sms, cudaStream_t s);
 
 }  // namespace bsg

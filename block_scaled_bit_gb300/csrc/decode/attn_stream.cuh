@@ -3,9 +3,11 @@
 // Sixteen query rows of one kv head (the heads that share it, of one sequence) against the
 // sequence's own positions.  Bound: K and V are read once from HBM; 16 rows give 16 flops a byte,
 // far below the tensor cores' ridge.  So every warp is a worker with a stream of its own: tiles of
-// 16 KB (4096 / D positions of K and V) through a ring in shared memory by cp.async, two tiles in
-// flight, no synchronisation but the warp's own; scores and P V on mma.sync m16n8k16, softmax in
-// registers with the running maximum in base 2.
+// 16 KB (4096 / D positions of K and V) through a ring in shared memory by TMA (a box per page or
+// tile and 64 d, 128-byte swizzle), two tiles in flight, no synchronisation but the warp's own;
+// scores and P V on mma.sync m16n8k16, softmax in registers with the running maximum in base 2.
+// (Loaded by cp.async, 32 of them a lane and tile with two shuffles each for the rows' places, the
+// loads took as many instructions as the products.)
 //
 // All tiles of all (sequence, kv head, row tile) are laid in a line and cut into equal ranges, one
 // per warp, so that the lengths' spread does not matter; a unit counts kAttnCost tiles more than
@@ -84,12 +86,12 @@ BSG_DEV void attn_prefix_sums(const AttnParams& p, int* cum, int* tmp) {
 }
 
 template <int D>
-BSG_DEV AttnSplit attn_split(const AttnParams& p, const int* cum, bool with_prefix, int workers) {
+BSG_DEV AttnSplit attn_split(const AttnParams& p, int own, bool with_prefix, int workers) {
   AttnSplit s;
   const int G = p.Hq / p.Hkv;
   s.row_tiles = (G + kAttnRows - 1) / kAttnRows;
   s.own_units = p.B * p.Hkv * s.row_tiles;
-  s.pre_start = cum[p.B] * p.Hkv * s.row_tiles;
+  s.pre_start = own * p.Hkv * s.row_tiles;  // (own: cum[B])
   s.pre_tiles = with_prefix ? (p.prefix_len + AttnTile<D>::kKeys - 1) / AttnTile<D>::kKeys + kAttnCost : 0;
   s.pre_units = s.pre_tiles ? p.Hkv * ((p.B * G + kAttnRows - 1) / kAttnRows) : 0;
   s.total = s.pre_start + s.pre_units * s.pre_tiles;
@@ -152,6 +154,26 @@ BSG_DEV AttnUnit attn_unit_at(const AttnParams& p, const AttnSplit& s, const int
   return u;
 }
 
+struct AttnStreamParams {
+  CUtensorMap tm_k, tm_v;   // [page][head][row][D], boxes of [box_rows][64 d]
+  AttnParams a;
+  int box_rows;
+};
+
+BSG_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, int w,
+                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+BSG_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 template <bool BF16, int D>
 struct AttnStream {
   using T = AttnTile<D>;
@@ -159,54 +181,53 @@ struct AttnStream {
   static constexpr int kSteps = D / 16;   // mma k-steps of the scores
   static constexpr int kCpr = D / 8;      // 16-byte chunks of a row
 
-  // Byte offset of chunk c of row r in a half tile: chunks swizzled by the row.
-  static BSG_DEV uint32_t at(int r, int c) { return r * (D * 2) + ((c ^ (r & 7)) << 4); }
+  // Byte offset of 16-byte chunk c of row r in a half tile: blocks of 64 d, rows of 128 bytes,
+  // chunks swizzled by the row.
+  static BSG_DEV uint32_t at(int r, int c) {
+    return (c >> 3) * (K * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  }
 
-  // A tile's rows into a ring stage (rows outside the unit: zeros).  Lane j knows where rows j
-  // (and j + 32) are; each step moves 32 chunks.  Page ids are fetched a tile ahead and used only
-  // when the tile is issued, so that their latency passes under the products.
-  static constexpr int kOff = K > 32 ? 2 : 1;
-  static BSG_DEV void fetch(const AttnParams& p, const AttnUnit& u, int tile, int lane,
-                            int (&page)[kOff]) {
-#pragma unroll
-    for (int i = 0; i < kOff; ++i) {
-      const int pos = (u.lo / K + tile) * K + lane + 32 * i;
-      page[i] = -1;
-      if (lane + 32 * i < K && pos >= u.lo && pos < u.hi) {
-        const int at = pos >> p.page_log2;
-        page[i] = u.b < 0 ? __ldg(p.prefix_table + at) : __ldg(p.tables + u.b * p.table_stride + at);
-      }
-    }
+  // A tile's boxes: lane i of kBoxes brings K (i even) or V rows of one page, 64 d of them.  The
+  // page id is fetched a tile ahead, so that its latency passes under the products.
+  struct Box {
+    int rows, count, r, d, kv;  // rows of a box, boxes of a tile, this lane's row, d block, K or V
+  };
+  static BSG_DEV Box box_of(const AttnStreamParams& p, int lane) {
+    Box b;
+    b.rows = p.box_rows;
+    b.count = K / p.box_rows * (D / 64) * 2;
+    b.kv = lane & 1;
+    b.d = (lane >> 1) % (D / 64);
+    b.r = (lane >> 1) / (D / 64) * p.box_rows;
+    return b;
   }
-  // Element offsets of the rows in the cache, -1 outside the unit or the pages.
-  static BSG_DEV void offsets(const AttnParams& p, const AttnUnit& u, int tile, int lane,
-                              const int (&page)[kOff], int64_t (&off)[kOff]) {
-#pragma unroll
-    for (int i = 0; i < kOff; ++i) {
-      const int pos = (u.lo / K + tile) * K + lane + 32 * i;
-      off[i] = page[i] < 0 || page[i] >= p.num_pages
-                   ? -1
-                   : page[i] * p.page_stride + u.h * p.head_stride +
-                         (pos & ((1 << p.page_log2) - 1)) * p.row_stride;
-    }
+  static BSG_DEV int fetch(const AttnParams& p, const AttnUnit& u, int tile, const Box& x) {
+    const int pos = (u.lo / K + tile) * K + x.r;
+    // a page of the table covers the box if any of the unit's positions is in it; past the cache
+    // (reads as zeros) otherwise
+    if (pos >= u.hi || pos + x.rows <= u.lo) return p.num_pages;
+    const int i = pos >> p.page_log2;
+    return u.b < 0 ? __ldg(p.prefix_table + i) : __ldg(p.tables + u.b * p.table_stride + i);
   }
-  static BSG_DEV void issue(const AttnParams& p, uint32_t stage, const int64_t (&off)[kOff],
-                            int lane) {
-    constexpr int kIter = K * kCpr / 32;
+  static BSG_DEV void issue(const AttnStreamParams& p, const AttnUnit& u, int tile, uint32_t stage,
+                            uint32_t bar, const Box& x, int page, int lane) {
+    const int pos = (u.lo / K + tile) * K + x.r;
+    if (lane == 0) mbar_arrive_expect_tx(bar, 2 * T::kHalf);
+    __syncwarp();
+    if (lane < x.count)
+      tma_load_4d(stage + x.kv * T::kHalf + x.d * (K * 128) + x.r * 128, x.kv ? &p.tm_v : &p.tm_k,
+                  x.d * 64, pos & ((1 << p.a.page_log2) - 1), u.h, page, bar);
+  }
+  // V rows of a landed tile that the unit does not attend to: zeros (their numerators are, but
+  // what the page holds there need not be finite).
+  static BSG_DEV void clear(uint8_t* stage, const AttnUnit& u, int pos0, int lane) {
+    for (int r = lane; r < K; r += 32)
+      if (pos0 + r < u.lo || pos0 + r >= u.hi)
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) {
-      const int x = i * 32 + lane, r = x / kCpr, c = x % kCpr;
-      int64_t o = __shfl_sync(0xFFFFFFFFu, off[0], r & 31);
-      if constexpr (kOff == 2) {
-        const int64_t o1 = __shfl_sync(0xFFFFFFFFu, off[1], r & 31);
-        if (r >= 32) o = o1;
-      }
-      const uint32_t n = o >= 0 ? 16u : 0u;
-      const int64_t e = (o >= 0 ? o : 0) + c * 8;
-      const uint32_t dst = stage + at(r, c);
-      cp_async16(dst, p.k + (o >= 0 ? e : 0), n);
-      cp_async16(dst + T::kHalf, p.v + (o >= 0 ? e : 0), n);
-    }
+        for (int c = 0; c < kCpr; ++c)
+          *reinterpret_cast<uint4*>(stage + T::kHalf + at(r, c)) = make_uint4(0u, 0u, 0u, 0u);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before TMA writes here again
+    __syncwarp();
   }
 
   static BSG_DEV void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -297,7 +318,7 @@ struct AttnStream {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float next = fmaxf(a.m[i], top[i]);
-        const float keep = a.m[i] == -INFINITY ? 0.f : exp2f(a.m[i] - next);
+        const float keep = a.m[i] == -INFINITY ? 0.f : ex2(a.m[i] - next);
         a.m[i] = next;
         a.l[i] *= keep;
 #pragma unroll
@@ -315,7 +336,7 @@ struct AttnStream {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int n = 2 * k + (x >> 1), i = x & 1;
-        f[x] = pack(exp2f(s[n][2 * i] - base[i]), exp2f(s[n][2 * i + 1] - base[i]));
+        f[x] = pack(ex2(s[n][2 * i] - base[i]), ex2(s[n][2 * i + 1] - base[i]));
         a.l[i] += half_to_f32<BF16>(f[x], 0) + half_to_f32<BF16>(f[x], 1);
       }
 #pragma unroll
@@ -346,9 +367,12 @@ struct AttnStream {
     }
   }
 
-  static BSG_DEV void worker(const AttnParams& p, const AttnSplit& s, const int* cum, uint32_t ring,
-                             uint8_t* ring_p, int w, int lane) {
+  static BSG_DEV void worker(const AttnStreamParams& sp, const AttnSplit& s, const int* cum,
+                             uint8_t* ring_p, uint32_t bars, int w, int lane) {
     if (w >= s.workers) return;
+    const AttnParams& p = sp.a;
+    const uint32_t ring = smem_u32(ring_p);
+    const Box box = box_of(sp, lane);
     const int x0 = attn_start(s, w), x1 = attn_start(s, w + 1);
     // the loads run ahead of the products, over units' ends: each has its own place in the line
     struct Place {
@@ -365,18 +389,14 @@ struct AttnStream {
     Place in = {attn_unit_at<D>(p, s, cum, x0), x0};
     settle(in);
     Place out = in;
-    int page[kOff];
-    if (in.x < x1) fetch(p, in.u, in.x - in.u.first, lane, page);
+    int page = in.x < x1 ? fetch(p, in.u, in.x - in.u.first, box) : 0;
     const auto load = [&](int stage) {
-      if (in.x < x1) {
-        int64_t off[kOff];
-        offsets(p, in.u, in.x - in.u.first, lane, page, off);
-        issue(p, ring + stage * 2 * T::kHalf, off, lane);
-        ++in.x;
-        settle(in);
-        if (in.x < x1) fetch(p, in.u, in.x - in.u.first, lane, page);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (in.x >= x1) return;
+      issue(sp, in.u, in.x - in.u.first, ring + stage * 2 * T::kHalf, bars + 8 * stage, box, page,
+            lane);
+      ++in.x;
+      settle(in);
+      if (in.x < x1) page = fetch(p, in.u, in.x - in.u.first, box);
     };
 #pragma unroll
     for (int i = 0; i < T::kStages - 1; ++i) load(i);
@@ -384,6 +404,7 @@ struct AttnStream {
     const uint32_t qs = ring + T::kStages * 2 * T::kHalf;
     Acc a;
     int stage = 0;
+    uint32_t phase = 0;
     bool fresh = true;
     while (out.x < x1) {
       const AttnUnit& u = out.u;
@@ -421,12 +442,20 @@ struct AttnStream {
           a.l[i] = 0.f;
         }
       }
-      asm volatile("cp.async.wait_group %0;" ::"n"(T::kStages - 2) : "memory");
-      __syncwarp();
-      tile(p, u, (u.lo / K + out.x - u.first) * K, ring + stage * 2 * T::kHalf, q, qs, lane, a);
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars + 8 * stage, phase, p.err, kErrTimeoutFull))) {
+        // the warp's work ends here, once its other tiles in flight have landed (bounded again)
+        for (int i = 1; i < T::kStages; ++i) {
+          if (++stage == T::kStages) { stage = 0; phase ^= 1u; }
+          mbar_wait(bars + 8 * stage, phase, p.err, kErrTimeoutFull);
+        }
+        return;
+      }
+      const int pos0 = (u.lo / K + out.x - u.first) * K;
+      if (pos0 < u.lo || pos0 + K > u.hi) clear(ring_p + stage * 2 * T::kHalf, u, pos0, lane);
+      tile(p, u, pos0, ring + stage * 2 * T::kHalf, q, qs, lane, a);
       __syncwarp();  // every lane is done with the stage that the next load fills
       load(stage == 0 ? T::kStages - 1 : stage - 1);
-      if (++stage == T::kStages) stage = 0;
+      if (++stage == T::kStages) { stage = 0; phase ^= 1u; }
       ++out.x;
       if (out.x == x1 || out.x == u.first + u.tiles) {
         store_part(p, w + u.unit, lane, a);
@@ -434,27 +463,37 @@ struct AttnStream {
         settle(out);
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   }
 };
 
 template <bool BF16, int D>
 __global__ void __launch_bounds__(32 * kAttnWarps, 1)
-    attn_stream_kernel(const __grid_constant__ AttnParams p, int mode) {
-  extern __shared__ __align__(128) uint8_t smem[];
+    attn_stream_kernel(const __grid_constant__ AttnStreamParams sp, int mode) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   using T = AttnTile<D>;
+  const AttnParams& p = sp.a;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int* cum = reinterpret_cast<int*>(smem + kAttnWarps * T::kWarpB);
+  uint8_t* bars = smem + kAttnWarps * T::kWarpB;
+  int* cum = reinterpret_cast<int*>(bars + kAttnWarps * 32);
+  if (lane == 0) {
+    for (int i = 0; i < T::kStages; ++i) mbar_init(smem_u32(bars) + warp * 32 + 8 * i, 1);
+    fence_mbar_init();
+    prefetch_tmap(&sp.tm_k);
+    prefetch_tmap(&sp.tm_v);
+  }
   // After the prefix kernel (which has waited for everything before it) nothing here depends on
   // the kernel before; the wait at the end keeps the order for the merge.
   if (mode != kAttnPrefixTensor) pdl_wait();
-  pdl_launch_dependents();  // (after the wait: the merge reads the lengths before its own)
+  pdl_launch_dependents();
   attn_prefix_sums<D>(p, cum, cum + p.B + 1);
+  if (blockIdx.x == 0)  // for the merge
+    for (int i = threadIdx.x; i <= p.B; i += blockDim.x) p.cum[i] = cum[i];
   const AttnSplit s =
-      attn_split<D>(p, cum, mode == kAttnPrefixStream, gridDim.x * kAttnWarps);
+      attn_split<D>(p, cum[p.B], mode == kAttnPrefixStream, gridDim.x * kAttnWarps);
   // neighbouring ranges on different SMs: warp-major over the blocks
-  AttnStream<BF16, D>::worker(p, s, cum, smem_u32(smem) + warp * T::kWarpB,
-                              smem + warp * T::kWarpB, warp * gridDim.x + blockIdx.x, lane);
+  AttnStream<BF16, D>::worker(sp, s, cum, smem + warp * T::kWarpB, smem_u32(bars) + warp * 32,
+                              warp * gridDim.x + blockIdx.x, lane);
   if (mode == kAttnPrefixTensor) pdl_wait();
 }
 

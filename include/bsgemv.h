@@ -423,7 +423,8 @@ int bsgemv_attn_plan(bsgemv_attn_plan_t* out, int act_bf16, int Hq, int Hkv, int
 /* Enqueue the attention of B (1 .. max_B) slots.  q, k, v, out 16-byte aligned, all strides
  * multiples of 8 elements; prefix_table, tables, lens int32 device memory (prefix_table may be
  * NULL when prefix_len == 0).  prefix_len is a host value: 0 <= prefix_len < 2^30.  Page ids
- * outside 0 .. num_pages-1 are read as zeros.  Deterministic: repeated calls are bit-identical. */
+ * outside 0 .. num_pages-1 are read as zeros.  Strides that a TMA tensor map cannot describe (2^40
+ * bytes or more): BSGEMV_ERR_UNSUPPORTED.  Deterministic: repeated calls are bit-identical. */
 int bsgemv_attn_run(bsgemv_attn_plan_t plan, const void* q, int64_t q_stride, const void* k,
                     const void* v, int64_t page_stride, int64_t head_stride, int64_t row_stride,
                     int num_pages, const int32_t* prefix_table, int prefix_len,
