@@ -7,7 +7,7 @@ namespace {
 
 // One block per (sequence, query head), D / 32 elements a lane.  A row has tens of parts, so
 // nothing is read one after the other: every warp takes a quarter of the parts, each of its lanes
-// fetches one part's m and l, the warp agrees on the weights, then the rows are fetched eight at a
+// fetches one part's m and l, the warp agrees on the weights, then the rows are fetched four at a
 // time; the warps' sums are put together in shared memory.
 template <bool BF16, int D>
 __global__ void __launch_bounds__(128)
@@ -24,20 +24,19 @@ __global__ void __launch_bounds__(128)
       attn_split<D>(p, __ldcg(p.cum + p.B), mode == kAttnPrefixStream, sms * kAttnWarps);
   const bool here = len >= max(p.prefix_len, 1);
 
-  // The row's parts: the prefix's, then its own; a part is sums, [rows] m, [rows] l.
+  // The row's parts: the prefix's, then its own; a part is [rows][D] sums, [rows] m, [rows] l.
   struct List {
     const float* first;     // part 0
     int64_t next;           // floats to the following part
     int count, rows, r;     // r: the row in a part
-    bool grouped;           // sums as [D / 4][rows][4] (the prefix kernel), else [rows][D]
-  } pre = {nullptr, 0, 0, 1, 0, false}, own = pre;
+  } pre = {nullptr, 0, 0, 1, 0}, own = pre;
   int twice = 1;            // two streams' rows in each part of the prefix
   if (here) {
     // (x0, tiles: a unit's stretch of the line)
     const auto stream_list = [&](int unit, int x0, int tiles, int r) {
       const int w0 = attn_owner(s, x0 + kAttnCost), w1 = attn_owner(s, x0 + tiles - 1);
       return List{p.parts + static_cast<int64_t>(w0 + unit) * attn_slot_floats(D),
-                  attn_slot_floats(D), w1 - w0 + 1, kAttnRows, r, false};
+                  attn_slot_floats(D), w1 - w0 + 1, kAttnRows, r};
     };
     if (mode == kAttnPrefixTensor) {
       const AttnPreSplit t = attn_pre_split<D>(p.B, p.Hq, p.Hkv, p.prefix_len, sms);
@@ -52,7 +51,7 @@ __global__ void __launch_bounds__(128)
       const int w0 = owner(x0), w1 = owner(x0 + t.tiles - 1);
       twice = t.pair ? 2 : 1;
       pre = List{p.pre_parts + static_cast<int64_t>(w0 + unit) * attn_pre_slot_floats(D),
-                 attn_pre_slot_floats(D), (w1 - w0 + 1) * twice, kRows, r % per, true};
+                 attn_pre_slot_floats(D), (w1 - w0 + 1) * twice, kRows, r % per};
     } else if (s.pre_tiles) {
       const int r = b * G + g, u = h * (s.pre_units / p.Hkv) + r / kAttnRows;
       pre = stream_list(s.own_units + u, s.pre_start + u * s.pre_tiles, s.pre_tiles, r % kAttnRows);
@@ -77,7 +76,7 @@ __global__ void __launch_bounds__(128)
       const int at = first ? i / twice : i - pre.count;
       const int r = first && twice == 2 ? x.r + 128 * (i & 1) : x.r;
       const float* part = x.first + at * x.next;
-      src = x.grouped ? part + r * 4 : part + r * D;
+      src = part + r * D;
       mi = __ldcg(part + x.rows * D + r);
       li = __ldcg(part + x.rows * (D + 1) + r);
     }
@@ -95,36 +94,45 @@ __global__ void __launch_bounds__(128)
     l = l * keep + sum;
 #pragma unroll
     for (int x = 0; x < kPer; ++x) o[x] *= keep;
-    constexpr int kAhead = D == 256 ? 4 : 8;
-    for (int j0 = 0; j0 < many; j0 += kAhead) {
-      float v[kAhead][kPer], t[kAhead];
+    constexpr int kVec = kPer < 4 ? kPer : 4;  // floats of a load
+    for (int j0 = 0; j0 < many; j0 += 4) {
+      float v[4][kPer], t[4];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const int from = min(j0 + j, many - 1);
         const float* row_j = reinterpret_cast<const float*>(
             __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(src), from));
         const float mj = __shfl_sync(0xFFFFFFFFu, mi, from);
         t[j] = __shfl_sync(0xFFFFFFFFu, take, from);
-        const bool none = mj == -INFINITY || j0 + j >= many;
-        const int rows = i0 + from < pre.count && pre.grouped ? pre.rows : 0;
+        const bool some = mj != -INFINITY && j0 + j < many;
 #pragma unroll
-        for (int x = 0; x < kPer / 2; ++x) {
-          const int col = lane * kPer + 2 * x;
-          const float2 f = none ? make_float2(0.f, 0.f)
-                                : __ldcg(reinterpret_cast<const float2*>(
-                                      row_j + (rows ? col / 4 * (4 * rows) + col % 4 : col)));
-          v[j][2 * x] = f.x;
-          v[j][2 * x + 1] = f.y;
+        for (int x = 0; x < kPer; x += kVec) {
+          const float* at = row_j + x / kVec * (32 * kVec) + lane * kVec;
+          if constexpr (kVec == 4) {
+            const float4 f = some ? __ldcg(reinterpret_cast<const float4*>(at))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[j][x] = f.x;
+            v[j][x + 1] = f.y;
+            v[j][x + 2] = f.z;
+            v[j][x + 3] = f.w;
+          } else {
+            const float2 f =
+                some ? __ldcg(reinterpret_cast<const float2*>(at)) : make_float2(0.f, 0.f);
+            v[j][x] = f.x;
+            v[j][x + 1] = f.y;
+          }
         }
       }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int x = 0; x < kPer; ++x) o[x] = fmaf(v[j][x], t[j], o[x]);
     }
   }
+  constexpr int kVec = kPer < 4 ? kPer : 4;
 #pragma unroll
-  for (int x = 0; x < kPer; ++x) sums[warp][lane * kPer + x] = o[x];
+  for (int x = 0; x < kPer; ++x)
+    sums[warp][x / kVec * (32 * kVec) + lane * kVec + x % kVec] = o[x];
   if (lane == 0) {
     tops[warp] = m;
     totals[warp] = l;

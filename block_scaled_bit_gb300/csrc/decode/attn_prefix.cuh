@@ -74,8 +74,7 @@ __host__ __device__ inline AttnPreSplit attn_pre_split(int B, int Hq, int Hkv, i
   return s;
 }
 
-// A part is [D / 4][rows] groups of four columns, then [rows] m, [rows] l: a row is a thread's, so
-// this is the order in which a warp's stores are whole lines.
+// A part is [rows][D] sums, [rows] m, [rows] l.
 __host__ __device__ constexpr int attn_pre_slot_floats(int D) {
   return (D == 256 ? 128 : 256) * (D + 2);
 }
@@ -533,16 +532,35 @@ struct AttnPrefix {
     const uint32_t last = job + jobs - 1;
     if (!wait_warp(c, c.out(Ctx::buf(stream, last)), Ctx::phase(last))) return false;
     tc_after();
+    // a thread holds a row; through shared memory, 16 columns at a time, into whole sectors.  The
+    // queries' place is free: this stream's scores are all done, and where both streams share the
+    // first tile of queries the second is unused.
+    const int warp = tid >> 5, lane = tid & 31;
+    static_assert(T::kQB / 2 >= 4 * 2048, "2 KB a warp");
+    uint8_t* mine = c.base + (c.s.pair ? T::kQB + stream * (T::kQB / 2) : stream * T::kQB) + warp * 2048;
+    float* rows = part + static_cast<int64_t>(stream * 128 + warp * 32) * D;
 #pragma unroll 1
     for (int i = 0; i < D; i += 32) {
       uint32_t o[32];
       tc_ld32(to + i, o);
       tc_wait_ld();
 #pragma unroll
-      for (int y = 0; y < 32; y += 4)
-        __stcg(reinterpret_cast<float4*>(part) + (i + y) / 4 * T::kSlotRows + row,
-               make_float4(__uint_as_float(o[y]), __uint_as_float(o[y + 1]),
-                           __uint_as_float(o[y + 2]), __uint_as_float(o[y + 3])));
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t* v = o + 16 * half + 4 * y;
+          *reinterpret_cast<uint4*>(mine + lane * 64 + ((y ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int r = 8 * y + (lane >> 2), ch = lane & 3;
+          __stcg(reinterpret_cast<float4*>(rows + static_cast<int64_t>(r) * D + i + 16 * half + 4 * ch),
+                 lsh<float4>(mine + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)));
+        }
+        __syncwarp();
+      }
     }
     tc_before();
     return true;
