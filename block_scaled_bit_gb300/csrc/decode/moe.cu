@@ -42,8 +42,8 @@ int maps_of(bsgemv_moe_plan_s* p, const MoeWeight& up, const MoeWeight& down, Mo
     }
   auto& m = p->maps[p->next_map];
   m.W13 = nullptr;
-  int rc = moe_encode(&m.up, up, p->E);
-  if (rc == BSGEMV_OK) rc = moe_encode(&m.down, down, p->E);
+  int rc = moe_encode(&m.up, up, p->E, true);
+  if (rc == BSGEMV_OK) rc = moe_encode(&m.down, down, p->E, false);
   if (rc != BSGEMV_OK) return rc;
   p->next_map = (p->next_map + 1) % bsgemv_moe_plan_s::kMaps;
   m.W13 = up.W;

@@ -45,12 +45,22 @@ BSG_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t b
       : "memory");
 }
 
+BSG_DEV void tma_load_4d_hint(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, int w,
+                              uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(policy)
+      : "memory");
+}
+
 constexpr int kMoeThreads = 160;  // copy warp, four decode warps
 constexpr int kMoeTileRows = 64;
 constexpr int kMoeBoxB = kMoeTileRows * 128;
 
 struct MoeGemmParams {
-  CUtensorMap tm;             // weight bytes [E * rows][row bytes], box [32][128], 128B swizzle
+  CUtensorMap tm;             // weight bytes, a box is a tile's 64 rows x 128 bytes, 128B swizzle:
+                              // UP [E][2][I][row bytes], box [2][32][128]; DOWN [E][1][H][...], [64]
   const uint8_t* x;           // packed activations [token (UP) or row (DOWN)][stage][row bytes]
   const Routing* route;
   const uint8_t *scales, *zp;
@@ -157,45 +167,27 @@ struct MoeGemm {
   static BSG_DEV int rows_of(const Ctx& c, int a) { return c.off(a + 1) - c.off(a); }
   static BSG_DEV int wrap(const Ctx& c, int r) { return r >= c.p.row_cap ? r - c.p.row_cap : r; }
 
-  // Scales (or zero points) of this lane's two rows of a tile, lane and lane + 32: copied in
-  // units of `unit` bytes where every row's part starts on one, else as the whole words that
-  // hold it (the reader adds the start's low two bits).  Nothing at or past `end` is read.
+  // Scales (or zero points) of this lane's two rows of a tile, lane and lane + 32.  Where every
+  // row's part of a stage is 4, 8, 16 or twice 16 bytes on such a boundary (`unit`), it is one copy
+  // a row (two); else (unit 0, or a tile with the array's last rows) the whole words that hold it
+  // are copied, nothing at or past `end`, and the reader adds the start's low two bits.
   struct Side {
-    const uint8_t* src;
-    int64_t off[2];  // of the row's first byte
-    int64_t end;
-    int unit, count, stride, bytes;
+    const uint8_t* src[2];  // the row's part of the run's next stage
+    const uint8_t* end;
+    int unit, stride, bytes;
+    bool edge;
   };
   static BSG_DEV Side side_of(const uint8_t* src, int64_t pitch, int64_t end, int unit, int stride,
-                              int bytes, int row, int second, int lane) {
+                              int bytes, const Run& w, int row, int second, int lane) {
     Side s;
-    s.src = src;
-    s.off[0] = (row + lane) * pitch;
-    s.off[1] = (row + lane + second) * pitch;
-    s.end = end;
+    s.src[0] = src + (row + lane) * pitch + w.ks * bytes;
+    s.src[1] = s.src[0] + second * pitch;
+    s.end = src + end;
     s.unit = unit;
-    s.count = unit ? bytes / unit : stride / 4;
     s.stride = stride;
     s.bytes = bytes;
+    s.edge = src + (static_cast<int64_t>(row) + second + 31) * pitch + (w.ks + w.n) * bytes + 4 > s.end;
     return s;
-  }
-  template <int UNIT>
-  static BSG_DEV void side_units(const Side& s, uint32_t dst, int at, int lane) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t off = (s.off[h] + at) & ~static_cast<int64_t>(3);
-      const int64_t left = s.end - off;
-      const uint8_t* src = s.src + off;
-      uint32_t to = dst + (lane + 32 * h) * s.stride;
-      if (left >= s.count * UNIT) {
-        for (int i = 0; i < s.count; ++i, to += UNIT, src += UNIT) cp_unit<UNIT>(to, src, UNIT);
-      } else {  // the array's last rows
-        for (int i = 0; i < s.count; ++i, to += UNIT) {
-          const int have = static_cast<int>(max(static_cast<int64_t>(0), min(left - i * UNIT, static_cast<int64_t>(UNIT))));
-          cp_unit<UNIT>(to, have > 0 ? src + i * UNIT : s.src, have);
-        }
-      }
-    }
   }
   template <int UNIT>
   static BSG_DEV void cp_unit(uint32_t dst, const uint8_t* src, int bytes) {
@@ -207,36 +199,75 @@ struct MoeGemm {
                    "r"(bytes)
                    : "memory");
   }
-  static BSG_DEV void side_copy(const Side& s, uint32_t dst, int ks, int lane) {
-    if (s.unit == 16) side_units<16>(s, dst, ks * s.bytes, lane);
-    else if (s.unit == 8) side_units<8>(s, dst, ks * s.bytes, lane);
-    else side_units<4>(s, dst, ks * s.bytes, lane);
+  static BSG_DEV void side_copy(Side& s, uint32_t dst, int lane) {
+    const uint32_t to = dst + lane * s.stride;
+    if (s.unit == 16 && !s.edge) {
+      cp_unit<16>(to, s.src[0], 16);
+      cp_unit<16>(to + 32 * s.stride, s.src[1], 16);
+      if (s.bytes == 32) {
+        cp_unit<16>(to + 16, s.src[0] + 16, 16);
+        cp_unit<16>(to + 32 * s.stride + 16, s.src[1] + 16, 16);
+      }
+    } else if (s.unit == 8 && !s.edge) {
+      cp_unit<8>(to, s.src[0], 8);
+      cp_unit<8>(to + 32 * s.stride, s.src[1], 8);
+    } else if (s.unit == 4 && !s.edge) {
+      cp_unit<4>(to, s.src[0], 4);
+      cp_unit<4>(to + 32 * s.stride, s.src[1], 4);
+    } else if (!s.edge) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* src = s.src[h] - (reinterpret_cast<uintptr_t>(s.src[h]) & 3);
+        const uint32_t at = to + h * 32 * s.stride;
+        cp_unit<4>(at, src, 4);
+#pragma unroll
+        for (int i = 1; i < 9; ++i)
+          if (4 * i < s.stride) cp_unit<4>(at + 4 * i, src + 4 * i, 4);
+      }
+    } else {
+      side_words(s, to);
+    }
+    s.src[0] += s.bytes;
+    s.src[1] += s.bytes;
+  }
+  static __device__ __noinline__ void side_words(const Side& s, uint32_t to) {
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* src = s.src[h] - (reinterpret_cast<uintptr_t>(s.src[h]) & 3);
+      for (int i = 0; i < s.stride; i += 4) {
+        const int64_t left = s.end - (src + i);
+        const int have = left >= 4 ? 4 : (left > 0 ? static_cast<int>(left) : 0);
+        // (nothing to read: any address of the array will do)
+        const uint8_t* none = s.end - 4 - (reinterpret_cast<uintptr_t>(s.end) & 3);
+        cp_unit<4>(to + h * 32 * s.stride + i, have ? src + i : none, have);
+      }
+    }
   }
 
-  // The weight boxes, scales and zero points of stages of one run.
+  // The weight box, scales and zero points of the stages of one run, in order.
   struct Weights {
-    int row;
+    int e, row;  // expert, first row of the tile
     Side s, z;
   };
   static BSG_DEV Weights weights_of(const Ctx& c, const Run& w, int lane) {
     const MoeGemmParams& p = c.p;
     Weights x;
-    x.row = weight_row(c, w);
-    x.s = side_of(p.scales, p.s_pitch, p.s_end, p.s_unit, p.s_stride, p.s_bytes, x.row, p.second, lane);
+    x.e = c.expert(w.a);
+    x.row = w.tile * p.step;
+    const int row = weight_row(c, w);
+    x.s = side_of(p.scales, p.s_pitch, p.s_end, p.s_unit, p.s_stride, p.s_bytes, w, row, p.second, lane);
     if (kInts && p.zp)
-      x.z = side_of(p.zp, p.z_pitch, p.z_end, p.z_unit, p.z_stride, p.z_bytes, x.row, p.second, lane);
+      x.z = side_of(p.zp, p.z_pitch, p.z_end, p.z_unit, p.z_stride, p.z_bytes, w, row, p.second, lane);
     return x;
   }
-  static BSG_DEV void issue_weights(const Ctx& c, const Weights& x, int ks, int slot, uint64_t pol,
+  static BSG_DEV void issue_weights(const Ctx& c, Weights& x, int ks, int slot, uint64_t pol,
                                     int lane) {
-    if (lane == 0) {
-      const uint32_t dst = c.base_u + slot * kMoeBoxB;
-      tma_load_2d_hint(dst, &c.p.tm, ks * 128, x.row, c.full(slot), pol);
-      tma_load_2d_hint(dst + kMoeBoxB / 2, &c.p.tm, ks * 128, x.row + c.p.second, c.full(slot), pol);
-    }
+    // one box: 64 rows, or 32 gate rows and the up rows that belong to them
+    if (lane == 0)
+      tma_load_4d_hint(c.base_u + slot * kMoeBoxB, &c.p.tm, ks * 128, x.row, 0, x.e, c.full(slot), pol);
     const uint32_t side = c.base_u + c.p.off_side + slot * c.p.side_bytes;
-    side_copy(x.s, side, ks, lane);
-    if (kInts && c.p.zp) side_copy(x.z, side + kMoeTileRows * c.p.s_stride, ks, lane);
+    side_copy(x.s, side, lane);
+    if (kInts && c.p.zp) side_copy(x.z, side + kMoeTileRows * c.p.s_stride, lane);
   }
 
   // Weights, scales and activations of every stage in order, as far ahead as the rings allow.
@@ -252,7 +283,7 @@ struct MoeGemm {
     if constexpr (DOWN) {
       Run e = w;
       while (early < p.stages) {
-        const Weights x = weights_of(c, e, lane);
+        Weights x = weights_of(c, e, lane);
         const int most = min(e.n, p.stages - early);
         for (int i = 0; i < most; ++i, ++early) {
           if (lane == 0) mbar_expect_tx(c.full(early), kMoeBoxB);
@@ -267,7 +298,7 @@ struct MoeGemm {
     int tslot = 0, tail_m = rows_of(c, tail.a);
     uint32_t tphase = 0;
     while (true) {
-      const Weights x = weights_of(c, w, lane);
+      Weights x = weights_of(c, w, lane);
       const int r0 = c.off(w.a), m = c.off(w.a + 1) - r0;
       const uint32_t tx = m * kRowB;
       const int64_t row = DOWN ? r0 + lane : (lane < m ? c.token(r0 + lane) : 0);
@@ -291,7 +322,16 @@ struct MoeGemm {
         const uint32_t full = c.full(slot);
         if (lane == 0) mbar_expect_tx(full, i < early ? tx : tx + kMoeBoxB);
         __syncwarp();  // the bytes are expected before any lane's copy can complete
-        if (i >= early) issue_weights(c, x, w.ks + k, slot, pol, lane);
+        if (i >= early) {
+          issue_weights(c, x, w.ks + k, slot, pol, lane);
+        } else {
+          x.s.src[0] += x.s.bytes;
+          x.s.src[1] += x.s.bytes;
+          if (kInts && p.zp) {
+            x.z.src[0] += x.z.bytes;
+            x.z.src[1] += x.z.bytes;
+          }
+        }
         if (lane < m)
           bulk_load(c.base_u + p.off_rows + wrap(c, head + lane) * kRowB, src, kRowB, full);
         src += kRowB;
@@ -322,7 +362,7 @@ struct MoeGemm {
 
   struct Lane {
     int cw, lane, g, t;
-    uint32_t w[4];  // ldmatrix address of chunk pair j in a stage's weights
+    uint32_t w;     // ldmatrix address of chunk pair 0 in a stage's weights; pair j's is w ^ 32 j
     int s[2], z[2];  // rows g and g + 8 in a stage's scales and zero points
   };
   static BSG_DEV Lane make_lane(const MoeGemmParams& p, int cw, int lane) {
@@ -332,8 +372,7 @@ struct MoeGemm {
     L.g = lane >> 2;
     L.t = lane & 3;
     const int i = lane >> 3, r = tile_row(cw, i & 1) + (lane & 7);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) L.w[j] = r * 128 + (((2 * j + (i >> 1)) ^ (r & 7)) << 4);
+    L.w = r * 128 + (((i >> 1) ^ (r & 7)) << 4);
 #pragma unroll
     for (int rr = 0; rr < 2; ++rr) {
       L.s[rr] = (tile_row(cw, rr) + L.g) * p.s_stride;
@@ -342,9 +381,8 @@ struct MoeGemm {
     return L;
   }
 
-  // B fragments of one chunk from a ring row (this lane's column).
-  static BSG_DEV void fragment(const uint8_t* row, int t, int chunk, uint32_t (&b)[kSteps][2]) {
-    const uint8_t* src = row + chunk * kChunkB + t * (kChunkB / 4);
+  // B fragments of one chunk from a ring row (this lane's column and quarter of the chunk).
+  static BSG_DEV void fragment(const uint8_t* src, uint32_t (&b)[kSteps][2]) {
     if constexpr (kFour) {
       const uint4 v = lsh<uint4>(src);
       if constexpr (FMT == kInt4) {
@@ -374,91 +412,106 @@ struct MoeGemm {
     return lsh<uint8_t>(row + blk);
   }
 
-  // The stage's products with one n8 tile of tokens.  row: the ring row of this lane's B column.
+  // The stage's products with one n8 tile of tokens.  row: the ring row of this lane's B column;
+  // ss, zs: what the rows' windows of words add to their starts.
   // (An expert with more than eight tokens has its stage decoded once for each eight: the
   // weights come from HBM once all the same, and all but the first eight are rare.)
-  // ss, zs: what the rows' windows of words add to their starts.
+  // The loop over chunk pairs is unrolled by two (blocks of a whole stage: by four): wholly
+  // unrolled, a small call spent 1000 cycles a stage more on fetching the code; rolled, a large
+  // one 15 % more on running it.
   static BSG_DEV void consume(const Ctx& c, const Lane& L, int ks, int slot, const uint8_t* row,
                               const int (&ss)[2], const int (&zs)[2], float (&st)[4]) {
     const MoeGemmParams& p = c.p;
-    const uint32_t wa = c.base_u + slot * kMoeBoxB;
-    // chunk pair j, loaded one pair ahead: (chunk 2j: row g, g + 8), (chunk 2j + 1: row g, g + 8)
-    uint32_t v[2][4];
-    ldsm_x4_at<0>(wa + L.w[0], v[0][0], v[0][1], v[0][2], v[0][3]);
+    const uint32_t wa = c.base_u + slot * kMoeBoxB + L.w;
+    // (chunk 2j: row g, g + 8), (chunk 2j + 1: row g, g + 8), loaded one pair ahead
+    uint32_t v[4], ahead[4];
+    ldsm_x4_at<0>(wa, ahead[0], ahead[1], ahead[2], ahead[3]);
     const uint8_t* side = c.base + p.off_side + slot * p.side_bytes;
     const int left = static_cast<int>(p.K) - ks * kKc;
     const int pairs = left >= kKc ? 4 : (left + 2 * kKpc - 1) / (2 * kKpc);
-    const uint8_t* const sr[2] = {side + L.s[0] + ss[0], side + L.s[1] + ss[1]};
+    const uint8_t* sr[2] = {side + L.s[0] + ss[0], side + L.s[1] + ss[1]};
     const uint8_t* const zr[2] = {side + L.z[0] + zs[0], side + L.z[1] + zs[1]};
     uint32_t zl[2] = {0u, 0u}, zh[2] = {0u, 0u};
     if constexpr (kInts)
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) zp_consts<FMT, false>(FMT == kInt4 ? 8u : 128u, zl[rr], zh[rr]);
     float tmp[kSub][4];  // a scale block's sums
-#pragma unroll
-    for (int x = 0; x < 4; ++x) st[x] = 0.f;
     float s[kSub][2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j >= pairs) break;
-      if (j < 3)
-        ldsm_x4_at<0>(wa + L.w[j + 1], v[(j + 1) & 1][0], v[(j + 1) & 1][1], v[(j + 1) & 1][2],
-                      v[(j + 1) & 1][3]);
+    for (int x = 0; x < 4; ++x) st[x] = 0.f;
+    if constexpr (kFold) {  // this lane's block of the first chunk: 16 elements, t / 2
+      sr[0] += L.t >> 1;
+      sr[1] += L.t >> 1;
+    }
+    constexpr int kRun = CPB == 0 ? 1 : CPB;  // chunks of a scale block
+    constexpr int kSpan = kFold || kRun < 4 ? 2 : kRun / 2;  // pairs of an iteration
+    const uint8_t* src = row + L.t * (kChunkB / 4);
+#pragma unroll 1
+    for (int j0 = 0; j0 < pairs; j0 += kSpan) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int chunk = 2 * j + q;
-        const uint32_t lo = v[j & 1][2 * q], hi = v[j & 1][2 * q + 1];
-        uint32_t a[kSteps][4];
-        constexpr int kRun = CPB == 0 ? 1 : CPB;
-        const bool opens = !kFold && chunk % kRun == 0, closes = !kFold && (chunk + 1) % kRun == 0;
-        if constexpr (kFold) {
+      for (int jj = 0; jj < kSpan; ++jj) {
+        const int j = j0 + jj;
+        if (kSpan == 2 && CPB != 4 && j >= pairs) break;
 #pragma unroll
-          for (int rr = 0; rr < 2; ++rr)  // 16-element block 2 chunk + t / 2
-            zl[rr] = e4m3x2_to_f16x2(0x0101u * lsh<uint8_t>(sr[rr] + 2 * chunk + (L.t >> 1)));
-          decode_nvfp4<false>(lo, hi, zl[0], zl[1], a);
-        } else {
-          if (opens) {
-            const int blk = CPB == 0 ? 2 * chunk : chunk / kRun;
+        for (int x = 0; x < 4; ++x) v[x] = ahead[x];
+        if (j < 3)
+          ldsm_x4_at<0>(wa ^ ((j + 1) << 5), ahead[0], ahead[1], ahead[2], ahead[3]);
 #pragma unroll
-            for (int rr = 0; rr < 2; ++rr) {
+        for (int q = 0; q < 2; ++q) {
+          const int chunk = 2 * j + q, in = 2 * jj + q;  // in: its place in the iteration
+          const uint32_t lo = v[2 * q], hi = v[2 * q + 1];
+          uint32_t a[kSteps][4];
+          const bool opens = !kFold && in % kRun == 0, closes = !kFold && (in + 1) % kRun == 0;
+          if constexpr (kFold) {
 #pragma unroll
-              for (int u = 0; u < kSub; ++u) s[u][rr] = scale_at(sr[rr], blk + u);
-              if constexpr (kInts)
-                if (p.zp)
-                  zp_consts<FMT, false>(zp_at(zr[rr], CPB == 0 ? blk + (L.t >> 1) : blk), zl[rr], zh[rr]);
-            }
-          }
-          if constexpr (FMT == kInt4) decode_int4<false>(lo, hi, zl[0], zh[0], zl[1], zh[1], a);
-          else if constexpr (FMT == kInt8) decode_int8<false>(lo, hi, zl[0], zl[1], a);
-          else decode_fp8<false>(lo, hi, a);
-        }
-        uint32_t b[kParts][kSteps][2];
+            for (int rr = 0; rr < 2; ++rr)
+              zl[rr] = e4m3x2_to_f16x2(0x0101u * lsh<uint8_t>(sr[rr] + 2 * chunk));
+            decode_nvfp4<false>(lo, hi, zl[0], zl[1], a);
+          } else {
+            if (opens) {
+              const int blk = CPB == 0 ? 2 * chunk : chunk / kRun;
 #pragma unroll
-        for (int part = 0; part < kParts; ++part)
-          fragment(row + part * kPitch, L.t, chunk, b[part]);
+              for (int rr = 0; rr < 2; ++rr) {
 #pragma unroll
-        for (int part = 0; part < kParts; ++part)
-#pragma unroll
-          for (int i = 0; i < kSteps; ++i) {
-            if constexpr (kFold) {
-              mma16816<false>(st, a[i], b[part][i][0], b[part][i][1]);
-            } else {
-              const bool first = opens && part == 0 && i == 0;
-#pragma unroll
-              for (int u = 0; u < kSub; ++u) {
-                // two blocks in a chunk: quad lanes t < 2 hold the first
-                const bool mine = kSub == 1 || (L.t >> 1) == u;
-                const uint32_t b0 = mine ? b[part][i][0] : 0u, b1 = mine ? b[part][i][1] : 0u;
-                if (first) mma16816_zc<false>(tmp[u], a[i], b0, b1);
-                else mma16816<false>(tmp[u], a[i], b0, b1);
+                for (int u = 0; u < kSub; ++u) s[u][rr] = scale_at(sr[rr], blk + u);
+                if constexpr (kInts)
+                  if (p.zp)
+                    zp_consts<FMT, false>(zp_at(zr[rr], CPB == 0 ? blk + (L.t >> 1) : blk), zl[rr],
+                                          zh[rr]);
               }
             }
+            if constexpr (FMT == kInt4) decode_int4<false>(lo, hi, zl[0], zh[0], zl[1], zh[1], a);
+            else if constexpr (FMT == kInt8) decode_int8<false>(lo, hi, zl[0], zl[1], a);
+            else decode_fp8<false>(lo, hi, a);
           }
-        if (closes) {
+          uint32_t b[kParts][kSteps][2];
 #pragma unroll
-          for (int u = 0; u < kSub; ++u)
+          for (int part = 0; part < kParts; ++part)
+            fragment(src + part * kPitch + chunk * kChunkB, b[part]);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) st[x] = fmaf(tmp[u][x], s[u][x >> 1], st[x]);
+          for (int part = 0; part < kParts; ++part)
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+              if constexpr (kFold) {
+                mma16816<false>(st, a[i], b[part][i][0], b[part][i][1]);
+              } else {
+                const bool first = opens && part == 0 && i == 0;
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) {
+                  // two blocks in a chunk: quad lanes t < 2 hold the first
+                  const bool mine = kSub == 1 || (L.t >> 1) == u;
+                  const uint32_t b0 = mine ? b[part][i][0] : 0u, b1 = mine ? b[part][i][1] : 0u;
+                  if (first) mma16816_zc<false>(tmp[u], a[i], b0, b1);
+                  else mma16816<false>(tmp[u], a[i], b0, b1);
+                }
+              }
+            }
+          if (closes) {
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) st[x] = fmaf(tmp[u][x], s[u][x >> 1], st[x]);
+          }
         }
       }
     }

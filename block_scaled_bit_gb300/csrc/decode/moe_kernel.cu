@@ -1,4 +1,6 @@
 // moe_kernel.cu -- the kernels of the mixture-of-experts layer and their launches.
+#include <math.h>
+
 #include "moe_gemm.cuh"
 #include "moe_kernel.cuh"
 
@@ -262,11 +264,21 @@ constexpr int kSmemPerSm = 233472;  // 228 KB, of which each block takes 1 KB fo
 
 int align_up(int v, int a) { return (v + a - 1) / a * a; }
 
-// The largest unit (16, 8 or 4 bytes) that every row's scales start on and are made of, or 0.
+// 16, 8 or 4 where a row's part of a stage is so many bytes (or twice 16) on such a boundary in
+// every row, else 0.
 int copy_unit(const void* base, int64_t pitch, int bytes) {
-  for (int u = 16; u >= 4; u /= 2)
-    if (aligned_to(base, u) && pitch % u == 0 && bytes % u == 0) return u;
-  return 0;
+  const int unit = bytes == 32 ? 16 : bytes;
+  const bool one = unit == 16 || unit == 8 || unit == 4;
+  return one && aligned_to(base, unit) && pitch % unit == 0 ? unit : 0;
+}
+
+// Activation rows of a stage to leave room for: twice what an active expert has on average when
+// every token chooses at random.
+int usual_rows(const MoeParams& c) {
+  const double p = static_cast<double>(c.top_k) / c.E;
+  const double active = c.E * (1.0 - pow(1.0 - p, c.max_T));
+  const int n = static_cast<int>(2.0 * c.max_T * c.top_k / active + 0.999);
+  return n < c.max_T ? n : c.max_T;
 }
 
 int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
@@ -316,9 +328,10 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
   const int budget = kSmemPerSm / blocks_per_sm(c.max_T) - 1024;
   const int route_bytes = align_up((4 * p.top_rows + 1) * 4, 16);
   p.slot_floats = down ? c.max_T * 16 : (wide ? 4 : 1) * 128;
+  const int rows = usual_rows(c);
   int smem = 0;
   for (p.stages = 12; p.stages >= 2; --p.stages) {
-    const int typical = p.stages * (c.max_T < 3 ? c.max_T : 3);
+    const int typical = p.stages * rows;
     p.row_cap = typical > c.max_T ? typical : c.max_T;
     int at = p.stages * kMoeBoxB;
     p.off_side = at;
@@ -371,11 +384,13 @@ MoeLayout moe_layout(int fmt, int64_t H, int64_t I, int E, int top_k, int max_T,
   return l;
 }
 
-int moe_encode(CUtensorMap* tm, const MoeWeight& w, int E) {
-  const uint64_t dims[2] = {static_cast<uint64_t>(w.row_bytes), static_cast<uint64_t>(w.rows) * E};
-  const uint64_t strides[1] = {static_cast<uint64_t>(w.row_bytes)};
-  const uint32_t box[2] = {128, 32};
-  return decode_encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, w.W, dims, strides, box,
+int moe_encode(CUtensorMap* tm, const MoeWeight& w, int E, bool up) {
+  const uint64_t parts = up ? 2 : 1, rows = static_cast<uint64_t>(w.rows) / parts;
+  const uint64_t bytes = static_cast<uint64_t>(w.row_bytes);
+  const uint64_t dims[4] = {bytes, rows, parts, static_cast<uint64_t>(E)};
+  const uint64_t strides[3] = {bytes, bytes * rows, bytes * rows * parts};
+  const uint32_t box[4] = {128, up ? 32u : 64u, up ? 2u : 1u, 1};
+  return decode_encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, w.W, dims, strides, box,
                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 

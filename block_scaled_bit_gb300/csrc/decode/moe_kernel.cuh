@@ -51,7 +51,7 @@ struct MoeParams {
   const int32_t* ids;
   const float* weights;
   MoeWeight up, down;
-  CUtensorMap tm_up, tm_down;  // weight bytes, boxes of [32 rows][128 bytes], 128-byte swizzle
+  CUtensorMap tm_up, tm_down;  // of the weights' bytes (moe_encode)
   uint16_t* y;
   unsigned* err;
   unsigned *counters_up, *counters_down;  // arrivals per (tile, decode warp), left at zero
@@ -92,7 +92,7 @@ inline int64_t moe_stages(int fmt, int64_t H, int64_t I, int E, int top_k, int m
 }
 
 // Tensor map of one stacked weight (BSGEMV_ERR_CUDA if it cannot be encoded).
-int moe_encode(CUtensorMap* tm, const MoeWeight& w, int E);
+int moe_encode(CUtensorMap* tm, const MoeWeight& w, int E, bool up);
 
 int launch_moe(const MoeParams& p, int sms, cudaStream_t s);
 
