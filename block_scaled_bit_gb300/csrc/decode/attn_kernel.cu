@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(128)
 
 template <bool BF16, int D>
 int launch(const AttnParams& p, int mode, const AttnMaps& maps, int sms, cudaStream_t s) {
-  static AttrRecord rec, pre_rec;
+  static AttrRecord rec, pre_rec, merge_rec;
   using T = AttnTile<D>;
   const int ps = 1 << p.page_log2;
   int rc;
@@ -192,6 +192,8 @@ int launch(const AttnParams& p, int mode, const AttnMaps& maps, int sms, cudaStr
   if (rc != BSGEMV_OK) return rc;
   rc = decode_launch(attn_stream_kernel<BF16, D>, dim3(sms), dim3(32 * kAttnWarps), smem, s, q,
                      mode);
+  if (rc != BSGEMV_OK) return rc;
+  rc = decode_smem(attn_merge<BF16, D>, merge_rec, 16);  // for the carveout
   if (rc != BSGEMV_OK) return rc;
   return decode_launch(attn_merge<BF16, D>, dim3(p.B * p.Hq), dim3(128), 0, s, p, mode, sms);
 }

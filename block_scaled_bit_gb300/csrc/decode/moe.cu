@@ -3,8 +3,7 @@
 //   route     one block: top-k of each token's logits, the experts that are wanted and their
 //             tokens (a 32-bit mask per expert: max_T <= 32)
 //             ... and, in other blocks, x packed for the tensor cores
-//   up        h[row][i] = p * silu(g) * u for every (expert, token) pair
-//   pack      h packed likewise
+//   up        h[row][i] = p * silu(g) * u for every (expert, token) pair, packed likewise
 //   down      y[t][n]   = sum over the token's experts, in expert order
 #include <math.h>
 
@@ -94,6 +93,7 @@ int run(bsgemv_moe_plan_s* p, const void* x, const void* logits, const int32_t* 
   q.err = reinterpret_cast<unsigned*>(w);
   q.route = reinterpret_cast<Routing*>(w + p->at.route);
   q.counters_up = reinterpret_cast<unsigned*>(w + p->at.counters_up);
+  q.counters_packed = reinterpret_cast<unsigned*>(w + p->at.counters_packed);
   q.counters_down = reinterpret_cast<unsigned*>(w + p->at.counters_down);
   q.partials = reinterpret_cast<float*>(w + p->at.partials);
   q.h = reinterpret_cast<float*>(w + p->at.h);

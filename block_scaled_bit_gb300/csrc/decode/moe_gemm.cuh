@@ -20,8 +20,8 @@
 // The weights go through mma.sync m16n8k16 as the A operand, decoded to f16 (every format's codes
 // are exact in f16, and the decoders to bf16 take three conversions more per pair at a quarter
 // of the rate), and the tokens as B, eight per tile and at most MT tiles; the decoders and the k
-// permutation are the GEMV's.  The activations come packed for this by small kernels (moe_pack):
-// per row and stage the values in f16 with a power of two taken out, and that factor, which
+// permutation are the GEMV's.  The activations come packed for this (x beside the routing, h by
+// UP): per row and stage the values in f16 with a power of two taken out, and that factor, which
 // multiplies the stage's fp32 sums: f16 x as it is; bf16 x scaled to just below the top of f16's
 // range, exact for every element within 2^29 of the largest of its 128 or 256, the others off by
 // 2^-40 of that; h (fp32) likewise in two f16 parts, h = hi + lo, each multiplied: 22 bits, where
@@ -61,13 +61,16 @@ constexpr int kMoeBoxB = kMoeTileRows * 128;
 struct MoeGemmParams {
   CUtensorMap tm;             // weight bytes, a box is a tile's 64 rows x 128 bytes, 128B swizzle:
                               // UP [E][2][I][row bytes], box [2][32][128]; DOWN [E][1][H][...], [64]
-  const uint8_t* x;           // packed activations [token (UP) or row (DOWN)][stage][row bytes]
+  const uint8_t* x;           // packed activations: UP [token][stage][row bytes], DOWN
+                              // [stage][row][row bytes] (an expert's rows of a stage are adjacent)
   const Routing* route;
   const uint8_t *scales, *zp;
   const float* gscale;        // NVFP4: [E]
   float* partials;
   unsigned *counters, *err;
   float* h;                   // UP: [rows][I]
+  uint8_t* h_packed;          // UP: [row][stage of I][2 pitches]
+  unsigned* packed;           // UP: [active expert][stage of I] warps that have stored into it
   uint16_t* y;                // DOWN: [T][H]
   uint64_t wait_ns;
   int64_t K;                  // elements of an activation row
@@ -87,6 +90,54 @@ struct MoeGemmParams {
   int off_side, side_bytes, off_rows, off_route, off_bar, off_sum;
   int slot_floats;            // floats of a partial sum (one warp's part of a tile)
 };
+
+// ---- packing
+BSG_DEV uint32_t pack_f16(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int N>
+BSG_DEV void put(uint8_t* dst, const uint32_t (&h)[N]) {
+  if constexpr (N == 4) *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+  else *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[1]);
+}
+
+// One warp packs one stage of a row, PER consecutive values a lane (see moe_gemm.cuh): the
+// largest finite magnitude scaled into [2^14, 2^15), f16 values (PARTS = 2: and their remainders),
+// the factor that undoes the scale.
+template <int PER, int PARTS>
+BSG_DEV void pack_stage(float (&v)[PER], uint8_t* dst, int lane) {
+  constexpr int kPitch = moe_pitch(PER == 8);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+    top = max(top, m < 0x7F800000u ? m : 0u);
+  }
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  const int e = min(max(static_cast<int>(top >> 23), 16), 240);  // scale and factor stay normal
+  const float scale = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - e) << 23);
+  if (lane == 0)
+    *reinterpret_cast<float*>(dst + 64 * PER) = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+  uint32_t hi[PER / 2];
+#pragma unroll
+  for (int i = 0; i < PER / 2; ++i) {
+    v[2 * i] *= scale;
+    v[2 * i + 1] *= scale;
+    hi[i] = pack_f16(v[2 * i], v[2 * i + 1]);
+  }
+  put(dst + lane * (2 * PER), hi);
+  if constexpr (PARTS == 2) {
+    uint32_t lo[PER / 2];
+#pragma unroll
+    for (int i = 0; i < PER / 2; ++i) {
+      const float a = half_to_f32<false>(hi[i], 0), b = half_to_f32<false>(hi[i], 1);
+      lo[i] = pack_f16(isfinite(a) ? v[2 * i] - a : 0.f, isfinite(b) ? v[2 * i + 1] - b : 0.f);
+    }
+    put(dst + kPitch + lane * (2 * PER), lo);
+  }
+}
 
 // CPB: 16-byte chunks of a row per scale block (the GEMV's block_mode): 0 = a chunk holds two
 // blocks, 8 = one block is the whole stage; NVFP4 folds its scales into the operand.
@@ -301,8 +352,11 @@ struct MoeGemm {
       Weights x = weights_of(c, w, lane);
       const int r0 = c.off(w.a), m = c.off(w.a + 1) - r0;
       const uint32_t tx = m * kRowB;
-      const int64_t row = DOWN ? r0 + lane : (lane < m ? c.token(r0 + lane) : 0);
-      const uint8_t* src = p.x + (row * p.spt + w.ks) * kRowB;  // this lane's row (lane < m)
+      // UP: lane j < m copies token j's row.  DOWN: lane 0 copies all rows, lane 1 those past the
+      // ring's end.
+      const int64_t row = DOWN ? static_cast<int64_t>(w.ks) * p.top_rows + r0
+                               : static_cast<int64_t>(lane < m ? c.token(r0 + lane) : 0) * p.spt + w.ks;
+      const uint8_t* src = p.x + row * kRowB;
       for (int k = 0; k < w.n; ++k, ++i) {
         while (free_slots == 0 || used + m > p.row_cap) {
           if (!__all_sync(0xFFFFFFFFu, mbar_wait(c.empty(tslot), tphase, p.err, kErrTimeoutEmpty,
@@ -332,9 +386,17 @@ struct MoeGemm {
             x.z.src[1] += x.z.bytes;
           }
         }
-        if (lane < m)
-          bulk_load(c.base_u + p.off_rows + wrap(c, head + lane) * kRowB, src, kRowB, full);
-        src += kRowB;
+        if constexpr (DOWN) {
+          const int here = min(m, p.row_cap - head);
+          if (lane == 0) bulk_load(c.base_u + p.off_rows + head * kRowB, src, here * kRowB, full);
+          if (lane == 1 && here < m)
+            bulk_load(c.base_u + p.off_rows, src + here * kRowB, (m - here) * kRowB, full);
+          src += static_cast<int64_t>(p.top_rows) * kRowB;
+        } else {
+          if (lane < m)
+            bulk_load(c.base_u + p.off_rows + wrap(c, head + lane) * kRowB, src, kRowB, full);
+          src += kRowB;
+        }
         cp_async_mbar_arrive(full);
         __syncwarp();
         if (lane == 0) mbar_arrive(full);
@@ -535,6 +597,78 @@ struct MoeGemm {
       }
   }
 
+  // UP: packing.  The last warp to store into a stage of DOWN's k (of kKc columns: 8 or 4 tiles of
+  // four warps) packs that stage of the expert's rows.  (By a kernel between the two products
+  // this took 3 us more of every call.)  A warp announces a tile when its next one is done, before
+  // that one's stores, and looks at the answer another tile later: announced at once, the wait
+  // for the stores and for the counter was an eighth of the kernel's time.
+  struct Packing {
+    int stored_a = -1, stored_ks = 0;        // stored, not announced
+    int told_a = -1, told_ks = 0;            // announced, answer not looked at
+    unsigned old = 0;
+  };
+  static BSG_DEV int pack_spt(const Ctx& c) { return (c.p.tiles + kKc / 32 - 1) / (kKc / 32); }
+  static BSG_DEV void pack_look(const Ctx& c, const Lane& L, Packing& k) {
+    if (k.told_a < 0) return;
+    constexpr int kTiles = kKc / 32;
+    const unsigned old = __shfl_sync(0xFFFFFFFFu, k.old, 0);
+    const int need = 4 * min(kTiles, c.p.tiles - k.told_ks * kTiles);
+    if (old == static_cast<unsigned>(need - 1)) pack_rows(c, L, k.told_a, k.told_ks);
+    k.told_a = -1;
+  }
+  static BSG_DEV void pack_tell(const Ctx& c, const Lane& L, Packing& k) {
+    if (k.stored_a < 0) return;
+    __syncwarp();  // the warp's stores before the announcement's release
+    if (L.lane == 0) k.old = atom_add_acq_rel_gpu(c.p.packed + k.stored_a * pack_spt(c) + k.stored_ks, 1u);
+    k.told_a = k.stored_a;
+    k.told_ks = k.stored_ks;
+    k.stored_a = -1;
+  }
+  // Before and after a tile's stores, and at the end of the work.
+  static BSG_DEV void pack_before(const Ctx& c, const Lane& L, Packing& k) {
+    pack_look(c, L, k);
+    pack_tell(c, L, k);
+  }
+  static BSG_DEV void pack_after(Packing& k, int a, int tile) {
+    k.stored_a = a;
+    k.stored_ks = tile / (kKc / 32);
+  }
+  static BSG_DEV void pack_end(const Ctx& c, const Lane& L, Packing& k) {
+    pack_look(c, L, k);
+    pack_tell(c, L, k);
+    pack_look(c, L, k);
+  }
+  static BSG_DEV void pack_rows(const Ctx& c, const Lane& L, int a, int ks) {
+    const MoeGemmParams& p = c.p;
+    __syncwarp();
+    if (L.lane == 0) p.packed[a * pack_spt(c) + ks] = 0u;
+    constexpr int kPer = kKc / 32;
+    const int r0 = c.off(a), m = c.off(a + 1) - r0;
+    const int64_t I = p.out_pitch, k = static_cast<int64_t>(ks) * kKc + L.lane * kPer;
+    const bool in = k < I;
+    float v[2][kPer];  // a row is packed while the next one's values are on their way
+    const auto load = [&](int j, float (&x)[kPer]) {
+      const float4* src = reinterpret_cast<const float4*>(p.h + (r0 + j) * I + (in ? k : 0));
+#pragma unroll
+      for (int i = 0; i < kPer / 4; ++i) {
+        const float4 f = in && j < m ? __ldcg(src + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[4 * i] = f.x;
+        x[4 * i + 1] = f.y;
+        x[4 * i + 2] = f.z;
+        x[4 * i + 3] = f.w;
+      }
+    };
+    load(0, v[0]);
+    for (int j = 0; j < m; j += 2) {
+      load(j + 1, v[1]);
+      uint8_t* dst = p.h_packed + (static_cast<int64_t>(ks) * p.top_rows + r0 + j) * (2 * kPitch);
+      pack_stage<kPer, 2>(v[0], dst, L.lane);
+      if (j + 1 >= m) break;
+      load(j + 2, v[0]);
+      pack_stage<kPer, 2>(v[1], dst + 2 * kPitch, L.lane);
+    }
+  }
+
   // DOWN: add an expert's products to the sums of its tokens (this warp's 16 rows).
   static BSG_DEV void add_sums(const Ctx& c, const Lane& L, int a, const float (&acc)[MT][4]) {
     const int r0 = c.off(a), m = c.off(a + 1) - r0;
@@ -578,7 +712,7 @@ struct MoeGemm {
   // A part of a tile is in the workspace: the last of its blocks to come adds the parts, in block
   // order, and finishes the tile.  (The parts' loads go out eight at a time; one after the other
   // they took longer than the products of a small call.)
-  static BSG_DEV void arrive(const Ctx& c, const Lane& L, int number) {
+  static BSG_DEV void arrive(const Ctx& c, const Lane& L, int number, Packing& k) {
     const int len = tile_len(c), x0 = number * len;
     const int first = owner(c, x0), last = owner(c, x0 + len - 1);
     __syncwarp();
@@ -629,7 +763,9 @@ struct MoeGemm {
         }
       }
       const int a = number / c.p.tiles;
+      pack_before(c, L, k);
       store_h(c, L, a, number - a * c.p.tiles, acc);
+      pack_after(k, a, number - a * c.p.tiles);
     }
   }
 
@@ -644,6 +780,7 @@ struct MoeGemm {
     uint32_t phase = 0;
     bool ok = true;
     Run w = first_run(c);
+    Packing packing;
     int s = c.s0;
     int seg = s;  // DOWN: first stage of the tile segment being summed
     while (true) {
@@ -711,7 +848,7 @@ struct MoeGemm {
           } else {
             float* dst = partial(c, blockIdx.x, seg == x0 ? 1 : 0, cw);
             for (int i = lane; i < p.T * 16; i += 32) __stcg(dst + i, sum[i]);
-            arrive(c, L, w.tile);
+            arrive(c, L, w.tile, packing);
           }
           for (int i = lane; i < p.T * 16; i += 32) sum[i] = 0.f;
           __syncwarp();
@@ -720,18 +857,21 @@ struct MoeGemm {
       } else {
         s += n;
         if (opens && ends) {
+          pack_before(c, L, packing);
           store_h(c, L, w.a, w.tile, acc);
+          pack_after(packing, w.a, w.tile);
         } else {
           float4* dst = reinterpret_cast<float4*>(partial(c, blockIdx.x, opens ? 1 : 0, cw)) + lane;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
             __stcg(dst + mt * 32, make_float4(acc[mt][0], acc[mt][1], acc[mt][2], acc[mt][3]));
-          arrive(c, L, w.a * p.tiles + w.tile);
+          arrive(c, L, w.a * p.tiles + w.tile, packing);
         }
       }
       if (w.left == 0) break;
       next_run(c, w);
     }
+    if constexpr (!DOWN) pack_end(c, L, packing);
     if (!ok && lane == 0) *c.abort_word() = 1u;
   }
 

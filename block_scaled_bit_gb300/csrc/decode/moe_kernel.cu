@@ -78,53 +78,6 @@ BSG_DEV void choose(const MoeParams& p, int t, int lane, int* ids, float* wts, u
 }
 
 // ------------------------------------------------------------------------------ packing
-BSG_DEV uint32_t pack_f16(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-template <int N>
-BSG_DEV void put(uint8_t* dst, const uint32_t (&h)[N]) {
-  if constexpr (N == 4) *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
-  else *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[1]);
-}
-
-// One warp packs one stage of a row, PER consecutive values a lane (see moe_gemm.cuh): the
-// largest finite magnitude scaled into [2^14, 2^15), f16 values (PARTS = 2: and their remainders),
-// the factor that undoes the scale.
-template <int PER, int PARTS>
-BSG_DEV void pack_stage(float (&v)[PER], uint8_t* dst, int lane) {
-  constexpr int kPitch = moe_pitch(PER == 8);
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-    top = max(top, m < 0x7F800000u ? m : 0u);
-  }
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  const int e = min(max(static_cast<int>(top >> 23), 16), 240);  // scale and factor stay normal
-  const float scale = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - e) << 23);
-  if (lane == 0)
-    *reinterpret_cast<float*>(dst + 64 * PER) = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
-  uint32_t hi[PER / 2];
-#pragma unroll
-  for (int i = 0; i < PER / 2; ++i) {
-    v[2 * i] *= scale;
-    v[2 * i + 1] *= scale;
-    hi[i] = pack_f16(v[2 * i], v[2 * i + 1]);
-  }
-  put(dst + lane * (2 * PER), hi);
-  if constexpr (PARTS == 2) {
-    uint32_t lo[PER / 2];
-#pragma unroll
-    for (int i = 0; i < PER / 2; ++i) {
-      const float a = half_to_f32<false>(hi[i], 0), b = half_to_f32<false>(hi[i], 1);
-      lo[i] = pack_f16(isfinite(a) ? v[2 * i] - a : 0.f, isfinite(b) ? v[2 * i + 1] - b : 0.f);
-    }
-    put(dst + kPitch + lane * (2 * PER), lo);
-  }
-}
-
 // Stage `ks` of token t's activations.  (k past the row packs zeros; K is a multiple of 64.)
 template <int PER>
 BSG_DEV void pack_x(const MoeParams& p, int t, int ks, int spt, int lane) {
@@ -147,28 +100,6 @@ BSG_DEV void pack_x(const MoeParams& p, int t, int ks, int spt, int lane) {
 #pragma unroll
   for (int i = 0; i < PER; ++i) v[i] = half_to_f32<true>(raw[i / 2], i & 1);
   pack_stage<PER, 1>(v, dst, lane);
-}
-
-// h packed, one warp per row and stage.
-template <int PER>
-__global__ void __launch_bounds__(256) moe_pack(const __grid_constant__ MoeParams p, int spt) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int unit = blockIdx.x * 8 + (threadIdx.x >> 5), r = unit / spt, ks = unit - r * spt;
-  if (r >= p.route->off[p.route->active]) return;
-  const int64_t k = static_cast<int64_t>(ks) * (32 * PER) + lane * PER;
-  const float4* src = reinterpret_cast<const float4*>(p.h + r * p.I + (k < p.I ? k : 0));
-  float v[PER];
-#pragma unroll
-  for (int i = 0; i < PER / 4; ++i) {
-    const float4 f = k < p.I ? __ldcg(src + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-    v[4 * i] = f.x;
-    v[4 * i + 1] = f.y;
-    v[4 * i + 2] = f.z;
-    v[4 * i + 3] = f.w;
-  }
-  pack_stage<PER, 2>(v, p.h_packed + static_cast<int64_t>(unit) * 2 * moe_pitch(PER == 8), lane);
 }
 
 // Block 0 routes: a warp per token, then a thread per expert.  The other blocks pack x, one warp
@@ -223,14 +154,15 @@ __global__ void __launch_bounds__(1024) moe_route(const __grid_constant__ MoePar
   }
   if (lane == 31) { warp_a[w] = a; warp_r[w] = r; }
   __syncthreads();
-  int base_a = 0, base_r = 0, all_a = 0, all_r = 0;
-  for (int i = 0; i < 32; ++i) {
-    if (i == w) { base_a = all_a; base_r = all_r; }
-    all_a += warp_a[i];
-    all_r += warp_r[i];
+  int sum_a = warp_a[lane], sum_r = warp_r[lane];  // sums over the warps up to `lane`
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int oa = __shfl_up_sync(~0u, sum_a, d), orr = __shfl_up_sync(~0u, sum_r, d);
+    if (lane >= d) { sum_a += oa; sum_r += orr; }
   }
-  a += base_a - (m != 0);
-  r += base_r - __popc(m);
+  const int all_a = __shfl_sync(~0u, sum_a, 31), all_r = __shfl_sync(~0u, sum_r, 31);
+  a += __shfl_sync(~0u, sum_a, w) - warp_a[w] - (m != 0);
+  r += __shfl_sync(~0u, sum_r, w) - warp_r[w] - __popc(m);
   Routing* R = p.route;
   if (m) {
     R->expert[a] = threadIdx.x;
@@ -296,6 +228,8 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
   p.counters = down ? c.counters_down : c.counters_up;
   p.err = c.err;
   p.h = c.h;
+  p.h_packed = c.h_packed;
+  p.packed = c.counters_packed;
   p.y = c.y;
   p.wait_ns = kDefaultWaitNs;
   p.K = w.k;
@@ -347,6 +281,10 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
     smem = at + 1024;  // the ring starts on a 1024-byte boundary
     if (smem <= budget || p.stages == 2) break;
   }
+  // Both products' blocks take the whole budget: blocks of two sizes, coming and going as one
+  // kernel follows the other, left shared memory in pieces that held no block, so that a few of
+  // the 456 or 608 blocks began when others had ended and the kernel took up to twice as long.
+  if (smem < budget) smem = budget;
   const int ctas = sms * blocks_per_sm(c.max_T);
   const int cpb = block_mode(c.fmt, c.bs);
   switch (c.fmt) {
@@ -373,6 +311,7 @@ MoeLayout moe_layout(int fmt, int64_t H, int64_t I, int E, int top_k, int max_T,
   const size_t slot = max_T <= 8 ? 128 : 512;  // floats: up 128 per n8 tile, down 16 max_T
   l.route = take(sizeof(Routing));
   l.counters_up = take(active * (I / 32) * 4 * sizeof(unsigned));
+  l.counters_packed = take(active * (static_cast<size_t>(I) / 128 + 1) * sizeof(unsigned));
   l.counters_down = take(static_cast<size_t>(H / 64) * 4 * sizeof(unsigned));
   l.partials = take(ctas * 2 * 4 * slot * sizeof(float));
   l.h = take(rows * I * sizeof(float));
@@ -397,12 +336,12 @@ int moe_encode(CUtensorMap* tm, const MoeWeight& w, int E, bool up) {
 int launch_moe(const MoeParams& p, int sms, cudaStream_t s) {
   const bool four = p.fmt == kInt4 || p.fmt == kNvfp4;
   const int kc = moe_stage_k(four);
-  const int up = static_cast<int>((p.H + kc - 1) / kc), down = static_cast<int>((p.I + kc - 1) / kc);
-  int rc = decode_launch(moe_route, dim3(1 + (p.T * up + 31) / 32), dim3(1024), 0, s, p, up);
+  const int up = static_cast<int>((p.H + kc - 1) / kc);
+  static AttrRecord rec;
+  int rc = decode_smem(moe_route, rec, 16);  // for the carveout
+  if (rc != BSGEMV_OK) return rc;
+  rc = decode_launch(moe_route, dim3(1 + (p.T * up + 31) / 32), dim3(1024), 0, s, p, up);
   if (rc == BSGEMV_OK) rc = launch_product(p, false, sms, s);
-  if (rc == BSGEMV_OK)
-    rc = decode_launch(four ? moe_pack<8> : moe_pack<4>, dim3((p.T * p.top_k * down + 7) / 8),
-                       dim3(256), 0, s, p, down);
   if (rc == BSGEMV_OK) rc = launch_product(p, true, sms, s);
   return rc;
 }
