@@ -7,13 +7,13 @@
 //
 // Bound: the active experts' weights are read once from HBM (their bytes over the copy bandwidth);
 // a few tokens per expert make the arithmetic small.  So the kernel is a weight stream: a copy
-// warp keeps a ring of 8 KB weight boxes in flight, four warps decode and multiply.
+// warp keeps a ring of 16 KB weight boxes in flight, eight warps decode and multiply.
 //
-// Work.  A tile is 64 weight rows of one expert -- for UP 32 gate rows and the 32 up rows that
+// Work.  A tile is 128 weight rows of one expert -- for UP 64 gate rows and the 64 up rows that
 // belong to them, arranged so that an mma fragment holds a gate row g and its up row g + 8 in the
-// same lane; for DOWN 64 output columns.  A stage is 128 bytes of each of the tile's rows (256 k
-// of the 4-bit formats, 128 of the 8-bit ones).  UP's tiles are (expert, 32 columns) over k = H;
-// DOWN's are 64 columns over all experts' k = I in turn, so that an output is summed in one
+// same lane; for DOWN 128 output columns.  A stage is 128 bytes of each of the tile's rows (256 k
+// of the 4-bit formats, 128 of the 8-bit ones).  UP's tiles are (expert, 64 columns) over k = H;
+// DOWN's are 128 columns over all experts' k = I in turn, so that an output is summed in one
 // place.  All stages are cut into equal ranges, one per block; a tile cut by a range boundary is
 // finished by the last block to arrive, which adds the parts in block order (deterministic).
 //
@@ -54,13 +54,14 @@ BSG_DEV void tma_load_4d_hint(uint32_t dst, const CUtensorMap* tm, int x, int y,
       : "memory");
 }
 
-constexpr int kMoeThreads = 160;  // copy warp, four decode warps
-constexpr int kMoeTileRows = 64;
+constexpr int kMoeWarps = 8;                          // decode warps
+constexpr int kMoeThreads = 32 * (kMoeWarps + 1);     // and a copy warp
+constexpr int kMoeTileRows = 16 * kMoeWarps;
 constexpr int kMoeBoxB = kMoeTileRows * 128;
 
 struct MoeGemmParams {
-  CUtensorMap tm;             // weight bytes, a box is a tile's 64 rows x 128 bytes, 128B swizzle:
-                              // UP [E][2][I][row bytes], box [2][32][128]; DOWN [E][1][H][...], [64]
+  CUtensorMap tm;             // weight bytes, a box is a tile's 128 rows x 128 bytes, 128B swizzle:
+                              // UP [E][2][I][row bytes], box [2][64][128]; DOWN [E][1][H][...], [128]
   const uint8_t* x;           // packed activations: UP [token][stage][row bytes], DOWN
                               // [stage][row][row bytes] (an expert's rows of a stage are adjacent)
   const Routing* route;
@@ -78,7 +79,7 @@ struct MoeGemmParams {
   int64_t s_pitch, z_pitch;   // bytes per weight row
   int64_t out_pitch;
   int rows;                   // weight rows of an expert
-  int second;                 // row distance of a tile's second 32 rows
+  int second;                 // row distance of a tile's second half
   int step;                   // row distance of two tiles
   int tiles, spt;             // tiles of an expert, stages of a tile's k
   int T, top_rows;            // tokens; routing rows a call can have
@@ -218,26 +219,29 @@ struct MoeGemm {
   static BSG_DEV int rows_of(const Ctx& c, int a) { return c.off(a + 1) - c.off(a); }
   static BSG_DEV int wrap(const Ctx& c, int r) { return r >= c.p.row_cap ? r - c.p.row_cap : r; }
 
-  // Scales (or zero points) of this lane's two rows of a tile, lane and lane + 32.  Where every
+  // Scales (or zero points) of this lane's four rows of a tile, lane + 32 h.  Where every
   // row's part of a stage is 4, 8, 16 or twice 16 bytes on such a boundary (`unit`), it is one copy
   // a row (two); else (unit 0, or a tile with the array's last rows) the whole words that hold it
   // are copied, nothing at or past `end`, and the reader adds the start's low two bits.
   struct Side {
-    const uint8_t* src[2];  // the row's part of the run's next stage
+    const uint8_t* src;     // row `lane`'s part of the run's next stage
+    int64_t next, half;     // to row lane + 32, to row lane + 64
     const uint8_t* end;
     int unit, stride, bytes;
-    bool edge;
+    bool edge;              // the tile has the array's last rows
+    BSG_DEV const uint8_t* row(int h) const { return src + (h & 1 ? next : 0) + (h & 2 ? half : 0); }
   };
   static BSG_DEV Side side_of(const uint8_t* src, int64_t pitch, int64_t end, int unit, int stride,
                               int bytes, const Run& w, int row, int second, int lane) {
     Side s;
-    s.src[0] = src + (row + lane) * pitch + w.ks * bytes;
-    s.src[1] = s.src[0] + second * pitch;
+    s.src = src + (row + lane) * pitch + w.ks * bytes;
+    s.next = 32 * pitch;
+    s.half = second * pitch;
     s.end = src + end;
     s.unit = unit;
     s.stride = stride;
     s.bytes = bytes;
-    s.edge = src + (static_cast<int64_t>(row) + second + 31) * pitch + (w.ks + w.n) * bytes + 4 > s.end;
+    s.edge = src + (static_cast<int64_t>(row) + second + 63) * pitch + (w.ks + w.n) * bytes + 4 > s.end;
     return s;
   }
   template <int UNIT>
@@ -252,45 +256,45 @@ struct MoeGemm {
   }
   static BSG_DEV void side_copy(Side& s, uint32_t dst, int lane) {
     const uint32_t to = dst + lane * s.stride;
-    if (s.unit == 16 && !s.edge) {
-      cp_unit<16>(to, s.src[0], 16);
-      cp_unit<16>(to + 32 * s.stride, s.src[1], 16);
-      if (s.bytes == 32) {
-        cp_unit<16>(to + 16, s.src[0] + 16, 16);
-        cp_unit<16>(to + 32 * s.stride + 16, s.src[1] + 16, 16);
-      }
-    } else if (s.unit == 8 && !s.edge) {
-      cp_unit<8>(to, s.src[0], 8);
-      cp_unit<8>(to + 32 * s.stride, s.src[1], 8);
-    } else if (s.unit == 4 && !s.edge) {
-      cp_unit<4>(to, s.src[0], 4);
-      cp_unit<4>(to + 32 * s.stride, s.src[1], 4);
-    } else if (!s.edge) {
+    // (only the lanes whose own rows come near the end go word by word)
+    if (s.edge && s.row(3) + s.bytes + 8 > s.end) {
+      side_words(s, to);
+    } else if (s.unit == 16) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint8_t* src = s.src[h] - (reinterpret_cast<uintptr_t>(s.src[h]) & 3);
-        const uint32_t at = to + h * 32 * s.stride;
+      for (int h = 0; h < 4; ++h) cp_unit<16>(to + 32 * h * s.stride, s.row(h), 16);
+      if (s.bytes == 32)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) cp_unit<16>(to + 32 * h * s.stride + 16, s.row(h) + 16, 16);
+    } else if (s.unit == 8) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) cp_unit<8>(to + 32 * h * s.stride, s.row(h), 8);
+    } else if (s.unit == 4) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) cp_unit<4>(to + 32 * h * s.stride, s.row(h), 4);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const uint8_t* src = s.row(h) - (reinterpret_cast<uintptr_t>(s.row(h)) & 3);
+        const uint32_t at = to + 32 * h * s.stride;
         cp_unit<4>(at, src, 4);
 #pragma unroll
-        for (int i = 1; i < 9; ++i)
+        for (int i = 1; i < 5; ++i)
           if (4 * i < s.stride) cp_unit<4>(at + 4 * i, src + 4 * i, 4);
+        for (int i = 20; i < s.stride; i += 4) cp_unit<4>(at + i, src + i, 4);
       }
-    } else {
-      side_words(s, to);
     }
-    s.src[0] += s.bytes;
-    s.src[1] += s.bytes;
+    s.src += s.bytes;
   }
   static __device__ __noinline__ void side_words(const Side& s, uint32_t to) {
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      const uint8_t* src = s.src[h] - (reinterpret_cast<uintptr_t>(s.src[h]) & 3);
+    for (int h = 0; h < 4; ++h) {
+      const uint8_t* src = s.row(h) - (reinterpret_cast<uintptr_t>(s.row(h)) & 3);
       for (int i = 0; i < s.stride; i += 4) {
         const int64_t left = s.end - (src + i);
         const int have = left >= 4 ? 4 : (left > 0 ? static_cast<int>(left) : 0);
         // (nothing to read: any address of the array will do)
         const uint8_t* none = s.end - 4 - (reinterpret_cast<uintptr_t>(s.end) & 3);
-        cp_unit<4>(to + h * 32 * s.stride + i, have ? src + i : none, have);
+        cp_unit<4>(to + 32 * h * s.stride + i, have ? src + i : none, have);
       }
     }
   }
@@ -306,14 +310,16 @@ struct MoeGemm {
     x.e = c.expert(w.a);
     x.row = w.tile * p.step;
     const int row = weight_row(c, w);
-    x.s = side_of(p.scales, p.s_pitch, p.s_end, p.s_unit, p.s_stride, p.s_bytes, w, row, p.second, lane);
+    // (where DOWN's last tile is half empty, its first half's scales again)
+    const int second = DOWN && x.row + 64 >= p.rows ? 0 : p.second;
+    x.s = side_of(p.scales, p.s_pitch, p.s_end, p.s_unit, p.s_stride, p.s_bytes, w, row, second, lane);
     if (kInts && p.zp)
-      x.z = side_of(p.zp, p.z_pitch, p.z_end, p.z_unit, p.z_stride, p.z_bytes, w, row, p.second, lane);
+      x.z = side_of(p.zp, p.z_pitch, p.z_end, p.z_unit, p.z_stride, p.z_bytes, w, row, second, lane);
     return x;
   }
   static BSG_DEV void issue_weights(const Ctx& c, Weights& x, int ks, int slot, uint64_t pol,
                                     int lane) {
-    // one box: 64 rows, or 32 gate rows and the up rows that belong to them
+    // one box: 128 rows, or 64 gate rows and the up rows that belong to them
     if (lane == 0)
       tma_load_4d_hint(c.base_u + slot * kMoeBoxB, &c.p.tm, ks * 128, x.row, 0, x.e, c.full(slot), pol);
     const uint32_t side = c.base_u + c.p.off_side + slot * c.p.side_bytes;
@@ -379,12 +385,8 @@ struct MoeGemm {
         if (i >= early) {
           issue_weights(c, x, w.ks + k, slot, pol, lane);
         } else {
-          x.s.src[0] += x.s.bytes;
-          x.s.src[1] += x.s.bytes;
-          if (kInts && p.zp) {
-            x.z.src[0] += x.z.bytes;
-            x.z.src[1] += x.z.bytes;
-          }
+          x.s.src += x.s.bytes;
+          if (kInts && p.zp) x.z.src += x.z.bytes;
         }
         if constexpr (DOWN) {
           const int here = min(m, p.row_cap - head);
@@ -420,7 +422,7 @@ struct MoeGemm {
 
   // ---------------------------------------------------------------- decode warps
   // Rows g and g + 8 of decode warp cw's fragment in the tile.
-  static BSG_DEV int tile_row(int cw, int half) { return DOWN ? 16 * cw + 8 * half : 8 * cw + 32 * half; }
+  static BSG_DEV int tile_row(int cw, int half) { return DOWN ? 16 * cw + 8 * half : 8 * cw + 64 * half; }
 
   struct Lane {
     int cw, lane, g, t;
@@ -585,7 +587,7 @@ struct MoeGemm {
     const MoeGemmParams& p = c.p;
     const int r0 = c.off(a), m = c.off(a + 1) - r0;
     const float gs = kFold ? p.gscale[c.expert(a)] : 1.f;
-    const int64_t col = static_cast<int64_t>(tile) * 32 + 8 * L.cw + L.g;
+    const int64_t col = static_cast<int64_t>(tile) * 64 + 8 * L.cw + L.g;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -597,8 +599,8 @@ struct MoeGemm {
       }
   }
 
-  // UP: packing.  The last warp to store into a stage of DOWN's k (of kKc columns: 8 or 4 tiles of
-  // four warps) packs that stage of the expert's rows.  (By a kernel between the two products
+  // UP: packing.  The last warp to store into a stage of DOWN's k (of kKc columns: 4 or 2 tiles of
+  // eight warps) packs that stage of the expert's rows.  (By a kernel between the two products
   // this took 3 us more of every call.)  A warp announces a tile when its next one is done, before
   // that one's stores, and looks at the answer another tile later: announced at once, the wait
   // for the stores and for the counter was an eighth of the kernel's time.
@@ -607,12 +609,12 @@ struct MoeGemm {
     int told_a = -1, told_ks = 0;            // announced, answer not looked at
     unsigned old = 0;
   };
-  static BSG_DEV int pack_spt(const Ctx& c) { return (c.p.tiles + kKc / 32 - 1) / (kKc / 32); }
+  static BSG_DEV int pack_spt(const Ctx& c) { return (c.p.tiles + kKc / 64 - 1) / (kKc / 64); }
   static BSG_DEV void pack_look(const Ctx& c, const Lane& L, Packing& k) {
     if (k.told_a < 0) return;
-    constexpr int kTiles = kKc / 32;
+    constexpr int kTiles = kKc / 64;
     const unsigned old = __shfl_sync(0xFFFFFFFFu, k.old, 0);
-    const int need = 4 * min(kTiles, c.p.tiles - k.told_ks * kTiles);
+    const int need = kMoeWarps * min(kTiles, c.p.tiles - k.told_ks * kTiles);
     if (old == static_cast<unsigned>(need - 1)) pack_rows(c, L, k.told_a, k.told_ks);
     k.told_a = -1;
   }
@@ -631,7 +633,7 @@ struct MoeGemm {
   }
   static BSG_DEV void pack_after(Packing& k, int a, int tile) {
     k.stored_a = a;
-    k.stored_ks = tile / (kKc / 32);
+    k.stored_ks = tile / (kKc / 64);
   }
   static BSG_DEV void pack_end(const Ctx& c, const Lane& L, Packing& k) {
     pack_look(c, L, k);
@@ -690,7 +692,9 @@ struct MoeGemm {
   static BSG_DEV void store_y(const Ctx& c, int cw, int tile, int idx, float v) {
     const int t = idx >> 4;
     if ((c.p.route->nan_rows >> t) & 1u) v = __int_as_float(0x7FC00000);
-    const int64_t at = t * c.p.out_pitch + static_cast<int64_t>(tile) * 64 + 16 * cw + (idx & 15);
+    const int64_t n = static_cast<int64_t>(tile) * kMoeTileRows + 16 * cw + (idx & 15);
+    if (n >= c.p.out_pitch) return;  // (H is a multiple of 64: the last tile may be half empty)
+    const int64_t at = t * c.p.out_pitch + n;
     c.p.y[at] = c.p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v))
                          : __half_as_ushort(__float2half_rn(v));
   }
@@ -706,7 +710,7 @@ struct MoeGemm {
   static BSG_DEV int tile_len(const Ctx& c) { return DOWN ? c.active * c.p.spt : c.p.spt; }
 
   static BSG_DEV float* partial(const Ctx& c, int block, int which, int cw) {
-    return c.p.partials + ((static_cast<int64_t>(block) * 2 + which) * 4 + cw) * c.p.slot_floats;
+    return c.p.partials + ((static_cast<int64_t>(block) * 2 + which) * kMoeWarps + cw) * c.p.slot_floats;
   }
 
   // A part of a tile is in the workspace: the last of its blocks to come adds the parts, in block
@@ -717,13 +721,13 @@ struct MoeGemm {
     const int first = owner(c, x0), last = owner(c, x0 + len - 1);
     __syncwarp();
     unsigned old = 0;
-    if (L.lane == 0) old = atom_add_acq_rel_gpu(c.p.counters + number * 4 + L.cw, 1u);
+    if (L.lane == 0) old = atom_add_acq_rel_gpu(c.p.counters + number * kMoeWarps + L.cw, 1u);
     old = __shfl_sync(0xFFFFFFFFu, old, 0);
     if (old != static_cast<unsigned>(last - first)) return;
     __syncwarp();
-    if (L.lane == 0) c.p.counters[number * 4 + L.cw] = 0u;
+    if (L.lane == 0) c.p.counters[number * kMoeWarps + L.cw] = 0u;
     // the first block's part opens the tile, the others' continue it
-    const int64_t stride = static_cast<int64_t>(c.p.slot_floats) * 8;  // of two blocks
+    const int64_t stride = static_cast<int64_t>(c.p.slot_floats) * (2 * kMoeWarps);  // of two blocks
     const float* src0 = partial(c, first, 1, L.cw);
     const float* src = partial(c, first, 0, L.cw);  // + (b - first) * stride
     const int n = last - first + 1;
@@ -796,7 +800,7 @@ struct MoeGemm {
         const uint32_t row = static_cast<uint32_t>(weight_row(c, w));
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
-          const uint32_t r = tile_row(cw, rr) + L.g, at = row + (r < 32 ? r : p.second + r - 32);
+          const uint32_t r = tile_row(cw, rr) + L.g, at = row + (r < 64 ? r : p.second + r - 64);
           sw[rr] = at * static_cast<uint32_t>(p.s_pitch);
           zw[rr] = at * static_cast<uint32_t>(p.z_pitch);
         }
@@ -883,7 +887,7 @@ struct MoeGemm {
     if (threadIdx.x == 0) {
       for (int i = 0; i < p.stages; ++i) {
         mbar_init(c.full(i), 1);
-        mbar_init(c.empty(i), 4);
+        mbar_init(c.empty(i), kMoeWarps);
       }
       *c.abort_word() = 0u;
       fence_mbar_init();
@@ -928,7 +932,7 @@ struct MoeGemm {
 };
 
 template <int FMT, int MT, bool DOWN, int CPB>
-__global__ void __launch_bounds__(kMoeThreads, MT == 1 ? 4 : 3)
+__global__ void __launch_bounds__(kMoeThreads, 2)
     moe_gemm_kernel(const __grid_constant__ MoeGemmParams p) {
   MoeGemm<FMT, MT, DOWN, CPB>::block(p);
 }

@@ -189,8 +189,7 @@ __global__ void __launch_bounds__(1024) moe_route(const __grid_constant__ MoePar
 // ------------------------------------------------------------------------------ launches
 namespace {
 
-// Blocks per SM: one n8 tile of tokens or four (more accumulators, more activation rows).
-int blocks_per_sm(int max_T) { return max_T <= 8 ? 4 : 3; }
+constexpr int kBlocksPerSm = 2;
 
 constexpr int kSmemPerSm = 233472;  // 228 KB, of which each block takes 1 KB for itself
 
@@ -239,9 +238,9 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
   p.s_pitch = w.scale_pitch;
   p.z_pitch = w.zp_pitch;
   p.out_pitch = down ? c.H : c.I;
-  p.second = down ? 32 : static_cast<int>(c.I);
-  p.step = down ? 64 : 32;
-  p.tiles = static_cast<int>(down ? c.H / 64 : c.I / 32);
+  p.second = down ? 64 : static_cast<int>(c.I);
+  p.step = down ? kMoeTileRows : 64;
+  p.tiles = static_cast<int>(down ? (c.H + kMoeTileRows - 1) / kMoeTileRows : c.I / 64);
   const int kc = moe_stage_k(four);
   p.spt = static_cast<int>((w.k + kc - 1) / kc);
   p.T = c.T;
@@ -259,7 +258,7 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
   }
   p.side_bytes = align_up(kMoeTileRows * (p.s_stride + p.z_stride), 16);
   const int row_bytes = moe_pitch(four) * (down ? 2 : 1);
-  const int budget = kSmemPerSm / blocks_per_sm(c.max_T) - 1024;
+  const int budget = kSmemPerSm / kBlocksPerSm - 1024;
   const int route_bytes = align_up((4 * p.top_rows + 1) * 4, 16);
   p.slot_floats = down ? c.max_T * 16 : (wide ? 4 : 1) * 128;
   const int rows = usual_rows(c);
@@ -277,15 +276,15 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
     p.off_bar = at;
     at += align_up(16 * p.stages + 8, 16);
     p.off_sum = at;
-    at += down ? 4 * c.T * 16 * 4 : 0;
+    at += down ? kMoeWarps * c.T * 16 * 4 : 0;
     smem = at + 1024;  // the ring starts on a 1024-byte boundary
     if (smem <= budget || p.stages == 2) break;
   }
   // Both products' blocks take the whole budget: blocks of two sizes, coming and going as one
   // kernel follows the other, left shared memory in pieces that held no block, so that a few of
-  // the 456 or 608 blocks began when others had ended and the kernel took up to twice as long.
+  // the blocks began when others had ended and the kernel took up to twice as long.
   if (smem < budget) smem = budget;
-  const int ctas = sms * blocks_per_sm(c.max_T);
+  const int ctas = sms * kBlocksPerSm;
   const int cpb = block_mode(c.fmt, c.bs);
   switch (c.fmt) {
     case kInt4: return launch_moe_int4(p, cpb, wide, down, ctas, smem, s);
@@ -307,13 +306,13 @@ MoeLayout moe_layout(int fmt, int64_t H, int64_t I, int E, int top_k, int max_T,
   };
   const size_t rows = static_cast<size_t>(max_T) * top_k;
   const size_t active = rows < static_cast<size_t>(E) ? rows : static_cast<size_t>(E);
-  const size_t ctas = static_cast<size_t>(sms) * blocks_per_sm(max_T);
+  const size_t ctas = static_cast<size_t>(sms) * kBlocksPerSm;
   const size_t slot = max_T <= 8 ? 128 : 512;  // floats: up 128 per n8 tile, down 16 max_T
   l.route = take(sizeof(Routing));
-  l.counters_up = take(active * (I / 32) * 4 * sizeof(unsigned));
+  l.counters_up = take(active * (I / 64) * kMoeWarps * sizeof(unsigned));
   l.counters_packed = take(active * (static_cast<size_t>(I) / 128 + 1) * sizeof(unsigned));
-  l.counters_down = take(static_cast<size_t>(H / 64) * 4 * sizeof(unsigned));
-  l.partials = take(ctas * 2 * 4 * slot * sizeof(float));
+  l.counters_down = take(static_cast<size_t>(H / 64) * kMoeWarps * sizeof(unsigned));
+  l.partials = take(ctas * 2 * kMoeWarps * slot * sizeof(float));
   l.h = take(rows * I * sizeof(float));
   const bool four = fmt == kInt4 || fmt == kNvfp4;
   const size_t kc = moe_stage_k(four), pitch = moe_pitch(four);
@@ -328,7 +327,7 @@ int moe_encode(CUtensorMap* tm, const MoeWeight& w, int E, bool up) {
   const uint64_t bytes = static_cast<uint64_t>(w.row_bytes);
   const uint64_t dims[4] = {bytes, rows, parts, static_cast<uint64_t>(E)};
   const uint64_t strides[3] = {bytes, bytes * rows, bytes * rows * parts};
-  const uint32_t box[4] = {128, up ? 32u : 64u, up ? 2u : 1u, 1};
+  const uint32_t box[4] = {128, up ? 64u : 128u, up ? 2u : 1u, 1};
   return decode_encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, w.W, dims, strides, box,
                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }

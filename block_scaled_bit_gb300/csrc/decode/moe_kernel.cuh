@@ -88,7 +88,7 @@ MoeLayout moe_layout(int fmt, int64_t H, int64_t I, int E, int top_k, int max_T,
 inline int64_t moe_stages(int fmt, int64_t H, int64_t I, int E, int top_k, int max_T) {
   const int64_t kc = moe_stage_k(fmt == kInt4 || fmt == kNvfp4);
   const int64_t active = E < top_k * max_T ? E : top_k * max_T;
-  const int64_t up = (I / 32) * ((H + kc - 1) / kc), down = (H / 64) * ((I + kc - 1) / kc);
+  const int64_t up = (I / 64) * ((H + kc - 1) / kc), down = (H + 127) / 128 * ((I + kc - 1) / kc);
   return active * (up > down ? up : down);
 }
 
