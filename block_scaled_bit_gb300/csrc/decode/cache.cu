@@ -7,6 +7,7 @@
 // of a page is made by one block in index order).
 #include <new>
 
+#include "../bsgemv_kernel.cuh"
 #include "decode_internal.h"
 
 struct bsgemv_cache_s {
@@ -20,6 +21,7 @@ namespace bsg {
 namespace {
 
 constexpr int kScan = 1024;  // threads of the block that picks pages
+constexpr int kCopyThreads = 256;
 
 // Everything a cache kernel needs.  `want`, `src`, `dst` are per-entry lists of the workspace,
 // `rows` a snapshot of table rows, `map` the page renaming of a compaction.
@@ -83,12 +85,22 @@ __device__ int block_scan(int v, int* sum) {
 // atomics changed them).
 __device__ int take_pages(const CacheParams& p, const int32_t* list, int count) {
   int given = 0;
-  for (int base = 0; base < p.num_pages && given < count; base += kScan) {
-    const int page = base + threadIdx.x;
-    const int free = page < p.num_pages && __ldcg(p.refs + page) == 0;
-    int sum;
-    const int r = given + block_scan(free, &sum);
-    if (free && r < count) p.got[list[r]] = page;
+  for (int base = 0; base < p.num_pages && given < count; base += 4 * kScan) {
+    const int page = base + 4 * threadIdx.x;
+    bool free[4];
+    int mine = 0, sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      free[i] = page + i < p.num_pages && __ldcg(p.refs + page + i) == 0;
+      mine += free[i];
+    }
+    int r = given + block_scan(mine, &sum);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (free[i]) {
+        if (r < count) p.got[list[r]] = page + i;
+        ++r;
+      }
     given += sum;
   }
   __syncthreads();
@@ -100,6 +112,8 @@ __device__ int take_pages(const CacheParams& p, const int32_t* list, int count) 
 // (so that it is not taken below), the child's old pages released.  The last block to arrive
 // then gives each entry that copies the lowest free pages in entry order.
 __global__ void __launch_bounds__(kScan) fork_refs(CacheParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int i = blockIdx.x;
   const int par = p.a[i], kid = p.b[i];
   const bool on = par >= 0 && par < p.max_seqs && kid >= 0 && kid < p.max_seqs && par != kid;
@@ -179,7 +193,6 @@ __global__ void __launch_bounds__(kScan) fork_refs(CacheParams p) {
 // Copy every page of the list in every plane: the list's pages x planes are cut into pieces of
 // kPiece bytes, dealt to the blocks in turn.  The call is bound by HBM: each byte is read and
 // written once, four 16-byte loads in flight per thread.
-constexpr int kCopyThreads = 256;
 constexpr int kPiece = kCopyThreads * 16 * 4;
 
 __device__ void copy_pages(const CacheParams& p, int count) {
@@ -209,11 +222,15 @@ __device__ void copy_pages(const CacheParams& p, int count) {
 }
 
 __global__ void __launch_bounds__(kCopyThreads) copy_list(CacheParams p, int count) {
+  pdl_launch_dependents();
+  pdl_wait();
   copy_pages(p, count);
 }
 
 // Fork, second kernel: the children's rows and lengths, and the copied pages.
 __global__ void __launch_bounds__(kCopyThreads) fork_finish(CacheParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
   for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
     const int len = p.len[i];
     if (len < 0) {
@@ -233,7 +250,9 @@ __global__ void __launch_bounds__(kCopyThreads) fork_finish(CacheParams p) {
   copy_pages(p, *p.copies);
 }
 
-__global__ void free_seqs(CacheParams p) {
+__global__ void __launch_bounds__(kCopyThreads) free_seqs(CacheParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int s = p.a[blockIdx.x];
   if (s < 0 || s >= p.max_seqs) return;
   int32_t* row = p.tables + static_cast<int64_t>(s) * p.max_pages;
@@ -248,6 +267,8 @@ __global__ void free_seqs(CacheParams p) {
 
 // Extend, first kernel (one block): which sequences need a page, the pages, the new state.
 __global__ void __launch_bounds__(kScan) extend_rows(CacheParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
   int want = 0;
   for (int base = 0; base < p.n; base += kScan) {
     const int e = base + threadIdx.x;
@@ -313,6 +334,8 @@ __global__ void __launch_bounds__(kScan) extend_rows(CacheParams p) {
 }
 
 __global__ void __launch_bounds__(kCopyThreads) extend_copy(CacheParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
   copy_pages(p, *p.copies);
 }
 
@@ -323,7 +346,9 @@ struct WriteParams {
 };
 
 // One block per sequence: its token's heads x D elements of K and of V, 8 at a time.
-__global__ void write_token(CacheParams p, WriteParams w) {
+__global__ void __launch_bounds__(kCopyThreads) write_token(CacheParams p, WriteParams w) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int s = p.a[blockIdx.x];
   if (s < 0 || s >= p.max_seqs) return;
   const int at = p.lens[s] - 1;
@@ -346,30 +371,37 @@ __global__ void write_token(CacheParams p, WriteParams w) {
 // order, the renaming and the new reference counts.
 __global__ void __launch_bounds__(kScan)
     compact_plan(CacheParams p, const int32_t* refs, int32_t* refs_out, int32_t* live_out) {
-  int live = 0;
-  for (int base = 0; base < p.num_pages; base += kScan) {
-    const int page = base + threadIdx.x;
-    int sum;
-    block_scan(page < p.num_pages && refs[page] > 0, &sum);
-    live += sum;
-  }
+  pdl_launch_dependents();
+  pdl_wait();
+  // (four pages a thread and scan; holes and movers share one: a hole counts 1, a mover 2^16 --
+  // at most 4096 of either in a step)
+  int mine = 0, live;
+  for (int page = threadIdx.x; page < p.num_pages; page += kScan) mine += refs[page] > 0;
+  block_scan(mine, &live);
   int holes = 0, movers = 0;
-  for (int base = 0; base < p.num_pages; base += kScan) {
-    const int page = base + threadIdx.x;
-    const int count = page < p.num_pages ? refs[page] : 0;
-    const int hole = page < live && page < p.num_pages && count <= 0;
-    const int mover = page >= live && count > 0;
-    int sum;
-    int r = holes + block_scan(hole, &sum);
-    if (hole) p.dst[r] = page;
-    holes += sum;
-    r = movers + block_scan(mover, &sum);
-    if (mover) p.src[r] = page;
-    movers += sum;
-    if (page < p.num_pages) {
-      p.map[page] = page;
-      refs_out[page] = count;
+  for (int base = 0; base < p.num_pages; base += 4 * kScan) {
+    const int page = base + 4 * threadIdx.x;
+    int count[4], kinds = 0, sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      count[i] = page + i < p.num_pages ? refs[page + i] : 0;
+      const bool inside = page + i < p.num_pages;
+      kinds += (inside && page + i < live && count[i] <= 0) ? 1 : 0;
+      kinds += (inside && page + i >= live && count[i] > 0) ? 1 << 16 : 0;
     }
+    const int before = block_scan(kinds, &sum);
+    int h = holes + (before & 0xFFFF), m = movers + (before >> 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = page + i;
+      if (at >= p.num_pages) break;
+      if (at < live && count[i] <= 0) p.dst[h++] = at;
+      if (at >= live && count[i] > 0) p.src[m++] = at;
+      p.map[at] = at;
+      refs_out[at] = count[i];
+    }
+    holes += sum & 0xFFFF;
+    movers += sum >> 16;
   }
   __syncthreads();
   for (int r = threadIdx.x; r < movers; r += blockDim.x) {
@@ -387,6 +419,8 @@ __global__ void __launch_bounds__(kScan)
 // Compaction, second kernel: the tables renamed, the pages moved.
 __global__ void __launch_bounds__(kCopyThreads)
     compact_move(CacheParams p, const int32_t* tables, int32_t* tables_out) {
+  pdl_launch_dependents();
+  pdl_wait();
   for (int s = blockIdx.x; s < p.max_seqs; s += gridDim.x) {
     const int held = (clamp_len(p.lens[s], p) + p.page_size - 1) / p.page_size;
     const int64_t at = static_cast<int64_t>(s) * p.max_pages;
@@ -487,13 +521,13 @@ int bsgemv_cache_copy(bsgemv_cache_t c, void* pool, const int32_t* src, const in
   if (!pool || !src || !dst) return BSGEMV_ERR_INVALID_ARG;
   if (!aligned_to(pool, 16) || !aligned_to(src, 4) || !aligned_to(dst, 4))
     return BSGEMV_ERR_MISALIGNED;
-  const int rc = decode_check_device(c->device);
+  int rc = decode_check_device(c->device);
   if (rc != BSGEMV_OK) return rc;
   CacheParams p = params_of(c, pool, n);
   p.src = const_cast<int32_t*>(src);
   p.dst = const_cast<int32_t*>(dst);
-  copy_list<<<copy_grid(c, n, 0), kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(p, n);
-  return decode_launched();
+  return decode_launch(copy_list, dim3(copy_grid(c, n, 0)), dim3(kCopyThreads), 0,
+                       static_cast<cudaStream_t>(stream), p, n);
 }
 
 int bsgemv_cache_fork(bsgemv_cache_t c, void* pool, int32_t* refs, int32_t* tables, int32_t* lens,
@@ -506,7 +540,7 @@ int bsgemv_cache_fork(bsgemv_cache_t c, void* pool, int32_t* refs, int32_t* tabl
       !aligned_to(lens, 4) || !aligned_to(parents, 4) || !aligned_to(children, 4) ||
       !aligned_to(new_pages, 4))
     return BSGEMV_ERR_MISALIGNED;
-  const int rc = decode_check_device(c->device);
+  int rc = decode_check_device(c->device);
   if (rc != BSGEMV_OK) return rc;
   CacheParams p = params_of(c, pool, n);
   p.refs = refs;
@@ -516,9 +550,9 @@ int bsgemv_cache_fork(bsgemv_cache_t c, void* pool, int32_t* refs, int32_t* tabl
   p.b = children;
   p.note = new_pages;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  fork_refs<<<n, kScan, 0, s>>>(p);
-  fork_finish<<<copy_grid(c, n, n), kCopyThreads, 0, s>>>(p);
-  return decode_launched();
+  rc = decode_launch(fork_refs, dim3(n), dim3(kScan), 0, s, p);
+  if (rc != BSGEMV_OK) return rc;
+  return decode_launch(fork_finish, dim3(copy_grid(c, n, n)), dim3(kCopyThreads), 0, s, p);
 }
 
 int bsgemv_cache_free(bsgemv_cache_t c, int32_t* refs, int32_t* tables, int32_t* lens,
@@ -529,15 +563,15 @@ int bsgemv_cache_free(bsgemv_cache_t c, int32_t* refs, int32_t* tables, int32_t*
   if (!aligned_to(refs, 4) || !aligned_to(tables, 4) || !aligned_to(lens, 4) ||
       !aligned_to(seqs, 4))
     return BSGEMV_ERR_MISALIGNED;
-  const int rc = decode_check_device(c->device);
+  int rc = decode_check_device(c->device);
   if (rc != BSGEMV_OK) return rc;
   CacheParams p = params_of(c, nullptr, n);
   p.refs = refs;
   p.tables = tables;
   p.lens = lens;
   p.a = seqs;
-  free_seqs<<<n, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return decode_launched();
+  return decode_launch(free_seqs, dim3(n), dim3(kCopyThreads), 0, static_cast<cudaStream_t>(stream),
+                       p);
 }
 
 int bsgemv_cache_extend(bsgemv_cache_t c, void* pool, int32_t* refs, int32_t* tables,
@@ -548,7 +582,7 @@ int bsgemv_cache_extend(bsgemv_cache_t c, void* pool, int32_t* refs, int32_t* ta
   if (!aligned_to(pool, 16) || !aligned_to(refs, 4) || !aligned_to(tables, 4) ||
       !aligned_to(lens, 4) || !aligned_to(seqs, 4) || !aligned_to(grown, 4))
     return BSGEMV_ERR_MISALIGNED;
-  const int rc = decode_check_device(c->device);
+  int rc = decode_check_device(c->device);
   if (rc != BSGEMV_OK) return rc;
   CacheParams p = params_of(c, pool, n);
   p.refs = refs;
@@ -557,9 +591,9 @@ int bsgemv_cache_extend(bsgemv_cache_t c, void* pool, int32_t* refs, int32_t* ta
   p.a = seqs;
   p.note = grown;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  extend_rows<<<1, kScan, 0, s>>>(p);
-  extend_copy<<<copy_grid(c, n, 0), kCopyThreads, 0, s>>>(p);
-  return decode_launched();
+  rc = decode_launch(extend_rows, dim3(1), dim3(kScan), 0, s, p);
+  if (rc != BSGEMV_OK) return rc;
+  return decode_launch(extend_copy, dim3(copy_grid(c, n, 0)), dim3(kCopyThreads), 0, s, p);
 }
 
 int bsgemv_cache_write(bsgemv_cache_t c, void* pool, const int32_t* tables, const int32_t* lens,
@@ -580,7 +614,7 @@ int bsgemv_cache_write(bsgemv_cache_t c, void* pool, const int32_t* tables, cons
   if (head_stride >= c->page_bytes || row_stride >= c->page_bytes) return BSGEMV_ERR_INVALID_ARG;
   if (2 * ((heads - 1) * head_stride + (c->page_size - 1) * row_stride + D) > c->page_bytes)
     return BSGEMV_ERR_INVALID_ARG;
-  const int rc = decode_check_device(c->device);
+  int rc = decode_check_device(c->device);
   if (rc != BSGEMV_OK) return rc;
   CacheParams p = params_of(c, pool, n);
   p.tables = const_cast<int32_t*>(tables);
@@ -588,8 +622,8 @@ int bsgemv_cache_write(bsgemv_cache_t c, void* pool, const int32_t* tables, cons
   p.a = seqs;
   const WriteParams w = {static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                          kv_stride, head_stride, row_stride, heads, D, k_plane, v_plane};
-  write_token<<<n, 256, 0, static_cast<cudaStream_t>(stream)>>>(p, w);
-  return decode_launched();
+  return decode_launch(write_token, dim3(n), dim3(kCopyThreads), 0,
+                       static_cast<cudaStream_t>(stream), p, w);
 }
 
 int bsgemv_cache_compact(bsgemv_cache_t c, void* pool, const int32_t* refs, const int32_t* tables,
@@ -601,15 +635,15 @@ int bsgemv_cache_compact(bsgemv_cache_t c, void* pool, const int32_t* refs, cons
       !aligned_to(lens, 4) || !aligned_to(refs_out, 4) || !aligned_to(tables_out, 4) ||
       !aligned_to(live_out, 4))
     return BSGEMV_ERR_MISALIGNED;
-  const int rc = decode_check_device(c->device);
+  int rc = decode_check_device(c->device);
   if (rc != BSGEMV_OK) return rc;
   CacheParams p = params_of(c, pool, 0);
   p.lens = const_cast<int32_t*>(lens);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  compact_plan<<<1, kScan, 0, s>>>(p, refs, refs_out, live_out);
-  compact_move<<<copy_grid(c, (c->num_pages + 1) / 2, c->max_seqs), kCopyThreads, 0, s>>>(
-      p, tables, tables_out);
-  return decode_launched();
+  rc = decode_launch(compact_plan, dim3(1), dim3(kScan), 0, s, p, refs, refs_out, live_out);
+  if (rc != BSGEMV_OK) return rc;
+  return decode_launch(compact_move, dim3(copy_grid(c, (c->num_pages + 1) / 2, c->max_seqs)),
+                       dim3(kCopyThreads), 0, s, p, tables, tables_out);
 }
 
 int bsgemv_cache_destroy(bsgemv_cache_t c) {
