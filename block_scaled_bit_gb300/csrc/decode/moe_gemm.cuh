@@ -82,6 +82,7 @@ struct MoeGemmParams {
   int second;                 // row distance of a tile's second half
   int step;                   // row distance of two tiles
   int tiles, spt;             // tiles of an expert, stages of a tile's k
+  int last_pairs;             // pairs of 16-byte chunks in a row's last stage
   int T, top_rows;            // tokens; routing rows a call can have
   int bf16;                   // x and y are bf16, else f16
   int s_bytes, z_bytes;       // bytes of a row's scales / zero points per stage
@@ -476,33 +477,34 @@ struct MoeGemm {
     return lsh<uint8_t>(row + blk);
   }
 
-  // The stage's products with one n8 tile of tokens.  row: the ring row of this lane's B column;
-  // ss, zs: what the rows' windows of words add to their starts.
+  // The stage's products with one n8 tile of tokens.  pairs: pairs of chunks in it; row: the ring
+  // row of this lane's B column; ss, zs: what the rows' windows of words add to their starts.
   // (An expert with more than eight tokens has its stage decoded once for each eight: the
   // weights come from HBM once all the same, and all but the first eight are rare.)
   // The loop over chunk pairs is unrolled by two (blocks of a whole stage: by four): wholly
   // unrolled, a small call spent 1000 cycles a stage more on fetching the code; rolled, a large
   // one 15 % more on running it.
-  static BSG_DEV void consume(const Ctx& c, const Lane& L, int ks, int slot, const uint8_t* row,
-                              const int (&ss)[2], const int (&zs)[2], float (&st)[4]) {
+  static BSG_DEV void consume(const Ctx& c, const Lane& L, uint32_t weights, const uint8_t* side,
+                              int pairs, const uint8_t* row, const uint32_t (&ss)[2],
+                              const uint32_t (&zs)[2], float (&st)[4]) {
     const MoeGemmParams& p = c.p;
-    const uint32_t wa = c.base_u + slot * kMoeBoxB + L.w;
+    const uint32_t wa = weights + L.w;
     // (chunk 2j: row g, g + 8), (chunk 2j + 1: row g, g + 8), loaded one pair ahead
     uint32_t v[4], ahead[4];
     ldsm_x4_at<0>(wa, ahead[0], ahead[1], ahead[2], ahead[3]);
-    const uint8_t* side = c.base + p.off_side + slot * p.side_bytes;
-    const int left = static_cast<int>(p.K) - ks * kKc;
-    const int pairs = left >= kKc ? 4 : (left + 2 * kKpc - 1) / (2 * kKpc);
     const uint8_t* sr[2] = {side + L.s[0] + ss[0], side + L.s[1] + ss[1]};
     const uint8_t* const zr[2] = {side + L.z[0] + zs[0], side + L.z[1] + zs[1]};
     uint32_t zl[2] = {0u, 0u}, zh[2] = {0u, 0u};
     if constexpr (kInts)
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) zp_consts<FMT, false>(FMT == kInt4 ? 8u : 128u, zl[rr], zh[rr]);
-    float tmp[kSub][4];  // a scale block's sums
+    float tmp[kSub][4];  // a scale block's sums (NVFP4: every other k-step's, a chain half as long)
     float s[kSub][2];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) st[x] = 0.f;
+    for (int x = 0; x < 4; ++x) {
+      st[x] = 0.f;
+      if (kFold) tmp[0][x] = 0.f;
+    }
     if constexpr (kFold) {  // this lane's block of the first chunk: 16 elements, t / 2
       sr[0] += L.t >> 1;
       sr[1] += L.t >> 1;
@@ -557,7 +559,7 @@ struct MoeGemm {
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
               if constexpr (kFold) {
-                mma16816<false>(st, a[i], b[part][i][0], b[part][i][1]);
+                mma16816<false>(i ? tmp[0] : st, a[i], b[part][i][0], b[part][i][1]);
               } else {
                 const bool first = opens && part == 0 && i == 0;
 #pragma unroll
@@ -579,6 +581,9 @@ struct MoeGemm {
         }
       }
     }
+    if constexpr (kFold)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) st[x] += tmp[0][x];
   }
 
   // h = p silu(g) u of this lane's two columns per n8 tile.
@@ -732,17 +737,26 @@ struct MoeGemm {
     const float* src = partial(c, first, 0, L.cw);  // + (b - first) * stride
     const int n = last - first + 1;
     if constexpr (DOWN) {
-      for (int i = L.lane; i < c.p.T * 16; i += 32) {
-        float v = 0.f;
+      // a lane takes four columns of a token at a time, eight parts in flight
+      for (int i = 4 * L.lane; i < c.p.T * 16; i += 128) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
         for (int b0 = 0; b0 < n; b0 += 8) {
-          float u[8];
+          float4 u[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            u[j] = b0 + j < n ? __ldcg((b0 + j ? src + (b0 + j) * stride : src0) + i) : 0.f;
+            u[j] = b0 + j < n ? __ldcg(reinterpret_cast<const float4*>(
+                                    (b0 + j ? src + (b0 + j) * stride : src0) + i))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v += u[j];
+          for (int j = 0; j < 8; ++j) {
+            v[0] += u[j].x;
+            v[1] += u[j].y;
+            v[2] += u[j].z;
+            v[3] += u[j].w;
+          }
         }
-        store_y(c, L.cw, number, i, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) store_y(c, L.cw, number, i + j, v[j]);
       }
     } else {
       float acc[MT][4];
@@ -805,38 +819,57 @@ struct MoeGemm {
           zw[rr] = at * static_cast<uint32_t>(p.z_pitch);
         }
       }
+      // ring offsets of the first n8 tile's rows: this lane's B column, its two result columns
+      const uint32_t rows_end = p.off_rows + p.row_cap * kRowB, rows_step = m * kRowB;
+      const auto row_at = [&](int col) {
+        return static_cast<uint32_t>(p.off_rows + wrap(c, head + (col < m ? col : 0)) * kRowB);
+      };
+      uint32_t at[3] = {row_at(L.g), row_at(2 * L.t), row_at(2 * L.t + 1)};
       for (int i = 0; i < n; ++i) {
         ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(c.full(slot), phase, p.err, kErrTimeoutFull,
                                                      p.wait_ns));
         if (ok) {
           const uint32_t ks = w.ks + i;
-          int ss[2] = {0, 0}, zs[2] = {0, 0};
+          const int pairs = ks + 1 == static_cast<uint32_t>(p.spt) ? p.last_pairs : 4;
+          uint32_t ss[2] = {0u, 0u}, zs[2] = {0u, 0u};
+          if (p.s_unit == 0 || p.z_unit == 0) {
 #pragma unroll
-          for (int rr = 0; rr < 2; ++rr) {
-            if (p.s_unit == 0) ss[rr] = (sw[rr] + ks * p.s_bytes) & 3;
-            if (kInts && p.z_unit == 0) zs[rr] = (zw[rr] + ks * p.z_bytes) & 3;
+            for (int rr = 0; rr < 2; ++rr) {
+              if (p.s_unit == 0) ss[rr] = (sw[rr] + ks * p.s_bytes) & 3;
+              if (kInts && p.z_unit == 0) zs[rr] = (zw[rr] + ks * p.z_bytes) & 3;
+            }
           }
-          for (int grp = 0; grp < nt; ++grp) {
-            const auto row_of = [&](int col) {
-              return c.base + p.off_rows + wrap(c, head + (col < m ? col : 0)) * kRowB;
-            };
-            float st[4];
-            consume(c, L, ks, slot, row_of(8 * grp + L.g), ss, zs, st);
-            const int col = 8 * grp + 2 * L.t;  // this lane's two result columns
-            const float f0 = lsh<float>(row_of(col) + 2 * kKc);
-            const float f1 = lsh<float>(row_of(col + 1) + 2 * kKc);
+          const uint32_t weights = c.base_u + slot * kMoeBoxB;
+          const uint8_t* side = c.base + p.off_side + slot * p.side_bytes;
+          float f0 = lsh<float>(c.base + at[1] + 2 * kKc), f1 = lsh<float>(c.base + at[2] + 2 * kKc);
+          float st[4];
+          consume(c, L, weights, side, pairs, c.base + at[0], ss, zs, st);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              if (MT == 1 || mt == grp) {
+          for (int x = 0; x < 4; ++x) acc[0][x] = fmaf(st[x], x & 1 ? f1 : f0, acc[0][x]);
+          if constexpr (MT > 1) {
+#pragma unroll 1
+            for (int grp = 1; grp < nt; ++grp) {
+              consume(c, L, weights, side, pairs, c.base + row_at(8 * grp + L.g), ss, zs, st);
+              f0 = lsh<float>(c.base + row_at(8 * grp + 2 * L.t) + 2 * kKc);
+              f1 = lsh<float>(c.base + row_at(8 * grp + 2 * L.t + 1) + 2 * kKc);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) acc[mt][x] = fmaf(st[x], x & 1 ? f1 : f0, acc[mt][x]);
-              }
+              for (int mt = 1; mt < MT; ++mt)
+                if (mt == grp) {
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) acc[mt][x] = fmaf(st[x], x & 1 ? f1 : f0, acc[mt][x]);
+                }
+            }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(c.empty(slot));
         }
         head += m;
         if (head >= p.row_cap) head -= p.row_cap;
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+          at[x] += rows_step;
+          if (at[x] >= rows_end) at[x] -= rows_end - p.off_rows;
+        }
         if (++slot == p.stages) { slot = 0; phase ^= 1u; }
       }
       const bool opens = w.ks == 0, ends = w.ks + n == p.spt;
@@ -851,7 +884,8 @@ struct MoeGemm {
             for (int i = lane; i < p.T * 16; i += 32) store_y(c, cw, w.tile, i, sum[i]);
           } else {
             float* dst = partial(c, blockIdx.x, seg == x0 ? 1 : 0, cw);
-            for (int i = lane; i < p.T * 16; i += 32) __stcg(dst + i, sum[i]);
+            for (int i = 4 * lane; i < p.T * 16; i += 128)
+              __stcg(reinterpret_cast<float4*>(dst + i), *reinterpret_cast<const float4*>(sum + i));
             arrive(c, L, w.tile, packing);
           }
           for (int i = lane; i < p.T * 16; i += 32) sum[i] = 0.f;

@@ -243,6 +243,7 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
   p.tiles = static_cast<int>(down ? (c.H + kMoeTileRows - 1) / kMoeTileRows : c.I / 64);
   const int kc = moe_stage_k(four);
   p.spt = static_cast<int>((w.k + kc - 1) / kc);
+  p.last_pairs = static_cast<int>((w.k - static_cast<int64_t>(p.spt - 1) * kc + (four ? 63 : 31)) / (four ? 64 : 32));
   p.T = c.T;
   p.top_rows = c.max_T * c.top_k;
   p.bf16 = c.bf16;
