@@ -62,8 +62,9 @@ constexpr int kMoeBoxB = kMoeTileRows * 128;
 struct MoeGemmParams {
   CUtensorMap tm;             // weight bytes, a box is a tile's 128 rows x 128 bytes, 128B swizzle:
                               // UP [E][2][I][row bytes], box [2][64][128]; DOWN [E][1][H][...], [128]
-  const uint8_t* x;           // packed activations: UP [token][stage][row bytes], DOWN
-                              // [stage][row][row bytes] (an expert's rows of a stage are adjacent)
+  const uint8_t* x;           // packed activations [stage][row][row bytes] (an expert's rows of a
+                              // stage are adjacent: one copy), or for UP of up to 8 tokens
+                              // [token][stage][row bytes] (packed before the routing is known)
   const Routing* route;
   const uint8_t *scales, *zp;
   const float* gscale;        // NVFP4: [E]
@@ -154,6 +155,7 @@ struct MoeGemm {
   static constexpr int kChunkB = 2 * kKpc;           // activation bytes of a chunk
   static constexpr int kPitch = moe_pitch(kFour);
   static constexpr int kParts = DOWN ? 2 : 1;
+  static constexpr bool kByToken = !DOWN && MT == 1;  // x is packed by token
   static constexpr int kRowB = kParts * kPitch;
   static constexpr int kSub = CPB == 0 ? 2 : 1;      // scale blocks per chunk
   static_assert(CPB != 0 || FMT == kInt4, "two scale blocks per chunk: int4, 16-element blocks");
@@ -329,8 +331,8 @@ struct MoeGemm {
   }
 
   // Weights, scales and activations of every stage in order, as far ahead as the rings allow.
-  // DOWN's first weights go out before the wait for the previous kernel (they do not depend on
-  // it, and the routing is older).  Everything that a run's stages share is worked out once per
+  // Where the routing is older than the kernel before this one, the first weights go out before
+  // the wait for that kernel (they do not depend on it).  Everything that a run's stages share is worked out once per
   // run: this warp's time per stage bounds the block's rate.  Returns the stages issued.
   static BSG_DEV int produce(const Ctx& c, int lane) {
     const MoeGemmParams& p = c.p;
@@ -338,7 +340,7 @@ struct MoeGemm {
     if (lane == 0) prefetch_tmap(&p.tm);
     Run w = first_run(c), tail = w;
     int early = 0;
-    if constexpr (DOWN) {
+    if constexpr (!kByToken) {
       Run e = w;
       while (early < p.stages) {
         Weights x = weights_of(c, e, lane);
@@ -359,10 +361,11 @@ struct MoeGemm {
       Weights x = weights_of(c, w, lane);
       const int r0 = c.off(w.a), m = c.off(w.a + 1) - r0;
       const uint32_t tx = m * kRowB;
-      // UP: lane j < m copies token j's row.  DOWN: lane 0 copies all rows, lane 1 those past the
-      // ring's end.
-      const int64_t row = DOWN ? static_cast<int64_t>(w.ks) * p.top_rows + r0
-                               : static_cast<int64_t>(lane < m ? c.token(r0 + lane) : 0) * p.spt + w.ks;
+      // by token: lane j < m copies token j's row; else lane 0 copies all rows, lane 1 those past
+      // the ring's end (a copy costs this warp some 170 cycles)
+      const int64_t row = kByToken
+                              ? static_cast<int64_t>(lane < m ? c.token(r0 + lane) : 0) * p.spt + w.ks
+                              : static_cast<int64_t>(w.ks) * p.top_rows + r0;
       const uint8_t* src = p.x + row * kRowB;
       for (int k = 0; k < w.n; ++k, ++i) {
         while (free_slots == 0 || used + m > p.row_cap) {
@@ -389,7 +392,7 @@ struct MoeGemm {
           x.s.src += x.s.bytes;
           if (kInts && p.zp) x.z.src += x.z.bytes;
         }
-        if constexpr (DOWN) {
+        if constexpr (!kByToken) {
           const int here = min(m, p.row_cap - head);
           if (lane == 0) bulk_load(c.base_u + p.off_rows + head * kRowB, src, here * kRowB, full);
           if (lane == 1 && here < m)
@@ -926,9 +929,10 @@ struct MoeGemm {
       *c.abort_word() = 0u;
       fence_mbar_init();
     }
-    // UP follows the routing kernel.  DOWN's routing is older than the kernel before it (UP has
-    // waited for it before letting DOWN start); only h needs the wait (in produce).
-    if constexpr (!DOWN) pdl_wait();
+    // By token, UP follows the routing kernel.  Else a kernel that has waited for the routing lies
+    // between (the one that packs x; UP for DOWN) and has let this one start: only the packed
+    // rows need the wait (in produce).
+    if constexpr (kByToken) pdl_wait();
     pdl_launch_dependents();
     const Routing* R = p.route;
     int* to = reinterpret_cast<int*>(base + p.off_route);
@@ -953,9 +957,9 @@ struct MoeGemm {
       else work(c, warp - 1, lane);
       __syncthreads();
       if (*c.abort_word() != 0u && threadIdx.x == 0) drain(c, issued);
-    } else if constexpr (DOWN) {
+    } else if constexpr (!kByToken) {
       pdl_wait();
-      if (c.total == 0)  // no token chose anything: empty rows are 0, NaN rows NaN
+      if (DOWN && c.total == 0)  // no token chose anything: empty rows are 0, NaN rows NaN
         for (int64_t i = static_cast<int64_t>(blockIdx.x) * kMoeThreads + threadIdx.x;
              i < p.T * p.out_pitch; i += static_cast<int64_t>(gridDim.x) * kMoeThreads) {
           const bool nan = (R->nan_rows >> (i / p.out_pitch)) & 1u;

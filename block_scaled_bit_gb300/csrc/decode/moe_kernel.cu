@@ -80,8 +80,7 @@ BSG_DEV void choose(const MoeParams& p, int t, int lane, int* ids, float* wts, u
 // ------------------------------------------------------------------------------ packing
 // Stage `ks` of token t's activations.  (k past the row packs zeros; K is a multiple of 64.)
 template <int PER>
-BSG_DEV void pack_x(const MoeParams& p, int t, int ks, int spt, int lane) {
-  uint8_t* dst = p.x_packed + (static_cast<int64_t>(t) * spt + ks) * moe_pitch(PER == 8);
+BSG_DEV void pack_x(const MoeParams& p, int t, int ks, uint8_t* dst, int lane) {
   const int64_t k = static_cast<int64_t>(ks) * (32 * PER) + lane * PER;
   const uint2* src = reinterpret_cast<const uint2*>(p.x + t * p.H + (k < p.H ? k : 0));
   uint32_t raw[PER / 2];
@@ -102,8 +101,20 @@ BSG_DEV void pack_x(const MoeParams& p, int t, int ks, int spt, int lane) {
   pack_stage<PER, 1>(v, dst, lane);
 }
 
-// Block 0 routes: a warp per token, then a thread per expert.  The other blocks pack x, one warp
-// per token and stage.
+// x packed by the routing's rows, one warp per row and stage (more than 8 tokens: an expert's rows
+// then come by one copy a stage, which saves more than this kernel's 3 us).
+template <int PER>
+__global__ void __launch_bounds__(256) moe_pack_rows(const __grid_constant__ MoeParams p, int spt) {
+  pdl_wait();
+  pdl_launch_dependents();  // (after the wait: UP reads the routing before its own)
+  const int unit = blockIdx.x * 8 + (threadIdx.x >> 5), r = unit / spt, ks = unit - r * spt;
+  if (r >= p.route->off[p.route->active]) return;
+  const int64_t row = static_cast<int64_t>(ks) * p.max_T * p.top_k + r;
+  pack_x<PER>(p, p.route->token[r], ks, p.x_packed + row * moe_pitch(PER == 8), threadIdx.x & 31);
+}
+
+// Block 0 routes: a warp per token, then a thread per expert.  The other blocks (up to 8 tokens)
+// pack x, one warp per token and stage.
 __global__ void __launch_bounds__(1024) moe_route(const __grid_constant__ MoeParams p, int spt) {
   __shared__ uint32_t mask[kMoeMaxE];
   __shared__ int ids[kMoeMaxT][kMoeMaxK];
@@ -117,8 +128,9 @@ __global__ void __launch_bounds__(1024) moe_route(const __grid_constant__ MoePar
     const int unit = (blockIdx.x - 1) * 32 + w, t = unit / spt;
     if (t >= p.T) return;
     const bool four = p.fmt == kInt4 || p.fmt == kNvfp4;
-    if (four) pack_x<8>(p, t, unit - t * spt, spt, lane);
-    else pack_x<4>(p, t, unit - t * spt, spt, lane);
+    uint8_t* dst = p.x_packed + static_cast<int64_t>(unit) * moe_pitch(four);
+    if (four) pack_x<8>(p, t, unit - t * spt, dst, lane);
+    else pack_x<4>(p, t, unit - t * spt, dst, lane);
     return;
   }
   mask[threadIdx.x] = 0;
@@ -317,7 +329,7 @@ MoeLayout moe_layout(int fmt, int64_t H, int64_t I, int E, int top_k, int max_T,
   l.h = take(rows * I * sizeof(float));
   const bool four = fmt == kInt4 || fmt == kNvfp4;
   const size_t kc = moe_stage_k(four), pitch = moe_pitch(four);
-  l.x_packed = take(max_T * ((H + kc - 1) / kc) * pitch);
+  l.x_packed = take((max_T > 8 ? rows : max_T) * ((H + kc - 1) / kc) * pitch);
   l.h_packed = take(rows * ((I + kc - 1) / kc) * 2 * pitch);
   l.total = at;
   return l;
@@ -340,7 +352,15 @@ int launch_moe(const MoeParams& p, int sms, cudaStream_t s) {
   static AttrRecord rec;
   int rc = decode_smem(moe_route, rec, 16);  // for the carveout
   if (rc != BSGEMV_OK) return rc;
-  rc = decode_launch(moe_route, dim3(1 + (p.T * up + 31) / 32), dim3(1024), 0, s, p, up);
+  const bool wide = p.max_T > 8;
+  rc = decode_launch(moe_route, dim3(wide ? 1 : 1 + (p.T * up + 31) / 32), dim3(1024), 0, s, p, up);
+  if (rc == BSGEMV_OK && wide) {
+    static AttrRecord rec8, rec4;
+    rc = four ? decode_smem(moe_pack_rows<8>, rec8, 16) : decode_smem(moe_pack_rows<4>, rec4, 16);
+    if (rc == BSGEMV_OK)
+      rc = decode_launch(four ? moe_pack_rows<8> : moe_pack_rows<4>,
+                         dim3((p.T * p.top_k * up + 7) / 8), dim3(256), 0, s, p, up);
+  }
   if (rc == BSGEMV_OK) rc = launch_product(p, false, sms, s);
   if (rc == BSGEMV_OK) rc = launch_product(p, true, sms, s);
   return rc;

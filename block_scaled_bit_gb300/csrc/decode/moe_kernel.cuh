@@ -59,7 +59,7 @@ struct MoeParams {
   float* partials;
   Routing* route;
   float* h;                    // [rows][I]
-  uint8_t *x_packed, *h_packed;  // [T][stages of H][pitch], [stages of I][rows][2 pitches]
+  uint8_t *x_packed, *h_packed;  // x: see MoeGemmParams; h: [stages of I][rows][2 pitches]
 };
 
 inline MoeWeight weight_of(int fmt, int bs, int has_zp, int64_t rows, int64_t k, const void* W,
