@@ -349,13 +349,14 @@ struct AttnStream {
     }
   }
 
-  static BSG_DEV void store_part(const AttnParams& p, int slot, int lane, Acc& a) {
+  static BSG_DEV void store_part(const AttnParams& p, const AttnUnit& u, int slot, int lane, Acc& a) {
     float* part = p.parts + static_cast<int64_t>(slot) * attn_slot_floats(D);
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       a.l[i] += __shfl_xor_sync(0xFFFFFFFFu, a.l[i], 1);
       a.l[i] += __shfl_xor_sync(0xFFFFFFFFu, a.l[i], 2);
+      if (q_row(p, u, g + 8 * i) == nullptr) continue;
       float* row = part + (g + 8 * i) * D + 2 * t;
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
@@ -458,7 +459,7 @@ struct AttnStream {
       if (++stage == T::kStages) { stage = 0; phase ^= 1u; }
       ++out.x;
       if (out.x == x1 || out.x == u.first + u.tiles) {
-        store_part(p, w + u.unit, lane, a);
+        store_part(p, u, w + u.unit, lane, a);
         fresh = true;
         settle(out);
       }

@@ -54,9 +54,10 @@ BSG_DEV void tma_load_4d_hint(uint32_t dst, const CUtensorMap* tm, int x, int y,
       : "memory");
 }
 
-constexpr int kMoeWarps = 8;                          // decode warps
+constexpr int kMoeFrags = 8;                          // mma fragments of 16 weight rows in a tile
+constexpr int kMoeWarps = kMoeFrags / 2;              // decode warps, two fragments each
 constexpr int kMoeThreads = 32 * (kMoeWarps + 1);     // and a copy warp
-constexpr int kMoeTileRows = 16 * kMoeWarps;
+constexpr int kMoeTileRows = 16 * kMoeFrags;
 constexpr int kMoeBoxB = kMoeTileRows * 128;
 
 struct MoeGemmParams {
@@ -178,7 +179,7 @@ struct MoeGemm {
     BSG_DEV int off(int a) const { return route()[p.top_rows + a]; }
     BSG_DEV int token(int r) const { return route()[2 * p.top_rows + 1 + r]; }
     BSG_DEV float weight(int r) const { return __int_as_float(route()[3 * p.top_rows + 1 + r]); }
-    BSG_DEV float* sums(int w) const {  // DOWN: [T][16] of decode warp w
+    BSG_DEV float* sums(int w) const {  // DOWN: [T][16] of fragment w
       return reinterpret_cast<float*>(base + p.off_sum) + w * p.T * 16;
     }
   };
@@ -425,13 +426,17 @@ struct MoeGemm {
   }
 
   // ---------------------------------------------------------------- decode warps
-  // Rows g and g + 8 of decode warp cw's fragment in the tile.
-  static BSG_DEV int tile_row(int cw, int half) { return DOWN ? 16 * cw + 8 * half : 8 * cw + 64 * half; }
+  // Rows g and g + 8 of fragment v in the tile (half 0 and 1); decode warp cw has fragments 2 cw
+  // and 2 cw + 1, whose rows are kNext apart.
+  static BSG_DEV int tile_row(int v, int half) { return DOWN ? 16 * v + 8 * half : 8 * v + 64 * half; }
+  static constexpr int kNext = DOWN ? 16 : 8;
 
   struct Lane {
     int cw, lane, g, t;
-    uint32_t w;     // ldmatrix address of chunk pair 0 in a stage's weights; pair j's is w ^ 32 j
-    int s[2], z[2];  // rows g and g + 8 in a stage's scales and zero points
+    // of the first fragment: ldmatrix address of chunk pair 0 in a stage's weights (pair j's is
+    // w ^ 32 j), rows g and g + 8 in its scales and zero points
+    uint32_t w;
+    int s[2], z[2];
   };
   static BSG_DEV Lane make_lane(const MoeGemmParams& p, int cw, int lane) {
     Lane L;
@@ -439,12 +444,12 @@ struct MoeGemm {
     L.lane = lane;
     L.g = lane >> 2;
     L.t = lane & 3;
-    const int i = lane >> 3, r = tile_row(cw, i & 1) + (lane & 7);
+    const int i = lane >> 3, r = tile_row(2 * cw, i & 1) + (lane & 7);
     L.w = r * 128 + (((i >> 1) ^ (r & 7)) << 4);
 #pragma unroll
     for (int rr = 0; rr < 2; ++rr) {
-      L.s[rr] = (tile_row(cw, rr) + L.g) * p.s_stride;
-      L.z[rr] = kMoeTileRows * p.s_stride + (tile_row(cw, rr) + L.g) * p.z_stride;
+      L.s[rr] = (tile_row(2 * cw, rr) + L.g) * p.s_stride;
+      L.z[rr] = kMoeTileRows * p.s_stride + (tile_row(2 * cw, rr) + L.g) * p.z_stride;
     }
     return L;
   }
@@ -489,28 +494,35 @@ struct MoeGemm {
   // one 15 % more on running it.
   static BSG_DEV void consume(const Ctx& c, const Lane& L, uint32_t weights, const uint8_t* side,
                               int pairs, const uint8_t* row, const uint32_t (&ss)[2],
-                              const uint32_t (&zs)[2], float (&st)[4]) {
+                              const uint32_t (&zs)[2], float (&st)[2][4]) {
     const MoeGemmParams& p = c.p;
     const uint32_t wa = weights + L.w;
     // (chunk 2j: row g, g + 8), (chunk 2j + 1: row g, g + 8), loaded one pair ahead
-    uint32_t v[4], ahead[4];
-    ldsm_x4_at<0>(wa, ahead[0], ahead[1], ahead[2], ahead[3]);
-    const uint8_t* sr[2] = {side + L.s[0] + ss[0], side + L.s[1] + ss[1]};
-    const uint8_t* const zr[2] = {side + L.z[0] + zs[0], side + L.z[1] + zs[1]};
-    uint32_t zl[2] = {0u, 0u}, zh[2] = {0u, 0u};
-    if constexpr (kInts)
+    uint32_t v[2][4], ahead[2][4];
+    const auto load = [&](int j) {
+      const uint32_t at = wa ^ (j << 5);
+      ldsm_x4_at<0>(at, ahead[0][0], ahead[0][1], ahead[0][2], ahead[0][3]);
+      ldsm_x4_at<0>(at + kNext * 128, ahead[1][0], ahead[1][1], ahead[1][2], ahead[1][3]);
+    };
+    load(0);
+    const uint8_t *sr[2][2], *zr[2][2];
+    uint32_t zl[2][2], zh[2][2];
+    float tmp[2][kSub][4];  // a scale block's sums (NVFP4: every other k-step's, a chain half as long)
+    float s[2][kSub][2];
 #pragma unroll
-      for (int rr = 0; rr < 2; ++rr) zp_consts<FMT, false>(FMT == kInt4 ? 8u : 128u, zl[rr], zh[rr]);
-    float tmp[kSub][4];  // a scale block's sums (NVFP4: every other k-step's, a chain half as long)
-    float s[kSub][2];
+    for (int f = 0; f < 2; ++f) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      st[x] = 0.f;
-      if (kFold) tmp[0][x] = 0.f;
-    }
-    if constexpr (kFold) {  // this lane's block of the first chunk: 16 elements, t / 2
-      sr[0] += L.t >> 1;
-      sr[1] += L.t >> 1;
+      for (int rr = 0; rr < 2; ++rr) {
+        sr[f][rr] = side + L.s[rr] + ss[rr] + f * kNext * p.s_stride;
+        zr[f][rr] = side + L.z[rr] + zs[rr] + f * kNext * p.z_stride;
+        if constexpr (kFold) sr[f][rr] += L.t >> 1;  // this lane's block of a chunk: 16 elements
+        if constexpr (kInts) zp_consts<FMT, false>(FMT == kInt4 ? 8u : 128u, zl[f][rr], zh[f][rr]);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        st[f][x] = 0.f;
+        if (kFold) tmp[f][0][x] = 0.f;
+      }
     }
     constexpr int kRun = CPB == 0 ? 1 : CPB;  // chunks of a scale block
     constexpr int kSpan = kFold || kRun < 4 ? 2 : kRun / 2;  // pairs of an iteration
@@ -522,93 +534,105 @@ struct MoeGemm {
         const int j = j0 + jj;
         if (kSpan == 2 && CPB != 4 && j >= pairs) break;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) v[x] = ahead[x];
-        if (j < 3)
-          ldsm_x4_at<0>(wa ^ ((j + 1) << 5), ahead[0], ahead[1], ahead[2], ahead[3]);
+        for (int x = 0; x < 4; ++x) {
+          v[0][x] = ahead[0][x];
+          v[1][x] = ahead[1][x];
+        }
+        if (j < 3) load(j + 1);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int chunk = 2 * j + q, in = 2 * jj + q;  // in: its place in the iteration
-          const uint32_t lo = v[2 * q], hi = v[2 * q + 1];
-          uint32_t a[kSteps][4];
           const bool opens = !kFold && in % kRun == 0, closes = !kFold && (in + 1) % kRun == 0;
-          if constexpr (kFold) {
-#pragma unroll
-            for (int rr = 0; rr < 2; ++rr)
-              zl[rr] = e4m3x2_to_f16x2(0x0101u * lsh<uint8_t>(sr[rr] + 2 * chunk));
-            decode_nvfp4<false>(lo, hi, zl[0], zl[1], a);
-          } else {
-            if (opens) {
-              const int blk = CPB == 0 ? 2 * chunk : chunk / kRun;
-#pragma unroll
-              for (int rr = 0; rr < 2; ++rr) {
-#pragma unroll
-                for (int u = 0; u < kSub; ++u) s[u][rr] = scale_at(sr[rr], blk + u);
-                if constexpr (kInts)
-                  if (p.zp)
-                    zp_consts<FMT, false>(zp_at(zr[rr], CPB == 0 ? blk + (L.t >> 1) : blk), zl[rr],
-                                          zh[rr]);
-              }
-            }
-            if constexpr (FMT == kInt4) decode_int4<false>(lo, hi, zl[0], zh[0], zl[1], zh[1], a);
-            else if constexpr (FMT == kInt8) decode_int8<false>(lo, hi, zl[0], zl[1], a);
-            else decode_fp8<false>(lo, hi, a);
-          }
           uint32_t b[kParts][kSteps][2];
 #pragma unroll
           for (int part = 0; part < kParts; ++part)
             fragment(src + part * kPitch + chunk * kChunkB, b[part]);
 #pragma unroll
-          for (int part = 0; part < kParts; ++part)
+          for (int f = 0; f < 2; ++f) {
+            const uint32_t lo = v[f][2 * q], hi = v[f][2 * q + 1];
+            uint32_t a[kSteps][4];
+            if constexpr (kFold) {
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-              if constexpr (kFold) {
-                mma16816<false>(i ? tmp[0] : st, a[i], b[part][i][0], b[part][i][1]);
-              } else {
-                const bool first = opens && part == 0 && i == 0;
+              for (int rr = 0; rr < 2; ++rr)
+                zl[f][rr] = e4m3x2_to_f16x2(0x0101u * lsh<uint8_t>(sr[f][rr] + 2 * chunk));
+              decode_nvfp4<false>(lo, hi, zl[f][0], zl[f][1], a);
+            } else {
+              if (opens) {
+                const int blk = CPB == 0 ? 2 * chunk : chunk / kRun;
 #pragma unroll
-                for (int u = 0; u < kSub; ++u) {
-                  // two blocks in a chunk: quad lanes t < 2 hold the first
-                  const bool mine = kSub == 1 || (L.t >> 1) == u;
-                  const uint32_t b0 = mine ? b[part][i][0] : 0u, b1 = mine ? b[part][i][1] : 0u;
-                  if (first) mma16816_zc<false>(tmp[u], a[i], b0, b1);
-                  else mma16816<false>(tmp[u], a[i], b0, b1);
+                for (int rr = 0; rr < 2; ++rr) {
+#pragma unroll
+                  for (int u = 0; u < kSub; ++u) s[f][u][rr] = scale_at(sr[f][rr], blk + u);
+                  if constexpr (kInts)
+                    if (p.zp)
+                      zp_consts<FMT, false>(zp_at(zr[f][rr], CPB == 0 ? blk + (L.t >> 1) : blk),
+                                            zl[f][rr], zh[f][rr]);
                 }
               }
+              if constexpr (FMT == kInt4)
+                decode_int4<false>(lo, hi, zl[f][0], zh[f][0], zl[f][1], zh[f][1], a);
+              else if constexpr (FMT == kInt8) decode_int8<false>(lo, hi, zl[f][0], zl[f][1], a);
+              else decode_fp8<false>(lo, hi, a);
             }
-          if (closes) {
 #pragma unroll
-            for (int u = 0; u < kSub; ++u)
+            for (int part = 0; part < kParts; ++part)
 #pragma unroll
-              for (int x = 0; x < 4; ++x) st[x] = fmaf(tmp[u][x], s[u][x >> 1], st[x]);
+              for (int i = 0; i < kSteps; ++i) {
+                if constexpr (kFold) {
+                  mma16816<false>(i ? tmp[f][0] : st[f], a[i], b[part][i][0], b[part][i][1]);
+                } else {
+                  const bool first = opens && part == 0 && i == 0;
+#pragma unroll
+                  for (int u = 0; u < kSub; ++u) {
+                    // two blocks in a chunk: quad lanes t < 2 hold the first
+                    const bool mine = kSub == 1 || (L.t >> 1) == u;
+                    const uint32_t b0 = mine ? b[part][i][0] : 0u, b1 = mine ? b[part][i][1] : 0u;
+                    if (first) mma16816_zc<false>(tmp[f][u], a[i], b0, b1);
+                    else mma16816<false>(tmp[f][u], a[i], b0, b1);
+                  }
+                }
+              }
+            if (closes) {
+#pragma unroll
+              for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  st[f][x] = fmaf(tmp[f][u][x], s[f][u][x >> 1], st[f][x]);
+            }
           }
         }
       }
     }
     if constexpr (kFold)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) st[x] += tmp[0][x];
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) st[f][x] += tmp[f][0][x];
   }
 
   // h = p silu(g) u of this lane's two columns per n8 tile.
   static BSG_DEV void store_h(const Ctx& c, const Lane& L, int a, int tile,
-                              const float (&acc)[MT][4]) {
+                              const float (&acc)[2][MT][4]) {
     const MoeGemmParams& p = c.p;
     const int r0 = c.off(a), m = c.off(a + 1) - r0;
     const float gs = kFold ? p.gscale[c.expert(a)] : 1.f;
-    const int64_t col = static_cast<int64_t>(tile) * 64 + 8 * L.cw + L.g;
+    const int64_t col = static_cast<int64_t>(tile) * 64 + 16 * L.cw + L.g;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int j = 8 * mt + 2 * L.t + x;
         if (j >= m) continue;
-        const float g = acc[mt][x] * gs, u = acc[mt][2 + x] * gs;
-        p.h[(r0 + j) * p.out_pitch + col] = c.weight(r0 + j) * (g / (1.f + expf(-g))) * u;
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const float g = acc[f][mt][x] * gs, u = acc[f][mt][2 + x] * gs;
+          p.h[(r0 + j) * p.out_pitch + col + 8 * f] = c.weight(r0 + j) * (g / (1.f + expf(-g))) * u;
+        }
       }
   }
 
   // UP: packing.  The last warp to store into a stage of DOWN's k (of kKc columns: 4 or 2 tiles of
-  // eight warps) packs that stage of the expert's rows.  (By a kernel between the two products
+  // four warps) packs that stage of the expert's rows.  (By a kernel between the two products
   // this took 3 us more of every call.)  A warp announces a tile when its next one is done, before
   // that one's stores, and looks at the answer another tile later: announced at once, the wait
   // for the stores and for the counter was an eighth of the kernel's time.
@@ -679,28 +703,32 @@ struct MoeGemm {
     }
   }
 
-  // DOWN: add an expert's products to the sums of its tokens (this warp's 16 rows).
-  static BSG_DEV void add_sums(const Ctx& c, const Lane& L, int a, const float (&acc)[MT][4]) {
+  // DOWN: add an expert's products to the sums of its tokens (this warp's fragments' rows).
+  static BSG_DEV void add_sums(const Ctx& c, const Lane& L, int a, const float (&acc)[2][MT][4]) {
     const int r0 = c.off(a), m = c.off(a + 1) - r0;
     const float gs = kFold ? c.p.gscale[c.expert(a)] : 1.f;
-    float* sum = c.sums(L.cw);
+    float* sum = c.sums(2 * L.cw);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int j = 8 * mt + 2 * L.t + x;
         if (j >= m) continue;
-        float* at = sum + c.token(r0 + j) * 16 + L.g;
-        at[0] += acc[mt][x] * gs;
-        at[8] += acc[mt][2 + x] * gs;
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          float* at = sum + (f * c.p.T + c.token(r0 + j)) * 16 + L.g;
+          at[0] += acc[f][mt][x] * gs;
+          at[8] += acc[f][mt][2 + x] * gs;
+        }
       }
     __syncwarp();
   }
 
+  // y of element idx of fragments 2 cw, 2 cw + 1's sums ([2][T][16]).
   static BSG_DEV void store_y(const Ctx& c, int cw, int tile, int idx, float v) {
-    const int t = idx >> 4;
+    const int second = idx >= c.p.T * 16, t = (idx >> 4) - (second ? c.p.T : 0);
     if ((c.p.route->nan_rows >> t) & 1u) v = __int_as_float(0x7FC00000);
-    const int64_t n = static_cast<int64_t>(tile) * kMoeTileRows + 16 * cw + (idx & 15);
+    const int64_t n = static_cast<int64_t>(tile) * kMoeTileRows + 16 * (2 * cw + second) + (idx & 15);
     if (n >= c.p.out_pitch) return;  // (H is a multiple of 64: the last tile may be half empty)
     const int64_t at = t * c.p.out_pitch + n;
     c.p.y[at] = c.p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v))
@@ -717,8 +745,8 @@ struct MoeGemm {
   // Stages of a tile (the unit that is finished in one place).
   static BSG_DEV int tile_len(const Ctx& c) { return DOWN ? c.active * c.p.spt : c.p.spt; }
 
-  static BSG_DEV float* partial(const Ctx& c, int block, int which, int cw) {
-    return c.p.partials + ((static_cast<int64_t>(block) * 2 + which) * kMoeWarps + cw) * c.p.slot_floats;
+  static BSG_DEV float* partial(const Ctx& c, int block, int which, int v) {
+    return c.p.partials + ((static_cast<int64_t>(block) * 2 + which) * kMoeFrags + v) * c.p.slot_floats;
   }
 
   // A part of a tile is in the workspace: the last of its blocks to come adds the parts, in block
@@ -735,20 +763,21 @@ struct MoeGemm {
     __syncwarp();
     if (L.lane == 0) c.p.counters[number * kMoeWarps + L.cw] = 0u;
     // the first block's part opens the tile, the others' continue it
-    const int64_t stride = static_cast<int64_t>(c.p.slot_floats) * (2 * kMoeWarps);  // of two blocks
-    const float* src0 = partial(c, first, 1, L.cw);
-    const float* src = partial(c, first, 0, L.cw);  // + (b - first) * stride
+    const int64_t stride = static_cast<int64_t>(c.p.slot_floats) * (2 * kMoeFrags);  // of two blocks
+    const float* src0 = partial(c, first, 1, 2 * L.cw);
+    const float* src = partial(c, first, 0, 2 * L.cw);  // + (b - first) * stride
     const int n = last - first + 1;
     if constexpr (DOWN) {
       // a lane takes four columns of a token at a time, eight parts in flight
-      for (int i = 4 * L.lane; i < c.p.T * 16; i += 128) {
+      for (int i = 4 * L.lane; i < c.p.T * 32; i += 128) {
+        const int at = i < c.p.T * 16 ? i : i - c.p.T * 16 + c.p.slot_floats;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         for (int b0 = 0; b0 < n; b0 += 8) {
           float4 u[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             u[j] = b0 + j < n ? __ldcg(reinterpret_cast<const float4*>(
-                                    (b0 + j ? src + (b0 + j) * stride : src0) + i))
+                                    (b0 + j ? src + (b0 + j) * stride : src0) + at))
                               : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -762,25 +791,31 @@ struct MoeGemm {
         for (int j = 0; j < 4; ++j) store_y(c, L.cw, number, i + j, v[j]);
       }
     } else {
-      float acc[MT][4];
+      float acc[2][MT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) acc[mt][x] = 0.f;
+        for (int x = 0; x < 4; ++x) acc[0][mt][x] = acc[1][mt][x] = 0.f;
         for (int b0 = 0; b0 < n; b0 += 4) {
-          float4 u[4];
+          float4 u[2][4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            u[j] = b0 + j < n ? __ldcg(reinterpret_cast<const float4*>(
-                                    b0 + j ? src + (b0 + j) * stride : src0) + L.lane + mt * 32)
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc[mt][0] += u[j].x;
-            acc[mt][1] += u[j].y;
-            acc[mt][2] += u[j].z;
-            acc[mt][3] += u[j].w;
-          }
+            for (int f = 0; f < 2; ++f)
+              u[f][j] = b0 + j < n ? __ldcg(reinterpret_cast<const float4*>(
+                                                (b0 + j ? src + (b0 + j) * stride : src0) +
+                                                f * c.p.slot_floats) +
+                                            L.lane + mt * 32)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              acc[f][mt][0] += u[f][j].x;
+              acc[f][mt][1] += u[f][j].y;
+              acc[f][mt][2] += u[f][j].z;
+              acc[f][mt][3] += u[f][j].w;
+            }
         }
       }
       const int a = number / c.p.tiles;
@@ -794,7 +829,7 @@ struct MoeGemm {
     const MoeGemmParams& p = c.p;
     const Lane L = make_lane(p, cw, lane);
     if constexpr (DOWN) {
-      for (int i = lane; i < p.T * 16; i += 32) c.sums(cw)[i] = 0.f;
+      for (int i = lane; i < p.T * 32; i += 32) c.sums(2 * cw)[i] = 0.f;
       __syncwarp();
     }
     int slot = 0, head = 0;
@@ -807,17 +842,18 @@ struct MoeGemm {
     while (true) {
       const int n = w.n;
       const int r0 = c.off(w.a), m = c.off(w.a + 1) - r0, nt = (m + 7) / 8;
-      float acc[MT][4];
+      float acc[2][MT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) acc[mt][x] = 0.f;
-      uint32_t sw[2] = {0u, 0u}, zw[2] = {0u, 0u};  // starts of the rows' scales, low bits
+        for (int x = 0; x < 4; ++x) acc[0][mt][x] = acc[1][mt][x] = 0.f;
+      uint32_t sw[2] = {0u, 0u}, zw[2] = {0u, 0u};  // starts of the rows' scales, low bits (both
+                                                    // fragments': their rows are 8 or 16 apart)
       if (p.s_unit == 0 || p.z_unit == 0) {
         const uint32_t row = static_cast<uint32_t>(weight_row(c, w));
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
-          const uint32_t r = tile_row(cw, rr) + L.g, at = row + (r < 64 ? r : p.second + r - 64);
+          const uint32_t r = tile_row(2 * cw, rr) + L.g, at = row + (r < 64 ? r : p.second + r - 64);
           sw[rr] = at * static_cast<uint32_t>(p.s_pitch);
           zw[rr] = at * static_cast<uint32_t>(p.z_pitch);
         }
@@ -845,10 +881,13 @@ struct MoeGemm {
           const uint32_t weights = c.base_u + slot * kMoeBoxB;
           const uint8_t* side = c.base + p.off_side + slot * p.side_bytes;
           float f0 = lsh<float>(c.base + at[1] + 2 * kKc), f1 = lsh<float>(c.base + at[2] + 2 * kKc);
-          float st[4];
+          float st[2][4];
           consume(c, L, weights, side, pairs, c.base + at[0], ss, zs, st);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) acc[0][x] = fmaf(st[x], x & 1 ? f1 : f0, acc[0][x]);
+          for (int x = 0; x < 4; ++x) {
+            acc[0][0][x] = fmaf(st[0][x], x & 1 ? f1 : f0, acc[0][0][x]);
+            acc[1][0][x] = fmaf(st[1][x], x & 1 ? f1 : f0, acc[1][0][x]);
+          }
           if constexpr (MT > 1) {
 #pragma unroll 1
             for (int grp = 1; grp < nt; ++grp) {
@@ -859,7 +898,10 @@ struct MoeGemm {
               for (int mt = 1; mt < MT; ++mt)
                 if (mt == grp) {
 #pragma unroll
-                  for (int x = 0; x < 4; ++x) acc[mt][x] = fmaf(st[x], x & 1 ? f1 : f0, acc[mt][x]);
+                  for (int x = 0; x < 4; ++x) {
+                    acc[0][mt][x] = fmaf(st[0][x], x & 1 ? f1 : f0, acc[0][mt][x]);
+                    acc[1][mt][x] = fmaf(st[1][x], x & 1 ? f1 : f0, acc[1][mt][x]);
+                  }
                 }
             }
           }
@@ -882,16 +924,17 @@ struct MoeGemm {
         const bool tile_ends = ends && w.a + 1 == c.active;
         if (tile_ends || s == c.s1) {
           const int x0 = w.tile * tile_len(c);
-          float* sum = c.sums(cw);
+          float* sum = c.sums(2 * cw);
           if (tile_ends && seg == x0) {
-            for (int i = lane; i < p.T * 16; i += 32) store_y(c, cw, w.tile, i, sum[i]);
+            for (int i = lane; i < p.T * 32; i += 32) store_y(c, cw, w.tile, i, sum[i]);
           } else {
-            float* dst = partial(c, blockIdx.x, seg == x0 ? 1 : 0, cw);
-            for (int i = 4 * lane; i < p.T * 16; i += 128)
-              __stcg(reinterpret_cast<float4*>(dst + i), *reinterpret_cast<const float4*>(sum + i));
+            float* dst = partial(c, blockIdx.x, seg == x0 ? 1 : 0, 2 * cw);
+            for (int i = 4 * lane; i < p.T * 32; i += 128)
+              __stcg(reinterpret_cast<float4*>(dst + (i < p.T * 16 ? i : i - p.T * 16 + p.slot_floats)),
+                     *reinterpret_cast<const float4*>(sum + i));
             arrive(c, L, w.tile, packing);
           }
-          for (int i = lane; i < p.T * 16; i += 32) sum[i] = 0.f;
+          for (int i = lane; i < p.T * 32; i += 32) sum[i] = 0.f;
           __syncwarp();
           seg = s;
         }
@@ -902,10 +945,15 @@ struct MoeGemm {
           store_h(c, L, w.a, w.tile, acc);
           pack_after(packing, w.a, w.tile);
         } else {
-          float4* dst = reinterpret_cast<float4*>(partial(c, blockIdx.x, opens ? 1 : 0, cw)) + lane;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            __stcg(dst + mt * 32, make_float4(acc[mt][0], acc[mt][1], acc[mt][2], acc[mt][3]));
+          for (int f = 0; f < 2; ++f) {
+            float4* dst =
+                reinterpret_cast<float4*>(partial(c, blockIdx.x, opens ? 1 : 0, 2 * cw + f)) + lane;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              __stcg(dst + mt * 32,
+                     make_float4(acc[f][mt][0], acc[f][mt][1], acc[f][mt][2], acc[f][mt][3]));
+          }
           arrive(c, L, w.a * p.tiles + w.tile, packing);
         }
       }

@@ -289,7 +289,7 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
     p.off_bar = at;
     at += align_up(16 * p.stages + 8, 16);
     p.off_sum = at;
-    at += down ? kMoeWarps * c.T * 16 * 4 : 0;
+    at += down ? kMoeFrags * c.T * 16 * 4 : 0;
     smem = at + 1024;  // the ring starts on a 1024-byte boundary
     if (smem <= budget || p.stages == 2) break;
   }
@@ -325,7 +325,7 @@ MoeLayout moe_layout(int fmt, int64_t H, int64_t I, int E, int top_k, int max_T,
   l.counters_up = take(active * (I / 64) * kMoeWarps * sizeof(unsigned));
   l.counters_packed = take(active * (static_cast<size_t>(I) / 128 + 1) * sizeof(unsigned));
   l.counters_down = take(static_cast<size_t>(H / 64) * kMoeWarps * sizeof(unsigned));
-  l.partials = take(ctas * 2 * kMoeWarps * slot * sizeof(float));
+  l.partials = take(ctas * 2 * kMoeFrags * slot * sizeof(float));
   l.h = take(rows * I * sizeof(float));
   const bool four = fmt == kInt4 || fmt == kNvfp4;
   const size_t kc = moe_stage_k(four), pitch = moe_pitch(four);
