@@ -10,41 +10,45 @@
 //   up to 128 rows       both work on the same rows, stream s on the key tiles i with i % 2 == s
 //   D = 256              one stream (its accumulator takes 256 of the 512 columns)
 // A job is a key tile of 64 positions for one stream.  One warp copies K and V tiles (TMA, one box
-// per page or tile and 64 d, 128-byte swizzle); a warp per stream issues its MMAs:  S = Q K^T (both from shared memory, M = 128) and O += P V (P from tensor memory, where it takes
-// the place of its scores; V's d is contiguous, an MN-major operand).  A stream has two score
-// buffers, so that a softmax never waits for its own products: with one buffer of 128 positions,
-// S, softmax and P V ran one after the other and took 5300 cycles a 128 positions where the copy
-// takes 2800.  And it has an MMA warp of its own: one warp for both waited in turn for either's
-// probabilities and buffers, 450 of the 1350 cycles of a job, while the tensor cores ran dry.  A row of S lies in one lane, so softmax
-// needs no exchange between threads.  O is scaled to a new maximum only when a row's has grown by
-// more than 2^8 since O's (P stays below 2^8, far from overflow), which is rare after the first
-// tiles.
+// per page or tile and 64 d, 128-byte swizzle); a warp per stream issues its MMAs:  S = Q K^T (both
+// from shared memory, M = 128) and O += P V (P from tensor memory; V's d is contiguous, an
+// MN-major operand).  A row of S lies in one lane, so softmax needs no exchange between threads.
+// Its threads take a row's scores into registers at once and free S's columns for the next tile's,
+// which the tensor cores work out while the numerators are made; P goes to one of two places of
+// its own.  (One MMA warp for both streams waited in turn for either's probabilities, 450 of 1350
+// cycles a job.  Two places of S, or P in its scores' place with two of them, are no faster at 128
+// d, and slower at 256, where the ring has few tiles.)
+// O is scaled to a new maximum only when a row's has grown by more than 2^8 since O's (P stays
+// below 2^8, far from overflow), which is rare after the first tiles.
 // The line of (kv head, row block, key tile) is cut into equal ranges, one per block; a unit counts
-// kAttnPreCost tiles more than it has, what it costs a block to begin and end one.
+// kAttnPreCost tiles more than it has, what it costs a block to begin and end one: at 256 rows of
+// 128 d, 2.7 us until the queries are there, 4 us to write the part, 0.9 us a tile (with a cost of
+// 4 the blocks that touch two units ended 5 us after the others).
 #pragma once
 
 #include "attn_stream.cuh"
 
 namespace bsg {
 
-constexpr int kAttnPreCost = 4;
+constexpr int kAttnPreCost = 8;
 
 template <int D>
 struct AttnPre {
   static constexpr int kKeys = 64;                      // positions of a tile
   static constexpr int kStreams = D == 256 ? 1 : 2;
-  static constexpr int kBufs = 2 * kStreams;            // score buffers
+  static constexpr int kBufs = 2 * kStreams;            // places of P
   static constexpr int kTileB = kKeys * D * 2;          // bytes of a K (or V) tile
   static constexpr int kQB = 128 * D * 2;               // bytes of a query tile
   static constexpr int kRingMax = (224 * 1024 - kStreams * kQB) / kTileB;
   static constexpr int kRing = kRingMax < 16 ? kRingMax : 16;
   static constexpr int kOffRing = kStreams * kQB;
   static constexpr int kOffBar = kOffRing + kRing * kTileB;
-  static constexpr int kBars = 2 * kRing + 3 * kBufs + 1;
+  static constexpr int kBars = 2 * kRing + 2 * kStreams + 2 * kBufs + 1;
   static constexpr int kSmem = kOffBar + (kBars * 8 + 12 + 15) / 16 * 16 + 1024;  // (1024-byte tiles)
   static constexpr int kThreads = 32 * (5 * kStreams + 1);
   static constexpr int kSlotRows = 128 * kStreams;
-  static constexpr int kColO = kBufs * kKeys;           // tensor memory: scores, then O
+  // tensor memory: per stream 64 columns of S and twice 32 of P, then the streams' O
+  static constexpr int kColO = kStreams * 2 * kKeys;
   static_assert(kColO + kStreams * D <= 512, "tensor memory");
   static_assert(kRing >= 5 && kSmem <= 232448, "shared memory");
 };
@@ -185,13 +189,21 @@ struct AttnPrefix {
     BSG_DEV uint32_t bar(int i) const { return base_u + T::kOffBar + 8 * i; }
     BSG_DEV uint32_t full(int i) const { return bar(i); }                   // ring tile landed
     BSG_DEV uint32_t empty(int i) const { return bar(T::kRing + i); }       // ring tile read
-    // of a stream's job j (numbered over the block's whole range): its buffer's barriers, their phase
+    // of a stream's job j (numbered over the block's whole range): its place of P, whose barriers'
+    // phase; those of S have phase j & 1
     static BSG_DEV uint32_t buf(uint32_t stream, uint32_t j) { return 2 * stream + (j & 1u); }
     static BSG_DEV uint32_t phase(uint32_t j) { return (j >> 1) & 1u; }
-    BSG_DEV uint32_t scores(uint32_t b) const { return bar(2 * T::kRing + b); }               // S written
-    BSG_DEV uint32_t probs(uint32_t b) const { return bar(2 * T::kRing + T::kBufs + b); }     // P written
-    BSG_DEV uint32_t out(uint32_t b) const { return bar(2 * T::kRing + 2 * T::kBufs + b); }   // P V done
-    BSG_DEV uint32_t query() const { return bar(2 * T::kRing + 3 * T::kBufs); }               // Q written
+    static constexpr int kS = 2 * T::kRing, kP = kS + 2 * T::kStreams;
+    BSG_DEV uint32_t scores(uint32_t stream) const { return bar(kS + stream); }               // S written
+    BSG_DEV uint32_t taken(uint32_t stream) const { return bar(kS + T::kStreams + stream); }  // S read
+    BSG_DEV uint32_t probs(uint32_t b) const { return bar(kP + b); }                          // P written
+    BSG_DEV uint32_t out(uint32_t b) const { return bar(kP + T::kBufs + b); }                 // P V done
+    BSG_DEV uint32_t query() const { return bar(kP + 2 * T::kBufs); }                         // Q written
+    // columns of S and P
+    static BSG_DEV uint32_t col_s(uint32_t stream) { return stream * 2 * K; }
+    static BSG_DEV uint32_t col_p(uint32_t stream, uint32_t j) {
+      return stream * 2 * K + K + (j & 1u) * (K / 2);
+    }
     BSG_DEV uint32_t tile(int i) const { return base_u + T::kOffRing + i * T::kTileB; }
     BSG_DEV volatile uint32_t* words() const {
       return reinterpret_cast<volatile uint32_t*>(base + T::kOffBar + 8 * T::kBars);
@@ -243,6 +255,7 @@ struct AttnPrefix {
       prefetch_tmap(&p.tm_v);
     }
     const int boxes = K / p.box_rows * kSub, r = lane / kSub * p.box_rows, d = lane % kSub;
+    const int first = c.s.pair ? 4 : 2;
     int slot = 0, i = 0;
     uint32_t phase = 1;
     for (int x = c.x0; x < c.x1;) {
@@ -252,6 +265,12 @@ struct AttnPrefix {
       for (int t = g.t0; t < g.t0 + g.n; ++t) {
         const int here = page, pos = t * K + r;
         page = fetch_page(c, t + 1, r);
+        // the first tiles out, the rest of the ring after the first queries: behind all blocks'
+        // rings they came 4 us later.  (The first segment goes on, so they are its.)
+        if (i == first && t == g.t0 + first / 2 && !wait_warp(c, c.query(), 0u)) {
+          if (lane == 0) c.words()[2] = i;
+          return false;
+        }
         for (int kv = 0; kv < 2; ++kv, ++i) {
           if (i >= T::kRing && !wait_warp(c, c.empty(slot), phase)) {
             if (lane == 0) c.words()[2] = i;
@@ -329,37 +348,34 @@ struct AttnPrefix {
       if (!c.wait(c.query(), seg_phase, kErrTimeoutFull)) return false;
       seg_phase ^= 1u;
       tc_after();
-      uint32_t sj = 0;  // the segment's next scores; their buffer is free
+      // (the segment's first: the jobs before have had their scores read)
       const auto scores = [&]() -> bool {
-        const uint32_t b = Ctx::buf(stream, job + sj);
         if (!c.wait(c.full(kr.slot), kr.phase, kErrTimeoutFull)) return false;
         if (lead) {
-          mma_scores(tmem + b * K, q_lo, k_lo + kr.slot * (T::kTileB / 16));
-          tc_commit(c.scores(b));
+          mma_scores(tmem + Ctx::col_s(stream), q_lo, k_lo + kr.slot * (T::kTileB / 16));
+          tc_commit(c.scores(stream));
           tc_commit(c.empty(kr.slot));
         }
         kr.move(step);
-        ++sj;
         return true;
       };
-      while (sj < 2 && sj < jobs)
-        if (!scores()) return false;
+      if (jobs > 0 && !scores()) return false;
       for (uint32_t j = 0; j < jobs; ++j) {
-        const uint32_t b = Ctx::buf(stream, job + j), phase = Ctx::phase(job + j);
-        if (!c.wait(c.probs(b), phase, kErrTimeoutFull)) return false;
+        const uint32_t n = job + j, b = Ctx::buf(stream, n);
+        if (j + 1 < jobs) {
+          if (!c.wait(c.taken(stream), n & 1u, kErrTimeoutFull)) return false;
+          tc_after();
+          if (!scores()) return false;
+        }
+        if (!c.wait(c.probs(b), Ctx::phase(n), kErrTimeoutFull)) return false;
         if (!c.wait(c.full(vr.slot), vr.phase, kErrTimeoutFull)) return false;
         tc_after();
         if (lead) {
-          mma_out(o, tmem + b * K, v_lo + vr.slot * (T::kTileB / 16), j > 0);
+          mma_out(o, tmem + Ctx::col_p(stream, n), v_lo + vr.slot * (T::kTileB / 16), j > 0);
           tc_commit(c.out(b));
           tc_commit(c.empty(vr.slot));
         }
         vr.move(step);
-        if (sj < jobs) {
-          // the next scores go where this job's P is read
-          if (!c.wait(c.out(b), phase, kErrTimeoutFull)) return false;
-          if (!scores()) return false;
-        }
       }
       job += jobs;
     }
@@ -374,31 +390,30 @@ struct AttnPrefix {
     const AttnParams& a = c.p.a;
     const int G = a.Hq / a.Hkv, head = g.unit / c.s.blocks, block = g.unit - head * c.s.blocks;
     const int first = block * (c.s.pair ? 128 : T::kSlotRows) + q * 128;
-    uint8_t* dst = c.base + q * T::kQB;
-    // eight loads in flight a thread: one after the other they took longer than the products
-    for (int i0 = tid; i0 < 128 * (D / 8); i0 += 8 * nthr) {
-      uint4 v[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i = i0 + u * nthr, row = first + i / (D / 8), b = row / G;
-        v[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (i < 128 * (D / 8) && b < a.B)
-          v[u] = __ldg(reinterpret_cast<const uint4*>(
-              a.q + b * a.q_stride + static_cast<int64_t>(head * G + row - b * G) * D +
-              i % (D / 8) * 8));
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i = i0 + u * nthr, r = i / (D / 8), ch = i % (D / 8);
-        if (i >= 128 * (D / 8)) break;
-        if (a.scale_log2 < 0.f) {
-          v[u].x ^= 0x80008000u;
-          v[u].y ^= 0x80008000u;
-          v[u].z ^= 0x80008000u;
-          v[u].w ^= 0x80008000u;
-        }
-        *reinterpret_cast<uint4*>(dst + (ch / 8) * (128 * 128) + r * 128 +
-                                  (((ch & 7) ^ (r & 7)) << 4)) = v[u];
+    const uint32_t dst = c.base_u + q * T::kQB;
+    const auto place = [&](int i) {
+      const int r = i / (D / 8), ch = i % (D / 8);
+      return (ch / 8) * (128 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+    };
+    // all of a thread's loads in flight at once (eight at a time, they took 3 to 5 us)
+    for (int i = tid; i < 128 * (D / 8); i += nthr) {
+      const int row = first + i / (D / 8), b = row / G;
+      const bool in = b < a.B;  // rows past the last: zeros
+      const uint16_t* src =
+          a.q + (in ? b * a.q_stride + static_cast<int64_t>(head * G + row - b * G) * D + i % (D / 8) * 8 : 0);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + place(i)), "l"(src),
+                   "r"(in ? 16 : 0) : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (a.scale_log2 < 0.f) {
+      uint8_t* mine = c.base + q * T::kQB;
+      for (int i = tid; i < 128 * (D / 8); i += nthr) {
+        uint4 v = lsh<uint4>(mine + place(i));
+        v.x ^= 0x80008000u;
+        v.y ^= 0x80008000u;
+        v.z ^= 0x80008000u;
+        v.w ^= 0x80008000u;
+        *reinterpret_cast<uint4*>(mine + place(i)) = v;
       }
     }
     fence_async_shared();
@@ -422,13 +437,22 @@ struct AttnPrefix {
     return ok;
   }
 
+  static BSG_DEV float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+  }
+
   // The largest of a row's scores (the first `valid` of them).
   template <bool PART>
   static BSG_DEV float row_max(const uint32_t (&raw)[K], int valid) {
     float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int i = 0; i < K; ++i)
-      if (!PART || i < valid) t[i & 3] = fmaxf(t[i & 3], __uint_as_float(raw[i]));
+    for (int i = 0; i < K; i += 2) {
+      const float a = !PART || i < valid ? __uint_as_float(raw[i]) : -INFINITY;
+      const float b = !PART || i + 1 < valid ? __uint_as_float(raw[i + 1]) : -INFINITY;
+      t[(i >> 1) & 3] = max3(t[(i >> 1) & 3], a, b);
+    }
     return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
   }
 
@@ -469,13 +493,15 @@ struct AttnPrefix {
     for (uint32_t j = 0; j < jobs; ++j) {
       const uint32_t b = Ctx::buf(stream, job + j), tile = tile_of(c, stream, j);
       const uint32_t before = job + j - 1;  // the job before, where there is one in the segment
-      if (!wait_warp(c, c.scores(b), Ctx::phase(job + j))) return false;
+      if (!wait_warp(c, c.scores(stream), (job + j) & 1u)) return false;
       tc_after();
-      const uint32_t ts = c.tmem + b * K + lanes;
+      const uint32_t ts = c.tmem + Ctx::col_s(stream) + lanes;
       uint32_t raw[K];
 #pragma unroll
       for (int i = 0; i < K; i += 32) tc_ld32(ts + i, raw + i);
       tc_wait_ld();
+      tc_before();
+      mbar_arrive(c.taken(stream));  // (before anything else: the next tile's scores wait for it)
       // positions of this tile, if below K: the others' scores do not count
       const int valid = p.a.prefix_len - (g.t0 + static_cast<int>(tile)) * K;
       const float top = valid < K ? row_max<true>(raw, valid) * scale : row_max<false>(raw, K) * scale;
@@ -505,8 +531,12 @@ struct AttnPrefix {
       const float base = m == -INFINITY ? 0.f : m;
       l += valid < K ? numerators<true>(raw, scale, base, valid)
                      : numerators<false>(raw, scale, base, K);
+      // P's place is free when the products of two jobs before are done
+      if (j >= 2 && !wait_warp(c, c.out(b), Ctx::phase(job + j - 2))) return false;
+      const uint32_t tp = c.tmem + Ctx::col_p(stream, job + j) + lanes;
+      tc_after();
 #pragma unroll
-      for (int i = 0; i < K / 2; i += 32) tc_st32(ts + i, raw + i);
+      for (int i = 0; i < K / 2; i += 32) tc_st32(tp + i, raw + i);
       tc_wait_st();
       if (valid < K) {
         // the page that the prefix ends in holds something else after it: zeros for V there
@@ -578,8 +608,11 @@ struct AttnPrefix {
         mbar_init(c.full(i), 1);
         mbar_init(c.empty(i), c.s.pair ? 1 : T::kStreams);  // streams that read a tile
       }
-      for (int b = 0; b < T::kBufs; ++b) {
+      for (int b = 0; b < T::kStreams; ++b) {
         mbar_init(c.scores(b), 1);
+        mbar_init(c.taken(b), 128);
+      }
+      for (int b = 0; b < T::kBufs; ++b) {
         mbar_init(c.probs(b), 128);
         mbar_init(c.out(b), 1);
       }
