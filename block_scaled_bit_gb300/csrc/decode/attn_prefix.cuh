@@ -41,6 +41,11 @@ struct AttnPre {
   static constexpr int kQB = 128 * D * 2;               // bytes of a query tile
   static constexpr int kRingMax = (224 * 1024 - kStreams * kQB) / kTileB;
   static constexpr int kRing = kRingMax < 16 ? kRingMax : 16;
+  // Where the streams take turns with the key tiles, a slot of the ring always serves the same
+  // stream, so that whoever waits for a tile in it has seen the tile before land.  (A barrier's
+  // parity tells a phase from the next only: with ten slots, a stream could take the other's
+  // tile, not landed yet, for its own.)
+  static constexpr int kPairRing = kRing / 4 * 4;
   static constexpr int kOffRing = kStreams * kQB;
   static constexpr int kOffBar = kOffRing + kRing * kTileB;
   static constexpr int kBars = 2 * kRing + 2 * kStreams + 2 * kBufs + 1;
@@ -186,6 +191,7 @@ struct AttnPrefix {
     uint8_t* base;
     uint32_t base_u, tmem;
     int x0, x1;
+    int ring;  // tiles in use
     BSG_DEV uint32_t bar(int i) const { return base_u + T::kOffBar + 8 * i; }
     BSG_DEV uint32_t full(int i) const { return bar(i); }                   // ring tile landed
     BSG_DEV uint32_t empty(int i) const { return bar(T::kRing + i); }       // ring tile read
@@ -272,7 +278,7 @@ struct AttnPrefix {
           return false;
         }
         for (int kv = 0; kv < 2; ++kv, ++i) {
-          if (i >= T::kRing && !wait_warp(c, c.empty(slot), phase)) {
+          if (i >= c.ring && !wait_warp(c, c.empty(slot), phase)) {
             if (lane == 0) c.words()[2] = i;
             return false;
           }
@@ -282,7 +288,7 @@ struct AttnPrefix {
           if (lane < boxes)
             tma_load_4d(c.tile(slot) + d * (K * 128) + r * 128, kv ? &p.tm_v : &p.tm_k, d * 64,
                         pos & ((1 << p.a.page_log2) - 1), head, here, bar);
-          if (++slot == T::kRing) { slot = 0; phase ^= 1u; }
+          if (++slot == c.ring) { slot = 0; phase ^= 1u; }
         }
       }
       x = g.end;
@@ -294,18 +300,18 @@ struct AttnPrefix {
   // After a wait that ran out: the copies in flight land before the block ends (bounded).
   static BSG_DEV void drain(const Ctx& c) {
     const int n = static_cast<int>(c.words()[2]);
-    for (int i = n > T::kRing ? n - T::kRing : 0; i < n; ++i)
-      c.wait(c.full(i % T::kRing), (i / T::kRing) & 1, kErrTimeoutFull);
+    for (int i = n > c.ring ? n - c.ring : 0; i < n; ++i)
+      c.wait(c.full(i % c.ring), (i / c.ring) & 1, kErrTimeoutFull);
   }
 
   // ---- MMA warp of a stream
   // Place in the ring of tiles, moved on by any number.
   struct Ring {
     uint32_t slot, phase;
-    BSG_DEV void move(uint32_t n) {
+    BSG_DEV void move(uint32_t n, uint32_t ring) {
       slot += n;
-      while (slot >= T::kRing) {
-        slot -= T::kRing;
+      while (slot >= ring) {
+        slot -= ring;
         phase ^= 1u;
       }
     }
@@ -323,7 +329,8 @@ struct AttnPrefix {
       tc_mma_ts(o, pr + k * 8, v_lo + k * 2048 / 16, kDescHi, kIdescO, add || k > 0);
   }
 
-  // The whole warp runs this; one elected lane issues.  (Run by one thread, with 64-bit descriptors
+  // The whole warp runs this; one elected lane issues.  (Every wait is the warp's: a lane left
+  // behind while the others go on would look at a phase that the barrier passes twice.)  (Run by one thread, with 64-bit descriptors
   // and phases worked out for every MMA, a job took 1700 cycles; the tensor cores need 640.)
   static BSG_DEV bool issue(const Ctx& c, uint32_t stream) {
     const bool lead = elect_one();
@@ -332,6 +339,7 @@ struct AttnPrefix {
     const uint32_t k_lo = desc_lo(c.base_u + T::kOffRing, 16);
     const uint32_t v_lo = desc_lo(c.base_u + T::kOffRing, K * 128);
     const uint32_t o = tmem + T::kColO + stream * D;
+    const uint32_t ring = c.ring;
     const uint32_t step = c.s.pair ? 4 : 2;  // ring tiles from a job's K (or V) to the next's
     Ring base = {0, 0};                      // the segment's first K
     uint32_t job = 0, seg_phase = 0;         // the segment's first job
@@ -341,41 +349,41 @@ struct AttnPrefix {
       if (g.n == 0) continue;
       const uint32_t jobs = jobs_of(c, stream, g.n);
       Ring kr = base, vr;
-      kr.move(2 * tile_of(c, stream, 0));
+      kr.move(2 * tile_of(c, stream, 0), ring);
       vr = kr;
-      vr.move(1);
-      base.move(2 * g.n);
-      if (!c.wait(c.query(), seg_phase, kErrTimeoutFull)) return false;
+      vr.move(1, ring);
+      base.move(2 * g.n, ring);
+      if (!wait_warp(c, c.query(), seg_phase)) return false;
       seg_phase ^= 1u;
       tc_after();
       // (the segment's first: the jobs before have had their scores read)
       const auto scores = [&]() -> bool {
-        if (!c.wait(c.full(kr.slot), kr.phase, kErrTimeoutFull)) return false;
+        if (!wait_warp(c, c.full(kr.slot), kr.phase)) return false;
         if (lead) {
           mma_scores(tmem + Ctx::col_s(stream), q_lo, k_lo + kr.slot * (T::kTileB / 16));
           tc_commit(c.scores(stream));
           tc_commit(c.empty(kr.slot));
         }
-        kr.move(step);
+        kr.move(step, ring);
         return true;
       };
       if (jobs > 0 && !scores()) return false;
       for (uint32_t j = 0; j < jobs; ++j) {
         const uint32_t n = job + j, b = Ctx::buf(stream, n);
         if (j + 1 < jobs) {
-          if (!c.wait(c.taken(stream), n & 1u, kErrTimeoutFull)) return false;
+          if (!wait_warp(c, c.taken(stream), n & 1u)) return false;
           tc_after();
           if (!scores()) return false;
         }
-        if (!c.wait(c.probs(b), Ctx::phase(n), kErrTimeoutFull)) return false;
-        if (!c.wait(c.full(vr.slot), vr.phase, kErrTimeoutFull)) return false;
+        if (!wait_warp(c, c.probs(b), Ctx::phase(n))) return false;
+        if (!wait_warp(c, c.full(vr.slot), vr.phase)) return false;
         tc_after();
         if (lead) {
           mma_out(o, tmem + Ctx::col_p(stream, n), v_lo + vr.slot * (T::kTileB / 16), j > 0);
           tc_commit(c.out(b));
           tc_commit(c.empty(vr.slot));
         }
-        vr.move(step);
+        vr.move(step, ring);
       }
       job += jobs;
     }
@@ -541,8 +549,8 @@ struct AttnPrefix {
       if (valid < K) {
         // the page that the prefix ends in holds something else after it: zeros for V there
         const uint32_t n = ring0 + 2 * tile + 1;
-        const int slot = static_cast<int>(n % T::kRing);
-        if (!wait_warp(c, c.full(slot), (n / T::kRing) & 1)) return false;
+        const int slot = static_cast<int>(n % c.ring);
+        if (!wait_warp(c, c.full(slot), (n / c.ring) & 1)) return false;
         uint8_t* v = c.base + T::kOffRing + slot * T::kTileB;
         for (int i = valid * 8 + tid; i < K * 8; i += 128)
 #pragma unroll
@@ -600,7 +608,8 @@ struct AttnPrefix {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Ctx c{p, attn_pre_split<D>(p.a.B, p.a.Hq, p.a.Hkv, p.a.prefix_len, gridDim.x), base,
-          smem_u32(base), 0u, 0, 0};
+          smem_u32(base), 0u, 0, 0, 0};
+    c.ring = c.s.pair ? T::kPairRing : T::kRing;
     const int warp = threadIdx.x >> 5;
     constexpr int kCopyWarp = 4 * T::kStreams, kMmaWarp = kCopyWarp + 1;
     if (threadIdx.x == 0) {

@@ -179,6 +179,22 @@ def test_lengths_around_the_tiles(n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B", [5, 16, 32])
+def test_a_long_prefix_many_times(B):
+    # the two streams of a block on the same rows run apart by chance; every wait has to hold
+    import torch
+    pr = Problem(torch, "bf16", B, 32, 8, 128, 16, 32768, [32769 + 5 * i for i in range(B)], "head",
+                 seed=B)
+    with bsgemv.AttnPlan(*pr.plan) as plan:
+        out, lse = pr.run(plan)
+        pr.check(out, lse)
+        for _ in range(400):
+            again, lse2 = pr.run(plan)
+            assert torch.equal(out, again) and torch.equal(lse, lse2)
+        assert plan.device_status() == 0
+
+
+@pytest.mark.gpu
 def test_large_scores_and_a_scale():
     """Scores in the thousands (one position takes nearly all the weight), a negative scale."""
     import torch
