@@ -103,8 +103,12 @@ int bsgemv_attn_run(bsgemv_attn_plan_t plan, const void* q, int64_t q_stride, co
       !aligned_to(prefix_table, 4) || !aligned_to(tables, 4) || !aligned_to(lens, 4) ||
       !aligned_to(lse, 4) || q_stride % 8 || page_stride % 8 || head_stride % 8 || row_stride % 8)
     return BSGEMV_ERR_MISALIGNED;
-  // the line of tiles (attn_stream.cuh) is counted in 32 bits
-  const int64_t row_tiles = (static_cast<int64_t>(B) * (plan->Hq / plan->Hkv) + 15) / 16;
+  const int rows = B * (plan->Hq / plan->Hkv);
+  const int mode = prefix_len == 0 ? kAttnNoPrefix
+                   : attn_prefix_streams(rows, plan->Hkv, plan->D, prefix_len) ? kAttnPrefixStream
+                                                                               : kAttnPrefixTensor;
+  // the line of tiles (attn_stream.cuh, attn_prefix.cuh) is counted in 32 bits
+  const int64_t row_tiles = (rows + kAttnRows - 1) / kAttnRows;
   if (row_tiles * plan->Hkv * (prefix_len / (4096 / plan->D) + 8) >= (int64_t{1} << 30))
     return BSGEMV_ERR_UNSUPPORTED;
   const int rc = decode_check_device(plan->device);
@@ -138,8 +142,6 @@ int bsgemv_attn_run(bsgemv_attn_plan_t plan, const void* q, int64_t q_stride, co
   p.cum = reinterpret_cast<int*>(static_cast<char*>(plan->ws) + plan->at.cum);
   const AttnMaps* maps = maps_of(plan, p);
   if (maps == nullptr) return BSGEMV_ERR_UNSUPPORTED;
-  int mode = prefix_len > 0 ? kAttnPrefixStream : kAttnNoPrefix;
-  if (mode && B * (plan->Hq / plan->Hkv) >= kAttnTensorRows) mode = kAttnPrefixTensor;
   return launch_attn(p, mode, *maps, plan->sms, static_cast<cudaStream_t>(stream));
 }
 

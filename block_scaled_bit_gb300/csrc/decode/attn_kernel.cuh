@@ -45,9 +45,19 @@ struct AttnLayout {
 };
 AttnLayout attn_layout(int Hq, int Hkv, int D, int max_B, int sms);
 
-// Query rows of a kv head from which the prefix goes through the tensor-memory kernel: at 16 rows
-// the streaming kernel reads the prefix once as well, and starts faster.
-constexpr int kAttnTensorRows = 17;
+// Whether the prefix goes through the streaming kernel with the sequences' own positions (one
+// launch fewer, 5 to 7 us faster to start), which reads it once for every 16 query rows of a kv
+// head, or through the tensor-memory kernel, which reads it once for every 128 or 256.  What the
+// streaming kernel reads again comes from L2 and costs about 1 us for 12 MB: it wins up to 80 MB.
+// Measured, us, streaming / tensor, 8 kv heads: D = 128, P = 500, 128 rows 16.3 / 21.6; P = 4096,
+// 64 rows 19.6 / 22.9, 128 rows 30.8 / 26.1; P = 32768, 16 rows 33.6 / 41.4, 32 rows 44.6 / 42;
+// D = 64, P = 32768, 32 rows 27.4 / 29.8, 64 rows 41.8 / 31.0.  At D = 256 its tiles have 16
+// positions and its warps are half as many: it wins up to 8 MB in all (2 kv heads, P = 500,
+// 128 rows 15.6 / 18.3; P = 4096, 16 rows 25.4 / 19.7, 128 rows 28.8 / 24.3).
+inline bool attn_prefix_streams(int rows, int Hkv, int D, int prefix_len) {
+  const int64_t once = int64_t{4} * Hkv * D * prefix_len, tiles = (rows + kAttnRows - 1) / kAttnRows;
+  return D == 256 ? tiles * once <= (int64_t{8} << 20) : (tiles - 1) * once <= (int64_t{80} << 20);
+}
 
 // Tensor maps of the cache: [page][head][row][D], boxes of 64 d and as many rows as a page and a
 // tile of the kernel have (false: the strides cannot be described).

@@ -139,6 +139,13 @@ CASES = [
     ("bf16", 8, 32, 8, 128, 64, 8192, [8193 + 100 * i for i in range(8)], "head"),
     ("f16", 20, 24, 8, 64, 32, 6001, [6002 + 11 * i for i in range(20)], "token"),
     ("bf16", 24, 16, 2, 256, 32, 4096, [4096 + 9 * i for i in range(24)], "token"),
+    # long or wide enough for the tensor-memory kernel: both its modes, ends inside pages and tiles
+    ("bf16", 128, 16, 8, 128, 16, 1501, [1500 + i % 40 for i in range(128)], "head"),
+    ("f16", 40, 24, 8, 128, 32, 3333, [3334 + 5 * i for i in range(40)], "token"),
+    ("bf16", 33, 32, 8, 64, 128, 7001, [7001 + 2 * i for i in range(33)], "token"),
+    ("f16", 24, 32, 8, 64, 8, 9001, [0 if i == 7 else 9001 + i for i in range(24)], "head"),
+    ("f16", 20, 8, 2, 256, 8, 1501, [1502 + 3 * i for i in range(20)], "token"),
+    ("bf16", 70, 16, 2, 256, 64, 1999, [2000 + i for i in range(70)], "head"),
 ]
 
 
