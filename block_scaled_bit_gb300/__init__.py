@@ -2,6 +2,10 @@
 
     y[M, N] = A[M, K] . deq(W)[N, K]^T,   M = 1..32
 
+and, for the rest of a decode step, a mixture-of-experts layer on the same weight formats
+(``bsgemv.MoePlan``), attention over a paged cache with a shared prefix (``bsgemv.AttnPlan``) and
+the pages of that cache (``bsgemv.PageCache``).
+
 The compute path is the C-ABI CUDA library ``libbsgemv.so`` (declared in ``include/bsgemv.h``);
 ``block_scaled_bit_gb300.bsgemv`` is a thin ctypes binding to it (argument marshalling only) and
 ``block_scaled_bit_gb300.synth`` draws seeded synthetic inputs.  Importing this package loads

@@ -5,6 +5,12 @@
 namespace bsg {
 namespace {
 
+// Bound by latency: lengths, then m and l, then rows, each a trip to L2 (64 sequences of 32 heads
+// of 128, 13 parts a row: 14.6 us alone under a profiler with a cold L2).  What does not depend on
+// the parts is worked out while the kernel before still runs; the sequences' stretches too, up to
+// one a thread and 1024 blocks: each block works them all out, beside the streaming kernel (us
+// with / without: 32 blocks 7.7 / 8.4, 768 blocks 38.2 / 40.2, 2048 blocks 73.5 / 72.2); beyond
+// that they are read from the streaming kernel's.
 // One block per (sequence, query head), D / 32 elements a lane.  A row has tens of parts, so
 // nothing is read one after the other: every warp takes a quarter of the parts, each of its lanes
 // fetches one part's m and l, the warp agrees on the weights, then the rows are fetched four at a
@@ -14,14 +20,19 @@ __global__ void __launch_bounds__(128)
     attn_merge(const __grid_constant__ AttnParams p, int mode, int sms) {
   constexpr int kPer = D / 32;
   __shared__ float sums[4][D], tops[4], totals[4];
+  __shared__ int cum[129], tmp[33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.x, b = row / p.Hq, hq = row - b * p.Hq;
   const int G = p.Hq / p.Hkv, h = hq / G, g = hq - h * G;
   pdl_launch_dependents();
-  pdl_wait();
-  const int len = p.lens[b], c0 = __ldcg(p.cum + b), c1 = __ldcg(p.cum + b + 1);
-  const AttnSplit s =
-      attn_split<D>(p, __ldcg(p.cum + p.B), mode == kAttnPrefixStream, sms * kAttnWarps);
+  // (the kernel before has let this one start after everything older was done: lens can be read)
+  const int len = p.lens[b];
+  const bool few = p.B <= 128 && gridDim.x <= 1024;
+  if (few) attn_prefix_sums<D>(p, cum, tmp);
+  else pdl_wait();
+  const int c0 = few ? cum[b] : __ldcg(p.cum + b), c1 = few ? cum[b + 1] : __ldcg(p.cum + b + 1);
+  const AttnSplit s = attn_split<D>(p, few ? cum[p.B] : __ldcg(p.cum + p.B),
+                                    mode == kAttnPrefixStream, sms * kAttnWarps);
   const bool here = len >= max(p.prefix_len, 1);
 
   // The row's parts: the prefix's, then its own; a part is [rows][D] sums, [rows] m, [rows] l.
@@ -62,6 +73,7 @@ __global__ void __launch_bounds__(128)
                         g % kAttnRows);
   }
   const int all = pre.count + own.count;
+  if (few) pdl_wait();
   const int n0 = all * warp / 4, n = all * (warp + 1) / 4;  // this warp's
   float o[kPer], m = -INFINITY, l = 0.f;
 #pragma unroll

@@ -7,7 +7,9 @@
 // tile and 64 d, 128-byte swizzle), two tiles in flight, no synchronisation but the warp's own;
 // scores and P V on mma.sync m16n8k16, softmax in registers with the running maximum in base 2.
 // (Loaded by cp.async, 32 of them a lane and tile with two shuffles each for the rows' places, the
-// loads took as many instructions as the products.)
+// loads took as many instructions as the products.  Eight warps with tiles of 8 KB are no faster.)
+// Measured: 64 sequences with 530 own positions on average, 8 kv heads of 128: 139 MB in 31 us; in
+// its loop 6.5 TB/s, before it 3.4 us until the first tile has come.
 //
 // All tiles of all (sequence, kv head, row tile) are laid in a line and cut into equal ranges, one
 // per warp, so that the lengths' spread does not matter; a unit counts kAttnCost tiles more than

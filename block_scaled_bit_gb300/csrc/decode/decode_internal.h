@@ -26,11 +26,6 @@ int decode_alloc(void** out, size_t bytes);
 // Synchronise `stream`, read and clear an error word: the status it stands for.
 int decode_error_status(unsigned* err, void* stream);
 
-// cudaGetLastError as a status.
-inline int decode_launched() {
-  return cudaGetLastError() == cudaSuccess ? BSGEMV_OK : BSGEMV_ERR_CUDA;
-}
-
 // A tiled tensor map with zero fill (strides in bytes, from the second dimension on).
 int decode_encode(CUtensorMap* tm, CUtensorMapDataType type, int rank, const void* base,
                   const uint64_t* dims, const uint64_t* strides, const uint32_t* box,

@@ -7,7 +7,12 @@
 //
 // Bound: the active experts' weights are read once from HBM (their bytes over the copy bandwidth);
 // a few tokens per expert make the arithmetic small.  So the kernel is a weight stream: a copy
-// warp keeps a ring of 16 KB weight boxes in flight, eight warps decode and multiply.
+// warp keeps a ring of 16 KB weight boxes in flight, four warps decode and multiply, two blocks an
+// SM.  What bounds it in fact: FP8 the stream (both products with routing: 32 tokens, 64 experts,
+// top 6, H 4096, I 1408, 1.09 GB in 222 us, 4.9 TB/s, 0.73 of the measured copy); NVFP4 and
+// int8 the decoding, 1600 to 2000 cycles a stage and warp where the copy needs 700 (8 tokens,
+// 137 MB in 57 us; 13 tokens with zero points, 282 MB in 112 us); one token its chain of start,
+// first load, cold code and sums (14 MB in 23 us).
 //
 // Work.  A tile is 128 weight rows of one expert -- for UP 64 gate rows and the 64 up rows that
 // belong to them, arranged so that an mma fragment holds a gate row g and its up row g + 8 in the
@@ -16,6 +21,11 @@
 // DOWN's are 128 columns over all experts' k = I in turn, so that an output is summed in one
 // place.  All stages are cut into equal ranges, one per block; a tile cut by a range boundary is
 // finished by the last block to arrive, which adds the parts in block order (deterministic).
+// A decode warp takes two of the tile's eight fragments, so that the activations' loads, the waits
+// and the ring's arithmetic serve 32 rows (eight warps with one each issued 430 to 460
+// instructions a stage, which bound the kernel: 59 / 119 / 231 us in the three cases above; three
+// blocks an SM, where a call's tokens let the registers reach, are 2 % faster with NVFP4 and no
+// faster with int4).
 //
 // The weights go through mma.sync m16n8k16 as the A operand, decoded to f16 (every format's codes
 // are exact in f16, and the decoders to bf16 take three conversions more per pair at a quarter
