@@ -6,9 +6,9 @@
 // for the rows r = (expert e_r, token t_r) that the routing lists, expert by expert.
 //
 // Bound: the active experts' weights are read once from HBM (their bytes over the copy bandwidth);
-// a few tokens per expert make the arithmetic small.  So the kernel is a weight stream: a copy
-// warp keeps a ring of 16 KB weight boxes in flight, four warps decode and multiply, two blocks an
-// SM.  What bounds it in fact: FP8 the stream (both products with routing: 32 tokens, 64 experts,
+// a few tokens per expert make the arithmetic small.  So the kernel is a weight stream: two copy
+// warps (weights and activations, scales and zero points) keep a ring of 16 KB weight boxes in
+// flight, four warps decode and multiply, two blocks an SM.  What bounds it in fact: FP8 the stream (both products with routing: 32 tokens, 64 experts,
 // top 6, H 4096, I 1408, 1.09 GB in 222 us, 4.9 TB/s, 0.73 of the measured copy); NVFP4 and
 // int8 the decoding, 1600 to 2000 cycles a stage and warp where the copy needs 700 (8 tokens,
 // 137 MB in 57 us; 13 tokens with zero points, 282 MB in 112 us); one token its chain of start,
@@ -66,7 +66,7 @@ BSG_DEV void tma_load_4d_hint(uint32_t dst, const CUtensorMap* tm, int x, int y,
 
 constexpr int kMoeFrags = 8;                          // mma fragments of 16 weight rows in a tile
 constexpr int kMoeWarps = kMoeFrags / 2;              // decode warps, two fragments each
-constexpr int kMoeThreads = 32 * (kMoeWarps + 1);     // and a copy warp
+constexpr int kMoeThreads = 32 * (kMoeWarps + 2);     // and two copy warps
 constexpr int kMoeTileRows = 16 * kMoeFrags;
 constexpr int kMoeBoxB = kMoeTileRows * 128;
 
@@ -226,7 +226,7 @@ struct MoeGemm {
     w.left -= w.n;
   }
 
-  // ---------------------------------------------------------------- copy warp
+  // ---------------------------------------------------------------- copy warps
   static BSG_DEV int weight_row(const Ctx& c, const Run& w) {
     return c.expert(w.a) * c.p.rows + w.tile * c.p.step;
   }
@@ -313,38 +313,53 @@ struct MoeGemm {
     }
   }
 
-  // The weight box, scales and zero points of the stages of one run, in order.
-  struct Weights {
-    int e, row;  // expert, first row of the tile
-    Side s, z;
-  };
-  static BSG_DEV Weights weights_of(const Ctx& c, const Run& w, int lane) {
+  // The second copy warp: scales and zero points of every stage in order, as far ahead as the ring
+  // allows (they depend on no kernel before).
+  static BSG_DEV void produce_sides(const Ctx& c, int lane) {
     const MoeGemmParams& p = c.p;
-    Weights x;
-    x.e = c.expert(w.a);
-    x.row = w.tile * p.step;
-    const int row = weight_row(c, w);
-    // (where DOWN's last tile is half empty, its first half's scales again)
-    const int second = DOWN && x.row + 64 >= p.rows ? 0 : p.second;
-    x.s = side_of(p.scales, p.s_pitch, p.s_end, p.s_unit, p.s_stride, p.s_bytes, w, row, second, lane);
-    if (kInts && p.zp)
-      x.z = side_of(p.zp, p.z_pitch, p.z_end, p.z_unit, p.z_stride, p.z_bytes, w, row, second, lane);
-    return x;
-  }
-  static BSG_DEV void issue_weights(const Ctx& c, Weights& x, int ks, int slot, uint64_t pol,
-                                    int lane) {
-    // one box: 128 rows, or 64 gate rows and the up rows that belong to them
-    if (lane == 0)
-      tma_load_4d_hint(c.base_u + slot * kMoeBoxB, &c.p.tm, ks * 128, x.row, 0, x.e, c.full(slot), pol);
-    const uint32_t side = c.base_u + c.p.off_side + slot * c.p.side_bytes;
-    side_copy(x.s, side, lane);
-    if (kInts && c.p.zp) side_copy(x.z, side + kMoeTileRows * c.p.s_stride, lane);
+    Run w = first_run(c);
+    int slot = 0, i = 0;
+    uint32_t phase = 1;
+    while (true) {
+      const int row = weight_row(c, w);
+      // (where DOWN's last tile is half empty, its first half's scales again)
+      const int second = DOWN && w.tile * p.step + 64 >= p.rows ? 0 : p.second;
+      Side x = side_of(p.scales, p.s_pitch, p.s_end, p.s_unit, p.s_stride, p.s_bytes, w, row, second, lane);
+      Side z = x;
+      if (kInts && p.zp)
+        z = side_of(p.zp, p.z_pitch, p.z_end, p.z_unit, p.z_stride, p.z_bytes, w, row, second, lane);
+      for (int k = 0; k < w.n; ++k, ++i) {
+        if (i >= p.stages &&
+            !__all_sync(0xFFFFFFFFu, mbar_wait(c.empty(slot), phase, p.err, kErrTimeoutEmpty, p.wait_ns))) {
+          if (lane == 0) *c.abort_word() = 1u;
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          return;
+        }
+        const uint32_t side = c.base_u + p.off_side + slot * p.side_bytes, full = c.full(slot);
+        side_copy(x, side, lane);
+        if (kInts && p.zp) side_copy(z, side + kMoeTileRows * p.s_stride, lane);
+        cp_async_mbar_arrive(full);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+        if (++slot == p.stages) { slot = 0; phase ^= 1u; }
+      }
+      if (w.left == 0) break;
+      next_run(c, w);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
 
-  // Weights, scales and activations of every stage in order, as far ahead as the rings allow.
-  // Where the routing is older than the kernel before this one, the first weights go out before
-  // the wait for that kernel (they do not depend on it).  Everything that a run's stages share is worked out once per
-  // run: this warp's time per stage bounds the block's rate.  Returns the stages issued.
+  // One box: 128 rows, or 64 gate rows and the up rows that belong to them.
+  static BSG_DEV void issue_box(const Ctx& c, const Run& w, int ks, int slot, uint64_t pol) {
+    tma_load_4d_hint(c.base_u + slot * kMoeBoxB, &c.p.tm, ks * 128, w.tile * c.p.step, 0, c.expert(w.a),
+                     c.full(slot), pol);
+  }
+
+  // The first copy warp: weights and activations of every stage in order, as far ahead as the rings
+  // allow.  Where the routing is older than the kernel before this one, the first weights go out
+  // before the wait for that kernel (they do not depend on it).  Everything that a run's stages
+  // share is worked out once per run: this warp's time per stage bounds the block's rate.  Returns
+  // the stages issued.
   static BSG_DEV int produce(const Ctx& c, int lane) {
     const MoeGemmParams& p = c.p;
     const uint64_t pol = policy_evict_first();
@@ -354,12 +369,12 @@ struct MoeGemm {
     if constexpr (!kByToken) {
       Run e = w;
       while (early < p.stages) {
-        Weights x = weights_of(c, e, lane);
         const int most = min(e.n, p.stages - early);
-        for (int i = 0; i < most; ++i, ++early) {
-          if (lane == 0) mbar_expect_tx(c.full(early), kMoeBoxB);
-          issue_weights(c, x, e.ks + i, early, pol, lane);
-        }
+        for (int i = 0; i < most; ++i, ++early)
+          if (lane == 0) {
+            mbar_expect_tx(c.full(early), kMoeBoxB);
+            issue_box(c, e, e.ks + i, early, pol);
+          }
         if (e.left == 0) break;
         next_run(c, e);
       }
@@ -369,7 +384,6 @@ struct MoeGemm {
     int tslot = 0, tail_m = rows_of(c, tail.a);
     uint32_t tphase = 0;
     while (true) {
-      Weights x = weights_of(c, w, lane);
       const int r0 = c.off(w.a), m = c.off(w.a + 1) - r0;
       const uint32_t tx = m * kRowB;
       // by token: lane j < m copies token j's row; else lane 0 copies all rows, lane 1 those past
@@ -383,7 +397,6 @@ struct MoeGemm {
           if (!__all_sync(0xFFFFFFFFu, mbar_wait(c.empty(tslot), tphase, p.err, kErrTimeoutEmpty,
                                                  p.wait_ns))) {
             if (lane == 0) *c.abort_word() = 1u;
-            asm volatile("cp.async.wait_all;" ::: "memory");
             return i;
           }
           used -= tail_m;
@@ -397,12 +410,7 @@ struct MoeGemm {
         const uint32_t full = c.full(slot);
         if (lane == 0) mbar_expect_tx(full, i < early ? tx : tx + kMoeBoxB);
         __syncwarp();  // the bytes are expected before any lane's copy can complete
-        if (i >= early) {
-          issue_weights(c, x, w.ks + k, slot, pol, lane);
-        } else {
-          x.s.src += x.s.bytes;
-          if (kInts && p.zp) x.z.src += x.z.bytes;
-        }
+        if (i >= early && lane == 0) issue_box(c, w, w.ks + k, slot, pol);
         if constexpr (!kByToken) {
           const int here = min(m, p.row_cap - head);
           if (lane == 0) bulk_load(c.base_u + p.off_rows + head * kRowB, src, here * kRowB, full);
@@ -414,7 +422,6 @@ struct MoeGemm {
             bulk_load(c.base_u + p.off_rows + wrap(c, head + lane) * kRowB, src, kRowB, full);
           src += kRowB;
         }
-        cp_async_mbar_arrive(full);
         __syncwarp();
         if (lane == 0) mbar_arrive(full);
         used += m;
@@ -425,7 +432,6 @@ struct MoeGemm {
       if (w.left == 0) break;
       next_run(c, w);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
     return i;
   }
 
@@ -981,7 +987,7 @@ struct MoeGemm {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
       for (int i = 0; i < p.stages; ++i) {
-        mbar_init(c.full(i), 1);
+        mbar_init(c.full(i), 2);  // the copy warps
         mbar_init(c.empty(i), kMoeWarps);
       }
       *c.abort_word() = 0u;
@@ -1012,7 +1018,8 @@ struct MoeGemm {
       c.s1 = start(c, blockIdx.x + 1);
       int issued = 0;
       if (warp == 0) issued = produce(c, lane);
-      else work(c, warp - 1, lane);
+      else if (warp == 1) produce_sides(c, lane);
+      else work(c, warp - 2, lane);
       __syncthreads();
       if (*c.abort_word() != 0u && threadIdx.x == 0) drain(c, issued);
     } else if constexpr (!kByToken) {
