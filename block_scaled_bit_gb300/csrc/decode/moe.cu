@@ -95,6 +95,7 @@ int run(bsgemv_moe_plan_s* p, const void* x, const void* logits, const int32_t* 
   q.counters_up = reinterpret_cast<unsigned*>(w + p->at.counters_up);
   q.counters_packed = reinterpret_cast<unsigned*>(w + p->at.counters_packed);
   q.counters_down = reinterpret_cast<unsigned*>(w + p->at.counters_down);
+  q.counters_group = reinterpret_cast<unsigned*>(w + p->at.counters_group);
   q.partials = reinterpret_cast<float*>(w + p->at.partials);
   q.h = reinterpret_cast<float*>(w + p->at.h);
   q.x_packed = reinterpret_cast<uint8_t*>(w + p->at.x_packed);

@@ -81,6 +81,7 @@ struct MoeGemmParams {
   const float* gscale;        // NVFP4: [E]
   float* partials;
   unsigned *counters, *err;
+  unsigned* group_counters;   // DOWN: of eight neighbours' parts, by (first block, it opens the tile)
   float* h;                   // UP: [rows][I]
   uint8_t* h_packed;          // UP: [row][stage of I][2 pitches]
   unsigned* packed;           // UP: [active expert][stage of I] warps that have stored into it
@@ -740,15 +741,20 @@ struct MoeGemm {
     __syncwarp();
   }
 
-  // y of element idx of fragments 2 cw, 2 cw + 1's sums ([2][T][16]).
-  static BSG_DEV void store_y(const Ctx& c, int cw, int tile, int idx, float v) {
+  // y of elements idx .. idx + 3 of fragments 2 cw, 2 cw + 1's sums ([2][T][16]).
+  static BSG_DEV void store_y(const Ctx& c, uint32_t nan_rows, int cw, int tile, int idx, float4 v) {
     const int second = idx >= c.p.T * 16, t = (idx >> 4) - (second ? c.p.T : 0);
-    if ((c.p.route->nan_rows >> t) & 1u) v = __int_as_float(0x7FC00000);
+    if ((nan_rows >> t) & 1u) v.x = v.y = v.z = v.w = __int_as_float(0x7FC00000);
     const int64_t n = static_cast<int64_t>(tile) * kMoeTileRows + 16 * (2 * cw + second) + (idx & 15);
     if (n >= c.p.out_pitch) return;  // (H is a multiple of 64: the last tile may be half empty)
-    const int64_t at = t * c.p.out_pitch + n;
-    c.p.y[at] = c.p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v))
-                         : __half_as_ushort(__float2half_rn(v));
+    uint2 two;
+    if (c.p.bf16) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+      two = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    } else {
+      two = make_uint2(pack_f16(v.x, v.y), pack_f16(v.z, v.w));
+    }
+    *reinterpret_cast<uint2*>(c.p.y + t * c.p.out_pitch + n) = two;
   }
 
   // Block that holds stage s, and the first stage of block b's range.
@@ -765,53 +771,104 @@ struct MoeGemm {
     return c.p.partials + ((static_cast<int64_t>(block) * 2 + which) * kMoeFrags + v) * c.p.slot_floats;
   }
 
+  // Arrive at a counter that `need` warps come to, after this warp's stores: whether this is the
+  // last one (the counter is zero again then).
+  static BSG_DEV bool last_to(unsigned* counter, int need, int lane) {
+    __syncwarp();
+    unsigned old = 0;
+    if (lane == 0) old = atom_add_acq_rel_gpu(counter, 1u);
+    old = __shfl_sync(0xFFFFFFFFu, old, 0);
+    if (old != static_cast<unsigned>(need - 1)) return false;
+    __syncwarp();
+    if (lane == 0) *counter = 0u;
+    return true;
+  }
+
+  // DOWN: the sum of n parts of the warp's two fragments, in order: part 0 at src0, part j > 0 at
+  // src + j * stride; to y (dst nullptr) or to dst.  A lane takes four columns of a token at a
+  // time, two of them and eight parts in flight.
+  static BSG_DEV void sum_parts(const Ctx& c, const Lane& L, int tile, const float* src0,
+                                const float* src, int64_t stride, int n, float* dst) {
+    const int all = c.p.T * 32;
+    const uint32_t nan_rows = c.p.route->nan_rows;
+    const auto at = [&](int i) { return i < c.p.T * 16 ? i : i - c.p.T * 16 + c.p.slot_floats; };
+    for (int i = 4 * L.lane; i < all; i += 256) {
+      const bool two = i + 128 < all;
+      float v[2][4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[0][x] = v[1][x] = 0.f;
+      for (int b0 = 0; b0 < n; b0 += 8) {
+        float4 u[2][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float* part = b0 + j ? src + (b0 + j) * stride : src0;
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            u[x][j] = b0 + j < n && (x == 0 || two)
+                          ? __ldcg(reinterpret_cast<const float4*>(part + at(i + 128 * x)))
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            v[x][0] += u[x][j].x;
+            v[x][1] += u[x][j].y;
+            v[x][2] += u[x][j].z;
+            v[x][3] += u[x][j].w;
+          }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (x && !two) break;
+        if (dst) {
+          __stcg(reinterpret_cast<float4*>(dst + at(i + 128 * x)),
+                 make_float4(v[x][0], v[x][1], v[x][2], v[x][3]));
+        } else {
+          store_y(c, nan_rows, L.cw, tile, i + 128 * x, make_float4(v[x][0], v[x][1], v[x][2], v[x][3]));
+        }
+      }
+    }
+  }
+
   // A part of a tile is in the workspace: the last of its blocks to come adds the parts, in block
   // order, and finishes the tile.  (The parts' loads go out eight at a time; one after the other
-  // they took longer than the products of a small call.)
+  // they took longer than the products of a small call.)  DOWN's tiles can have dozens of parts
+  // (few tiles, many blocks) of up to 4 KB a warp: then eight neighbours' are added by the last of them
+  // first, in the first one's place, and these sums by the last group (one warp adding 38 parts of
+  // 28 tokens took 20 us; 16 parts of one token take 1.5 us more by groups).
   static BSG_DEV void arrive(const Ctx& c, const Lane& L, int number, Packing& k) {
     const int len = tile_len(c), x0 = number * len;
     const int first = owner(c, x0), last = owner(c, x0 + len - 1);
-    __syncwarp();
-    unsigned old = 0;
-    if (L.lane == 0) old = atom_add_acq_rel_gpu(c.p.counters + number * kMoeWarps + L.cw, 1u);
-    old = __shfl_sync(0xFFFFFFFFu, old, 0);
-    if (old != static_cast<unsigned>(last - first)) return;
-    __syncwarp();
-    if (L.lane == 0) c.p.counters[number * kMoeWarps + L.cw] = 0u;
     // the first block's part opens the tile, the others' continue it
-    const int64_t stride = static_cast<int64_t>(c.p.slot_floats) * (2 * kMoeFrags);  // of two blocks
+    int64_t stride = static_cast<int64_t>(c.p.slot_floats) * (2 * kMoeFrags);  // of two blocks
     const float* src0 = partial(c, first, 1, 2 * L.cw);
     const float* src = partial(c, first, 0, 2 * L.cw);  // + (b - first) * stride
-    const int n = last - first + 1;
+    int n = last - first + 1;
+    unsigned* counter = c.p.counters + number * kMoeWarps + L.cw;
     if constexpr (DOWN) {
-      // a lane takes four columns of a token at a time, eight parts in flight
-      for (int i = 4 * L.lane; i < c.p.T * 32; i += 128) {
-        const int at = i < c.p.T * 16 ? i : i - c.p.T * 16 + c.p.slot_floats;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int b0 = 0; b0 < n; b0 += 8) {
-          float4 u[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            u[j] = b0 + j < n ? __ldcg(reinterpret_cast<const float4*>(
-                                    (b0 + j ? src + (b0 + j) * stride : src0) + at))
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            v[0] += u[j].x;
-            v[1] += u[j].y;
-            v[2] += u[j].z;
-            v[3] += u[j].w;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) store_y(c, L.cw, number, i + j, v[j]);
+      // rounds of loads, one after the other: all by one warp, or by groups and then their sums,
+      // and some three rounds' time for the second counter
+      const int per = (c.p.T + 7) / 8;
+      if ((n + 7) / 8 * per > (1 + (n + 63) / 64) * per + 3) {
+        const int group = (static_cast<int>(blockIdx.x) - first) >> 3, lead = first + 8 * group;
+        const int opens = group == 0, size = min(8, n - 8 * group);
+        if (!last_to(c.p.group_counters + (2 * lead + opens) * kMoeWarps + L.cw, size, L.lane)) return;
+        float* to = partial(c, lead, opens, 2 * L.cw);
+        sum_parts(c, L, number, to, partial(c, lead, 0, 2 * L.cw), stride, size, to);
+        n = (n + 7) >> 3;
+        stride *= 8;
       }
+      if (last_to(counter, n, L.lane)) sum_parts(c, L, number, src0, src, stride, n, nullptr);
     } else {
+      if (!last_to(counter, n, L.lane)) return;
+      const int a = number / c.p.tiles, m = rows_of(c, a);
       float acc[2][MT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) acc[0][mt][x] = acc[1][mt][x] = 0.f;
+        if (8 * mt >= m) continue;
         for (int b0 = 0; b0 < n; b0 += 4) {
           float4 u[2][4];
 #pragma unroll
@@ -834,7 +891,6 @@ struct MoeGemm {
             }
         }
       }
-      const int a = number / c.p.tiles;
       pack_before(c, L, k);
       store_h(c, L, a, number - a * c.p.tiles, acc);
       pack_after(k, a, number - a * c.p.tiles);
@@ -942,7 +998,9 @@ struct MoeGemm {
           const int x0 = w.tile * tile_len(c);
           float* sum = c.sums(2 * cw);
           if (tile_ends && seg == x0) {
-            for (int i = lane; i < p.T * 32; i += 32) store_y(c, cw, w.tile, i, sum[i]);
+            const uint32_t nan_rows = p.route->nan_rows;
+            for (int i = 4 * lane; i < p.T * 32; i += 128)
+              store_y(c, nan_rows, cw, w.tile, i, *reinterpret_cast<const float4*>(sum + i));
           } else {
             float* dst = partial(c, blockIdx.x, seg == x0 ? 1 : 0, 2 * cw);
             for (int i = 4 * lane; i < p.T * 32; i += 128)
@@ -967,8 +1025,9 @@ struct MoeGemm {
                 reinterpret_cast<float4*>(partial(c, blockIdx.x, opens ? 1 : 0, 2 * cw + f)) + lane;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
-              __stcg(dst + mt * 32,
-                     make_float4(acc[f][mt][0], acc[f][mt][1], acc[f][mt][2], acc[f][mt][3]));
+              if (8 * mt < m)
+                __stcg(dst + mt * 32,
+                       make_float4(acc[f][mt][0], acc[f][mt][1], acc[f][mt][2], acc[f][mt][3]));
           }
           arrive(c, L, w.a * p.tiles + w.tile, packing);
         }

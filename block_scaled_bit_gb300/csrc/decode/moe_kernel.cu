@@ -237,6 +237,7 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
   p.gscale = w.gscale;
   p.partials = c.partials;
   p.counters = down ? c.counters_down : c.counters_up;
+  p.group_counters = c.counters_group;
   p.err = c.err;
   p.h = c.h;
   p.h_packed = c.h_packed;
@@ -325,6 +326,7 @@ MoeLayout moe_layout(int fmt, int64_t H, int64_t I, int E, int top_k, int max_T,
   l.counters_up = take(active * (I / 64) * kMoeWarps * sizeof(unsigned));
   l.counters_packed = take(active * (static_cast<size_t>(I) / 128 + 1) * sizeof(unsigned));
   l.counters_down = take(static_cast<size_t>(H / 64) * kMoeWarps * sizeof(unsigned));
+  l.counters_group = take(ctas * 2 * kMoeWarps * sizeof(unsigned));
   l.partials = take(ctas * 2 * kMoeFrags * slot * sizeof(float));
   l.h = take(rows * I * sizeof(float));
   const bool four = fmt == kInt4 || fmt == kNvfp4;

@@ -55,6 +55,7 @@ struct MoeParams {
   uint16_t* y;
   unsigned* err;
   unsigned *counters_up, *counters_down;  // arrivals per (tile, decode warp), left at zero
+  unsigned* counters_group;               // ... per (block, its part opens the tile, decode warp)
   unsigned* counters_packed;              // ... per (active expert, stage of I)
   float* partials;
   Routing* route;
@@ -80,7 +81,7 @@ inline MoeWeight weight_of(int fmt, int bs, int has_zp, int64_t rows, int64_t k,
 
 // The workspace's parts, in bytes from its start (the error word is at 0).
 struct MoeLayout {
-  size_t route, counters_up, counters_packed, counters_down, partials, h, x_packed, h_packed, total;
+  size_t route, counters_up, counters_packed, counters_down, counters_group, partials, h, x_packed, h_packed, total;
 };
 MoeLayout moe_layout(int fmt, int64_t H, int64_t I, int E, int top_k, int max_T, int sms);
 

@@ -135,6 +135,13 @@ CASES = [
     ("nvfp4", "bf16", 16, False, 832, 448, 4, 1, 32, 32),
     ("nvfp4", "bf16", 16, False, 2048, 512, 12, 8, 7, 8),
     ("int4", "bf16", 32, False, 2048, 512, 16, 8, 13, 32),
+    # few columns of y over many k: a tile's parts come from a hundred blocks and more
+    ("fp8", "bf16", 128, False, 128, 1408, 11, 6, 32, 32),
+    ("int8", "f16", 32, True, 64, 1152, 30, 4, 27, 32),
+    ("nvfp4", "f16", 16, False, 192, 1472, 40, 8, 6, 8),
+    ("int4", "f16", 32, True, 320, 1024, 24, 7, 30, 30),
+    # k over many stages, few experts: UP's tiles too
+    ("fp8", "f16", 128, False, 4096, 128, 2, 2, 19, 32),
 ]
 
 
