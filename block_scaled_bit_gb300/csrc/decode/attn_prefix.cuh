@@ -4,9 +4,9 @@
 // once for every 256 rows.  Bound: 128 rows give 128 flops a byte of K and V, 256 rows 256, so
 // up to there the kernel is a memory stream, beyond it the tensor cores' and the exponentials'.
 // Measured: 256 rows, 8 kv heads of 128, 32768 positions: 35 us for 134 MB and 34 Gflop, of which
-// 0.9 us for each of the 27 key tiles of a block (softmax 1250 cycles a job, the MMAs 1280 for both
-// streams: scores of 64 columns take 48 cycles each, the rate of shared memory), 3.4 before the
-// first scores, 4 to write the parts.  384 rows, 2 kv heads of 256, 16384 positions in pages of 16:
+// 0.9 us for each of the 27 key tiles of a block (softmax 1250 cycles a job, the MMAs some 1280 for
+// both streams: scores of 64 columns take 48 cycles a step, the rate of shared memory), 3.4 us
+// before the first scores, 4 to write the parts.  384 rows, 2 kv heads of 256, 16384 positions in pages of 16:
 // 22 us, 1.2 us a tile: its K and V come as 32 boxes of 2 KB, three times from L2.
 //
 // A block (one per SM) holds two streams of work, each a warpgroup with its own running maximum and

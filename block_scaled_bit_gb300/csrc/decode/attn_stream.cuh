@@ -58,8 +58,8 @@ BSG_DEV int own_tiles(const AttnParams& p, int b) {
   return (len + K - 1) / K - p.prefix_len / K;
 }
 
-// cum[b] = stretch (tiles and cost) of one (head, row tile) of the sequences before b, b <= B, by the whole block;
-// cum must hold B + 1 integers, tmp 33.
+// cum[b] = stretch (tiles and cost) of one (head, row tile) of the sequences before b, b <= B, by
+// the whole block; cum must hold B + 1 integers, tmp 33.
 template <int D>
 BSG_DEV void attn_prefix_sums(const AttnParams& p, int* cum, int* tmp) {
   const int n = blockDim.x, per = (p.B + n - 1) / n, lane = threadIdx.x & 31, w = threadIdx.x >> 5;

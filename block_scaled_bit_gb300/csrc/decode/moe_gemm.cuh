@@ -9,10 +9,10 @@
 // a few tokens per expert make the arithmetic small.  So the kernel is a weight stream: two copy
 // warps (weights and activations, scales and zero points) keep a ring of 16 KB weight boxes in
 // flight, four warps decode and multiply, two blocks an SM.  What bounds it in fact: FP8 the stream (both products with routing: 32 tokens, 64 experts,
-// top 6, H 4096, I 1408, 1.09 GB in 222 us, 4.9 TB/s, 0.73 of the measured copy); NVFP4 and
+// top 6, H 4096, I 1408, 1.09 GB in 216 us, 5.1 TB/s, 0.75 of the measured copy); NVFP4 and
 // int8 the decoding, 1600 to 2000 cycles a stage and warp where the copy needs 700 (8 tokens,
-// 137 MB in 57 us; 13 tokens with zero points, 282 MB in 112 us); one token its chain of start,
-// first load, cold code and sums (14 MB in 23 us).
+// 137 MB in 57 us; 13 tokens with zero points, 282 MB in 105 us; a second copy warp took 5 us off
+// that); one token its chain of start, first load, cold code and sums (14 MB in 24 us).
 //
 // Work.  A tile is 128 weight rows of one expert -- for UP 64 gate rows and the 64 up rows that
 // belong to them, arranged so that an mma fragment holds a gate row g and its up row g + 8 in the
@@ -27,7 +27,9 @@
 // blocks an SM, where a call's tokens let the registers reach, are 2 % faster with NVFP4 and no
 // faster with int4).
 //
-// The weights go through mma.sync m16n8k16 as the A operand, decoded to f16 (every format's codes
+// The weights go through mma.sync m16n8k16 as the A operand (an expert's one to four tokens would
+// leave nearly all of a tcgen05 tile's columns empty, and its weights would have to be decoded into
+// shared memory first), decoded to f16 (every format's codes
 // are exact in f16, and the decoders to bf16 take three conversions more per pair at a quarter
 // of the rate), and the tokens as B, eight per tile and at most MT tiles; the decoders and the k
 // permutation are the GEMV's.  The activations come packed for this (x beside the routing, h by

@@ -102,7 +102,8 @@ BSG_DEV void pack_x(const MoeParams& p, int t, int ks, uint8_t* dst, int lane) {
 }
 
 // x packed by the routing's rows, one warp per row and stage (more than 8 tokens: an expert's rows
-// then come by one copy a stage, which saves more than this kernel's 3 us).
+// then come by one copy a stage, which saves more than this kernel's 3 us: FP8, 32 tokens, 231 us
+// for the call where copies of single rows took 239; 13 tokens the same either way).
 template <int PER>
 __global__ void __launch_bounds__(256) moe_pack_rows(const __grid_constant__ MoeParams p, int spt) {
   pdl_wait();
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(256) moe_pack_rows(const __grid_constant__ Moe
   pack_x<PER>(p, p.route->token[r], ks, p.x_packed + row * moe_pitch(PER == 8), threadIdx.x & 31);
 }
 
+// Bound by latency (logits, then one block's reductions and sums; with the start some 4 us a call).
 // Block 0 routes: a warp per token, then a thread per expert.  The other blocks (up to 8 tokens)
 // pack x, one warp per token and stage.
 __global__ void __launch_bounds__(1024) moe_route(const __grid_constant__ MoeParams p, int spt) {

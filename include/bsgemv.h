@@ -345,8 +345,9 @@ int bsgemv_dense_destroy(bsgemv_dense_plan_t plan);
  *
  * x, y and (unless BSGEMV_MOE_LOGITS_F32) the logits are in the activation dtype.  Sums, softmax
  * and the intermediate are fp32 (the intermediate enters the second product as two f16 parts with
- * a power of two for every 128 or 256 of a row, 22 bits of the largest); y is rounded once.  An expert's weights are read
- * once for all tokens that chose it, and other experts' weights are not read.  A logit of -inf is
+ * a power of two for every 128 or 256 of a row: to 2^-22 of the largest of them); y is rounded
+ * once.  An expert's weights are read once for all tokens that chose it, and other experts' weights
+ * are not read.  A logit of -inf is
  * never chosen; a row with nothing to choose gives y = 0.  A row that holds a NaN or +inf logit
  * gives NaN, as the softmax has it.  What one token chose never reaches another token's row, NaN
  * weights included.
