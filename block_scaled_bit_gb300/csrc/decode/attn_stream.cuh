@@ -152,7 +152,6 @@ BSG_DEV AttnUnit attn_unit_at(const AttnParams& p, const AttnSplit& s, const int
   u.first = cum[a] * per + i * len + kAttnCost;
   u.lo = p.prefix_len;
   u.hi = p.lens[a];
-  (void)K;
   return u;
 }
 

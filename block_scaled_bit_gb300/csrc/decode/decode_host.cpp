@@ -65,7 +65,8 @@ int decode_alloc(void** out, size_t bytes) {
     *out = nullptr;
     return BSGEMV_ERR_CUDA;
   }
-  if (cudaMemset(*out, 0, bytes) != cudaSuccess) {
+  // (waited for: the first call may come on a stream that does not follow the default one)
+  if (cudaMemset(*out, 0, bytes) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) {
     cudaGetLastError();
     cudaFree(*out);
     *out = nullptr;

@@ -175,7 +175,17 @@ int bsgemv_moe_device_status(bsgemv_moe_plan_t plan, void* stream) {
   if (plan == nullptr) return BSGEMV_ERR_INVALID_ARG;
   const int rc = decode_check_device(plan->device);
   if (rc != BSGEMV_OK) return rc;
-  return decode_error_status(static_cast<unsigned*>(plan->ws), stream);
+  const int status = decode_error_status(static_cast<unsigned*>(plan->ws), stream);
+  // a call whose wait ran out left arrivals in the counters: the next one starts from zero again
+  if (status == BSGEMV_ERR_DEVICE_TIMEOUT &&
+      (cudaMemsetAsync(static_cast<char*>(plan->ws) + plan->at.counters_up, 0,
+                       plan->at.partials - plan->at.counters_up,
+                       static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+       cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)) {
+    cudaGetLastError();
+    return BSGEMV_ERR_CUDA;
+  }
+  return status;
 }
 
 int bsgemv_moe_destroy(bsgemv_moe_plan_t plan) {

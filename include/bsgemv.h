@@ -386,7 +386,9 @@ int bsgemv_moe_run_routed(bsgemv_moe_plan_t plan, const void* x, const int32_t* 
                           const void* zp13, const void* W2, const void* scales2, const void* zp2,
                           void* y, int T, void* stream);
 
-/* Synchronise `stream`, then read and clear the plan's error word (as bsgemv_device_status). */
+/* Synchronise `stream`, then read and clear the plan's error word (as bsgemv_device_status).  After
+ * BSGEMV_ERR_DEVICE_TIMEOUT the plan can be used again; calls between the failed one and this are
+ * not to be relied on. */
 int bsgemv_moe_device_status(bsgemv_moe_plan_t plan, void* stream);
 
 /* Free the plan (synchronises the device first).  NULL is a no-op. */
