@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(128)
     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
     const float next = fmaxf(m, top), base = next == -INFINITY ? 0.f : next;
     const float keep = ex2(m - base);
-    // a part without positions has m = -inf: its sums may not be written and are not read
+    // (only a part without positions has m = -inf: its sums may not be written and are not read)
     const float take = mi == -INFINITY ? 0.f : ex2(mi - base);
     float sum = mi == -INFINITY ? 0.f : li * take;
 #pragma unroll

@@ -4,6 +4,9 @@
 // leaves its softmax unnormalised in the workspace: per row the running maximum m (of the scores in
 // base 2), the sum l of the rounded numerators and the fp32 row of their products with V.
 // attn_merge puts a row's parts together:  o = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.
+// m = -inf says that a part has no positions (its sums may not be written).  A running maximum
+// passes NaN over and can be -inf over positions all of whose scores are; such a part is stored
+// with the lowest finite m, so that what its sums hold (NaN, or 0 times a NaN value) reaches the row.
 #pragma once
 
 #include <cuda.h>
@@ -39,6 +42,9 @@ struct AttnParams {
 
 // What a call does with the prefix.
 enum AttnPrefixMode { kAttnNoPrefix = 0, kAttnPrefixStream = 1, kAttnPrefixTensor = 2 };
+
+// m as a part with positions stores it.
+__device__ __forceinline__ float attn_part_max(float m) { return fmaxf(m, -3.402823466e38f); }
 
 struct AttnLayout {
   size_t cum, parts, pre_parts, total;

@@ -569,9 +569,9 @@ struct AttnPrefix {
     // the part: O, m and l
     float* part = p.parts + (static_cast<int64_t>(blockIdx.x) + g.unit) * attn_pre_slot_floats(D);
     const int row = stream * 128 + tid;
-    __stcg(part + T::kSlotRows * D + row, m);
+    __stcg(part + T::kSlotRows * D + row, jobs ? attn_part_max(m) : -INFINITY);
     __stcg(part + T::kSlotRows * (D + 1) + row, l);
-    if (jobs == 0) return true;  // (m = -inf: the merge leaves this part out)
+    if (jobs == 0) return true;  // (the merge leaves this part out)
     const uint32_t last = job + jobs - 1;
     if (!wait_warp(c, c.out(Ctx::buf(stream, last)), Ctx::phase(last))) return false;
     tc_after();

@@ -363,7 +363,7 @@ struct AttnStream {
       for (int n = 0; n < D / 8; ++n)
         __stcg(reinterpret_cast<float2*>(row + 8 * n), make_float2(a.o[n][2 * i], a.o[n][2 * i + 1]));
       if (t == 0) {
-        __stcg(part + kAttnRows * D + g + 8 * i, a.m[i]);
+        __stcg(part + kAttnRows * D + g + 8 * i, attn_part_max(a.m[i]));
         __stcg(part + kAttnRows * (D + 1) + g + 8 * i, a.l[i]);
       }
     }

@@ -412,7 +412,9 @@ int bsgemv_moe_destroy(bsgemv_moe_plan_t plan);
  * like the cache.  k and v: element (page, head, row, d) of the cache at
  * page * page_stride + head * head_stride + row * row_stride + d elements, num_pages pages;
  * both layouts ([page][head][row][D] and [page][row][head][D]) are strides.  lse, if not NULL:
- * [B][Hq] fp32, log of the softmax's denominator with the maximum put back.  Scores, softmax and
+ * [B][Hq] fp32, log of the softmax's denominator with the maximum put back.  NaN among a row's
+ * scores, or a score of +inf, gives NaN in its out and lse, NaN in a value its column (a weight of
+ * 0 or not); a row all of whose scores are -inf gives NaN in out and -inf in lse.  Scores, softmax and
  * sums are fp32; the softmax numerators are rounded to the cache's dtype for the second product
  * and summed as rounded.
  */
