@@ -133,7 +133,8 @@ BSG_DEV void pack_stage(float (&v)[PER], uint8_t* dst, int lane) {
     top = max(top, m < 0x7F800000u ? m : 0u);
   }
   top = __reduce_max_sync(0xFFFFFFFFu, top);
-  const int e = min(max(static_cast<int>(top >> 23), 16), 240);  // scale and factor stay normal
+  // (both exponent fields stay normal: 268 - e from 14 to 252, e - 14 from 2 to 240)
+  const int e = max(static_cast<int>(top >> 23), 16);
   const float scale = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - e) << 23);
   if (lane == 0)
     *reinterpret_cast<float*>(dst + 64 * PER) = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
