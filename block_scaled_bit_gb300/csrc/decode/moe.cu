@@ -78,7 +78,6 @@ int run(bsgemv_moe_plan_s* p, const void* x, const void* logits, const int32_t* 
   q.E = p->E;
   q.top_k = p->top_k;
   q.T = T;
-  q.max_T = p->max_T;
   q.flags = p->flags;
   q.x = static_cast<const uint16_t*>(x);
   q.logits = logits;

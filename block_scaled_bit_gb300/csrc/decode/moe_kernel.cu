@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(256) moe_pack_rows(const __grid_constant__ Moe
   pdl_launch_dependents();  // (after the wait: UP reads the routing before its own)
   const int unit = blockIdx.x * 8 + (threadIdx.x >> 5), r = unit / spt, ks = unit - r * spt;
   if (r >= p.route->off[p.route->active]) return;
-  const int64_t row = static_cast<int64_t>(ks) * p.max_T * p.top_k + r;
+  const int64_t row = static_cast<int64_t>(ks) * p.T * p.top_k + r;
   pack_x<PER>(p, p.route->token[r], ks, p.x_packed + row * moe_pitch(PER == 8), threadIdx.x & 31);
 }
 
@@ -221,14 +221,19 @@ int copy_unit(const void* base, int64_t pitch, int bytes) {
 // every token chooses at random.
 int usual_rows(const MoeParams& c) {
   const double p = static_cast<double>(c.top_k) / c.E;
-  const double active = c.E * (1.0 - pow(1.0 - p, c.max_T));
-  const int n = static_cast<int>(2.0 * c.max_T * c.top_k / active + 0.999);
-  return n < c.max_T ? n : c.max_T;
+  const double active = c.E * (1.0 - pow(1.0 - p, c.T));
+  const int n = static_cast<int>(2.0 * c.T * c.top_k / active + 0.999);
+  return n < c.T ? n : c.T;
 }
+
+// Whether a call goes through the kernels for up to 32 tokens.  By the call's tokens, not the
+// plan's: a plan for 32 called with 1 to 8 took 2 to 5 us more through them (the launch that packs x,
+// a smaller ring; int8, H 2752, I 960: 34 / 55 / 78 us for 1 / 4 / 8 tokens, 30 / 51 / 74 through the others).
+bool wide_call(const MoeParams& c) { return c.T > 8; }
 
 int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
   const bool four = c.fmt == kInt4 || c.fmt == kNvfp4;
-  const bool wide = c.max_T > 8;
+  const bool wide = wide_call(c);
   const MoeWeight& w = down ? c.down : c.up;
   MoeGemmParams p = {};
   p.tm = down ? c.tm_down : c.tm_up;
@@ -260,7 +265,7 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
   p.spt = static_cast<int>((w.k + kc - 1) / kc);
   p.last_pairs = static_cast<int>((w.k - static_cast<int64_t>(p.spt - 1) * kc + (four ? 63 : 31)) / (four ? 64 : 32));
   p.T = c.T;
-  p.top_rows = c.max_T * c.top_k;
+  p.top_rows = c.T * c.top_k;
   p.bf16 = c.bf16;
   const int blocks = kc / c.bs;
   p.s_bytes = blocks * (c.fmt == kFp8 ? 4 : c.fmt == kNvfp4 ? 1 : 2);
@@ -276,12 +281,12 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
   const int row_bytes = moe_pitch(four) * (down ? 2 : 1);
   const int budget = kSmemPerSm / kBlocksPerSm - 1024;
   const int route_bytes = align_up((4 * p.top_rows + 1) * 4, 16);
-  p.slot_floats = down ? c.max_T * 16 : (wide ? 4 : 1) * 128;
+  p.slot_floats = down ? c.T * 16 : (wide ? 4 : 1) * 128;
   const int rows = usual_rows(c);
   int smem = 0;
   for (p.stages = 12; p.stages >= 2; --p.stages) {
     const int typical = p.stages * rows;
-    p.row_cap = typical > c.max_T ? typical : c.max_T;
+    p.row_cap = typical > c.T ? typical : c.T;
     int at = p.stages * kMoeBoxB;
     p.off_side = at;
     at += p.stages * p.side_bytes;
@@ -323,7 +328,7 @@ MoeLayout moe_layout(int fmt, int64_t H, int64_t I, int E, int top_k, int max_T,
   const size_t rows = static_cast<size_t>(max_T) * top_k;
   const size_t active = rows < static_cast<size_t>(E) ? rows : static_cast<size_t>(E);
   const size_t ctas = static_cast<size_t>(sms) * kBlocksPerSm;
-  const size_t slot = max_T <= 8 ? 128 : 512;  // floats: up 128 per n8 tile, down 16 max_T
+  const size_t slot = max_T <= 8 ? 128 : 512;  // floats: up 128 per n8 tile, down 16 a token
   l.route = take(sizeof(Routing));
   l.counters_up = take(active * (I / 64) * kMoeWarps * sizeof(unsigned));
   l.counters_packed = take(active * (static_cast<size_t>(I) / 128 + 1) * sizeof(unsigned));
@@ -333,7 +338,7 @@ MoeLayout moe_layout(int fmt, int64_t H, int64_t I, int E, int top_k, int max_T,
   l.h = take(rows * I * sizeof(float));
   const bool four = fmt == kInt4 || fmt == kNvfp4;
   const size_t kc = moe_stage_k(four), pitch = moe_pitch(four);
-  l.x_packed = take((max_T > 8 ? rows : max_T) * ((H + kc - 1) / kc) * pitch);
+  l.x_packed = take((max_T > 8 ? rows : max_T) * ((H + kc - 1) / kc) * pitch);  // (rows >= 8 tokens)
   l.h_packed = take(rows * ((I + kc - 1) / kc) * 2 * pitch);
   l.total = at;
   return l;
@@ -356,7 +361,7 @@ int launch_moe(const MoeParams& p, int sms, cudaStream_t s) {
   static AttrRecord rec;
   int rc = decode_smem(moe_route, rec, 16);  // for the carveout
   if (rc != BSGEMV_OK) return rc;
-  const bool wide = p.max_T > 8;
+  const bool wide = wide_call(p);
   rc = decode_launch(moe_route, dim3(wide ? 1 : 1 + (p.T * up + 31) / 32), dim3(1024), 0, s, p, up);
   if (rc == BSGEMV_OK && wide) {
     static AttrRecord rec8, rec4;

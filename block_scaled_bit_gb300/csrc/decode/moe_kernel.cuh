@@ -45,7 +45,7 @@ struct MoeWeight {
 struct MoeParams {
   int fmt, bf16, bs, has_zp, flags;
   int64_t H, I;
-  int E, top_k, T, max_T;
+  int E, top_k, T;
   const uint16_t* x;
   const void* logits;
   const int32_t* ids;
