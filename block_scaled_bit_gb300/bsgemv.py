@@ -181,13 +181,15 @@ _current = None
 
 def _stream(stream) -> int | None:
     if stream is None:
-        # the current stream's handle without a Stream object for it: 0.4 us a call instead of 3
+        # the current stream's handle without a Stream object for it: 0.2 us a call instead of 3
         global _current
         if _current is None:
             import torch
+            torch.cuda.current_device()  # (initialises the device)
             raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
             _current = (lambda: torch.cuda.current_stream().cuda_stream) if raw is None else \
-                (lambda: raw(torch.cuda.current_device()))
+                (lambda: raw(device()))
         return _current()
     return getattr(stream, "cuda_stream", stream)
 
@@ -344,6 +346,28 @@ class DensePlan:
         return lib().bsgemv_dense_device_status(self._h, _stream(stream))
 
 
+def _arg(what: str, t, nbytes: int, dtypes=None) -> int | None:
+    """The address of a tensor that a kernel takes for `nbytes` bytes in a row; refused if it holds
+    fewer, or not in a row, or other types.  None and raw addresses are passed on."""
+    if t is None:
+        return None
+    try:
+        if t.nbytes >= nbytes and (dtypes is None or t.dtype in dtypes) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        if isinstance(t, int):
+            return t
+        raise
+    raise BsgemvError(ERR_INVALID_ARG, what)
+
+
+def _types(act: str):
+    """(the activation type or its bits, int32, fp32), as _arg takes them."""
+    import torch
+    return ({"f16": torch.float16, "bf16": torch.bfloat16}[act], torch.int16, torch.uint16), \
+        (torch.int32,), (torch.float32,)
+
+
 class _Handle:
     """Owner of one library handle: closed by close(), the end of a with block or collection."""
 
@@ -370,7 +394,8 @@ class _Handle:
 class MoePlan(_Handle):
     """A mixture-of-experts layer for up to max_T <= 32 tokens: top-k routing, the chosen experts'
     gate / up / down products in a block-scaled format, and the weighted sum (bsgemv_moe_plan).
-    logits: "act" (the activation dtype) or "f32"."""
+    logits: "act" (the activation dtype) or "f32".  Tensors that are too small for the plan or not
+    contiguous are refused (BSGEMV_ERR_INVALID_ARG)."""
 
     _destroy = "bsgemv_moe_destroy"
 
@@ -385,13 +410,32 @@ class MoePlan(_Handle):
                                      int(has_zp), H, I, E, top_k, max_T, flags),
                "bsgemv_moe_plan")
         self._h = h
+        self._act, self._i32, self._f32 = _types(act)
+        self._logits = (2, self._act) if logits == "act" else (4, self._f32)
+        # bytes of each stacked weight, its scales and its zero points (NVFP4: the experts' scales)
+        self._bytes = []
+        for rows, k in ((2 * I, H), (H, I)):
+            n, nb = E * rows, k // block_size
+            self._bytes += [n * k // (2 if fmt in ("int4", "nvfp4") else 1),
+                            n * nb * {"int4": 2, "int8": 2, "fp8": 4, "nvfp4": 1}[fmt],
+                            4 * E if fmt == "nvfp4" else n * ((nb + 1) // 2 if fmt == "int4" else nb)]
+
+    def _weights(self, *tensors):
+        return [_arg("W, scales or zp", t, n) for t, n in zip(tensors, self._bytes)]
 
     def run_status(self, x, logits, W13, scales13, zp13, W2, scales2, zp2, y,
                    T: int | None = None, stream=None) -> int:
         T = x.shape[0] if T is None else T
-        return lib().bsgemv_moe_run(self._h, _ptr(x), _ptr(logits), _ptr(W13), _ptr(scales13),
-                                    _ptr(zp13), _ptr(W2), _ptr(scales2), _ptr(zp2), _ptr(y),
-                                    int(T), _stream(stream))
+        n = T if 0 < T <= self.max_T else 0  # (other T: the library's to refuse)
+        size, types = self._logits
+        try:
+            return lib().bsgemv_moe_run(
+                self._h, _arg("x", x, 2 * n * self.H, self._act),
+                _arg("logits", logits, size * n * self.E, types),
+                *self._weights(W13, scales13, zp13, W2, scales2, zp2),
+                _arg("y", y, 2 * n * self.H, self._act), int(T), _stream(stream))
+        except BsgemvError as e:
+            return e.status
 
     def run(self, x, logits, W13, scales13, zp13, W2, scales2, zp2, y, T: int | None = None,
             stream=None) -> None:
@@ -403,10 +447,14 @@ class MoePlan(_Handle):
                    T: int | None = None, stream=None) -> None:
         """The layer with the caller's routing: ids [T, top_k] int32, weights [T, top_k] fp32."""
         T = x.shape[0] if T is None else T
-        _check(lib().bsgemv_moe_run_routed(self._h, _ptr(x), _ptr(ids), _ptr(weights), _ptr(W13),
-                                           _ptr(scales13), _ptr(zp13), _ptr(W2), _ptr(scales2),
-                                           _ptr(zp2), _ptr(y), int(T), _stream(stream)),
-               "bsgemv_moe_run_routed")
+        n = T if 0 < T <= self.max_T else 0
+        _check(lib().bsgemv_moe_run_routed(
+            self._h, _arg("x", x, 2 * n * self.H, self._act),
+            _arg("ids", ids, 4 * n * self.top_k, self._i32),
+            _arg("weights", weights, 4 * n * self.top_k, self._f32),
+            *self._weights(W13, scales13, zp13, W2, scales2, zp2),
+            _arg("y", y, 2 * n * self.H, self._act), int(T), _stream(stream)),
+            "bsgemv_moe_run_routed")
 
     def device_status(self, stream=None) -> int:
         return lib().bsgemv_moe_device_status(self._h, _stream(stream))
@@ -414,7 +462,8 @@ class MoePlan(_Handle):
 
 class AttnPlan(_Handle):
     """Single-token attention of up to max_B sequences that share a prefix, over a paged cache
-    (bsgemv_attn_plan)."""
+    (bsgemv_attn_plan).  Tensors of other shapes, types or orders than run() says are refused
+    (BSGEMV_ERR_INVALID_ARG)."""
 
     _destroy = "bsgemv_attn_destroy"
 
@@ -425,27 +474,39 @@ class AttnPlan(_Handle):
         _check(lib().bsgemv_attn_plan(ctypes.byref(h), int(act == "bf16"), Hq, Hkv, D, page_size,
                                       max_B), "bsgemv_attn_plan")
         self._h = h
-
-    def run_status(self, q, k, v, prefix_table, prefix_len: int, tables, lens, out, lse=None,
-                   scale: float | None = None, stream=None) -> int:
-        ks, shape, qs, ts = k.stride(), k.shape, q.stride(), tables.stride()
-        if ks != v.stride() or shape != v.shape or ks[3] != 1 or qs[2] != 1 or qs[1] != self.D or \
-                ts[1] != 1 or shape[1:] != (self.Hkv, self.page_size, self.D) or \
-                not out.is_contiguous():
-            return ERR_INVALID_ARG
-        return lib().bsgemv_attn_run(self._h, q.data_ptr(), qs[0], k.data_ptr(), v.data_ptr(),
-                                     ks[0], ks[1], ks[2], shape[0], _ptr(prefix_table),
-                                     prefix_len, tables.data_ptr(), ts[0], lens.data_ptr(),
-                                     q.shape[0], self.D ** -0.5 if scale is None else scale,
-                                     out.data_ptr(), _ptr(lse), _stream(stream))
+        self._act, self._i32, self._f32 = _types(act)
+        self._scale = D ** -0.5
 
     def run(self, q, k, v, prefix_table, prefix_len: int, tables, lens, out, lse=None,
             scale: float | None = None, stream=None) -> None:
         """out [B, Hq, D] from q [B, Hq, D] (any stride between sequences); k and v are views
-        [pages, Hkv, page_size, D] of the cache in either layout (strides are passed on); scale
-        defaults to D ** -0.5."""
-        _check(self.run_status(q, k, v, prefix_table, prefix_len, tables, lens, out, lse, scale,
-                               stream), "bsgemv_attn_run")
+        [pages, Hkv, page_size, D] of the cache in either layout (strides are passed on);
+        prefix_table [pages of the prefix or more], tables [B or more, columns] (any stride between
+        rows) and lens [B or more] are int32, lse [B, Hq] fp32; scale defaults to D ** -0.5."""
+        B, Hq, D = q.shape
+        pages, heads, rows, width = shape = k.shape
+        ks, (qs, qh, q1), (ts, t1), act = k.stride(), q.stride(), tables.stride(), self._act
+        if ks != v.stride() or shape != v.shape or D != self.D or width != D or ks[3] != 1 or \
+                q1 != 1 or t1 != 1 or Hq != self.Hq or qh != D and Hq > 1 or heads != self.Hkv or \
+                rows != self.page_size or tables.shape[0] < B or q.dtype not in act or \
+                k.dtype not in act or v.dtype not in act or tables.dtype not in self._i32:
+            raise BsgemvError(ERR_INVALID_ARG, "bsgemv_attn_run")
+        status = lib().bsgemv_attn_run(
+            self._h, q.data_ptr(), qs, k.data_ptr(), v.data_ptr(), ks[0], ks[1], ks[2], pages,
+            _arg("prefix_table", prefix_table, 4 * -(-prefix_len // rows), self._i32), prefix_len,
+            tables.data_ptr(), ts, _arg("lens", lens, 4 * B, self._i32), B,
+            self._scale if scale is None else scale, _arg("out", out, 2 * B * Hq * D, act),
+            _arg("lse", lse, 4 * B * Hq, self._f32), _stream(stream))
+        if status != OK:
+            raise BsgemvError(status, "bsgemv_attn_run")
+
+    def run_status(self, *args, **kw) -> int:
+        """As run, with the status returned."""
+        try:
+            self.run(*args, **kw)
+        except BsgemvError as e:
+            return e.status
+        return OK
 
     def device_status(self, stream=None) -> int:
         return lib().bsgemv_attn_device_status(self._h, _stream(stream))
@@ -453,7 +514,9 @@ class AttnPlan(_Handle):
 
 class PageCache(_Handle):
     """The pages of a cache (bsgemv_cache_plan): pool [planes, num_pages, page_bytes], refs
-    [num_pages], tables [max_seqs, max_pages] and lens [max_seqs] (int32) are the caller's."""
+    [num_pages], tables [max_seqs, max_pages] and lens [max_seqs] (int32) are the caller's, as the
+    lists (int32).  Tensors of fewer elements, of other types or not contiguous are refused
+    (BSGEMV_ERR_INVALID_ARG)."""
 
     _destroy = "bsgemv_cache_destroy"
 
@@ -465,48 +528,69 @@ class PageCache(_Handle):
         _check(lib().bsgemv_cache_plan(ctypes.byref(h), planes, num_pages, page_bytes, page_size,
                                        max_seqs, max_pages), "bsgemv_cache_plan")
         self._h = h
+        self._i32 = _types("f16")[1]
+        # bytes of the state's parts
+        self._pool, self._refs = planes * num_pages * page_bytes, 4 * num_pages
+        self._tables, self._lens = 4 * max_seqs * max_pages, 4 * max_seqs
 
     def copy(self, pool, src, dst, stream=None) -> None:
         """Page src[i] to page dst[i] in every plane."""
-        _check(lib().bsgemv_cache_copy(self._h, _ptr(pool), _ptr(src), _ptr(dst), src.shape[0],
-                                       _stream(stream)), "bsgemv_cache_copy")
+        n, i32 = src.shape[0], self._i32
+        _check(lib().bsgemv_cache_copy(
+            self._h, _arg("pool", pool, self._pool), _arg("src", src, 4 * n, i32),
+            _arg("dst", dst, 4 * n, i32), n, _stream(stream)), "bsgemv_cache_copy")
 
     def fork(self, pool, refs, tables, lens, parents, children, new_pages=None,
              stream=None) -> None:
         """Slot children[i] becomes a copy of sequence parents[i]."""
-        _check(lib().bsgemv_cache_fork(self._h, _ptr(pool), _ptr(refs), _ptr(tables), _ptr(lens),
-                                       _ptr(parents), _ptr(children), _ptr(new_pages),
-                                       parents.shape[0], _stream(stream)), "bsgemv_cache_fork")
+        n, i32 = parents.shape[0], self._i32
+        _check(lib().bsgemv_cache_fork(
+            self._h, _arg("pool", pool, self._pool), _arg("refs", refs, self._refs, i32),
+            _arg("tables", tables, self._tables, i32), _arg("lens", lens, self._lens, i32),
+            _arg("parents", parents, 4 * n, i32), _arg("children", children, 4 * n, i32),
+            _arg("new_pages", new_pages, 4 * n, i32), n, _stream(stream)), "bsgemv_cache_fork")
 
     def free(self, refs, tables, lens, seqs, stream=None) -> None:
         """Release the sequences."""
-        _check(lib().bsgemv_cache_free(self._h, _ptr(refs), _ptr(tables), _ptr(lens), _ptr(seqs),
-                                       seqs.shape[0], _stream(stream)), "bsgemv_cache_free")
+        n, i32 = seqs.shape[0], self._i32
+        _check(lib().bsgemv_cache_free(
+            self._h, _arg("refs", refs, self._refs, i32), _arg("tables", tables, self._tables, i32),
+            _arg("lens", lens, self._lens, i32), _arg("seqs", seqs, 4 * n, i32), n,
+            _stream(stream)), "bsgemv_cache_free")
 
     def extend(self, pool, refs, tables, lens, seqs, grown=None, stream=None) -> None:
         """Room for one more token in each of the sequences."""
-        _check(lib().bsgemv_cache_extend(self._h, _ptr(pool), _ptr(refs), _ptr(tables),
-                                         _ptr(lens), _ptr(seqs), _ptr(grown), seqs.shape[0],
-                                         _stream(stream)), "bsgemv_cache_extend")
+        n, i32 = seqs.shape[0], self._i32
+        _check(lib().bsgemv_cache_extend(
+            self._h, _arg("pool", pool, self._pool), _arg("refs", refs, self._refs, i32),
+            _arg("tables", tables, self._tables, i32), _arg("lens", lens, self._lens, i32),
+            _arg("seqs", seqs, 4 * n, i32), _arg("grown", grown, 4 * n, i32), n,
+            _stream(stream)), "bsgemv_cache_extend")
 
     def write(self, pool, tables, lens, seqs, k, v, head_stride: int, row_stride: int,
               k_plane: int, v_plane: int, stream=None) -> None:
-        """k, v [n, heads, D] (any stride between sequences) to the sequences' last positions."""
-        if k.stride() != v.stride() or k.shape != v.shape or k.stride(-1) != 1 or \
-                k.stride(1) != k.shape[2]:
+        """k, v [n, heads, D] (2-byte elements, any stride between sequences) to the sequences' last
+        positions."""
+        n, (rows, heads, D), ks, i32 = seqs.shape[0], k.shape, k.stride(), self._i32
+        if ks != v.stride() or v.shape != k.shape or ks[2] != 1 or ks[1] != D and heads > 1 or \
+                k.itemsize != 2 or v.itemsize != 2 or rows < n:
             raise BsgemvError(ERR_INVALID_ARG, "bsgemv_cache_write")
-        _check(lib().bsgemv_cache_write(self._h, _ptr(pool), _ptr(tables), _ptr(lens), _ptr(seqs),
-                                        _ptr(k), _ptr(v), k.stride(0), k.shape[1], k.shape[2],
-                                        head_stride, row_stride, k_plane, v_plane, seqs.shape[0],
-                                        _stream(stream)), "bsgemv_cache_write")
+        _check(lib().bsgemv_cache_write(
+            self._h, _arg("pool", pool, self._pool), _arg("tables", tables, self._tables, i32),
+            _arg("lens", lens, self._lens, i32), _arg("seqs", seqs, 4 * n, i32), k.data_ptr(),
+            v.data_ptr(), ks[0], heads, D, head_stride, row_stride, k_plane, v_plane, n,
+            _stream(stream)), "bsgemv_cache_write")
 
     def compact(self, pool, refs, tables, lens, refs_out, tables_out, live_out,
                 stream=None) -> None:
         """Live pages to the front; the new state in refs_out, tables_out and live_out [1]."""
-        _check(lib().bsgemv_cache_compact(self._h, _ptr(pool), _ptr(refs), _ptr(tables),
-                                          _ptr(lens), _ptr(refs_out), _ptr(tables_out),
-                                          _ptr(live_out), _stream(stream)),
-               "bsgemv_cache_compact")
+        i32 = self._i32
+        _check(lib().bsgemv_cache_compact(
+            self._h, _arg("pool", pool, self._pool), _arg("refs", refs, self._refs, i32),
+            _arg("tables", tables, self._tables, i32), _arg("lens", lens, self._lens, i32),
+            _arg("refs_out", refs_out, self._refs, i32),
+            _arg("tables_out", tables_out, self._tables, i32), _arg("live_out", live_out, 4, i32),
+            _stream(stream)), "bsgemv_cache_compact")
 
 
 def upload(case, device="cuda"):
