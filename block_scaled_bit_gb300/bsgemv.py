@@ -38,7 +38,7 @@ EXPORTS = ("bsgemv_plan", "bsgemv_run", "bsgemv_run_bias", "bsgemv_run_host",
            "bsgemv_dense_plan", "bsgemv_dense_run", "bsgemv_dense_describe",
            "bsgemv_dense_geometry_for", "bsgemv_dense_device_status", "bsgemv_dense_destroy",
            "bsgemv_moe_plan", "bsgemv_moe_run", "bsgemv_moe_run_routed",
-           "bsgemv_moe_device_status", "bsgemv_moe_destroy",
+           "bsgemv_moe_device_status", "bsgemv_moe_set_test_fault", "bsgemv_moe_destroy",
            "bsgemv_attn_plan", "bsgemv_attn_run", "bsgemv_attn_device_status",
            "bsgemv_attn_destroy",
            "bsgemv_cache_plan", "bsgemv_cache_copy", "bsgemv_cache_fork", "bsgemv_cache_free",
@@ -110,6 +110,7 @@ def lib() -> ctypes.CDLL:
         L.bsgemv_moe_run.argtypes = [vp] * 10 + [ci, vp]
         L.bsgemv_moe_run_routed.argtypes = [vp] * 11 + [ci, vp]
         L.bsgemv_moe_device_status.argtypes = [vp, vp]
+        L.bsgemv_moe_set_test_fault.argtypes = [vp, ci, ci, i64]
         L.bsgemv_moe_destroy.argtypes = [vp]
         L.bsgemv_attn_plan.argtypes = [ctypes.POINTER(vp)] + [ci] * 6
         L.bsgemv_attn_run.argtypes = [vp, vp, i64, vp, vp, i64, i64, i64, ci, vp, ci, vp, i64, vp,
@@ -458,6 +459,11 @@ class MoePlan(_Handle):
 
     def device_status(self, stream=None) -> int:
         return lib().bsgemv_moe_device_status(self._h, _stream(stream))
+
+    def set_test_fault(self, product: int = 0, skip_stage: int = -1, wait_ns: int = 0) -> int:
+        """Test hook of the bounded waits (bsgemv_moe_set_test_fault); (0, -1, 0) undoes it."""
+        return lib().bsgemv_moe_set_test_fault(self._h, int(product), int(skip_stage),
+                                               int(wait_ns))
 
 
 class AttnPlan(_Handle):

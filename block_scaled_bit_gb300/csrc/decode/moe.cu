@@ -17,6 +17,8 @@ struct bsgemv_moe_plan_s {
   int fmt = 0, bf16 = 0, block_size = 0, has_zp = 0;
   int64_t H = 0, I = 0;
   int E = 0, top_k = 0, max_T = 0, flags = 0;
+  int fault_skip[2] = {-1, -1};   // bsgemv_moe_set_test_fault
+  uint64_t fault_wait_ns = 0;
   void* ws = nullptr;
   bsg::MoeLayout at = {};
   // tensor maps of the last few (W13, W2) pairs (a layer each: a plan serves layers in turn)
@@ -79,6 +81,9 @@ int run(bsgemv_moe_plan_s* p, const void* x, const void* logits, const int32_t* 
   q.top_k = p->top_k;
   q.T = T;
   q.flags = p->flags;
+  q.wait_ns = p->fault_wait_ns ? p->fault_wait_ns : kDefaultWaitNs;
+  q.skip_stage[0] = p->fault_skip[0];
+  q.skip_stage[1] = p->fault_skip[1];
   q.x = static_cast<const uint16_t*>(x);
   q.logits = logits;
   q.ids = ids;
@@ -168,6 +173,16 @@ int bsgemv_moe_run_routed(bsgemv_moe_plan_t plan, const void* x, const int32_t* 
                           const void* zp13, const void* W2, const void* scales2, const void* zp2,
                           void* y, int T, void* stream) {
   return run(plan, x, nullptr, ids, weights, W13, scales13, zp13, W2, scales2, zp2, y, T, stream);
+}
+
+int bsgemv_moe_set_test_fault(bsgemv_moe_plan_t plan, int product, int skip_stage,
+                              int64_t wait_ns) {
+  if (plan == nullptr || product < 0 || product > 1 || skip_stage < -1 || wait_ns < 0)
+    return BSGEMV_ERR_INVALID_ARG;
+  plan->fault_skip[product] = skip_stage;
+  plan->fault_skip[1 - product] = -1;
+  plan->fault_wait_ns = static_cast<uint64_t>(wait_ns);
+  return BSGEMV_OK;
 }
 
 int bsgemv_moe_device_status(bsgemv_moe_plan_t plan, void* stream) {

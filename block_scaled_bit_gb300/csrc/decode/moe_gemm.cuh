@@ -85,10 +85,11 @@ struct MoeGemmParams {
   unsigned *counters, *err;
   unsigned* group_counters;   // DOWN: of eight neighbours' parts, by (first block, it opens the tile)
   float* h;                   // UP: [rows][I]
-  uint8_t* h_packed;          // UP: [row][stage of I][2 pitches]
+  uint8_t* h_packed;          // UP: [stage of I][row][2 pitches]
   unsigned* packed;           // UP: [active expert][stage of I] warps that have stored into it
   uint16_t* y;                // DOWN: [T][H]
-  uint64_t wait_ns;
+  uint64_t wait_ns;           // limit of every wait but the drain's
+  int skip_stage;             // test hook: block 0 leaves out the copies of this stage; -1 none
   int64_t K;                  // elements of an activation row
   int64_t s_end, z_end;       // bytes of scales and zero points
   int64_t s_pitch, z_pitch;   // bytes per weight row
@@ -187,6 +188,9 @@ struct MoeGemm {
     BSG_DEV volatile uint32_t* abort_word() const {
       return reinterpret_cast<volatile uint32_t*>(base + p.off_bar + 16 * p.stages);
     }
+    // stages that the second copy warp has arrived for, when it has ended
+    BSG_DEV volatile uint32_t* sides_word() const { return abort_word() + 1; }
+    BSG_DEV int skip() const { return blockIdx.x == 0 ? p.skip_stage : -1; }
     // the routing, as copied to shared memory: [expert][off, one more][token][weight]
     BSG_DEV const int* route() const { return reinterpret_cast<const int*>(base + p.off_route); }
     BSG_DEV int expert(int a) const { return route()[a]; }
@@ -335,7 +339,10 @@ struct MoeGemm {
       for (int k = 0; k < w.n; ++k, ++i) {
         if (i >= p.stages &&
             !__all_sync(0xFFFFFFFFu, mbar_wait(c.empty(slot), phase, p.err, kErrTimeoutEmpty, p.wait_ns))) {
-          if (lane == 0) *c.abort_word() = 1u;
+          if (lane == 0) {
+            *c.abort_word() = 1u;
+            *c.sides_word() = i;
+          }
           asm volatile("cp.async.wait_all;" ::: "memory");
           return;
         }
@@ -350,8 +357,15 @@ struct MoeGemm {
       if (w.left == 0) break;
       next_run(c, w);
     }
+    if (lane == 0) *c.sides_word() = i;
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
+
+  // What the first copy warp has issued: weight boxes of the stages below `boxes`, activations (and
+  // its arrivals) of those below `rows`.
+  struct Issued {
+    int boxes, rows;
+  };
 
   // One box: 128 rows, or 64 gate rows and the up rows that belong to them.
   static BSG_DEV void issue_box(const Ctx& c, const Run& w, int ks, int slot, uint64_t pol) {
@@ -362,9 +376,8 @@ struct MoeGemm {
   // The first copy warp: weights and activations of every stage in order, as far ahead as the rings
   // allow.  Where the routing is older than the kernel before this one, the first weights go out
   // before the wait for that kernel (they do not depend on it).  Everything that a run's stages
-  // share is worked out once per run: this warp's time per stage bounds the block's rate.  Returns
-  // the stages issued.
-  static BSG_DEV int produce(const Ctx& c, int lane) {
+  // share is worked out once per run: this warp's time per stage bounds the block's rate.
+  static BSG_DEV Issued produce(const Ctx& c, int lane) {
     const MoeGemmParams& p = c.p;
     const uint64_t pol = policy_evict_first();
     if (lane == 0) prefetch_tmap(&p.tm);
@@ -375,7 +388,7 @@ struct MoeGemm {
       while (early < p.stages) {
         const int most = min(e.n, p.stages - early);
         for (int i = 0; i < most; ++i, ++early)
-          if (lane == 0) {
+          if (lane == 0 && early != c.skip()) {
             mbar_expect_tx(c.full(early), kMoeBoxB);
             issue_box(c, e, e.ks + i, early, pol);
           }
@@ -401,7 +414,7 @@ struct MoeGemm {
           if (!__all_sync(0xFFFFFFFFu, mbar_wait(c.empty(tslot), tphase, p.err, kErrTimeoutEmpty,
                                                  p.wait_ns))) {
             if (lane == 0) *c.abort_word() = 1u;
-            return i;
+            return {max(i, early), i};
           }
           used -= tail_m;
           ++free_slots;
@@ -412,22 +425,24 @@ struct MoeGemm {
           if (++tslot == p.stages) { tslot = 0; tphase ^= 1u; }
         }
         const uint32_t full = c.full(slot);
-        if (lane == 0) mbar_expect_tx(full, i < early ? tx : tx + kMoeBoxB);
+        const bool left_out = i == c.skip();
+        if (lane == 0 && !left_out) mbar_expect_tx(full, i < early ? tx : tx + kMoeBoxB);
         __syncwarp();  // the bytes are expected before any lane's copy can complete
-        if (i >= early && lane == 0) issue_box(c, w, w.ks + k, slot, pol);
+        if (i >= early && lane == 0 && !left_out) issue_box(c, w, w.ks + k, slot, pol);
         if constexpr (!kByToken) {
           const int here = min(m, p.row_cap - head);
-          if (lane == 0) bulk_load(c.base_u + p.off_rows + head * kRowB, src, here * kRowB, full);
-          if (lane == 1 && here < m)
+          if (lane == 0 && !left_out)
+            bulk_load(c.base_u + p.off_rows + head * kRowB, src, here * kRowB, full);
+          if (lane == 1 && here < m && !left_out)
             bulk_load(c.base_u + p.off_rows, src + here * kRowB, (m - here) * kRowB, full);
           src += static_cast<int64_t>(p.top_rows) * kRowB;
         } else {
-          if (lane < m)
+          if (lane < m && !left_out)
             bulk_load(c.base_u + p.off_rows + wrap(c, head + lane) * kRowB, src, kRowB, full);
           src += kRowB;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(full);
+        if (lane == 0 && !left_out) mbar_arrive(full);
         used += m;
         --free_slots;
         head = wrap(c, head + m);
@@ -436,13 +451,23 @@ struct MoeGemm {
       if (w.left == 0) break;
       next_run(c, w);
     }
-    return i;
+    return {i, i};
   }
 
-  // After a wait that ran out: the copies in flight land before the block ends (bounded again).
-  static BSG_DEV void drain(const Ctx& c, int n) {
-    for (int i = n > c.p.stages ? n - c.p.stages : 0; i < n; ++i)
-      mbar_wait(c.full(i % c.p.stages), (i / c.p.stages) & 1, c.p.err, kErrTimeoutFull, c.p.wait_ns);
+  // After a wait that ran out (all warps have ended their work): the copies in flight land before
+  // the block ends.  A stage's barrier completes once its bytes are there and both copy warps have
+  // arrived; an arrival that a warp did not come to is made up for here.  (The second warp has waited
+  // for its own copies.)  The limit is the usual one whatever the waits': shared memory that a copy
+  // still writes to must not go to another block.
+  static BSG_DEV void drain(const Ctx& c, const Issued& n) {
+    const int sides = static_cast<int>(*c.sides_word());
+    for (int i = max(n.boxes - c.p.stages, 0); i < n.boxes; ++i) {
+      if (i == c.skip()) continue;
+      const uint32_t full = c.full(i % c.p.stages);
+      if (i >= n.rows) mbar_arrive(full);
+      if (i >= sides) mbar_arrive(full);
+      mbar_wait(full, (i / c.p.stages) & 1, c.p.err, kErrTimeoutFull, kDefaultWaitNs);
+    }
   }
 
   // ---------------------------------------------------------------- decode warps
@@ -1078,7 +1103,7 @@ struct MoeGemm {
       c.extra = c.total - c.base_len * c.G;
       c.s0 = start(c, blockIdx.x);
       c.s1 = start(c, blockIdx.x + 1);
-      int issued = 0;
+      Issued issued = {0, 0};
       if (warp == 0) issued = produce(c, lane);
       else if (warp == 1) produce_sides(c, lane);
       else work(c, warp - 2, lane);

@@ -250,7 +250,8 @@ int launch_product(const MoeParams& c, bool down, int sms, cudaStream_t s) {
   p.h_packed = c.h_packed;
   p.packed = c.counters_packed;
   p.y = c.y;
-  p.wait_ns = kDefaultWaitNs;
+  p.wait_ns = c.wait_ns;
+  p.skip_stage = c.skip_stage[down];
   p.K = w.k;
   p.rows = static_cast<int>(w.rows);
   p.s_end = w.scale_pitch * w.rows * c.E;

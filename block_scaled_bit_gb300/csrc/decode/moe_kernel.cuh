@@ -46,6 +46,8 @@ struct MoeParams {
   int fmt, bf16, bs, has_zp, flags;
   int64_t H, I;
   int E, top_k, T;
+  uint64_t wait_ns;            // limit of the products' waits
+  int skip_stage[2];           // test hook, UP's and DOWN's: see MoeGemmParams
   const uint16_t* x;
   const void* logits;
   const int32_t* ids;

@@ -391,6 +391,13 @@ int bsgemv_moe_run_routed(bsgemv_moe_plan_t plan, const void* x, const int32_t* 
  * not to be relied on. */
 int bsgemv_moe_device_status(bsgemv_moe_plan_t plan, void* stream);
 
+/* Test hook, as bsgemv_plan_set_test_fault: in the plan's next calls block 0 of the first (product
+ * 0: gate and up) or second (1: down) product leaves out the copies of stage `skip_stage` of its range
+ * (-1: none), and all waits give up after wait_ns (0: the default).  (plan, 0, -1, 0) restores normal
+ * calls. */
+int bsgemv_moe_set_test_fault(bsgemv_moe_plan_t plan, int product, int skip_stage,
+                              int64_t wait_ns);
+
 /* Free the plan (synchronises the device first).  NULL is a no-op. */
 int bsgemv_moe_destroy(bsgemv_moe_plan_t plan);
 
