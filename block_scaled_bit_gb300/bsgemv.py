@@ -40,7 +40,7 @@ EXPORTS = ("bsgemv_plan", "bsgemv_run", "bsgemv_run_bias", "bsgemv_run_host",
            "bsgemv_moe_plan", "bsgemv_moe_run", "bsgemv_moe_run_routed",
            "bsgemv_moe_device_status", "bsgemv_moe_set_test_fault", "bsgemv_moe_destroy",
            "bsgemv_attn_plan", "bsgemv_attn_run", "bsgemv_attn_device_status",
-           "bsgemv_attn_destroy",
+           "bsgemv_attn_set_test_fault", "bsgemv_attn_destroy",
            "bsgemv_cache_plan", "bsgemv_cache_copy", "bsgemv_cache_fork", "bsgemv_cache_free",
            "bsgemv_cache_extend", "bsgemv_cache_write", "bsgemv_cache_compact",
            "bsgemv_cache_destroy",
@@ -116,6 +116,7 @@ def lib() -> ctypes.CDLL:
         L.bsgemv_attn_run.argtypes = [vp, vp, i64, vp, vp, i64, i64, i64, ci, vp, ci, vp, i64, vp,
                                       ci, f32, vp, vp, vp]
         L.bsgemv_attn_device_status.argtypes = [vp, vp]
+        L.bsgemv_attn_set_test_fault.argtypes = [vp, ci, ci, i64]
         L.bsgemv_attn_destroy.argtypes = [vp]
         L.bsgemv_cache_plan.argtypes = [ctypes.POINTER(vp), ci, ci, i64, ci, ci, ci]
         L.bsgemv_cache_copy.argtypes = [vp, vp, vp, vp, ci, vp]
@@ -516,6 +517,10 @@ class AttnPlan(_Handle):
 
     def device_status(self, stream=None) -> int:
         return lib().bsgemv_attn_device_status(self._h, _stream(stream))
+
+    def set_test_fault(self, kernel: int = 0, skip_tile: int = -1, wait_ns: int = 0) -> int:
+        """Test hook of the bounded waits (bsgemv_attn_set_test_fault); (0, -1, 0) undoes it."""
+        return lib().bsgemv_attn_set_test_fault(self._h, int(kernel), int(skip_tile), int(wait_ns))
 
 
 class PageCache(_Handle):

@@ -11,6 +11,8 @@ struct bsgemv_attn_plan_s {
   int device = -1, sms = 0;
   int bf16 = 0, Hq = 0, Hkv = 0, D = 0, page_size = 0, max_B = 0;
   void* ws = nullptr;
+  int fault_skip[2] = {-1, -1};   // bsgemv_attn_set_test_fault
+  uint64_t fault_wait_ns = 0;
   bsg::AttnLayout at = {};
   // tensor maps of the last few caches seen (a layer each)
   struct MapEntry {
@@ -137,12 +139,25 @@ int bsgemv_attn_run(bsgemv_attn_plan_t plan, const void* q, int64_t q_stride, co
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.err = static_cast<unsigned*>(plan->ws);
+  p.wait_ns = plan->fault_wait_ns ? plan->fault_wait_ns : kDefaultWaitNs;
+  p.skip[0] = plan->fault_skip[0];
+  p.skip[1] = plan->fault_skip[1];
   p.parts = reinterpret_cast<float*>(static_cast<char*>(plan->ws) + plan->at.parts);
   p.pre_parts = reinterpret_cast<float*>(static_cast<char*>(plan->ws) + plan->at.pre_parts);
   p.cum = reinterpret_cast<int*>(static_cast<char*>(plan->ws) + plan->at.cum);
   const AttnMaps* maps = maps_of(plan, p);
   if (maps == nullptr) return BSGEMV_ERR_UNSUPPORTED;
   return launch_attn(p, mode, *maps, plan->sms, static_cast<cudaStream_t>(stream));
+}
+
+int bsgemv_attn_set_test_fault(bsgemv_attn_plan_t plan, int kernel, int skip_tile,
+                               int64_t wait_ns) {
+  if (plan == nullptr || kernel < 0 || kernel > 1 || skip_tile < -1 || wait_ns < 0)
+    return BSGEMV_ERR_INVALID_ARG;
+  plan->fault_skip[kernel] = skip_tile;
+  plan->fault_skip[1 - kernel] = -1;
+  plan->fault_wait_ns = static_cast<uint64_t>(wait_ns);
+  return BSGEMV_OK;
 }
 
 int bsgemv_attn_device_status(bsgemv_attn_plan_t plan, void* stream) {

@@ -186,7 +186,6 @@ int launch(const AttnParams& p, int mode, const AttnMaps& maps, int sms, cudaStr
     q.a = p;
     q.box_rows = ps < P::kKeys ? ps : P::kKeys;
     q.parts = p.pre_parts;
-    q.wait_ns = kDefaultWaitNs;
     rc = decode_smem(attn_prefix_kernel<BF16, D>, pre_rec, P::kSmem);
     if (rc != BSGEMV_OK) return rc;
     const AttnPreSplit split = attn_pre_split<D>(p.B, p.Hq, p.Hkv, p.prefix_len, sms);

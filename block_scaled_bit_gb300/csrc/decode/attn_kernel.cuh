@@ -35,6 +35,9 @@ struct AttnParams {
   uint16_t* out;
   float* lse;
   unsigned* err;
+  uint64_t wait_ns;   // limit of every wait but the drains'
+  int skip[2];        // test hook: the tile whose copy the streaming kernel's first warp, or the
+                      // prefix kernel's first block, leaves out; -1 none
   float* parts;       // streaming parts: slots of [16][D] sums, then [16] m, [16] l
   float* pre_parts;   // the prefix kernel's parts
   int* cum;           // [B + 1] the sequences' stretches of the line, from the streaming kernel

@@ -53,7 +53,7 @@ struct AttnPre {
   static constexpr int kPairRing = kRing / 4 * 4;
   static constexpr int kOffRing = kStreams * kQB;
   static constexpr int kOffBar = kOffRing + kRing * kTileB;
-  static constexpr int kBars = 2 * kRing + 2 * kStreams + 2 * kBufs + 1;
+  static constexpr int kBars = 2 * kRing + 3 * kStreams + 2 * kBufs + 1;
   static constexpr int kSmem = kOffBar + (kBars * 8 + 12 + 15) / 16 * 16 + 1024;  // (1024-byte tiles)
   static constexpr int kThreads = 32 * (5 * kStreams + 1);
   static constexpr int kSlotRows = 128 * kStreams;
@@ -98,7 +98,6 @@ struct AttnPreParams {
   AttnParams a;
   int box_rows;
   float* parts;             // slots of [rows][D] sums, [rows] m, [rows] l
-  uint64_t wait_ns;
 };
 
 // ---- tcgen05
@@ -210,6 +209,8 @@ struct AttnPrefix {
     BSG_DEV uint32_t probs(uint32_t b) const { return bar(kP + b); }                          // P written
     BSG_DEV uint32_t out(uint32_t b) const { return bar(kP + T::kBufs + b); }                 // P V done
     BSG_DEV uint32_t query() const { return bar(kP + 2 * T::kBufs); }                         // Q written
+    BSG_DEV uint32_t ended(uint32_t stream) const { return bar(kP + 2 * T::kBufs + 1 + stream); }  // (drain)
+    BSG_DEV int skip() const { return blockIdx.x == 0 ? p.a.skip[1] : -1; }
     // columns of S and P
     static BSG_DEV uint32_t col_s(uint32_t stream) { return stream * 2 * K; }
     static BSG_DEV uint32_t col_p(uint32_t stream, uint32_t j) {
@@ -220,7 +221,7 @@ struct AttnPrefix {
       return reinterpret_cast<volatile uint32_t*>(base + T::kOffBar + 8 * T::kBars);
     }
     BSG_DEV bool wait(uint32_t b, uint32_t parity, unsigned code) const {
-      return mbar_wait(b, parity, p.a.err, code, p.wait_ns);
+      return mbar_wait(b, parity, p.a.err, code, p.a.wait_ns);
     }
   };
 
@@ -288,9 +289,10 @@ struct AttnPrefix {
             return false;
           }
           const uint32_t bar = c.full(slot);
-          if (lane == 0) mbar_arrive_expect_tx(bar, T::kTileB);
+          const bool left_out = i == c.skip();
+          if (lane == 0 && !left_out) mbar_arrive_expect_tx(bar, T::kTileB);
           __syncwarp();
-          if (lane < boxes)
+          if (lane < boxes && !left_out)
             tma_load_4d(c.tile(slot) + d * (K * 128) + r * 128, kv ? &p.tm_v : &p.tm_k, d * 64,
                         pos & ((1 << p.a.page_log2) - 1), head, here, bar);
           if (++slot == c.ring) { slot = 0; phase ^= 1u; }
@@ -302,11 +304,19 @@ struct AttnPrefix {
     return true;
   }
 
-  // After a wait that ran out: the copies in flight land before the block ends (bounded).
-  static BSG_DEV void drain(const Ctx& c) {
+  // After a wait that ran out (every warp has ended its work): the copies in flight land, and the
+  // MMAs that a warp has issued end, before tensor memory is freed and shared memory goes to another
+  // block.  The limit is the usual one, whatever the waits'.
+  static BSG_DEV void drain_copies(const Ctx& c) {
     const int n = static_cast<int>(c.words()[2]);
     for (int i = n > c.ring ? n - c.ring : 0; i < n; ++i)
-      c.wait(c.full(i % c.ring), (i / c.ring) & 1, kErrTimeoutFull);
+      if (i != c.skip())
+        mbar_wait(c.full(i % c.ring), (i / c.ring) & 1, c.p.a.err, kErrTimeoutFull, kDefaultWaitNs);
+  }
+  static BSG_DEV void drain_mma(const Ctx& c, uint32_t stream) {
+    if (elect_one()) tc_commit(c.ended(stream));  // (the lane that issued them)
+    __syncwarp();
+    mbar_wait(c.ended(stream), 0u, c.p.a.err, kErrTimeoutFull, kDefaultWaitNs);
   }
 
   // ---- MMA warp of a stream
@@ -625,6 +635,7 @@ struct AttnPrefix {
       for (int b = 0; b < T::kStreams; ++b) {
         mbar_init(c.scores(b), 1);
         mbar_init(c.taken(b), 128);
+        mbar_init(c.ended(b), 1);
       }
       for (int b = 0; b < T::kBufs; ++b) {
         mbar_init(c.probs(b), 128);
@@ -656,7 +667,11 @@ struct AttnPrefix {
     tc_before();
     __syncthreads();
     tc_after();
-    if (c.words()[1] != 0u && threadIdx.x == 0) drain(c);
+    if (c.words()[1] != 0u) {
+      if (warp == kCopyWarp && (threadIdx.x & 31) == 0) drain_copies(c);
+      if (warp >= kMmaWarp) drain_mma(c, warp - kMmaWarp);
+      __syncthreads();
+    }
     if (warp == kMmaWarp) tc_dealloc(c.tmem, 512);
   }
 };

@@ -446,6 +446,14 @@ int bsgemv_attn_run(bsgemv_attn_plan_t plan, const void* q, int64_t q_stride, co
 /* Synchronise `stream`, then read and clear the plan's error word (as bsgemv_device_status). */
 int bsgemv_attn_device_status(bsgemv_attn_plan_t plan, void* stream);
 
+/* Test hook, as bsgemv_plan_set_test_fault: in the plan's next calls the first warp of the streaming
+ * kernel (kernel 0: a tile is 4096 / D positions, K and V) or the first block of the tensor-memory
+ * prefix kernel (kernel 1: 64 positions, K and V in turn) leaves out the copy of tile `skip_tile` of its
+ * range (-1: none), and all waits give up after wait_ns (0: the default).  (plan, 0, -1, 0) restores
+ * normal calls. */
+int bsgemv_attn_set_test_fault(bsgemv_attn_plan_t plan, int kernel, int skip_tile,
+                               int64_t wait_ns);
+
 /* Free the plan (synchronises the device first).  NULL is a no-op. */
 int bsgemv_attn_destroy(bsgemv_attn_plan_t plan);
 

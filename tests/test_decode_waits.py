@@ -6,6 +6,7 @@ reports it once, and the plan's next calls give the bits of a call made before.
 import pytest
 
 from block_scaled_bit_gb300 import bsgemv
+from test_attn import Problem
 from test_moe import Layer, inputs, small_scales
 
 WAIT_NS = 1_000_000
@@ -57,5 +58,21 @@ def test_experts(fmt, act, bs, zp, H, I, E, k, T, product, where):
         recovers(torch, plan, run, product, 0 if where == "first" else n0 - 1)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("act,B,Hq,Hkv,D,ps,P", [
+    ("bf16", 32, 32, 8, 128, 16, 32768),   # both streams of a block on the same rows
+    ("bf16", 64, 32, 8, 128, 64, 32768),   # 256 rows
+    ("f16", 24, 40, 8, 64, 32, 20001),
+    ("bf16", 48, 16, 2, 256, 16, 65536),   # one stream
+])
+@pytest.mark.parametrize("tile", [0, 1, 3, 12])
+def test_prefix_on_tensor_memory(act, B, Hq, Hkv, D, ps, P, tile):
+    import torch
+    pr = Problem(torch, act, B, Hq, Hkv, D, ps, P, [P + 1 + 3 * i for i in range(B)], seed=9)
+    with bsgemv.AttnPlan(*pr.plan) as plan:
+        recovers(torch, plan, lambda: pr.run(plan), 1, tile)
+
+
 def test_refused():
+    assert bsgemv.lib().bsgemv_attn_set_test_fault(None, 0, 0, 0) == bsgemv.ERR_INVALID_ARG
     assert bsgemv.lib().bsgemv_moe_set_test_fault(None, 0, 0, 0) == bsgemv.ERR_INVALID_ARG
