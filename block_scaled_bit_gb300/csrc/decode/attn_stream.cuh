@@ -392,10 +392,13 @@ struct AttnStream {
     settle(in);
     Place out = in;
     int page = in.x < x1 ? fetch(p, in.u, in.x - in.u.first, box) : 0;
+    int loads = 0, done = 0;  // tiles sent for, tiles worked on
+    const int skip = w == 0 ? p.skip[0] : -1;
     const auto load = [&](int stage) {
       if (in.x >= x1) return;
-      issue(sp, in.u, in.x - in.u.first, ring + stage * 2 * T::kHalf, bars + 8 * stage, box, page,
-            lane);
+      if (loads++ != skip)
+        issue(sp, in.u, in.x - in.u.first, ring + stage * 2 * T::kHalf, bars + 8 * stage, box, page,
+              lane);
       ++in.x;
       settle(in);
       if (in.x < x1) page = fetch(p, in.u, in.x - in.u.first, box);
@@ -444,11 +447,14 @@ struct AttnStream {
           a.l[i] = 0.f;
         }
       }
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars + 8 * stage, phase, p.err, kErrTimeoutFull))) {
-        // the warp's work ends here, once its other tiles in flight have landed (bounded again)
-        for (int i = 1; i < T::kStages; ++i) {
+      if (!__all_sync(0xFFFFFFFFu,
+                      mbar_wait(bars + 8 * stage, phase, p.err, kErrTimeoutFull, p.wait_ns))) {
+        // the warp's work ends here, once its tiles in flight have landed: this one and those after
+        // it that were sent for (bounded by the usual limit, whatever the waits')
+        for (; done < loads; ++done) {
+          if (done != skip)
+            mbar_wait(bars + 8 * stage, phase, p.err, kErrTimeoutFull, kDefaultWaitNs);
           if (++stage == T::kStages) { stage = 0; phase ^= 1u; }
-          mbar_wait(bars + 8 * stage, phase, p.err, kErrTimeoutFull);
         }
         return;
       }
@@ -456,6 +462,7 @@ struct AttnStream {
       if (pos0 < u.lo || pos0 + K > u.hi) clear(ring_p + stage * 2 * T::kHalf, u, pos0, lane);
       tile(p, u, pos0, ring + stage * 2 * T::kHalf, q, qs, lane, a);
       __syncwarp();  // every lane is done with the stage that the next load fills
+      ++done;
       load(stage == 0 ? T::kStages - 1 : stage - 1);
       if (++stage == T::kStages) { stage = 0; phase ^= 1u; }
       ++out.x;

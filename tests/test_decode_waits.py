@@ -73,6 +73,21 @@ def test_prefix_on_tensor_memory(act, B, Hq, Hkv, D, ps, P, tile):
         recovers(torch, plan, lambda: pr.run(plan), 1, tile)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("act,B,Hq,Hkv,D,ps,P,own", [
+    ("bf16", 16, 32, 8, 128, 16, 0, 4000),     # own positions only
+    ("f16", 8, 8, 4, 64, 32, 30000, 12000),    # with the prefix
+    ("bf16", 8, 16, 2, 256, 16, 300, 9000),
+    ("bf16", 64, 32, 8, 128, 64, 32768, 2500),  # beside the prefix kernel
+])
+@pytest.mark.parametrize("tile", [0, 1, 2, 4])
+def test_streaming(act, B, Hq, Hkv, D, ps, P, own, tile):
+    import torch
+    pr = Problem(torch, act, B, Hq, Hkv, D, ps, P, [P + own + 3 * i for i in range(B)], seed=9)
+    with bsgemv.AttnPlan(*pr.plan) as plan:
+        recovers(torch, plan, lambda: pr.run(plan), 0, tile)
+
+
 def test_refused():
     assert bsgemv.lib().bsgemv_attn_set_test_fault(None, 0, 0, 0) == bsgemv.ERR_INVALID_ARG
     assert bsgemv.lib().bsgemv_moe_set_test_fault(None, 0, 0, 0) == bsgemv.ERR_INVALID_ARG
