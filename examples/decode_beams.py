@@ -2,8 +2,8 @@
 
     prompt      its tokens go through the step one by one, into one sequence of the cache
     fork        every beam becomes a copy of the prompt's sequence: whole pages are shared
-    step        extend -> per layer: qkv GEMV, write, attention over shared prefix and own pages,
-                output GEMV, router, experts -> vocabulary GEMV
+    step        extend -> per layer: qkv GEMV, write (the sequences that grew), attention over shared
+                prefix and own pages, output GEMV, router, experts -> vocabulary GEMV
     fork        the best continuations' parents become the next beams
     compact     at the end, with the prompt's own sequence freed
 
@@ -92,6 +92,7 @@ class Decoder:
                                 device="cuda")
         self.refs, self.tables = ints(num_pages), ints(max_seqs, max_pages, fill=-1)
         self.lens = ints(max_seqs)
+        self.short = torch.zeros((), dtype=torch.bool, device="cuda")  # a page was wanted, none left
         self.cache = bsgemv.PageCache(2 * layers, num_pages, page_size * Hkv * D * 2, page_size,
                                       max_seqs, max_pages)
 
@@ -104,13 +105,17 @@ class Decoder:
         probabilities [n, vocab]."""
         n, Hq, Hkv, D = tokens.shape[0], self.Hq, self.Hkv, self.D
         slots = torch.arange(seqs, seqs + n, dtype=torch.int32, device="cuda")
-        self.cache.extend(self.pool, self.refs, self.tables, self.lens, slots)
+        grown = torch.empty_like(slots)
+        self.cache.extend(self.pool, self.refs, self.tables, self.lens, slots, grown)
+        self.short |= (grown == 0).any()
+        # a sequence that did not grow has its last token where a new one would be written
+        write = torch.where(grown > 0, slots, -1)
         tables, lens = self.tables[seqs:seqs + n], self.lens[seqs:seqs + n]
         x = self.embed[tokens] + self.place[lens.long() - 1]
         for i, (qkv_of, o_of, experts) in enumerate(zip(self.qkv, self.o, self.experts)):
             qkv = qkv_of(norm(x)).view(n, Hq + 2 * Hkv, D)
             q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
-            self.cache.write(self.pool, self.tables, self.lens, slots, k, v, head_stride=D,
+            self.cache.write(self.pool, self.tables, self.lens, write, k, v, head_stride=D,
                              row_stride=Hkv * D, k_plane=2 * i, v_plane=2 * i + 1)
             out = torch.empty(n, Hq, D, dtype=torch.float16, device="cuda")
             self.attn.run(q, self.plane(2 * i), self.plane(2 * i + 1), self.tables[prefix_seq],
@@ -119,7 +124,15 @@ class Decoder:
             x = x + experts(norm(x))
         return torch.log_softmax(self.head(norm(x)).float(), -1)
 
+    def fork(self, parents, children):
+        new = torch.empty_like(children)
+        self.cache.fork(self.pool, self.refs, self.tables, self.lens, parents.int(), children, new)
+        self.short |= (new == -2).any()
+
     def check(self):
+        """Raises if a sequence found no page or row to grow in, or a wait of a kernel ran out."""
+        if self.short:
+            raise RuntimeError("the cache's pages or a sequence's row ran out")
         for plan in [self.attn] + [e.plan for e in self.experts]:
             status = plan.device_status()
             if status != 0:
@@ -129,20 +142,17 @@ class Decoder:
 def beam_search(model: Decoder, prompt, beams: int, tokens: int):
     """The `beams` best continuations found, [beams, tokens] with their log probabilities.  Slots
     0 .. beams-1 hold the beams, slot `beams` the prompt."""
-    def fork(parents):
-        model.cache.fork(model.pool, model.refs, model.tables, model.lens, parents.int(), slots)
-
     slots = torch.arange(beams, dtype=torch.int32, device="cuda")
     for t in prompt:
         logp = model.step(t[None], seqs=beams)
     score, last = logp[0].topk(beams)
-    fork(torch.full_like(slots, beams))
+    model.fork(torch.full_like(slots, beams), slots)
     out = last[:, None]
     for _ in range(tokens - 1):
         logp = model.step(last, seqs=0, prefix_seq=beams, prefix_len=len(prompt))
         score, flat = (score[:, None] + logp).flatten().topk(beams)
         parents, last = flat // logp.shape[1], flat % logp.shape[1]
-        fork(parents)
+        model.fork(parents, slots)
         out = torch.cat([out[parents], last[:, None]], 1)
     model.check()
     return out, score
@@ -154,7 +164,13 @@ def main() -> int:
     ap.add_argument("--tokens", type=int, default=24)
     ap.add_argument("--prompt", type=int, default=37)
     a = ap.parse_args()
-    model = Decoder(max_seqs=a.beams + 1)
+    if not 1 <= a.beams <= 31 or a.tokens < 1 or a.prompt < 1:
+        ap.error("1 to 31 beams, a token and a prompt of one token at least")
+    # every sequence's pages, and the copies of a fork beside the pages that it gives back
+    ps = 16
+    pages = -(-(a.prompt + a.tokens) // ps)
+    model = Decoder(max_seqs=a.beams + 1, page_size=ps, max_pages=pages,
+                    num_pages=(a.beams + 1) * pages + a.beams)
     g = torch.Generator().manual_seed(1)
     prompt = torch.randint(model.embed.shape[0], (a.prompt,), generator=g).cuda()
     out, score = beam_search(model, prompt, a.beams, a.tokens)

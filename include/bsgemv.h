@@ -512,7 +512,9 @@ int bsgemv_cache_extend(bsgemv_cache_t cache, void* pool, int32_t* refs, int32_t
  * Put one token's K and V of one layer at the last position (lens - 1) of each of the sequences
  * seqs[0 .. n-1]: for i < n, head h < heads and d: k[i * kv_stride + h * D + d] goes to element
  * h * head_stride + row * row_stride + d of its page in plane k_plane, and v likewise in v_plane.
- * 2-byte elements; D and the strides multiples of 8; k, v and pool 16-byte aligned.
+ * 2-byte elements; D and the strides multiples of 8; k, v and pool 16-byte aligned.  Only for
+ * sequences that the last bsgemv_cache_extend let grow: the last position of one that it left as it was
+ * is a token already there, in a page that other sequences may hold, and is overwritten.
  */
 int bsgemv_cache_write(bsgemv_cache_t cache, void* pool, const int32_t* tables,
                        const int32_t* lens, const int32_t* seqs, const void* k, const void* v,
