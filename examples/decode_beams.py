@@ -51,13 +51,14 @@ class Experts:
         self.w13, self.w2 = stacked(2 * I, H, seed), stacked(H, I, seed + 1)
         g = torch.Generator().manual_seed(seed)
         self.router = (torch.randn(H, E, generator=g) / math.sqrt(H)).half().cuda()  # [K, N]
-        self.route = bsgemv.DensePlan("f16", E, H, max_M=min(max_T, 32))
+        self.route = bsgemv.DensePlan("f16", E, H, max_M=min(max_T, 8))  # eight rows a call at most
         self.plan = bsgemv.MoePlan("int4", "f16", 32, True, H, I, E, top_k, max_T)
         self.E = E
 
     def __call__(self, x):
         logits = torch.empty(x.shape[0], self.E, dtype=torch.float16, device=x.device)
-        self.route.run(x, self.router, logits)
+        for i in range(0, x.shape[0], 8):
+            self.route.run(x[i:i + 8], self.router, logits[i:i + 8])
         y = torch.empty_like(x)
         self.plan.run(x, logits, self.w13.W, self.w13.scales, self.w13.zp,
                       self.w2.W, self.w2.scales, self.w2.zp, y)

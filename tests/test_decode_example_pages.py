@@ -50,7 +50,9 @@ def test_a_row_that_is_full_is_an_error():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("args", [(), ("--tokens", "60", "--prompt", "290", "--beams", "7"),
-                                  ("--tokens", "1", "--prompt", "1", "--beams", "1")])
+                                  ("--tokens", "1", "--prompt", "1", "--beams", "1"),
+                                  ("--tokens", "9", "--beams", "8"),
+                                  ("--tokens", "5", "--beams", "31")])
 def test_the_command_sizes_its_cache(args):
     r = subprocess.run([sys.executable, HERE + "/../examples/decode_beams.py", *args],
                        capture_output=True, text=True, timeout=300)
