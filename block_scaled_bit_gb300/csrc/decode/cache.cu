@@ -367,7 +367,8 @@ __global__ void __launch_bounds__(kCopyThreads) write_token(CacheParams p, Write
     const int x = is_v ? u - w.heads * per : u, h = x / per, d = (x % per) * 8;
     const int plane = is_v ? w.v_plane : w.k_plane;
     uint8_t* base = p.pool + (static_cast<int64_t>(plane) * p.num_pages + page) * p.page_bytes;
-    const uint16_t* from = (is_v ? w.v : w.k) + blockIdx.x * w.kv_stride + h * w.D + d;
+    const uint16_t* from =
+        (is_v ? w.v : w.k) + blockIdx.x * w.kv_stride + static_cast<int64_t>(h) * w.D + d;
     *reinterpret_cast<uint4*>(base + 2 * (h * w.head_stride + row * w.row_stride + d)) =
         *reinterpret_cast<const uint4*>(from);
   }
@@ -616,10 +617,12 @@ int bsgemv_cache_write(bsgemv_cache_t c, void* pool, const int32_t* tables, cons
       !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(tables, 4) || !aligned_to(lens, 4) ||
       !aligned_to(seqs, 4))
     return BSGEMV_ERR_MISALIGNED;
-  // the last element of a page
-  if (head_stride >= c->page_bytes || row_stride >= c->page_bytes) return BSGEMV_ERR_INVALID_ARG;
-  if (2 * ((heads - 1) * head_stride + (c->page_size - 1) * row_stride + D) > c->page_bytes)
-    return BSGEMV_ERR_INVALID_ARG;
+  // The last element of a page lies in it: its elements after the last head's first, then after the
+  // last row's first (by division: the products can pass 64 bits).
+  int64_t left = c->page_bytes / 2 - D;
+  if (left < 0 || (heads > 1 && head_stride > left / (heads - 1))) return BSGEMV_ERR_INVALID_ARG;
+  left -= (heads - 1) * head_stride;
+  if (c->page_size > 1 && row_stride > left / (c->page_size - 1)) return BSGEMV_ERR_INVALID_ARG;
   int rc = decode_check_device(c->device);
   if (rc != BSGEMV_OK) return rc;
   CacheParams p = params_of(c, pool, n);
