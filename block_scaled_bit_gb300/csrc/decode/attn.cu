@@ -109,7 +109,8 @@ int bsgemv_attn_run(bsgemv_attn_plan_t plan, const void* q, int64_t q_stride, co
   const int mode = prefix_len == 0 ? kAttnNoPrefix
                    : attn_prefix_streams(rows, plan->Hkv, plan->D, prefix_len) ? kAttnPrefixStream
                                                                                : kAttnPrefixTensor;
-  // the line of tiles (attn_stream.cuh, attn_prefix.cuh) is counted in 32 bits
+  // the line of tiles (attn_stream.cuh, attn_prefix.cuh) is counted in 31 bits: the prefix's part of it
+  // (the sequences' own follows from lens, on the device)
   const int64_t row_tiles = (rows + kAttnRows - 1) / kAttnRows;
   if (row_tiles * plan->Hkv * (prefix_len / (4096 / plan->D) + 8) >= (int64_t{1} << 30))
     return BSGEMV_ERR_UNSUPPORTED;
@@ -164,7 +165,7 @@ int bsgemv_attn_device_status(bsgemv_attn_plan_t plan, void* stream) {
   if (plan == nullptr) return BSGEMV_ERR_INVALID_ARG;
   const int rc = decode_check_device(plan->device);
   if (rc != BSGEMV_OK) return rc;
-  return decode_error_status(static_cast<unsigned*>(plan->ws), stream);
+  return decode_error_status(static_cast<unsigned*>(plan->ws), stream, kErrAttnLine);
 }
 
 int bsgemv_attn_destroy(bsgemv_attn_plan_t plan) {

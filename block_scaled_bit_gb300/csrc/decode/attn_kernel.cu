@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(128)
     int count, rows, r;     // r: the row in a part
   } pre = {nullptr, 0, 0, 1, 0}, own = pre;
   int twice = 1;            // two streams' rows in each part of the prefix
-  if (here) {
+  if (here && !s.over) {  // (else the row is NaN, and the status call says why)
     // (x0, tiles: a unit's stretch of the line)
     const auto stream_list = [&](int unit, int x0, int tiles, int r) {
       const int w0 = attn_owner(s, x0 + kAttnCost), w1 = attn_owner(s, x0 + tiles - 1);

@@ -21,6 +21,10 @@ constexpr int kAttnMaxGroup = 64;
 constexpr int kAttnRows = 16;      // query rows of a streaming part (an mma tile)
 constexpr int kAttnWarps = 4;      // warps of a streaming block, each a worker of its own
 
+// Bit of the error word, beside those of waits that ran out: the lengths' tiles are more than a
+// call can count.
+constexpr unsigned kErrAttnLine = 4u;
+
 struct AttnParams {
   const uint16_t *q, *k, *v;
   int64_t q_stride, page_stride, head_stride, row_stride;

@@ -32,7 +32,8 @@ struct AttnSplit {
   int pre_units;     // prefix units, 0 where another kernel does it
   int pre_tiles;     // stretch of a prefix unit
   int pre_start;     // where the prefix units start
-  int total;         // the line's length (below 2^31)
+  int total;         // the line's length; nothing is done where it does not fit 31 bits
+  bool over;         // it does not
   int base, extra;   // a worker's range; the first `extra` have one more
   int workers;       // workers with a range
 };
@@ -48,12 +49,18 @@ struct AttnTile {
   static constexpr int kWarpB = kStages * 2 * kHalf + kQ;
 };
 
+// Lengths come from the device, so no host check bounds them or their sum: sums of tiles stop at
+// kAttnMost, where a single sequence of more than 2^30 positions is at once.
+constexpr int kAttnMost = 1 << 29;
+BSG_DEV int attn_sum(int a, int b) { return min(a + b, kAttnMost); }
+
 // Tiles of sequence b's own positions: [prefix_len, len) in tiles that start at a multiple of
 // kKeys.  A slot without a sequence has none.
 template <int D>
 BSG_DEV int own_tiles(const AttnParams& p, int b) {
   const int len = p.lens[b];
   if (len < max(p.prefix_len, 1) || len == p.prefix_len) return 0;
+  if (len > (1 << 30)) return kAttnMost;
   constexpr int K = AttnTile<D>::kKeys;
   return (len + K - 1) / K - p.prefix_len / K;
 }
@@ -69,21 +76,21 @@ BSG_DEV void attn_prefix_sums(const AttnParams& p, int* cum, int* tmp) {
     if (b0 + i < p.B) {
       const int t = own_tiles<D>(p, b0 + i);
       cum[b0 + i] = sum;
-      sum += t ? t + kAttnCost : 0;
+      sum = attn_sum(sum, t ? t + kAttnCost : 0);
     }
   int inc = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-    if (lane >= d) inc += o;
+    if (lane >= d) inc = attn_sum(inc, o);
   }
   if (lane == 31) tmp[w] = inc;
   __syncthreads();
   int before = inc - sum;
-  for (int i = 0; i < w; ++i) before += tmp[i];
+  for (int i = 0; i < w; ++i) before = attn_sum(before, tmp[i]);
   for (int i = 0; i < per; ++i)
     if (b0 + i < p.B) cum[b0 + i] += before;
-  if (threadIdx.x == n - 1) cum[p.B] = before + sum;
+  if (threadIdx.x == n - 1) cum[p.B] = attn_sum(before, sum);
   __syncthreads();
 }
 
@@ -93,10 +100,13 @@ BSG_DEV AttnSplit attn_split(const AttnParams& p, int own, bool with_prefix, int
   const int G = p.Hq / p.Hkv;
   s.row_tiles = (G + kAttnRows - 1) / kAttnRows;
   s.own_units = p.B * p.Hkv * s.row_tiles;
-  s.pre_start = own * p.Hkv * s.row_tiles;  // (own: cum[B])
+  const int64_t start = static_cast<int64_t>(own) * (p.Hkv * s.row_tiles);  // (own: cum[B])
   s.pre_tiles = with_prefix ? (p.prefix_len + AttnTile<D>::kKeys - 1) / AttnTile<D>::kKeys + kAttnCost : 0;
   s.pre_units = s.pre_tiles ? p.Hkv * ((p.B * G + kAttnRows - 1) / kAttnRows) : 0;
-  s.total = s.pre_start + s.pre_units * s.pre_tiles;
+  const int64_t total = start + s.pre_units * s.pre_tiles;
+  s.over = own == kAttnMost || total > 0x7FFFFFFF;
+  s.pre_start = s.over ? 0 : static_cast<int>(start);
+  s.total = s.over ? 0 : static_cast<int>(total);
   s.workers = min(workers, s.total);
   s.base = s.workers ? s.total / s.workers : 0;
   s.extra = s.total - s.base * s.workers;
@@ -500,6 +510,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1)
     for (int i = threadIdx.x; i <= p.B; i += blockDim.x) p.cum[i] = cum[i];
   const AttnSplit s =
       attn_split<D>(p, cum[p.B], mode == kAttnPrefixStream, gridDim.x * kAttnWarps);
+  if (s.over && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, kErrAttnLine);
   // neighbouring ranges on different SMs: warp-major over the blocks
   AttnStream<BF16, D>::worker(sp, s, cum, smem + warp * T::kWarpB, smem_u32(bars) + warp * 32,
                               warp * gridDim.x + blockIdx.x, lane);

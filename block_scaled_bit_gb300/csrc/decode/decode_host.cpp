@@ -75,7 +75,7 @@ int decode_alloc(void** out, size_t bytes) {
   return BSGEMV_OK;
 }
 
-int decode_error_status(unsigned* err, void* stream) {
+int decode_error_status(unsigned* err, void* stream, unsigned unsupported) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   unsigned word = 0;
   if (cudaMemcpyAsync(&word, err, sizeof word, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
@@ -84,7 +84,8 @@ int decode_error_status(unsigned* err, void* stream) {
     cudaGetLastError();
     return BSGEMV_ERR_CUDA;
   }
-  return word == 0 ? BSGEMV_OK : BSGEMV_ERR_DEVICE_TIMEOUT;
+  if (word & ~unsupported) return BSGEMV_ERR_DEVICE_TIMEOUT;
+  return word == 0 ? BSGEMV_OK : BSGEMV_ERR_UNSUPPORTED;
 }
 
 }  // namespace bsg

@@ -23,8 +23,9 @@ int decode_check_device(int device);
 // A zeroed device allocation (BSGEMV_ERR_CUDA if it cannot be had).
 int decode_alloc(void** out, size_t bytes);
 
-// Synchronise `stream`, read and clear an error word: the status it stands for.
-int decode_error_status(unsigned* err, void* stream);
+// Synchronise `stream`, read and clear an error word: the status it stands for (BSGEMV_ERR_UNSUPPORTED
+// for the bits of `unsupported` alone).
+int decode_error_status(unsigned* err, void* stream, unsigned unsupported = 0);
 
 // A tiled tensor map with zero fill (strides in bytes, from the second dimension on).
 int decode_encode(CUtensorMap* tm, CUtensorMapDataType type, int rank, const void* base,

@@ -412,7 +412,8 @@ int bsgemv_moe_destroy(bsgemv_moe_plan_t plan);
  * prefix_table[j / page_size] for the prefix, of page tables[b * table_stride + j / page_size]
  * for own positions (a page in which the prefix ends is read from prefix_table up to prefix_len
  * and from the sequence's table after it).  What pages hold outside these positions does not
- * matter, NaN included.  A slot with lens[b] < max(prefix_len, 1) holds no sequence: its
+ * matter, NaN included.  lens[b] is at most page_size times the entries of the sequence's row of
+ * `tables`.  A slot with lens[b] < max(prefix_len, 1) holds no sequence: its
  * out rows are 0 and its lse -inf, and its row of `tables` is not read.
  *
  * q [B][Hq][D] with q_stride elements between sequences, out [B][Hq][D] contiguous, fp16 or bf16
@@ -443,7 +444,11 @@ int bsgemv_attn_run(bsgemv_attn_plan_t plan, const void* q, int64_t q_stride, co
                     const int32_t* tables, int64_t table_stride, const int32_t* lens, int B,
                     float scale, void* out, float* lse, void* stream);
 
-/* Synchronise `stream`, then read and clear the plan's error word (as bsgemv_device_status). */
+/* Synchronise `stream`, then read and clear the plan's error word (as bsgemv_device_status).
+ * BSGEMV_ERR_UNSUPPORTED: a call's lens are more than it can take.  Each is at most 2^30, and
+ * Hkv * ceil(Hq / Hkv / 16) times the sum of (lens[b] - prefix_len) * D / 4096 + 4 over the slots has to
+ * stay below 2^30 (16 TB of keys and values to read).  Beyond that a call may read none of them; the out
+ * rows of its sequences are NaN then. */
 int bsgemv_attn_device_status(bsgemv_attn_plan_t plan, void* stream);
 
 /* Test hook, as bsgemv_plan_set_test_fault: in the plan's next calls the first warp of the streaming
