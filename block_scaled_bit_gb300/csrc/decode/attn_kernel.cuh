@@ -2,7 +2,7 @@
 //
 // Every part of the work -- a tile of query rows of one kv head with a range of positions --
 // leaves its softmax unnormalised in the workspace: per row the running maximum m (of the scores in
-// base 2), the sum l of the rounded numerators and the fp32 row of their products with V.
+// base 2), the sum l of the numerators and the fp32 row of their products with V.
 // attn_merge puts a row's parts together:  o = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.
 // m = -inf says that a part has no positions (its sums may not be written).  A running maximum
 // passes NaN over and can be -inf over positions all of whose scores are; such a part is stored
@@ -62,11 +62,12 @@ AttnLayout attn_layout(int Hq, int Hkv, int D, int max_B, int sms);
 // launch fewer, 5 to 7 us faster to start), which reads it once for every 16 query rows of a kv
 // head, or through the tensor-memory kernel, which reads it once for every 128 or 256.  What the
 // streaming kernel reads again comes from L2 and costs about 1 us for 12 MB: it wins up to 80 MB.
-// Measured, us, streaming / tensor, 8 kv heads: D = 128, P = 500, 128 rows 16.3 / 21.6; P = 4096,
-// 64 rows 19.6 / 22.9, 128 rows 30.8 / 26.1; P = 32768, 16 rows 33.6 / 41.4, 32 rows 44.6 / 42;
-// D = 64, P = 32768, 32 rows 27.4 / 29.8, 64 rows 41.8 / 31.0.  At D = 256 its tiles have 16
-// positions and its warps are half as many: it wins up to 8 MB in all (2 kv heads, P = 500,
-// 128 rows 15.6 / 18.3; P = 4096, 16 rows 25.4 / 19.7, 128 rows 28.8 / 24.3).
+// Measured, us, streaming / tensor, 8 kv heads: D = 128, P = 496, 128 rows 13.2 / 17.9; P = 1024,
+// 256 rows 25.1 / 25.9; P = 4096, 64 rows 18.3 / 20.5, 128 rows 28.4 / 21.6; P = 8192, 64 rows
+// 27.0 / 23.1; P = 32768, 16 rows 32.7 / 43.8, 32 rows 45.3 / 45.3; D = 64, P = 32768, 32 rows
+// 27.0 / 33.9, 64 rows 45.2 / 34.5.  At D = 256 its tiles have 16
+// positions and its warps are half as many: it wins up to 8 MB in all (8 kv heads, P = 256, 64 rows
+// 15.7 / 18.6, P = 512, 128 rows 22.3 / 20.9; 2 kv heads, P = 128, 128 rows 12.8 / 13.1).
 inline bool attn_prefix_streams(int rows, int Hkv, int D, int prefix_len) {
   const int64_t once = int64_t{4} * Hkv * D * prefix_len, tiles = (rows + kAttnRows - 1) / kAttnRows;
   return D == 256 ? tiles * once <= (int64_t{8} << 20) : (tiles - 1) * once <= (int64_t{80} << 20);

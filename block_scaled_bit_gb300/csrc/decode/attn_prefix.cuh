@@ -1,13 +1,19 @@
 // attn_prefix.cuh -- the shared prefix on the 5th-generation tensor cores.
 //
 // All sequences' query rows of a kv head (B x Hq / Hkv of them) against the prefix's K and V, read
-// once for every 256 rows.  Bound: 128 rows give 128 flops a byte of K and V, 256 rows 256, so
-// up to there the kernel is a memory stream, beyond it the tensor cores' and the exponentials'.
-// Measured: 256 rows, 8 kv heads of 128, 32768 positions: 35 us for 134 MB and 34 Gflop, of which
-// 0.9 us for each of the 27 key tiles of a block (softmax 1250 cycles a job, the MMAs some 1280 for
-// both streams: scores of 64 columns take 48 cycles a step, the rate of shared memory), 3.4 us
-// before the first scores, 4 to write the parts.  384 rows, 2 kv heads of 256, 16384 positions in pages of 16:
-// 22 us, 1.2 us a tile: its K and V come as 32 boxes of 2 KB, three times from L2.
+// once for every 256 rows.  Bound: 128 rows give 192 flops a byte of K and V (P V is done twice, see
+// below), 256 rows 384, so with 128 the kernel is a memory stream, beyond it the tensor cores' and
+// the exponentials'.
+// Measured: 256 rows, 8 kv heads of 128, 32768 positions: 41 us for 134 MB and 52 Gflop: some 1.1 us for
+// each of the 27 key tiles of a block (the MMAs 1850 cycles for both streams: scores of 64 columns
+// take 48 cycles a step, the rate of shared memory, a step of P V 67), 3.4 us before the first
+// scores, 4 to write the parts.  384 rows, 2 kv heads of 256, 16384 positions in pages of 16: 27 us
+// under a profiler; its K and V come as 32 boxes of 2 KB, three times from L2.
+//
+// P enters the second product in two parts of V's type, rounded and what the rounding left, so that it
+// keeps 2^-16 (bf16) or 2^-22 (f16) of itself.  With one part, the outputs' rms error against 64 bits
+// was 1.1 to 1.4 times that of attention in fp32 (64 sequences, bf16: 4.08e-5 and 2.91e-5); with two
+// it is the same.  It costs 6 us of the 41 here, 1.5 of 27 at 256 d, 2 to 5 % of the streaming kernel.
 //
 // A block (one per SM) holds two streams of work, each a warpgroup with its own running maximum and
 // sum, and an output accumulator in tensor memory:
@@ -19,16 +25,14 @@
 // from shared memory, M = 128) and O += P V (P from tensor memory; V's d is contiguous, an
 // MN-major operand).  A row of S lies in one lane, so softmax needs no exchange between threads.
 // Its threads take a row's scores into registers at once and free S's columns for the next tile's,
-// which the tensor cores work out while the numerators are made; P goes to one of two places of
-// its own.  (One MMA warp for both streams waited in turn for either's probabilities, 450 of 1350
-// cycles a job.  Two places of S, or P in its scores' place with two of them, are no faster at 128
-// d, and slower at 256, where the ring has few tiles.)
+// which the tensor cores work out while the numerators are made; P goes to a place of its own.
+// (One MMA warp for both streams waited in turn for either's probabilities, a third of a job's time.)
 // O is scaled to a new maximum only when a row's has grown by more than 2^8 since O's (P stays
 // below 2^8, far from overflow), which is rare after the first tiles.
 // The line of (kv head, row block, key tile) is cut into equal ranges, one per block; a unit counts
 // kAttnPreCost tiles more than it has, what it costs a block to begin and end one: at 256 rows of
-// 128 d, 2.7 us until the queries are there, 4 us to write the part, 0.9 us a tile (with a cost of
-// 4 the blocks that touch two units ended 5 us after the others).
+// 128 d, 2.7 us until the queries are there, 4 us to write the part, 0.9 to 1.1 us a tile (with a cost
+// of 4 the blocks that touch two units ended 5 us after the others).
 #pragma once
 
 #include "attn_stream.cuh"
@@ -41,7 +45,6 @@ template <int D>
 struct AttnPre {
   static constexpr int kKeys = 64;                      // positions of a tile
   static constexpr int kStreams = D == 256 ? 1 : 2;
-  static constexpr int kBufs = 2 * kStreams;            // places of P
   static constexpr int kTileB = kKeys * D * 2;          // bytes of a K (or V) tile
   static constexpr int kQB = 128 * D * 2;               // bytes of a query tile
   static constexpr int kRingMax = (224 * 1024 - kStreams * kQB) / kTileB;
@@ -53,11 +56,12 @@ struct AttnPre {
   static constexpr int kPairRing = kRing / 4 * 4;
   static constexpr int kOffRing = kStreams * kQB;
   static constexpr int kOffBar = kOffRing + kRing * kTileB;
-  static constexpr int kBars = 2 * kRing + 3 * kStreams + 2 * kBufs + 1;
+  static constexpr int kBars = 2 * kRing + 5 * kStreams + 1;
   static constexpr int kSmem = kOffBar + (kBars * 8 + 12 + 15) / 16 * 16 + 1024;  // (1024-byte tiles)
   static constexpr int kThreads = 32 * (5 * kStreams + 1);
   static constexpr int kSlotRows = 128 * kStreams;
-  // tensor memory: per stream 64 columns of S and twice 32 of P, then the streams' O
+  // tensor memory: per stream 64 columns of S and twice 32 of P (rounded, and what that left), then the
+  // streams' O
   static constexpr int kColO = kStreams * 2 * kKeys;
   static_assert(kColO + kStreams * D <= 512, "tensor memory");
   static_assert(kRing >= 5 && kSmem <= 232448, "shared memory");
@@ -199,23 +203,18 @@ struct AttnPrefix {
     BSG_DEV uint32_t bar(int i) const { return base_u + T::kOffBar + 8 * i; }
     BSG_DEV uint32_t full(int i) const { return bar(i); }                   // ring tile landed
     BSG_DEV uint32_t empty(int i) const { return bar(T::kRing + i); }       // ring tile read
-    // of a stream's job j (numbered over the block's whole range): its place of P, whose barriers'
-    // phase; those of S have phase j & 1
-    static BSG_DEV uint32_t buf(uint32_t stream, uint32_t j) { return 2 * stream + (j & 1u); }
-    static BSG_DEV uint32_t phase(uint32_t j) { return (j >> 1) & 1u; }
+    // of a stream; its job j (numbered over the block's whole range) is their phase j & 1
     static constexpr int kS = 2 * T::kRing, kP = kS + 2 * T::kStreams;
     BSG_DEV uint32_t scores(uint32_t stream) const { return bar(kS + stream); }               // S written
     BSG_DEV uint32_t taken(uint32_t stream) const { return bar(kS + T::kStreams + stream); }  // S read
-    BSG_DEV uint32_t probs(uint32_t b) const { return bar(kP + b); }                          // P written
-    BSG_DEV uint32_t out(uint32_t b) const { return bar(kP + T::kBufs + b); }                 // P V done
-    BSG_DEV uint32_t query() const { return bar(kP + 2 * T::kBufs); }                         // Q written
-    BSG_DEV uint32_t ended(uint32_t stream) const { return bar(kP + 2 * T::kBufs + 1 + stream); }  // (drain)
+    BSG_DEV uint32_t probs(uint32_t stream) const { return bar(kP + stream); }                // P written
+    BSG_DEV uint32_t out(uint32_t stream) const { return bar(kP + T::kStreams + stream); }    // P V done
+    BSG_DEV uint32_t ended(uint32_t stream) const { return bar(kP + 2 * T::kStreams + stream); }  // (drain)
+    BSG_DEV uint32_t query() const { return bar(kP + 3 * T::kStreams); }                      // Q written
     BSG_DEV int skip() const { return blockIdx.x == 0 ? p.a.skip[1] : -1; }
     // columns of S and P
     static BSG_DEV uint32_t col_s(uint32_t stream) { return stream * 2 * K; }
-    static BSG_DEV uint32_t col_p(uint32_t stream, uint32_t j) {
-      return stream * 2 * K + K + (j & 1u) * (K / 2);
-    }
+    static BSG_DEV uint32_t col_p(uint32_t stream) { return stream * 2 * K + K; }
     BSG_DEV uint32_t tile(int i) const { return base_u + T::kOffRing + i * T::kTileB; }
     BSG_DEV volatile uint32_t* words() const {
       return reinterpret_cast<volatile uint32_t*>(base + T::kOffBar + 8 * T::kBars);
@@ -341,7 +340,10 @@ struct AttnPrefix {
   static BSG_DEV void mma_out(uint32_t o, uint32_t pr, uint32_t v_lo, bool add) {
 #pragma unroll
     for (int k = 0; k < K / 16; ++k)
-      tc_mma_ts(o, pr + k * 8, v_lo + k * 2048 / 16, kDescHi, kIdescO, add || k > 0);
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+        tc_mma_ts(o, pr + part * (K / 2) + k * 8, v_lo + k * 2048 / 16, kDescHi, kIdescO,
+                  add || k > 0 || part > 0);
   }
 
   // The whole warp runs this; one elected lane issues.  (Every wait is the warp's: a lane left
@@ -384,18 +386,18 @@ struct AttnPrefix {
       };
       if (jobs > 0 && !scores()) return false;
       for (uint32_t j = 0; j < jobs; ++j) {
-        const uint32_t n = job + j, b = Ctx::buf(stream, n);
+        const uint32_t n = job + j;
         if (j + 1 < jobs) {
           if (!wait_warp(c, c.taken(stream), n & 1u)) return false;
           tc_after();
           if (!scores()) return false;
         }
-        if (!wait_warp(c, c.probs(b), Ctx::phase(n))) return false;
+        if (!wait_warp(c, c.probs(stream), n & 1u)) return false;
         if (!wait_warp(c, c.full(vr.slot), vr.phase)) return false;
         tc_after();
         if (lead) {
-          mma_out(o, tmem + Ctx::col_p(stream, n), v_lo + vr.slot * (T::kTileB / 16), j > 0);
-          tc_commit(c.out(b));
+          mma_out(o, tmem + Ctx::col_p(stream), v_lo + vr.slot * (T::kTileB / 16), j > 0);
+          tc_commit(c.out(stream));
           tc_commit(c.empty(vr.slot));
         }
         vr.move(step, ring);
@@ -479,11 +481,13 @@ struct AttnPrefix {
     return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
   }
 
-  // Scores to rounded numerators 2^(scale s - base), packed into the first half of raw; their sum.
+  // Scores to numerators 2^(scale s - base), in two parts: rounded, packed into the first half of raw,
+  // and what the rounding left, into the second; their sum.
   template <bool PART>
   static BSG_DEV float numerators(uint32_t (&raw)[K], float scale, float base, int valid) {
     const uint64_t sc = f32x2(scale, scale), mb = f32x2(-base, -base);
     uint64_t sum[2] = {0ull, 0ull};
+    uint32_t hi[K / 2], lo[K / 2];
 #pragma unroll
     for (int i = 0; i < K / 2; ++i) {
       uint64_t e;
@@ -494,10 +498,14 @@ struct AttnPrefix {
         a = 2 * i < valid ? a : 0.f;
         b = 2 * i + 1 < valid ? b : 0.f;
       }
-      const uint32_t f = pack(a, b);
-      asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[i & 1])
-          : "l"(f32x2(half_to_f32<BF16>(f, 0), half_to_f32<BF16>(f, 1))));
-      raw[i] = f;
+      hi[i] = pack(a, b);
+      lo[i] = pack(a - half_to_f32<BF16>(hi[i], 0), b - half_to_f32<BF16>(hi[i], 1));
+      asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[i & 1]) : "l"(f32x2(a, b)));
+    }
+#pragma unroll
+    for (int i = 0; i < K / 2; ++i) {
+      raw[i] = hi[i];
+      raw[K / 2 + i] = lo[i];
     }
     return (f32x2_lo(sum[0]) + f32x2_hi(sum[0])) + (f32x2_lo(sum[1]) + f32x2_hi(sum[1]));
   }
@@ -514,7 +522,7 @@ struct AttnPrefix {
     const float scale = fabsf(p.a.scale_log2);  // (a negative scale's sign went into Q)
     float m = -INFINITY, l = 0.f;  // m: the maximum that O and l are scaled to
     for (uint32_t j = 0; j < jobs; ++j) {
-      const uint32_t b = Ctx::buf(stream, job + j), tile = tile_of(c, stream, j);
+      const uint32_t tile = tile_of(c, stream, j);
       const uint32_t before = job + j - 1;  // the job before, where there is one in the segment
       if (!wait_warp(c, c.scores(stream), (job + j) & 1u)) return false;
       tc_after();
@@ -537,7 +545,7 @@ struct AttnPrefix {
         m = next;
         if (j > 0) {
           // the accumulator's last product is done
-          if (!wait_warp(c, c.out(Ctx::buf(stream, before)), Ctx::phase(before))) return false;
+          if (!wait_warp(c, c.out(stream), before & 1u)) return false;
           tc_after();
 #pragma unroll 1
           for (int i = 0; i < D; i += 32) {
@@ -554,12 +562,12 @@ struct AttnPrefix {
       const float base = m == -INFINITY ? 0.f : m;
       l += valid < K ? numerators<true>(raw, scale, base, valid)
                      : numerators<false>(raw, scale, base, K);
-      // P's place is free when the products of two jobs before are done
-      if (j >= 2 && !wait_warp(c, c.out(b), Ctx::phase(job + j - 2))) return false;
-      const uint32_t tp = c.tmem + Ctx::col_p(stream, job + j) + lanes;
+      // P's place is free when the products of the job before are done
+      if (j >= 1 && !wait_warp(c, c.out(stream), before & 1u)) return false;
+      const uint32_t tp = c.tmem + Ctx::col_p(stream) + lanes;
       tc_after();
 #pragma unroll
-      for (int i = 0; i < K / 2; i += 32) tc_st32(tp + i, raw + i);
+      for (int i = 0; i < K; i += 32) tc_st32(tp + i, raw + i);
       tc_wait_st();
       if (valid < K) {
         // the page that the prefix ends in holds something else after it: zeros for V there
@@ -574,7 +582,7 @@ struct AttnPrefix {
         fence_async_shared();
       }
       tc_before();
-      mbar_arrive(c.probs(b));
+      mbar_arrive(c.probs(stream));
     }
     // the part: O, m and l
     float* part = p.parts + (static_cast<int64_t>(blockIdx.x) + g.unit) * attn_pre_slot_floats(D);
@@ -583,7 +591,7 @@ struct AttnPrefix {
     __stcg(part + T::kSlotRows * (D + 1) + row, l);
     if (jobs == 0) return true;  // (the merge leaves this part out)
     const uint32_t last = job + jobs - 1;
-    if (!wait_warp(c, c.out(Ctx::buf(stream, last)), Ctx::phase(last))) return false;
+    if (!wait_warp(c, c.out(stream), last & 1u)) return false;
     tc_after();
     // a thread holds a row; through shared memory, 16 columns at a time, into whole sectors.  The
     // queries' place is free: this stream's scores are all done, and where both streams share the
@@ -635,11 +643,9 @@ struct AttnPrefix {
       for (int b = 0; b < T::kStreams; ++b) {
         mbar_init(c.scores(b), 1);
         mbar_init(c.taken(b), 128);
-        mbar_init(c.ended(b), 1);
-      }
-      for (int b = 0; b < T::kBufs; ++b) {
         mbar_init(c.probs(b), 128);
         mbar_init(c.out(b), 1);
+        mbar_init(c.ended(b), 1);
       }
       mbar_init(c.query(), 128 * T::kStreams);
       c.words()[1] = 0u;

@@ -8,8 +8,9 @@
 // scores and P V on mma.sync m16n8k16, softmax in registers with the running maximum in base 2.
 // (Loaded by cp.async, 32 of them a lane and tile with two shuffles each for the rows' places, the
 // loads took as many instructions as the products.  Eight warps with tiles of 8 KB are no faster.)
-// Measured: 64 sequences with 530 own positions on average, 8 kv heads of 128: 139 MB in 31 us; in
-// its loop 6.5 TB/s, before it 3.4 us until the first tile has come.
+// P enters the second product in two parts of V's type (why: attn_prefix.cuh).
+// Measured: 64 sequences with 530 own positions on average, 8 kv heads of 128: 139 MB in 33 us, of
+// which 3.4 until the first tile has come (31 us with P in one part).
 //
 // All tiles of all (sequence, kv head, row tile) are laid in a line and cut into equal ranges, one
 // per warp, so that the lengths' spread does not matter; a unit counts kAttnCost tiles more than
@@ -343,12 +344,14 @@ struct AttnStream {
     for (int i = 0; i < 2; ++i) base[i] = a.m[i] == -INFINITY ? 0.f : a.m[i];
 #pragma unroll
     for (int k = 0; k < K / 16; ++k) {
-      uint32_t f[4];  // P of keys 16 k .. + 15, rounded
+      uint32_t f[4], r[4];  // P of keys 16 k .. + 15, rounded; what the rounding left
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int n = 2 * k + (x >> 1), i = x & 1;
-        f[x] = pack(ex2(s[n][2 * i] - base[i]), ex2(s[n][2 * i + 1] - base[i]));
-        a.l[i] += half_to_f32<BF16>(f[x], 0) + half_to_f32<BF16>(f[x], 1);
+        const float e0 = ex2(s[n][2 * i] - base[i]), e1 = ex2(s[n][2 * i + 1] - base[i]);
+        f[x] = pack(e0, e1);
+        r[x] = pack(e0 - half_to_f32<BF16>(f[x], 0), e1 - half_to_f32<BF16>(f[x], 1));
+        a.l[i] += e0 + e1;
       }
 #pragma unroll
       for (int n = 0; n < D / 8; n += 2) {
@@ -356,6 +359,8 @@ struct AttnStream {
         ldsm4_t(stage + T::kHalf + at(16 * k + (lane & 15), n + (lane >> 4)), vb);
         mma16816<BF16>(a.o[n], f, vb[0], vb[1]);
         mma16816<BF16>(a.o[n + 1], f, vb[2], vb[3]);
+        mma16816<BF16>(a.o[n], r, vb[0], vb[1]);
+        mma16816<BF16>(a.o[n + 1], r, vb[2], vb[3]);
       }
     }
   }

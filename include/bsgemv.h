@@ -423,8 +423,8 @@ int bsgemv_moe_destroy(bsgemv_moe_plan_t plan);
  * [B][Hq] fp32, log of the softmax's denominator with the maximum put back.  NaN among a row's
  * scores, or a score of +inf, gives NaN in its out and lse, NaN in a value its column (a weight of
  * 0 or not); a row all of whose scores are -inf gives NaN in out and -inf in lse.  Scores, softmax and
- * sums are fp32; the softmax numerators are rounded to the cache's dtype for the second product
- * and summed as rounded.
+ * sums are fp32; the softmax numerators enter the second product in two parts of the cache's dtype, to
+ * 2^-16 (bf16) or 2^-22 (fp16) of themselves.
  */
 typedef struct bsgemv_attn_plan_s* bsgemv_attn_plan_t;
 
