@@ -65,12 +65,15 @@ AttnLayout attn_layout(int Hq, int Hkv, int D, int max_B, int sms);
 // Measured, us, streaming / tensor, 8 kv heads: D = 128, P = 496, 128 rows 13.2 / 17.9; P = 1024,
 // 256 rows 25.1 / 25.9; P = 4096, 64 rows 18.3 / 20.5, 128 rows 28.4 / 21.6; P = 8192, 64 rows
 // 27.0 / 23.1; P = 32768, 16 rows 32.7 / 43.8, 32 rows 45.3 / 45.3; D = 64, P = 32768, 32 rows
-// 27.0 / 33.9, 64 rows 45.2 / 34.5.  At D = 256 its tiles have 16
-// positions and its warps are half as many: it wins up to 8 MB in all (8 kv heads, P = 256, 64 rows
-// 15.7 / 18.6, P = 512, 128 rows 22.3 / 20.9; 2 kv heads, P = 128, 128 rows 12.8 / 13.1).
+// 27.0 / 33.9, 64 rows 45.2 / 34.5.  At D = 256 its tiles have 16 positions and its warps are half as
+// many, and it wins up to 256 positions and 16 MB in all (2 kv heads: P = 256, 128 rows 13.7 / 13.3,
+// 512 rows 17.6 / 20.3, 1024 rows 28.6 / 27.5, P = 2048, 16 rows 18.2 / 13.9; 8 kv heads: P = 128, 256
+// rows 22.9 / 26.2, 512 rows 36.4 / 32.6, P = 256, 16 rows 13.4 / 13.1, 128 rows 17.6 / 20.2, 256 rows
+// 28.3 / 27.4, P = 512, 16 rows 14.2 / 13.3, 64 rows 16.8 / 19.2, 128 rows 22.3 / 20.9).
 inline bool attn_prefix_streams(int rows, int Hkv, int D, int prefix_len) {
   const int64_t once = int64_t{4} * Hkv * D * prefix_len, tiles = (rows + kAttnRows - 1) / kAttnRows;
-  return D == 256 ? tiles * once <= (int64_t{8} << 20) : (tiles - 1) * once <= (int64_t{80} << 20);
+  if (D == 256) return prefix_len <= 256 && tiles * once <= (int64_t{16} << 20);
+  return (tiles - 1) * once <= (int64_t{80} << 20);
 }
 
 // Tensor maps of the cache: [page][head][row][D], boxes of 64 d and as many rows as a page and a
