@@ -15,17 +15,8 @@ from block_scaled_bit_gb300 import bsgemv
 from test_attn_nonfinite import PLANS, problem
 
 
-@pytest.mark.gpu
-@pytest.mark.parametrize("plan", PLANS)
-@pytest.mark.parametrize("qscale", [0.3, 1.5, 6.0])
-def test_numerators_are_not_rounded_to_16_bits(plan, qscale):
-    import torch
-    pr = problem(torch, *plan, seed=11)
-    pr.q.mul_(qscale / 1.5)
-    with bsgemv.AttnPlan(*pr.plan) as p:
-        out, lse = pr.run(p)
-        assert p.device_status() == bsgemv.OK
-    f16, D, scale = pr.act == "f16", pr.D, pr.D ** -0.5
+def check(torch, pr, out, lse, scale):
+    f16, D = pr.act == "f16", pr.D
     B, Hq, _ = pr.q.shape
     for b in range(B):
         page, row = (torch.tensor(x, device="cuda") for x in zip(*pr.places(b)))
@@ -34,7 +25,7 @@ def test_numerators_are_not_rounded_to_16_bits(plan, qscale):
         v = pr.v[page, :, row].double().repeat_interleave(Hq // pr.Hkv, 1)
         q = pr.q[b].double()
         s = torch.einsum("hd,nhd->hn", q, k) * scale
-        mag = torch.einsum("hd,nhd->hn", q.abs(), k.abs()) * scale
+        mag = torch.einsum("hd,nhd->hn", q.abs(), k.abs()) * abs(scale)
         e_s = ((D / 16 + 8) * 2.0 ** -23 * mag + 2.0 ** -21 * s.abs()).amax(1) + 2.0 ** -20
         e = torch.exp(s - s.amax(1, keepdim=True))
         total = e.sum(1)
@@ -49,3 +40,29 @@ def test_numerators_are_not_rounded_to_16_bits(plan, qscale):
         assert off.max().item() <= 1, f"lse of sequence {b}: {off.max().item():.3g}"
         low, high = (want - tol).to(out.dtype), (want + tol).to(out.dtype)
         assert ((low <= out[b]) & (out[b] <= high)).all(), f"out of sequence {b}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("plan", PLANS)
+@pytest.mark.parametrize("qscale", [0.3, 1.5, 6.0])
+def test_numerators_are_not_rounded_to_16_bits(plan, qscale):
+    import torch
+    pr = problem(torch, *plan, seed=11)
+    pr.q.mul_(qscale / 1.5)
+    with bsgemv.AttnPlan(*pr.plan) as p:
+        out, lse = pr.run(p)
+        assert p.device_status() == bsgemv.OK
+    check(torch, pr, out, lse, pr.D ** -0.5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("plan", PLANS)
+@pytest.mark.parametrize("scale", [-0.07, 0.0, 1e-4, 0.9])
+def test_scales_of_every_kind(plan, scale):
+    """In each kernel: negative, none (the mean of the values), small, and scores in the tens."""
+    import torch
+    pr = problem(torch, *plan, seed=12)
+    with bsgemv.AttnPlan(*pr.plan) as p:
+        out, lse = pr.run(p, scale=scale)
+        assert p.device_status() == bsgemv.OK
+    check(torch, pr, out, lse, scale)
