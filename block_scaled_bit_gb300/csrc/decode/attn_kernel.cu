@@ -8,9 +8,9 @@ namespace {
 // Bound by latency: lengths, then m and l, then rows, each a trip to L2 (64 sequences of 32 heads
 // of 128, 13 parts a row: 14.6 us alone under a profiler with a cold L2).  What does not depend on
 // the parts is worked out while the kernel before still runs; the sequences' stretches too, up to
-// one a thread and 1024 blocks: each block works them all out, beside the streaming kernel (us
-// with / without: 32 blocks 7.7 / 8.4, 768 blocks 38.2 / 40.2, 2048 blocks 73.5 / 72.2); beyond
-// that they are read from the streaming kernel's.
+// one a thread and 1024 blocks: each block works them all out, beside the streaming kernel (a call
+// of 32 blocks is 0.7 us shorter for it, one of 768 blocks 2 us, one of 2048 blocks 1.3 us longer);
+// beyond that they are read from the streaming kernel's.
 // One block per (sequence, query head), D / 32 elements a lane.  A row has tens of parts, so
 // nothing is read one after the other: every warp takes a quarter of the parts, each of its lanes
 // fetches one part's m and l, the warp agrees on the weights, then the rows are fetched four at a

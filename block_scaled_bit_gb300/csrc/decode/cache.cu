@@ -6,10 +6,10 @@
 // depend on the order in which blocks or atomics run (integer additions commute, and every choice
 // of a page is made by one block in index order).
 //
-// Bound: pages moved at the copy bandwidth (512 of 2048 pages of 64 KB moved in 16 planes: 131 us
+// Bound: pages moved at the copy bandwidth (512 of 2048 pages of 64 KB moved in 16 planes: 135 us
 // for 0.54 GB read and as much written, more than DRAM alone gives as some stays in L2); below
-// some MB a chain of two kernels that depend on one another (8.6 us for a fork of 4 that copies
-// 4 pages in 8 planes; the launches overlap, so that one costs 3 us, not 5).  The integers are
+// some MB a chain of two kernels that depend on one another (8.6 us in a graph for a fork of 4 that
+// copies 4 pages in 8 planes; the launches overlap, so that one costs 3 us, not 5).  The integers are
 // worked out by one block of 1024 threads: more blocks would have to agree on the lowest page.
 #include <new>
 

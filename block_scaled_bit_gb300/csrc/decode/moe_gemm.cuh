@@ -9,9 +9,9 @@
 // a few tokens per expert make the arithmetic small.  So the kernel is a weight stream: two copy
 // warps (weights and activations, scales and zero points) keep a ring of 16 KB weight boxes in
 // flight, four warps decode and multiply, two blocks an SM.  What bounds it in fact: FP8 the stream (both products with routing: 32 tokens, 64 experts,
-// top 6, H 4096, I 1408, 1.09 GB in 216 us, 5.1 TB/s, 0.75 of the measured copy); NVFP4 and
+// top 6, H 4096, I 1408, 1.09 GB in 217 us, 5.0 TB/s, 0.74 of the measured copy); NVFP4 and
 // int8 the decoding, 1600 to 2000 cycles a stage and warp where the copy needs 700 (8 tokens,
-// 137 MB in 57 us; 13 tokens with zero points, 282 MB in 105 us; a second copy warp took 5 us off
+// 137 MB in 56 us; 13 tokens with zero points, 282 MB in 104 us; a second copy warp took 5 us off
 // that); one token its chain of start, first load, cold code and sums (14 MB in 24 us).
 //
 // Work.  A tile is 128 weight rows of one expert -- for UP 64 gate rows and the 64 up rows that
