@@ -8,6 +8,7 @@ plain addresses.  Importing this module loads the library and raises if it has n
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 from . import _build
@@ -17,6 +18,7 @@ ACT_BF16 = 0x100
 VARIANTS = {"auto": 0, "mma": 1, "cuda_core": 2}
 SPLITS = {"auto": 0, "stream_k": 1, "cluster": 2}
 MOE_RENORMALIZE, MOE_LOGITS_F32 = 1, 2
+ROPE_INTERLEAVED = 1
 
 OK = 0
 ERR_INVALID_ARG = -1
@@ -43,7 +45,10 @@ EXPORTS = ("bsgemv_plan", "bsgemv_run", "bsgemv_run_bias", "bsgemv_run_host",
            "bsgemv_attn_set_test_fault", "bsgemv_attn_destroy",
            "bsgemv_cache_plan", "bsgemv_cache_copy", "bsgemv_cache_fork", "bsgemv_cache_free",
            "bsgemv_cache_extend", "bsgemv_cache_write", "bsgemv_cache_compact",
-           "bsgemv_cache_destroy",
+           "bsgemv_cache_grow", "bsgemv_cache_append", "bsgemv_cache_destroy",
+           "bsgemv_rope_plan", "bsgemv_rope_destroy",
+           "bsgemv_chunk_plan", "bsgemv_chunk_run", "bsgemv_chunk_device_status",
+           "bsgemv_chunk_destroy",
            "bsgemv_version")
 
 
@@ -125,7 +130,18 @@ def lib() -> ctypes.CDLL:
         L.bsgemv_cache_extend.argtypes = [vp] * 7 + [ci, vp]
         L.bsgemv_cache_write.argtypes = [vp] * 7 + [i64, ci, ci, i64, i64, ci, ci, ci, vp]
         L.bsgemv_cache_compact.argtypes = [vp] * 9
+        L.bsgemv_cache_grow.argtypes = [vp] * 8 + [ci, vp]
+        L.bsgemv_cache_append.argtypes = [vp] * 7 + [ci, ci] + [vp, i64] * 3 + \
+            [vp, vp, f32, vp, vp, i64, i64, i64, ci, ci, vp]
         L.bsgemv_cache_destroy.argtypes = [vp]
+        L.bsgemv_rope_plan.argtypes = [ctypes.POINTER(vp)] + [ci] * 6 + \
+            [ctypes.POINTER(ctypes.c_double), ctypes.c_double]
+        L.bsgemv_rope_destroy.argtypes = [vp]
+        L.bsgemv_chunk_plan.argtypes = [ctypes.POINTER(vp)] + [ci] * 7
+        L.bsgemv_chunk_run.argtypes = [vp, vp, i64, vp, vp, i64, i64, i64, ci, vp, i64, ci, ci, vp,
+                                       vp, vp, ci, ci, f32, f32, ci, vp, vp, vp, vp]
+        L.bsgemv_chunk_device_status.argtypes = [vp, vp]
+        L.bsgemv_chunk_destroy.argtypes = [vp]
         for name in EXPORTS:
             if name != "bsgemv_status_string":
                 getattr(L, name).restype = ci
@@ -523,6 +539,115 @@ class AttnPlan(_Handle):
         return lib().bsgemv_attn_set_test_fault(self._h, int(kernel), int(skip_tile), int(wait_ns))
 
 
+class ChunkPlan(_Handle):
+    """Attention of up to max_T new tokens, in up to max_n ragged entries, over a paged cache
+    (bsgemv_chunk_plan): chunks of prompts, draft tokens to verify, single tokens.  Tensors of other
+    shapes, types or orders than run() says are refused (BSGEMV_ERR_INVALID_ARG)."""
+
+    _destroy = "bsgemv_chunk_destroy"
+
+    def __init__(self, act: str, Hq: int, Hkv: int, D: int, page_size: int, max_n: int,
+                 max_T: int):
+        self.act, self.Hq, self.Hkv, self.D = act, Hq, Hkv, D
+        self.page_size, self.max_n, self.max_T = page_size, max_n, max_T
+        h = ctypes.c_void_p()
+        _check(lib().bsgemv_chunk_plan(ctypes.byref(h), int(act == "bf16"), Hq, Hkv, D, page_size,
+                                       max_n, max_T), "bsgemv_chunk_plan")
+        self._h = h
+        self._act, self._i32, self._f32 = _types(act)
+        self._scale = D ** -0.5
+
+    def run(self, q, k, v, tables, lens, seqs, starts, out, lse=None, scale: float | None = None,
+            cap: float = 0.0, window: int = 0, slopes=None, stream=None) -> None:
+        """out [T, Hq, D] from q [T, Hq, D] (any stride between rows): rows starts[i] ..
+        starts[i + 1] - 1 are the last tokens of sequence seqs[i].  k and v are views [pages, Hkv,
+        page_size, D] of the cache in either layout; tables [sequences, columns] (any stride between
+        rows), lens [sequences or more], seqs [n], starts [n + 1] are int32, slopes [Hq] and lse
+        [T, Hq] fp32; scale defaults to D ** -0.5, cap and window to none (0)."""
+        T, Hq, D = q.shape
+        pages, heads, rows, width = shape = k.shape
+        ks, (qs, qh, q1), (ts, t1), act = k.stride(), q.stride(), tables.stride(), self._act
+        num_seqs, cols = tables.shape
+        n = seqs.shape[0]
+        if ks != v.stride() or shape != v.shape or D != self.D or width != D or ks[3] != 1 or \
+                q1 != 1 or t1 != 1 and cols > 1 or Hq != self.Hq or qh != D and Hq > 1 or \
+                heads != self.Hkv or rows != self.page_size or q.dtype not in act or \
+                k.dtype not in act or v.dtype not in act or tables.dtype not in self._i32:
+            raise BsgemvError(ERR_INVALID_ARG, "bsgemv_chunk_run")
+        status = lib().bsgemv_chunk_run(
+            self._h, q.data_ptr(), qs if T > 1 else Hq * D, k.data_ptr(), v.data_ptr(), ks[0], ks[1],
+            ks[2], pages, tables.data_ptr(), ts if num_seqs > 1 else cols, num_seqs, cols,
+            _arg("lens", lens, 4 * num_seqs, self._i32), _arg("seqs", seqs, 4 * n, self._i32),
+            _arg("starts", starts, 4 * n + 4, self._i32), n, T,
+            self._scale if scale is None else scale, cap, window,
+            _arg("slopes", slopes, 4 * Hq, self._f32), _arg("out", out, 2 * T * Hq * D, act),
+            _arg("lse", lse, 4 * T * Hq, self._f32), _stream(stream))
+        if status != OK:
+            raise BsgemvError(status, "bsgemv_chunk_run")
+
+    def run_status(self, *args, **kw) -> int:
+        """As run, with the status returned."""
+        try:
+            self.run(*args, **kw)
+        except BsgemvError as e:
+            return e.status
+        return OK
+
+    def device_status(self, stream=None) -> int:
+        return lib().bsgemv_chunk_device_status(self._h, _stream(stream))
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, linear: float = 1.0, ntk: float = 1.0,
+                     parts: tuple | None = None) -> list:
+    """Radians a position of the rot / 2 pairs: base ** (-2 p / rot), stretched for contexts longer
+    than the trained one by
+      linear   all of them divided by it
+      ntk      the base grown so that the slowest pair is divided by it and the fastest stays
+      parts    (factor, trained length, low, high): a pair with t turns over the trained length is
+               divided by factor where t <= low, stays where t >= high, and between them is mixed in
+               proportion"""
+    if ntk != 1.0:
+        base = base * ntk ** (rot / (rot - 2))
+    freqs = [base ** (-2.0 * p / rot) / linear for p in range(rot // 2)]
+    if parts is not None:
+        factor, trained, low, high = parts
+        for p, f in enumerate(freqs):
+            t = trained * f / (2 * math.pi)
+            keep = min(1.0, max(0.0, (t - low) / (high - low)))
+            freqs[p] = f * keep + f / factor * (1 - keep)
+    return freqs
+
+
+class RopePlan(_Handle):
+    """What is done to new tokens' queries and keys before they are used (bsgemv_rope_plan): the
+    rotation of the first `rot` (default: all) of a head's D elements by position, in halves or
+    (interleaved) in pairs, and the norms that PageCache.append is given weights for.  Frequencies:
+    freqs (rot / 2 radians a position), or those of rope_frequencies; factor multiplies the rotated
+    elements."""
+
+    _destroy = "bsgemv_rope_destroy"
+
+    def __init__(self, act: str, Hq: int, Hkv: int, D: int, rot: int | None = None,
+                 base: float = 10000.0, interleaved: bool = False, freqs=None,
+                 linear: float = 1.0, ntk: float = 1.0, parts: tuple | None = None,
+                 factor: float = 1.0):
+        rot = D if rot is None else rot
+        if freqs is None:
+            freqs = rope_frequencies(rot, base, linear, ntk, parts) if rot > 0 else []
+        freqs = [float(f) for f in freqs]
+        if len(freqs) != max(rot, 0) // 2:
+            raise BsgemvError(ERR_INVALID_ARG, "bsgemv_rope_plan")
+        self.act, self.Hq, self.Hkv, self.D, self.rot = act, Hq, Hkv, D, rot
+        self.interleaved, self.freqs = bool(interleaved), freqs
+        h = ctypes.c_void_p()
+        _check(lib().bsgemv_rope_plan(
+            ctypes.byref(h), int(act == "bf16"), Hq, Hkv, D, rot,
+            ROPE_INTERLEAVED if interleaved else 0,
+            (ctypes.c_double * len(freqs))(*freqs) if freqs else None, factor), "bsgemv_rope_plan")
+        self._h = h
+        self._act, self._i32, _ = _types(act)
+
+
 class PageCache(_Handle):
     """The pages of a cache (bsgemv_cache_plan): pool [planes, num_pages, page_bytes], refs
     [num_pages], tables [max_seqs, max_pages] and lens [max_seqs] (int32) are the caller's, as the
@@ -577,6 +702,44 @@ class PageCache(_Handle):
             _arg("tables", tables, self._tables, i32), _arg("lens", lens, self._lens, i32),
             _arg("seqs", seqs, 4 * n, i32), _arg("grown", grown, 4 * n, i32), n,
             _stream(stream)), "bsgemv_cache_extend")
+
+    def grow(self, pool, refs, tables, lens, seqs, starts, grown=None, stream=None) -> None:
+        """Room for starts[i + 1] - starts[i] more tokens in each of the sequences."""
+        n, i32 = seqs.shape[0], self._i32
+        _check(lib().bsgemv_cache_grow(
+            self._h, _arg("pool", pool, self._pool), _arg("refs", refs, self._refs, i32),
+            _arg("tables", tables, self._tables, i32), _arg("lens", lens, self._lens, i32),
+            _arg("seqs", seqs, 4 * n, i32), _arg("starts", starts, 4 * n + 4, i32),
+            _arg("grown", grown, 4 * n, i32), n, _stream(stream)), "bsgemv_cache_grow")
+
+    def append(self, rope, pool, tables, lens, seqs, starts, q, k, v, q_out, head_stride: int = 0,
+               row_stride: int = 0, k_plane: int = 0, v_plane: int = 0, q_weight=None,
+               k_weight=None, eps: float = 1e-6, pos=None, stream=None) -> None:
+        """q [T, Hq, D], normalised (q_weight [D]) and rotated, to q_out [T, Hq, D]; k [T, Hkv, D]
+        likewise (k_weight), and v as it is, to the places of the new tokens: rows starts[i] ..
+        starts[i + 1] - 1 are the last tokens of sequence seqs[i].  q, k, v and q_out: any stride
+        between rows; q and q_out, or k and v, may be None.  pos [T]: other positions to rotate by."""
+        n, i32, act = seqs.shape[0], self._i32, rope._act
+        T = (k if q is None else q).shape[0]
+        args = []
+        for t, heads in ((q, rope.Hq), (k, rope.Hkv), (v, rope.Hkv), (q_out, rope.Hq)):
+            if t is None:
+                args += [None, 0]
+                continue
+            (rows, h, D), (st, sh, s1) = t.shape, t.stride()
+            if rows != T or h != heads or D != rope.D or s1 != 1 or sh != D and h > 1 or \
+                    t.dtype not in act:
+                raise BsgemvError(ERR_INVALID_ARG, "bsgemv_cache_append")
+            args += [t.data_ptr(), st if T > 1 else h * D]  # (one row's stride is of no account)
+        status = lib().bsgemv_cache_append(
+            self._h, rope._h, _arg("pool", pool, self._pool),
+            _arg("tables", tables, self._tables, i32), _arg("lens", lens, self._lens, i32),
+            _arg("seqs", seqs, 4 * n, i32), _arg("starts", starts, 4 * n + 4, i32), n, T, *args[:6],
+            _arg("q_weight", q_weight, 2 * rope.D, act), _arg("k_weight", k_weight, 2 * rope.D, act),
+            eps, _arg("pos", pos, 4 * T, i32), *args[6:], head_stride, row_stride, k_plane, v_plane,
+            _stream(stream))
+        if status != OK:
+            raise BsgemvError(status, "bsgemv_cache_append")
 
     def write(self, pool, tables, lens, seqs, k, v, head_stride: int, row_stride: int,
               k_plane: int, v_plane: int, stream=None) -> None:

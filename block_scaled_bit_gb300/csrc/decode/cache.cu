@@ -1,4 +1,4 @@
-// cache.cu -- the pages of a cache: copy, fork, free, extend, write, compact.
+// cache.cu -- the pages of a cache: copy, fork, free, extend, grow, write, compact.
 //
 // What these calls move is pages (2 x planes x page_bytes for each page that changes place) and
 // the integers that name them.  The state is the caller's refs / tables / lens: a free page is
@@ -14,14 +14,8 @@
 #include <new>
 
 #include "../bsgemv_kernel.cuh"
+#include "cache_internal.h"
 #include "decode_internal.h"
-
-struct bsgemv_cache_s {
-  int device = -1, sms = 0;
-  int planes = 0, num_pages = 0, page_size = 0, max_seqs = 0, max_pages = 0;
-  int64_t page_bytes = 0;
-  void* ws = nullptr;
-};
 
 namespace bsg {
 namespace {
@@ -345,6 +339,125 @@ __global__ void __launch_bounds__(kCopyThreads) extend_copy(CacheParams p) {
   copy_pages(p, *p.copies);
 }
 
+// Grow, first kernel (one block): each entry's wish (pages, and whether the last page is to be
+// copied), the free pages in index order, and the copies of the entries that are served.  len[e]: the
+// sequence's length, -1 = stays as it is; got[e]: pages that the entries before it want; last[e]: the
+// page to copy.  An entry is served if its last wish is among the free pages: since wishes add up in
+// order, those served are the entries before the first that is not, and entries that want none.
+BSG_DEV int pages_of(int64_t tokens, const CacheParams& p) {
+  return static_cast<int>((tokens + p.page_size - 1) / p.page_size);
+}
+BSG_DEV int count_of(const CacheParams& p, int e) {
+  const int64_t c = static_cast<int64_t>(p.b[e + 1]) - p.b[e];
+  return c < 0 ? 0 : (c > INT32_MAX ? INT32_MAX : static_cast<int>(c));
+}
+
+__global__ void __launch_bounds__(kScan) grow_wishes(CacheParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t most = static_cast<int64_t>(p.max_pages) * p.page_size;
+  int want = 0;
+  for (int base = 0; base < p.n; base += kScan) {
+    const int e = base + threadIdx.x;
+    int need = 0, state = -1, from = -1;
+    if (e < p.n) {
+      const int s = p.a[e], count = count_of(p, e);
+      if (s >= 0 && s < p.max_seqs) {
+        const int len = p.lens[s];
+        if (len >= 0 && static_cast<int64_t>(len) + count <= most) {
+          state = len;
+          if (count > 0) {
+            need = pages_of(static_cast<int64_t>(len) + count, p) - pages_of(len, p);
+            if (len % p.page_size) {
+              const int page = p.tables[static_cast<int64_t>(s) * p.max_pages + len / p.page_size];
+              if (!is_page(page, p)) {
+                ++need;
+                from = -2;  // a page in its place, nothing to copy
+              } else if (p.refs[page] > 1) {
+                ++need;
+                from = page;
+              }
+            }
+          }
+        }
+      }
+    }
+    int sum;
+    const int before = want + block_scan(need, &sum);
+    if (e < p.n) {
+      p.len[e] = state;
+      p.last[e] = from;
+      p.got[e] = before;
+    }
+    want += sum;
+  }
+  // the free pages, as many as are wanted (a thread's four are side by side)
+  int given = 0;
+  for (int base = 0; base < p.num_pages && given < want; base += 4 * kScan) {
+    const int page = base + 4 * threadIdx.x;
+    bool free[4];
+    int mine = 0, sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      free[i] = page + i < p.num_pages && p.refs[page + i] == 0;
+      mine += free[i];
+    }
+    int r = given + block_scan(mine, &sum);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (free[i]) p.map[r++] = page + i;
+    given += sum;
+  }
+  __syncthreads();
+  int copies = 0;
+  for (int base = 0; base < p.n; base += kScan) {
+    const int e = base + threadIdx.x;
+    int copy = 0, from = -1, first = 0;
+    if (e < p.n) {
+      from = p.last[e];
+      first = p.got[e];
+      const int end = e + 1 < p.n ? p.got[e + 1] : want;
+      if (end > first && end > given) p.len[e] = -1;
+      else copy = from >= 0;
+    }
+    int sum;
+    const int r = copies + block_scan(copy, &sum);
+    if (copy) {
+      p.src[r] = from;
+      p.dst[r] = p.map[first];
+      atomicSub(p.refs + from, 1);
+    }
+    copies += sum;
+  }
+  if (threadIdx.x == 0) {
+    *p.copies = copies;
+    p.copies[1] = want;
+  }
+}
+
+// Grow, second kernel: the entries' rows, references and lengths, and the copied pages.
+__global__ void __launch_bounds__(kCopyThreads) grow_rows(CacheParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  for (int e = blockIdx.x; e < p.n; e += gridDim.x) {
+    const int len = p.len[e];
+    if (len >= 0) {
+      const int s = p.a[e], first = p.got[e], end = e + 1 < p.n ? p.got[e + 1] : p.copies[1];
+      // its pages: in the place of the last one (to be copied, or not a page), then after it
+      const int at = pages_of(len, p) - (p.last[e] != -1);
+      int32_t* row = p.tables + static_cast<int64_t>(s) * p.max_pages + at;
+      for (int j = first + threadIdx.x; j < end; j += blockDim.x) {
+        const int page = p.map[j];
+        row[j - first] = page;
+        p.refs[page] = 1;
+      }
+      if (threadIdx.x == 0) p.lens[s] = len + count_of(p, e);
+    }
+    if (threadIdx.x == 0 && p.note) p.note[e] = len >= 0;
+  }
+  copy_pages(p, *p.copies);
+}
+
 struct WriteParams {
   const uint16_t *k, *v;
   int64_t kv_stride, head_stride, row_stride;
@@ -603,6 +716,31 @@ int bsgemv_cache_extend(bsgemv_cache_t c, void* pool, int32_t* refs, int32_t* ta
   return decode_launch(extend_copy, dim3(copy_grid(c, n, 0)), dim3(kCopyThreads), 0, s, p);
 }
 
+int bsgemv_cache_grow(bsgemv_cache_t c, void* pool, int32_t* refs, int32_t* tables, int32_t* lens,
+                      const int32_t* seqs, const int32_t* starts, int32_t* grown, int n,
+                      void* stream) {
+  if (c == nullptr || n < 0 || n > c->max_seqs) return BSGEMV_ERR_INVALID_ARG;
+  if (n == 0) return BSGEMV_OK;
+  if (!pool || !refs || !tables || !lens || !seqs || !starts) return BSGEMV_ERR_INVALID_ARG;
+  if (!aligned_to(pool, 16) || !aligned_to(refs, 4) || !aligned_to(tables, 4) ||
+      !aligned_to(lens, 4) || !aligned_to(seqs, 4) || !aligned_to(starts, 4) ||
+      !aligned_to(grown, 4))
+    return BSGEMV_ERR_MISALIGNED;
+  int rc = decode_check_device(c->device);
+  if (rc != BSGEMV_OK) return rc;
+  CacheParams p = params_of(c, pool, n);
+  p.refs = refs;
+  p.tables = tables;
+  p.lens = lens;
+  p.a = seqs;
+  p.b = starts;
+  p.note = grown;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  rc = decode_launch(grow_wishes, dim3(1), dim3(kScan), 0, s, p);
+  if (rc != BSGEMV_OK) return rc;
+  return decode_launch(grow_rows, dim3(copy_grid(c, n, n)), dim3(kCopyThreads), 0, s, p);
+}
+
 int bsgemv_cache_write(bsgemv_cache_t c, void* pool, const int32_t* tables, const int32_t* lens,
                        const int32_t* seqs, const void* k, const void* v, int64_t kv_stride,
                        int heads, int D, int64_t head_stride, int64_t row_stride, int k_plane,
@@ -617,12 +755,7 @@ int bsgemv_cache_write(bsgemv_cache_t c, void* pool, const int32_t* tables, cons
       !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(tables, 4) || !aligned_to(lens, 4) ||
       !aligned_to(seqs, 4))
     return BSGEMV_ERR_MISALIGNED;
-  // The last element of a page lies in it: its elements after the last head's first, then after the
-  // last row's first (by division: the products can pass 64 bits).
-  int64_t left = c->page_bytes / 2 - D;
-  if (left < 0 || (heads > 1 && head_stride > left / (heads - 1))) return BSGEMV_ERR_INVALID_ARG;
-  left -= (heads - 1) * head_stride;
-  if (c->page_size > 1 && row_stride > left / (c->page_size - 1)) return BSGEMV_ERR_INVALID_ARG;
+  if (!page_holds(c, heads, D, head_stride, row_stride)) return BSGEMV_ERR_INVALID_ARG;
   int rc = decode_check_device(c->device);
   if (rc != BSGEMV_OK) return rc;
   CacheParams p = params_of(c, pool, n);

@@ -463,6 +463,54 @@ int bsgemv_attn_set_test_fault(bsgemv_attn_plan_t plan, int kernel, int skip_til
 int bsgemv_attn_destroy(bsgemv_attn_plan_t plan);
 
 /*
+ * Attention of new tokens over the paged cache: a chunk of a prompt, draft tokens to verify, single
+ * tokens, in one ragged batch.  Rows starts[i] .. starts[i + 1] - 1 of q (starts: int32 [n + 1],
+ * device, not decreasing) are the last tokens of sequence seqs[i], i < n, whose keys and values are
+ * in the cache already: row r has position i_r = lens[seqs[i]] - (starts[i + 1] - r) and sees the
+ * positions j of its sequence up to its own, the last `window` of them where window > 0:
+ *
+ *     t(r, h, j)  = scale * q[r, h] . k_j                  (kv head h / (Hq / Hkv))
+ *     t           = cap * tanh(t / cap)                    where cap > 0
+ *     t           = t + slopes[h] * (j - i_r)              where slopes is not NULL
+ *     out[r, h]   = sum over j of softmax_j(t) v_j,        lse[r, h] = log of sum exp(t)
+ *
+ * Position j of sequence s lies in row j % page_size of page tables[s * table_stride + j /
+ * page_size]; entries of tables past a sequence's last page are not read.  Rows of an entry whose
+ * seqs is outside 0 .. num_seqs-1, and rows before a sequence's first position, get 0 in out and
+ * -inf in lse; rows outside starts[0] .. starts[n] - 1 are left as they were.  A sequence counts with
+ * max_pages * page_size tokens at most.  What the cache holds in places that a row does not see does
+ * not reach it, NaN and infinities included.
+ *
+ * q: head h of row r at q + r * q_stride + h * D elements, out [T][Hq][D] and lse [T][Hq] (fp32, or
+ * NULL) contiguous, dtypes, cache layout and strides as bsgemv_attn_run.  NaN and infinities among
+ * what a row sees act as there.
+ */
+typedef struct bsgemv_chunk_plan_s* bsgemv_chunk_plan_t;
+
+/* act_bf16, Hq, Hkv, D and page_size as bsgemv_attn_plan.  1 <= max_n <= 65536 entries and
+ * 1 <= max_T < 2^24 rows a call, max_T * Hq below 2^28. */
+int bsgemv_chunk_plan(bsgemv_chunk_plan_t* out, int act_bf16, int Hq, int Hkv, int D,
+                      int page_size, int max_n, int max_T);
+
+/* Enqueue the attention of T (1 .. max_T) rows in n (1 .. max_n) entries.  cap: 0 for none, or > 0;
+ * window: 0 for none, or >= 1; slopes: Hq fp32 (device) or NULL.  Alignment and strides as
+ * bsgemv_attn_run; table_stride >= max_pages.  Page ids outside 0 .. num_pages-1 are read as zeros.
+ * Deterministic: repeated calls are bit-identical. */
+int bsgemv_chunk_run(bsgemv_chunk_plan_t plan, const void* q, int64_t q_stride, const void* k,
+                     const void* v, int64_t page_stride, int64_t head_stride, int64_t row_stride,
+                     int num_pages, const int32_t* tables, int64_t table_stride, int num_seqs,
+                     int max_pages, const int32_t* lens, const int32_t* seqs,
+                     const int32_t* starts, int n, int T, float scale, float cap, int window,
+                     const float* slopes, void* out, float* lse, void* stream);
+
+/* Synchronise `stream`, then read and clear the plan's error word (as bsgemv_device_status).
+ * BSGEMV_ERR_UNSUPPORTED: a call's key tiles were more than it can count; its out rows are NaN. */
+int bsgemv_chunk_device_status(bsgemv_chunk_plan_t plan, void* stream);
+
+/* Free the plan (synchronises the device first).  NULL is a no-op. */
+int bsgemv_chunk_destroy(bsgemv_chunk_plan_t plan);
+
+/*
  * The pages of a cache.  The caller owns
  *
  *     pool    [planes][num_pages][page_bytes]   K and V of every layer, a plane each
@@ -525,6 +573,73 @@ int bsgemv_cache_write(bsgemv_cache_t cache, void* pool, const int32_t* tables,
                        const int32_t* lens, const int32_t* seqs, const void* k, const void* v,
                        int64_t kv_stride, int heads, int D, int64_t head_stride,
                        int64_t row_stride, int k_plane, int v_plane, int n, void* stream);
+
+/*
+ * counts[i] = starts[i + 1] - starts[i] more tokens for each of the sequences seqs[0 .. n-1]
+ * (distinct), as bsgemv_cache_extend gives one: pages for all of them, and a copy of the last page
+ * where it is partly filled and other sequences hold it too.  starts: int32 [n + 1] (device).
+ * Entries are served in order, all of an entry's pages or none: one that finds too few pages left
+ * stays as it is, and so does every entry after it that needs a page.  One with no room in its row
+ * stays as it is and takes nothing; a count below 1 adds nothing.  grown [n], if not NULL, is 1
+ * where the sequence has its tokens now, or 0.
+ */
+int bsgemv_cache_grow(bsgemv_cache_t cache, void* pool, int32_t* refs, int32_t* tables,
+                      int32_t* lens, const int32_t* seqs, const int32_t* starts, int32_t* grown,
+                      int n, void* stream);
+
+/*
+ * What is done to the queries and keys of new tokens before they are used: a norm over each head
+ * (optional, with weights at the call) and the rotation of `rot` of its D elements by the token's
+ * position,
+ *
+ *     y = x / sqrt(mean(x^2) + eps) * weight                 over the head's D elements
+ *     (a, b) -> factor * (a cos f - b sin f, a sin f + b cos f),     f = position * freqs[p]
+ *
+ * for pair p < rot / 2: elements (p, p + rot / 2), or (2 p, 2 p + 1) with BSGEMV_ROPE_INTERLEAVED.
+ * Elements from rot on are normalised only.  Angles are worked out modulo a turn in 64-bit fixed
+ * point (2^-64 of a turn a position, freqs to the last bit of a double), so far positions lose
+ * nothing; norms and products are fp32, one rounding at the end.
+ */
+typedef struct bsgemv_rope_s* bsgemv_rope_t;
+
+enum bsgemv_rope_flags { BSGEMV_ROPE_INTERLEAVED = 1 };
+
+/* act_bf16: 0 = fp16, 1 = bf16.  D a multiple of 16 up to 512; rot a multiple of 16, 0 <= rot <= D;
+ * Hq, Hkv 1 .. 1024.  freqs: rot / 2 doubles in HOST memory, radians a position (finite, below 2^31;
+ * NULL with rot == 0); factor: finite. */
+int bsgemv_rope_plan(bsgemv_rope_t* out, int act_bf16, int Hq, int Hkv, int D, int rot, int flags,
+                     const double* freqs, double factor);
+
+/* Free the plan (synchronises the device first).  NULL is a no-op. */
+int bsgemv_rope_destroy(bsgemv_rope_t rope);
+
+/*
+ * New tokens of one layer on their way into the cache: rows starts[i] .. starts[i + 1] - 1 of q, k
+ * and v (starts: int32 [n + 1], device, not decreasing) are the last tokens of sequence seqs[i],
+ * i < n: row r has position lens[seqs[i]] - (starts[i + 1] - r).  Queries, normalised and rotated
+ * as `rope` says, go to q_out; keys likewise, and values as they are, to their places in the pages,
+ * in planes k_plane and v_plane, as bsgemv_cache_write puts them.  So a call follows
+ * bsgemv_cache_grow (or _extend), for the entries that grew.
+ *
+ * q: head h of row r at q + r * q_stride + h * D elements (Hq heads), k and v likewise (Hkv heads),
+ * q_out likewise; q_out may be q with the same stride.  q and q_out may be NULL together (keys and
+ * values only), or k and v (queries only; pool, tables may be NULL then).  q_weight, k_weight: D
+ * elements of the activation dtype, or NULL for no norm.  pos: int32 [T] positions for the rotation
+ * (below zero allowed), or NULL for the positions in the sequences.  T: rows of the tensors.  Rows
+ * outside starts[0] .. starts[n] - 1 or past T, rows of an entry whose seqs is outside 0 ..
+ * max_seqs-1 and rows before a sequence's first position are left alone, in q_out and the pool; a
+ * key whose page is not one of the pool's is not written.  q, k, v, q_out, weights and pool 16-byte
+ * aligned, strides multiples of 8 elements; 0 <= n <= max_seqs, 0 <= T < 2^24.  The sequences are
+ * distinct.
+ */
+int bsgemv_cache_append(bsgemv_cache_t cache, bsgemv_rope_t rope, void* pool,
+                        const int32_t* tables, const int32_t* lens, const int32_t* seqs,
+                        const int32_t* starts, int n, int T, const void* q, int64_t q_stride,
+                        const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                        const void* q_weight, const void* k_weight, float eps,
+                        const int32_t* pos, void* q_out, int64_t q_out_stride,
+                        int64_t head_stride, int64_t row_stride, int k_plane, int v_plane,
+                        void* stream);
 
 /*
  * Move the live pages to the front: with L live pages, the i-th live page at or after L (in index
