@@ -48,7 +48,7 @@ EXPORTS = ("bsgemv_plan", "bsgemv_run", "bsgemv_run_bias", "bsgemv_run_host",
            "bsgemv_cache_grow", "bsgemv_cache_append", "bsgemv_cache_destroy",
            "bsgemv_rope_plan", "bsgemv_rope_destroy",
            "bsgemv_chunk_plan", "bsgemv_chunk_run", "bsgemv_chunk_device_status",
-           "bsgemv_chunk_destroy",
+           "bsgemv_chunk_set_test_fault", "bsgemv_chunk_destroy",
            "bsgemv_version")
 
 
@@ -141,6 +141,7 @@ def lib() -> ctypes.CDLL:
         L.bsgemv_chunk_run.argtypes = [vp, vp, i64, vp, vp, i64, i64, i64, ci, vp, i64, ci, ci, vp,
                                        vp, vp, ci, ci, f32, f32, ci, vp, vp, vp, vp]
         L.bsgemv_chunk_device_status.argtypes = [vp, vp]
+        L.bsgemv_chunk_set_test_fault.argtypes = [vp, ci, i64]
         L.bsgemv_chunk_destroy.argtypes = [vp]
         for name in EXPORTS:
             if name != "bsgemv_status_string":
@@ -595,6 +596,10 @@ class ChunkPlan(_Handle):
 
     def device_status(self, stream=None) -> int:
         return lib().bsgemv_chunk_device_status(self._h, _stream(stream))
+
+    def set_test_fault(self, skip_tile: int = -1, wait_ns: int = 0) -> int:
+        """Test hook of the bounded waits (bsgemv_chunk_set_test_fault); (-1, 0) undoes it."""
+        return lib().bsgemv_chunk_set_test_fault(self._h, int(skip_tile), int(wait_ns))
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, linear: float = 1.0, ntk: float = 1.0,

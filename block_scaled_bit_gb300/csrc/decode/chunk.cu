@@ -10,7 +10,46 @@ struct bsgemv_chunk_plan_s {
   int device = -1, sms = 0;
   int bf16 = 0, Hq = 0, Hkv = 0, D = 0, page_size = 0, max_n = 0, max_T = 0;
   void* ws = nullptr;
+  int fault_skip = -1;  // bsgemv_chunk_set_test_fault
+  uint64_t fault_wait_ns = 0;
+  bsg::ChunkLayout at = {};
+  // tensor maps of the last few caches seen (a layer each)
+  struct MapEntry {
+    bool valid = false;
+    const void *k = nullptr, *v = nullptr;
+    int64_t page_stride = 0, head_stride = 0, row_stride = 0;
+    int num_pages = 0;
+    bsg::ChunkMaps maps;
+  };
+  static constexpr int kMaps = 64;
+  MapEntry maps[kMaps];
+  int next_map = 0;
 };
+
+namespace {
+
+// The cache's tensor maps, nullptr where its strides cannot be described.
+const bsg::ChunkMaps* maps_of(bsgemv_chunk_plan_s* plan, const bsg::ChunkParams& p) {
+  for (auto& m : plan->maps)
+    if (m.valid && m.k == p.k && m.v == p.v && m.page_stride == p.page_stride &&
+        m.head_stride == p.head_stride && m.row_stride == p.row_stride &&
+        m.num_pages == p.num_pages)
+      return &m.maps;
+  auto& m = plan->maps[plan->next_map];
+  m.valid = false;
+  if (!bsg::chunk_encode(p, &m.maps)) return nullptr;
+  plan->next_map = (plan->next_map + 1) % bsgemv_chunk_plan_s::kMaps;
+  m.valid = true;
+  m.k = p.k;
+  m.v = p.v;
+  m.page_stride = p.page_stride;
+  m.head_stride = p.head_stride;
+  m.row_stride = p.row_stride;
+  m.num_pages = p.num_pages;
+  return &m.maps;
+}
+
+}  // namespace
 
 using namespace bsg;
 
@@ -41,7 +80,8 @@ int bsgemv_chunk_plan(bsgemv_chunk_plan_t* out, int act_bf16, int Hq, int Hkv, i
   p->page_size = page_size;
   p->max_n = max_n;
   p->max_T = max_T;
-  rc = decode_alloc(&p->ws, 256);
+  p->at = chunk_layout(Hq, Hkv, D, max_n, max_T, sms);
+  rc = decode_alloc(&p->ws, p->at.total);
   if (rc != BSGEMV_OK) {
     delete p;
     return rc;
@@ -68,8 +108,6 @@ int bsgemv_chunk_run(bsgemv_chunk_plan_t plan, const void* q, int64_t q_stride, 
       !aligned_to(starts, 4) || !aligned_to(slopes, 4) || !aligned_to(lse, 4) || q_stride % 8 ||
       page_stride % 8 || head_stride % 8 || row_stride % 8)
     return BSGEMV_ERR_MISALIGNED;
-  constexpr int64_t kFar = int64_t{1} << 39;  // elements: what a tensor map's strides can hold
-  if (page_stride >= kFar || head_stride >= kFar || row_stride >= kFar) return BSGEMV_ERR_UNSUPPORTED;
   const int rc = decode_check_device(plan->device);
   if (rc != BSGEMV_OK) return rc;
   ChunkParams p = {};
@@ -101,16 +139,33 @@ int bsgemv_chunk_run(bsgemv_chunk_plan_t plan, const void* q, int64_t q_stride, 
   p.slopes = slopes;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
-  p.err = static_cast<unsigned*>(plan->ws);
-  p.wait_ns = kDefaultWaitNs;
-  return launch_chunk(p, plan->sms, static_cast<cudaStream_t>(stream));
+  char* ws = static_cast<char*>(plan->ws);
+  p.head = reinterpret_cast<ChunkHead*>(ws);
+  p.blocks = reinterpret_cast<ChunkBlock*>(ws + plan->at.blocks);
+  p.max_blocks = plan->at.max_blocks;
+  p.first = reinterpret_cast<int*>(ws + plan->at.first);
+  p.fills = reinterpret_cast<int2*>(ws + plan->at.fills);
+  p.cuts = reinterpret_cast<int2*>(ws + plan->at.cuts);
+  p.parts = reinterpret_cast<float*>(ws + plan->at.parts);
+  p.wait_ns = plan->fault_wait_ns ? plan->fault_wait_ns : kDefaultWaitNs;
+  p.skip = plan->fault_skip;
+  const ChunkMaps* maps = maps_of(plan, p);
+  if (maps == nullptr) return BSGEMV_ERR_UNSUPPORTED;
+  return launch_chunk(p, *maps, plan->sms, static_cast<cudaStream_t>(stream));
+}
+
+int bsgemv_chunk_set_test_fault(bsgemv_chunk_plan_t plan, int skip_tile, int64_t wait_ns) {
+  if (plan == nullptr || skip_tile < -1 || wait_ns < 0) return BSGEMV_ERR_INVALID_ARG;
+  plan->fault_skip = skip_tile;
+  plan->fault_wait_ns = static_cast<uint64_t>(wait_ns);
+  return BSGEMV_OK;
 }
 
 int bsgemv_chunk_device_status(bsgemv_chunk_plan_t plan, void* stream) {
   if (plan == nullptr) return BSGEMV_ERR_INVALID_ARG;
   const int rc = decode_check_device(plan->device);
   if (rc != BSGEMV_OK) return rc;
-  return decode_error_status(static_cast<unsigned*>(plan->ws), stream);
+  return decode_error_status(static_cast<unsigned*>(plan->ws), stream, kErrChunkLine);
 }
 
 int bsgemv_chunk_destroy(bsgemv_chunk_plan_t plan) {

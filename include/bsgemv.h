@@ -478,7 +478,7 @@ int bsgemv_attn_destroy(bsgemv_attn_plan_t plan);
  * page_size]; entries of tables past a sequence's last page are not read.  Rows of an entry whose
  * seqs is outside 0 .. num_seqs-1, and rows before a sequence's first position, get 0 in out and
  * -inf in lse; rows outside starts[0] .. starts[n] - 1 are left as they were.  A sequence counts with
- * max_pages * page_size tokens at most.  What the cache holds in places that a row does not see does
+ * max_pages * page_size tokens, and 2^30, at most.  What the cache holds in places that a row does not see does
  * not reach it, NaN and infinities included.
  *
  * q: head h of row r at q + r * q_stride + h * D elements, out [T][Hq][D] and lse [T][Hq] (fp32, or
@@ -506,6 +506,11 @@ int bsgemv_chunk_run(bsgemv_chunk_plan_t plan, const void* q, int64_t q_stride, 
 /* Synchronise `stream`, then read and clear the plan's error word (as bsgemv_device_status).
  * BSGEMV_ERR_UNSUPPORTED: a call's key tiles were more than it can count; its out rows are NaN. */
 int bsgemv_chunk_device_status(bsgemv_chunk_plan_t plan, void* stream);
+
+/* Test hook, as bsgemv_plan_set_test_fault: in the plan's next calls the first block leaves out the
+ * copy of tile `skip_tile` of its range (K and V tiles in turn; -1: none), and all waits give up after
+ * wait_ns (0: the default).  (plan, -1, 0) restores normal calls. */
+int bsgemv_chunk_set_test_fault(bsgemv_chunk_plan_t plan, int skip_tile, int64_t wait_ns);
 
 /* Free the plan (synchronises the device first).  NULL is a no-op. */
 int bsgemv_chunk_destroy(bsgemv_chunk_plan_t plan);
