@@ -1,7 +1,6 @@
 // chunk_tensor.cuh -- new tokens over the paged cache on the 5th-generation tensor cores.
 //
-// A block (one per SM) holds two streams, each a warpgroup with 128 query rows, its running maximum
-// and sum, and an output accumulator in tensor memory.  Of a unit of more than 128 rows, stream s
+// A block (one per SM) holds two streams, each 128 query rows with their running maxima and sums, and an output accumulator in tensor memory.  Of a unit of more than 128 rows, stream s
 // takes rows 128 s .. and both go through every key tile; of a smaller one both take the same rows,
 // and every other key tile, and are joined at the end (in shared memory).  At D = 256 there is one
 // stream (its accumulator is half of tensor memory) with two score buffers.
@@ -9,8 +8,8 @@
 // A job is a key tile (128 positions; 64 at D = 256) of one stream:
 //   S = Q K^T   from shared memory, M = 128; with 128 columns a step costs what the MMA does (with 64
 //               it is bound by shared memory, which reads Q again for each)
-//   softmax     a row of S lies in one lane; its thread takes all of it, and puts the numerators P
-//               into S's place
+//   softmax     a row of S lies in one lane; two threads take half of it each, and put the numerators
+//               P into S's place
 //   O += P V    P from tensor memory
 // One warp copies tiles (TMA, one box per page or tile and 64 d), a warp per stream issues its MMAs:
 // the scores of its next tile right behind P V of the last, so that the tensor cores work for one
@@ -40,12 +39,15 @@ struct ChunkTile {
   static constexpr int kRing = kRingMax < 12 ? kRingMax : 12;
   static constexpr int kOffRing = kStreams * kQB;
   static constexpr int kOffBar = kOffRing + kRing * kTileB;
-  static constexpr int kBars = 3 * kRing + 2 + 3 * kStreams + 3;
+  static constexpr int kBars = 3 * kRing + 2 + 7 * kStreams + 3;
   static constexpr int kOffWords = kOffBar + 8 * kBars;
   static constexpr int kWords = 8 + 4 * kRing;          // notes, then the guard's flags of each slot
-  static constexpr int kOffPair = (kOffWords + 4 * kWords + 15) / 16 * 16;  // m and l of stream 1
-  static constexpr int kSmem = kOffPair + (kStreams == 2 ? 1024 : 0) + 1024;  // (1024-byte tiles)
-  static constexpr int kThreads = 32 * (5 * kStreams + 2);
+  // what the two threads of a row tell each other, a float each; and stream 1's tell stream 0
+  static constexpr int kOffTell = (kOffWords + 4 * kWords + 15) / 16 * 16;
+  static constexpr int kOffSeg = kOffTell + 1024 * kStreams;   // the softmax warps' segment, and the next
+  static constexpr int kSmem = kOffSeg + 2 * 80;
+  static constexpr int kSoft = 8;                       // softmax warps of a stream
+  static constexpr int kThreads = 32 * ((kSoft + 1) * kStreams + 2);
   // tensor memory: the score buffers (P in their place), then the streams' O
   static constexpr int kColO = kStreams * kBufs * kKeys;
   static_assert(kColO + kStreams * D <= 512, "tensor memory");
@@ -100,6 +102,25 @@ BSG_DEV uint32_t tc_ld1(uint32_t addr) {
 BSG_DEV void tc_st1(uint32_t addr, uint32_t r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(r) : "memory");
 }
+// 16 columns, and back.
+BSG_DEV void tc_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+BSG_DEV void tc_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]), "r"(r[1]),
+      "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
 BSG_DEV float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -133,20 +154,23 @@ struct ChunkTensor {
       return bar(kS + (T::kBufs == 2 ? (j & 1u) : stream));
     }
     static BSG_DEV uint32_t scores_phase(uint32_t j) { return (T::kBufs == 2 ? j >> 1 : j) & 1u; }
-    // phase j & 1 of these is job j's
-    BSG_DEV uint32_t probs(uint32_t stream) const { return bar(kP + stream); }                // P written
-    BSG_DEV uint32_t out(uint32_t stream) const { return bar(kP + T::kStreams + stream); }    // P V done
+    BSG_DEV uint32_t probs(uint32_t stream) const { return bar(kP + stream); }  // P written (phase: job)
+    // P V done: of every job with two score buffers, of a segment's last with one
+    BSG_DEV uint32_t out(uint32_t stream) const { return bar(kP + T::kStreams + stream); }
     BSG_DEV uint32_t ended(uint32_t stream) const { return bar(kP + 2 * T::kStreams + stream); }  // (drain)
-    BSG_DEV uint32_t query() const { return bar(kP + 3 * T::kStreams); }       // Q written (phase: segment)
-    BSG_DEV uint32_t read() const { return bar(kP + 3 * T::kStreams + 1); }    // stream 0's scores all done
-    BSG_DEV uint32_t joined() const { return bar(kP + 3 * T::kStreams + 2); }  // stream 1's rows written
+    // the two warps of 32 rows have both come (phase: how often)
+    BSG_DEV uint32_t both(uint32_t stream, uint32_t w) const { return bar(kP + 3 * T::kStreams + 4 * stream + w); }
+    static constexpr int kQ = kP + 7 * T::kStreams;
+    BSG_DEV uint32_t query() const { return bar(kQ); }       // Q written (phase: segment)
+    BSG_DEV uint32_t read() const { return bar(kQ + 1); }    // stream 0's scores all done
+    BSG_DEV uint32_t joined() const { return bar(kQ + 2); }  // stream 1's rows written
     BSG_DEV int skip() const { return blockIdx.x == 0 ? p.a.skip : -1; }
     static BSG_DEV uint32_t col_s(uint32_t stream, uint32_t j) {
       return (T::kBufs == 2 ? (j & 1u) : stream) * K;
     }
     BSG_DEV uint32_t tile(int i) const { return base_u + T::kOffRing + i * T::kTileB; }
     // 0: tensor memory's address, 1: a wait ran out, 2: tiles sent for, 3: the row block, 4 + stream:
-    // 1 + the job whose O was given values before its first product
+    // 1 + the job whose O was given values before its first product, 6: whose turn it is to issue
     BSG_DEV volatile uint32_t* words() const {
       return reinterpret_cast<volatile uint32_t*>(base + T::kOffWords);
     }
@@ -167,6 +191,7 @@ struct ChunkTensor {
     int e, head;
     int t0, n, end;     // end: where its stretch ends in this range
     int from;           // where it starts
+    int lo_all, hi_all; // positions that all of the unit's rows see
     bool pair;          // both streams work on the same rows
     bool whole;         // all of the unit's tiles
   };
@@ -174,6 +199,9 @@ struct ChunkTensor {
     const int4* src = reinterpret_cast<const int4*>(c.p.a.blocks + e);
     const int4 x = __ldcg(src), y = __ldcg(src + 1);
     return ChunkBlock{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  }
+  static BSG_DEV ChunkSpan span(const Ctx& c, const Seg& g, int first, int rows) {
+    return chunk_span(g.b.pos0, g.b.row0 + first, rows, c.p.a.Hq / c.p.a.Hkv, c.p.a.window);
   }
   static BSG_DEV void place(const Ctx& c, Seg& g, int x) {
     const int len = g.b.tiles + kChunkCost, begin = g.b.cum * c.p.a.Hkv + g.head * len;
@@ -184,6 +212,9 @@ struct ChunkTensor {
     g.n = max(g.end - begin - kChunkCost - g.t0, 0);
     g.pair = T::kStreams == 2 && g.b.rows <= 128;
     g.whole = g.n == g.b.tiles;
+    const ChunkSpan s = span(c, g, 0, g.b.rows);
+    g.lo_all = s.lo_all;
+    g.hi_all = s.hi_all;
   }
   static BSG_DEV Seg first_seg(const Ctx& c) {
     Seg g;
@@ -202,9 +233,6 @@ struct ChunkTensor {
     place(c, g, g.end);
   }
 
-  static BSG_DEV ChunkSpan span(const Ctx& c, const Seg& g, int first, int rows) {
-    return chunk_span(g.b.pos0, g.b.row0 + first, rows, c.p.a.Hq / c.p.a.Hkv, c.p.a.window);
-  }
   // The tiles a .. b - 1 of a segment (from its first) that are a stream's, every step-th.
   struct Jobs {
     int a, b, step;
@@ -298,8 +326,8 @@ struct ChunkTensor {
 
   // ---- guard warp
   // Whether some row of the unit does not see all of key tile `tile`.
-  static BSG_DEV bool partial(const ChunkSpan& s, int tile) {
-    return (tile + 1) * K > s.hi_all || tile * K < s.lo_all;
+  static BSG_DEV bool partial(const Seg& g, int tile) {
+    return (tile + 1) * K > g.hi_all || tile * K < g.lo_all;
   }
   static BSG_DEV uint32_t not_finite(uint32_t w) {  // bit 15 or 31 set: that half is not finite
     constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
@@ -346,7 +374,7 @@ struct ChunkTensor {
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv, r.next()) {
           if (!wait_warp(c, c.full(r.slot), r.phase)) return false;
-          if (kv && partial(s, tile)) clean(c, s, tile, r.slot, lane);
+          if (kv && partial(g, tile)) clean(c, s, tile, r.slot, lane);
           __syncwarp();
           if (lane == 0) mbar_arrive(c.vok(r.slot));
         }
@@ -367,8 +395,41 @@ struct ChunkTensor {
     for (int k = 0; k < K / 16; ++k)
 #pragma unroll
       for (int part = 0; part < 2; ++part)
-        tc_mma_ts(o, pr + part * (K / 2) + k * 8, v_lo + k * 2048 / 16, kDescHi, kIdescO,
+        tc_mma_ts(o, pr + k * 16 + part * 8, v_lo + k * 2048 / 16, kDescHi, kIdescO,
                   add || k > 0 || part > 0);
+  }
+
+  // The streams' MMAs go to the tensor cores a job at a time: P V of one and the scores of the next.
+  // Without that, two streams that are ready together have theirs mixed, both wait for all of them,
+  // and stay in step: the tensor cores then stand still while both softmaxes run.
+  static BSG_DEV bool take_turn(const Ctx& c, bool lead) {
+    bool ok = true;
+    if (T::kStreams == 2) {
+      if (lead) {
+        const uint32_t lock = smem_u32(const_cast<uint32_t*>(c.words() + 6));
+        const auto free = [&] {
+          uint32_t was;
+          asm volatile("atom.acquire.cta.shared::cta.cas.b32 %0, [%1], 0, 1;" : "=r"(was) : "r"(lock) : "memory");
+          return was == 0u;
+        };
+        if (!free()) {
+          const uint64_t t0 = globaltimer_ns();
+          while (!free())
+            if (globaltimer_ns() - t0 > c.p.a.wait_ns) {
+              atomicOr(&c.p.a.head->err, kErrTimeoutFull);
+              ok = false;
+              break;
+            }
+        }
+      }
+      ok = __all_sync(0xFFFFFFFFu, ok);
+    }
+    return ok;
+  }
+  static BSG_DEV void end_turn(const Ctx& c, bool lead) {
+    if (T::kStreams == 2 && lead)
+      asm volatile("st.release.cta.shared::cta.u32 [%0], 0;" ::"r"(smem_u32(const_cast<uint32_t*>(c.words() + 6)))
+                   : "memory");
   }
 
   // The whole warp runs this; one elected lane issues.  A ring tile is free when every stream has
@@ -379,7 +440,7 @@ struct ChunkTensor {
     const uint32_t k_lo = desc_lo(c.base_u + T::kOffRing, 16);
     const uint32_t v_lo = desc_lo(c.base_u + T::kOffRing, K * 128);
     const uint32_t o = tmem + T::kColO + stream * D;
-    Ring kr = {0, 0}, vr = {1, 0};   // the next K and V tile
+    Ring kr = {0, 0};                     // the next K tile
     uint32_t job = 0, seg_phase = 0;
     for (Seg g = first_seg(c);; next_seg(c, g)) {
       if (g.n) {
@@ -388,52 +449,90 @@ struct ChunkTensor {
         if (!wait_warp(c, c.query(), seg_phase)) return false;
         seg_phase ^= 1u;
         tc_after();
-        const auto mine = [&](int t) { return t >= my.a && t < my.b && (t - my.a) % my.step == 0; };
-        uint32_t ahead = job;  // the next job to have its scores
-        // scores of tile t, or the tile given back
-        const auto scores = [&](int t) -> bool {
+        const uint32_t job0 = job;
+        const auto scores = [&](uint32_t j, uint32_t slot) {  // by the elected lane
+          mma_scores(tmem + Ctx::col_s(stream, j), q_lo, k_lo + slot * (T::kTileB / 16));
+          tc_commit(c.scores(stream, j));
+          tc_commit(c.empty(slot));
+        };
+        const auto products = [&](uint32_t j, uint32_t slot) {
+          const bool add = j != job0 || c.words()[4 + stream] == j + 1;
+          mma_out(o, tmem + Ctx::col_s(stream, j), v_lo + slot * (T::kTileB / 16), add);
+          tc_commit(c.empty(slot));
+        };
+        Ring vr = kr;                     // the V tile of the job that has its scores
+        if (T::kBufs == 2) {
+          // all tiles are the stream's; the scores of a tile ahead of P V of the one before
           if (!wait_warp(c, c.full(kr.slot), kr.phase)) return false;
-          if (mine(t)) {
+          if (lead) scores(job, kr.slot);
+          for (int t = 0; t < g.n; ++t, ++job) {
+            kr.next();
+            vr = kr;
+            kr.next();
+            if (t + 1 < g.n) {
+              if (!wait_warp(c, c.full(kr.slot), kr.phase)) return false;
+              if (lead) scores(job + 1, kr.slot);
+            }
+            if (!wait_warp(c, c.vok(vr.slot), vr.phase) || !wait_warp(c, c.probs(stream), job & 1u))
+              return false;
+            tc_after();
             if (lead) {
-              mma_scores(tmem + Ctx::col_s(stream, ahead), q_lo, k_lo + kr.slot * (T::kTileB / 16));
-              tc_commit(c.scores(stream, ahead));
-              tc_commit(c.empty(kr.slot));
+              products(job, vr.slot);
+              tc_commit(c.out(stream));
+            }
+          }
+        } else {
+          bool pending = false;           // job `job` has its scores
+          for (int t = 0; t < g.n; ++t) {
+            const Ring k_at = kr;
+            kr.next();
+            const Ring v_at = kr;
+            kr.next();
+            if (!wait_warp(c, c.full(k_at.slot), k_at.phase)) return false;
+            if (t < my.a || t >= my.b || (t - my.a) % my.step) {
+              if (!wait_warp(c, c.vok(v_at.slot), v_at.phase)) return false;
+              if (lead) {
+                mbar_arrive(c.empty(k_at.slot));
+                mbar_arrive(c.empty(v_at.slot));
+              }
+              continue;
+            }
+            if (pending && (!wait_warp(c, c.vok(vr.slot), vr.phase) ||
+                            !wait_warp(c, c.probs(stream), job & 1u)))
+              return false;
+            if (!take_turn(c, lead)) return false;
+            tc_after();
+            if (lead) {
+              if (pending) products(job, vr.slot);
+              scores(job + pending, k_at.slot);
               if (g.pair && g.n > 1 && stream == 0 && t + 2 >= g.n) tc_commit(c.read());
             }
-            ++ahead;
-          } else if (lead) {
-            mbar_arrive(c.empty(kr.slot));
+            end_turn(c, lead);
+            job += pending;
+            pending = true;
+            vr = v_at;
           }
-          kr.next();
-          kr.next();
-          return true;
-        };
-        if (T::kBufs == 2 && !scores(0)) return false;
-        for (int t = 0; t < g.n; ++t) {
-          if (T::kBufs == 2 ? t + 1 < g.n && !scores(t + 1) : !scores(t)) return false;
-          if (mine(t) && !wait_warp(c, c.probs(stream), job & 1u)) return false;
-          if (!wait_warp(c, c.vok(vr.slot), vr.phase)) return false;
-          if (mine(t)) {
+          if (pending) {
+            if (!wait_warp(c, c.vok(vr.slot), vr.phase) || !wait_warp(c, c.probs(stream), job & 1u))
+              return false;
+            if (!take_turn(c, lead)) return false;
             tc_after();
-            const bool add = t != my.a || c.words()[4 + stream] == job + 1;
             if (lead) {
-              mma_out(o, tmem + Ctx::col_s(stream, job), v_lo + vr.slot * (T::kTileB / 16), add);
+              products(job, vr.slot);
               tc_commit(c.out(stream));
-              tc_commit(c.empty(vr.slot));
             }
+            end_turn(c, lead);
             ++job;
-          } else if (lead) {
-            mbar_arrive(c.empty(vr.slot));
           }
-          vr.next();
-          vr.next();
         }
       }
       if (g.end == c.x1) return true;
     }
   }
 
-  // ---- softmax warpgroup `stream`; thread = row
+  // ---- softmax warps of `stream`: two threads a row, each half of a tile's positions (and of O's
+  // columns).  (With one, a row's 128 scores one after the other, the tensor cores waited.)
+  static constexpr int H = K / 2;
   static BSG_DEV uint32_t pack(float a, float b) { return AttnStream<BF16, 64>::pack(a, b); }
 
   // Query rows of tile `q` of a unit into shared memory (nthr threads, this one `tid`).
@@ -470,21 +569,27 @@ struct ChunkTensor {
     fence_async_shared();
   }
 
-  // What a thread knows of its row.
+  // Row `at` of a segment's: its place among the entry's tokens and heads.
   struct Row {
-    int lo, hi;        // positions it sees
-    int pos;
-    float slope;       // of its head, in base 2
-    int64_t out;       // its place in out; < 0: no row
-    int64_t lse;
+    int tok, head;
   };
+  static BSG_DEV Row row_of(const Ctx& c, const Seg& g, int at) {
+    const int G = c.p.a.Hq / c.p.a.Hkv, r = g.b.row0 + min(at, g.b.rows - 1), tok = r / G;
+    return Row{tok, g.head * G + r - tok * G};
+  }
 
-  // The largest of a row's scores; PART: of those from a to b - 1.
+  // One lane's arrival for the warp's 32.
+  static BSG_DEV void arrive_warp(uint32_t bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  }
+
+  // The largest of 32 scores; PART: of those from a to b - 1.
   template <bool PART>
-  static BSG_DEV float row_max(const uint32_t (&raw)[K], int a, int b) {
+  static BSG_DEV float max32(const uint32_t (&raw)[32], int a, int b) {
     float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int i = 0; i < K; i += 2) {
+    for (int i = 0; i < 32; i += 2) {
       const float x = !PART || (i >= a && i < b) ? __uint_as_float(raw[i]) : -INFINITY;
       const float y = !PART || (i + 1 >= a && i + 1 < b) ? __uint_as_float(raw[i + 1]) : -INFINITY;
       t[(i >> 1) & 3] = AttnPrefix<BF16, 64>::max3(t[(i >> 1) & 3], x, y);
@@ -492,47 +597,51 @@ struct ChunkTensor {
     return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
   }
 
-  // Scores to numerators 2^(scale s - base), written to P's place in two parts -- rounded to V's type,
-  // and what the rounding left (why: attn_prefix.cuh) -- 64 of them at a time; returns their sum.
+  // A thread's scores to numerators 2^(scale s - base), each 16 in their own place, in two parts:
+  // rounded to V's type, and what the rounding left (why: attn_prefix.cuh).  Their sum.
   template <bool PART>
-  static BSG_DEV float numerators(const uint32_t (&raw)[K], float scale, float base, int a, int b,
-                                  uint32_t tp) {
+  static BSG_DEV float numerators(uint32_t ts, float scale, float base, int a, int b) {
     const uint64_t sc = f32x2(scale, scale), mb = f32x2(-base, -base);
     uint64_t sum[2] = {0ull, 0ull};
+    uint32_t raw[2][16];
+    tc_ld16(ts, raw[0]);
 #pragma unroll
-    for (int h = 0; h < K; h += 64) {
-      uint32_t hi[32], lo[32];
+    for (int j = 0; j < H; j += 16) {
+      const uint32_t(&s)[16] = raw[(j / 16) & 1];
+      tc_wait_ld();
+      if (j + 16 < H) tc_ld16(ts + j + 16, raw[(j / 16 + 1) & 1]);
+      uint32_t out[16];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int j = h + 2 * i;
+      for (int i = 0; i < 8; ++i) {
+        const int k = j + 2 * i;
         uint64_t e;
         asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e)
-            : "l"(f32x2(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1]))), "l"(sc), "l"(mb));
+            : "l"(f32x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]))), "l"(sc), "l"(mb));
         float x = ex2(f32x2_lo(e)), y = ex2(f32x2_hi(e));
         if (PART) {
-          x = j >= a && j < b ? x : 0.f;
-          y = j + 1 >= a && j + 1 < b ? y : 0.f;
+          x = k >= a && k < b ? x : 0.f;
+          y = k + 1 >= a && k + 1 < b ? y : 0.f;
         }
-        hi[i] = pack(x, y);
-        lo[i] = pack(x - half_to_f32<BF16>(hi[i], 0), y - half_to_f32<BF16>(hi[i], 1));
+        out[i] = pack(x, y);
+        out[8 + i] = pack(x - half_to_f32<BF16>(out[i], 0), y - half_to_f32<BF16>(out[i], 1));
         asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[i & 1]) : "l"(f32x2(x, y)));
       }
-      tc_st32(tp + h / 2, hi);
-      tc_st32(tp + K / 2 + h / 2, lo);
+      tc_st16(ts + j, out);
     }
     return (f32x2_lo(sum[0]) + f32x2_hi(sum[0])) + (f32x2_lo(sum[1]) + f32x2_hi(sum[1]));
   }
 
   // Values that are not finite, which the guard took out of tile `tile`: each row that sees them adds
-  // them, times its weight, to its O (which nothing else works on now).  first: O has no values yet.
-  static __device__ __noinline__ void add_not_finite(const Ctx& c, const Seg& g, const Row& row,
+  // them, times its weight, to its O (which nothing else works on now), half of the columns a thread.
+  // first: O has no values yet.
+  static __device__ __noinline__ void add_not_finite(const Ctx& c, const Seg& g, int pos_row, int half,
                                                      int tile, int slot, uint32_t tp, uint32_t to,
                                                      bool first) {
     const ChunkParams& p = c.p.a;
     if (first) {
       const uint32_t zero[32] = {};
 #pragma unroll 1
-      for (int i = 0; i < D; i += 32) tc_st32(to + i, zero);
+      for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 32) tc_st32(to + i, zero);
       tc_wait_st();
     }
 #pragma unroll 1
@@ -543,13 +652,14 @@ struct ChunkTensor {
       if (page < 0 || page >= p.num_pages) continue;
       const uint16_t* v = p.v + page * p.page_stride + g.head * p.head_stride +
                           (pos & ((1 << p.page_log2) - 1)) * p.row_stride;
-      const uint32_t hi = tc_ld1(tp + kk / 2), lo = tc_ld1(tp + K / 2 + kk / 2);
+      const uint32_t at = tp + kk / 16 * 16 + kk % 16 / 2;
+      const uint32_t hi = tc_ld1(at), lo = tc_ld1(at + 8);
       tc_wait_ld();
       const float w = (kk & 1) ? half_to_f32<BF16>(hi, 1) + half_to_f32<BF16>(lo, 1)
                                : half_to_f32<BF16>(hi, 0) + half_to_f32<BF16>(lo, 0);
-      const bool sees = pos >= row.lo && pos < row.hi;
+      const bool sees = pos >= chunk_lo(pos_row, p.window) && pos <= pos_row;
 #pragma unroll 1
-      for (int d = 0; d < D; ++d) {
+      for (int d = half * (D / 2); d < (half + 1) * (D / 2); ++d) {
         const uint32_t x = __ldg(v + d);
         if (!(not_finite(x) & 0x8000u)) continue;
         const uint32_t o = tc_ld1(to + d);
@@ -560,97 +670,123 @@ struct ChunkTensor {
     }
   }
 
+  // What a softmax thread counts, over the block's whole range.
+  struct Counts {
+    uint32_t job;     // jobs of its stream
+    uint32_t tiles;   // ring tiles before the segment
+    uint32_t ends;    // segments in which its stream had jobs
+    uint32_t joins;   // segments whose streams were joined
+    uint32_t both;    // times that it met its row's other thread
+  };
+
+  // The segment lies in shared memory, and the one after it: what a thread keeps in registers besides
+  // its scores would go to local memory, which is L2's with this much shared memory.
   static BSG_DEV bool softmax(const Ctx& c, int stream, int tid) {
-    const ChunkParams& p = c.p.a;
-    const int G = p.Hq / p.Hkv;
-    uint32_t job = 0;     // the segment's first job
-    uint32_t tiles = 0;   // ring tiles before the segment
-    uint32_t joins = 0;   // segments before this one whose streams were joined
+    Seg* segs = reinterpret_cast<Seg*>(c.base + T::kOffSeg);
+    static_assert(sizeof(Seg) <= 80, "their place");
+    Counts n = {};
     bool ok = true;
-    for (Seg g = first_seg(c);; next_seg(c, g)) {
-      if (g.n) {
-        // everyone is done with the queries of the segment before (a warp whose wait ran out still
-        // comes here)
-        asm volatile("bar.sync 1, %0;" ::"n"(128 * T::kStreams) : "memory");
-        const Jobs my = jobs_of(c, g, stream);
-        const bool join = g.pair && g.n > 1;
-        if (ok) {
-          Row row;
-          const int at = (g.pair ? 0 : 128 * stream) + tid;
-          const int r = g.b.row0 + min(at, g.b.rows - 1), tok = r / G, h = g.head * G + r - tok * G;
-          row.pos = g.b.pos0 + tok;
-          row.lo = chunk_lo(row.pos, p.window);
-          row.hi = row.pos + 1;
-          row.slope = EXTRA && p.slopes ? __ldg(p.slopes + h) * 1.4426950408889634f : 0.f;
-          row.lse = static_cast<int64_t>(g.b.tok0 + tok) * p.Hq + h;
-          row.out = at < g.b.rows ? row.lse * D : -1;
-          ok = segment(c, g, my, row, stream, tid, job, tiles, joins, join);
-        }
-        job += my.count();
-        tiles += 2 * g.n;
-        joins += join;
+    if (threadIdx.x == 0) segs[0] = first_seg(c);
+    for (int i = 0;; i ^= 1) {
+      // everyone is done with the queries of the segment before (a warp whose wait ran out still
+      // comes here)
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * T::kSoft * T::kStreams) : "memory");
+      const Seg& g = segs[i];
+      Seg* next = threadIdx.x == 0 && g.end != c.x1 ? segs + (i ^ 1) : nullptr;
+      if (ok && g.n) {
+        ok = segment(c, g, next, stream, tid, n);
+      } else if (next) {
+        *next = g;
+        next_seg(c, *next);
       }
+      n.tiles += 2 * g.n;
+      n.ends += jobs_of(c, g, stream).count() > 0;
+      n.joins += g.pair && g.n > 1;
       if (g.end == c.x1) return ok;
     }
   }
 
-  static BSG_DEV bool segment(const Ctx& c, const Seg& g, const Jobs& my, const Row& row, int stream,
-                              int tid, uint32_t job0, uint32_t tiles, uint32_t joins, bool join) {
+  static BSG_DEV bool segment(const Ctx& c, const Seg& g, Seg* next, int stream, int tid, Counts& n) {
     const ChunkParams& p = c.p.a;
-    const uint32_t lanes = static_cast<uint32_t>((tid >> 5) * 32) << 16;
+    const int half = tid >> 7, quad = (tid >> 5) & 3, lane = tid & 31;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t to = c.tmem + T::kColO + stream * D + lanes;
-    if (g.pair) load_q(c, g, 0, stream * 128 + tid, 256);
-    else load_q(c, g, stream, tid, 128);
-    mbar_arrive(c.query());
-    const ChunkSpan s = span(c, g, 0, g.b.rows);
-    const uint32_t jobs = my.count();
+    if (g.pair) load_q(c, g, 0, stream * (32 * T::kSoft) + tid, 2 * 32 * T::kSoft);
+    else load_q(c, g, stream, tid, 32 * T::kSoft);
+    arrive_warp(c.query(), lane);
+    if (next) {
+      *next = g;
+      next_seg(c, *next);
+    }
+    const Jobs my = jobs_of(c, g, stream);
+    const int first = g.b.tile0 + g.t0;
+    float slope = 0.f;  // base 2
+    int pos;            // the row's
+    {
+      const Row row = row_of(c, g, (g.pair ? 0 : 128 * stream) + (tid & 127));
+      pos = g.b.pos0 + row.tok;
+      if (EXTRA && p.slopes) slope = __ldg(p.slopes + row.head) * 1.4426950408889634f;
+    }
     constexpr float kLog2e = 1.4426950408889634f;
-    const float scale_log2 = fabsf(p.scale) * kLog2e;
     const bool capped = EXTRA && p.cap > 0.f;
-    const float cap_log2 = p.cap * kLog2e, cap_in = capped ? 2.f * scale_log2 / p.cap : 0.f;
-    // score, base 2 = scale * raw (EXTRA: raw is turned into it first)
-    const float scale = EXTRA ? 1.f : scale_log2;
-    float m = -INFINITY, l = 0.f;  // m: the maximum that O and l are scaled to
+    // this thread's word for its row's other one, and that one's for it
+    float* tell = reinterpret_cast<float*>(c.base + T::kOffTell) + stream * 256;
+    float m = -INFINITY, l = 0.f;  // m: the maximum that O and l are scaled to; l: of its positions
     bool seen = false;             // some of the tiles had positions that this row sees
-    uint32_t job = job0;
-    for (int t = my.a; t < my.b; t += my.step, ++job) {
-      const int tile = g.b.tile0 + g.t0 + t;
-      if (!wait_warp(c, c.scores(stream, job), Ctx::scores_phase(job))) return false;
+    for (int t = my.a; t < my.b; t += my.step, ++n.job) {
+      const int tile = first + t;
+      if (!wait_warp(c, c.scores(stream, n.job), Ctx::scores_phase(n.job))) return false;
       tc_after();
-      const uint32_t ts = c.tmem + Ctx::col_s(stream, job) + lanes;
-      uint32_t raw[K];
+      const uint32_t ts = c.tmem + Ctx::col_s(stream, n.job) + lanes + half * H;  // its scores
+      // score, base 2 = scale * raw (EXTRA: raw is turned into it first)
+      const float scale = EXTRA ? 1.f : fabsf(p.scale) * kLog2e;
+      const int at0 = tile * K + half * H;  // this thread's first position
+      const int a = chunk_lo(pos, p.window) - at0, b = pos + 1 - at0;  // those that the row sees: a .. b - 1
+      seen |= a + half * H < K && b + half * H > 0;
+      const bool cut = __any_sync(0xFFFFFFFFu, a > 0 || b < H);
+      float top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < K; i += 32) tc_ld32(ts + i, raw + i);
-      tc_wait_ld();
-      if (EXTRA) {
-        const float off = static_cast<float>(tile * K - row.pos);
+      for (int i = 0; i < H; i += 32) {
+        uint32_t raw[32];
+        tc_ld32(ts + i, raw);
+        tc_wait_ld();
+        if (EXTRA) {
+          const float scale_log2 = fabsf(p.scale) * kLog2e, cap_log2 = p.cap * kLog2e;
+          const float cap_in = capped ? 2.f * scale_log2 / p.cap : 0.f;
+          const float off = static_cast<float>(at0 + i - pos);
 #pragma unroll
-        for (int i = 0; i < K; ++i) {
-          float x = __uint_as_float(raw[i]);
-          // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap))
-          if (capped) x = fmaf(-2.f * cap_log2, rcp_approx(1.f + ex2(x * cap_in)), cap_log2);
-          else x *= scale_log2;
-          raw[i] = __float_as_uint(fmaf(row.slope, off + static_cast<float>(i), x));
+          for (int y = 0; y < 32; ++y) {
+            float x = __uint_as_float(raw[y]);
+            // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap))
+            if (capped) x = fmaf(-2.f * cap_log2, rcp_approx(1.f + ex2(x * cap_in)), cap_log2);
+            else x *= scale_log2;
+            raw[y] = __float_as_uint(fmaf(slope, off + static_cast<float>(y), x));
+          }
+          tc_st32(ts + i, raw);
         }
+        top = fmaxf(top, cut ? max32<true>(raw, a - i, b - i) : max32<false>(raw, 0, 32));
       }
-      // the row's positions in this tile
-      const int a = row.lo - tile * K, b = row.hi - tile * K;
-      seen |= a < K && b > 0;
-      const bool cut = __any_sync(0xFFFFFFFFu, a > 0 || b < K);
-      const float top = (cut ? row_max<true>(raw, a, b) : row_max<false>(raw, 0, K)) * scale;
+      if (EXTRA) tc_wait_st();
+      // the other half's
+      tell[tid] = top;
+      arrive_warp(c.both(stream, quad), lane);
+      if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
+      top = fmaxf(top, tell[tid ^ 128]) * scale;
       // O and l move to a new maximum when it is more than 8 above theirs (or the first)
       const bool grow = top > m + 8.f;
       if (__any_sync(0xFFFFFFFFu, grow)) {
-        const float next = grow ? top : m;
-        const float keep = grow ? ex2(m - next) : 1.f;
+        const float next_m = grow ? top : m;
+        const float keep = grow ? ex2(m - next_m) : 1.f;
         l *= keep;
-        m = next;
+        m = next_m;
         if (t != my.a) {
           // the accumulator's last product is done (one buffer: the scores came after it)
-          if (T::kBufs == 2 && !wait_warp(c, c.out(stream), (job - 1) & 1u)) return false;
-          tc_after();
+          if (T::kBufs == 2) {
+            if (!wait_warp(c, c.out(stream), (n.job - 1) & 1u)) return false;
+            tc_after();
+          }
 #pragma unroll 1
-          for (int i = 0; i < D; i += 32) {
+          for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 32) {
             uint32_t o[32];
             tc_ld32(to + i, o);
             tc_wait_ld();
@@ -658,47 +794,62 @@ struct ChunkTensor {
             for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * keep);
             tc_st32(to + i, o);
           }
-          tc_wait_st();
         }
       }
       const float base = m == -INFINITY ? 0.f : m;
-      l += cut ? numerators<true>(raw, scale, base, a, b, ts) : numerators<false>(raw, scale, base, 0, K, ts);
+      l += cut ? numerators<true>(ts, scale, base, a, b) : numerators<false>(ts, scale, base, 0, H);
       tc_wait_st();
-      // (done already with one buffer: the wait keeps in step with the barrier's phases)
-      if (t != my.a && !wait_warp(c, c.out(stream), (job - 1) & 1u)) return false;
-      if (partial(s, tile)) {
-        const uint32_t n = tiles + 2 * t + 1;
-        const int slot = static_cast<int>(n % T::kRing);
-        if (!wait_warp(c, c.vok(slot), (n / T::kRing) & 1u)) return false;
+      // (two buffers: in step with the barrier's phases; one: these scores came after that product)
+      if (T::kBufs == 2 && t != my.a && !wait_warp(c, c.out(stream), (n.job - 1) & 1u)) return false;
+      if (partial(g, tile)) {
+        const uint32_t i = n.tiles + 2 * t + 1;
+        const int slot = static_cast<int>(i % T::kRing);
+        if (!wait_warp(c, c.vok(slot), (i / T::kRing) & 1u)) return false;
         uint32_t bad = 0u;
 #pragma unroll
-        for (int i = 0; i < K / 32; ++i) bad |= c.flags(slot)[i];
+        for (int x = 0; x < K / 32; ++x) bad |= c.flags(slot)[x];
         if (bad) {
+          // (the other half's P is there)
+          tc_before();
+          arrive_warp(c.both(stream, quad), lane);
+          if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
           tc_after();
-          add_not_finite(c, g, row, tile, slot, ts, to, t == my.a);
-          if (t == my.a && tid == 0) c.words()[4 + stream] = job + 1;
+          add_not_finite(c, g, pos, half, tile, slot, ts - half * H, to, t == my.a);
+          if (t == my.a && tid == 0) c.words()[4 + stream] = n.job + 1;
         }
       }
       tc_before();
-      mbar_arrive(c.probs(stream));
+      arrive_warp(c.probs(stream), lane);
     }
+    // the row's sum
+    tell[tid] = l;
+    arrive_warp(c.both(stream, quad), lane);
+    if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
+    l += tell[tid ^ 128];
+    const uint32_t jobs = my.count();
+    const bool join = g.pair && g.n > 1;
     if (jobs) {
-      if (!wait_warp(c, c.out(stream), (job - 1) & 1u)) return false;
+      if (!wait_warp(c, c.out(stream), (T::kBufs == 2 ? n.job - 1 : n.ends) & 1u)) return false;
       tc_after();
     }
-    const bool end = finish(c, g, row, stream, tid, jobs, to, seen ? attn_part_max(m) : -INFINITY, l, joins, join);
+    // (the other thread has read what it was told, and all words are free again)
+    arrive_warp(c.both(stream, quad), lane);
+    if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
+    const bool end = finish(c, g, stream, tid, jobs, to, seen ? attn_part_max(m) : -INFINITY, l, n.joins, join);
     tc_before();
     return end;
   }
 
-  // The segment's rows: out where it has the whole unit, else a part.  m = -inf: no positions.
-  static BSG_DEV bool finish(const Ctx& c, const Seg& g, const Row& row, int stream, int tid,
-                             uint32_t jobs, uint32_t to, float m, float l, uint32_t joins, bool join) {
+  // The segment's rows, half of the columns a thread: out where it has the whole unit, else a part.
+  // m = -inf: no positions.
+  static BSG_DEV bool finish(const Ctx& c, const Seg& g, int stream, int tid, uint32_t jobs,
+                             uint32_t to, float m, float l, uint32_t joins, bool join) {
     const ChunkParams& p = c.p.a;
-    const int warp = tid >> 5, lane = tid & 31;
+    const int warp = tid >> 5, lane = tid & 31, half = tid >> 7, r128 = tid & 127;
+    const int d0 = half * (D / 2), d1 = d0 + D / 2;
     bool has0 = true, has1 = false;  // the streams' sums that count, and their weights
     float w0 = 1.f, w1 = 0.f;
-    float* ml = reinterpret_cast<float*>(c.base + T::kOffPair);
+    float* ml = reinterpret_cast<float*>(c.base + T::kOffTell) + 256;  // (stream 1's place)
     // stream 1's rows, [column][row], in the place of both query tiles
     float* other = reinterpret_cast<float*>(c.base);
     if (join) {
@@ -706,20 +857,19 @@ struct ChunkTensor {
         // stream 0 has had its last scores
         if (!wait_warp(c, c.read(), joins & 1u)) return false;
 #pragma unroll 1
-        for (int i = 0; i < D; i += 32) {
+        for (int i = d0; i < d1; i += 32) {
           uint32_t o[32];
           tc_ld32(to + i, o);
           tc_wait_ld();
 #pragma unroll
-          for (int y = 0; y < 32; ++y) other[(i + y) * 128 + tid] = __uint_as_float(o[y]);
+          for (int y = 0; y < 32; ++y) other[(i + y) * 128 + r128] = __uint_as_float(o[y]);
         }
-        ml[tid] = m;
-        ml[128 + tid] = l;
-        mbar_arrive(c.joined());
+        ml[tid] = half ? l : m;
+        arrive_warp(c.joined(), lane);
         return true;
       }
       if (!wait_warp(c, c.joined(), joins & 1u)) return false;
-      const float m1 = ml[tid], l1 = ml[128 + tid];
+      const float m1 = ml[r128], l1 = ml[128 + r128];
       const float top = fmaxf(m, m1), base = top == -INFINITY ? 0.f : top;
       has0 = m != -INFINITY;
       has1 = m1 != -INFINITY;
@@ -731,23 +881,26 @@ struct ChunkTensor {
       return true;  // (one tile, stream 0's)
     }
     float* part = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + (g.from == c.x0 ? 0 : 1)) * chunk_slot_floats(D);
-    const int at = (g.pair ? 0 : 128 * stream) + tid;
+    const int at = (g.pair ? 0 : 128 * stream) + r128;
     const float inv = 1.f / l;
-    if (row.out >= 0) {
-      if (g.whole) {
-        if (p.lse) p.lse[row.lse] = (m + log2f(l)) * 0.6931471805599453f;
-      } else {
+    int64_t mine = -1;  // where the row begins, in bytes; < 0: no row
+    if (at < g.b.rows) {
+      const Row row = row_of(c, g, at);
+      const int64_t r = static_cast<int64_t>(g.b.tok0 + row.tok) * p.Hq + row.head;
+      mine = g.whole ? r * D * 2 : static_cast<int64_t>(at) * D * 4;
+      if (half == 0 && g.whole) {
+        if (p.lse) p.lse[r] = (m + log2f(l)) * 0.6931471805599453f;
+      } else if (half == 0) {
         __stcg(part + T::kRows * D + at, m);
         __stcg(part + T::kRows * (D + 1) + at, l);
       }
     }
     if (jobs == 0) return true;  // (a part without tiles: nothing of it is read but m)
     // A thread holds a row; through shared memory, 64 bytes at a time, into whole sectors.  Row i of a
-    // warp's 32 lies at stage(i): in the stream's query tile, or where the columns just read lay.
-    const int64_t mine = g.whole ? row.out * 2 : (row.out < 0 ? -1 : static_cast<int64_t>(at) * D * 4);
+    // warp's 32 lies at line i / 2: in the stream's query tile, or where the columns just read lay.
     uint8_t* dst = g.whole ? reinterpret_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(part);
 #pragma unroll 1
-    for (int i = 0; i < D; i += 32) {
+    for (int i = d0; i < d1; i += 32) {
       uint32_t o[32];
       tc_ld32(to + i, o);
       tc_wait_ld();
@@ -755,11 +908,12 @@ struct ChunkTensor {
 #pragma unroll
         for (int y = 0; y < 32; ++y) {
           const float x = has0 ? __uint_as_float(o[y]) * w0 : 0.f;
-          o[y] = __float_as_uint(has1 ? fmaf(other[(i + y) * 128 + tid], w1, x) : x);
+          o[y] = __float_as_uint(has1 ? fmaf(other[(i + y) * 128 + r128], w1, x) : x);
         }
         __syncwarp();
       }
-      uint8_t* stage = join ? c.base + i * 512 + warp * 128 : c.base + (g.pair ? 0 : stream) * T::kQB + warp * 2048;
+      uint8_t* stage = join ? c.base + i * 512 + (warp & 3) * 128
+                            : c.base + (g.pair ? 0 : stream) * T::kQB + warp * 2048;
       const int line = join ? 512 : 128;
       const auto put = [&](const uint4& v, int y) {
         *reinterpret_cast<uint4*>(stage + (lane >> 1) * line + (lane & 1) * 64 +
@@ -788,13 +942,13 @@ struct ChunkTensor {
         send(2 * i);
       } else {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int x = 0; x < 2; ++x) {
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const uint32_t* v = o + 16 * half + 4 * y;
+            const uint32_t* v = o + 16 * x + 4 * y;
             put(make_uint4(v[0], v[1], v[2], v[3]), y);
           }
-          send(4 * (i + 16 * half));
+          send(4 * (i + 16 * x));
         }
       }
     }
@@ -803,10 +957,14 @@ struct ChunkTensor {
 
   static BSG_DEV void block(const ChunkTensorParams& p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    Ctx c{p, {}, base, smem_u32(base), 0u, 0, 0, 0};
+    Ctx c{p, {}, smem_raw, smem_u32(smem_raw), 0u, 0, 0, 0};
+    // (the swizzle's 1024-byte tiles: the array's alignment, which nothing but the linker can break)
+    if (c.base_u & 1023u) {
+      if (threadIdx.x == 0) atomicOr(&p.a.head->err, kErrTimeoutFull);
+      return;
+    }
     const int warp = threadIdx.x >> 5;
-    constexpr int kCopyWarp = 4 * T::kStreams, kGuardWarp = kCopyWarp + 1, kMmaWarp = kCopyWarp + 2;
+    constexpr int kCopyWarp = T::kSoft * T::kStreams, kGuardWarp = kCopyWarp + 1, kMmaWarp = kCopyWarp + 2;
     if (threadIdx.x == 0) {
       for (int i = 0; i < T::kRing; ++i) {
         mbar_init(c.full(i), 1);
@@ -815,13 +973,14 @@ struct ChunkTensor {
       }
       for (int i = 0; i < 2; ++i) mbar_init(c.bar(Ctx::kS + i), 1);
       for (int b = 0; b < T::kStreams; ++b) {
-        mbar_init(c.probs(b), 128);
+        mbar_init(c.probs(b), T::kSoft);
+        for (int w = 0; w < 4; ++w) mbar_init(c.both(b, w), 2);
         mbar_init(c.out(b), 1);
         mbar_init(c.ended(b), 1);
       }
-      mbar_init(c.query(), 128 * T::kStreams);
+      mbar_init(c.query(), T::kSoft * T::kStreams);
       mbar_init(c.read(), 1);
-      mbar_init(c.joined(), 128);
+      mbar_init(c.joined(), T::kSoft);
       for (int i = 1; i < T::kWords; ++i) c.words()[i] = 0u;
       fence_mbar_init();
     }
@@ -845,17 +1004,13 @@ struct ChunkTensor {
       __syncthreads();
       c.e0 = c.words()[3];
       bool ok;
-      // (with two streams the other four warps leave theirs registers: 256 threads of 216 and 128 of 72
-      // are the 384 of 168 that the block was launched with)
       if (warp < kCopyWarp) {
-        if constexpr (T::kStreams == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
         if (threadIdx.x == 0) {  // for chunk_finish
           const Seg g = first_seg(c);
           p.a.cuts[blockIdx.x] = make_int2(g.e, g.head);
         }
-        ok = softmax(c, warp / 4, threadIdx.x & 127);
+        ok = softmax(c, warp / T::kSoft, threadIdx.x % (32 * T::kSoft));
       } else {
-        if constexpr (T::kStreams == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
         if (warp == kCopyWarp) ok = copy(c, threadIdx.x & 31);
         else if (warp == kGuardWarp) ok = guard(c, threadIdx.x & 31);
         else ok = issue(c, warp - kMmaWarp);
