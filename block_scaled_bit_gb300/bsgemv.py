@@ -141,7 +141,7 @@ def lib() -> ctypes.CDLL:
         L.bsgemv_chunk_run.argtypes = [vp, vp, i64, vp, vp, i64, i64, i64, ci, vp, i64, ci, ci, vp,
                                        vp, vp, ci, ci, f32, f32, ci, vp, vp, vp, vp]
         L.bsgemv_chunk_device_status.argtypes = [vp, vp]
-        L.bsgemv_chunk_set_test_fault.argtypes = [vp, ci, i64]
+        L.bsgemv_chunk_set_test_fault.argtypes = [vp, ci, ci, i64]
         L.bsgemv_chunk_destroy.argtypes = [vp]
         for name in EXPORTS:
             if name != "bsgemv_status_string":
@@ -597,9 +597,9 @@ class ChunkPlan(_Handle):
     def device_status(self, stream=None) -> int:
         return lib().bsgemv_chunk_device_status(self._h, _stream(stream))
 
-    def set_test_fault(self, skip_tile: int = -1, wait_ns: int = 0) -> int:
-        """Test hook of the bounded waits (bsgemv_chunk_set_test_fault); (-1, 0) undoes it."""
-        return lib().bsgemv_chunk_set_test_fault(self._h, int(skip_tile), int(wait_ns))
+    def set_test_fault(self, kernel: int = 0, skip_tile: int = -1, wait_ns: int = 0) -> int:
+        """Test hook of the bounded waits (bsgemv_chunk_set_test_fault); (0, -1, 0) undoes it."""
+        return lib().bsgemv_chunk_set_test_fault(self._h, int(kernel), int(skip_tile), int(wait_ns))
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, linear: float = 1.0, ntk: float = 1.0,

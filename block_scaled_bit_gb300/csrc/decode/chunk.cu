@@ -10,7 +10,7 @@ struct bsgemv_chunk_plan_s {
   int device = -1, sms = 0;
   int bf16 = 0, Hq = 0, Hkv = 0, D = 0, page_size = 0, max_n = 0, max_T = 0;
   void* ws = nullptr;
-  int fault_skip = -1;  // bsgemv_chunk_set_test_fault
+  int fault_skip[2] = {-1, -1};  // bsgemv_chunk_set_test_fault
   uint64_t fault_wait_ns = 0;
   bsg::ChunkLayout at = {};
   // tensor maps of the last few caches seen (a layer each)
@@ -141,22 +141,29 @@ int bsgemv_chunk_run(bsgemv_chunk_plan_t plan, const void* q, int64_t q_stride, 
   p.lse = lse;
   char* ws = static_cast<char*>(plan->ws);
   p.head = reinterpret_cast<ChunkHead*>(ws);
-  p.blocks = reinterpret_cast<ChunkBlock*>(ws + plan->at.blocks);
-  p.max_blocks = plan->at.max_blocks;
+  for (int i = 0; i < 2; ++i) {
+    ChunkLine& line = i ? p.stream : p.tensor;
+    const auto& at = i ? plan->at.stream : plan->at.tensor;
+    line.blocks = reinterpret_cast<ChunkBlock*>(ws + at.blocks);
+    line.cuts = reinterpret_cast<ChunkCut*>(ws + at.cuts);
+    line.parts = reinterpret_cast<float*>(ws + at.parts);
+    line.max_blocks = at.max_blocks;
+  }
   p.first = reinterpret_cast<int*>(ws + plan->at.first);
   p.fills = reinterpret_cast<int2*>(ws + plan->at.fills);
-  p.cuts = reinterpret_cast<int2*>(ws + plan->at.cuts);
-  p.parts = reinterpret_cast<float*>(ws + plan->at.parts);
   p.wait_ns = plan->fault_wait_ns ? plan->fault_wait_ns : kDefaultWaitNs;
-  p.skip = plan->fault_skip;
+  p.skip[0] = plan->fault_skip[0];
+  p.skip[1] = plan->fault_skip[1];
   const ChunkMaps* maps = maps_of(plan, p);
   if (maps == nullptr) return BSGEMV_ERR_UNSUPPORTED;
   return launch_chunk(p, *maps, plan->sms, static_cast<cudaStream_t>(stream));
 }
 
-int bsgemv_chunk_set_test_fault(bsgemv_chunk_plan_t plan, int skip_tile, int64_t wait_ns) {
-  if (plan == nullptr || skip_tile < -1 || wait_ns < 0) return BSGEMV_ERR_INVALID_ARG;
-  plan->fault_skip = skip_tile;
+int bsgemv_chunk_set_test_fault(bsgemv_chunk_plan_t plan, int kernel, int skip_tile, int64_t wait_ns) {
+  if (plan == nullptr || kernel < 0 || kernel > 1 || skip_tile < -1 || wait_ns < 0)
+    return BSGEMV_ERR_INVALID_ARG;
+  plan->fault_skip[kernel] = skip_tile;
+  plan->fault_skip[1 - kernel] = -1;
   plan->fault_wait_ns = static_cast<uint64_t>(wait_ns);
   return BSGEMV_OK;
 }

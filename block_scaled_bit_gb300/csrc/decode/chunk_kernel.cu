@@ -1,5 +1,6 @@
 // chunk_kernel.cu -- attention of new tokens over the paged cache: its line of work, what is put
 // together at the end, and the launches.
+#include "chunk_stream.cuh"
 #include "chunk_tensor.cuh"
 
 namespace bsg {
@@ -62,62 +63,100 @@ BSG_DEV ChunkEntry chunk_entry(const ChunkParams& p, int i) {
   return e;
 }
 
-// The line of work, by one block.
+// The lines of work, by one block.  short_rows: entries of up to this many rows go to the streaming
+// kernel.
+struct ChunkKinds {
+  int short_rows;
+  int rows[2], keys[2];   // of a row block and a key tile: tensor-memory kernel, streaming kernel
+};
+
 __global__ void __launch_bounds__(kSetup)
-    chunk_setup(const __grid_constant__ ChunkParams p, int block_rows, int keys) {
+    chunk_setup(const __grid_constant__ ChunkParams p, const __grid_constant__ ChunkKinds kinds) {
   pdl_wait();
   pdl_launch_dependents();
   const int G = p.Hq / p.Hkv;
-  int total = 0, sum, any = 0;
+  const auto kind_of = [&](int64_t rows) { return rows <= kinds.short_rows ? 1 : 0; };
+  int total[2] = {0, 0}, sum, any = 0;
   for (int base = 0; base < p.n; base += kSetup) {
     const int i = base + threadIdx.x;
-    int need = 0;
+    int need = 0, kind = 0;
     if (i < p.n) {
       const ChunkEntry e = chunk_entry(p, i);
       const int64_t rows = static_cast<int64_t>(e.count - e.gone) * G;
-      need = static_cast<int>((rows + block_rows - 1) / block_rows);
+      kind = kind_of(rows);
+      need = static_cast<int>((rows + kinds.rows[kind] - 1) / kinds.rows[kind]);
       any |= e.gone > 0;
       p.fills[i] = make_int2(e.tok0, e.gone);
     }
-    const int before = chunk_sum(total, chunk_scan(need, &sum));
-    if (i < p.n) p.first[i] = before;
-    total = chunk_sum(total, sum);
+    int before = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int at = chunk_sum(total[k], chunk_scan(kind == k ? need : 0, &sum));
+      if (kind == k) before = at;
+      total[k] = chunk_sum(total[k], sum);
+    }
+    if (i < p.n) p.first[i] = need ? 2 * before + kind : -1;
   }
   any = __syncthreads_or(any);
-  bool over = total > p.max_blocks;  // (entries on the same rows)
-  const int blocks = over ? 0 : total;
-  int stretch = 0;
-  for (int base = 0; base < blocks; base += kSetup) {
-    const int x = base + threadIdx.x;
-    ChunkBlock b = {};
-    int len = 0;
-    if (x < blocks) {
-      int lo = 0, hi = p.n;  // the last entry with first <= x
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.first[mid] <= x) lo = mid;
-        else hi = mid;
-      }
-      const ChunkEntry e = chunk_entry(p, lo);
-      b.seq = e.seq;
-      b.tok0 = e.tok0 + e.gone;
-      b.pos0 = e.pos0;
-      b.row0 = (x - p.first[lo]) * block_rows;
-      b.rows = min((e.count - e.gone) * G - b.row0, block_rows);
-      const ChunkSpan s = chunk_span(b.pos0, b.row0, b.rows, G, p.window);
-      b.tile0 = s.lo / keys;
-      b.tiles = (s.hi + keys - 1) / keys - b.tile0;
-      len = b.tiles + kChunkCost;
+  bool over = total[0] > p.tensor.max_blocks || total[1] > p.stream.max_blocks;  // (entries on the same rows)
+  int stretch[2] = {0, 0}, blocks[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const ChunkLine& line = k ? p.stream : p.tensor;
+    blocks[k] = over ? 0 : total[k];
+    // each entry leaves its number at its first row block, the blocks after it find it there
+    for (int x = threadIdx.x; x < blocks[k]; x += kSetup) line.blocks[x].cum = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.n && blocks[k]; i += kSetup) {
+      const int f = p.first[i];
+      if (f >= 0 && (f & 1) == k) line.blocks[f >> 1].cum = -1 - i;
     }
-    b.cum = chunk_sum(stretch, chunk_scan(len, &sum));
-    if (x < blocks) p.blocks[x] = b;
-    stretch = chunk_sum(stretch, sum);
+    __syncthreads();
+    int entry = -1;  // of the last row block of the step before
+    for (int base = 0; base < blocks[k]; base += kSetup) {
+      const int x = base + threadIdx.x;
+      // the last entry that begins at x or before: a maximum over the row blocks so far
+      __shared__ int latest[32];
+      int mine = -1;
+      if (x < blocks[k] && line.blocks[x].cum < 0) mine = -1 - line.blocks[x].cum;
+      const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(~0u, mine, d);
+        if (lane >= d) mine = max(mine, o);
+      }
+      if (lane == 31) latest[w] = mine;
+      __syncthreads();
+      mine = max(mine, entry);
+      for (int o = 0; o < w; ++o) mine = max(mine, latest[o]);
+      int last = entry;
+      for (int o = 0; o < 32; ++o) last = max(last, latest[o]);
+      entry = last;
+      ChunkBlock b = {};
+      int len = 0;
+      if (x < blocks[k]) {
+        const ChunkEntry e = chunk_entry(p, mine);
+        b.seq = e.seq;
+        b.tok0 = e.tok0 + e.gone;
+        b.pos0 = e.pos0;
+        b.row0 = (x - (p.first[mine] >> 1)) * kinds.rows[k];
+        b.rows = min((e.count - e.gone) * G - b.row0, kinds.rows[k]);
+        const ChunkSpan s = chunk_span(b.pos0, b.row0, b.rows, G, p.window);
+        b.tile0 = s.lo / kinds.keys[k];
+        b.tiles = (s.hi + kinds.keys[k] - 1) / kinds.keys[k] - b.tile0;
+        len = b.tiles + kChunkCost;
+      }
+      b.cum = chunk_sum(stretch[k], chunk_scan(len, &sum));
+      if (x < blocks[k]) line.blocks[x] = b;
+      stretch[k] = chunk_sum(stretch[k], sum);
+    }
+    over |= stretch[k] >= kChunkMost || static_cast<int64_t>(stretch[k]) * p.Hkv >= (int64_t{1} << 30);
   }
-  over |= stretch >= kChunkMost || static_cast<int64_t>(stretch) * p.Hkv >= (int64_t{1} << 30);
   if (threadIdx.x == 0) {
-    p.blocks[blocks].cum = stretch;
-    p.head->blocks = blocks;
-    p.head->stretch = stretch;
+    p.tensor.blocks[blocks[0]].cum = stretch[0];
+    p.stream.blocks[blocks[1]].cum = stretch[1];
+    p.head->tensor = ChunkHead::Line{blocks[0], stretch[0]};
+    p.head->stream = ChunkHead::Line{blocks[1], stretch[1]};
     p.head->fill = over ? 2 : any;
     if (over) atomicOr(&p.head->err, kErrChunkLine);
   }
@@ -128,21 +167,106 @@ __global__ void __launch_bounds__(kSetup)
     }
 }
 
-// Units that a cut went through: their parts put together, a warp a row; and the rows to fill.  Block
-// (w, y): the unit that range w + 1 begins in, every gridDim.y-th four rows of it.
+// One row of a cut unit, by a warp: its parts put together.  (Four parts' rows are fetched at once with
+// all the maxima and sums: what is known of them is where they lie.)
+template <bool BF16, int D, int ROWS>
+BSG_DEV void finish_row(const ChunkParams& p, const ChunkLine& line, const ChunkCut& cut, int r, int lane) {
+  constexpr int kPer = D / 32, kVec = kPer < 4 ? kPer : 4;
+  const int G = p.Hq / p.Hkv;
+  const auto slot = [&](int i) {
+    return line.parts + static_cast<int64_t>(i ? cut.next + 2 * (i - 1) : cut.slot0) * chunk_slot_floats(ROWS, D);
+  };
+  const auto fetch = [&](int i, float* v) {
+    const float* row = slot(i) + r * D;
+#pragma unroll
+    for (int x = 0; x < kPer; x += kVec) {
+      const float* at = row + x / kVec * (32 * kVec) + lane * kVec;
+      if constexpr (kVec == 4) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(at));
+        v[x] = f.x;
+        v[x + 1] = f.y;
+        v[x + 2] = f.z;
+        v[x + 3] = f.w;
+      } else {
+        const float2 f = __ldcg(reinterpret_cast<const float2*>(at));
+        v[x] = f.x;
+        v[x + 1] = f.y;
+      }
+    }
+  };
+  float o[kPer] = {}, m = -INFINITY, l = 0.f;
+  for (int i0 = 0; i0 < cut.count; i0 += 32) {
+    const int i = i0 + lane, many = min(32, cut.count - i0);
+    float v[4][kPer];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < many) fetch(i0 + j, v[j]);
+    float mi = -INFINITY, li = 0.f;
+    if (i < cut.count) {
+      const float* part = slot(i);
+      mi = __ldcg(part + ROWS * D + r);
+      li = __ldcg(part + ROWS * (D + 1) + r);
+    }
+    float top = mi;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    const float next = fmaxf(m, top), base = next == -INFINITY ? 0.f : next;
+    const float keep = ex2(m - base);
+    // (only a part without positions has m = -inf: its sums may not be written and do not count)
+    const float take = mi == -INFINITY ? 0.f : ex2(mi - base);
+    float sum = mi == -INFINITY ? 0.f : li * take;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    m = next;
+    l = l * keep + sum;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) o[x] *= keep;
+    const unsigned some = __ballot_sync(0xFFFFFFFFu, mi != -INFINITY);
+    for (int j0 = 0; j0 < many; j0 += 4) {
+      if (j0)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j0 + j < many) fetch(i0 + j0 + j, v[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float t = __shfl_sync(0xFFFFFFFFu, take, (j0 + j) & 31);
+        if (j0 + j < many && (some >> (j0 + j) & 1u))
+#pragma unroll
+          for (int x = 0; x < kPer; ++x) o[x] = fmaf(v[j][x], t, o[x]);
+      }
+    }
+  }
+  const int at = cut.row0 + r, tok = at / G;
+  const int64_t to = static_cast<int64_t>(cut.tok0 + tok) * p.Hq + cut.head * G + at - tok * G;
+  const float inv = 1.f / l;
+#pragma unroll
+  for (int x = 0; x < kPer; x += 2)
+    *reinterpret_cast<uint32_t*>(p.out + to * D + x / kVec * (32 * kVec) + lane * kVec + x % kVec) =
+        AttnStream<BF16, 64>::pack(o[x] * inv, o[x + 1] * inv);
+  if (lane == 0 && p.lse) p.lse[to] = (m + log2f(l)) * 0.6931471805599453f;
+}
+
+constexpr int kFinishStream = 4;    // blocks of four warps for a cut unit: a row a warp,
+constexpr int kFinishTensor = 16;   // and up to four
+
+// Units that a cut went through, and the rows to fill.  Block (w, y): the unit noted by range w + 1 of
+// the streaming kernel (y < kFinishStream) or the tensor-memory kernel, every so many-th four rows.
 template <bool BF16, int D>
-__global__ void __launch_bounds__(128)
-    chunk_finish(const __grid_constant__ ChunkParams p, int workers) {
-  constexpr int kPer = D / 32, kVec = kPer < 4 ? kPer : 4, kRows = D == 256 ? 128 : 256;
+__global__ void __launch_bounds__(128) chunk_finish(const __grid_constant__ ChunkParams p) {
+  constexpr int kRows = D == 256 ? 128 : 256;
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int4 h4 = __ldcg(reinterpret_cast<const int4*>(p.head));
-  const ChunkHead head = {0u, h4.y, h4.z, h4.w};
-  if (head.fill) {
+  const bool stream = blockIdx.y < kFinishStream;
+  const ChunkLine& line = stream ? p.stream : p.tensor;
+  const int4* src = reinterpret_cast<const int4*>(line.cuts + blockIdx.x + 1);
+  const int4 a = __ldcg(src), b = __ldcg(src + 1);
+  const int fill = __ldcg(&p.head->fill);
+  const int blocks = __ldcg(stream ? &p.head->stream.blocks : &p.head->tensor.blocks);
+  if (fill) {
     // zeros for rows without a position, NaN for all where there was too much to count
-    const uint32_t value = head.fill == 1 ? 0u : (BF16 ? 0x7FC07FC0u : 0x7E007E00u);
-    const float lse = head.fill == 1 ? -INFINITY : __int_as_float(0x7FC00000);
+    const uint32_t value = fill == 1 ? 0u : (BF16 ? 0x7FC07FC0u : 0x7E007E00u);
+    const float lse = fill == 1 ? -INFINITY : __int_as_float(0x7FC00000);
     for (int i = blockIdx.y * gridDim.x + blockIdx.x; i < p.n; i += gridDim.x * gridDim.y) {
       const int2 f = __ldcg(p.fills + i);
       const int64_t first = static_cast<int64_t>(f.x) * p.Hq, many = static_cast<int64_t>(f.y) * p.Hq;
@@ -153,148 +277,101 @@ __global__ void __launch_bounds__(128)
         for (int64_t x = threadIdx.x; x < many; x += blockDim.x) p.lse[first + x] = lse;
     }
   }
-  const ChunkSplit s = chunk_split(head, p.Hkv, workers);
-  const int w = blockIdx.x + 1;
-  if (w >= s.workers) return;
-  const int2 cut = __ldcg(p.cuts + w);
-  const int4* src = reinterpret_cast<const int4*>(p.blocks + cut.x);
-  const int4 b0 = __ldcg(src), b1 = __ldcg(src + 1);
-  const int rows = b1.y, row0 = b1.x, len = b1.w + kChunkCost;
-  const int begin = b0.x * p.Hkv + cut.y * len;
-  const int w0 = chunk_owner(s, begin + kChunkCost), w1 = chunk_owner(s, begin + len - 1);
-  if (w != w0 + 1 || w > w1) return;
-  const int G = p.Hq / p.Hkv, count = w1 - w0 + 1;
-  // (the first part lies in its range's first slot only if the range begins with the unit or in it)
-  const int slot0 = 2 * w0 + (begin <= chunk_start(s, w0) ? 0 : 1);
-  for (int r = blockIdx.y * 4 + warp; r < rows; r += gridDim.y * 4) {
-    float o[kPer], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) o[x] = 0.f;
-    for (int i0 = 0; i0 < count; i0 += 32) {
-      const int i = i0 + lane, many = min(32, count - i0);
-      const float* row = nullptr;
-      float mi = -INFINITY, li = 0.f;
-      if (i < count) {
-        const float* part = p.parts + static_cast<int64_t>(i ? 2 * (w0 + i) : slot0) * chunk_slot_floats(D);
-        row = part + r * D;
-        mi = __ldcg(part + kRows * D + r);
-        li = __ldcg(part + kRows * (D + 1) + r);
-      }
-      float top = mi;
-#pragma unroll
-      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-      const float next = fmaxf(m, top), base = next == -INFINITY ? 0.f : next;
-      const float keep = ex2(m - base);
-      // (only a part without positions has m = -inf: its sums are not read)
-      const float take = mi == -INFINITY ? 0.f : ex2(mi - base);
-      float sum = mi == -INFINITY ? 0.f : li * take;
-#pragma unroll
-      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-      m = next;
-      l = l * keep + sum;
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) o[x] *= keep;
-      for (int j0 = 0; j0 < many; j0 += 4) {
-        float v[4][kPer], t[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int from = min(j0 + j, many - 1);
-          const float* row_j = reinterpret_cast<const float*>(
-              __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(row), from));
-          const float mj = __shfl_sync(0xFFFFFFFFu, mi, from);
-          t[j] = __shfl_sync(0xFFFFFFFFu, take, from);
-          const bool some = mj != -INFINITY && j0 + j < many;
-#pragma unroll
-          for (int x = 0; x < kPer; x += kVec) {
-            const float* at = row_j + x / kVec * (32 * kVec) + lane * kVec;
-            if constexpr (kVec == 4) {
-              const float4 f = some ? __ldcg(reinterpret_cast<const float4*>(at)) : make_float4(0.f, 0.f, 0.f, 0.f);
-              v[j][x] = f.x;
-              v[j][x + 1] = f.y;
-              v[j][x + 2] = f.z;
-              v[j][x + 3] = f.w;
-            } else {
-              const float2 f = some ? __ldcg(reinterpret_cast<const float2*>(at)) : make_float2(0.f, 0.f);
-              v[j][x] = f.x;
-              v[j][x + 1] = f.y;
-            }
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int x = 0; x < kPer; ++x) o[x] = fmaf(v[j][x], t[j], o[x]);
-      }
-    }
-    const int at = row0 + r, tok = at / G;
-    const int64_t to = static_cast<int64_t>(b0.z + tok) * p.Hq + cut.y * G + at - tok * G;
-    const float inv = 1.f / l;
-#pragma unroll
-    for (int x = 0; x < kPer; x += kVec) {
-      uint16_t* dst = p.out + to * D + x / kVec * (32 * kVec) + lane * kVec;
-      using A = AttnStream<BF16, 64>;
-      if constexpr (kVec == 4)
-        *reinterpret_cast<uint2*>(dst) =
-            make_uint2(A::pack(o[x] * inv, o[x + 1] * inv), A::pack(o[x + 2] * inv, o[x + 3] * inv));
-      else
-        *reinterpret_cast<uint32_t*>(dst) = A::pack(o[x] * inv, o[x + 1] * inv);
-    }
-    if (lane == 0 && p.lse) p.lse[to] = (m + log2f(l)) * 0.6931471805599453f;
+  if (blocks == 0) return;  // (its kernel may not have run, and has noted nothing then)
+  const ChunkCut cut = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, 0};
+  if (stream) {
+    const int r = blockIdx.y * 4 + warp;
+    if (r < cut.rows) finish_row<BF16, D, kChunkRows>(p, line, cut, r, lane);
+  } else {
+    for (int r = (blockIdx.y - kFinishStream) * 4 + warp; r < cut.rows; r += kFinishTensor * 4)
+      finish_row<BF16, D, kRows>(p, line, cut, r, lane);
   }
 }
 
 template <bool BF16, int D>
 int launch(const ChunkParams& p, const ChunkMaps& maps, int sms, cudaStream_t s) {
-  static AttrRecord rec, extra_rec;
+  static AttrRecord rec[2], extra_rec[2];
   using T = ChunkTile<D>;
-  const int ps = 1 << p.page_log2;
+  using S = ChunkStreamTile<D>;
+  const int ps = 1 << p.page_log2, G = p.Hq / p.Hkv;
   const bool extra = p.cap > 0.f || p.slopes;
-  ChunkTensorParams q;
-  q.tm_k = maps.k;
-  q.tm_v = maps.v;
-  q.a = p;
-  q.box_rows = ps < T::kKeys ? ps : T::kKeys;
-  const auto kernel = extra ? chunk_tensor_kernel<BF16, D, true> : chunk_tensor_kernel<BF16, D, false>;
-  int rc = decode_smem(kernel, extra ? extra_rec : rec, T::kSmem);
+  // one entry of more rows: nothing for the streaming kernel; no more rows in all: nothing for the other
+  const bool tensor = static_cast<int64_t>(p.T) * G > kChunkShort, stream = p.n > 1 || !tensor;
+  const ChunkKinds kinds = {stream ? kChunkShort : 0, {T::kRows, kChunkRows}, {T::kKeys, S::kKeys}};
+  int rc = decode_launch(chunk_setup, dim3(1), dim3(kSetup), 0, s, p, kinds);
   if (rc != BSGEMV_OK) return rc;
-  rc = decode_launch(chunk_setup, dim3(1), dim3(kSetup), 0, s, p, T::kRows, T::kKeys);
-  if (rc != BSGEMV_OK) return rc;
-  rc = decode_launch(kernel, dim3(sms), dim3(T::kThreads), T::kSmem, s, q);
-  if (rc != BSGEMV_OK) return rc;
-  return decode_launch(chunk_finish<BF16, D>, dim3(sms > 1 ? sms - 1 : 1, 16), dim3(128), 0, s, p, sms);
+  if (stream) {
+    ChunkStreamParams q;
+    q.tm_k = maps.stream_k;
+    q.tm_v = maps.stream_v;
+    q.a = p;
+    q.box_rows = ps < S::kKeys ? ps : S::kKeys;
+    const auto kernel = extra ? chunk_stream_kernel<BF16, D, true> : chunk_stream_kernel<BF16, D, false>;
+    rc = decode_smem(kernel, extra ? extra_rec[1] : rec[1], S::kSmem);
+    if (rc != BSGEMV_OK) return rc;
+    rc = decode_launch(kernel, dim3(sms), dim3(32 * kChunkWarps), S::kSmem, s, q);
+    if (rc != BSGEMV_OK) return rc;
+  }
+  if (tensor) {
+    ChunkTensorParams q;
+    q.tm_k = maps.k;
+    q.tm_v = maps.v;
+    q.a = p;
+    q.box_rows = ps < T::kKeys ? ps : T::kKeys;
+    const auto kernel = extra ? chunk_tensor_kernel<BF16, D, true> : chunk_tensor_kernel<BF16, D, false>;
+    rc = decode_smem(kernel, extra ? extra_rec[0] : rec[0], T::kSmem);
+    if (rc != BSGEMV_OK) return rc;
+    rc = decode_launch(kernel, dim3(sms), dim3(T::kThreads), T::kSmem, s, q);
+    if (rc != BSGEMV_OK) return rc;
+  }
+  return decode_launch(chunk_finish<BF16, D>, dim3(sms > 1 ? sms - 1 : 1, kFinishStream + (tensor ? kFinishTensor : 0)),
+                       dim3(128), 0, s, p);
 }
 
 }  // namespace
 
 ChunkLayout chunk_layout(int Hq, int Hkv, int D, int max_n, int max_T, int sms) {
   ChunkLayout l = {};
-  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const int64_t rows = D == 256 ? 128 : 256;
-  l.max_blocks = static_cast<int>((static_cast<int64_t>(max_T) * (Hq / Hkv) + rows - 1) / rows + max_n);
-  l.blocks = 256;
-  l.first = l.blocks + up((static_cast<size_t>(l.max_blocks) + 1) * sizeof(ChunkBlock));
-  l.fills = l.first + up((static_cast<size_t>(max_n) + 1) * 4);
-  l.cuts = l.fills + up(static_cast<size_t>(max_n) * 8);
-  l.parts = l.cuts + up(static_cast<size_t>(sms) * 8);
-  l.total = l.parts + static_cast<size_t>(sms) * 2 * chunk_slot_floats(D) * 4;
+  size_t at = 256;
+  const auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  const int64_t rows = D == 256 ? 128 : 256, G = Hq / Hkv;
+  l.tensor.max_blocks = static_cast<int>((max_T * G + rows - 1) / rows + max_n);
+  l.stream.max_blocks = max_n * (kChunkShort / kChunkRows);
+  for (auto* line : {&l.tensor, &l.stream}) {
+    const int block_rows = line == &l.tensor ? static_cast<int>(rows) : kChunkRows;
+    line->blocks = take((static_cast<size_t>(line->max_blocks) + 1) * sizeof(ChunkBlock));
+    line->cuts = take((static_cast<size_t>(sms) + 1) * sizeof(ChunkCut));
+    line->parts = take(static_cast<size_t>(sms) * 2 * chunk_slot_floats(block_rows, D) * 4);
+  }
+  l.first = take(static_cast<size_t>(max_n) * 4);
+  l.fills = take(static_cast<size_t>(max_n) * 8);
+  l.total = at;
   return l;
 }
 
 bool chunk_encode(const ChunkParams& p, ChunkMaps* m) {
-  const int ps = 1 << p.page_log2, keys = p.D == 256 ? 64 : 128;
+  const int ps = 1 << p.page_log2;
   const uint64_t dims[4] = {static_cast<uint64_t>(p.D), static_cast<uint64_t>(ps),
                             static_cast<uint64_t>(p.Hkv), static_cast<uint64_t>(p.num_pages)};
   // (the stride of a dimension of one is of no account)
   const uint64_t row = p.row_stride * 2;
   const uint64_t strides[3] = {row, p.Hkv > 1 ? p.head_stride * 2 : row * ps,
                                p.num_pages > 1 ? p.page_stride * 2 : row * ps * p.Hkv};
-  const uint32_t box[4] = {64, static_cast<uint32_t>(ps < keys ? ps : keys), 1, 1};
   const CUtensorMapDataType type =
       p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  return decode_encode(&m->k, type, 4, p.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == BSGEMV_OK &&
-         decode_encode(&m->v, type, 4, p.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == BSGEMV_OK;
+  CUtensorMap* const maps[4] = {&m->k, &m->v, &m->stream_k, &m->stream_v};
+  for (int i = 0; i < 4; ++i) {
+    const int keys = i < 2 ? (p.D == 256 ? 64 : 128) : 4096 / p.D;  // positions of a tile
+    const uint32_t box[4] = {64, static_cast<uint32_t>(ps < keys ? ps : keys), 1, 1};
+    if (decode_encode(maps[i], type, 4, i & 1 ? p.v : p.k, dims, strides, box,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) != BSGEMV_OK)
+      return false;
+  }
+  return true;
 }
 
 int launch_chunk(const ChunkParams& p, const ChunkMaps& maps, int sms, cudaStream_t s) {

@@ -1,13 +1,14 @@
-// chunk_kernel.cuh -- parameters, work split and launches of the attention of new tokens over the
-// paged cache.
+// chunk_kernel.cuh -- parameters and launches of the attention of new tokens over the paged cache.
 //
 // The rows of an entry (its tokens x the query heads that share a kv head, token by token) are cut
 // into row blocks; a unit is a row block of one kv head with the key tiles that any of its rows sees.
-// All units' tiles are laid in a line, row blocks outside, heads inside, and the line is cut into
-// equal ranges, one for each block of the device: a unit counts kChunkCost tiles more than it has,
-// what it costs to begin and end one.  What the lengths are is known on the device only, so a kernel
-// of one block writes the row blocks down first (chunk_setup), and another one puts together the
-// units that a cut went through (chunk_finish).
+// Entries of up to kChunkShort rows go to the streaming kernel (chunk_stream.cuh), in row blocks of
+// 16, others to the tensor-memory kernel (chunk_tensor.cuh), in row blocks of 256 (128 at D = 256).
+// Each kernel's units are laid in a line, row blocks outside, heads inside, and the line is cut into
+// equal ranges, one for each of its blocks: a unit counts kChunkCost tiles more than it has, what it
+// costs to begin and end one.  What the lengths are is known on the device only, so a kernel of one
+// block writes the row blocks down first (chunk_setup), and a last one puts together the units that a
+// cut went through (chunk_finish).
 #pragma once
 
 #include <cuda.h>
@@ -20,6 +21,8 @@ namespace bsg {
 constexpr int kChunkCost = 4;
 constexpr int kChunkMost = 1 << 29;     // sums of stretches stop here
 constexpr int kChunkMaxLen = 1 << 30;   // tokens of a sequence that count
+constexpr int kChunkShort = 32;         // rows of an entry that the streaming kernel takes
+constexpr int kChunkRows = 16;          // rows of its row blocks
 
 // Bit of the error word, beside those of waits that ran out: the call's tiles are more than it can
 // count.
@@ -37,12 +40,32 @@ struct alignas(16) ChunkBlock {
   int tiles;    // how many
 };
 
+// A unit that a cut went through, noted by the first block but one that works on it.
+struct alignas(16) ChunkCut {
+  int rows;     // 0: none
+  int tok0, row0, head;
+  int slot0;    // its first part
+  int next;     // its second part; the others follow, every second slot
+  int count;    // parts
+  int pad;
+};
+
+// One kernel's line of work.
+struct ChunkLine {
+  ChunkBlock* blocks;
+  ChunkCut* cuts;       // [blocks of the kernel]
+  float* parts;         // two slots for each of them: its first unit, and its last
+  int max_blocks;       // room for row blocks
+};
+
 // What chunk_setup leaves at the start of the workspace.
 struct ChunkHead {
   unsigned err;   // error word
-  int blocks;     // row blocks
-  int stretch;    // sum of their stretches
   int fill;       // rows to fill: 0 none, 1 with zeros (no position, no sequence), 2 all with NaN
+  struct Line {
+    int blocks;   // row blocks
+    int stretch;  // sum of their stretches
+  } tensor, stream;
 };
 
 struct ChunkParams {
@@ -61,26 +84,28 @@ struct ChunkParams {
   uint16_t* out;
   float* lse;           // may be null
   ChunkHead* head;
-  ChunkBlock* blocks;
-  int max_blocks;       // room for row blocks
-  int* first;           // [n + 1] first row block of each entry
+  ChunkLine tensor, stream;
+  int* first;           // [n] the entries' first row blocks
   int2* fills;          // [n] rows to fill: first, how many
-  int2* cuts;           // [blocks of the device] the unit that a range begins in: row block, head
-  float* parts;         // two slots a range: its first unit, and its last
   uint64_t wait_ns;     // limit of every wait but the drains'
-  int skip;             // test hook: the tile whose copy block 0 leaves out, -1 none
+  int skip[2];          // test hook: the tile whose copy the tensor-memory kernel's first block, or the
+                        // streaming kernel's first warp, leaves out; -1 none
 };
 
 struct ChunkLayout {
-  size_t blocks, first, fills, cuts, parts, total;
-  int max_blocks;
+  size_t first, fills, total;
+  struct Line {
+    size_t blocks, cuts, parts;
+    int max_blocks;
+  } tensor, stream;
 };
 ChunkLayout chunk_layout(int Hq, int Hkv, int D, int max_n, int max_T, int sms);
 
 // Tensor maps of the cache: [page][head][row][D], boxes of 64 d and as many rows as a page and a
-// tile have (false: the strides cannot be described).
+// tile of the kernel have (false: the strides cannot be described).
 struct ChunkMaps {
-  CUtensorMap k, v;
+  CUtensorMap k, v;                // the tensor-memory kernel's
+  CUtensorMap stream_k, stream_v;  // the streaming kernel's
 };
 bool chunk_encode(const ChunkParams& p, ChunkMaps* m);
 

@@ -1,0 +1,101 @@
+// chunk_line.cuh -- the line of work of the two chunk attention kernels, on the device.
+#pragma once
+
+#include "../bsgemv_kernel.cuh"
+#include "chunk_kernel.cuh"
+
+namespace bsg {
+
+BSG_DEV ChunkHead chunk_head(const ChunkParams& p) {
+  const int2* h = reinterpret_cast<const int2*>(p.head);
+  const int2 a = __ldcg(h), b = __ldcg(h + 1), c = __ldcg(h + 2);
+  return ChunkHead{0u, a.y, {b.x, b.y}, {c.x, c.y}};
+}
+
+// A line, cut into ranges.
+struct ChunkSplit {
+  int total, workers, base, extra;
+};
+BSG_DEV ChunkSplit chunk_split(const ChunkHead& h, const ChunkHead::Line& line, int Hkv, int workers) {
+  ChunkSplit s;
+  s.total = h.fill == 2 ? 0 : line.stretch * Hkv;
+  s.workers = min(workers, s.total);
+  s.base = s.workers ? s.total / s.workers : 0;
+  s.extra = s.total - s.base * s.workers;
+  return s;
+}
+BSG_DEV int chunk_start(const ChunkSplit& s, int w) { return w * s.base + min(w, s.extra); }
+BSG_DEV int chunk_owner(const ChunkSplit& s, int x) {
+  const int cut = s.extra * (s.base + 1);
+  return x < cut ? x / (s.base + 1) : s.extra + (x - cut) / s.base;
+}
+
+// Positions that the rows of a block see: [lo, hi), of which [lo_all, hi_all) by all of them.
+struct ChunkSpan {
+  int lo, hi, lo_all, hi_all;
+};
+BSG_DEV int chunk_lo(int pos, int window) { return window > 0 ? max(pos - window + 1, 0) : 0; }
+BSG_DEV ChunkSpan chunk_span(int pos0, int row0, int rows, int G, int window) {
+  const int a = pos0 + row0 / G, b = pos0 + (row0 + rows - 1) / G;
+  return ChunkSpan{chunk_lo(a, window), b + 1, chunk_lo(b, window), a + 1};
+}
+
+// A part: [rows][D] sums, [rows] maxima, [rows] sums of the numerators.
+__host__ __device__ constexpr int chunk_slot_floats(int rows, int D) { return rows * (D + 2); }
+
+BSG_DEV ChunkBlock chunk_block(const ChunkLine& line, int e) {
+  const int4* src = reinterpret_cast<const int4*>(line.blocks + e);
+  const int4 x = __ldcg(src), y = __ldcg(src + 1);
+  return ChunkBlock{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+}
+// Whether place x of the line lies in row block e.
+BSG_DEV bool chunk_holds(const ChunkLine& line, int Hkv, int e, int x) {
+  return __ldcg(&line.blocks[e].cum) * Hkv <= x && __ldcg(&line.blocks[e + 1].cum) * Hkv > x;
+}
+
+// A segment of a range: key tiles t0 .. t0 + n - 1 (of the unit's) of one unit.
+struct ChunkSeg {
+  ChunkBlock b;
+  int e, head;
+  int t0, n;
+  int from, end;      // its stretch of the line
+  bool whole;         // all of the unit's tiles
+};
+BSG_DEV void chunk_place(ChunkSeg& g, int Hkv, int x, int x1) {
+  const int len = g.b.tiles + kChunkCost, begin = g.b.cum * Hkv + g.head * len;
+  const int at = x - begin;
+  g.from = x;
+  g.end = min(begin + len, x1);
+  g.t0 = max(at - kChunkCost, 0);
+  g.n = max(g.end - begin - kChunkCost - g.t0, 0);
+  g.whole = g.n == g.b.tiles;
+}
+BSG_DEV void chunk_first_seg(ChunkSeg& g, const ChunkLine& line, int Hkv, int e0, int x0, int x1) {
+  g.e = e0;
+  g.b = chunk_block(line, e0);
+  g.head = (x0 - g.b.cum * Hkv) / (g.b.tiles + kChunkCost);
+  chunk_place(g, Hkv, x0, x1);
+}
+// The segment after g (g.end < x1).
+BSG_DEV void chunk_next_seg(ChunkSeg& g, const ChunkLine& line, int Hkv, int x1) {
+  if (++g.head == Hkv) {
+    g.head = 0;
+    g.b = chunk_block(line, ++g.e);
+  }
+  chunk_place(g, Hkv, g.end, x1);
+}
+
+// Range w's first segment g: whether a cut went through its unit, noted by the range after the one
+// that has the unit's first tile.
+BSG_DEV void chunk_note_cut(const ChunkLine& line, const ChunkSplit& s, int Hkv, const ChunkSeg& g, int w) {
+  const int len = g.b.tiles + kChunkCost, begin = g.b.cum * Hkv + g.head * len;
+  const int w0 = chunk_owner(s, begin + kChunkCost), w1 = chunk_owner(s, begin + len - 1);
+  ChunkCut c = {};
+  if (w == w0 + 1 && w <= w1)
+    // (the first part lies in its range's first slot if the range begins with the unit or inside it)
+    c = ChunkCut{g.b.rows, g.b.tok0, g.b.row0, g.head, 2 * w0 + (begin <= chunk_start(s, w0) ? 0 : 1),
+                 2 * w, w1 - w0 + 1, 0};
+  line.cuts[w] = c;
+}
+
+}  // namespace bsg

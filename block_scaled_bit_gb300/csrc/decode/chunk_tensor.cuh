@@ -23,7 +23,7 @@
 #pragma once
 
 #include "attn_prefix.cuh"
-#include "chunk_kernel.cuh"
+#include "chunk_line.cuh"
 
 namespace bsg {
 
@@ -54,38 +54,6 @@ struct ChunkTile {
   static_assert(kRing >= 4 && kSmem <= 232448, "shared memory");
   static_assert(kStreams == 1 || 2 * kQB >= 128 * D * 4, "a stream's rows in the queries' place");
 };
-
-__host__ __device__ constexpr int chunk_slot_floats(int D) {
-  return (D == 256 ? 128 : 256) * (D + 2);
-}
-
-// The line, cut into ranges.
-struct ChunkSplit {
-  int total, workers, base, extra;
-};
-BSG_DEV ChunkSplit chunk_split(const ChunkHead& h, int Hkv, int workers) {
-  ChunkSplit s;
-  s.total = h.fill == 2 ? 0 : h.stretch * Hkv;
-  s.workers = min(workers, s.total);
-  s.base = s.workers ? s.total / s.workers : 0;
-  s.extra = s.total - s.base * s.workers;
-  return s;
-}
-BSG_DEV int chunk_start(const ChunkSplit& s, int w) { return w * s.base + min(w, s.extra); }
-BSG_DEV int chunk_owner(const ChunkSplit& s, int x) {
-  const int cut = s.extra * (s.base + 1);
-  return x < cut ? x / (s.base + 1) : s.extra + (x - cut) / s.base;
-}
-
-// Positions that the rows of a block see: [lo, hi), of which [lo_all, hi_all) by all of them.
-struct ChunkSpan {
-  int lo, hi, lo_all, hi_all;
-};
-BSG_DEV int chunk_lo(int pos, int window) { return window > 0 ? max(pos - window + 1, 0) : 0; }
-BSG_DEV ChunkSpan chunk_span(int pos0, int row0, int rows, int G, int window) {
-  const int a = pos0 + row0 / G, b = pos0 + (row0 + rows - 1) / G;
-  return ChunkSpan{chunk_lo(a, window), b + 1, chunk_lo(b, window), a + 1};
-}
 
 struct ChunkTensorParams {
   CUtensorMap tm_k, tm_v;   // [page][head][row][D], boxes of [64 d][box_rows]
@@ -164,13 +132,13 @@ struct ChunkTensor {
     BSG_DEV uint32_t query() const { return bar(kQ); }       // Q written (phase: segment)
     BSG_DEV uint32_t read() const { return bar(kQ + 1); }    // stream 0's scores all done
     BSG_DEV uint32_t joined() const { return bar(kQ + 2); }  // stream 1's rows written
-    BSG_DEV int skip() const { return blockIdx.x == 0 ? p.a.skip : -1; }
+    BSG_DEV int skip() const { return blockIdx.x == 0 ? p.a.skip[0] : -1; }
     static BSG_DEV uint32_t col_s(uint32_t stream, uint32_t j) {
       return (T::kBufs == 2 ? (j & 1u) : stream) * K;
     }
     BSG_DEV uint32_t tile(int i) const { return base_u + T::kOffRing + i * T::kTileB; }
     // 0: tensor memory's address, 1: a wait ran out, 2: tiles sent for, 3: the row block, 4 + stream:
-    // 1 + the job whose O was given values before its first product, 6: whose turn it is to issue
+    // 1 + the job whose O was given values before its first product, 6: a stream is issuing
     BSG_DEV volatile uint32_t* words() const {
       return reinterpret_cast<volatile uint32_t*>(base + T::kOffWords);
     }
@@ -184,53 +152,30 @@ struct ChunkTensor {
     return __all_sync(0xFFFFFFFFu, c.wait(bar, phase));
   }
 
-  // ---- a block's way along its range.  A segment: key tiles t0 .. t0 + n - 1 (of the unit's) of one
-  // unit.
-  struct Seg {
-    ChunkBlock b;
-    int e, head;
-    int t0, n, end;     // end: where its stretch ends in this range
-    int from;           // where it starts
+  // A segment of the block's way along its range.
+  struct Seg : ChunkSeg {
     int lo_all, hi_all; // positions that all of the unit's rows see
     bool pair;          // both streams work on the same rows
-    bool whole;         // all of the unit's tiles
   };
-  static BSG_DEV ChunkBlock load_block(const Ctx& c, int e) {
-    const int4* src = reinterpret_cast<const int4*>(c.p.a.blocks + e);
-    const int4 x = __ldcg(src), y = __ldcg(src + 1);
-    return ChunkBlock{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-  }
-  static BSG_DEV ChunkSpan span(const Ctx& c, const Seg& g, int first, int rows) {
+  static BSG_DEV ChunkSpan span(const Ctx& c, const ChunkSeg& g, int first, int rows) {
     return chunk_span(g.b.pos0, g.b.row0 + first, rows, c.p.a.Hq / c.p.a.Hkv, c.p.a.window);
   }
-  static BSG_DEV void place(const Ctx& c, Seg& g, int x) {
-    const int len = g.b.tiles + kChunkCost, begin = g.b.cum * c.p.a.Hkv + g.head * len;
-    const int at = x - begin;
-    g.from = x;
-    g.end = min(begin + len, c.x1);
-    g.t0 = max(at - kChunkCost, 0);
-    g.n = max(g.end - begin - kChunkCost - g.t0, 0);
+  static BSG_DEV void look(const Ctx& c, Seg& g) {
     g.pair = T::kStreams == 2 && g.b.rows <= 128;
-    g.whole = g.n == g.b.tiles;
     const ChunkSpan s = span(c, g, 0, g.b.rows);
     g.lo_all = s.lo_all;
     g.hi_all = s.hi_all;
   }
   static BSG_DEV Seg first_seg(const Ctx& c) {
     Seg g;
-    g.e = c.e0;
-    g.b = load_block(c, g.e);
-    g.head = (c.x0 - g.b.cum * c.p.a.Hkv) / (g.b.tiles + kChunkCost);
-    place(c, g, c.x0);
+    chunk_first_seg(g, c.p.a.tensor, c.p.a.Hkv, c.e0, c.x0, c.x1);
+    look(c, g);
     return g;
   }
   // The segment after g (g.end < x1).
   static BSG_DEV void next_seg(const Ctx& c, Seg& g) {
-    if (++g.head == c.p.a.Hkv) {
-      g.head = 0;
-      g.b = load_block(c, ++g.e);
-    }
-    place(c, g, g.end);
+    chunk_next_seg(g, c.p.a.tensor, c.p.a.Hkv, c.x1);
+    look(c, g);
   }
 
   // The tiles a .. b - 1 of a segment (from its first) that are a stream's, every step-th.
@@ -401,33 +346,19 @@ struct ChunkTensor {
 
   // The streams' MMAs go to the tensor cores a job at a time: P V of one and the scores of the next.
   // Without that, two streams that are ready together have theirs mixed, both wait for all of them,
-  // and stay in step: the tensor cores then stand still while both softmaxes run.
-  static BSG_DEV bool take_turn(const Ctx& c, bool lead) {
-    bool ok = true;
-    if (T::kStreams == 2) {
-      if (lead) {
-        const uint32_t lock = smem_u32(const_cast<uint32_t*>(c.words() + 6));
-        const auto free = [&] {
-          uint32_t was;
-          asm volatile("atom.acquire.cta.shared::cta.cas.b32 %0, [%1], 0, 1;" : "=r"(was) : "r"(lock) : "memory");
-          return was == 0u;
-        };
-        if (!free()) {
-          const uint64_t t0 = globaltimer_ns();
-          while (!free())
-            if (globaltimer_ns() - t0 > c.p.a.wait_ns) {
-              atomicOr(&c.p.a.head->err, kErrTimeoutFull);
-              ok = false;
-              break;
-            }
-        }
-      }
-      ok = __all_sync(0xFFFFFFFFu, ok);
+  // and stay in step: the tensor cores then stand still while both softmaxes run.  A turn that does not
+  // come in some 10 us is not waited for: nothing but the order depends on it.
+  static BSG_DEV void take_turn(const Ctx& c) {
+    if (T::kStreams == 1) return;
+    const uint32_t lock = smem_u32(const_cast<uint32_t*>(c.words() + 6));
+    for (int i = 0; i < 200; ++i) {
+      uint32_t was;
+      asm volatile("atom.acquire.cta.shared::cta.cas.b32 %0, [%1], 0, 1;" : "=r"(was) : "r"(lock) : "memory");
+      if (was == 0u) return;
     }
-    return ok;
   }
-  static BSG_DEV void end_turn(const Ctx& c, bool lead) {
-    if (T::kStreams == 2 && lead)
+  static BSG_DEV void end_turn(const Ctx& c) {
+    if (T::kStreams == 2)
       asm volatile("st.release.cta.shared::cta.u32 [%0], 0;" ::"r"(smem_u32(const_cast<uint32_t*>(c.words() + 6)))
                    : "memory");
   }
@@ -500,14 +431,14 @@ struct ChunkTensor {
             if (pending && (!wait_warp(c, c.vok(vr.slot), vr.phase) ||
                             !wait_warp(c, c.probs(stream), job & 1u)))
               return false;
-            if (!take_turn(c, lead)) return false;
             tc_after();
             if (lead) {
+              take_turn(c);
               if (pending) products(job, vr.slot);
               scores(job + pending, k_at.slot);
               if (g.pair && g.n > 1 && stream == 0 && t + 2 >= g.n) tc_commit(c.read());
+              end_turn(c);
             }
-            end_turn(c, lead);
             job += pending;
             pending = true;
             vr = v_at;
@@ -515,13 +446,13 @@ struct ChunkTensor {
           if (pending) {
             if (!wait_warp(c, c.vok(vr.slot), vr.phase) || !wait_warp(c, c.probs(stream), job & 1u))
               return false;
-            if (!take_turn(c, lead)) return false;
             tc_after();
             if (lead) {
+              take_turn(c);
               products(job, vr.slot);
               tc_commit(c.out(stream));
+              end_turn(c);
             }
-            end_turn(c, lead);
             ++job;
           }
         }
@@ -622,9 +553,19 @@ struct ChunkTensor {
           x = k >= a && k < b ? x : 0.f;
           y = k + 1 >= a && k + 1 < b ? y : 0.f;
         }
-        out[i] = pack(x, y);
-        out[8 + i] = pack(x - half_to_f32<BF16>(out[i], 0), y - half_to_f32<BF16>(out[i], 1));
-        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[i & 1]) : "l"(f32x2(x, y)));
+        uint64_t rest;
+        if constexpr (BF16) {  // (cut off, not rounded: the upper halves as they are)
+          out[i] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+          rest = f32x2(-__uint_as_float(__float_as_uint(x) & 0xFFFF0000u),
+                       -__uint_as_float(__float_as_uint(y) & 0xFFFF0000u));
+        } else {
+          out[i] = pack(x, y);
+          rest = f32x2(-half_to_f32<BF16>(out[i], 0), -half_to_f32<BF16>(out[i], 1));
+        }
+        const uint64_t xy = f32x2(x, y);
+        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(rest) : "l"(xy));
+        out[8 + i] = pack(f32x2_lo(rest), f32x2_hi(rest));
+        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[i & 1]) : "l"(xy));
       }
       tc_st16(ts + j, out);
     }
@@ -686,7 +627,10 @@ struct ChunkTensor {
     static_assert(sizeof(Seg) <= 80, "their place");
     Counts n = {};
     bool ok = true;
-    if (threadIdx.x == 0) segs[0] = first_seg(c);
+    if (threadIdx.x == 0) {
+      segs[0] = first_seg(c);
+      chunk_note_cut(c.p.a.tensor, c.s, c.p.a.Hkv, segs[0], blockIdx.x);
+    }
     for (int i = 0;; i ^= 1) {
       // everyone is done with the queries of the segment before (a warp whose wait ran out still
       // comes here)
@@ -745,11 +689,13 @@ struct ChunkTensor {
       seen |= a + half * H < K && b + half * H > 0;
       const bool cut = __any_sync(0xFFFFFFFFu, a > 0 || b < H);
       float top = -INFINITY;
+      uint32_t all[H];
+#pragma unroll
+      for (int i = 0; i < H; i += 32) tc_ld32(ts + i, all + i);
+      tc_wait_ld();
 #pragma unroll
       for (int i = 0; i < H; i += 32) {
-        uint32_t raw[32];
-        tc_ld32(ts + i, raw);
-        tc_wait_ld();
+        uint32_t(&raw)[32] = *reinterpret_cast<uint32_t(*)[32]>(all + i);
         if (EXTRA) {
           const float scale_log2 = fabsf(p.scale) * kLog2e, cap_log2 = p.cap * kLog2e;
           const float cap_in = capped ? 2.f * scale_log2 / p.cap : 0.f;
@@ -880,7 +826,8 @@ struct ChunkTensor {
     } else if (g.pair && stream == 1) {
       return true;  // (one tile, stream 0's)
     }
-    float* part = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + (g.from == c.x0 ? 0 : 1)) * chunk_slot_floats(D);
+    float* part = p.tensor.parts + (2 * static_cast<int64_t>(blockIdx.x) + (g.from == c.x0 ? 0 : 1)) *
+                                       chunk_slot_floats(T::kRows, D);
     const int at = (g.pair ? 0 : 128 * stream) + r128;
     const float inv = 1.f / l;
     int64_t mine = -1;  // where the row begins, in bytes; < 0: no row
@@ -987,28 +934,24 @@ struct ChunkTensor {
     if (warp == kMmaWarp) tc_alloc(smem_u32(const_cast<uint32_t*>(c.words())), 512);
     pdl_wait();
     pdl_launch_dependents();
-    const int4 head = __ldcg(reinterpret_cast<const int4*>(p.a.head));
-    c.s = chunk_split(ChunkHead{0u, head.y, head.z, head.w}, p.a.Hkv, gridDim.x);
+    const ChunkHead head = chunk_head(p.a);
+    c.s = chunk_split(head, head.tensor, p.a.Hkv, gridDim.x);
     c.x0 = chunk_start(c.s, blockIdx.x);
     c.x1 = static_cast<int>(blockIdx.x) < c.s.workers ? chunk_start(c.s, blockIdx.x + 1) : c.x0;
     tc_before();
     __syncthreads();
     tc_after();
     c.tmem = c.words()[0];
-    if (c.x1 > c.x0) {
+    if (c.x1 == c.x0) {
+      if (threadIdx.x == 0) p.a.tensor.cuts[blockIdx.x].rows = 0;
+    } else {
       // the row block that x0 lies in
-      for (int e = threadIdx.x; e < head.y; e += T::kThreads) {
-        const int2 x = make_int2(__ldcg(&p.a.blocks[e].cum), __ldcg(&p.a.blocks[e + 1].cum));
-        if (x.x * p.a.Hkv <= c.x0 && x.y * p.a.Hkv > c.x0) c.words()[3] = e;
-      }
+      for (int e = threadIdx.x; e < head.tensor.blocks; e += T::kThreads)
+        if (chunk_holds(p.a.tensor, p.a.Hkv, e, c.x0)) c.words()[3] = e;
       __syncthreads();
       c.e0 = c.words()[3];
       bool ok;
       if (warp < kCopyWarp) {
-        if (threadIdx.x == 0) {  // for chunk_finish
-          const Seg g = first_seg(c);
-          p.a.cuts[blockIdx.x] = make_int2(g.e, g.head);
-        }
         ok = softmax(c, warp / T::kSoft, threadIdx.x % (32 * T::kSoft));
       } else {
         if (warp == kCopyWarp) ok = copy(c, threadIdx.x & 31);

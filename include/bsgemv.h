@@ -507,10 +507,13 @@ int bsgemv_chunk_run(bsgemv_chunk_plan_t plan, const void* q, int64_t q_stride, 
  * BSGEMV_ERR_UNSUPPORTED: a call's key tiles were more than it can count; its out rows are NaN. */
 int bsgemv_chunk_device_status(bsgemv_chunk_plan_t plan, void* stream);
 
-/* Test hook, as bsgemv_plan_set_test_fault: in the plan's next calls the first block leaves out the
- * copy of tile `skip_tile` of its range (K and V tiles in turn; -1: none), and all waits give up after
- * wait_ns (0: the default).  (plan, -1, 0) restores normal calls. */
-int bsgemv_chunk_set_test_fault(bsgemv_chunk_plan_t plan, int skip_tile, int64_t wait_ns);
+/* Test hook, as bsgemv_plan_set_test_fault: in the plan's next calls the first block of the
+ * tensor-memory kernel (kernel 0: K and V tiles in turn) or the first warp of the streaming kernel
+ * (kernel 1: a tile is 4096 / D positions, K and V) leaves out the copy of tile `skip_tile` of its
+ * range (-1: none), and all waits give up after wait_ns (0: the default).  (plan, 0, -1, 0) restores
+ * normal calls. */
+int bsgemv_chunk_set_test_fault(bsgemv_chunk_plan_t plan, int kernel, int skip_tile,
+                                int64_t wait_ns);
 
 /* Free the plan (synchronises the device first).  NULL is a no-op. */
 int bsgemv_chunk_destroy(bsgemv_chunk_plan_t plan);
