@@ -290,11 +290,11 @@ __global__ void __launch_bounds__(128) chunk_finish(const __grid_constant__ Chun
 
 template <bool BF16, int D>
 int launch(const ChunkParams& p, const ChunkMaps& maps, int sms, cudaStream_t s) {
-  static AttrRecord rec[2], extra_rec[2];
+  static AttrRecord tensor_rec[3], stream_rec[2];
   using T = ChunkTile<D>;
   using S = ChunkStreamTile<D>;
   const int ps = 1 << p.page_log2, G = p.Hq / p.Hkv;
-  const bool extra = p.cap > 0.f || p.slopes;
+  const int mode = p.cap > 0.f || p.scale == 0.f ? kChunkAhead : (p.slopes ? kChunkSlopes : kChunkPlain);
   // one entry of more rows: nothing for the streaming kernel; no more rows in all: nothing for the other
   const bool tensor = static_cast<int64_t>(p.T) * G > kChunkShort, stream = p.n > 1 || !tensor;
   const ChunkKinds kinds = {stream ? kChunkShort : 0, {T::kRows, kChunkRows}, {T::kKeys, S::kKeys}};
@@ -306,8 +306,9 @@ int launch(const ChunkParams& p, const ChunkMaps& maps, int sms, cudaStream_t s)
     q.tm_v = maps.stream_v;
     q.a = p;
     q.box_rows = ps < S::kKeys ? ps : S::kKeys;
+    const bool extra = p.cap > 0.f || p.slopes;
     const auto kernel = extra ? chunk_stream_kernel<BF16, D, true> : chunk_stream_kernel<BF16, D, false>;
-    rc = decode_smem(kernel, extra ? extra_rec[1] : rec[1], S::kSmem);
+    rc = decode_smem(kernel, stream_rec[extra], S::kSmem);
     if (rc != BSGEMV_OK) return rc;
     rc = decode_launch(kernel, dim3(sms), dim3(32 * kChunkWarps), S::kSmem, s, q);
     if (rc != BSGEMV_OK) return rc;
@@ -318,8 +319,10 @@ int launch(const ChunkParams& p, const ChunkMaps& maps, int sms, cudaStream_t s)
     q.tm_v = maps.v;
     q.a = p;
     q.box_rows = ps < T::kKeys ? ps : T::kKeys;
-    const auto kernel = extra ? chunk_tensor_kernel<BF16, D, true> : chunk_tensor_kernel<BF16, D, false>;
-    rc = decode_smem(kernel, extra ? extra_rec[0] : rec[0], T::kSmem);
+    const auto kernel = mode == kChunkAhead    ? chunk_tensor_kernel<BF16, D, kChunkAhead>
+                        : mode == kChunkSlopes ? chunk_tensor_kernel<BF16, D, kChunkSlopes>
+                                               : chunk_tensor_kernel<BF16, D, kChunkPlain>;
+    rc = decode_smem(kernel, tensor_rec[mode], T::kSmem);
     if (rc != BSGEMV_OK) return rc;
     rc = decode_launch(kernel, dim3(sms), dim3(T::kThreads), T::kSmem, s, q);
     if (rc != BSGEMV_OK) return rc;

@@ -89,13 +89,22 @@ BSG_DEV void tc_st16(uint32_t addr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
       : "memory");
 }
+// 32 bytes, aligned to as many.
+BSG_DEV void store_sector(void* to, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
 BSG_DEV float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-template <bool BF16, int D, bool EXTRA>
+// What scores are besides scaled products: a bias by distance, or worked out ahead of the rest (capped,
+// or with a scale of 0, which a score of -inf must not meet).
+enum ChunkMode { kChunkPlain = 0, kChunkSlopes = 1, kChunkAhead = 2 };
+
+template <bool BF16, int D, int MODE>
 struct ChunkTensor {
   using T = ChunkTile<D>;
   static constexpr int K = T::kKeys;
@@ -466,35 +475,35 @@ struct ChunkTensor {
   static constexpr int H = K / 2;
   static BSG_DEV uint32_t pack(float a, float b) { return AttnStream<BF16, 64>::pack(a, b); }
 
-  // Query rows of tile `q` of a unit into shared memory (nthr threads, this one `tid`).
+  // Query rows of tile `q` of a unit into shared memory (nthr threads, this one `tid`).  A thread keeps
+  // its column; a row's token is a product with 2^16 / G away, exact for up to 1024 rows of 64 heads.
   static BSG_DEV void load_q(const Ctx& c, const Seg& g, int q, int tid, int nthr) {
     const ChunkParams& a = c.p.a;
-    const int G = a.Hq / a.Hkv;
-    const uint32_t dst = c.base_u + q * T::kQB;
-    const auto place = [&](int i) {
-      const int r = i / (D / 8), ch = i % (D / 8);
-      return (ch / 8) * (128 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-    };
-    for (int i = tid; i < 128 * (D / 8); i += nthr) {
-      const int at = q * 128 + i / (D / 8), row = g.b.row0 + at, tok = row / G;
-      const bool in = at < g.b.rows;  // rows past the last: zeros
-      const uint16_t* src = a.q + (in ? (g.b.tok0 + tok) * a.q_stride +
-                                            static_cast<int64_t>(g.head * G + row - tok * G) * D +
-                                            i % (D / 8) * 8
-                                      : 0);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + place(i)), "l"(src),
-                   "r"(in ? 16 : 0) : "memory");
+    const unsigned G = a.Hq / a.Hkv, inv = (65536u + G - 1) / G;
+    const int tok0 = g.b.row0 / static_cast<int>(G);
+    const unsigned rest = g.b.row0 - tok0 * G;  // heads of that token before the block's first row
+    const int ch = tid % (D / 8);
+    const uint32_t dst = c.base_u + q * T::kQB + (ch / 8) * (128 * 128);
+    const uint16_t* src = a.q + (g.b.tok0 + tok0) * a.q_stride + static_cast<int64_t>(g.head * G) * D + ch * 8;
+#pragma unroll 4
+    for (int r = tid / (D / 8); r < 128; r += nthr / (D / 8)) {
+      const unsigned x = rest + q * 128 + r, tok = x * inv >> 16;
+      const bool in = q * 128 + r < g.b.rows;  // rows past the last: zeros
+      const uint16_t* from = in ? src + tok * a.q_stride + (x - tok * G) * D : a.q;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4)), "l"(from), "r"(in ? 16 : 0) : "memory");
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (a.scale < 0.f) {  // (a negative scale's sign goes into Q)
-      uint8_t* mine = c.base + q * T::kQB;
-      for (int i = tid; i < 128 * (D / 8); i += nthr) {
-        uint4 v = lsh<uint4>(mine + place(i));
+      uint8_t* mine = c.base + q * T::kQB + (ch / 8) * (128 * 128);
+      for (int r = tid / (D / 8); r < 128; r += nthr / (D / 8)) {
+        uint4* at = reinterpret_cast<uint4*>(mine + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+        uint4 v = *at;
         v.x ^= 0x80008000u;
         v.y ^= 0x80008000u;
         v.z ^= 0x80008000u;
         v.w ^= 0x80008000u;
-        *reinterpret_cast<uint4*>(mine + place(i)) = v;
+        *at = v;
       }
     }
     fence_async_shared();
@@ -515,24 +524,90 @@ struct ChunkTensor {
     if (lane == 0) mbar_arrive(bar);
   }
 
-  // The largest of 32 scores; PART: of those from a to b - 1.
-  template <bool PART>
-  static BSG_DEV float max32(const uint32_t (&raw)[32], int a, int b) {
+  // What turns a thread's raw scores into base-2 ones: raw * scale + (off + slope i) for its i-th.
+  struct Lin {
+    float scale, off, slope;
+  };
+  static BSG_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+  }
+  static BSG_DEV uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+  }
+  static BSG_DEV uint64_t pair(uint32_t a, uint32_t b) { return f32x2(__uint_as_float(a), __uint_as_float(b)); }
+
+  // The largest of a thread's scores, base 2.  Those that its row does not see (not a <= i < b) become
+  // -inf where they are, and so do not count after this either; kChunkAhead: all become base-2 scores.
+  static BSG_DEV float look_at(const ChunkParams& p, uint32_t ts, const Lin& f, bool cut, int a, int b) {
+    // all of them at once, but where working on them takes registers
+    constexpr int N = MODE == kChunkAhead ? 32 : H;
     float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const float x = !PART || (i >= a && i < b) ? __uint_as_float(raw[i]) : -INFINITY;
-      const float y = !PART || (i + 1 >= a && i + 1 < b) ? __uint_as_float(raw[i + 1]) : -INFINITY;
-      t[(i >> 1) & 3] = AttnPrefix<BF16, 64>::max3(t[(i >> 1) & 3], x, y);
+    for (int j = 0; j < H; j += N) {
+      uint32_t raw[N];
+#pragma unroll
+      for (int i = 0; i < N; i += 32) tc_ld32(ts + j + i, raw + i);
+      tc_wait_ld();
+      if constexpr (MODE == kChunkAhead) {
+        if (p.cap > 0.f) {
+          // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap))
+          constexpr float kLog2e = 1.4426950408889634f;
+          const float in = 2.f * f.scale / p.cap, top = p.cap * kLog2e;
+          const uint64_t in2 = f32x2(in, in), top2 = f32x2(top, top), two2 = f32x2(-2.f * top, -2.f * top);
+#pragma unroll
+          for (int i = 0; i < N; i += 2) {
+            const uint64_t x = mul_f32x2(pair(raw[i], raw[i + 1]), in2);
+            const uint64_t y = add2(f32x2(ex2(f32x2_lo(x)), ex2(f32x2_hi(x))), f32x2(1.f, 1.f));
+            const uint64_t z = fma2(f32x2(rcp_approx(f32x2_lo(y)), rcp_approx(f32x2_hi(y))), two2, top2);
+            raw[i] = __float_as_uint(f32x2_lo(z));
+            raw[i + 1] = __float_as_uint(f32x2_hi(z));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * f.scale);
+        }
+        if (p.slopes) {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            raw[i] = __float_as_uint(__uint_as_float(raw[i]) + fmaf(f.slope, static_cast<float>(j + i), f.off));
+        }
+      }
+      if (cut) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) raw[i] = j + i < b ? raw[i] : 0xFF800000u;
+        if (p.window > 0) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) raw[i] = j + i >= a ? raw[i] : 0xFF800000u;
+        }
+      }
+      if (MODE == kChunkAhead || cut)
+#pragma unroll
+        for (int i = 0; i < N; i += 32) tc_st32(ts + j + i, raw + i);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        uint64_t x = pair(raw[i], raw[i + 1]);
+        if constexpr (MODE == kChunkSlopes)
+          x = fma2(x, f32x2(f.scale, f.scale),
+                   fma2(f32x2(f.slope, f.slope), f32x2(static_cast<float>(j + i), static_cast<float>(j + i + 1)),
+                        f32x2(f.off, f.off)));
+        t[(i >> 1) & 3] = AttnPrefix<BF16, 64>::max3(t[(i >> 1) & 3], f32x2_lo(x), f32x2_hi(x));
+      }
     }
-    return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+    if (MODE == kChunkAhead || cut) tc_wait_st();
+    const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+    return MODE == kChunkPlain ? top * f.scale : top;
   }
 
-  // A thread's scores to numerators 2^(scale s - base), each 16 in their own place, in two parts:
-  // rounded to V's type, and what the rounding left (why: attn_prefix.cuh).  Their sum.
-  template <bool PART>
-  static BSG_DEV float numerators(uint32_t ts, float scale, float base, int a, int b) {
-    const uint64_t sc = f32x2(scale, scale), mb = f32x2(-base, -base);
+  // A thread's scores to numerators 2^(score - base), each 16 in their own place, in two parts: rounded
+  // to V's type (bf16: cut off), and what that left (why: attn_prefix.cuh).  Their sum.
+  static BSG_DEV float numerators(uint32_t ts, const Lin& f, float base) {
+    const uint64_t sc = f32x2(f.scale, f.scale), sl = f32x2(f.slope, f.slope);
+    const float less = MODE == kChunkSlopes ? f.off - base : -base;
+    const uint64_t mb = f32x2(less, less);
     uint64_t sum[2] = {0ull, 0ull};
     uint32_t raw[2][16];
     tc_ld16(ts, raw[0]);
@@ -544,28 +619,24 @@ struct ChunkTensor {
       uint32_t out[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int k = j + 2 * i;
+        const uint64_t x = pair(s[2 * i], s[2 * i + 1]);
         uint64_t e;
-        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e)
-            : "l"(f32x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]))), "l"(sc), "l"(mb));
-        float x = ex2(f32x2_lo(e)), y = ex2(f32x2_hi(e));
-        if (PART) {
-          x = k >= a && k < b ? x : 0.f;
-          y = k + 1 >= a && k + 1 < b ? y : 0.f;
-        }
+        if constexpr (MODE == kChunkPlain) e = fma2(x, sc, mb);
+        else if constexpr (MODE == kChunkAhead) e = add2(x, mb);
+        else e = fma2(x, sc, fma2(sl, f32x2(static_cast<float>(j + 2 * i), static_cast<float>(j + 2 * i + 1)), mb));
+        const uint64_t xy = f32x2(ex2(f32x2_lo(e)), ex2(f32x2_hi(e)));
+        const uint32_t ux = __float_as_uint(f32x2_lo(xy)), uy = __float_as_uint(f32x2_hi(xy));
         uint64_t rest;
-        if constexpr (BF16) {  // (cut off, not rounded: the upper halves as they are)
-          out[i] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-          rest = f32x2(-__uint_as_float(__float_as_uint(x) & 0xFFFF0000u),
-                       -__uint_as_float(__float_as_uint(y) & 0xFFFF0000u));
+        if constexpr (BF16) {
+          out[i] = __byte_perm(ux, uy, 0x7632);
+          rest = pair((ux & 0xFFFF0000u) ^ 0x80000000u, (uy & 0xFFFF0000u) ^ 0x80000000u);
         } else {
-          out[i] = pack(x, y);
+          out[i] = pack(f32x2_lo(xy), f32x2_hi(xy));
           rest = f32x2(-half_to_f32<BF16>(out[i], 0), -half_to_f32<BF16>(out[i], 1));
         }
-        const uint64_t xy = f32x2(x, y);
-        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(rest) : "l"(xy));
+        rest = add2(rest, xy);
         out[8 + i] = pack(f32x2_lo(rest), f32x2_hi(rest));
-        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[i & 1]) : "l"(xy));
+        sum[i & 1] = add2(sum[i & 1], xy);
       }
       tc_st16(ts + j, out);
     }
@@ -664,15 +735,14 @@ struct ChunkTensor {
     }
     const Jobs my = jobs_of(c, g, stream);
     const int first = g.b.tile0 + g.t0;
+    constexpr float kLog2e = 1.4426950408889634f;
     float slope = 0.f;  // base 2
     int pos;            // the row's
     {
       const Row row = row_of(c, g, (g.pair ? 0 : 128 * stream) + (tid & 127));
       pos = g.b.pos0 + row.tok;
-      if (EXTRA && p.slopes) slope = __ldg(p.slopes + row.head) * 1.4426950408889634f;
+      if (MODE != kChunkPlain && p.slopes) slope = __ldg(p.slopes + row.head) * kLog2e;
     }
-    constexpr float kLog2e = 1.4426950408889634f;
-    const bool capped = EXTRA && p.cap > 0.f;
     // this thread's word for its row's other one, and that one's for it
     float* tell = reinterpret_cast<float*>(c.base + T::kOffTell) + stream * 256;
     float m = -INFINITY, l = 0.f;  // m: the maximum that O and l are scaled to; l: of its positions
@@ -682,42 +752,17 @@ struct ChunkTensor {
       if (!wait_warp(c, c.scores(stream, n.job), Ctx::scores_phase(n.job))) return false;
       tc_after();
       const uint32_t ts = c.tmem + Ctx::col_s(stream, n.job) + lanes + half * H;  // its scores
-      // score, base 2 = scale * raw (EXTRA: raw is turned into it first)
-      const float scale = EXTRA ? 1.f : fabsf(p.scale) * kLog2e;
       const int at0 = tile * K + half * H;  // this thread's first position
       const int a = chunk_lo(pos, p.window) - at0, b = pos + 1 - at0;  // those that the row sees: a .. b - 1
       seen |= a + half * H < K && b + half * H > 0;
       const bool cut = __any_sync(0xFFFFFFFFu, a > 0 || b < H);
-      float top = -INFINITY;
-      uint32_t all[H];
-#pragma unroll
-      for (int i = 0; i < H; i += 32) tc_ld32(ts + i, all + i);
-      tc_wait_ld();
-#pragma unroll
-      for (int i = 0; i < H; i += 32) {
-        uint32_t(&raw)[32] = *reinterpret_cast<uint32_t(*)[32]>(all + i);
-        if (EXTRA) {
-          const float scale_log2 = fabsf(p.scale) * kLog2e, cap_log2 = p.cap * kLog2e;
-          const float cap_in = capped ? 2.f * scale_log2 / p.cap : 0.f;
-          const float off = static_cast<float>(at0 + i - pos);
-#pragma unroll
-          for (int y = 0; y < 32; ++y) {
-            float x = __uint_as_float(raw[y]);
-            // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap))
-            if (capped) x = fmaf(-2.f * cap_log2, rcp_approx(1.f + ex2(x * cap_in)), cap_log2);
-            else x *= scale_log2;
-            raw[y] = __float_as_uint(fmaf(slope, off + static_cast<float>(y), x));
-          }
-          tc_st32(ts + i, raw);
-        }
-        top = fmaxf(top, cut ? max32<true>(raw, a - i, b - i) : max32<false>(raw, 0, 32));
-      }
-      if (EXTRA) tc_wait_st();
+      const Lin f = {fabsf(p.scale) * kLog2e, MODE == kChunkPlain ? 0.f : slope * static_cast<float>(at0 - pos), slope};
+      float top = look_at(p, ts, f, cut, a, b);
       // the other half's
       tell[tid] = top;
       arrive_warp(c.both(stream, quad), lane);
       if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
-      top = fmaxf(top, tell[tid ^ 128]) * scale;
+      top = fmaxf(top, tell[tid ^ 128]);
       // O and l move to a new maximum when it is more than 8 above theirs (or the first)
       const bool grow = top > m + 8.f;
       if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -743,7 +788,7 @@ struct ChunkTensor {
         }
       }
       const float base = m == -INFINITY ? 0.f : m;
-      l += cut ? numerators<true>(ts, scale, base, a, b) : numerators<false>(ts, scale, base, 0, H);
+      l += numerators(ts, f, base);
       tc_wait_st();
       // (two buffers: in step with the barrier's phases; one: these scores came after that product)
       if (T::kBufs == 2 && t != my.a && !wait_warp(c, c.out(stream), (n.job - 1) & 1u)) return false;
@@ -791,7 +836,7 @@ struct ChunkTensor {
   static BSG_DEV bool finish(const Ctx& c, const Seg& g, int stream, int tid, uint32_t jobs,
                              uint32_t to, float m, float l, uint32_t joins, bool join) {
     const ChunkParams& p = c.p.a;
-    const int warp = tid >> 5, lane = tid & 31, half = tid >> 7, r128 = tid & 127;
+    const int lane = tid & 31, half = tid >> 7, r128 = tid & 127;
     const int d0 = half * (D / 2), d1 = d0 + D / 2;
     bool has0 = true, has1 = false;  // the streams' sums that count, and their weights
     float w0 = 1.f, w1 = 0.f;
@@ -843,12 +888,13 @@ struct ChunkTensor {
       }
     }
     if (jobs == 0) return true;  // (a part without tiles: nothing of it is read but m)
-    // A thread holds a row; through shared memory, 64 bytes at a time, into whole sectors.  Row i of a
-    // warp's 32 lies at line i / 2: in the stream's query tile, or where the columns just read lay.
-    uint8_t* dst = g.whole ? reinterpret_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(part);
+    // a thread writes its row's columns, 32 bytes (a sector) at a time
+    uint8_t* dst = (g.whole ? reinterpret_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(part)) + mine;
+    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
 #pragma unroll 1
     for (int i = d0; i < d1; i += 32) {
       uint32_t o[32];
+      __syncwarp();
       tc_ld32(to + i, o);
       tc_wait_ld();
       if (join) {
@@ -857,46 +903,23 @@ struct ChunkTensor {
           const float x = has0 ? __uint_as_float(o[y]) * w0 : 0.f;
           o[y] = __float_as_uint(has1 ? fmaf(other[(i + y) * 128 + r128], w1, x) : x);
         }
-        __syncwarp();
       }
-      uint8_t* stage = join ? c.base + i * 512 + (warp & 3) * 128
-                            : c.base + (g.pair ? 0 : stream) * T::kQB + warp * 2048;
-      const int line = join ? 512 : 128;
-      const auto put = [&](const uint4& v, int y) {
-        *reinterpret_cast<uint4*>(stage + (lane >> 1) * line + (lane & 1) * 64 +
-                                  ((y ^ ((lane >> 1) & 3)) << 4)) = v;
-      };
-      const auto send = [&](int64_t more) {
-        __syncwarp();
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int r = 8 * y + (lane >> 2), ch = lane & 3;
-          const int64_t to_r = __shfl_sync(0xFFFFFFFFu, mine, r);
-          const uint4 v = lsh<uint4>(stage + (r >> 1) * line + (r & 1) * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
-          if (to_r >= 0) __stcg(reinterpret_cast<uint4*>(dst + to_r + more + 16 * ch), v);
-        }
-        __syncwarp();
-      };
+      if (mine < 0) continue;
       if (g.whole) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t h[4];
+        for (int y = 0; y < 16; ++y)
+          o[y] = pack(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv);
+        if (wide) {
+          store_sector(dst + 2 * i, o);
+          store_sector(dst + 2 * i + 32, o + 8);
+        } else {
 #pragma unroll
-          for (int z = 0; z < 4; ++z)
-            h[z] = pack(__uint_as_float(o[8 * y + 2 * z]) * inv, __uint_as_float(o[8 * y + 2 * z + 1]) * inv);
-          put(make_uint4(h[0], h[1], h[2], h[3]), y);
+          for (int y = 0; y < 16; y += 4)
+            __stcg(reinterpret_cast<uint4*>(dst + 2 * i + 4 * y), make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]));
         }
-        send(2 * i);
       } else {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint32_t* v = o + 16 * x + 4 * y;
-            put(make_uint4(v[0], v[1], v[2], v[3]), y);
-          }
-          send(4 * (i + 16 * x));
-        }
+        for (int y = 0; y < 32; y += 8) store_sector(dst + 4 * i + 4 * y, o + y);
       }
     }
     return true;
@@ -972,10 +995,10 @@ struct ChunkTensor {
   }
 };
 
-template <bool BF16, int D, bool EXTRA>
+template <bool BF16, int D, int MODE>
 __global__ void __launch_bounds__(ChunkTile<D>::kThreads, 1)
     chunk_tensor_kernel(const __grid_constant__ ChunkTensorParams p) {
-  ChunkTensor<BF16, D, EXTRA>::block(p);
+  ChunkTensor<BF16, D, MODE>::block(p);
 }
 
 }  // namespace bsg
