@@ -149,7 +149,6 @@ int bsgemv_chunk_run(bsgemv_chunk_plan_t plan, const void* q, int64_t q_stride, 
     line.parts = reinterpret_cast<float*>(ws + at.parts);
     line.max_blocks = at.max_blocks;
   }
-  p.first = reinterpret_cast<int*>(ws + plan->at.first);
   p.fills = reinterpret_cast<int2*>(ws + plan->at.fills);
   p.wait_ns = plan->fault_wait_ns ? plan->fault_wait_ns : kDefaultWaitNs;
   p.skip[0] = plan->fault_skip[0];

@@ -9,33 +9,34 @@ namespace {
 constexpr int kSetup = 1024;
 
 BSG_DEV int chunk_sum(int a, int b) { return min(a + b, kChunkMost); }
+BSG_DEV int2 chunk_sum(int2 a, int2 b) { return make_int2(chunk_sum(a.x, b.x), chunk_sum(a.y, b.y)); }
+BSG_DEV int2 shift_up(int2 v, int d) {
+  return make_int2(__shfl_up_sync(~0u, v.x, d), __shfl_up_sync(~0u, v.y, d));
+}
 
-// Exclusive prefix sum over the block of kSetup threads, stopping at kChunkMost; total in *sum.
-BSG_DEV int chunk_scan(int v, int* sum) {
-  __shared__ int warp_sum[32];
+// Exclusive prefix sums over the block of kSetup threads, stopping at kChunkMost; totals in *sum.
+BSG_DEV int2 chunk_scan(int2 v, int2* sum) {
+  __shared__ int2 warp_sum[32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int inc = v;
+  int2 inc = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(~0u, inc, d);
+    const int2 o = shift_up(inc, d);
     if (lane >= d) inc = chunk_sum(inc, o);
   }
-  int before = __shfl_up_sync(~0u, inc, 1);
-  if (lane == 0) before = 0;
+  int2 before = shift_up(inc, 1);
+  if (lane == 0) before = make_int2(0, 0);
   if (lane == 31) warp_sum[w] = inc;
   __syncthreads();
-  if (w == 0) {
-    int s = warp_sum[lane];
+  int2 s = warp_sum[lane];  // (every warp works the warps' sums out)
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(~0u, s, d);
-      if (lane >= d) s = chunk_sum(s, o);
-    }
-    warp_sum[lane] = s;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int2 o = shift_up(s, d);
+    if (lane >= d) s = chunk_sum(s, o);
   }
-  __syncthreads();
-  *sum = warp_sum[31];
-  before = chunk_sum(before, w ? warp_sum[w - 1] : 0);
+  *sum = make_int2(__shfl_sync(~0u, s.x, 31), __shfl_sync(~0u, s.y, 31));
+  const int2 front = make_int2(__shfl_sync(~0u, s.x, (w - 1) & 31), __shfl_sync(~0u, s.y, (w - 1) & 31));
+  if (w) before = chunk_sum(before, front);
   __syncthreads();
   return before;
 }
@@ -64,99 +65,91 @@ BSG_DEV ChunkEntry chunk_entry(const ChunkParams& p, int i) {
 }
 
 // The lines of work, by one block.  short_rows: entries of up to this many rows go to the streaming
-// kernel.
+// kernel.  Index 0: tensor-memory kernel, 1: streaming kernel.
 struct ChunkKinds {
   int short_rows;
-  int rows[2], keys[2];   // of a row block and a key tile: tensor-memory kernel, streaming kernel
+  int rows[2], keys[2];   // of a row block and a key tile
 };
 
+// 1024 entries at a time: what they are into shared memory, sums of their row blocks, then the row
+// blocks, 1024 of a line at a time, each of which finds its entry by halving.
 __global__ void __launch_bounds__(kSetup)
     chunk_setup(const __grid_constant__ ChunkParams p, const __grid_constant__ ChunkKinds kinds) {
+  __shared__ int seq[kSetup], tok0[kSetup], pos0[kSetup], rows[kSetup], first[2][kSetup];
   pdl_wait();
   pdl_launch_dependents();
   const int G = p.Hq / p.Hkv;
-  const auto kind_of = [&](int64_t rows) { return rows <= kinds.short_rows ? 1 : 0; };
-  int total[2] = {0, 0}, sum, any = 0;
+  int2 total = make_int2(0, 0), stretch = total, sum;
+  int any = 0;
+  bool over = false;
   for (int base = 0; base < p.n; base += kSetup) {
-    const int i = base + threadIdx.x;
-    int need = 0, kind = 0;
+    const int i = base + threadIdx.x, many = min(p.n - base, kSetup);
+    int2 need = make_int2(0, 0);
     if (i < p.n) {
       const ChunkEntry e = chunk_entry(p, i);
-      const int64_t rows = static_cast<int64_t>(e.count - e.gone) * G;
-      kind = kind_of(rows);
-      need = static_cast<int>((rows + kinds.rows[kind] - 1) / kinds.rows[kind]);
+      const int64_t live = static_cast<int64_t>(e.count - e.gone) * G;
+      const bool few = live <= kinds.short_rows;
+      (few ? need.y : need.x) = static_cast<int>((live + kinds.rows[few] - 1) / kinds.rows[few]);
       any |= e.gone > 0;
       p.fills[i] = make_int2(e.tok0, e.gone);
+      seq[threadIdx.x] = e.seq;
+      tok0[threadIdx.x] = e.tok0 + e.gone;
+      pos0[threadIdx.x] = e.pos0;
+      rows[threadIdx.x] = static_cast<int>(live);  // (T * Hq is below 2^28)
     }
-    int before = 0;
+    const int2 before = chunk_sum(total, chunk_scan(need, &sum));
+    const int2 after = chunk_sum(total, sum);
+    first[0][threadIdx.x] = before.x;
+    first[1][threadIdx.x] = before.y;
+    __syncthreads();
+    over |= after.x > p.tensor.max_blocks || after.y > p.stream.max_blocks;  // (entries on the same rows)
+    if (over) break;
+    const int steps = max(after.x - total.x, after.y - total.y);
+    for (int s0 = 0; s0 < steps; s0 += kSetup) {
+      int2 len = make_int2(0, 0);
+      ChunkBlock b[2] = {};
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int at = chunk_sum(total[k], chunk_scan(kind == k ? need : 0, &sum));
-      if (kind == k) before = at;
-      total[k] = chunk_sum(total[k], sum);
+      for (int k = 0; k < 2; ++k) {
+        const int x = (k ? total.y : total.x) + s0 + threadIdx.x;
+        if (x >= (k ? after.y : after.x)) continue;
+        int lo = 0, hi = many;  // the last entry with first <= x
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (first[k][mid] <= x) lo = mid;
+          else hi = mid;
+        }
+        b[k].seq = seq[lo];
+        b[k].tok0 = tok0[lo];
+        b[k].pos0 = pos0[lo];
+        b[k].row0 = (x - first[k][lo]) * kinds.rows[k];
+        b[k].rows = min(rows[lo] - b[k].row0, kinds.rows[k]);
+        const ChunkSpan s = chunk_span(b[k].pos0, b[k].row0, b[k].rows, G, p.window);
+        b[k].tile0 = s.lo / kinds.keys[k];
+        b[k].tiles = (s.hi + kinds.keys[k] - 1) / kinds.keys[k] - b[k].tile0;
+        (k ? len.y : len.x) = b[k].tiles + kChunkCost;
+      }
+      const int2 cum = chunk_sum(stretch, chunk_scan(len, &sum));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int x = (k ? total.y : total.x) + s0 + threadIdx.x;
+        if (x >= (k ? after.y : after.x)) continue;
+        b[k].cum = k ? cum.y : cum.x;
+        (k ? p.stream : p.tensor).blocks[x] = b[k];
+      }
+      stretch = chunk_sum(stretch, sum);
     }
-    if (i < p.n) p.first[i] = need ? 2 * before + kind : -1;
+    total = after;
   }
   any = __syncthreads_or(any);
-  bool over = total[0] > p.tensor.max_blocks || total[1] > p.stream.max_blocks;  // (entries on the same rows)
-  int stretch[2] = {0, 0}, blocks[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const ChunkLine& line = k ? p.stream : p.tensor;
-    blocks[k] = over ? 0 : total[k];
-    // each entry leaves its number at its first row block, the blocks after it find it there
-    for (int x = threadIdx.x; x < blocks[k]; x += kSetup) line.blocks[x].cum = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.n && blocks[k]; i += kSetup) {
-      const int f = p.first[i];
-      if (f >= 0 && (f & 1) == k) line.blocks[f >> 1].cum = -1 - i;
-    }
-    __syncthreads();
-    int entry = -1;  // of the last row block of the step before
-    for (int base = 0; base < blocks[k]; base += kSetup) {
-      const int x = base + threadIdx.x;
-      // the last entry that begins at x or before: a maximum over the row blocks so far
-      __shared__ int latest[32];
-      int mine = -1;
-      if (x < blocks[k] && line.blocks[x].cum < 0) mine = -1 - line.blocks[x].cum;
-      const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(~0u, mine, d);
-        if (lane >= d) mine = max(mine, o);
-      }
-      if (lane == 31) latest[w] = mine;
-      __syncthreads();
-      mine = max(mine, entry);
-      for (int o = 0; o < w; ++o) mine = max(mine, latest[o]);
-      int last = entry;
-      for (int o = 0; o < 32; ++o) last = max(last, latest[o]);
-      entry = last;
-      ChunkBlock b = {};
-      int len = 0;
-      if (x < blocks[k]) {
-        const ChunkEntry e = chunk_entry(p, mine);
-        b.seq = e.seq;
-        b.tok0 = e.tok0 + e.gone;
-        b.pos0 = e.pos0;
-        b.row0 = (x - (p.first[mine] >> 1)) * kinds.rows[k];
-        b.rows = min((e.count - e.gone) * G - b.row0, kinds.rows[k]);
-        const ChunkSpan s = chunk_span(b.pos0, b.row0, b.rows, G, p.window);
-        b.tile0 = s.lo / kinds.keys[k];
-        b.tiles = (s.hi + kinds.keys[k] - 1) / kinds.keys[k] - b.tile0;
-        len = b.tiles + kChunkCost;
-      }
-      b.cum = chunk_sum(stretch[k], chunk_scan(len, &sum));
-      if (x < blocks[k]) line.blocks[x] = b;
-      stretch[k] = chunk_sum(stretch[k], sum);
-    }
-    over |= stretch[k] >= kChunkMost || static_cast<int64_t>(stretch[k]) * p.Hkv >= (int64_t{1} << 30);
-  }
+  over |= max(stretch.x, stretch.y) >= kChunkMost ||
+          static_cast<int64_t>(max(stretch.x, stretch.y)) * p.Hkv >= (int64_t{1} << 30);
   if (threadIdx.x == 0) {
-    p.tensor.blocks[blocks[0]].cum = stretch[0];
-    p.stream.blocks[blocks[1]].cum = stretch[1];
-    p.head->tensor = ChunkHead::Line{blocks[0], stretch[0]};
-    p.head->stream = ChunkHead::Line{blocks[1], stretch[1]};
+    if (!over) {
+      p.tensor.blocks[total.x].cum = stretch.x;
+      p.stream.blocks[total.y].cum = stretch.y;
+    }
+    p.head->tensor = ChunkHead::Line{over ? 0 : total.x, stretch.x};
+    p.head->stream = ChunkHead::Line{over ? 0 : total.y, stretch.y};
     p.head->fill = over ? 2 : any;
     if (over) atomicOr(&p.head->err, kErrChunkLine);
   }
@@ -246,18 +239,18 @@ BSG_DEV void finish_row(const ChunkParams& p, const ChunkLine& line, const Chunk
   if (lane == 0 && p.lse) p.lse[to] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
-constexpr int kFinishStream = 4;    // blocks of four warps for a cut unit: a row a warp,
-constexpr int kFinishTensor = 16;   // and up to four
+constexpr int kFinishWarps = 16;    // a block: a row a warp of the streaming kernel's units,
+constexpr int kFinishBlocks = 4;    // and so many blocks for one of the other's
 
 // Units that a cut went through, and the rows to fill.  Block (w, y): the unit noted by range w + 1 of
-// the streaming kernel (y < kFinishStream) or the tensor-memory kernel, every so many-th four rows.
+// the streaming kernel (y = 0) or the tensor-memory kernel, every so many-th row of it.
 template <bool BF16, int D>
-__global__ void __launch_bounds__(128) chunk_finish(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(32 * kFinishWarps) chunk_finish(const __grid_constant__ ChunkParams p) {
   constexpr int kRows = D == 256 ? 128 : 256;
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool stream = blockIdx.y < kFinishStream;
+  const bool stream = blockIdx.y == 0;
   const ChunkLine& line = stream ? p.stream : p.tensor;
   const int4* src = reinterpret_cast<const int4*>(line.cuts + blockIdx.x + 1);
   const int4 a = __ldcg(src), b = __ldcg(src + 1);
@@ -280,13 +273,13 @@ __global__ void __launch_bounds__(128) chunk_finish(const __grid_constant__ Chun
   if (blocks == 0) return;  // (its kernel may not have run, and has noted nothing then)
   const ChunkCut cut = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, 0};
   if (stream) {
-    const int r = blockIdx.y * 4 + warp;
-    if (r < cut.rows) finish_row<BF16, D, kChunkRows>(p, line, cut, r, lane);
+    if (warp < cut.rows) finish_row<BF16, D, kChunkRows>(p, line, cut, warp, lane);
   } else {
-    for (int r = (blockIdx.y - kFinishStream) * 4 + warp; r < cut.rows; r += kFinishTensor * 4)
+    for (int r = (blockIdx.y - 1) * kFinishWarps + warp; r < cut.rows; r += kFinishBlocks * kFinishWarps)
       finish_row<BF16, D, kRows>(p, line, cut, r, lane);
   }
 }
+static_assert(kFinishWarps == kChunkRows, "a warp for each row of a streaming unit");
 
 template <bool BF16, int D>
 int launch(const ChunkParams& p, const ChunkMaps& maps, int sms, cudaStream_t s) {
@@ -327,8 +320,8 @@ int launch(const ChunkParams& p, const ChunkMaps& maps, int sms, cudaStream_t s)
     rc = decode_launch(kernel, dim3(sms), dim3(T::kThreads), T::kSmem, s, q);
     if (rc != BSGEMV_OK) return rc;
   }
-  return decode_launch(chunk_finish<BF16, D>, dim3(sms > 1 ? sms - 1 : 1, kFinishStream + (tensor ? kFinishTensor : 0)),
-                       dim3(128), 0, s, p);
+  return decode_launch(chunk_finish<BF16, D>, dim3(sms > 1 ? sms - 1 : 1, 1 + (tensor ? kFinishBlocks : 0)),
+                       dim3(32 * kFinishWarps), 0, s, p);
 }
 
 }  // namespace
@@ -350,7 +343,6 @@ ChunkLayout chunk_layout(int Hq, int Hkv, int D, int max_n, int max_T, int sms) 
     line->cuts = take((static_cast<size_t>(sms) + 1) * sizeof(ChunkCut));
     line->parts = take(static_cast<size_t>(sms) * 2 * chunk_slot_floats(block_rows, D) * 4);
   }
-  l.first = take(static_cast<size_t>(max_n) * 4);
   l.fills = take(static_cast<size_t>(max_n) * 8);
   l.total = at;
   return l;

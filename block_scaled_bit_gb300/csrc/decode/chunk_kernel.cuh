@@ -85,7 +85,6 @@ struct ChunkParams {
   float* lse;           // may be null
   ChunkHead* head;
   ChunkLine tensor, stream;
-  int* first;           // [n] the entries' first row blocks
   int2* fills;          // [n] rows to fill: first, how many
   uint64_t wait_ns;     // limit of every wait but the drains'
   int skip[2];          // test hook: the tile whose copy the tensor-memory kernel's first block, or the
@@ -93,7 +92,7 @@ struct ChunkParams {
 };
 
 struct ChunkLayout {
-  size_t first, fills, total;
+  size_t fills, total;
   struct Line {
     size_t blocks, cuts, parts;
     int max_blocks;

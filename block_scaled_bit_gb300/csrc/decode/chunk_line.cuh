@@ -48,9 +48,44 @@ BSG_DEV ChunkBlock chunk_block(const ChunkLine& line, int e) {
   const int4 x = __ldcg(src), y = __ldcg(src + 1);
   return ChunkBlock{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 }
-// Whether place x of the line lies in row block e.
-BSG_DEV bool chunk_holds(const ChunkLine& line, int Hkv, int e, int x) {
-  return __ldcg(&line.blocks[e].cum) * Hkv <= x && __ldcg(&line.blocks[e + 1].cum) * Hkv > x;
+
+// Where a kernel's block begins in its line: its range [x0, x1), and in `note` (nine words of shared
+// memory) the number and the contents of the row block that x0 lies in.  By all its threads.  The first
+// row blocks are fetched with the line's length, before that says whether they are.
+struct ChunkRange {
+  ChunkSplit s;
+  int x0, x1;
+};
+BSG_DEV ChunkRange chunk_range(const ChunkParams& p, const ChunkLine& line, bool tensor, volatile int* note) {
+  ChunkRange r = {};
+  int e = threadIdx.x;
+  ChunkBlock b = {};
+  int next = 0;
+  const auto fetch = [&] {
+    if (e < line.max_blocks) {
+      b = chunk_block(line, e);
+      next = __ldcg(&line.blocks[e + 1].cum);
+    }
+  };
+  fetch();
+  const ChunkHead head = chunk_head(p);
+  const ChunkHead::Line& mine = tensor ? head.tensor : head.stream;
+  r.s = chunk_split(head, mine, p.Hkv, gridDim.x);
+  r.x0 = chunk_start(r.s, blockIdx.x);
+  r.x1 = static_cast<int>(blockIdx.x) < r.s.workers ? chunk_start(r.s, blockIdx.x + 1) : r.x0;
+  if (r.x0 == r.x1) return r;
+  while (true) {
+    if (e < mine.blocks && b.cum * p.Hkv <= r.x0 && next * p.Hkv > r.x0) {
+      const int v[9] = {e, b.cum, b.seq, b.tok0, b.pos0, b.row0, b.rows, b.tile0, b.tiles};
+#pragma unroll
+      for (int i = 0; i < 9; ++i) note[i] = v[i];
+    }
+    e += blockDim.x;
+    if (e >= mine.blocks) break;
+    fetch();
+  }
+  __syncthreads();
+  return r;
 }
 
 // A segment of a range: key tiles t0 .. t0 + n - 1 (of the unit's) of one unit.
@@ -70,9 +105,9 @@ BSG_DEV void chunk_place(ChunkSeg& g, int Hkv, int x, int x1) {
   g.n = max(g.end - begin - kChunkCost - g.t0, 0);
   g.whole = g.n == g.b.tiles;
 }
-BSG_DEV void chunk_first_seg(ChunkSeg& g, const ChunkLine& line, int Hkv, int e0, int x0, int x1) {
-  g.e = e0;
-  g.b = chunk_block(line, e0);
+BSG_DEV void chunk_first_seg(ChunkSeg& g, const volatile int* note, int Hkv, int x0, int x1) {
+  g.e = note[0];
+  g.b = ChunkBlock{note[1], note[2], note[3], note[4], note[5], note[6], note[7], note[8]};
   g.head = (x0 - g.b.cum * Hkv) / (g.b.tiles + kChunkCost);
   chunk_place(g, Hkv, x0, x1);
 }
@@ -85,16 +120,20 @@ BSG_DEV void chunk_next_seg(ChunkSeg& g, const ChunkLine& line, int Hkv, int x1)
   chunk_place(g, Hkv, g.end, x1);
 }
 
-// Range w's first segment g: whether a cut went through its unit, noted by the range after the one
-// that has the unit's first tile.
-BSG_DEV void chunk_note_cut(const ChunkLine& line, const ChunkSplit& s, int Hkv, const ChunkSeg& g, int w) {
-  const int len = g.b.tiles + kChunkCost, begin = g.b.cum * Hkv + g.head * len;
-  const int w0 = chunk_owner(s, begin + kChunkCost), w1 = chunk_owner(s, begin + len - 1);
+// Range w's first unit: whether a cut went through it, noted by the range after the one that has the
+// unit's first tile.
+BSG_DEV void chunk_note_cut(const ChunkLine& line, const ChunkRange& r, int Hkv, const volatile int* note, int w) {
   ChunkCut c = {};
-  if (w == w0 + 1 && w <= w1)
-    // (the first part lies in its range's first slot if the range begins with the unit or inside it)
-    c = ChunkCut{g.b.rows, g.b.tok0, g.b.row0, g.head, 2 * w0 + (begin <= chunk_start(s, w0) ? 0 : 1),
-                 2 * w, w1 - w0 + 1, 0};
+  if (r.x1 > r.x0) {
+    ChunkSeg g;
+    chunk_first_seg(g, note, Hkv, r.x0, r.x1);
+    const int len = g.b.tiles + kChunkCost, begin = g.b.cum * Hkv + g.head * len;
+    const int w0 = chunk_owner(r.s, begin + kChunkCost), w1 = chunk_owner(r.s, begin + len - 1);
+    if (w == w0 + 1 && w <= w1)
+      // (the first part lies in its range's first slot if the range begins with the unit or inside it)
+      c = ChunkCut{g.b.rows, g.b.tok0, g.b.row0, g.head, 2 * w0 + (begin <= chunk_start(r.s, w0) ? 0 : 1),
+                   2 * w, w1 - w0 + 1, 0};
+  }
   line.cuts[w] = c;
 }
 

@@ -22,7 +22,7 @@ struct ChunkStreamTile : AttnTile<D> {
   static constexpr int kOffSums = kChunkWarps * AttnTile<D>::kWarpB;
   static constexpr int kOffMl = kOffSums + kChunkWarps * kChunkRows * kPitch * 4;  // maxima, sums
   static constexpr int kOffBar = kOffMl + kChunkWarps * 2 * kChunkRows * 4;
-  static constexpr int kSmem = kOffBar + kChunkWarps * 32 + 16;
+  static constexpr int kSmem = kOffBar + kChunkWarps * 32 + 48;
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -47,8 +47,8 @@ struct ChunkStream {
   };
   struct Ctx {
     const ChunkStreamParams& p;
-    ChunkSplit s;
-    int x0, x1, e0, warp, lane;
+    const volatile int* note;   // where the range begins
+    int x0, x1, warp, lane;
   };
   static BSG_DEV ChunkSpan span(const Ctx& c, const ChunkSeg& g) {
     return chunk_span(g.b.pos0, g.b.row0, g.b.rows, c.p.a.Hq / c.p.a.Hkv, c.p.a.window);
@@ -62,7 +62,7 @@ struct ChunkStream {
   }
   static BSG_DEV Place first(const Ctx& c) {
     Place a;
-    chunk_first_seg(a.g, c.p.a.stream, c.p.a.Hkv, c.e0, c.x0, c.x1);
+    chunk_first_seg(a.g, c.note, c.p.a.Hkv, c.x0, c.x1);
     begin(c, a);
     return a;
   }
@@ -491,23 +491,10 @@ __global__ void __launch_bounds__(32 * kChunkWarps, 1)
   }
   pdl_wait();
   pdl_launch_dependents();
-  const ChunkHead head = chunk_head(p);
-  typename S::Ctx c{sp, chunk_split(head, head.stream, p.Hkv, gridDim.x), 0, 0, 0, warp, lane};
-  c.x0 = chunk_start(c.s, blockIdx.x);
-  c.x1 = static_cast<int>(blockIdx.x) < c.s.workers ? chunk_start(c.s, blockIdx.x + 1) : c.x0;
-  if (c.x1 == c.x0) {
-    if (threadIdx.x == 0) p.stream.cuts[blockIdx.x].rows = 0;
-    return;
-  }
-  for (int e = threadIdx.x; e < head.stream.blocks; e += 32 * kChunkWarps)
-    if (chunk_holds(p.stream, p.Hkv, e, c.x0)) *note = e;
-  __syncthreads();
-  c.e0 = *note;
-  if (threadIdx.x == 0) {
-    ChunkSeg g;
-    chunk_first_seg(g, p.stream, p.Hkv, c.e0, c.x0, c.x1);
-    chunk_note_cut(p.stream, c.s, p.Hkv, g, blockIdx.x);
-  }
+  const ChunkRange r = chunk_range(p, p.stream, false, note);
+  if (threadIdx.x == 0) chunk_note_cut(p.stream, r, p.Hkv, note, blockIdx.x);
+  if (r.x1 == r.x0) return;
+  const typename S::Ctx c{sp, note, r.x0, r.x1, warp, lane};
   S::worker(c, smem_raw);
 }
 

@@ -41,11 +41,11 @@ struct ChunkTile {
   static constexpr int kOffBar = kOffRing + kRing * kTileB;
   static constexpr int kBars = 3 * kRing + 2 + 7 * kStreams + 3;
   static constexpr int kOffWords = kOffBar + 8 * kBars;
-  static constexpr int kWords = 8 + 4 * kRing;          // notes, then the guard's flags of each slot
+  static constexpr int kWords = 20 + 4 * kRing;         // notes, then the guard's flags of each slot
   // what the two threads of a row tell each other, a float each; and stream 1's tell stream 0
   static constexpr int kOffTell = (kOffWords + 4 * kWords + 15) / 16 * 16;
-  static constexpr int kOffSeg = kOffTell + 1024 * kStreams;   // the softmax warps' segment, and the next
-  static constexpr int kSmem = kOffSeg + 2 * 80;
+  static constexpr int kOffSeg = kOffTell + 1024 * kStreams;   // the softmax warps' segment, and the next two
+  static constexpr int kSmem = kOffSeg + 3 * 80;
   static constexpr int kSoft = 8;                       // softmax warps of a stream
   static constexpr int kThreads = 32 * ((kSoft + 1) * kStreams + 2);
   // tensor memory: the score buffers (P in their place), then the streams' O
@@ -116,11 +116,9 @@ struct ChunkTensor {
 
   struct Ctx {
     const ChunkTensorParams& p;
-    ChunkSplit s;
     uint8_t* base;
     uint32_t base_u, tmem;
     int x0, x1;
-    int e0;         // the row block that x0 lies in
     BSG_DEV uint32_t bar(int i) const { return base_u + T::kOffBar + 8 * i; }
     BSG_DEV uint32_t full(int i) const { return bar(i); }                   // ring tile landed
     BSG_DEV uint32_t empty(int i) const { return bar(T::kRing + i); }       // ring tile read
@@ -146,12 +144,13 @@ struct ChunkTensor {
       return (T::kBufs == 2 ? (j & 1u) : stream) * K;
     }
     BSG_DEV uint32_t tile(int i) const { return base_u + T::kOffRing + i * T::kTileB; }
-    // 0: tensor memory's address, 1: a wait ran out, 2: tiles sent for, 3: the row block, 4 + stream:
-    // 1 + the job whose O was given values before its first product, 6: a stream is issuing
+    // 0: tensor memory's address, 1: a wait ran out, 2: tiles sent for, 4 + stream: 1 + the job whose O
+    // was given values before its first product, 6: a stream is issuing, 8 ..: where the range begins
     BSG_DEV volatile uint32_t* words() const {
       return reinterpret_cast<volatile uint32_t*>(base + T::kOffWords);
     }
-    BSG_DEV volatile uint32_t* flags(int slot) const { return words() + 8 + 4 * slot; }
+    BSG_DEV volatile int* range() const { return reinterpret_cast<volatile int*>(words() + 8); }
+    BSG_DEV volatile uint32_t* flags(int slot) const { return words() + 20 + 4 * slot; }
     BSG_DEV bool wait(uint32_t b, uint32_t parity, unsigned code = kErrTimeoutFull) const {
       return mbar_wait(b, parity, &p.a.head->err, code, p.a.wait_ns);
     }
@@ -177,7 +176,7 @@ struct ChunkTensor {
   }
   static BSG_DEV Seg first_seg(const Ctx& c) {
     Seg g;
-    chunk_first_seg(g, c.p.a.tensor, c.p.a.Hkv, c.e0, c.x0, c.x1);
+    chunk_first_seg(g, c.range(), c.p.a.Hkv, c.x0, c.x1);
     look(c, g);
     return g;
   }
@@ -298,20 +297,26 @@ struct ChunkTensor {
       const int r = r0 + lane, pos = tile * K + r;
       const bool in = pos >= s.lo && pos < s.hi;
       uint32_t bad = 0u;
-#pragma unroll 4
-      for (int i = 0; i < 8 * kSub; ++i) {
-        // (chunks in the order of the swizzle: a row's start at different banks)
-        uint8_t* at = v + (i >> 3) * (K * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4);
-        if (in) {
-          const uint4 x = lsh<uint4>(at);
-          const uint32_t here = not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w);
-          if (here)
-            *reinterpret_cast<uint4*>(at) = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y),
-                                                       finite_or_zero(x.z), finite_or_zero(x.w));
-          bad |= here;
-        } else {
-          *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+      for (int d = 0; d < kSub; ++d) {
+        // (chunks in the order of the swizzle: the lanes' rows start at different banks)
+        uint8_t* row = v + d * (K * 128) + r * 128;
+        uint4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = lsh<uint4>(row + ((i ^ (r & 7)) << 4));
+        uint32_t here = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          here |= not_finite(x[i].x) | not_finite(x[i].y) | not_finite(x[i].z) | not_finite(x[i].w);
+        if (!in || here) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(row + ((i ^ (r & 7)) << 4)) =
+                in ? make_uint4(finite_or_zero(x[i].x), finite_or_zero(x[i].y), finite_or_zero(x[i].z),
+                                finite_or_zero(x[i].w))
+                   : make_uint4(0u, 0u, 0u, 0u);
         }
+        bad |= in ? here : 0u;
       }
       const unsigned rows = __ballot_sync(0xFFFFFFFFu, bad != 0u);
       if (lane == 0) c.flags(slot)[r0 / 32] = rows;
@@ -477,7 +482,7 @@ struct ChunkTensor {
 
   // Query rows of tile `q` of a unit into shared memory (nthr threads, this one `tid`).  A thread keeps
   // its column; a row's token is a product with 2^16 / G away, exact for up to 1024 rows of 64 heads.
-  static BSG_DEV void load_q(const Ctx& c, const Seg& g, int q, int tid, int nthr) {
+  static BSG_DEV void send_q(const Ctx& c, const Seg& g, int q, int tid, int nthr) {
     const ChunkParams& a = c.p.a;
     const unsigned G = a.Hq / a.Hkv, inv = (65536u + G - 1) / G;
     const int tok0 = g.b.row0 / static_cast<int>(G);
@@ -493,8 +498,12 @@ struct ChunkTensor {
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                        dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4)), "l"(from), "r"(in ? 16 : 0) : "memory");
     }
+  }
+  // They are there: what this thread sent for.
+  static BSG_DEV void take_q(const Ctx& c, int q, int tid, int nthr) {
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (a.scale < 0.f) {  // (a negative scale's sign goes into Q)
+    if (c.p.a.scale < 0.f) {  // (a negative scale's sign goes into Q)
+      const int ch = tid % (D / 8);
       uint8_t* mine = c.base + q * T::kQB + (ch / 8) * (128 * 128);
       for (int r = tid / (D / 8); r < 128; r += nthr / (D / 8)) {
         uint4* at = reinterpret_cast<uint4*>(mine + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
@@ -700,39 +709,45 @@ struct ChunkTensor {
     bool ok = true;
     if (threadIdx.x == 0) {
       segs[0] = first_seg(c);
-      chunk_note_cut(c.p.a.tensor, c.s, c.p.a.Hkv, segs[0], blockIdx.x);
+      if (segs[0].end != c.x1) {
+        segs[1] = segs[0];
+        next_seg(c, segs[1]);
+      }
     }
-    for (int i = 0;; i ^= 1) {
-      // everyone is done with the queries of the segment before (a warp whose wait ran out still
-      // comes here)
+    bool ahead = false;   // this segment's queries are on their way
+    for (int i = 0;; i = i == 2 ? 0 : i + 1) {
+      // everyone is done with the segment before, its queries too (a warp whose wait ran out still comes
+      // here); the next segment is known
       asm volatile("bar.sync 1, %0;" ::"n"(32 * T::kSoft * T::kStreams) : "memory");
       const Seg& g = segs[i];
-      Seg* next = threadIdx.x == 0 && g.end != c.x1 ? segs + (i ^ 1) : nullptr;
-      if (ok && g.n) {
-        ok = segment(c, g, next, stream, tid, n);
-      } else if (next) {
-        *next = g;
-        next_seg(c, *next);
+      const Seg* next = g.end == c.x1 ? nullptr : segs + (i == 2 ? 0 : i + 1);
+      if (threadIdx.x == 0 && next && next->end != c.x1) {
+        Seg& after = segs[i == 0 ? 2 : i - 1];
+        after = *next;
+        next_seg(c, after);
       }
+      if (ok && g.n) ok = segment(c, g, next, stream, tid, n, ahead);
+      else ahead = false;
       n.tiles += 2 * g.n;
       n.ends += jobs_of(c, g, stream).count() > 0;
       n.joins += g.pair && g.n > 1;
-      if (g.end == c.x1) return ok;
+      if (!next) return ok;
     }
   }
 
-  static BSG_DEV bool segment(const Ctx& c, const Seg& g, Seg* next, int stream, int tid, Counts& n) {
+  // ahead: the queries were sent for at the end of the segment before; of the next (nullptr: none) after.
+  static BSG_DEV bool segment(const Ctx& c, const Seg& g, const Seg* next, int stream, int tid, Counts& n,
+                              bool& ahead) {
     const ChunkParams& p = c.p.a;
     const int half = tid >> 7, quad = (tid >> 5) & 3, lane = tid & 31;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t to = c.tmem + T::kColO + stream * D + lanes;
-    if (g.pair) load_q(c, g, 0, stream * (32 * T::kSoft) + tid, 2 * 32 * T::kSoft);
-    else load_q(c, g, stream, tid, 32 * T::kSoft);
+    const int sharers = g.pair ? 2 : 1;  // streams that fetch the same tile of queries
+    const int q_tile = g.pair ? 0 : stream, q_tid = g.pair ? stream * (32 * T::kSoft) + tid : tid;
+    if (!ahead) send_q(c, g, q_tile, q_tid, sharers * 32 * T::kSoft);
+    ahead = false;
+    take_q(c, q_tile, q_tid, sharers * 32 * T::kSoft);
     arrive_warp(c.query(), lane);
-    if (next) {
-      *next = g;
-      next_seg(c, *next);
-    }
     const Jobs my = jobs_of(c, g, stream);
     const int first = g.b.tile0 + g.t0;
     constexpr float kLog2e = 1.4426950408889634f;
@@ -811,6 +826,13 @@ struct ChunkTensor {
       }
       tc_before();
       arrive_warp(c.probs(stream), lane);
+    }
+    // The stream's scores are done, and with them its queries: the next ones are sent for while the
+    // last products run and the rows are written.  (Both streams of a pair share theirs, and meet in
+    // their place.)
+    if (next && next->n && !g.pair && !next->pair) {
+      send_q(c, *next, stream, tid, 32 * T::kSoft);
+      ahead = true;
     }
     // the row's sum
     tell[tid] = l;
@@ -927,7 +949,7 @@ struct ChunkTensor {
 
   static BSG_DEV void block(const ChunkTensorParams& p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    Ctx c{p, {}, smem_raw, smem_u32(smem_raw), 0u, 0, 0, 0};
+    Ctx c{p, smem_raw, smem_u32(smem_raw), 0u, 0, 0};
     // (the swizzle's 1024-byte tiles: the array's alignment, which nothing but the linker can break)
     if (c.base_u & 1023u) {
       if (threadIdx.x == 0) atomicOr(&p.a.head->err, kErrTimeoutFull);
@@ -951,28 +973,23 @@ struct ChunkTensor {
       mbar_init(c.query(), T::kSoft * T::kStreams);
       mbar_init(c.read(), 1);
       mbar_init(c.joined(), T::kSoft);
-      for (int i = 1; i < T::kWords; ++i) c.words()[i] = 0u;
+      for (int i = 1; i < 8; ++i) c.words()[i] = 0u;
       fence_mbar_init();
     }
     if (warp == kMmaWarp) tc_alloc(smem_u32(const_cast<uint32_t*>(c.words())), 512);
     pdl_wait();
     pdl_launch_dependents();
-    const ChunkHead head = chunk_head(p.a);
-    c.s = chunk_split(head, head.tensor, p.a.Hkv, gridDim.x);
-    c.x0 = chunk_start(c.s, blockIdx.x);
-    c.x1 = static_cast<int>(blockIdx.x) < c.s.workers ? chunk_start(c.s, blockIdx.x + 1) : c.x0;
+    {
+      const ChunkRange r = chunk_range(p.a, p.a.tensor, true, c.range());
+      c.x0 = r.x0;
+      c.x1 = r.x1;
+      if (threadIdx.x == 0) chunk_note_cut(p.a.tensor, r, p.a.Hkv, c.range(), blockIdx.x);
+    }
     tc_before();
     __syncthreads();
     tc_after();
     c.tmem = c.words()[0];
-    if (c.x1 == c.x0) {
-      if (threadIdx.x == 0) p.a.tensor.cuts[blockIdx.x].rows = 0;
-    } else {
-      // the row block that x0 lies in
-      for (int e = threadIdx.x; e < head.tensor.blocks; e += T::kThreads)
-        if (chunk_holds(p.a.tensor, p.a.Hkv, e, c.x0)) c.words()[3] = e;
-      __syncthreads();
-      c.e0 = c.words()[3];
+    if (c.x1 > c.x0) {
       bool ok;
       if (warp < kCopyWarp) {
         ok = softmax(c, warp / T::kSoft, threadIdx.x % (32 * T::kSoft));
