@@ -8,8 +8,7 @@
 // A job is a key tile (128 positions; 64 at D = 256) of one stream:
 //   S = Q K^T   from shared memory, M = 128; with 128 columns a step costs what the MMA does (with 64
 //               it is bound by shared memory, which reads Q again for each)
-//   softmax     a row of S lies in one lane; two threads take half of it each, and put the numerators
-//               P into S's place
+//   softmax     a row of S lies in one lane, whose thread puts the numerators P into S's place
 //   O += P V    P from tensor memory
 // One warp copies tiles (TMA, one box per page or tile and 64 d), a warp per stream issues its MMAs:
 // the scores of its next tile right behind P V of the last, so that the tensor cores work for one
@@ -46,7 +45,8 @@ struct ChunkTile {
   static constexpr int kOffTell = (kOffWords + 4 * kWords + 15) / 16 * 16;
   static constexpr int kOffSeg = kOffTell + 1024 * kStreams;   // the softmax warps' segment, and the next two
   static constexpr int kSmem = kOffSeg + 3 * 80;
-  static constexpr int kSoft = 8;                       // softmax warps of a stream
+  static constexpr int kHalves = D == 256 ? 2 : 1;      // threads that share a row
+  static constexpr int kSoft = 4 * kHalves;             // softmax warps of a stream
   static constexpr int kThreads = 32 * ((kSoft + 1) * kStreams + 2);
   // tensor memory: the score buffers (P in their place), then the streams' O
   static constexpr int kColO = kStreams * kBufs * kKeys;
@@ -133,7 +133,7 @@ struct ChunkTensor {
     // P V done: of every job with two score buffers, of a segment's last with one
     BSG_DEV uint32_t out(uint32_t stream) const { return bar(kP + T::kStreams + stream); }
     BSG_DEV uint32_t ended(uint32_t stream) const { return bar(kP + 2 * T::kStreams + stream); }  // (drain)
-    // the two warps of 32 rows have both come (phase: how often)
+    // (two threads a row) the two warps of 32 rows have both come (phase: how often)
     BSG_DEV uint32_t both(uint32_t stream, uint32_t w) const { return bar(kP + 3 * T::kStreams + 4 * stream + w); }
     static constexpr int kQ = kP + 7 * T::kStreams;
     BSG_DEV uint32_t query() const { return bar(kQ); }       // Q written (phase: segment)
@@ -298,20 +298,21 @@ struct ChunkTensor {
       const bool in = pos >= s.lo && pos < s.hi;
       uint32_t bad = 0u;
 #pragma unroll 1
-      for (int d = 0; d < kSub; ++d) {
+      for (int d = 0; d < 2 * kSub; ++d) {
         // (chunks in the order of the swizzle: the lanes' rows start at different banks)
-        uint8_t* row = v + d * (K * 128) + r * 128;
-        uint4 x[8];
+        uint8_t* row = v + (d >> 1) * (K * 128) + r * 128;
+        const int first = (d & 1) * 4;
+        uint4 x[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = lsh<uint4>(row + ((i ^ (r & 7)) << 4));
+        for (int i = 0; i < 4; ++i) x[i] = lsh<uint4>(row + (((first + i) ^ (r & 7)) << 4));
         uint32_t here = 0u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
           here |= not_finite(x[i].x) | not_finite(x[i].y) | not_finite(x[i].z) | not_finite(x[i].w);
         if (!in || here) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(row + ((i ^ (r & 7)) << 4)) =
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(row + (((first + i) ^ (r & 7)) << 4)) =
                 in ? make_uint4(finite_or_zero(x[i].x), finite_or_zero(x[i].y), finite_or_zero(x[i].z),
                                 finite_or_zero(x[i].w))
                    : make_uint4(0u, 0u, 0u, 0u);
@@ -475,9 +476,12 @@ struct ChunkTensor {
     }
   }
 
-  // ---- softmax warps of `stream`: two threads a row, each half of a tile's positions (and of O's
-  // columns).  (With one, a row's 128 scores one after the other, the tensor cores waited.)
-  static constexpr int H = K / 2;
+  // ---- softmax warps of `stream`.  One thread a row with two streams, whose registers hold its 128
+  // scores; two at D = 256, half of a tile's positions (and of O's columns) each.  (Two threads a row
+  // with two streams have 96 registers: reading the scores twice, or local memory, which is L2 with this
+  // much shared memory, made a job 15 % longer.)
+  static constexpr int H = K / T::kHalves;  // positions of a thread
+  static constexpr int DH = D / T::kHalves;  // columns of O
   static BSG_DEV uint32_t pack(float a, float b) { return AttnStream<BF16, 64>::pack(a, b); }
 
   // Query rows of tile `q` of a unit into shared memory (nthr threads, this one `tid`).  A thread keeps
@@ -549,86 +553,72 @@ struct ChunkTensor {
   }
   static BSG_DEV uint64_t pair(uint32_t a, uint32_t b) { return f32x2(__uint_as_float(a), __uint_as_float(b)); }
 
-  // The largest of a thread's scores, base 2.  Those that its row does not see (not a <= i < b) become
-  // -inf where they are, and so do not count after this either; kChunkAhead: all become base-2 scores.
-  static BSG_DEV float look_at(const ChunkParams& p, uint32_t ts, const Lin& f, bool cut, int a, int b) {
-    // all of them at once, but where working on them takes registers
-    constexpr int N = MODE == kChunkAhead ? 32 : H;
-    float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  // A thread's scores into registers, and the largest of them, base 2.  Those that its row does not see
+  // (not a <= i < b) become -inf; kChunkAhead: all become base-2 scores.
+  static BSG_DEV float look_at(const ChunkParams& p, uint32_t ts, const Lin& f, bool cut, int a, int b,
+                               uint32_t (&raw)[H]) {
 #pragma unroll
-    for (int j = 0; j < H; j += N) {
-      uint32_t raw[N];
+    for (int i = 0; i < H; i += 32) tc_ld32(ts + i, raw + i);
+    tc_wait_ld();
+    if constexpr (MODE == kChunkAhead) {
+      if (p.cap > 0.f) {
+        // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap))
+        constexpr float kLog2e = 1.4426950408889634f;
+        const float in = 2.f * f.scale / p.cap, top = p.cap * kLog2e;
+        const uint64_t in2 = f32x2(in, in), top2 = f32x2(top, top), two2 = f32x2(-2.f * top, -2.f * top);
 #pragma unroll
-      for (int i = 0; i < N; i += 32) tc_ld32(ts + j + i, raw + i);
-      tc_wait_ld();
-      if constexpr (MODE == kChunkAhead) {
-        if (p.cap > 0.f) {
-          // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap))
-          constexpr float kLog2e = 1.4426950408889634f;
-          const float in = 2.f * f.scale / p.cap, top = p.cap * kLog2e;
-          const uint64_t in2 = f32x2(in, in), top2 = f32x2(top, top), two2 = f32x2(-2.f * top, -2.f * top);
-#pragma unroll
-          for (int i = 0; i < N; i += 2) {
-            const uint64_t x = mul_f32x2(pair(raw[i], raw[i + 1]), in2);
-            const uint64_t y = add2(f32x2(ex2(f32x2_lo(x)), ex2(f32x2_hi(x))), f32x2(1.f, 1.f));
-            const uint64_t z = fma2(f32x2(rcp_approx(f32x2_lo(y)), rcp_approx(f32x2_hi(y))), two2, top2);
-            raw[i] = __float_as_uint(f32x2_lo(z));
-            raw[i + 1] = __float_as_uint(f32x2_hi(z));
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < N; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * f.scale);
+        for (int i = 0; i < H; i += 2) {
+          const uint64_t x = mul_f32x2(pair(raw[i], raw[i + 1]), in2);
+          const uint64_t y = add2(f32x2(ex2(f32x2_lo(x)), ex2(f32x2_hi(x))), f32x2(1.f, 1.f));
+          const uint64_t z = fma2(f32x2(rcp_approx(f32x2_lo(y)), rcp_approx(f32x2_hi(y))), two2, top2);
+          raw[i] = __float_as_uint(f32x2_lo(z));
+          raw[i + 1] = __float_as_uint(f32x2_hi(z));
         }
-        if (p.slopes) {
+      } else {
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-            raw[i] = __float_as_uint(__uint_as_float(raw[i]) + fmaf(f.slope, static_cast<float>(j + i), f.off));
-        }
+        for (int i = 0; i < H; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * f.scale);
       }
-      if (cut) {
+      if (p.slopes) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) raw[i] = j + i < b ? raw[i] : 0xFF800000u;
-        if (p.window > 0) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) raw[i] = j + i >= a ? raw[i] : 0xFF800000u;
-        }
-      }
-      if (MODE == kChunkAhead || cut)
-#pragma unroll
-        for (int i = 0; i < N; i += 32) tc_st32(ts + j + i, raw + i);
-#pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        uint64_t x = pair(raw[i], raw[i + 1]);
-        if constexpr (MODE == kChunkSlopes)
-          x = fma2(x, f32x2(f.scale, f.scale),
-                   fma2(f32x2(f.slope, f.slope), f32x2(static_cast<float>(j + i), static_cast<float>(j + i + 1)),
-                        f32x2(f.off, f.off)));
-        t[(i >> 1) & 3] = AttnPrefix<BF16, 64>::max3(t[(i >> 1) & 3], f32x2_lo(x), f32x2_hi(x));
+        for (int i = 0; i < H; ++i)
+          raw[i] = __float_as_uint(__uint_as_float(raw[i]) + fmaf(f.slope, static_cast<float>(i), f.off));
       }
     }
-    if (MODE == kChunkAhead || cut) tc_wait_st();
+    if (cut) {
+#pragma unroll
+      for (int i = 0; i < H; ++i) raw[i] = i < b ? raw[i] : 0xFF800000u;
+      if (p.window > 0) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) raw[i] = i >= a ? raw[i] : 0xFF800000u;
+      }
+    }
+    float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < H; i += 2) {
+      uint64_t x = pair(raw[i], raw[i + 1]);
+      if constexpr (MODE == kChunkSlopes)
+        x = fma2(x, f32x2(f.scale, f.scale),
+                 fma2(f32x2(f.slope, f.slope), f32x2(static_cast<float>(i), static_cast<float>(i + 1)),
+                      f32x2(f.off, f.off)));
+      t[(i >> 1) & 3] = AttnPrefix<BF16, 64>::max3(t[(i >> 1) & 3], f32x2_lo(x), f32x2_hi(x));
+    }
     const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
     return MODE == kChunkPlain ? top * f.scale : top;
   }
 
   // A thread's scores to numerators 2^(score - base), each 16 in their own place, in two parts: rounded
   // to V's type (bf16: cut off), and what that left (why: attn_prefix.cuh).  Their sum.
-  static BSG_DEV float numerators(uint32_t ts, const Lin& f, float base) {
+  static BSG_DEV float numerators(const uint32_t (&raw)[H], uint32_t ts, const Lin& f, float base) {
     const uint64_t sc = f32x2(f.scale, f.scale), sl = f32x2(f.slope, f.slope);
     const float less = MODE == kChunkSlopes ? f.off - base : -base;
     const uint64_t mb = f32x2(less, less);
     uint64_t sum[2] = {0ull, 0ull};
-    uint32_t raw[2][16];
-    tc_ld16(ts, raw[0]);
 #pragma unroll
     for (int j = 0; j < H; j += 16) {
-      const uint32_t(&s)[16] = raw[(j / 16) & 1];
-      tc_wait_ld();
-      if (j + 16 < H) tc_ld16(ts + j + 16, raw[(j / 16 + 1) & 1]);
       uint32_t out[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint64_t x = pair(s[2 * i], s[2 * i + 1]);
+        const uint64_t x = pair(raw[j + 2 * i], raw[j + 2 * i + 1]);
         uint64_t e;
         if constexpr (MODE == kChunkPlain) e = fma2(x, sc, mb);
         else if constexpr (MODE == kChunkAhead) e = add2(x, mb);
@@ -662,7 +652,7 @@ struct ChunkTensor {
     if (first) {
       const uint32_t zero[32] = {};
 #pragma unroll 1
-      for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 32) tc_st32(to + i, zero);
+      for (int i = half * DH; i < (half + 1) * DH; i += 32) tc_st32(to + i, zero);
       tc_wait_st();
     }
 #pragma unroll 1
@@ -680,7 +670,7 @@ struct ChunkTensor {
                                : half_to_f32<BF16>(hi, 0) + half_to_f32<BF16>(lo, 0);
       const bool sees = pos >= chunk_lo(pos_row, p.window) && pos <= pos_row;
 #pragma unroll 1
-      for (int d = half * (D / 2); d < (half + 1) * (D / 2); ++d) {
+      for (int d = half * DH; d < (half + 1) * DH; ++d) {
         const uint32_t x = __ldg(v + d);
         if (!(not_finite(x) & 0x8000u)) continue;
         const uint32_t o = tc_ld1(to + d);
@@ -772,12 +762,14 @@ struct ChunkTensor {
       seen |= a + half * H < K && b + half * H > 0;
       const bool cut = __any_sync(0xFFFFFFFFu, a > 0 || b < H);
       const Lin f = {fabsf(p.scale) * kLog2e, MODE == kChunkPlain ? 0.f : slope * static_cast<float>(at0 - pos), slope};
-      float top = look_at(p, ts, f, cut, a, b);
-      // the other half's
-      tell[tid] = top;
-      arrive_warp(c.both(stream, quad), lane);
-      if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
-      top = fmaxf(top, tell[tid ^ 128]);
+      uint32_t raw[H];
+      float top = look_at(p, ts, f, cut, a, b, raw);
+      if (T::kHalves == 2) {  // the other half's
+        tell[tid] = top;
+        arrive_warp(c.both(stream, quad), lane);
+        if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
+        top = fmaxf(top, tell[tid ^ 128]);
+      }
       // O and l move to a new maximum when it is more than 8 above theirs (or the first)
       const bool grow = top > m + 8.f;
       if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -792,7 +784,7 @@ struct ChunkTensor {
             tc_after();
           }
 #pragma unroll 1
-          for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 32) {
+          for (int i = half * DH; i < (half + 1) * DH; i += 32) {
             uint32_t o[32];
             tc_ld32(to + i, o);
             tc_wait_ld();
@@ -803,7 +795,7 @@ struct ChunkTensor {
         }
       }
       const float base = m == -INFINITY ? 0.f : m;
-      l += numerators(ts, f, base);
+      l += numerators(raw, ts, f, base);
       tc_wait_st();
       // (two buffers: in step with the barrier's phases; one: these scores came after that product)
       if (T::kBufs == 2 && t != my.a && !wait_warp(c, c.out(stream), (n.job - 1) & 1u)) return false;
@@ -815,10 +807,11 @@ struct ChunkTensor {
 #pragma unroll
         for (int x = 0; x < K / 32; ++x) bad |= c.flags(slot)[x];
         if (bad) {
-          // (the other half's P is there)
-          tc_before();
-          arrive_warp(c.both(stream, quad), lane);
-          if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
+          if (T::kHalves == 2) {  // (the other half's P is there)
+            tc_before();
+            arrive_warp(c.both(stream, quad), lane);
+            if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
+          }
           tc_after();
           add_not_finite(c, g, pos, half, tile, slot, ts - half * H, to, t == my.a);
           if (t == my.a && tid == 0) c.words()[4 + stream] = n.job + 1;
@@ -834,20 +827,21 @@ struct ChunkTensor {
       send_q(c, *next, stream, tid, 32 * T::kSoft);
       ahead = true;
     }
-    // the row's sum
-    tell[tid] = l;
-    arrive_warp(c.both(stream, quad), lane);
-    if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
-    l += tell[tid ^ 128];
+    if (T::kHalves == 2) {  // the row's sum
+      tell[tid] = l;
+      arrive_warp(c.both(stream, quad), lane);
+      if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
+      l += tell[tid ^ 128];
+      // (the other thread has read it too before the words are used again)
+      arrive_warp(c.both(stream, quad), lane);
+      if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
+    }
     const uint32_t jobs = my.count();
     const bool join = g.pair && g.n > 1;
     if (jobs) {
       if (!wait_warp(c, c.out(stream), (T::kBufs == 2 ? n.job - 1 : n.ends) & 1u)) return false;
       tc_after();
     }
-    // (the other thread has read what it was told, and all words are free again)
-    arrive_warp(c.both(stream, quad), lane);
-    if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
     const bool end = finish(c, g, stream, tid, jobs, to, seen ? attn_part_max(m) : -INFINITY, l, n.joins, join);
     tc_before();
     return end;
@@ -859,7 +853,7 @@ struct ChunkTensor {
                              uint32_t to, float m, float l, uint32_t joins, bool join) {
     const ChunkParams& p = c.p.a;
     const int lane = tid & 31, half = tid >> 7, r128 = tid & 127;
-    const int d0 = half * (D / 2), d1 = d0 + D / 2;
+    const int d0 = half * DH, d1 = d0 + DH;
     bool has0 = true, has1 = false;  // the streams' sums that count, and their weights
     float w0 = 1.f, w1 = 0.f;
     float* ml = reinterpret_cast<float*>(c.base + T::kOffTell) + 256;  // (stream 1's place)
@@ -877,7 +871,8 @@ struct ChunkTensor {
 #pragma unroll
           for (int y = 0; y < 32; ++y) other[(i + y) * 128 + r128] = __uint_as_float(o[y]);
         }
-        ml[tid] = half ? l : m;
+        ml[r128] = m;
+        ml[128 + r128] = l;
         arrive_warp(c.joined(), lane);
         return true;
       }
@@ -991,9 +986,13 @@ struct ChunkTensor {
     c.tmem = c.words()[0];
     if (c.x1 > c.x0) {
       bool ok;
+      // (with two streams the other four warps leave theirs registers: 256 threads of 216 and 128 of 72
+      // are the 384 of 168 that the block was launched with)
       if (warp < kCopyWarp) {
+        if constexpr (T::kStreams == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
         ok = softmax(c, warp / T::kSoft, threadIdx.x % (32 * T::kSoft));
       } else {
+        if constexpr (T::kStreams == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
         if (warp == kCopyWarp) ok = copy(c, threadIdx.x & 31);
         else if (warp == kGuardWarp) ok = guard(c, threadIdx.x & 31);
         else ok = issue(c, warp - kMmaWarp);
