@@ -38,7 +38,7 @@ struct ChunkTile {
   static constexpr int kRing = kRingMax < 12 ? kRingMax : 12;
   static constexpr int kOffRing = kStreams * kQB;
   static constexpr int kOffBar = kOffRing + kRing * kTileB;
-  static constexpr int kBars = 3 * kRing + 2 + 7 * kStreams + 3;
+  static constexpr int kBars = 3 * kRing + 2 + 8 * kStreams + 3;
   static constexpr int kOffWords = kOffBar + 8 * kBars;
   static constexpr int kWords = 20 + 4 * kRing;         // notes, then the guard's flags of each slot
   // what the two threads of a row tell each other, a float each; and stream 1's tell stream 0
@@ -129,13 +129,14 @@ struct ChunkTensor {
       return bar(kS + (T::kBufs == 2 ? (j & 1u) : stream));
     }
     static BSG_DEV uint32_t scores_phase(uint32_t j) { return (T::kBufs == 2 ? j >> 1 : j) & 1u; }
-    BSG_DEV uint32_t probs(uint32_t stream) const { return bar(kP + stream); }  // P written (phase: job)
+    // P written, the first half of a tile's positions and the second (phase: job)
+    BSG_DEV uint32_t probs(uint32_t stream, uint32_t part) const { return bar(kQ + 3 + part * T::kStreams + stream); }
     // P V done: of every job with two score buffers, of a segment's last with one
-    BSG_DEV uint32_t out(uint32_t stream) const { return bar(kP + T::kStreams + stream); }
-    BSG_DEV uint32_t ended(uint32_t stream) const { return bar(kP + 2 * T::kStreams + stream); }  // (drain)
+    BSG_DEV uint32_t out(uint32_t stream) const { return bar(kP + stream); }
+    BSG_DEV uint32_t ended(uint32_t stream) const { return bar(kP + T::kStreams + stream); }  // (drain)
     // (two threads a row) the two warps of 32 rows have both come (phase: how often)
-    BSG_DEV uint32_t both(uint32_t stream, uint32_t w) const { return bar(kP + 3 * T::kStreams + 4 * stream + w); }
-    static constexpr int kQ = kP + 7 * T::kStreams;
+    BSG_DEV uint32_t both(uint32_t stream, uint32_t w) const { return bar(kP + 2 * T::kStreams + 4 * stream + w); }
+    static constexpr int kQ = kP + 6 * T::kStreams;
     BSG_DEV uint32_t query() const { return bar(kQ); }       // Q written (phase: segment)
     BSG_DEV uint32_t read() const { return bar(kQ + 1); }    // stream 0's scores all done
     BSG_DEV uint32_t joined() const { return bar(kQ + 2); }  // stream 1's rows written
@@ -350,13 +351,16 @@ struct ChunkTensor {
       tc_mma_ss(s, q + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16,
                 k_lo + ((k / 4) * (K * 128) + (k % 4) * 32) / 16, kDescHi, kIdescS, k > 0);
   }
-  static BSG_DEV void mma_out(uint32_t o, uint32_t pr, uint32_t v_lo, bool add) {
+  // half: of the tile's positions
+  static BSG_DEV void mma_out(uint32_t o, uint32_t pr, uint32_t v_lo, bool add, int half) {
 #pragma unroll
-    for (int k = 0; k < K / 16; ++k)
+    for (int i = 0; i < K / 32; ++i) {
+      const int k = half * (K / 32) + i;
 #pragma unroll
       for (int part = 0; part < 2; ++part)
-        tc_mma_ts(o, pr + k * 16 + part * 8, v_lo + k * 2048 / 16, kDescHi, kIdescO,
+        tc_mma_ts(o, pr + k * 16 + part * 8, v_lo + k * (2048 / 16), kDescHi, kIdescO,
                   add || k > 0 || part > 0);
+    }
   }
 
   // The streams' MMAs go to the tensor cores a job at a time: P V of one and the scores of the next.
@@ -401,10 +405,10 @@ struct ChunkTensor {
           tc_commit(c.scores(stream, j));
           tc_commit(c.empty(slot));
         };
-        const auto products = [&](uint32_t j, uint32_t slot) {
+        const auto products = [&](uint32_t j, uint32_t slot, int half) {
           const bool add = j != job0 || c.words()[4 + stream] == j + 1;
-          mma_out(o, tmem + Ctx::col_s(stream, j), v_lo + slot * (T::kTileB / 16), add);
-          tc_commit(c.empty(slot));
+          mma_out(o, tmem + Ctx::col_s(stream, j), v_lo + slot * (T::kTileB / 16), add, half);
+          if (half) tc_commit(c.empty(slot));
         };
         Ring vr = kr;                     // the V tile of the job that has its scores
         if (T::kBufs == 2) {
@@ -419,16 +423,33 @@ struct ChunkTensor {
               if (!wait_warp(c, c.full(kr.slot), kr.phase)) return false;
               if (lead) scores(job + 1, kr.slot);
             }
-            if (!wait_warp(c, c.vok(vr.slot), vr.phase) || !wait_warp(c, c.probs(stream), job & 1u))
+            if (!wait_warp(c, c.vok(vr.slot), vr.phase) || !wait_warp(c, c.probs(stream, 0), job & 1u) ||
+                !wait_warp(c, c.probs(stream, 1), job & 1u))
               return false;
             tc_after();
             if (lead) {
-              products(job, vr.slot);
+              products(job, vr.slot, 0);
+              products(job, vr.slot, 1);
               tc_commit(c.out(stream));
             }
           }
         } else {
           bool pending = false;           // job `job` has its scores
+          // P V of the job that has its scores: the first half of its positions while the softmax works
+          // on the second.  The turn is kept until the end.
+          const auto pv = [&]() -> bool {
+            if (!wait_warp(c, c.vok(vr.slot), vr.phase) || !wait_warp(c, c.probs(stream, 0), job & 1u))
+              return false;
+            tc_after();
+            if (lead) {
+              take_turn(c);
+              products(job, vr.slot, 0);
+            }
+            if (!wait_warp(c, c.probs(stream, 1), job & 1u)) return false;
+            tc_after();
+            if (lead) products(job, vr.slot, 1);
+            return true;
+          };
           for (int t = 0; t < g.n; ++t) {
             const Ring k_at = kr;
             kr.next();
@@ -443,13 +464,9 @@ struct ChunkTensor {
               }
               continue;
             }
-            if (pending && (!wait_warp(c, c.vok(vr.slot), vr.phase) ||
-                            !wait_warp(c, c.probs(stream), job & 1u)))
-              return false;
-            tc_after();
+            if (pending && !pv()) return false;
             if (lead) {
-              take_turn(c);
-              if (pending) products(job, vr.slot);
+              if (!pending) take_turn(c);
               scores(job + pending, k_at.slot);
               if (g.pair && g.n > 1 && stream == 0 && t + 2 >= g.n) tc_commit(c.read());
               end_turn(c);
@@ -459,12 +476,8 @@ struct ChunkTensor {
             vr = v_at;
           }
           if (pending) {
-            if (!wait_warp(c, c.vok(vr.slot), vr.phase) || !wait_warp(c, c.probs(stream), job & 1u))
-              return false;
-            tc_after();
+            if (!pv()) return false;
             if (lead) {
-              take_turn(c);
-              products(job, vr.slot);
               tc_commit(c.out(stream));
               end_turn(c);
             }
@@ -608,13 +621,15 @@ struct ChunkTensor {
 
   // A thread's scores to numerators 2^(score - base), each 16 in their own place, in two parts: rounded
   // to V's type (bf16: cut off), and what that left (why: attn_prefix.cuh).  Their sum.
+  // (From the J0-th to before the J1-th.)
+  template <int J0, int J1>
   static BSG_DEV float numerators(const uint32_t (&raw)[H], uint32_t ts, const Lin& f, float base) {
     const uint64_t sc = f32x2(f.scale, f.scale), sl = f32x2(f.slope, f.slope);
     const float less = MODE == kChunkSlopes ? f.off - base : -base;
     const uint64_t mb = f32x2(less, less);
     uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-    for (int j = 0; j < H; j += 16) {
+    for (int j = J0; j < J1; j += 16) {
       uint32_t out[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -795,11 +810,22 @@ struct ChunkTensor {
         }
       }
       const float base = m == -INFINITY ? 0.f : m;
-      l += numerators(raw, ts, f, base);
+      const bool some = partial(g, tile);
+      if constexpr (T::kHalves == 1) {
+        l += numerators<0, H / 2>(raw, ts, f, base);
+        if (!some) {  // (else O may have to be added to first)
+          tc_wait_st();
+          tc_before();
+          arrive_warp(c.probs(stream, 0), lane);
+        }
+        l += numerators<H / 2, H>(raw, ts, f, base);
+      } else {
+        l += numerators<0, H>(raw, ts, f, base);
+      }
       tc_wait_st();
       // (two buffers: in step with the barrier's phases; one: these scores came after that product)
       if (T::kBufs == 2 && t != my.a && !wait_warp(c, c.out(stream), (n.job - 1) & 1u)) return false;
-      if (partial(g, tile)) {
+      if (some) {
         const uint32_t i = n.tiles + 2 * t + 1;
         const int slot = static_cast<int>(i % T::kRing);
         if (!wait_warp(c, c.vok(slot), (i / T::kRing) & 1u)) return false;
@@ -818,7 +844,8 @@ struct ChunkTensor {
         }
       }
       tc_before();
-      arrive_warp(c.probs(stream), lane);
+      if (some || T::kHalves == 2) arrive_warp(c.probs(stream, 0), lane);
+      arrive_warp(c.probs(stream, 1), lane);
     }
     // The stream's scores are done, and with them its queries: the next ones are sent for while the
     // last products run and the rows are written.  (Both streams of a pair share theirs, and meet in
@@ -960,7 +987,7 @@ struct ChunkTensor {
       }
       for (int i = 0; i < 2; ++i) mbar_init(c.bar(Ctx::kS + i), 1);
       for (int b = 0; b < T::kStreams; ++b) {
-        mbar_init(c.probs(b), T::kSoft);
+        for (int i = 0; i < 2; ++i) mbar_init(c.probs(b, i), T::kSoft);
         for (int w = 0; w < 4; ++w) mbar_init(c.both(b, w), 2);
         mbar_init(c.out(b), 1);
         mbar_init(c.ended(b), 1);
