@@ -345,11 +345,14 @@ struct ChunkTensor {
   }
 
   // ---- MMA warp of a stream
-  static BSG_DEV void mma_scores(uint32_t s, uint32_t q, uint32_t k_lo) {
+  static BSG_DEV void mma_scores(const Ctx& c, uint32_t s, uint32_t q, uint32_t k_lo) {
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k)
+    for (int k = 0; k < D / 16; ++k) {
+      // (the turn goes on a little early: the other stream's first MMAs are there when these end)
+      if (T::kBufs == 1 && k == D / 16 - 2) end_turn(c);
       tc_mma_ss(s, q + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16,
                 k_lo + ((k / 4) * (K * 128) + (k % 4) * 32) / 16, kDescHi, kIdescS, k > 0);
+    }
   }
   // half: of the tile's positions
   static BSG_DEV void mma_out(uint32_t o, uint32_t pr, uint32_t v_lo, bool add, int half) {
@@ -401,7 +404,7 @@ struct ChunkTensor {
         tc_after();
         const uint32_t job0 = job;
         const auto scores = [&](uint32_t j, uint32_t slot) {  // by the elected lane
-          mma_scores(tmem + Ctx::col_s(stream, j), q_lo, k_lo + slot * (T::kTileB / 16));
+          mma_scores(c, tmem + Ctx::col_s(stream, j), q_lo, k_lo + slot * (T::kTileB / 16));
           tc_commit(c.scores(stream, j));
           tc_commit(c.empty(slot));
         };
@@ -469,7 +472,6 @@ struct ChunkTensor {
               if (!pending) take_turn(c);
               scores(job + pending, k_at.slot);
               if (g.pair && g.n > 1 && stream == 0 && t + 2 >= g.n) tc_commit(c.read());
-              end_turn(c);
             }
             job += pending;
             pending = true;
@@ -566,45 +568,55 @@ struct ChunkTensor {
   }
   static BSG_DEV uint64_t pair(uint32_t a, uint32_t b) { return f32x2(__uint_as_float(a), __uint_as_float(b)); }
 
-  // A thread's scores into registers, and the largest of them, base 2.  Those that its row does not see
-  // (not a <= i < b) become -inf; kChunkAhead: all become base-2 scores.
-  static BSG_DEV float look_at(const ChunkParams& p, uint32_t ts, const Lin& f, bool cut, int a, int b,
-                               uint32_t (&raw)[H]) {
+  // What has to be done to a thread's scores before they are looked at: those that its row does not see
+  // (not a <= i < b) become -inf; kChunkAhead: all become base-2 scores.  32 at a time, where they are:
+  // most tiles need none of this, and code that has not run yet costs more than the extra way.
+  static BSG_DEV void prepare(const ChunkParams& p, uint32_t ts, const Lin& f, bool cut, int a, int b) {
+#pragma unroll 1
+    for (int j = 0; j < H; j += 32, a -= 32, b -= 32) {
+      uint32_t raw[32];
+      tc_ld32(ts + j, raw);
+      tc_wait_ld();
+      if constexpr (MODE == kChunkAhead) {
+        if (p.cap > 0.f) {
+          // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap))
+          constexpr float kLog2e = 1.4426950408889634f;
+          const float in = 2.f * f.scale / p.cap, top = p.cap * kLog2e;
+          const uint64_t in2 = f32x2(in, in), top2 = f32x2(top, top), two2 = f32x2(-2.f * top, -2.f * top);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const uint64_t x = mul_f32x2(pair(raw[i], raw[i + 1]), in2);
+            const uint64_t y = add2(f32x2(ex2(f32x2_lo(x)), ex2(f32x2_hi(x))), f32x2(1.f, 1.f));
+            const uint64_t z = fma2(f32x2(rcp_approx(f32x2_lo(y)), rcp_approx(f32x2_hi(y))), two2, top2);
+            raw[i] = __float_as_uint(f32x2_lo(z));
+            raw[i + 1] = __float_as_uint(f32x2_hi(z));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * f.scale);
+        }
+        if (p.slopes) {
+          const float off = f.off + f.slope * static_cast<float>(j);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            raw[i] = __float_as_uint(__uint_as_float(raw[i]) + fmaf(f.slope, static_cast<float>(i), off));
+        }
+      }
+      if (cut) {
+        const unsigned many = static_cast<unsigned>(max(b - a, 0));
+#pragma unroll
+        for (int i = 0; i < 32; ++i) raw[i] = static_cast<unsigned>(i - a) < many ? raw[i] : 0xFF800000u;
+      }
+      tc_st32(ts + j, raw);
+    }
+    tc_wait_st();
+  }
+
+  // A thread's scores into registers, and the largest of them, base 2.
+  static BSG_DEV float look_at(uint32_t ts, const Lin& f, uint32_t (&raw)[H]) {
 #pragma unroll
     for (int i = 0; i < H; i += 32) tc_ld32(ts + i, raw + i);
     tc_wait_ld();
-    if constexpr (MODE == kChunkAhead) {
-      if (p.cap > 0.f) {
-        // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap))
-        constexpr float kLog2e = 1.4426950408889634f;
-        const float in = 2.f * f.scale / p.cap, top = p.cap * kLog2e;
-        const uint64_t in2 = f32x2(in, in), top2 = f32x2(top, top), two2 = f32x2(-2.f * top, -2.f * top);
-#pragma unroll
-        for (int i = 0; i < H; i += 2) {
-          const uint64_t x = mul_f32x2(pair(raw[i], raw[i + 1]), in2);
-          const uint64_t y = add2(f32x2(ex2(f32x2_lo(x)), ex2(f32x2_hi(x))), f32x2(1.f, 1.f));
-          const uint64_t z = fma2(f32x2(rcp_approx(f32x2_lo(y)), rcp_approx(f32x2_hi(y))), two2, top2);
-          raw[i] = __float_as_uint(f32x2_lo(z));
-          raw[i + 1] = __float_as_uint(f32x2_hi(z));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < H; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * f.scale);
-      }
-      if (p.slopes) {
-#pragma unroll
-        for (int i = 0; i < H; ++i)
-          raw[i] = __float_as_uint(__uint_as_float(raw[i]) + fmaf(f.slope, static_cast<float>(i), f.off));
-      }
-    }
-    if (cut) {
-#pragma unroll
-      for (int i = 0; i < H; ++i) raw[i] = i < b ? raw[i] : 0xFF800000u;
-      if (p.window > 0) {
-#pragma unroll
-        for (int i = 0; i < H; ++i) raw[i] = i >= a ? raw[i] : 0xFF800000u;
-      }
-    }
     float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < H; i += 2) {
@@ -778,7 +790,8 @@ struct ChunkTensor {
       const bool cut = __any_sync(0xFFFFFFFFu, a > 0 || b < H);
       const Lin f = {fabsf(p.scale) * kLog2e, MODE == kChunkPlain ? 0.f : slope * static_cast<float>(at0 - pos), slope};
       uint32_t raw[H];
-      float top = look_at(p, ts, f, cut, a, b, raw);
+      if (MODE == kChunkAhead || cut) prepare(p, ts, f, cut, a, b);
+      float top = look_at(ts, f, raw);
       if (T::kHalves == 2) {  // the other half's
         tell[tid] = top;
         arrive_warp(c.both(stream, quad), lane);
