@@ -640,9 +640,9 @@ struct ChunkTensor {
     const float less = MODE == kChunkSlopes ? f.off - base : -base;
     const uint64_t mb = f32x2(less, less);
     uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-    for (int j = J0; j < J1; j += 16) {
-      uint32_t out[16];
+    // the next 16's exponentials are on their way while these are taken apart
+    uint64_t xy[2][8];
+    const auto raise = [&](int j) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint64_t x = pair(raw[j + 2 * i], raw[j + 2 * i + 1]);
@@ -650,19 +650,29 @@ struct ChunkTensor {
         if constexpr (MODE == kChunkPlain) e = fma2(x, sc, mb);
         else if constexpr (MODE == kChunkAhead) e = add2(x, mb);
         else e = fma2(x, sc, fma2(sl, f32x2(static_cast<float>(j + 2 * i), static_cast<float>(j + 2 * i + 1)), mb));
-        const uint64_t xy = f32x2(ex2(f32x2_lo(e)), ex2(f32x2_hi(e)));
-        const uint32_t ux = __float_as_uint(f32x2_lo(xy)), uy = __float_as_uint(f32x2_hi(xy));
+        xy[(j / 16) & 1][i] = f32x2(ex2(f32x2_lo(e)), ex2(f32x2_hi(e)));
+      }
+    };
+    raise(J0);
+#pragma unroll
+    for (int j = J0; j < J1; j += 16) {
+      if (j + 16 < J1) raise(j + 16);
+      uint32_t out[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t v = xy[(j / 16) & 1][i];
+        const uint32_t ux = __float_as_uint(f32x2_lo(v)), uy = __float_as_uint(f32x2_hi(v));
         uint64_t rest;
         if constexpr (BF16) {
           out[i] = __byte_perm(ux, uy, 0x7632);
           rest = pair((ux & 0xFFFF0000u) ^ 0x80000000u, (uy & 0xFFFF0000u) ^ 0x80000000u);
         } else {
-          out[i] = pack(f32x2_lo(xy), f32x2_hi(xy));
+          out[i] = pack(f32x2_lo(v), f32x2_hi(v));
           rest = f32x2(-half_to_f32<BF16>(out[i], 0), -half_to_f32<BF16>(out[i], 1));
         }
-        rest = add2(rest, xy);
+        rest = add2(rest, v);
         out[8 + i] = pack(f32x2_lo(rest), f32x2_hi(rest));
-        sum[i & 1] = add2(sum[i & 1], xy);
+        sum[i & 1] = add2(sum[i & 1], v);
       }
       tc_st16(ts + j, out);
     }
