@@ -160,90 +160,111 @@ __global__ void __launch_bounds__(kSetup)
     }
 }
 
-// One row of a cut unit, by a warp: its parts put together.  (Four parts' rows are fetched at once with
-// all the maxima and sums: what is known of them is where they lie.)
-template <bool BF16, int D, int ROWS>
-BSG_DEV void finish_row(const ChunkParams& p, const ChunkLine& line, const ChunkCut& cut, int r, int lane) {
+// Rows r0, r0 + step, ... (R of them, below `rows`) of a cut unit, by a warp: their parts put together,
+// two at a time of all the rows at once.  The first two parts' rows are fetched with all the maxima and
+// sums: where they lie is known.
+template <bool BF16, int D, int ROWS, int R>
+BSG_DEV void finish_rows(const ChunkParams& p, const ChunkLine& line, const ChunkCut& cut, int r0, int step,
+                         int lane) {
   constexpr int kPer = D / 32, kVec = kPer < 4 ? kPer : 4;
   const int G = p.Hq / p.Hkv;
   const auto slot = [&](int i) {
     return line.parts + static_cast<int64_t>(i ? cut.next + 2 * (i - 1) : cut.slot0) * chunk_slot_floats(ROWS, D);
   };
-  const auto fetch = [&](int i, float* v) {
-    const float* row = slot(i) + r * D;
+  const auto row = [&](int j) { return min(r0 + j * step, cut.rows - 1); };  // (past the last: not stored)
+  float v[R][2][kPer], o[R][kPer] = {}, m[R], l[R];
+  const auto fetch = [&](int i, float (&to)[kPer], int j) {
+    const float* from = slot(i) + row(j) * D;
 #pragma unroll
     for (int x = 0; x < kPer; x += kVec) {
-      const float* at = row + x / kVec * (32 * kVec) + lane * kVec;
+      const float* at = from + x / kVec * (32 * kVec) + lane * kVec;
       if constexpr (kVec == 4) {
         const float4 f = __ldcg(reinterpret_cast<const float4*>(at));
-        v[x] = f.x;
-        v[x + 1] = f.y;
-        v[x + 2] = f.z;
-        v[x + 3] = f.w;
+        to[x] = f.x;
+        to[x + 1] = f.y;
+        to[x + 2] = f.z;
+        to[x + 3] = f.w;
       } else {
         const float2 f = __ldcg(reinterpret_cast<const float2*>(at));
-        v[x] = f.x;
-        v[x + 1] = f.y;
+        to[x] = f.x;
+        to[x + 1] = f.y;
       }
     }
   };
-  float o[kPer] = {}, m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    m[j] = -INFINITY;
+    l[j] = 0.f;
+  }
   for (int i0 = 0; i0 < cut.count; i0 += 32) {
     const int i = i0 + lane, many = min(32, cut.count - i0);
-    float v[4][kPer];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < many) fetch(i0 + j, v[j]);
-    float mi = -INFINITY, li = 0.f;
-    if (i < cut.count) {
-      const float* part = slot(i);
-      mi = __ldcg(part + ROWS * D + r);
-      li = __ldcg(part + ROWS * (D + 1) + r);
-    }
-    float top = mi;
+    for (int y = 0; y < 2; ++y)
+      if (y < many)
 #pragma unroll
-    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    const float next = fmaxf(m, top), base = next == -INFINITY ? 0.f : next;
-    const float keep = ex2(m - base);
-    // (only a part without positions has m = -inf: its sums may not be written and do not count)
-    const float take = mi == -INFINITY ? 0.f : ex2(mi - base);
-    float sum = mi == -INFINITY ? 0.f : li * take;
+        for (int j = 0; j < R; ++j) fetch(i0 + y, v[j][y], j);
+    float take[R];
+    unsigned some[R];  // the parts that have positions (others' sums may not be written, and do not count)
 #pragma unroll
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    m = next;
-    l = l * keep + sum;
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) o[x] *= keep;
-    const unsigned some = __ballot_sync(0xFFFFFFFFu, mi != -INFINITY);
-    for (int j0 = 0; j0 < many; j0 += 4) {
-      if (j0)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j0 + j < many) fetch(i0 + j0 + j, v[j]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float t = __shfl_sync(0xFFFFFFFFu, take, (j0 + j) & 31);
-        if (j0 + j < many && (some >> (j0 + j) & 1u))
-#pragma unroll
-          for (int x = 0; x < kPer; ++x) o[x] = fmaf(v[j][x], t, o[x]);
+    for (int j = 0; j < R; ++j) {
+      float mi = -INFINITY, li = 0.f;
+      if (i < cut.count) {
+        const float* part = slot(i);
+        mi = __ldcg(part + ROWS * D + row(j));
+        li = __ldcg(part + ROWS * (D + 1) + row(j));
       }
+      float top = mi;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+      const float next = fmaxf(m[j], top), base = next == -INFINITY ? 0.f : next;
+      const float keep = ex2(m[j] - base);
+      take[j] = mi == -INFINITY ? 0.f : ex2(mi - base);
+      some[j] = __ballot_sync(0xFFFFFFFFu, mi != -INFINITY);
+      float sum = mi == -INFINITY ? 0.f : li * take[j];
+#pragma unroll
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+      m[j] = next;
+      l[j] = l[j] * keep + sum;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) o[j][x] *= keep;
+    }
+    for (int y0 = 0; y0 < many; y0 += 2) {
+      if (y0)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          if (y0 + y < many)
+#pragma unroll
+            for (int j = 0; j < R; ++j) fetch(i0 + y0 + y, v[j][y], j);
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          const float t = __shfl_sync(0xFFFFFFFFu, take[j], (y0 + y) & 31);
+          if (y0 + y < many && (some[j] >> (y0 + y) & 1u))
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) o[j][x] = fmaf(v[j][y][x], t, o[j][x]);
+        }
     }
   }
-  const int at = cut.row0 + r, tok = at / G;
-  const int64_t to = static_cast<int64_t>(cut.tok0 + tok) * p.Hq + cut.head * G + at - tok * G;
-  const float inv = 1.f / l;
 #pragma unroll
-  for (int x = 0; x < kPer; x += 2)
-    *reinterpret_cast<uint32_t*>(p.out + to * D + x / kVec * (32 * kVec) + lane * kVec + x % kVec) =
-        AttnStream<BF16, 64>::pack(o[x] * inv, o[x + 1] * inv);
-  if (lane == 0 && p.lse) p.lse[to] = (m + log2f(l)) * 0.6931471805599453f;
+  for (int j = 0; j < R; ++j) {
+    const int r = r0 + j * step;
+    if (r >= cut.rows) break;
+    const int at = cut.row0 + r, tok = at / G;
+    const int64_t to = static_cast<int64_t>(cut.tok0 + tok) * p.Hq + cut.head * G + at - tok * G;
+    const float inv = 1.f / l[j];
+#pragma unroll
+    for (int x = 0; x < kPer; x += 2)
+      *reinterpret_cast<uint32_t*>(p.out + to * D + x / kVec * (32 * kVec) + lane * kVec + x % kVec) =
+          AttnStream<BF16, 64>::pack(o[j][x] * inv, o[j][x + 1] * inv);
+    if (lane == 0 && p.lse) p.lse[to] = (m[j] + log2f(l[j])) * 0.6931471805599453f;
+  }
 }
 
-constexpr int kFinishWarps = 16;    // a block: a row a warp of the streaming kernel's units,
-constexpr int kFinishBlocks = 4;    // and so many blocks for one of the other's
+constexpr int kFinishWarps = 8;
 
 // Units that a cut went through, and the rows to fill.  Block (w, y): the unit noted by range w + 1 of
-// the streaming kernel (y = 0) or the tensor-memory kernel, every so many-th row of it.
+// the streaming kernel (y = 0: two rows a warp) or the tensor-memory kernel (four a warp).
 template <bool BF16, int D>
 __global__ void __launch_bounds__(32 * kFinishWarps) chunk_finish(const __grid_constant__ ChunkParams p) {
   constexpr int kRows = D == 256 ? 128 : 256;
@@ -273,13 +294,12 @@ __global__ void __launch_bounds__(32 * kFinishWarps) chunk_finish(const __grid_c
   if (blocks == 0) return;  // (its kernel may not have run, and has noted nothing then)
   const ChunkCut cut = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, 0};
   if (stream) {
-    if (warp < cut.rows) finish_row<BF16, D, kChunkRows>(p, line, cut, warp, lane);
+    if (warp < cut.rows) finish_rows<BF16, D, kChunkRows, 2>(p, line, cut, warp, kFinishWarps, lane);
   } else {
-    for (int r = (blockIdx.y - 1) * kFinishWarps + warp; r < cut.rows; r += kFinishBlocks * kFinishWarps)
-      finish_row<BF16, D, kRows>(p, line, cut, r, lane);
+    const int r = (blockIdx.y - 1) * (4 * kFinishWarps) + warp;
+    if (r < cut.rows) finish_rows<BF16, D, kRows, 4>(p, line, cut, r, kFinishWarps, lane);
   }
 }
-static_assert(kFinishWarps == kChunkRows, "a warp for each row of a streaming unit");
 
 template <bool BF16, int D>
 int launch(const ChunkParams& p, const ChunkMaps& maps, int sms, cudaStream_t s) {
@@ -320,7 +340,7 @@ int launch(const ChunkParams& p, const ChunkMaps& maps, int sms, cudaStream_t s)
     rc = decode_launch(kernel, dim3(sms), dim3(T::kThreads), T::kSmem, s, q);
     if (rc != BSGEMV_OK) return rc;
   }
-  return decode_launch(chunk_finish<BF16, D>, dim3(sms > 1 ? sms - 1 : 1, 1 + (tensor ? kFinishBlocks : 0)),
+  return decode_launch(chunk_finish<BF16, D>, dim3(sms > 1 ? sms - 1 : 1, 1 + (tensor ? T::kRows / (4 * kFinishWarps) : 0)),
                        dim3(32 * kFinishWarps), 0, s, p);
 }
 
