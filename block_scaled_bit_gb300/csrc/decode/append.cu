@@ -7,7 +7,10 @@
 // A lane works on 16 elements of a head at a time: 8 pairs of the rotation, which are two chunks of
 // 16 bytes in either layout (p and p + rot / 2: a chunk from each half; 2 p and 2 p + 1: two chunks
 // side by side).  D / 16 lanes share a head, so the norm is a sum over a few lanes, and a warp takes
-// 32 / (D / 16) heads at once; all its heads are one token's, so a lane keeps its 8 cosines and sines.
+// 32 / (D / 16) heads at once.  All its heads are one token's: their cosines and sines are worked out once
+// a warp, and a lane keeps its 8 of each, multiplied by its weights, in packed pairs.  (The first version,
+// scalar, with every lane its own 8 sines, took 4200 instructions a token of 48 heads and 45 us for 8192
+// tokens, 0.66 of the schedulers' slots.)
 // Angles: position times frequency modulo a turn, in 64-bit fixed point -- one integer product that
 // wraps where the turns are whole, so no position is too far for it.
 #include <math.h>
@@ -45,7 +48,7 @@ struct AppendParams {
   int lanes_log2;   // lanes of a head: D / 16, to a power of two
   int slices;       // warps of a token
   int k_plane, v_plane;
-  float eps, factor;
+  float eps, factor, inv_D;
   const unsigned long long* freqs;
 };
 
@@ -66,35 +69,100 @@ BSG_DEV int entry_of(const int32_t* starts, int n, int r, int lane) {
   return m ? lo + __ffs(m) - 1 : n;
 }
 
-template <bool BF16>
-BSG_DEV void unpack8(const uint4& a, float* x) {
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// A lane's 16 elements as packed fp32: first[i] and second[i] are the first and second elements of pairs
+// 2 i and 2 i + 1.
+struct Packs {
+  uint64_t first[4], second[4];
+};
+template <bool BF16, bool INTER>
+BSG_DEV Packs unpack(const uint4& a, const uint4& b) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  Packs x;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = half_to_f32<BF16>(w[i], 0);
-    x[2 * i + 1] = half_to_f32<BF16>(w[i], 1);
+    if constexpr (INTER) {  // a word is a pair
+      x.first[i] = f32x2(half_to_f32<BF16>(w[2 * i], 0), half_to_f32<BF16>(w[2 * i + 1], 0));
+      x.second[i] = f32x2(half_to_f32<BF16>(w[2 * i], 1), half_to_f32<BF16>(w[2 * i + 1], 1));
+    } else {
+      x.first[i] = f32x2(half_to_f32<BF16>(w[i], 0), half_to_f32<BF16>(w[i], 1));
+      x.second[i] = f32x2(half_to_f32<BF16>(w[4 + i], 0), half_to_f32<BF16>(w[4 + i], 1));
+    }
   }
+  return x;
 }
 template <bool BF16>
-BSG_DEV uint4 pack8(const float* x) {
-  uint32_t w[4];
+BSG_DEV uint32_t word(float a, float b) {
+  uint32_t w;
+  if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+  return w;
+}
+template <bool BF16, bool INTER>
+BSG_DEV void repack(const Packs& x, uint4& a, uint4& b) {
+  uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
-    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+    if constexpr (INTER) {
+      w[2 * i] = word<BF16>(f32x2_lo(x.first[i]), f32x2_lo(x.second[i]));
+      w[2 * i + 1] = word<BF16>(f32x2_hi(x.first[i]), f32x2_hi(x.second[i]));
+    } else {
+      w[i] = word<BF16>(f32x2_lo(x.first[i]), f32x2_hi(x.first[i]));
+      w[4 + i] = word<BF16>(f32x2_lo(x.second[i]), f32x2_hi(x.second[i]));
+    }
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  a = make_uint4(w[0], w[1], w[2], w[3]);
+  b = make_uint4(w[4], w[5], w[6], w[7]);
+}
+BSG_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
 }
 
 template <bool BF16, bool INTER>
-__global__ void __launch_bounds__(32 * kAppendWarps)
+__global__ void __launch_bounds__(32 * kAppendWarps, 5)
     append_tokens(const __grid_constant__ AppendParams p) {
+  __shared__ float2 turns[kAppendWarps][256];  // cosine and sine of a warp's row
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
+  float2* turn_of = turns[threadIdx.x >> 5];
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
   const int r = static_cast<int>(w / p.slices), slice = static_cast<int>(w - static_cast<int64_t>(r) * p.slices);
   if (r >= p.T) return;
   pdl_wait();
+
+  // this lane's place in a head
+  const int per = 1 << p.lanes_log2, item = lane & (per - 1), sub = lane >> p.lanes_log2;
+  const int at_once = 32 >> p.lanes_log2;  // heads
+  const bool in = item < p.D / 16, turned = item < p.rot / 16;
+  const int c0 = INTER || !turned ? 16 * item : 8 * item;
+  const int c1 = INTER || !turned ? c0 + 8 : c0 + p.rot / 2;
+  // A slice's heads of a tensor, at_once at a time: the first, and the step to the next.  Queries, keys
+  // and values are laid end to end, so that slices share all of them evenly.
+  const int q_steps = p.q ? (p.Hq + at_once - 1) / at_once : 0, kv_steps = p.k ? (p.Hkv + at_once - 1) / at_once : 0;
+  const int step = at_once * p.slices;
+  const auto begin = [&](int before) {
+    const int late = before % p.slices;
+    return (slice >= late ? slice - late : slice - late + p.slices) * at_once + sub;
+  };
+  struct Chunks {
+    uint4 a, b;
+  };
+  const auto fetch = [&](const uint16_t* row, int h, int heads) {
+    Chunks x = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    if (in && h < heads) {
+      const uint16_t* src = row + h * p.D;
+      x.a = *reinterpret_cast<const uint4*>(src + c0);
+      x.b = *reinterpret_cast<const uint4*>(src + c1);
+    }
+    return x;
+  };
+  // (the first loads, before the row's place is known)
+  const uint16_t* q_row = p.q + r * p.q_stride;
+  const int q_first = begin(0);
+  Chunks q_ahead = {};
+  if (p.q) q_ahead = fetch(q_row, q_first, p.Hq);
+
   const int e = entry_of(p.starts, p.n, r, lane);
   if (e >= p.n || r < __ldg(p.starts + e)) return;
   const int s = __ldg(p.seqs + e);
@@ -103,109 +171,101 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
   const int64_t len = min(static_cast<int64_t>(__ldg(p.lens + s)), most);
   const int64_t at = len - (static_cast<int64_t>(__ldg(p.starts + e + 1)) - r);
   if (at < 0) return;
-  const int turn = p.pos ? __ldg(p.pos + r) : static_cast<int>(at);
+  int page = -1;
+  if (p.k) page = __ldg(p.tables + static_cast<int64_t>(s) * p.max_pages + at / p.page_size);
 
-  // this lane's place in a head
-  const int per = 1 << p.lanes_log2, item = lane & (per - 1), sub = lane >> p.lanes_log2;
-  const int heads_at_once = 32 >> p.lanes_log2;
-  const bool in = item < p.D / 16, turned = item < p.rot / 16;
-  const int c0 = INTER || !turned ? 16 * item : 8 * item;
-  const int c1 = INTER || !turned ? c0 + 8 : c0 + p.rot / 2;
-  float cs[8], sn[8];
+  const int pos = p.pos ? __ldg(p.pos + r) : static_cast<int>(at);
+  for (int i = lane; i < p.rot / 2; i += 32) {
+    // turns in [-1/2, 1/2): the product's upper word; sine and cosine of pi times it, doubled
+    const unsigned long long f = __ldg(p.freqs + i);
+    const int top = static_cast<int>((f * static_cast<unsigned long long>(static_cast<long long>(pos))) >> 32);
+    float a, b;
+    sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &a, &b);  // 2^-31
+    turn_of[i] = make_float2(b * p.factor, a * p.factor);
+  }
+  __syncwarp();
+  // The heads of one tensor, normalised and turned:  (a, b) -> scale (a wa c - b wb s, a wa s + b wb c),
+  // weights and turns multiplied ahead.
+  const auto heads = [&](const uint16_t* row, Chunks next, int h, int many, const uint16_t* weight, uint16_t* out,
+                         int64_t out_step) {
+    uint64_t fc[4], fs[4], gc[4], gs[4];
+    {
+      Packs u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    cs[i] = 1.f;
-    sn[i] = 0.f;
-    if (turned) {
-      // turns in [-1/2, 1/2): the product's upper word; sine and cosine of pi times it, doubled
-      const unsigned long long f = __ldg(p.freqs + 8 * item + i);
-      const int top = static_cast<int>((f * static_cast<unsigned long long>(static_cast<long long>(turn))) >> 32);
-      float a, b;
-      sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &a, &b);  // 2^-31
-      sn[i] = a * p.factor;
-      cs[i] = b * p.factor;
+      for (int i = 0; i < 4; ++i) u.first[i] = u.second[i] = f32x2(1.f, 1.f);
+      if (weight && in)
+        u = unpack<BF16, INTER>(__ldg(reinterpret_cast<const uint4*>(weight + c0)),
+                                __ldg(reinterpret_cast<const uint4*>(weight + c1)));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // (elements that are not turned: by a cosine of 1)
+        float2 x = make_float2(1.f, 0.f), y = x;
+        if (turned) {
+          x = turn_of[8 * item + 2 * i];
+          y = turn_of[8 * item + 2 * i + 1];
+        }
+        const uint64_t cs = f32x2(x.x, y.x), sn = f32x2(x.y, y.y);
+        fc[i] = mul_f32x2(u.first[i], cs);
+        fs[i] = mul_f32x2(u.first[i], sn);
+        gc[i] = mul_f32x2(u.second[i], cs);
+        gs[i] = mul_f32x2(u.second[i], sn) ^ 0x8000000080000000ull;
+      }
     }
-  }
-  uint8_t* k_page = nullptr;
-  uint8_t* v_page = nullptr;
-  if (p.k) {
-    const int page = __ldg(p.tables + static_cast<int64_t>(s) * p.max_pages + at / p.page_size);
-    if (page >= 0 && page < p.num_pages) {
-      const int64_t row = 2 * (at % p.page_size) * p.row_stride;
-      k_page = p.pool + (static_cast<int64_t>(p.k_plane) * p.num_pages + page) * p.page_bytes + row;
-      v_page = p.pool + (static_cast<int64_t>(p.v_plane) * p.num_pages + page) * p.page_bytes + row;
-    }
-  }
-  const int q_heads = p.q ? p.Hq : 0, kv_heads = p.k ? p.Hkv : 0;
-  const int q_steps = (q_heads + heads_at_once - 1) / heads_at_once;
-  const int kv_steps = (kv_heads + heads_at_once - 1) / heads_at_once;
-  for (int step = slice; step < q_steps + 2 * kv_steps; step += p.slices) {
-    const int kind = step < q_steps ? 0 : (step < q_steps + kv_steps ? 1 : 2);  // queries, keys, values
-    const int h = (step - (kind == 0 ? 0 : q_steps + (kind - 1) * kv_steps)) * heads_at_once + sub;
-    const bool on = in && h < (kind == 0 ? q_heads : kv_heads);
-    const uint16_t* src =
-        (kind == 0 ? p.q + r * p.q_stride : kind == 1 ? p.k + r * p.k_stride : p.v + r * p.v_stride) +
-        static_cast<int64_t>(h) * p.D;
-    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-    if (on) {
-      a = *reinterpret_cast<const uint4*>(src + c0);
-      b = *reinterpret_cast<const uint4*>(src + c1);
-    }
-    if (kind != 2) {
-      float x[8], y[8];
-      unpack8<BF16>(a, x);
-      unpack8<BF16>(b, y);
-      const uint16_t* weight = kind == 0 ? p.q_weight : p.k_weight;
+    for (; h - sub < many; h += step) {
+      const Chunks now = next;
+      next = fetch(row, h + step, many);
+      Packs x = unpack<BF16, INTER>(now.a, now.b);
+      float scale = 1.f;
       if (weight) {
-        float sum = 0.f;
+        uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += x[i] * x[i] + y[i] * y[i];
+        for (int i = 0; i < 4; ++i) {
+          fma_f32x2(sum2[0], x.first[i], x.first[i]);
+          fma_f32x2(sum2[1], x.second[i], x.second[i]);
+        }
+        float sum = (f32x2_lo(sum2[0]) + f32x2_hi(sum2[0])) + (f32x2_lo(sum2[1]) + f32x2_hi(sum2[1]));
         for (int d = 1; d < per; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        const float scale = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
-        if (in) {
-          float u[8];
-          unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(weight + c0)), u);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = x[i] * scale * u[i];
-          unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(weight + c1)), u);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = y[i] * scale * u[i];
-        }
+        scale = rsqrtf(sum * p.inv_D + p.eps);
       }
+      const uint64_t sc = f32x2(scale, scale);
       if (turned) {
-        if constexpr (INTER) {
-          // chunk a holds pairs 0 .. 3, chunk b pairs 4 .. 7
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
-            x[2 * i] = x0 * cs[i] - x1 * sn[i];
-            x[2 * i + 1] = x0 * sn[i] + x1 * cs[i];
-            y[2 * i] = y0 * cs[4 + i] - y1 * sn[4 + i];
-            y[2 * i + 1] = y0 * sn[4 + i] + y1 * cs[4 + i];
-          }
-        } else {
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t a = mul_f32x2(x.first[i], sc), b = mul_f32x2(x.second[i], sc);
+          x.first[i] = fma2(b, gs[i], mul_f32x2(a, fc[i]));
+          x.second[i] = fma2(b, gc[i], mul_f32x2(a, fs[i]));
+        }
+      } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float x0 = x[i], y0 = y[i];
-            x[i] = x0 * cs[i] - y0 * sn[i];
-            y[i] = x0 * sn[i] + y0 * cs[i];
-          }
+        for (int i = 0; i < 4; ++i) {
+          x.first[i] = mul_f32x2(mul_f32x2(x.first[i], sc), fc[i]);
+          x.second[i] = mul_f32x2(mul_f32x2(x.second[i], sc), gc[i]);
         }
       }
-      a = pack8<BF16>(x);
-      b = pack8<BF16>(y);
+      if (in && h < many) {
+        uint4 a, b;
+        repack<BF16, INTER>(x, a, b);
+        uint16_t* dst = out + h * out_step;
+        *reinterpret_cast<uint4*>(dst + c0) = a;
+        *reinterpret_cast<uint4*>(dst + c1) = b;
+      }
     }
-    if (!on) continue;
-    uint16_t* dst;
-    if (kind == 0) {
-      dst = p.q_out + r * p.q_out_stride + static_cast<int64_t>(h) * p.D;
-    } else {
-      uint8_t* page = kind == 1 ? k_page : v_page;
-      if (!page) continue;
-      dst = reinterpret_cast<uint16_t*>(page) + h * p.head_stride;
-    }
-    *reinterpret_cast<uint4*>(dst + c0) = a;
-    *reinterpret_cast<uint4*>(dst + c1) = b;
+  };
+  if (p.q) heads(q_row, q_ahead, q_first, p.Hq, p.q_weight, p.q_out + r * p.q_out_stride, p.D);
+  if (p.k == nullptr || page < 0 || page >= p.num_pages) return;
+  const int64_t place = at % p.page_size * p.row_stride;
+  const auto plane = [&](int which) {
+    return reinterpret_cast<uint16_t*>(p.pool + (static_cast<int64_t>(which) * p.num_pages + page) * p.page_bytes) + place;
+  };
+  const uint16_t *k_row = p.k + r * p.k_stride, *v_row = p.v + r * p.v_stride;
+  const int k_first = begin(q_steps);
+  heads(k_row, fetch(k_row, k_first, p.Hkv), k_first, p.Hkv, p.k_weight, plane(p.k_plane), p.head_stride);
+  uint16_t* out = plane(p.v_plane);
+  for (int h = begin(q_steps + kv_steps); h < p.Hkv; h += step) {
+    const Chunks x = fetch(v_row, h, p.Hkv);
+    if (!in) continue;
+    *reinterpret_cast<uint4*>(out + h * p.head_stride + c0) = x.a;
+    *reinterpret_cast<uint4*>(out + h * p.head_stride + c1) = x.b;
   }
 }
 
@@ -335,6 +395,7 @@ int bsgemv_cache_append(bsgemv_cache_t c, bsgemv_rope_t rope, void* pool, const 
   p.rot = rope->rot;
   p.eps = eps;
   p.factor = rope->factor;
+  p.inv_D = 1.f / static_cast<float>(rope->D);
   p.k_plane = k_plane;
   p.v_plane = v_plane;
   p.freqs = static_cast<const unsigned long long*>(rope->freqs);
