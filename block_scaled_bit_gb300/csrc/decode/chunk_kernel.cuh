@@ -108,6 +108,19 @@ struct ChunkMaps {
 };
 bool chunk_encode(const ChunkParams& p, ChunkMaps* m);
 
+// Which entries go to which kernel: up to short_rows rows to the streaming kernel (index 1), others to the
+// tensor-memory kernel (0).
+struct ChunkKinds {
+  int short_rows;
+  int rows[2], keys[2];   // of a row block and a key tile
+};
+
 int launch_chunk(const ChunkParams& p, const ChunkMaps& maps, int sms, cudaStream_t s);
+
+// The first of a call's kernels, and all of them for a head size.
+int launch_chunk_setup(const ChunkParams& p, const ChunkKinds& kinds, cudaStream_t s);
+int launch_chunk_64(const ChunkParams& p, const ChunkMaps& maps, int sms, cudaStream_t s);
+int launch_chunk_128(const ChunkParams& p, const ChunkMaps& maps, int sms, cudaStream_t s);
+int launch_chunk_256(const ChunkParams& p, const ChunkMaps& maps, int sms, cudaStream_t s);
 
 }  // namespace bsg
