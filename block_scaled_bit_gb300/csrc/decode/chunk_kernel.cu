@@ -193,7 +193,7 @@ bool chunk_encode(const ChunkParams& p, ChunkMaps* m) {
       p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap* const maps[4] = {&m->k, &m->v, &m->stream_k, &m->stream_v};
   for (int i = 0; i < 4; ++i) {
-    const int keys = i < 2 ? 64 : 4096 / p.D;  // positions of a tile
+    const int keys = i < 2 ? (p.D == 256 ? 64 : 128) : 4096 / p.D;  // positions of a tile
     const uint32_t box[4] = {64, static_cast<uint32_t>(ps < keys ? ps : keys), 1, 1};
     if (decode_encode(maps[i], type, 4, i & 1 ? p.v : p.k, dims, strides, box,
                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) != BSGEMV_OK)

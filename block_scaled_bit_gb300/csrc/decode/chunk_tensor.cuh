@@ -5,16 +5,15 @@
 // and every other key tile, and are joined at the end (in shared memory).  At D = 256 there is one
 // stream (its accumulator is half of tensor memory) with two score buffers.
 //
-// A job is a key tile (64 positions) of one stream:
-//   S = Q K^T   from shared memory, M = 128
+// A job is a key tile (128 positions; 64 at D = 256) of one stream:
+//   S = Q K^T   from shared memory, M = 128; with 128 columns a step costs what the MMA does (with 64
+//               it is bound by shared memory, which reads Q again for each)
 //   softmax     a row of S lies in one lane, whose thread puts the numerators P into S's place
 //   O += P V    P from tensor memory
-// One warp copies tiles (TMA, one box per page or tile and 64 d), a warp per stream issues its MMAs.  A
-// stream has two score buffers: its next tile's scores are there when its softmax comes back, and the
-// tensor cores always have work of one of the streams.  (Tiles of 128 positions and one buffer make the
-// scores a third cheaper -- with 64 columns shared memory, which reads Q again for each tile, is their
-// limit -- but leave a stream's softmax and products to wait for each other: COMPARE.)
-// O is scaled to a new maximum only when a row's has grown by more than 2^8 since O's.
+// One warp copies tiles (TMA, one box per page or tile and 64 d), a warp per stream issues its MMAs:
+// the scores of its next tile right behind P V of the last, so that the tensor cores work for one
+// stream while the other's softmax runs.  O is scaled to a new maximum only when a row's has grown by
+// more than 2^8 since O's.
 //
 // Places that a row does not see must not reach it, whatever they hold.  Keys: their scores are
 // replaced.  Values: a weight of 0 times NaN or infinity is NaN, so a warp (the guard) looks at the V
@@ -29,17 +28,17 @@ namespace bsg {
 
 template <int D>
 struct ChunkTile {
-  static constexpr int kKeys = 64;                      // positions of a tile
+  static constexpr int kKeys = D == 256 ? 64 : 128;     // positions of a tile
   static constexpr int kStreams = D == 256 ? 1 : 2;
-  static constexpr int kBufs = 2;                       // score buffers of a stream
+  static constexpr int kBufs = D == 256 ? 2 : 1;        // score buffers of a stream
   static constexpr int kRows = 128 * kStreams;          // rows of a row block
   static constexpr int kTileB = kKeys * D * 2;          // bytes of a K (or V) tile
   static constexpr int kQB = 128 * D * 2;               // bytes of a query tile
   static constexpr int kRingMax = (224 * 1024 - kStreams * kQB) / kTileB;
-  static constexpr int kRing = kRingMax < 16 ? kRingMax : 16;
+  static constexpr int kRing = kRingMax < 12 ? kRingMax : 12;
   static constexpr int kOffRing = kStreams * kQB;
   static constexpr int kOffBar = kOffRing + kRing * kTileB;
-  static constexpr int kBars = 3 * kRing + 9 * kStreams + 3;
+  static constexpr int kBars = 3 * kRing + 2 + 8 * kStreams + 3;
   static constexpr int kOffWords = kOffBar + 8 * kBars;
   static constexpr int kWords = 20 + 4 * kRing;         // notes, then the guard's flags of each slot
   // what the two threads of a row tell each other, a float each; and stream 1's tell stream 0
@@ -124,15 +123,16 @@ struct ChunkTensor {
     BSG_DEV uint32_t full(int i) const { return bar(i); }                   // ring tile landed
     BSG_DEV uint32_t empty(int i) const { return bar(T::kRing + i); }       // ring tile read
     BSG_DEV uint32_t vok(int i) const { return bar(2 * T::kRing + i); }     // the guard is done with it
-    static constexpr int kS = 3 * T::kRing, kP = kS + T::kBufs * T::kStreams;
+    static constexpr int kS = 3 * T::kRing, kP = kS + 2;
     // scores of a stream's job j (numbered over the block's whole range) are written
     BSG_DEV uint32_t scores(uint32_t stream, uint32_t j) const {
-      return bar(kS + T::kBufs * stream + (j & 1u));
+      return bar(kS + (T::kBufs == 2 ? (j & 1u) : stream));
     }
-    static BSG_DEV uint32_t scores_phase(uint32_t j) { return (j >> 1) & 1u; }
-    // phase j & 1 of these is job j's
-    BSG_DEV uint32_t probs(uint32_t stream) const { return bar(kQ + 3 + stream); }  // P written
-    BSG_DEV uint32_t out(uint32_t stream) const { return bar(kP + stream); }        // P V done
+    static BSG_DEV uint32_t scores_phase(uint32_t j) { return (T::kBufs == 2 ? j >> 1 : j) & 1u; }
+    // P written, the first half of a tile's positions and the second (phase: job)
+    BSG_DEV uint32_t probs(uint32_t stream, uint32_t part) const { return bar(kQ + 3 + part * T::kStreams + stream); }
+    // P V done: of every job with two score buffers, of a segment's last with one
+    BSG_DEV uint32_t out(uint32_t stream) const { return bar(kP + stream); }
     BSG_DEV uint32_t ended(uint32_t stream) const { return bar(kP + T::kStreams + stream); }  // (drain)
     // (two threads a row) the two warps of 32 rows have both come (phase: how often)
     BSG_DEV uint32_t both(uint32_t stream, uint32_t w) const { return bar(kP + 2 * T::kStreams + 4 * stream + w); }
@@ -142,11 +142,11 @@ struct ChunkTensor {
     BSG_DEV uint32_t joined() const { return bar(kQ + 2); }  // stream 1's rows written
     BSG_DEV int skip() const { return blockIdx.x == 0 ? p.a.skip[0] : -1; }
     static BSG_DEV uint32_t col_s(uint32_t stream, uint32_t j) {
-      return (T::kBufs * stream + (j & 1u)) * K;
+      return (T::kBufs == 2 ? (j & 1u) : stream) * K;
     }
     BSG_DEV uint32_t tile(int i) const { return base_u + T::kOffRing + i * T::kTileB; }
     // 0: tensor memory's address, 1: a wait ran out, 2: tiles sent for, 4 + stream: 1 + the job whose O
-    // was given values before its first product, 8 ..: where the range begins
+    // was given values before its first product, 6: a stream is issuing, 8 ..: where the range begins
     BSG_DEV volatile uint32_t* words() const {
       return reinterpret_cast<volatile uint32_t*>(base + T::kOffWords);
     }
@@ -345,31 +345,55 @@ struct ChunkTensor {
   }
 
   // ---- MMA warp of a stream
-  static BSG_DEV void mma_scores(uint32_t s, uint32_t q, uint32_t k_lo) {
+  static BSG_DEV void mma_scores(const Ctx& c, uint32_t s, uint32_t q, uint32_t k_lo) {
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k)
+    for (int k = 0; k < D / 16; ++k) {
+      // (the turn goes on a little early: the other stream's first MMAs are there when these end)
+      if (T::kBufs == 1 && k == D / 16 - 2) end_turn(c);
       tc_mma_ss(s, q + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16,
                 k_lo + ((k / 4) * (K * 128) + (k % 4) * 32) / 16, kDescHi, kIdescS, k > 0);
+    }
   }
-  static BSG_DEV void mma_out(uint32_t o, uint32_t pr, uint32_t v_lo, bool add) {
+  // half: of the tile's positions
+  static BSG_DEV void mma_out(uint32_t o, uint32_t pr, uint32_t v_lo, bool add, int half) {
 #pragma unroll
-    for (int k = 0; k < K / 16; ++k)
+    for (int i = 0; i < K / 32; ++i) {
+      const int k = half * (K / 32) + i;
 #pragma unroll
       for (int part = 0; part < 2; ++part)
         tc_mma_ts(o, pr + k * 16 + part * 8, v_lo + k * (2048 / 16), kDescHi, kIdescO,
                   add || k > 0 || part > 0);
+    }
   }
 
-  // The whole warp runs this; one elected lane issues.  The scores of the stream's next tile go to the
-  // tensor cores ahead of P V of this one.  A ring tile is free when every stream has given it back: with
-  // the commit of what read it, or at once where it is not the stream's.
+  // The streams' MMAs go to the tensor cores a job at a time: P V of one and the scores of the next.
+  // Without that, two streams that are ready together have theirs mixed, both wait for all of them,
+  // and stay in step: the tensor cores then stand still while both softmaxes run.  A turn that does not
+  // come in some 10 us is not waited for: nothing but the order depends on it.
+  static BSG_DEV void take_turn(const Ctx& c) {
+    if (T::kStreams == 1) return;
+    const uint32_t lock = smem_u32(const_cast<uint32_t*>(c.words() + 6));
+    for (int i = 0; i < 200; ++i) {
+      uint32_t was;
+      asm volatile("atom.acquire.cta.shared::cta.cas.b32 %0, [%1], 0, 1;" : "=r"(was) : "r"(lock) : "memory");
+      if (was == 0u) return;
+    }
+  }
+  static BSG_DEV void end_turn(const Ctx& c) {
+    if (T::kStreams == 2)
+      asm volatile("st.release.cta.shared::cta.u32 [%0], 0;" ::"r"(smem_u32(const_cast<uint32_t*>(c.words() + 6)))
+                   : "memory");
+  }
+
+  // The whole warp runs this; one elected lane issues.  A ring tile is free when every stream has
+  // given it back: with the commit of what read it, or at once where it is not the stream's.
   static BSG_DEV bool issue(const Ctx& c, uint32_t stream) {
     const bool lead = elect_one();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, c.tmem, 0);
     const uint32_t k_lo = desc_lo(c.base_u + T::kOffRing, 16);
     const uint32_t v_lo = desc_lo(c.base_u + T::kOffRing, K * 128);
     const uint32_t o = tmem + T::kColO + stream * D;
-    Ring kr = {0, 0}, vr = {1, 0};        // the next K and V tile
+    Ring kr = {0, 0};                     // the next K tile
     uint32_t job = 0, seg_phase = 0;
     for (Seg g = first_seg(c);; next_seg(c, g)) {
       if (g.n) {
@@ -379,64 +403,98 @@ struct ChunkTensor {
         seg_phase ^= 1u;
         tc_after();
         const uint32_t job0 = job;
-        uint32_t ahead = job;             // the next job to have its scores
-        const auto mine = [&](int t) { return t >= my.a && t < my.b && (t - my.a) % my.step == 0; };
-        // scores of tile t, or the tile given back
-        const auto key_tile = [&](int t) -> bool {
+        const auto scores = [&](uint32_t j, uint32_t slot) {  // by the elected lane
+          mma_scores(c, tmem + Ctx::col_s(stream, j), q_lo, k_lo + slot * (T::kTileB / 16));
+          tc_commit(c.scores(stream, j));
+          tc_commit(c.empty(slot));
+        };
+        const auto products = [&](uint32_t j, uint32_t slot, int half) {
+          const bool add = j != job0 || c.words()[4 + stream] == j + 1;
+          mma_out(o, tmem + Ctx::col_s(stream, j), v_lo + slot * (T::kTileB / 16), add, half);
+          if (half) tc_commit(c.empty(slot));
+        };
+        Ring vr = kr;                     // the V tile of the job that has its scores
+        if (T::kBufs == 2) {
+          // all tiles are the stream's; the scores of a tile ahead of P V of the one before
           if (!wait_warp(c, c.full(kr.slot), kr.phase)) return false;
-          if (mine(t)) {
+          if (lead) scores(job, kr.slot);
+          for (int t = 0; t < g.n; ++t, ++job) {
+            kr.next();
+            vr = kr;
+            kr.next();
+            if (t + 1 < g.n) {
+              if (!wait_warp(c, c.full(kr.slot), kr.phase)) return false;
+              if (lead) scores(job + 1, kr.slot);
+            }
+            if (!wait_warp(c, c.vok(vr.slot), vr.phase) || !wait_warp(c, c.probs(stream, 0), job & 1u) ||
+                !wait_warp(c, c.probs(stream, 1), job & 1u))
+              return false;
+            tc_after();
             if (lead) {
-              mma_scores(tmem + Ctx::col_s(stream, ahead), q_lo, k_lo + kr.slot * (T::kTileB / 16));
-              tc_commit(c.scores(stream, ahead));
-              tc_commit(c.empty(kr.slot));
+              products(job, vr.slot, 0);
+              products(job, vr.slot, 1);
+              tc_commit(c.out(stream));
+            }
+          }
+        } else {
+          bool pending = false;           // job `job` has its scores
+          // P V of the job that has its scores: the first half of its positions while the softmax works
+          // on the second.  The turn is kept until the end.
+          const auto pv = [&]() -> bool {
+            if (!wait_warp(c, c.vok(vr.slot), vr.phase) || !wait_warp(c, c.probs(stream, 0), job & 1u))
+              return false;
+            tc_after();
+            if (lead) {
+              take_turn(c);
+              products(job, vr.slot, 0);
+            }
+            if (!wait_warp(c, c.probs(stream, 1), job & 1u)) return false;
+            tc_after();
+            if (lead) products(job, vr.slot, 1);
+            return true;
+          };
+          for (int t = 0; t < g.n; ++t) {
+            const Ring k_at = kr;
+            kr.next();
+            const Ring v_at = kr;
+            kr.next();
+            if (!wait_warp(c, c.full(k_at.slot), k_at.phase)) return false;
+            if (t < my.a || t >= my.b || (t - my.a) % my.step) {
+              if (!wait_warp(c, c.vok(v_at.slot), v_at.phase)) return false;
+              if (lead) {
+                mbar_arrive(c.empty(k_at.slot));
+                mbar_arrive(c.empty(v_at.slot));
+              }
+              continue;
+            }
+            if (pending && !pv()) return false;
+            if (lead) {
+              if (!pending) take_turn(c);
+              scores(job + pending, k_at.slot);
               if (g.pair && g.n > 1 && stream == 0 && t + 2 >= g.n) tc_commit(c.read());
             }
-            ++ahead;
-          } else if (lead) {
-            mbar_arrive(c.empty(kr.slot));
+            job += pending;
+            pending = true;
+            vr = v_at;
           }
-          kr.next();
-          kr.next();
-          return true;
-        };
-        // P V of tile t, or the tile given back
-        const auto value_tile = [&](int t) -> bool {
-          if (!wait_warp(c, c.vok(vr.slot), vr.phase)) return false;
-          if (mine(t)) {
-            if (!wait_warp(c, c.probs(stream), job & 1u)) return false;
-            tc_after();
-            const bool add = job != job0 || c.words()[4 + stream] == job + 1;
+          if (pending) {
+            if (!pv()) return false;
             if (lead) {
-              mma_out(o, tmem + Ctx::col_s(stream, job), v_lo + vr.slot * (T::kTileB / 16), add);
               tc_commit(c.out(stream));
-              tc_commit(c.empty(vr.slot));
+              end_turn(c);
             }
             ++job;
-          } else if (lead) {
-            mbar_arrive(c.empty(vr.slot));
           }
-          vr.next();
-          vr.next();
-          return true;
-        };
-        for (int t = 0; t < min(my.a, g.n); ++t)
-          if (!key_tile(t) || !value_tile(t)) return false;
-        if (my.a < my.b && !key_tile(my.a)) return false;
-        for (int t = my.a; t < my.b; ++t) {
-          if (mine(t))
-            for (int x = t + 1; x <= t + my.step && x < my.b; ++x)
-              if (!key_tile(x)) return false;
-          if (!value_tile(t)) return false;
         }
-        for (int t = max(my.a, my.b); t < g.n; ++t)
-          if (!key_tile(t) || !value_tile(t)) return false;
       }
       if (g.end == c.x1) return true;
     }
   }
 
-  // ---- softmax warps of `stream`.  One thread a row with two streams; two at D = 256, half of a tile's
-  // positions (and of O's columns) each.
+  // ---- softmax warps of `stream`.  One thread a row with two streams, whose registers hold its 128
+  // scores; two at D = 256, half of a tile's positions (and of O's columns) each.  (Two threads a row
+  // with two streams have 96 registers: reading the scores twice, or local memory, which is L2 with this
+  // much shared memory, made a job 15 % longer.)
   static constexpr int H = K / T::kHalves;  // positions of a thread
   static constexpr int DH = D / T::kHalves;  // columns of O
   static BSG_DEV uint32_t pack(float a, float b) { return AttnStream<BF16, 64>::pack(a, b); }
@@ -575,6 +633,8 @@ struct ChunkTensor {
 
   // A thread's scores to numerators 2^(score - base), each 16 in their own place, in two parts: rounded
   // to V's type (bf16: cut off), and what that left (why: attn_prefix.cuh).  Their sum.
+  // (From the J0-th to before the J1-th.)
+  template <int J0, int J1>
   static BSG_DEV float numerators(const uint32_t (&raw)[H], uint32_t ts, const Lin& f, float base) {
     const uint64_t sc = f32x2(f.scale, f.scale), sl = f32x2(f.slope, f.slope);
     const float less = MODE == kChunkSlopes ? f.off - base : -base;
@@ -593,10 +653,10 @@ struct ChunkTensor {
         xy[(j / 16) & 1][i] = f32x2(ex2(f32x2_lo(e)), ex2(f32x2_hi(e)));
       }
     };
-    raise(0);
+    raise(J0);
 #pragma unroll
-    for (int j = 0; j < H; j += 16) {
-      if (j + 16 < H) raise(j + 16);
+    for (int j = J0; j < J1; j += 16) {
+      if (j + 16 < J1) raise(j + 16);
       uint32_t out[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -662,6 +722,7 @@ struct ChunkTensor {
   struct Counts {
     uint32_t job;     // jobs of its stream
     uint32_t tiles;   // ring tiles before the segment
+    uint32_t ends;    // segments in which its stream had jobs
     uint32_t joins;   // segments whose streams were joined
     uint32_t both;    // times that it met its row's other thread
   };
@@ -695,6 +756,7 @@ struct ChunkTensor {
       if (ok && g.n) ok = segment(c, g, next, stream, tid, n, ahead);
       else ahead = false;
       n.tiles += 2 * g.n;
+      n.ends += jobs_of(c, g, stream).count() > 0;
       n.joins += g.pair && g.n > 1;
       if (!next) return ok;
     }
@@ -754,9 +816,11 @@ struct ChunkTensor {
         l *= keep;
         m = next_m;
         if (t != my.a) {
-          // the accumulator's last product is done
-          if (!wait_warp(c, c.out(stream), (n.job - 1) & 1u)) return false;
-          tc_after();
+          // the accumulator's last product is done (one buffer: the scores came after it)
+          if (T::kBufs == 2) {
+            if (!wait_warp(c, c.out(stream), (n.job - 1) & 1u)) return false;
+            tc_after();
+          }
 #pragma unroll 1
           for (int i = half * DH; i < (half + 1) * DH; i += 32) {
             uint32_t o[32];
@@ -769,11 +833,22 @@ struct ChunkTensor {
         }
       }
       const float base = m == -INFINITY ? 0.f : m;
-      l += numerators(raw, ts, f, base);
+      const bool some = partial(g, tile);
+      if constexpr (T::kHalves == 1) {
+        l += numerators<0, H / 2>(raw, ts, f, base);
+        if (!some) {  // (else O may have to be added to first)
+          tc_wait_st();
+          tc_before();
+          arrive_warp(c.probs(stream, 0), lane);
+        }
+        l += numerators<H / 2, H>(raw, ts, f, base);
+      } else {
+        l += numerators<0, H>(raw, ts, f, base);
+      }
       tc_wait_st();
-      // (in step with the barrier's phases)
-      if (t != my.a && !wait_warp(c, c.out(stream), (n.job - 1) & 1u)) return false;
-      if (partial(g, tile)) {
+      // (two buffers: in step with the barrier's phases; one: these scores came after that product)
+      if (T::kBufs == 2 && t != my.a && !wait_warp(c, c.out(stream), (n.job - 1) & 1u)) return false;
+      if (some) {
         const uint32_t i = n.tiles + 2 * t + 1;
         const int slot = static_cast<int>(i % T::kRing);
         if (!wait_warp(c, c.vok(slot), (i / T::kRing) & 1u)) return false;
@@ -792,7 +867,8 @@ struct ChunkTensor {
         }
       }
       tc_before();
-      arrive_warp(c.probs(stream), lane);
+      if (some || T::kHalves == 2) arrive_warp(c.probs(stream, 0), lane);
+      arrive_warp(c.probs(stream, 1), lane);
     }
     // The stream's scores are done, and with them its queries: the next ones are sent for while the
     // last products run and the rows are written.  (Both streams of a pair share theirs, and meet in
@@ -813,7 +889,7 @@ struct ChunkTensor {
     const uint32_t jobs = my.count();
     const bool join = g.pair && g.n > 1;
     if (jobs) {
-      if (!wait_warp(c, c.out(stream), (n.job - 1) & 1u)) return false;
+      if (!wait_warp(c, c.out(stream), (T::kBufs == 2 ? n.job - 1 : n.ends) & 1u)) return false;
       tc_after();
     }
     const bool end = finish(c, g, stream, tid, jobs, to, seen ? attn_part_max(m) : -INFINITY, l, n.joins, join);
@@ -932,9 +1008,9 @@ struct ChunkTensor {
         mbar_init(c.empty(i), T::kStreams);
         mbar_init(c.vok(i), 1);
       }
-      for (int i = 0; i < T::kBufs * T::kStreams; ++i) mbar_init(c.bar(Ctx::kS + i), 1);
+      for (int i = 0; i < 2; ++i) mbar_init(c.bar(Ctx::kS + i), 1);
       for (int b = 0; b < T::kStreams; ++b) {
-        mbar_init(c.probs(b), T::kSoft);
+        for (int i = 0; i < 2; ++i) mbar_init(c.probs(b, i), T::kSoft);
         for (int w = 0; w < 4; ++w) mbar_init(c.both(b, w), 2);
         mbar_init(c.out(b), 1);
         mbar_init(c.ended(b), 1);
@@ -960,9 +1036,13 @@ struct ChunkTensor {
     c.tmem = c.words()[0];
     if (c.x1 > c.x0) {
       bool ok;
+      // (with two streams the other four warps leave theirs registers: 256 threads of 216 and 128 of 72
+      // are the 384 of 168 that the block was launched with)
       if (warp < kCopyWarp) {
+        if constexpr (T::kStreams == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
         ok = softmax(c, warp / T::kSoft, threadIdx.x % (32 * T::kSoft));
       } else {
+        if constexpr (T::kStreams == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
         if (warp == kCopyWarp) ok = copy(c, threadIdx.x & 31);
         else if (warp == kGuardWarp) ok = guard(c, threadIdx.x & 31);
         else ok = issue(c, warp - kMmaWarp);
