@@ -98,7 +98,8 @@ int bsgemv_chunk_run(bsgemv_chunk_plan_t plan, const void* q, int64_t q_stride, 
                      const float* slopes, void* out, float* lse, void* stream) {
   if (plan == nullptr || n < 1 || T < 1 || num_pages < 1 || num_seqs < 1 || max_pages < 1 ||
       table_stride < max_pages || page_stride < 0 || head_stride < 0 || row_stride < 0 ||
-      !isfinite(scale) || !isfinite(cap) || cap < 0.f || window < 0)
+      !isfinite(scale) || !isfinite(cap) || cap < 0.f || !isfinite(cap * 1.4426950408889634f) ||
+      (cap > 0.f && !isfinite(scale / cap)) || window < 0)
     return BSGEMV_ERR_INVALID_ARG;
   if (n > plan->max_n || T > plan->max_T) return BSGEMV_ERR_M_TOO_LARGE;
   if (!q || !k || !v || !tables || !lens || !seqs || !starts || !out) return BSGEMV_ERR_INVALID_ARG;

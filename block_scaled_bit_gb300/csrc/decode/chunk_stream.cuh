@@ -222,14 +222,7 @@ struct ChunkStream {
         const int pos = pos0 + 8 * n + 2 * t + (x & 1), i = x >> 1;
         float v = s[n][x];
         if (EXTRA) {
-          // cap tanh(y / cap) = cap - 2 cap / (1 + e^(2 y / cap))
-          if (p.cap > 0.f) {
-            float z;
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(1.f + ex2(v * (2.f * scale / p.cap))));
-            v = fmaf(-2.f * kLog2e * p.cap, z, p.cap * kLog2e);
-          } else {
-            v *= scale;
-          }
+          v = p.cap > 0.f ? p.cap * kLog2e * chunk_tanh(v * (p.scale / p.cap)) : v * scale;
           v = fmaf(my.slope[i], static_cast<float>(pos - my.pos[i]), v);
         } else {
           v *= scale;

@@ -94,12 +94,6 @@ BSG_DEV void store_sector(void* to, const uint32_t* r) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
 }
-BSG_DEV float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // What scores are besides scaled products: a bias by distance, or worked out ahead of the rest (capped,
 // or with a scale of 0, which a score of -inf must not meet).
 enum ChunkMode { kChunkPlain = 0, kChunkSlopes = 1, kChunkAhead = 2 };
@@ -579,18 +573,11 @@ struct ChunkTensor {
       tc_wait_ld();
       if constexpr (MODE == kChunkAhead) {
         if (p.cap > 0.f) {
-          // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap))
           constexpr float kLog2e = 1.4426950408889634f;
-          const float in = 2.f * f.scale / p.cap, top = p.cap * kLog2e;
-          const uint64_t in2 = f32x2(in, in), top2 = f32x2(top, top), two2 = f32x2(-2.f * top, -2.f * top);
+          const float in = fabsf(p.scale) / p.cap, top = p.cap * kLog2e;
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const uint64_t x = mul_f32x2(pair(raw[i], raw[i + 1]), in2);
-            const uint64_t y = add2(f32x2(ex2(f32x2_lo(x)), ex2(f32x2_hi(x))), f32x2(1.f, 1.f));
-            const uint64_t z = fma2(f32x2(rcp_approx(f32x2_lo(y)), rcp_approx(f32x2_hi(y))), two2, top2);
-            raw[i] = __float_as_uint(f32x2_lo(z));
-            raw[i + 1] = __float_as_uint(f32x2_hi(z));
-          }
+          for (int i = 0; i < 32; ++i)
+            raw[i] = __float_as_uint(top * chunk_tanh(__uint_as_float(raw[i]) * in));
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * f.scale);

@@ -207,6 +207,18 @@ def test_options(D, Hq, Hkv, kw):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_cap_far_above_the_scores_changes_nothing(D):
+    """cap tanh(t / cap) is t but for t^3 / (3 cap^2): below 2^-25 of scores of up to 100 at a cap of a
+    million, so the capped scores are held to the uncapped tolerance (2^-20 of themselves)."""
+    import torch
+    for new in ([100, 3], [2, 1, 2]):
+        pr = Chunk(torch, "f16", 8, 2, D, 16, new, [300] * len(new), seed=D, qscale=4.0)
+        with bsgemv.ChunkPlan(*pr.plan) as plan:
+            pr.check(*pr.run(plan, cap=1e6))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("junk", [math.nan, math.inf, -math.inf, 60000.0])
 @pytest.mark.parametrize("D,Hq,ps", [(64, 8, 16), (128, 32, 64), (256, 16, 8)])
 def test_unused_places_do_not_matter(junk, D, Hq, ps):
@@ -496,6 +508,7 @@ def test_calls_refused():
             assert call(**{name: None}) == bsgemv.ERR_INVALID_ARG
         for kw in (dict(n=0), dict(T=0), dict(pages=0), dict(seqs_n=0), dict(cols=0), dict(ts=1), dict(qs=64),
                    dict(scale=math.nan), dict(scale=math.inf), dict(cap=-1.0), dict(cap=math.nan),
+                   dict(cap=3e38), dict(cap=1e-40),
                    dict(window=-1), dict(sp=-8)):
             assert call(**kw) == bsgemv.ERR_INVALID_ARG, kw
         assert call(n=3) == call(T=9) == bsgemv.ERR_M_TOO_LARGE
