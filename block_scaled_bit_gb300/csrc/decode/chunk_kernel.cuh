@@ -18,10 +18,15 @@
 
 namespace bsg {
 
-constexpr int kChunkCost = 4;
+constexpr int kChunkCost = 4;           // (6, 8 and 12 are within 3 %, 12 is worse for long units)
 constexpr int kChunkMost = 1 << 29;     // sums of stretches stop here
 constexpr int kChunkMaxLen = 1 << 30;   // tokens of a sequence that count
-constexpr int kChunkShort = 32;         // rows of an entry that the streaming kernel takes
+// Rows of an entry that the streaming kernel takes: those of one of its row blocks.  The other kernel
+// reads K and V once for 128 rows.  With 32 here (two row blocks), us for entries of 32 rows, 8 kv heads of
+// 128, streaming / the other: 8 entries after 1000 positions 44 / 42, after 8000 127 / 97, 32 after 4000
+// 218 / 165, 2 after 30000 112 / 93, 1 after 1000 22 / 30 (one launch fewer); of 16 rows or fewer the
+// streaming kernel's are its own.
+constexpr int kChunkShort = 16;
 constexpr int kChunkRows = 16;          // rows of its row blocks
 
 // Bit of the error word, beside those of waits that ran out: the call's tiles are more than it can

@@ -137,18 +137,22 @@ BSG_DEV void chunk_note_cut(const ChunkLine& line, const ChunkRange& r, int Hkv,
   line.cuts[w] = c;
 }
 
+BSG_DEV float chunk_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // tanh(u), to 2^-20 of itself: 1 - 2 / (1 + e^2u), whose error is 2^-23, and near zero, where that is not
 // small beside the result, u - u^3 / 3 + 2 u^5 / 15 - 17 u^7 / 315 + 62 u^9 / 2835 (below 0.3 the next
 // term is 2^-23 of u).
 BSG_DEV float chunk_tanh(float u) {
   const float w = u * u;
-  float near = fmaf(w, 62.f / 2835.f, -17.f / 315.f), e, r;
+  float near = fmaf(w, 62.f / 2835.f, -17.f / 315.f), e;
   near = fmaf(w, near, 2.f / 15.f);
   near = fmaf(w, near, -1.f / 3.f);
   near = fmaf(w * u, near, u);
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(u * 2.8853900817779268f));  // (2 log2 e)
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return fabsf(u) < 0.3f ? near : fmaf(-2.f, r, 1.f);
+  return fabsf(u) < 0.3f ? near : fmaf(-2.f, chunk_rcp(1.f + e), 1.f);
 }
 
 }  // namespace bsg

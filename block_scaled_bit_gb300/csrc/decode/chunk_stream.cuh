@@ -7,6 +7,10 @@
 // mma.sync m16n8k16, softmax in registers (the pieces of attn_stream.cuh).  The four take a segment's
 // tiles in turn and put their sums together in shared memory at its end: a unit that lies in one
 // block's range is written from there, others leave a part a block, not a part a warp.
+// Measured: 33 sequences of 3100 positions on average, 24/8 heads of 64, one token each: 190 MB in 44 us;
+// 8 sequences of 1004 positions, 32/8 heads of 128, four tokens each: 33 MB in 13 us, of which 3 until
+// the first tile has come, 1.2 a tile, 1.2 to join a segment.  (Eight warps with tiles of half the size
+// are no faster.)
 #pragma once
 
 #include "attn_stream.cuh"

@@ -10,10 +10,21 @@
 //               it is bound by shared memory, which reads Q again for each)
 //   softmax     a row of S lies in one lane, whose thread puts the numerators P into S's place
 //   O += P V    P from tensor memory
-// One warp copies tiles (TMA, one box per page or tile and 64 d), a warp per stream issues its MMAs:
-// the scores of its next tile right behind P V of the last, so that the tensor cores work for one
-// stream while the other's softmax runs.  O is scaled to a new maximum only when a row's has grown by
-// more than 2^8 since O's.
+// One warp copies tiles (TMA, one box per page or tile and 64 d), a warp per stream issues its MMAs: P V
+// of the first half of a tile while the softmax works on the second, then the rest and the scores of the
+// next tile, so that the tensor cores work for one stream while the other's softmax runs.  O is scaled to
+// a new maximum only when a row's has grown by more than 2^8 since O's.
+//
+// Bound: the tensor cores, P V counted twice (P in two parts, as attn_prefix.cuh has it): 3072 cycles of
+// MMAs for 128 positions and 256 rows of 128 d, of 3900 that they take; short units by their beginnings
+// and ends.  Measured, 32/8 heads of 128, bf16: 2048 tokens after 30720 positions 910 us, 1170 Tflop/s,
+// with the second part 1755 (cuBLAS: 1919, 1720 sustained); 1024 after 7168 144 us.  What it came from:
+// MMAs of the two streams mixed 1400 us (below: turns), taken in turn 1013, without local memory in the
+// softmax 957, P V by halves 928, the turn given on early 913.  Tiles of 64 positions with two score
+// buffers, as at D = 256, took 1140 (and 56 in place of 62 us for short prompts of 8/8 heads of 64).
+// At D = 256 the tiles of 64 positions come through L2 at 37 bytes a cycle and SM, for 128 rows only: that
+// and the softmax make it 530 Tflop/s with a window and a cap.  Exponentials: 128 a row and tile take 1000
+// cycles of the special-function units, which bounds D = 64.
 //
 // Places that a row does not see must not reach it, whatever they hold.  Keys: their scores are
 // replaced.  Values: a weight of 0 times NaN or infinity is NaN, so a warp (the guard) looks at the V
@@ -362,7 +373,8 @@ struct ChunkTensor {
 
   // The streams' MMAs go to the tensor cores a job at a time: P V of one and the scores of the next.
   // Without that, two streams that are ready together have theirs mixed, both wait for all of them,
-  // and stay in step: the tensor cores then stand still while both softmaxes run.  A turn that does not
+  // and stay in step: the tensor cores then stand still while both softmaxes run (1400 us for 1013).  A
+  // turn that does not
   // come in some 10 us is not waited for: nothing but the order depends on it.
   static BSG_DEV void take_turn(const Ctx& c) {
     if (T::kStreams == 1) return;
@@ -487,8 +499,8 @@ struct ChunkTensor {
 
   // ---- softmax warps of `stream`.  One thread a row with two streams, whose registers hold its 128
   // scores; two at D = 256, half of a tile's positions (and of O's columns) each.  (Two threads a row
-  // with two streams have 96 registers: reading the scores twice, or local memory, which is L2 with this
-  // much shared memory, made a job 15 % longer.)
+  // with two streams have 96 registers; scores read again from tensor memory, 16 at a time, then took
+  // 976 us where this takes 957.)
   static constexpr int H = K / T::kHalves;  // positions of a thread
   static constexpr int DH = D / T::kHalves;  // columns of O
   static BSG_DEV uint32_t pack(float a, float b) { return AttnStream<BF16, 64>::pack(a, b); }
@@ -575,9 +587,25 @@ struct ChunkTensor {
         if (p.cap > 0.f) {
           constexpr float kLog2e = 1.4426950408889634f;
           const float in = fabsf(p.scale) / p.cap, top = p.cap * kLog2e;
+          if (p.cap <= 64.f) {
+            // cap - 2 cap / (1 + e^(2 x / cap)) is off by 2^-23 cap, here 2^-17 at most: what P keeps of
+            // itself.  (With the other form for all, 1024 tokens after 7168, 32/8 heads of 128, took 294 us
+            // in place of 234.)
+            const uint64_t in2 = f32x2(2.f * kLog2e * in, 2.f * kLog2e * in), top2 = f32x2(top, top);
+            const uint64_t two2 = f32x2(-2.f * top, -2.f * top);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            raw[i] = __float_as_uint(top * chunk_tanh(__uint_as_float(raw[i]) * in));
+            for (int i = 0; i < 32; i += 2) {
+              const uint64_t x = mul_f32x2(pair(raw[i], raw[i + 1]), in2);
+              const uint64_t y = add2(f32x2(ex2(f32x2_lo(x)), ex2(f32x2_hi(x))), f32x2(1.f, 1.f));
+              const uint64_t z = fma2(f32x2(chunk_rcp(f32x2_lo(y)), chunk_rcp(f32x2_hi(y))), two2, top2);
+              raw[i] = __float_as_uint(f32x2_lo(z));
+              raw[i + 1] = __float_as_uint(f32x2_hi(z));
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              raw[i] = __float_as_uint(top * chunk_tanh(__uint_as_float(raw[i]) * in));
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * f.scale);
@@ -745,7 +773,10 @@ struct ChunkTensor {
       n.tiles += 2 * g.n;
       n.ends += jobs_of(c, g, stream).count() > 0;
       n.joins += g.pair && g.n > 1;
-      if (!next) return ok;
+      if (!next) {
+        asm volatile("cp.async.wait_all;" ::: "memory");  // (after a wait that ran out: queries on their way)
+        return ok;
+      }
     }
   }
 
