@@ -15,7 +15,7 @@
 // next tile, so that the tensor cores work for one stream while the other's softmax runs.  O is scaled to
 // a new maximum only when a row's has grown by more than 2^8 since O's.
 //
-// Bound: the tensor cores, P V counted twice (P in two parts, as attn_prefix.cuh has it): 3072 cycles of
+// Bound: the tensor cores, P V counted twice (P in two parts, as attn_prefix.cuh has it): some 3100 cycles of
 // MMAs for 128 positions and 256 rows of 128 d, of 3900 that they take; short units by their beginnings
 // and ends.  Measured, 32/8 heads of 128, bf16: 2048 tokens after 30720 positions 910 us, 1170 Tflop/s,
 // with the second part 1755 (cuBLAS: 1919, 1720 sustained); 1024 after 7168 144 us.  What it came from:
