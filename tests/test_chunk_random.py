@@ -4,6 +4,7 @@ import random
 
 import pytest
 
+from block_scaled_bit_gb300 import bsgemv
 from test_chunk import Chunk, once
 
 
@@ -41,3 +42,40 @@ def test_random_batches(seed):
     import torch
     pr, kw = problem(torch, seed)
     once(pr, **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1023, 1025, 2500])
+def test_many_entries(n):
+    """More entries and row blocks of both kernels than one step of the line's kernel takes."""
+    import torch
+    r = random.Random(n)
+    new = [r.choice([0, 1, 2, 17, 20]) for _ in range(n)]
+    pr = Chunk(torch, "f16", 1, 1, 64, 8, new, [r.randint(0, 30) for _ in range(n)], seed=n,
+               skip=[i for i in range(n) if i % 97 == 5], lead=1, tail=1)
+    once(pr)
+
+
+@pytest.mark.gpu
+def test_more_row_blocks_than_a_step_takes():
+    import torch
+    pr = Chunk(torch, "bf16", 32, 1, 64, 128, [9000, 1, 300], [100, 70, 5], seed=7)
+    with bsgemv.ChunkPlan(*pr.plan) as plan:
+        out, lse = pr.run(plan, window=40)
+        # the first rows and the last of the long entry (all of them would be 2 GB a head in 64 bits)
+        a, keep = pr.start[:], pr.new[:]
+        i = 0
+        for first, many in ((a[i], 200), (a[i + 1] - 200, 200)):
+            pos = torch.arange(first - a[i] + 100, first - a[i] + 100 + many, device="cuda")
+            lo = int(pos[0]) - 39 if int(pos[0]) > 39 else 0
+            page, row = pr.places(pr.seq[i], lo, int(pos[-1]) + 1)
+            j = torch.arange(lo, int(pos[-1]) + 1, device="cuda")
+            seen = (j[None] <= pos[:, None]) & (j[None] > pos[:, None] - 40)
+            k, v = pr.k[page, 0, row].double(), pr.v[page, 0, row].double()
+            for h in (0, 13, 31):
+                t = torch.where(seen, pr.q[first:first + many, h].double() @ k.T / 8, -float("inf"))
+                o = torch.softmax(t, -1) @ v
+                # numerators and the output are rounded once each, 2^-8 of values below 6
+                assert (out[first:first + many, h].double() - o).abs().max().item() <= 2 * 2.0 ** -8 * 6
+        assert keep == pr.new and torch.isfinite(out).all() and torch.isfinite(lse).all()
+        assert plan.device_status() == bsgemv.OK
