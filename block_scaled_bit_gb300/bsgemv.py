@@ -724,24 +724,38 @@ class PageCache(_Handle):
         likewise (k_weight), and v as it is, to the places of the new tokens: rows starts[i] ..
         starts[i + 1] - 1 are the last tokens of sequence seqs[i].  q, k, v and q_out: any stride
         between rows; q and q_out, or k and v, may be None.  pos [T]: other positions to rotate by."""
-        n, i32, act = seqs.shape[0], self._i32, rope._act
+        n, i32, act, D = seqs.shape[0], self._i32, rope._act, rope.D
         T = (k if q is None else q).shape[0]
-        args = []
-        for t, heads in ((q, rope.Hq), (k, rope.Hkv), (v, rope.Hkv), (q_out, rope.Hq)):
-            if t is None:
-                args += [None, 0]
-                continue
-            (rows, h, D), (st, sh, s1) = t.shape, t.stride()
-            if rows != T or h != heads or D != rope.D or s1 != 1 or sh != D and h > 1 or \
-                    t.dtype not in act:
-                raise BsgemvError(ERR_INVALID_ARG, "bsgemv_cache_append")
-            args += [t.data_ptr(), st if T > 1 else h * D]  # (one row's stride is of no account)
+        # (spelt out: a call for one token is as long as its arguments take)
+        qp = kp = vp = op = None
+        qs = ks = vs = os = 0
+        bad = False
+        if q is not None:
+            qp, (qs, sh, s1) = q.data_ptr(), q.stride()
+            bad |= q.shape != (T, rope.Hq, D) or s1 != 1 or sh != D and rope.Hq > 1 or q.dtype not in act
+        if q_out is not None:
+            op, (os, sh, s1) = q_out.data_ptr(), q_out.stride()
+            bad |= q_out.shape != (T, rope.Hq, D) or s1 != 1 or sh != D and rope.Hq > 1 or \
+                q_out.dtype not in act
+        if k is not None:
+            kp, (ks, sh, s1) = k.data_ptr(), k.stride()
+            bad |= k.shape != (T, rope.Hkv, D) or s1 != 1 or sh != D and rope.Hkv > 1 or \
+                k.dtype not in act
+        if v is not None:
+            vp, (vs, sh, s1) = v.data_ptr(), v.stride()
+            bad |= v.shape != (T, rope.Hkv, D) or s1 != 1 or sh != D and rope.Hkv > 1 or \
+                v.dtype not in act
+        if bad:
+            raise BsgemvError(ERR_INVALID_ARG, "bsgemv_cache_append")
+        if T == 1:  # (one row's stride is of no account)
+            qs = os = rope.Hq * D
+            ks = vs = rope.Hkv * D
         status = lib().bsgemv_cache_append(
             self._h, rope._h, _arg("pool", pool, self._pool),
             _arg("tables", tables, self._tables, i32), _arg("lens", lens, self._lens, i32),
-            _arg("seqs", seqs, 4 * n, i32), _arg("starts", starts, 4 * n + 4, i32), n, T, *args[:6],
-            _arg("q_weight", q_weight, 2 * rope.D, act), _arg("k_weight", k_weight, 2 * rope.D, act),
-            eps, _arg("pos", pos, 4 * T, i32), *args[6:], head_stride, row_stride, k_plane, v_plane,
+            _arg("seqs", seqs, 4 * n, i32), _arg("starts", starts, 4 * n + 4, i32), n, T, qp, qs, kp, ks,
+            vp, vs, _arg("q_weight", q_weight, 2 * D, act), _arg("k_weight", k_weight, 2 * D, act),
+            eps, _arg("pos", pos, 4 * T, i32), op, os, head_stride, row_stride, k_plane, v_plane,
             _stream(stream))
         if status != OK:
             raise BsgemvError(status, "bsgemv_cache_append")
