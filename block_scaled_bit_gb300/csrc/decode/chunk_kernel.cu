@@ -6,7 +6,9 @@
 namespace bsg {
 namespace {
 
-constexpr int kSetup = 1024;
+// Threads of the block that writes the lines down.  Up to 128 entries 128 are enough: a call of eight takes
+// 25.8 us then and 26.6 with 1024, whose sums go over 32 warps.  With more entries 1024 take fewer steps.
+constexpr int kSetup = 1024, kSetupFew = 128;
 
 BSG_DEV int chunk_sum(int a, int b) { return min(a + b, kChunkMost); }
 BSG_DEV int2 chunk_sum(int2 a, int2 b) { return make_int2(chunk_sum(a.x, b.x), chunk_sum(a.y, b.y)); }
@@ -14,9 +16,10 @@ BSG_DEV int2 shift_up(int2 v, int d) {
   return make_int2(__shfl_up_sync(~0u, v.x, d), __shfl_up_sync(~0u, v.y, d));
 }
 
-// Exclusive prefix sums over the block of kSetup threads, stopping at kChunkMost; totals in *sum.
+// Exclusive prefix sums over the block of N threads, stopping at kChunkMost; totals in *sum.
+template <int N>
 BSG_DEV int2 chunk_scan(int2 v, int2* sum) {
-  __shared__ int2 warp_sum[32];
+  __shared__ int2 warp_sum[N / 32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int2 inc = v;
 #pragma unroll
@@ -28,7 +31,7 @@ BSG_DEV int2 chunk_scan(int2 v, int2* sum) {
   if (lane == 0) before = make_int2(0, 0);
   if (lane == 31) warp_sum[w] = inc;
   __syncthreads();
-  int2 s = warp_sum[lane];  // (every warp works the warps' sums out)
+  int2 s = lane < N / 32 ? warp_sum[lane] : make_int2(0, 0);  // (every warp works the warps' sums out)
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int2 o = shift_up(s, d);
@@ -64,19 +67,20 @@ BSG_DEV ChunkEntry chunk_entry(const ChunkParams& p, int i) {
   return e;
 }
 
-// The lines of work, by one block, 1024 entries at a time: what they are into shared memory, sums of their row blocks, then the row
-// blocks, 1024 of a line at a time, each of which finds its entry by halving.
-__global__ void __launch_bounds__(kSetup)
+// The lines of work, by one block, N entries at a time: what they are into shared memory, sums of their row blocks, then the row
+// blocks, N of a line at a time, each of which finds its entry by halving.
+template <int N>
+__global__ void __launch_bounds__(N)
     chunk_setup(const __grid_constant__ ChunkParams p, const __grid_constant__ ChunkKinds kinds) {
-  __shared__ int seq[kSetup], tok0[kSetup], pos0[kSetup], rows[kSetup], first[2][kSetup];
+  __shared__ int seq[N], tok0[N], pos0[N], rows[N], first[2][N];
   pdl_wait();
   pdl_launch_dependents();
   const int G = p.Hq / p.Hkv;
   int2 total = make_int2(0, 0), stretch = total, sum;
   int any = 0;
   bool over = false;
-  for (int base = 0; base < p.n; base += kSetup) {
-    const int i = base + threadIdx.x, many = min(p.n - base, kSetup);
+  for (int base = 0; base < p.n; base += N) {
+    const int i = base + threadIdx.x, many = min(p.n - base, N);
     int2 need = make_int2(0, 0);
     if (i < p.n) {
       const ChunkEntry e = chunk_entry(p, i);
@@ -90,7 +94,7 @@ __global__ void __launch_bounds__(kSetup)
       pos0[threadIdx.x] = e.pos0;
       rows[threadIdx.x] = static_cast<int>(live);  // (T * Hq is below 2^28)
     }
-    const int2 before = chunk_sum(total, chunk_scan(need, &sum));
+    const int2 before = chunk_sum(total, chunk_scan<N>(need, &sum));
     const int2 after = chunk_sum(total, sum);
     first[0][threadIdx.x] = before.x;
     first[1][threadIdx.x] = before.y;
@@ -98,7 +102,7 @@ __global__ void __launch_bounds__(kSetup)
     over |= after.x > p.tensor.max_blocks || after.y > p.stream.max_blocks;  // (entries on the same rows)
     if (over) break;
     const int steps = max(after.x - total.x, after.y - total.y);
-    for (int s0 = 0; s0 < steps; s0 += kSetup) {
+    for (int s0 = 0; s0 < steps; s0 += N) {
       int2 len = make_int2(0, 0);
       ChunkBlock b[2] = {};
 #pragma unroll
@@ -121,7 +125,7 @@ __global__ void __launch_bounds__(kSetup)
         b[k].tiles = (s.hi + kinds.keys[k] - 1) / kinds.keys[k] - b[k].tile0;
         (k ? len.y : len.x) = b[k].tiles + kChunkCost;
       }
-      const int2 cum = chunk_sum(stretch, chunk_scan(len, &sum));
+      const int2 cum = chunk_sum(stretch, chunk_scan<N>(len, &sum));
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int x = (k ? total.y : total.x) + s0 + threadIdx.x;
@@ -147,7 +151,7 @@ __global__ void __launch_bounds__(kSetup)
     if (over) atomicOr(&p.head->err, kErrChunkLine);
   }
   if (over)
-    for (int i = threadIdx.x; i < p.n; i += kSetup) {
+    for (int i = threadIdx.x; i < p.n; i += N) {
       const ChunkEntry e = chunk_entry(p, i);
       p.fills[i] = make_int2(e.tok0, e.count);
     }
@@ -156,7 +160,8 @@ __global__ void __launch_bounds__(kSetup)
 }  // namespace
 
 int launch_chunk_setup(const ChunkParams& p, const ChunkKinds& kinds, cudaStream_t s) {
-  return decode_launch(chunk_setup, dim3(1), dim3(kSetup), 0, s, p, kinds);
+  if (p.n <= kSetupFew) return decode_launch(chunk_setup<kSetupFew>, dim3(1), dim3(kSetupFew), 0, s, p, kinds);
+  return decode_launch(chunk_setup<kSetup>, dim3(1), dim3(kSetup), 0, s, p, kinds);
 }
 
 ChunkLayout chunk_layout(int Hq, int Hkv, int D, int max_n, int max_T, int sms) {
