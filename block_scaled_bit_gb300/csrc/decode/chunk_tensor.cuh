@@ -52,9 +52,9 @@ struct ChunkTile {
   static constexpr int kBars = 3 * kRing + 2 + 8 * kStreams + 3;
   static constexpr int kOffWords = kOffBar + 8 * kBars;
   static constexpr int kWords = 20 + 4 * kRing;         // notes, then the guard's flags of each slot
-  // what the two threads of a row tell each other, a float each; and stream 1's tell stream 0
+  // two floats a thread of a stream for its row's other one (D = 256), or stream 1's maxima and sums
   static constexpr int kOffTell = (kOffWords + 4 * kWords + 15) / 16 * 16;
-  static constexpr int kOffSeg = kOffTell + 1024 * kStreams;   // the softmax warps' segment, and the next two
+  static constexpr int kOffSeg = kOffTell + 2 * 1024;   // the softmax warps' segment, and the next two
   static constexpr int kSmem = kOffSeg + 3 * 80;
   static constexpr int kHalves = D == 256 ? 2 : 1;      // threads that share a row
   static constexpr int kSoft = 4 * kHalves;             // softmax warps of a stream
@@ -742,6 +742,23 @@ struct ChunkTensor {
     uint32_t both;    // times that it met its row's other thread
   };
 
+  // (two threads a row) The two warps of these rows have both come.
+  static BSG_DEV bool meet(const Ctx& c, int stream, int tid, Counts& n) {
+    const uint32_t bar = c.both(stream, (tid >> 5) & 3);
+    arrive_warp(bar, tid & 31);
+    return wait_warp(c, bar, n.both++ & 1u);
+  }
+  // `mine` for the row's other thread, and what that one has.  The words are those of every other meeting:
+  // a thread writes one again only after the next meeting, to which the other one comes after it has read it.
+  static BSG_DEV bool exchange(const Ctx& c, int stream, int tid, Counts& n, float mine, float& other) {
+    static_assert(T::kHalves == 1 || T::kStreams == 1, "one stream's words");
+    float* word = reinterpret_cast<float*>(c.base + T::kOffTell) + (n.both & 1u) * 256;
+    word[tid] = mine;
+    if (!meet(c, stream, tid, n)) return false;
+    other = word[tid ^ 128];
+    return true;
+  }
+
   // The segment lies in shared memory, and the one after it: what a thread keeps in registers besides
   // its scores would go to local memory, which is L2's with this much shared memory.
   static BSG_DEV bool softmax(const Ctx& c, int stream, int tid) {
@@ -803,8 +820,6 @@ struct ChunkTensor {
       pos = g.b.pos0 + row.tok;
       if (MODE != kChunkPlain && p.slopes) slope = __ldg(p.slopes + row.head) * kLog2e;
     }
-    // this thread's word for its row's other one, and that one's for it
-    float* tell = reinterpret_cast<float*>(c.base + T::kOffTell) + stream * 256;
     float m = -INFINITY, l = 0.f;  // m: the maximum that O and l are scaled to; l: of its positions
     bool seen = false;             // some of the tiles had positions that this row sees
     for (int t = my.a; t < my.b; t += my.step, ++n.job) {
@@ -821,10 +836,9 @@ struct ChunkTensor {
       if (MODE == kChunkAhead || cut) prepare(p, ts, f, cut, a, b);
       float top = look_at(ts, f, raw);
       if (T::kHalves == 2) {  // the other half's
-        tell[tid] = top;
-        arrive_warp(c.both(stream, quad), lane);
-        if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
-        top = fmaxf(top, tell[tid ^ 128]);
+        float other;
+        if (!exchange(c, stream, tid, n, top, other)) return false;
+        top = fmaxf(top, other);
       }
       // O and l move to a new maximum when it is more than 8 above theirs (or the first)
       const bool grow = top > m + 8.f;
@@ -876,8 +890,7 @@ struct ChunkTensor {
         if (bad) {
           if (T::kHalves == 2) {  // (the other half's P is there)
             tc_before();
-            arrive_warp(c.both(stream, quad), lane);
-            if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
+            if (!meet(c, stream, tid, n)) return false;
           }
           tc_after();
           add_not_finite(c, g, pos, half, tile, slot, ts - half * H, to, t == my.a);
@@ -896,13 +909,9 @@ struct ChunkTensor {
       ahead = true;
     }
     if (T::kHalves == 2) {  // the row's sum
-      tell[tid] = l;
-      arrive_warp(c.both(stream, quad), lane);
-      if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
-      l += tell[tid ^ 128];
-      // (the other thread has read it too before the words are used again)
-      arrive_warp(c.both(stream, quad), lane);
-      if (!wait_warp(c, c.both(stream, quad), n.both++ & 1u)) return false;
+      float other;
+      if (!exchange(c, stream, tid, n, l, other)) return false;
+      l += other;
     }
     const uint32_t jobs = my.count();
     const bool join = g.pair && g.n > 1;
