@@ -342,7 +342,10 @@ struct ChunkTensor {
           if (!wait_warp(c, c.full(r.slot), r.phase)) return false;
           if (kv && partial(g, tile)) clean(c, s, tile, r.slot, lane);
           __syncwarp();
-          if (lane == 0) mbar_arrive(c.vok(r.slot));
+          if (lane == 0) {
+            mbar_arrive(c.vok(r.slot));
+            mbar_arrive(c.empty(r.slot));
+          }
         }
       }
       if (g.end == c.x1) return true;
@@ -391,8 +394,9 @@ struct ChunkTensor {
                    : "memory");
   }
 
-  // The whole warp runs this; one elected lane issues.  A ring tile is free when every stream has
-  // given it back: with the commit of what read it, or at once where it is not the stream's.
+  // The whole warp runs this; one elected lane issues.  A ring tile is free when every stream and the guard
+  // have given it back: with the commit of what read it, or at once where it is not the stream's.  (The guard
+  // too: a K tile does not wait for it, and it would miss a slot's filling if another came before it looked.)
   static BSG_DEV bool issue(const Ctx& c, uint32_t stream) {
     const bool lead = elect_one();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, c.tmem, 0);
@@ -1032,7 +1036,7 @@ struct ChunkTensor {
     if (threadIdx.x == 0) {
       for (int i = 0; i < T::kRing; ++i) {
         mbar_init(c.full(i), 1);
-        mbar_init(c.empty(i), T::kStreams);
+        mbar_init(c.empty(i), T::kStreams + 1);
         mbar_init(c.vok(i), 1);
       }
       for (int i = 0; i < 2; ++i) mbar_init(c.bar(Ctx::kS + i), 1);

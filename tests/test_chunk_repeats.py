@@ -37,3 +37,28 @@ def test_maxima_that_two_threads_share(act, new, past):
         pr.k[page, :, row] = keys.to(pr.k.dtype)[:, None].expand(-1, 2, -1)
     pr.q.copy_((4 * q + 0.01 * torch.randn(pr.q.shape, device="cuda")).to(pr.q.dtype))
     repeats(pr)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act,Hq,Hkv,D,new,past,window", [
+    ("bf16", 4, 4, 64, [1500], [0], 70),        # all tiles but the first are seen in part by every row block
+    ("f16", 16, 4, 128, [700, 300], [900, 5], 150),
+    ("bf16", 8, 4, 128, [40, 20], [3000, 2000], 2900),   # both streams on the same rows
+    ("f16", 8, 2, 256, [400], [1000], 50),
+])
+def test_tiles_that_are_looked_at_before_their_products(act, Hq, Hkv, D, new, past, window):
+    """The guard is busy with nearly every V tile, whose values NaN lies between; K tiles pass it in the
+    meantime, and their slots of the ring are filled again."""
+    import torch
+    repeats(Chunk(torch, act, Hq, Hkv, D, 16, new, past, seed=23, junk=float("nan")), window=window)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act,Hq,Hkv,D,new,past", [
+    ("bf16", 32, 8, 128, [300], [6000]),        # long ranges: every slot of the ring many times
+    ("f16", 8, 8, 64, [130, 700, 17], [2000, 0, 4000]),
+    ("bf16", 8, 2, 256, [200], [5000]),
+])
+def test_long_ranges(act, Hq, Hkv, D, new, past):
+    import torch
+    repeats(Chunk(torch, act, Hq, Hkv, D, 16, new, past, seed=29))
