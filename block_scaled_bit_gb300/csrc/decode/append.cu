@@ -52,12 +52,15 @@ struct AppendParams {
   const unsigned long long* freqs;
 };
 
+// What the kernel before may still write while this one is resident (starts, seqs, lens, tables, pos) is read
+// past L1, never by the read-only path, whose data may not change in a kernel's life.
+//
 // The entry of row r: the first i with r < starts[i + 1], by the warp, 32 ways a step.  n if none.
 BSG_DEV int entry_of(const int32_t* starts, int n, int r, int lane) {
   int lo = 0, hi = n;  // starts[lo] <= r, and the entry is in [lo, hi] (lo = 0 not looked at yet)
   while (hi - lo > 32) {
     const int step = (hi - lo + 31) / 32, at = min(lo + (lane + 1) * step, hi);
-    const unsigned m = __ballot_sync(0xFFFFFFFFu, __ldg(starts + at) > r);
+    const unsigned m = __ballot_sync(0xFFFFFFFFu, __ldcg(starts + at) > r);
     const int first = m ? __ffs(m) - 1 : 32;  // the entry is before lo + (first + 1) * step
     if (first == 32) return n;
     const int base = lo;
@@ -65,7 +68,7 @@ BSG_DEV int entry_of(const int32_t* starts, int n, int r, int lane) {
     hi = min(base + (first + 1) * step, hi);
   }
   const int at = lo + 1 + lane;
-  const unsigned m = __ballot_sync(0xFFFFFFFFu, at <= hi && __ldg(starts + at) > r);
+  const unsigned m = __ballot_sync(0xFFFFFFFFu, at <= hi && __ldcg(starts + at) > r);
   return m ? lo + __ffs(m) - 1 : n;
 }
 
@@ -164,17 +167,17 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 5)
   if (p.q) q_ahead = fetch(q_row, q_first, p.Hq);
 
   const int e = entry_of(p.starts, p.n, r, lane);
-  if (e >= p.n || r < __ldg(p.starts + e)) return;
-  const int s = __ldg(p.seqs + e);
+  if (e >= p.n || r < __ldcg(p.starts + e)) return;
+  const int s = __ldcg(p.seqs + e);
   if (s < 0 || s >= p.max_seqs) return;
   const int64_t most = static_cast<int64_t>(p.max_pages) * p.page_size;
-  const int64_t len = min(static_cast<int64_t>(__ldg(p.lens + s)), most);
-  const int64_t at = len - (static_cast<int64_t>(__ldg(p.starts + e + 1)) - r);
+  const int64_t len = min(static_cast<int64_t>(__ldcg(p.lens + s)), most);
+  const int64_t at = len - (static_cast<int64_t>(__ldcg(p.starts + e + 1)) - r);
   if (at < 0) return;
   int page = -1;
-  if (p.k) page = __ldg(p.tables + static_cast<int64_t>(s) * p.max_pages + at / p.page_size);
+  if (p.k) page = __ldcg(p.tables + static_cast<int64_t>(s) * p.max_pages + at / p.page_size);
 
-  const int pos = p.pos ? __ldg(p.pos + r) : static_cast<int>(at);
+  const int pos = p.pos ? __ldcg(p.pos + r) : static_cast<int>(at);
   for (int i = lane; i < p.rot / 2; i += 32) {
     // turns in [-1/2, 1/2): the product's upper word; sine and cosine of pi times it, doubled
     const unsigned long long f = __ldg(p.freqs + i);
@@ -194,8 +197,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 5)
 #pragma unroll
       for (int i = 0; i < 4; ++i) u.first[i] = u.second[i] = f32x2(1.f, 1.f);
       if (weight && in)
-        u = unpack<BF16, INTER>(__ldg(reinterpret_cast<const uint4*>(weight + c0)),
-                                __ldg(reinterpret_cast<const uint4*>(weight + c1)));
+        u = unpack<BF16, INTER>(*reinterpret_cast<const uint4*>(weight + c0),
+                                *reinterpret_cast<const uint4*>(weight + c1));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // (elements that are not turned: by a cosine of 1)
