@@ -717,19 +717,27 @@ class PageCache(_Handle):
             _arg("seqs", seqs, 4 * n, i32), _arg("starts", starts, 4 * n + 4, i32),
             _arg("grown", grown, 4 * n, i32), n, _stream(stream)), "bsgemv_cache_grow")
 
-    def append(self, rope, pool, tables, lens, seqs, starts, q, k, v, q_out, head_stride: int = 0,
-               row_stride: int = 0, k_plane: int = 0, v_plane: int = 0, q_weight=None,
+    def append(self, rope, pool, tables, lens, seqs, starts, q, k, v, q_out,
+               head_stride: int | None = None, row_stride: int | None = None,
+               k_plane: int | None = None, v_plane: int | None = None, q_weight=None,
                k_weight=None, eps: float = 1e-6, pos=None, stream=None) -> None:
         """q [T, Hq, D], normalised (q_weight [D]) and rotated, to q_out [T, Hq, D]; k [T, Hkv, D]
         likewise (k_weight), and v as it is, to the places of the new tokens: rows starts[i] ..
         starts[i + 1] - 1 are the last tokens of sequence seqs[i].  q, k, v and q_out: any stride
-        between rows; q and q_out, or k and v, may be None.  pos [T]: other positions to rotate by."""
+        between rows; q and q_out, or k and v, may be None.  With k and v, where they go: the strides
+        (elements) of a page's heads and rows, and the planes.  pos [T]: other positions to rotate by."""
         n, i32, act, D = seqs.shape[0], self._i32, rope._act, rope.D
+        if q is None and k is None:
+            raise BsgemvError(ERR_INVALID_ARG, "bsgemv_cache_append")
         T = (k if q is None else q).shape[0]
         # (spelt out: a call for one token is as long as its arguments take)
         qp = kp = vp = op = None
         qs = ks = vs = os = 0
         bad = False
+        if k is None:
+            head_stride = row_stride = k_plane = v_plane = 0
+        elif head_stride is None or row_stride is None or k_plane is None or v_plane is None:
+            bad = True
         if q is not None:
             qp, (qs, sh, s1) = q.data_ptr(), q.stride()
             bad |= q.shape != (T, rope.Hq, D) or s1 != 1 or sh != D and rope.Hq > 1 or q.dtype not in act

@@ -362,7 +362,9 @@ int bsgemv_cache_append(bsgemv_cache_t c, bsgemv_rope_t rope, void* pool, const 
       (q && (q_stride % 8 || q_out_stride % 8)) ||
       (k && (k_stride % 8 || v_stride % 8 || head_stride % 8 || row_stride % 8)))
     return BSGEMV_ERR_MISALIGNED;
-  if (k && !page_holds(c, rope->Hkv, rope->D, head_stride, row_stride)) return BSGEMV_ERR_INVALID_ARG;
+  if (k && (!page_holds(c, rope->Hkv, rope->D, head_stride, row_stride) ||
+            !page_apart(c, rope->Hkv, rope->D, head_stride, row_stride) || k_plane == v_plane))
+    return BSGEMV_ERR_INVALID_ARG;
   if (rope->device != c->device) return BSGEMV_ERR_WRONG_DEVICE;
   const int rc = decode_check_device(c->device);
   if (rc != BSGEMV_OK) return rc;

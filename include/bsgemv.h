@@ -627,7 +627,8 @@ int bsgemv_rope_destroy(bsgemv_rope_t rope);
  * and v (starts: int32 [n + 1], device, not decreasing) are the last tokens of sequence seqs[i],
  * i < n: row r has position lens[seqs[i]] - (starts[i + 1] - r).  Queries, normalised and rotated
  * as `rope` says, go to q_out; keys likewise, and values as they are, to their places in the pages,
- * in planes k_plane and v_plane, as bsgemv_cache_write puts them.  So a call follows
+ * in planes k_plane and v_plane, as bsgemv_cache_write puts them: strides by which two heads or
+ * rows of a page share an element, and one plane for both, are refused.  So a call follows
  * bsgemv_cache_grow (or _extend), for the entries that grew.
  *
  * q: head h of row r at q + r * q_stride + h * D elements (Hq heads), k and v likewise (Hkv heads),
