@@ -10,9 +10,9 @@ namespace {
 
 // Rows r0, r0 + step, ... (R of them, below `rows`) of a cut unit, by a warp: their parts put together,
 // two at a time of all the rows at once.  The first two parts' rows are fetched with all the maxima and
-// sums: where they lie is known.
+// sums: where they lie is known.  Returns which of the rows have something that is not finite.
 template <bool BF16, int D, int ROWS, int R>
-BSG_DEV void finish_rows(const ChunkParams& p, const ChunkLine& line, const ChunkCut& cut, int r0, int step,
+BSG_DEV unsigned finish_rows(const ChunkParams& p, const ChunkLine& line, const ChunkCut& cut, int r0, int step,
                          int lane) {
   constexpr int kPer = D / 32, kVec = kPer < 4 ? kPer : 4;
   const int G = p.Hq / p.Hkv;
@@ -94,6 +94,7 @@ BSG_DEV void finish_rows(const ChunkParams& p, const ChunkLine& line, const Chun
         }
     }
   }
+  unsigned again = 0u;  // rows with something that is not finite
 #pragma unroll
   for (int j = 0; j < R; ++j) {
     const int r = r0 + j * step;
@@ -101,20 +102,30 @@ BSG_DEV void finish_rows(const ChunkParams& p, const ChunkLine& line, const Chun
     const int at = cut.row0 + r, tok = at / G;
     const int64_t to = static_cast<int64_t>(cut.tok0 + tok) * p.Hq + cut.head * G + at - tok * G;
     const float inv = 1.f / l[j];
+    uint32_t watch = 0u;
 #pragma unroll
-    for (int x = 0; x < kPer; x += 2)
-      *reinterpret_cast<uint32_t*>(p.out + to * D + x / kVec * (32 * kVec) + lane * kVec + x % kVec) =
-          AttnStream<BF16, 64>::pack(o[j][x] * inv, o[j][x + 1] * inv);
+    for (int x = 0; x < kPer; x += 2) {
+      const uint32_t word = AttnStream<BF16, 64>::pack(o[j][x] * inv, o[j][x + 1] * inv);
+      watch = chunk_watch<BF16>(word, watch);
+      *reinterpret_cast<uint32_t*>(p.out + to * D + x / kVec * (32 * kVec) + lane * kVec + x % kVec) = word;
+    }
+    // (l: with weights that are numbers)
+    if (__any_sync(0xFFFFFFFFu, chunk_not_finite<BF16>(watch) != 0u) && l[j] > 0.f && l[j] < INFINITY)
+      again |= 1u << j;
     if (lane == 0 && p.lse) p.lse[to] = (m[j] + log2f(l[j])) * 0.6931471805599453f;
   }
+  return again;
 }
 
 constexpr int kFinishWarps = 8;
 
 // Units that a cut went through, and the rows to fill.  Block (w, y): the unit noted by range w + 1 of
 // the streaming kernel (y = 0: two rows a warp) or the tensor-memory kernel (four a warp).
+// (As many blocks an SM as the rows in registers allow; one at D = 256, with 140 registers, and a call of
+// three chunks over a window takes 138 us in place of 134.)
 template <bool BF16, int D>
-__global__ void __launch_bounds__(32 * kFinishWarps) chunk_finish(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(32 * kFinishWarps, D == 256 ? 2 : (D == 128 ? 3 : 4))
+    chunk_finish(const __grid_constant__ ChunkParams p) {
   constexpr int kRows = D == 256 ? 128 : 256;
   pdl_launch_dependents();
   pdl_wait();
@@ -140,12 +151,16 @@ __global__ void __launch_bounds__(32 * kFinishWarps) chunk_finish(const __grid_c
     }
   }
   if (blocks == 0) return;  // (its kernel may not have run, and has noted nothing then)
-  const ChunkCut cut = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, 0};
-  if (stream) {
-    if (warp < cut.rows) finish_rows<BF16, D, kChunkRows, 2>(p, line, cut, warp, kFinishWarps, lane);
-  } else {
-    const int r = (blockIdx.y - 1) * (4 * kFinishWarps) + warp;
-    if (r < cut.rows) finish_rows<BF16, D, kRows, 4>(p, line, cut, r, kFinishWarps, lane);
+  const ChunkCut cut = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const int r0 = stream ? warp : (blockIdx.y - 1) * (4 * kFinishWarps) + warp;
+  if (r0 >= cut.rows) return;
+  const unsigned again = stream ? finish_rows<BF16, D, kChunkRows, 2>(p, line, cut, r0, kFinishWarps, lane)
+                                : finish_rows<BF16, D, kRows, 4>(p, line, cut, r0, kFinishWarps, lane);
+  if (again) {
+    const ChunkBlock b = chunk_block(line, cut.block);
+    const int G = p.Hq / p.Hkv, at = cut.row0 + r0 + lane * kFinishWarps, tok = at / G;  // (lane j's: row j)
+    chunk_look_again<BF16, D>(p, again, b.seq, cut.head, b.pos0 + tok,
+                              static_cast<int64_t>(cut.tok0 + tok) * p.Hq + cut.head * G + at - tok * G, 0, D);
   }
 }
 

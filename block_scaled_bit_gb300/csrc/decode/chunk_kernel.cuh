@@ -52,7 +52,7 @@ struct alignas(16) ChunkCut {
   int slot0;    // its first part
   int next;     // its second part; the others follow, every second slot
   int count;    // parts
-  int pad;
+  int block;    // its row block
 };
 
 // One kernel's line of work.

@@ -132,7 +132,7 @@ BSG_DEV void chunk_note_cut(const ChunkLine& line, const ChunkRange& r, int Hkv,
     if (w == w0 + 1 && w <= w1)
       // (the first part lies in its range's first slot if the range begins with the unit or inside it)
       c = ChunkCut{g.b.rows, g.b.tok0, g.b.row0, g.head, 2 * w0 + (begin <= chunk_start(r.s, w0) ? 0 : 1),
-                   2 * w, w1 - w0 + 1, 0};
+                   2 * w, w1 - w0 + 1, g.e};
   }
   line.cuts[w] = c;
 }

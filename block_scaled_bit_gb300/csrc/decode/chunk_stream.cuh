@@ -15,6 +15,7 @@
 
 #include "attn_stream.cuh"
 #include "chunk_line.cuh"
+#include "chunk_values.cuh"
 
 namespace bsg {
 
@@ -116,10 +117,7 @@ struct ChunkStream {
     return c.p.a.q + (g.b.tok0 + r.tok) * c.p.a.q_stride + static_cast<int64_t>(r.head) * D;
   }
 
-  static BSG_DEV uint32_t not_finite(uint32_t w) {  // bit 15 or 31 set: that half is not finite
-    constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
-    return ((w & kExp) + kOne) & 0x80008000u;
-  }
+  static BSG_DEV uint32_t not_finite(uint32_t w) { return chunk_not_finite<BF16>(w); }
 
   struct Acc {
     float o[D / 8][4];   // rows g and g + 8: columns 8 n + 2 t, + 1
@@ -328,6 +326,7 @@ struct ChunkStream {
     constexpr int kPer = D / 32, kVec = kPer < 4 ? kPer : 4;
     float* part = p.stream.parts + (2 * static_cast<int64_t>(blockIdx.x) + (g.from == c.x0 ? 0 : 1)) *
                                        chunk_slot_floats(kChunkRows, D);
+    unsigned again = 0u;  // rows with something that is not finite
 #pragma unroll 1
     for (int r = c.warp; r < g.b.rows; r += kChunkWarps) {
       float m[kChunkWarps], l = 0.f, top = -INFINITY, o[kPer] = {};
@@ -350,10 +349,15 @@ struct ChunkStream {
         const Row at = row_of(c, g, r);
         const int64_t to = static_cast<int64_t>(g.b.tok0 + at.tok) * p.Hq + at.head;
         const float inv = 1.f / l;
+        uint32_t watch = 0u;
 #pragma unroll
-        for (int x = 0; x < kPer; x += 2)
-          *reinterpret_cast<uint32_t*>(p.out + to * D + x / kVec * (32 * kVec) + c.lane * kVec + x % kVec) =
-              A::pack(o[x] * inv, o[x + 1] * inv);
+        for (int x = 0; x < kPer; x += 2) {
+          const uint32_t word = A::pack(o[x] * inv, o[x + 1] * inv);
+          watch = chunk_watch<BF16>(word, watch);
+          *reinterpret_cast<uint32_t*>(p.out + to * D + x / kVec * (32 * kVec) + c.lane * kVec + x % kVec) = word;
+        }
+        // (l: with weights that are numbers)
+        if (__any_sync(0xFFFFFFFFu, not_finite(watch) != 0u) && l > 0.f && l < INFINITY) again |= 1u << r;
         if (c.lane == 0 && p.lse) p.lse[to] = (top + log2f(l)) * 0.6931471805599453f;
       } else {
 #pragma unroll
@@ -365,6 +369,11 @@ struct ChunkStream {
           __stcg(part + kChunkRows * (D + 1) + r, l);
         }
       }
+    }
+    if (again) {
+      const Row at = row_of(c, g, c.lane);  // (the lane's)
+      chunk_look_again<BF16, D>(p, again, g.b.seq, g.head, g.b.pos0 + at.tok,
+                                static_cast<int64_t>(g.b.tok0 + at.tok) * p.Hq + at.head, 0, D);
     }
   }
 

@@ -29,11 +29,12 @@
 // Places that a row does not see must not reach it, whatever they hold.  Keys: their scores are
 // replaced.  Values: a weight of 0 times NaN or infinity is NaN, so a warp (the guard) looks at the V
 // tiles that some row does not see all of before they are used: what nobody sees becomes 0; what is
-// not finite too, and the rows that do see it add it by hand.
+// not finite too, and the rows that do see it add it by hand.  (What comes of such values: chunk_values.cuh.)
 #pragma once
 
 #include "attn_prefix.cuh"
 #include "chunk_line.cuh"
+#include "chunk_values.cuh"
 
 namespace bsg {
 
@@ -288,10 +289,7 @@ struct ChunkTensor {
   static BSG_DEV bool partial(const Seg& g, int tile) {
     return (tile + 1) * K > g.hi_all || tile * K < g.lo_all;
   }
-  static BSG_DEV uint32_t not_finite(uint32_t w) {  // bit 15 or 31 set: that half is not finite
-    constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
-    return ((w & kExp) + kOne) & 0x80008000u;
-  }
+  static BSG_DEV uint32_t not_finite(uint32_t w) { return chunk_not_finite<BF16>(w); }
   static BSG_DEV uint32_t finite_or_zero(uint32_t w) {
     const uint32_t bad = not_finite(w);
     return w & ~((bad & 0x8000u ? 0xFFFFu : 0u) | (bad & 0x80000000u ? 0xFFFF0000u : 0u));
@@ -974,8 +972,10 @@ struct ChunkTensor {
     const int at = (g.pair ? 0 : 128 * stream) + r128;
     const float inv = 1.f / l;
     int64_t mine = -1;  // where the row begins, in bytes; < 0: no row
+    int pos = 0;
     if (at < g.b.rows) {
       const Row row = row_of(c, g, at);
+      pos = g.b.pos0 + row.tok;
       const int64_t r = static_cast<int64_t>(g.b.tok0 + row.tok) * p.Hq + row.head;
       mine = g.whole ? r * D * 2 : static_cast<int64_t>(at) * D * 4;
       if (half == 0 && g.whole) {
@@ -989,6 +989,7 @@ struct ChunkTensor {
     // a thread writes its row's columns, 32 bytes (a sector) at a time
     uint8_t* dst = (g.whole ? reinterpret_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(part)) + mine;
     const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+    uint32_t watch = 0u;
 #pragma unroll 1
     for (int i = d0; i < d1; i += 32) {
       uint32_t o[32];
@@ -1007,6 +1008,8 @@ struct ChunkTensor {
 #pragma unroll
         for (int y = 0; y < 16; ++y)
           o[y] = pack(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv);
+#pragma unroll
+        for (int y = 0; y < 16; ++y) watch = chunk_watch<BF16>(o[y], watch);
         if (wide) {
           store_sector(dst + 2 * i, o);
           store_sector(dst + 2 * i + 32, o + 8);
@@ -1020,6 +1023,9 @@ struct ChunkTensor {
         for (int y = 0; y < 32; y += 8) store_sector(dst + 4 * i + 4 * y, o + y);
       }
     }
+    // (l: with weights that are numbers)
+    const unsigned again = __ballot_sync(0xFFFFFFFFu, not_finite(watch) != 0u && l > 0.f && l < INFINITY);
+    if (again) chunk_look_again<BF16, D>(p, again, g.b.seq, g.head, pos, mine / (2 * D), d0, d1);
     return true;
   }
 

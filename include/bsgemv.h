@@ -482,8 +482,10 @@ int bsgemv_attn_destroy(bsgemv_attn_plan_t plan);
  * not reach it, NaN and infinities included.
  *
  * q: head h of row r at q + r * q_stride + h * D elements, out [T][Hq][D] and lse [T][Hq] (fp32, or
- * NULL) contiguous, dtypes, cache layout and strides as bsgemv_attn_run.  NaN and infinities among
- * what a row sees act as there.
+ * NULL) contiguous, dtypes, cache layout and strides as bsgemv_attn_run.  NaN among a row's scores, or a
+ * score of +inf, gives NaN in its out and lse; a row all of whose scores are -inf gets NaN in out and -inf
+ * in lse.  Otherwise a column of out is infinite where an infinity is among the column's values that the
+ * row sees, and NaN where infinities of both signs or NaN are (a weight of 0 or not).
  */
 typedef struct bsgemv_chunk_plan_s* bsgemv_chunk_plan_t;
 
