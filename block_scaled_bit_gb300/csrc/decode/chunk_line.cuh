@@ -145,14 +145,17 @@ BSG_DEV float chunk_rcp(float x) {
 // tanh(u), to 2^-20 of itself: 1 - 2 / (1 + e^2u), whose error is 2^-23, and near zero, where that is not
 // small beside the result, u - u^3 / 3 + 2 u^5 / 15 - 17 u^7 / 315 + 62 u^9 / 2835 (below 0.3 the next
 // term is 2^-23 of u).
+constexpr float kChunkNear = 0.3f, kChunkTwoLog2e = 2.8853900817779268f;
+constexpr float kChunkTanh3 = -1.f / 3.f, kChunkTanh5 = 2.f / 15.f, kChunkTanh7 = -17.f / 315.f,
+                kChunkTanh9 = 62.f / 2835.f;
 BSG_DEV float chunk_tanh(float u) {
   const float w = u * u;
-  float near = fmaf(w, 62.f / 2835.f, -17.f / 315.f), e;
-  near = fmaf(w, near, 2.f / 15.f);
-  near = fmaf(w, near, -1.f / 3.f);
+  float near = fmaf(w, kChunkTanh9, kChunkTanh7), e;
+  near = fmaf(w, near, kChunkTanh5);
+  near = fmaf(w, near, kChunkTanh3);
   near = fmaf(w * u, near, u);
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(u * 2.8853900817779268f));  // (2 log2 e)
-  return fabsf(u) < 0.3f ? near : fmaf(-2.f, chunk_rcp(1.f + e), 1.f);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(u * kChunkTwoLog2e));
+  return fabsf(u) < kChunkNear ? near : fmaf(-2.f, chunk_rcp(1.f + e), 1.f);
 }
 
 }  // namespace bsg

@@ -576,6 +576,21 @@ struct ChunkTensor {
   }
   static BSG_DEV uint64_t pair(uint32_t a, uint32_t b) { return f32x2(__uint_as_float(a), __uint_as_float(b)); }
 
+  // chunk_tanh, two at once: its two sides.
+  static BSG_DEV uint64_t tanh_near2(uint64_t u) {
+    const auto two = [](float x) { return f32x2(x, x); };
+    const uint64_t w = mul_f32x2(u, u);
+    uint64_t near = fma2(w, two(kChunkTanh9), two(kChunkTanh7));
+    near = fma2(w, near, two(kChunkTanh5));
+    near = fma2(w, near, two(kChunkTanh3));
+    return fma2(mul_f32x2(w, u), near, u);
+  }
+  static BSG_DEV uint64_t tanh_far2(uint64_t u) {
+    const uint64_t x = mul_f32x2(u, f32x2(kChunkTwoLog2e, kChunkTwoLog2e));
+    const uint64_t y = add2(f32x2(1.f, 1.f), f32x2(ex2(f32x2_lo(x)), ex2(f32x2_hi(x))));
+    return fma2(f32x2(-2.f, -2.f), f32x2(chunk_rcp(f32x2_lo(y)), chunk_rcp(f32x2_hi(y))), f32x2(1.f, 1.f));
+  }
+
   // What has to be done to a thread's scores before they are looked at: those that its row does not see
   // (not a <= i < b) become -inf; kChunkAhead: all become base-2 scores.  32 at a time, where they are:
   // most tiles need none of this, and code that has not run yet costs more than the extra way.
@@ -589,24 +604,30 @@ struct ChunkTensor {
         if (p.cap > 0.f) {
           constexpr float kLog2e = 1.4426950408889634f;
           const float in = fabsf(p.scale) / p.cap, top = p.cap * kLog2e;
-          if (p.cap <= 64.f) {
-            // cap - 2 cap / (1 + e^(2 x / cap)) is off by 2^-23 cap, here 2^-17 at most: what P keeps of
-            // itself.  (With the other form for all, 1024 tokens after 7168, 32/8 heads of 128, took 294 us
-            // in place of 234.)
-            const uint64_t in2 = f32x2(2.f * kLog2e * in, 2.f * kLog2e * in), top2 = f32x2(top, top);
-            const uint64_t two2 = f32x2(-2.f * top, -2.f * top);
+          // Where all of a warp's 32 columns are near zero, which a cap in common use leaves nearly all: no
+          // special functions.  (1024 tokens after 7168, 32/8 heads of 128, scores of spread 1.5: 225 us with a cap
+          // of 50, 242 of 20, 282 of 5, 144 without one.)
+          float far = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            far = AttnPrefix<BF16, 64>::max3(far, fabsf(__uint_as_float(raw[i])), fabsf(__uint_as_float(raw[i + 1])));
+          const uint64_t in2 = f32x2(in, in), top2 = f32x2(top, top);
+          if (__any_sync(0xFFFFFFFFu, far * in >= kChunkNear)) {
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              const uint64_t x = mul_f32x2(pair(raw[i], raw[i + 1]), in2);
-              const uint64_t y = add2(f32x2(ex2(f32x2_lo(x)), ex2(f32x2_hi(x))), f32x2(1.f, 1.f));
-              const uint64_t z = fma2(f32x2(chunk_rcp(f32x2_lo(y)), chunk_rcp(f32x2_hi(y))), two2, top2);
-              raw[i] = __float_as_uint(f32x2_lo(z));
-              raw[i + 1] = __float_as_uint(f32x2_hi(z));
+              const uint64_t u = mul_f32x2(pair(raw[i], raw[i + 1]), in2), n = tanh_near2(u), f = tanh_far2(u);
+              const float a = fabsf(f32x2_lo(u)) < kChunkNear ? f32x2_lo(n) : f32x2_lo(f);
+              const float b = fabsf(f32x2_hi(u)) < kChunkNear ? f32x2_hi(n) : f32x2_hi(f);
+              raw[i] = __float_as_uint(top * a);
+              raw[i + 1] = __float_as_uint(top * b);
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              raw[i] = __float_as_uint(top * chunk_tanh(__uint_as_float(raw[i]) * in));
+            for (int i = 0; i < 32; i += 2) {
+              const uint64_t z = mul_f32x2(top2, tanh_near2(mul_f32x2(pair(raw[i], raw[i + 1]), in2)));
+              raw[i] = __float_as_uint(f32x2_lo(z));
+              raw[i + 1] = __float_as_uint(f32x2_hi(z));
+            }
           }
         } else {
 #pragma unroll

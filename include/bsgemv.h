@@ -495,8 +495,8 @@ int bsgemv_chunk_plan(bsgemv_chunk_plan_t* out, int act_bf16, int Hq, int Hkv, i
                       int page_size, int max_n, int max_T);
 
 /* Enqueue the attention of T (1 .. max_T) rows in n (1 .. max_n) entries.  cap: 0 for none, or > 0
- * with scale / cap and cap * log2(e) finite in fp32; window: 0 for none, or >= 1; slopes: Hq fp32
- * (device) or NULL.  Alignment and strides as bsgemv_attn_run; table_stride >= max_pages.  Page ids
+ * with scale / cap and cap * log2(e) finite in fp32 (capped scores are right to 2^-20 of themselves
+ * and the error of the scores); window: 0 for none, or >= 1; slopes: Hq fp32 (device) or NULL.  Alignment and strides as bsgemv_attn_run; table_stride >= max_pages.  Page ids
  * outside 0 .. num_pages-1 are read as zeros.  Deterministic: repeated calls are bit-identical (the
  * bits of a row may depend on the entries beside it: they decide where sums are cut). */
 int bsgemv_chunk_run(bsgemv_chunk_plan_t plan, const void* q, int64_t q_stride, const void* k,
