@@ -12,7 +12,7 @@
 // scalar, with every lane its own 8 sines, took 4200 instructions a token of 48 heads and 45 us for 8192
 // tokens, 0.66 of the schedulers' slots.)
 // Angles: position times frequency modulo a turn, in 64-bit fixed point -- one integer product that
-// wraps where the turns are whole, so no position is too far for it.
+// wraps where the turns are whole, so no position is too far for it -- then rounded once to fp32.
 #include <math.h>
 #include <string.h>
 
@@ -179,11 +179,12 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 5)
 
   const int pos = p.pos ? __ldcg(p.pos + r) : static_cast<int>(at);
   for (int i = lane; i < p.rot / 2; i += 32) {
-    // turns in [-1/2, 1/2): the product's upper word; sine and cosine of pi times it, doubled
+    // turns in [-1/2, 1/2), all 64 bits rounded to fp32 (small angles keep their last bits); sine and cosine
+    // of pi times it, doubled
     const unsigned long long f = __ldg(p.freqs + i);
-    const int top = static_cast<int>((f * static_cast<unsigned long long>(static_cast<long long>(pos))) >> 32);
+    const long long turn = static_cast<long long>(f * static_cast<unsigned long long>(static_cast<long long>(pos)));
     float a, b;
-    sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &a, &b);  // 2^-31
+    sincospif(__ll2float_rn(turn) * 1.0842021724855044e-19f, &a, &b);  // 2^-63
     turn_of[i] = make_float2(b * p.factor, a * p.factor);
   }
   __syncwarp();
