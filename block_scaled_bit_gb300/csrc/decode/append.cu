@@ -292,11 +292,12 @@ int bsgemv_rope_plan(bsgemv_rope_t* out, int act_bf16, int Hq, int Hkv, int D, i
   unsigned long long turns[256] = {};
   for (int i = 0; i < rot / 2; ++i) {
     if (!isfinite(freqs[i]) || fabs(freqs[i]) >= 2147483648.0) return BSGEMV_ERR_INVALID_ARG;
-    // freqs / (2 pi) as a product and what its rounding left, the whole turns taken off
-    const double t = freqs[i] * kTurn, rest = fma(freqs[i], kTurn, -t) + freqs[i] * kTurnRest;
-    const double part = t - floor(t);  // (1 if t is a hair below a whole number: 0 then)
-    turns[i] = part >= 1.0 ? 0ull : static_cast<unsigned long long>(part * 18446744073709551616.0);
-    turns[i] += static_cast<unsigned long long>(static_cast<long long>(rest * 18446744073709551616.0));
+    // |freqs| / (2 pi) as a product and what its rounding left, the whole turns taken off (exact above zero),
+    // then the sign
+    const double f = fabs(freqs[i]), t = f * kTurn, rest = fma(f, kTurnRest, fma(f, kTurn, -t));
+    turns[i] = static_cast<unsigned long long>((t - floor(t)) * 18446744073709551616.0) +
+               static_cast<unsigned long long>(static_cast<long long>(rest * 18446744073709551616.0));
+    if (freqs[i] < 0.0) turns[i] = 0ull - turns[i];
   }
   int dev = -1, sms = 0;
   int rc = decode_device(&dev, &sms);

@@ -1,4 +1,4 @@
-"""The rotation's angles to their last bits.
+"""The rotation's angles to their last bits: sines near zero, and frequencies below it.
 
 Queries (1, 0): the rotated pair is factor (cos, sin), so each output shows its own error.  Of the value: sine
 and cosine 2 ulp, two products and the factor, below 2^-20; the output's rounding, 2^-11 and at least 2^-25.
@@ -51,3 +51,13 @@ def test_sines_near_zero(inter, factor):
     check(geometric(64, 500000.0, 8.0), factor, inter)
     check(geometric(16, 1e7), factor, inter)
 
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("factor", [1.0, 4096.0])
+def test_frequencies_below_zero(inter, factor):
+    """As exact as those above it, however small."""
+    check([-f for f in geometric(64, 500000.0, 8.0)], factor, inter)
+    check([f if p % 2 else -f for p, f in enumerate(geometric(16, 1e6))], factor, inter)
+    check([-1e-12, -3.0, -1e-13, 5e8, -5e8, 2.0 ** 30, -0.0, -3e-14], factor, inter)
