@@ -1,5 +1,7 @@
 """Growing and appending one after the other, nothing between them: an append is under way on the device
 before the growth has written the lengths and tables that it goes by, and has to see them all the same."""
+import gc
+
 import pytest
 
 from block_scaled_bit_gb300 import bsgemv
@@ -65,6 +67,7 @@ def test_append_sees_what_grow_has_written(act, n, counts):
         s.run()
         assert all(torch.equal(a, b) for a, b in zip(s.state, want))
     s.clear()
+    gc.collect()  # (a plan that is freed during the capture would end it)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         s.run()
@@ -73,3 +76,6 @@ def test_append_sees_what_grow_has_written(act, n, counts):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(s.state, want))
+    del graph
+    s.cache.close()
+    s.rope.close()
