@@ -1,8 +1,11 @@
 // append.cu -- new tokens' queries, keys and values on their way to attention: head norms, the
 // rotation by position, and keys and values into the pages of the cache, in one pass.
 //
-// Bound: every element of q, k and v is read once and written once; beyond some hundred tokens the
-// call is a copy, below it a chain of loads (row -> entry -> sequence -> length -> page).
+// Bound: every element of q, k and v is read once and written once; up to some hundred tokens the call is a
+// chain of loads (row -> entry -> sequence -> length -> page).  8192 tokens of 32/8 heads of 128 take 45 us
+// for 201 MB, 4.4 TB/s of the 6.7 that a copy has: latency, with 36 % of the issue slots used and most stalls
+// at loads.  A warp goes through the chain for one token, its queries' loads are one step ahead, those of keys
+// begin after the queries, those of values have none ahead.
 //
 // A lane works on 16 elements of a head at a time: 8 pairs of the rotation, which are two chunks of
 // 16 bytes in either layout (p and p + rot / 2: a chunk from each half; 2 p and 2 p + 1: two chunks

@@ -17,14 +17,20 @@
 //
 // Bound: the tensor cores, P V counted twice (P in two parts, as attn_prefix.cuh has it): some 3100 cycles of
 // MMAs for 128 positions and 256 rows of 128 d, of 3900 that they take; short units by their beginnings
-// and ends.  Measured, 32/8 heads of 128, bf16: 2048 tokens after 30720 positions 910 us, 1170 Tflop/s,
-// with the second part 1755 (cuBLAS: 1919, 1720 sustained); 1024 after 7168 144 us.  What it came from:
-// MMAs of the two streams mixed 1400 us (below: turns), taken in turn 1013, without local memory in the
-// softmax 957, P V by halves 928, the turn given on early 913.  Tiles of 64 positions with two score
-// buffers, as at D = 256, took 1140 (and 56 in place of 62 us for short prompts of 8/8 heads of 64).
+// and ends.  Measured, 32/8 heads of 128, bf16: 2048 tokens after 30720 positions 1042 us back to back, 1022
+// Tflop/s, with the second part 1533 (cuBLAS: 1720 sustained), and 940 for the first few calls, before the
+// power limit tells; 1024 after 7168 144 us.  What it came from, with pauses between calls: MMAs of the two
+// streams mixed 1400 us (below: turns), taken in turn 1013, without local memory in the softmax 957, P V by
+// halves 928, the turn given on early 913.  Tiles of 64 positions with two score buffers, as at D = 256, took
+// 1140 (and 56 in place of 62 us for short prompts of 8/8 heads of 64).
 // At D = 256 the tiles of 64 positions come through L2 at 37 bytes a cycle and SM, for 128 rows only: that
-// and the softmax make it 530 Tflop/s with a window and a cap.  Exponentials: 128 a row and tile take 1000
+// and the softmax make it 550 Tflop/s with a window and a cap.  Exponentials: 128 a row and tile take 1000
 // cycles of the special-function units, which bounds D = 64.
+//
+// Sums are fp32, but the tensor cores add 16 products to one at a time and cut off what does not fit: with two
+// parts a sum over n positions is cut n / 8 times, by half a unit of it on average, always towards zero.
+// Measured where a block has all of a row's n (f16): outputs 1.0e-5 of themselves too small after 6656
+// positions, 4.0e-5 after 31744, 1.5e-4 after 121024 (half a step of f16 is 2.4e-4 to 4.9e-4).
 //
 // Places that a row does not see must not reach it, whatever they hold.  Keys: their scores are
 // replaced.  Values: a weight of 0 times NaN or infinity is NaN, so a warp (the guard) looks at the V

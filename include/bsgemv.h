@@ -486,6 +486,9 @@ int bsgemv_attn_destroy(bsgemv_attn_plan_t plan);
  * score of +inf, gives NaN in its out and lse; a row all of whose scores are -inf gets NaN in out and -inf
  * in lse.  Otherwise a column of out is infinite where an infinity is among the column's values that the
  * row sees, and NaN where infinities of both signs or NaN are (a weight of 0 or not).
+ *
+ * Scores, softmax and sums are fp32; numerators as in bsgemv_attn_run.  The tensor cores cut off what does
+ * not fit when they add: a row that sees n positions is up to about 1.5e-9 n of itself too small.
  */
 typedef struct bsgemv_chunk_plan_s* bsgemv_chunk_plan_t;
 
@@ -494,7 +497,8 @@ typedef struct bsgemv_chunk_plan_s* bsgemv_chunk_plan_t;
 int bsgemv_chunk_plan(bsgemv_chunk_plan_t* out, int act_bf16, int Hq, int Hkv, int D,
                       int page_size, int max_n, int max_T);
 
-/* Enqueue the attention of T (1 .. max_T) rows in n (1 .. max_n) entries.  cap: 0 for none, or > 0
+/* Enqueue the attention of T (1 .. max_T) rows in n (1 .. max_n) entries (a call without any is refused,
+ * as bsgemv_attn_run's; bsgemv_cache_grow and _append return BSGEMV_OK).  cap: 0 for none, or > 0
  * with scale / cap and cap * log2(e) finite in fp32 (capped scores are right to 2^-20 of themselves
  * and the error of the scores); window: 0 for none, or >= 1; slopes: Hq fp32 (device) or NULL.  Alignment and strides as bsgemv_attn_run; table_stride >= max_pages.  Page ids
  * outside 0 .. num_pages-1 are read as zeros.  Deterministic: repeated calls are bit-identical (the
@@ -608,8 +612,8 @@ int bsgemv_cache_grow(bsgemv_cache_t cache, void* pool, int32_t* refs, int32_t* 
  *
  * for pair p < rot / 2: elements (p, p + rot / 2), or (2 p, 2 p + 1) with BSGEMV_ROPE_INTERLEAVED.
  * Elements from rot on are normalised only.  Angles are worked out modulo a turn in 64-bit fixed
- * point (2^-64 of a turn a position, freqs to the last bit of a double), so far positions lose
- * nothing; norms and products are fp32, one rounding at the end.
+ * point (to 2^-63 of a turn a position, with freqs as the doubles that they are) and rounded to fp32;
+ * sines, norms and products are fp32, with one rounding at the end.
  */
 typedef struct bsgemv_rope_s* bsgemv_rope_t;
 
