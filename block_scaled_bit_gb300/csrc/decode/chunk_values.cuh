@@ -6,7 +6,7 @@
 // entries beside it.  But nothing makes it finite again.  So the three places that write rows look at what they
 // write, an operation for two columns, and a warp with something that is not finite goes over the values of
 // its rows once more: a column has their sum, infinity or NaN, where some are not finite, and else stays.
-// (The looking takes 1 % of long chunks of heads of 128 and 1.5 us of a call whose units are cut.  With an
+// (The looking takes 1 to 2 % of long chunks of heads of 128 and 1.5 us of a call whose units are cut.  With an
 // infinity that all rows see, 2048 tokens after 30720 of 32/8 heads of 128 take 9 ms in place of 1, 33
 // sequences of 3100 positions 750 us in place of 95: 0.6 us a warp for eight positions of 64 columns.  The
 // tensor-memory kernel's other warps wait for that; their limit of 4 s bears 2 * 10^7 positions.)

@@ -500,9 +500,10 @@ int bsgemv_chunk_plan(bsgemv_chunk_plan_t* out, int act_bf16, int Hq, int Hkv, i
 /* Enqueue the attention of T (1 .. max_T) rows in n (1 .. max_n) entries (a call without any is refused,
  * as bsgemv_attn_run's; bsgemv_cache_grow and _append return BSGEMV_OK).  cap: 0 for none, or > 0
  * with scale / cap and cap * log2(e) finite in fp32 (capped scores are right to 2^-20 of themselves
- * and the error of the scores); window: 0 for none, or >= 1; slopes: Hq fp32 (device) or NULL.  Alignment and strides as bsgemv_attn_run; table_stride >= max_pages.  Page ids
- * outside 0 .. num_pages-1 are read as zeros.  Deterministic: repeated calls are bit-identical (the
- * bits of a row may depend on the entries beside it: they decide where sums are cut). */
+ * and the error of the scores); window: 0 for none, or >= 1; slopes: Hq fp32 (device) or NULL.
+ * Alignment and strides as bsgemv_attn_run; table_stride >= max_pages.  Page ids outside 0 ..
+ * num_pages-1 are read as zeros.  Deterministic: repeated calls are bit-identical (the bits of a row
+ * may depend on the entries beside it: they decide where sums are cut). */
 int bsgemv_chunk_run(bsgemv_chunk_plan_t plan, const void* q, int64_t q_stride, const void* k,
                      const void* v, int64_t page_stride, int64_t head_stride, int64_t row_stride,
                      int num_pages, const int32_t* tables, int64_t table_stride, int num_seqs,
